@@ -1,4 +1,5 @@
-"""ctypes binding of libmuon_mi355x.so (declared in include/muon.h).
+"""ctypes binding of libmuon_mi355x.so (declared in include/muon.h and
+include/muon_blocks.h).
 
 Argument marshalling only: tensors become device pointers, row strides and
 dtype codes; the torch stream becomes a hipStream_t.  Every step of the
@@ -107,6 +108,22 @@ class StepHparams(ctypes.Structure):
     ]
 
 
+class BlockDesc(ctypes.Structure):
+    """muon_block_desc (include/muon_blocks.h)."""
+    _fields_ = [
+        ("blocks", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+        ("ld_param", ctypes.c_int64), ("ld_grad", ctypes.c_int64), ("ld_mom", ctypes.c_int64),
+        ("stride_param", ctypes.c_int64), ("stride_grad", ctypes.c_int64), ("stride_mom", ctypes.c_int64),
+        ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("mom_dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+BLOCKS_NS = 0
+BLOCKS_VJP = 1
+BLOCKS_STEP = 2
+
+
 _VP = ctypes.c_void_p
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _lib = None
@@ -167,6 +184,15 @@ def lib() -> ctypes.CDLL:
     L.muon_stream_submit.restype = i32
     L.muon_stream_plan_destroy.argtypes = [_VP]
     L.muon_stream_plan_destroy.restype = i32
+    B, C = ctypes.POINTER(BlockDesc), ctypes.POINTER(NsCoeffs)
+    L.muon_ns_blocks.argtypes = [_PP, _PP, B, i32, NsCoeffs, i32, C, _VP, u64, _VP]
+    L.muon_ns_blocks.restype = i32
+    L.muon_ns_blocks_vjp.argtypes = [_PP, _PP, _PP, B, i32, NsCoeffs, i32, C, _VP, u64, _VP]
+    L.muon_ns_blocks_vjp.restype = i32
+    L.muon_step_blocks.argtypes = [_PP, _PP, _PP, B, i32, ctypes.POINTER(StepHparams), _PP, _VP, u64, _VP]
+    L.muon_step_blocks.restype = i32
+    L.muon_blocks_workspace_bytes.argtypes = [i32, B, i32, NsCoeffs, i32, C]
+    L.muon_blocks_workspace_bytes.restype = u64
     _lib = L
     return L
 
@@ -525,3 +551,184 @@ def muon_workspace_bytes(shapes, precision=NS_BF16) -> int:
         d.precision = precs[i]
         d.grad_dtype = DTYPE_BF16
     return int(lib().muon_workspace_bytes(descs, n))
+
+
+# ------------------------------------------------------------ stacks of blocks
+#
+# A stack is a 3-D tensor (blocks, rows, cols), any view of a weight whose
+# rows are contiguous: `w.view(heads, dim, width)` for heads in rows,
+# `w.unflatten(1, (heads, dim)).transpose(0, 1)` for heads in columns.
+
+
+class _BlocksArgs:
+    """Pointer and descriptor arrays of a fixed list of stacks, built once and
+    reused by every call on the same tensors.  All tensors live on one GPU;
+    the calls run on it, whatever the current device."""
+
+    op = None
+
+    def __init__(self, lists):
+        """lists: {field: (argument name, stacks)} for the fields grad, param and mom."""
+        n = len(next(iter(lists.values()))[1])
+        for name, ts in lists.values():
+            if len(ts) != n:
+                raise ValueError(f"{name}: {len(ts)} stacks where the others have {n}")
+        self.count = n
+        self.descs = (BlockDesc * max(n, 1))()
+        self.ptrs = {}
+        self.device = None
+        for i in range(n):
+            d, shape = self.descs[i], None
+            for field, (name, ts) in lists.items():
+                t = ts[i]
+                if t.dim() != 3:
+                    raise ValueError(f"{name}[{i}] must be 3-D: blocks, rows, cols (got shape {tuple(t.shape)})")
+                if shape is None:
+                    shape = tuple(t.shape)
+                    d.blocks, d.rows, d.cols = shape
+                elif tuple(t.shape) != shape:
+                    raise ValueError(f"stack {i}: {name} has shape {tuple(t.shape)}, not {shape}")
+                if t.stride(2) != 1 and t.shape[2] > 1:
+                    raise ValueError(f"{name}[{i}] must have unit column stride")
+                ld = max(int(t.stride(1)), int(t.shape[2])) if t.shape[1] == 1 else int(t.stride(1))
+                setattr(d, f"ld_{field}", ld)
+                setattr(d, f"stride_{field}", int(t.stride(0)) if t.shape[0] > 1 else 0)
+                setattr(d, f"{field}_dtype", dtype_code(t.dtype))
+                if not t.is_cuda:
+                    raise ValueError(f"{name}[{i}] is on {t.device}, not on a GPU")
+                if self.device is None:
+                    self.device = t.device
+                elif t.device != self.device:
+                    raise ValueError(f"{name}[{i}] is on {t.device}, the first stack on {self.device}")
+        for field, (_, ts) in lists.items():
+            self.ptrs[field] = _ptr_array([t.data_ptr() for t in ts])
+        self._keep = lists
+
+    def workspace_bytes(self, *, ns_coeffs, ns_steps, ns_schedule=None) -> int:
+        """Bytes a `workspace` of a call with these coefficients needs."""
+        sched, keep = _schedule(ns_schedule, ns_steps)
+        with _on_device(self.device):
+            got = int(lib().muon_blocks_workspace_bytes(self.op, self.descs, self.count, _coeffs(ns_coeffs),
+                                                        int(ns_steps), sched))
+            detail = muon_last_error()
+        del keep
+        if not got and detail:
+            raise MuonError(MUON_ERR_INVALID_ARGUMENT, detail)
+        return got
+
+
+def _on_device(device):
+    return torch.cuda.device(device if device is not None else -1)
+
+
+def _coeffs(ns_coeffs) -> NsCoeffs:
+    a, b, c = ns_coeffs
+    return NsCoeffs(float(a), float(b), float(c))
+
+
+def _schedule(ns_schedule, ns_steps):
+    if ns_schedule is None:
+        return None, None
+    if len(ns_schedule) != int(ns_steps):
+        raise ValueError("ns_schedule needs one triple per step")
+    arr = (NsCoeffs * max(len(ns_schedule), 1))(*[_coeffs(t) for t in ns_schedule])
+    return ctypes.cast(arr, ctypes.POINTER(NsCoeffs)), arr
+
+
+def _workspace(ws, device):
+    """(address, bytes) of a caller's workspace tensor, or (None, 0)."""
+    if ws is None:
+        return None, 0
+    if not ws.is_cuda or ws.device != device or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the stacks' device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+class NsBlocksArgs(_BlocksArgs):
+    """Stacks of muon_ns_blocks."""
+
+    op = BLOCKS_NS
+
+    def __init__(self, x_in, x_out):
+        super().__init__({"grad": ("x_in", x_in), "param": ("x_out", x_out)})
+
+
+class VjpBlocksArgs(_BlocksArgs):
+    """Stacks of muon_ns_blocks_vjp."""
+
+    op = BLOCKS_VJP
+
+    def __init__(self, x_in, grad_out, grad_in):
+        super().__init__({"grad": ("x_in", x_in), "mom": ("grad_out", grad_out), "param": ("grad_in", grad_in)})
+
+
+class StepBlocksArgs(_BlocksArgs):
+    """Stacks of muon_step_blocks."""
+
+    op = BLOCKS_STEP
+
+    def __init__(self, params, grads, momenta, updates_out=None):
+        super().__init__({"param": ("params", params), "grad": ("grads", grads), "mom": ("momenta", momenta)})
+        self.updates = None
+        if updates_out is not None:
+            if len(updates_out) != self.count:
+                raise ValueError("one updates_out entry per stack (None allowed)")
+            for i, u in enumerate(updates_out):
+                d = self.descs[i]
+                if u is not None and (u.dtype != torch.float32 or not u.is_contiguous() or u.device != self.device
+                                      or tuple(u.shape) != (d.blocks, d.rows, d.cols)):
+                    raise ValueError(f"updates_out[{i}] must be a contiguous float32 tensor shaped like its stack")
+            self.updates = _ptr_array([0 if u is None else u.data_ptr() for u in updates_out])
+            self._keep = (self._keep, updates_out)
+
+
+def muon_ns_blocks(x_in, x_out=None, *, ns_coeffs, ns_steps, ns_schedule=None, workspace=None, stream=None):
+    """x_out[i][b] = Newton-Schulz orthogonalisation of block x_in[i][b], on
+    lists of (blocks, rows, cols) stacks (or on a prebuilt NsBlocksArgs)."""
+    args = x_in if isinstance(x_in, NsBlocksArgs) else NsBlocksArgs(x_in, x_out)
+    if args.count == 0:
+        return
+    sched, keep = _schedule(ns_schedule, ns_steps)
+    with _on_device(args.device):
+        ws, nbytes = _workspace(workspace, args.device)
+        status = lib().muon_ns_blocks(args.ptrs["grad"], args.ptrs["param"], args.descs, args.count,
+                                      _coeffs(ns_coeffs), int(ns_steps), sched, ws, nbytes, _stream_handle(stream))
+        del keep
+        _check(status)
+
+
+def muon_ns_blocks_vjp(x_in, grad_out=None, grad_in=None, *, ns_coeffs, ns_steps, ns_schedule=None, workspace=None,
+                       stream=None):
+    """grad_in[i] = gradient with respect to x_in[i] of <muon_ns_blocks(x_in[i]), grad_out[i]>
+    (lists of stacks, or a prebuilt VjpBlocksArgs)."""
+    args = x_in if isinstance(x_in, VjpBlocksArgs) else VjpBlocksArgs(x_in, grad_out, grad_in)
+    if args.count == 0:
+        return
+    sched, keep = _schedule(ns_schedule, ns_steps)
+    with _on_device(args.device):
+        ws, nbytes = _workspace(workspace, args.device)
+        status = lib().muon_ns_blocks_vjp(args.ptrs["grad"], args.ptrs["mom"], args.ptrs["param"], args.descs,
+                                          args.count, _coeffs(ns_coeffs), int(ns_steps), sched, ws, nbytes,
+                                          _stream_handle(stream))
+        del keep
+        _check(status)
+
+
+def muon_step_blocks(params, grads=None, momenta=None, *, lr, beta, nesterov, ns_coeffs, ns_steps,
+                     scale_rule=SCALE_NONE, ns_schedule=None, weight_decay=0.0, momentum_kind=MOMENTUM_HEAVY_BALL,
+                     lr_per_stack=None, scale_per_stack=None, updates_out=None, workspace=None, stream=None):
+    """One Muon step on lists of stacks (or on a prebuilt StepBlocksArgs), every
+    block orthogonalised as a matrix of its own."""
+    args = params if isinstance(params, StepBlocksArgs) else StepBlocksArgs(params, grads, momenta, updates_out)
+    if args.count == 0:
+        return
+    opt, keep = _step_options(args.count, ns_steps, ns_schedule, weight_decay, momentum_kind, lr_per_stack,
+                              scale_per_stack, LAUNCH_AUTO, TILES_AUTO)
+    hp = StepHparams(float(lr), float(beta), int(nesterov), _coeffs(ns_coeffs), int(ns_steps), int(scale_rule),
+                     ctypes.pointer(opt))
+    with _on_device(args.device):
+        ws, nbytes = _workspace(workspace, args.device)
+        status = lib().muon_step_blocks(args.ptrs["param"], args.ptrs["grad"], args.ptrs["mom"], args.descs, args.count,
+                                        ctypes.byref(hp), args.updates, ws, nbytes, _stream_handle(stream))
+        del keep
+        _check(status)

@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuon_mi355x.so")
 
 SOURCES = ["muon_api.cpp", "elementwise.hip", "ns_gemm.hip", "ns_chain.hip", "adamw.hip", "probe.hip",
-           "noalloc.hip"]
+           "noalloc.hip", "muon_blocks.cpp", "blocks_gram.hip", "blocks_iterate.hip", "blocks_apply.hip"]
 ARCH = os.environ.get("MUON_OFFLOAD_ARCH", "gfx950")
 
 

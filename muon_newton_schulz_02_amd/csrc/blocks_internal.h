@@ -1,0 +1,100 @@
+// Types shared by the host side of the block operators and their kernels
+// (stacks of blocks with min(rows, cols) <= 128; see muon_blocks.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace muon {
+
+constexpr int BLOCK_MAX_M = 128;
+
+enum BlockFlags : uint32_t {
+  BF_X_BF16 = 1,      // x is bfloat16 (else binary32)
+  BF_Y_BF16 = 2,
+  BF_OUT_BF16 = 4,
+  BF_X_VEC = 8,       // rows of x allow 16-byte access at multiples of 16 bytes
+  BF_Y_VEC = 16,
+  BF_OUT_VEC = 32,
+  BF_TR = 64,         // rows > cols: element (i, j) of the wide block is at j * ld + i
+  BF_WRITEBACK = 128  // apply: out is a weight, out <- rnd(out * d - t * O)
+};
+
+// One stack as the kernels see it, at one stage of the computation.
+struct BlockStack {
+  const void* x;      // input, gradient of the step, or iterate of an earlier stage
+  int64_t x_ld, x_bs;
+  const void* y;      // gradient: cotangent; step: momentum (binary32, written by the gram pass)
+  int64_t y_ld, y_bs;
+  void* out;
+  int64_t out_ld, out_bs;
+  float* upd;         // exported update, blocks x rows x cols contiguous, or null
+  int64_t part0;      // first float of the stack's Gram partials
+  int32_t m, n;       // wide shape
+  int32_t cols;       // row length of upd
+  int32_t block0;     // index of the stack's first block in the launch
+  int32_t goff, gsplit, gchunk;  // gram workgroups: first, per block, columns of each
+  int32_t aoff, asplit, achunk;  // apply workgroups
+  uint32_t flags;
+  float t, d;         // write-back scalars
+  int32_t blocks;
+};
+
+// The stacks of a launch: up to BLOCK_INLINE in the kernel's arguments, else
+// in a device table (written by block_table_kernel, so that a call needs no
+// host-to-device copy).
+constexpr int BLOCK_INLINE = 16;
+struct BlockTable {
+  const BlockStack* ext;
+  int32_t count;
+  int32_t pad;
+  BlockStack inl[BLOCK_INLINE];
+};
+static_assert(sizeof(BlockTable) <= 3072, "kernel arguments stay small");
+
+// Momentum of the step: M <- beta M + g1 G, U = nesterov ? g1 G + beta M : M
+// with g1 = 1 (heavy ball) or fl32(1 - beta) (EMA).
+struct BlockMom {
+  float beta, g1;
+  int32_t nesterov, ema;
+};
+
+// The steps of one stage of the m x m recursion.
+constexpr int BLOCK_STAGE_STEPS = 32;
+struct BlockSteps {
+  float a[BLOCK_STAGE_STEPS], b[BLOCK_STAGE_STEPS], c[BLOCK_STAGE_STEPS];
+  int32_t steps;
+  int32_t first;      // x is not normalised yet: fold 1 / (||x|| + eps)
+};
+
+enum BlockKind : int { BK_X = 0, BK_STEP = 1, BK_VJP = 2 };
+
+// Row tiles of 16 that a block of m rows is padded to: 2, 4 or 8 (the
+// kernels' template sizes; 32, 64 or 128 rows).
+constexpr int block_mt(int m) { return m <= 32 ? 2 : m <= 64 ? 4 : 8; }
+// Gram partials of one block and workgroup: 8 / MT waves sum separate columns.
+constexpr int block_kw(int mt) { return 8 / mt; }
+// Floats of one partial: the upper triangle of 16 x 16 tiles, and for the
+// gradient all tiles of y x^T.
+constexpr int block_part_floats(int mt, int kind) {
+  return ((mt / 2) * (mt + 1) + (kind == BK_VJP ? mt * mt : 0)) * 256;
+}
+// Columns a gram workgroup takes at a time, and columns of an apply workgroup's strip.
+constexpr int block_kc(int mt) { return mt == 2 ? 128 : 64; }
+constexpr int BLOCK_STRIP = 256;
+
+// The launchers.  pl: bfloat16 parts of an element of x (1, 2, 3); pp: parts
+// of an element of P (2, 3).
+hipError_t launch_block_table(const BlockStack* host, int32_t count, BlockStack* dev, hipStream_t stream);
+hipError_t launch_block_gram(int mt, int pl, int kind, const BlockTable& tab, int32_t wgs, float* partials,
+                             const BlockMom& mom, hipStream_t stream);
+// Sums the partials of every block, runs the recursion and writes P (and, for
+// the gradient, T) as pp planes of bfloat16 parts, mp x mp each.  scratch: 2
+// mp x mp binary32 matrices per block (gradient only).
+hipError_t launch_block_iterate(int mt, int pp, int kind, const BlockTable& tab, int32_t blocks,
+                                const float* partials, uint16_t* p_out, uint16_t* t_out, float* scratch,
+                                const BlockSteps& steps, hipStream_t stream);
+hipError_t launch_block_apply(int mt, int pl, int pp, int kind, const BlockTable& tab, int32_t wgs,
+                              const uint16_t* p, const uint16_t* t, const BlockMom& mom, hipStream_t stream);
+
+}  // namespace muon

@@ -17,6 +17,7 @@
 #include <string>
 #include <vector>
 
+#include "api_internal.h"
 #include "muon_internal.h"
 
 namespace muon {
@@ -1772,6 +1773,16 @@ muon_status run_adamw(const AdamwCall& c) {
 }
 
 }  // namespace
+
+muon_status api_fail(muon_status s, const char* text) { return fail(s, "%s", text); }
+void api_clear_error() { t_last_error.clear(); }
+std::mutex& api_mutex() { return g_mu; }
+hipError_t api_device_alloc(void** p, size_t bytes) { return device_alloc(p, bytes); }
+hipError_t api_timed(int kc, hipStream_t stream, const std::function<hipError_t()>& launch) {
+  return timed(kc, stream, launch);
+}
+void (*api_release_hook)() = nullptr;
+
 }  // namespace muon
 
 using namespace muon;
@@ -1994,6 +2005,7 @@ muon_status muon_release_workspace(void) {
     for (hipEvent_t ev : kv.second.last_call)
       if (ev) (void)hipEventDestroy(ev);
   }
+  if (api_release_hook) api_release_hook();
   if (have_dev) (void)hipSetDevice(cur);
   g_dev.clear();
   (void)hipGetLastError();

@@ -1,0 +1,810 @@
+// Host side of the block operators (muon_blocks.h): validation, the stages
+// of the recursion, the workspace and the launches.
+//
+// A call is a sequence of stages; each runs three kernels over every block of
+// a group of stacks: the Gram pass, the m x m recursion and the apply pass.
+// Stacks are grouped by what selects a kernel's template: padded m, types and
+// the stage limit.
+#include "muon_blocks.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+#include <map>
+#include <new>
+#include <vector>
+
+#include "api_internal.h"
+#include "blocks_internal.h"
+
+namespace muon {
+namespace {
+
+constexpr int64_t MAX_DIM = 65536;
+constexpr int64_t MAX_BLOCKS = 1 << 20;
+constexpr int32_t MAX_COUNT = 1 << 20;
+constexpr int32_t MAX_NS_STEPS = 1000;
+constexpr int64_t MAX_STRIDE = int64_t(1) << 40;
+
+// Largest growth of small singular values between two Gram matrices.  The
+// Gram matrix holds eigenvalues down to about 2^-24 of its trace, and the
+// recursion carries its error on with the square of that growth; measured
+// against float64 over spectra from flat to i^-3 and rank-16 spikes, five
+// quintic steps: 512 (one stage) 1e-4 to 6e-4, 48 (3 + 2 steps) 1e-6 to
+// 2e-5, as binary32 arithmetic on the iterates themselves.
+constexpr double LIMIT_BF16 = 512.0;
+constexpr double LIMIT_F32 = 48.0;
+// Binary32 gradients of nearly square blocks (n < 2 m), whose singular values
+// reach down to zero: one step a stage (a 100 x 100 block, six steps: 6e-6
+// against 2e-5 with LIMIT_F32; binary32 iterates 6e-6).
+constexpr double LIMIT_VJP_SQUARE = 1.0;
+
+muon_status fail(muon_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return api_fail(s, buf);
+}
+
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+int esize(int32_t dt) { return dt == MUON_DTYPE_BF16 ? 2 : 4; }
+
+struct Call {
+  int op = MUON_BLOCKS_NS;
+  const void* const* x = nullptr;   // grad fields
+  const void* const* y = nullptr;   // mom fields: cotangent (VJP) or momentum (STEP, written)
+  void* const* out = nullptr;       // param fields
+  float* const* upd = nullptr;
+  const muon_block_desc* stacks = nullptr;
+  int32_t count = 0;
+  muon_ns_coeffs co = {0.f, 0.f, 0.f};
+  int32_t ns_steps = 0;
+  const muon_ns_coeffs* schedule = nullptr;
+  const muon_step_hparams* hp = nullptr;
+  void* ws = nullptr;
+  uint64_t ws_bytes = 0;
+  hipStream_t stream = nullptr;
+};
+
+// ------------------------------------------------------------- validation
+
+// Bytes a tensor of blocks may touch, and the grid its rows lie on: rows
+// start `row` bytes apart from the first and are `win` bytes long (row = 0:
+// no such grid).
+struct Region {
+  uintptr_t lo, hi;
+  uint64_t row, win;
+  bool written;
+  int32_t idx;
+  const char* what;
+};
+
+Region region_of(const void* p, const muon_block_desc& d, int64_t ld, int64_t stride, int esz, bool written,
+                 int32_t idx, const char* what) {
+  Region r;
+  r.lo = reinterpret_cast<uintptr_t>(p);
+  r.hi = r.lo + uint64_t((d.blocks - 1) * stride + (d.rows - 1) * ld + d.cols) * uint64_t(esz);
+  r.row = r.win = 0;
+  if (d.blocks == 1 || stride % ld == 0) {
+    r.row = uint64_t(ld) * esz;
+    r.win = uint64_t(d.cols) * esz;
+  } else if ((d.blocks - 1) * stride + d.cols <= ld) {
+    r.row = uint64_t(ld) * esz;
+    r.win = uint64_t((d.blocks - 1) * stride + d.cols) * esz;
+  }
+  r.written = written;
+  r.idx = idx;
+  r.what = what;
+  return r;
+}
+
+bool share_bytes(const Region& a, const Region& b) {  // a.lo <= b.lo
+  if (b.lo >= a.hi) return false;
+  if (a.row == 0 || a.row != b.row) return true;
+  // rows on one grid: disjoint if the windows are
+  const uint64_t d = (b.lo - a.lo) % a.row;
+  return !(d >= a.win && d + b.win <= a.row);
+}
+
+muon_status check_alias(std::vector<Region>& v) {
+  std::sort(v.begin(), v.end(), [](const Region& a, const Region& b) { return a.lo < b.lo; });
+  for (size_t i = 0; i < v.size(); ++i)
+    for (size_t j = i + 1; j < v.size() && v[j].lo < v[i].hi; ++j)
+      if ((v[i].written || v[j].written) && share_bytes(v[i], v[j]))
+        return fail(MUON_ERR_ALIAS, "%s of stack %d overlaps %s of stack %d", v[j].what, v[j].idx, v[i].what, v[i].idx);
+  return MUON_OK;
+}
+
+muon_status check_view(int32_t i, const char* what, const muon_block_desc& d, int64_t ld, int64_t stride,
+                       int32_t dtype, bool f32_only, bool written) {
+  if (dtype != MUON_DTYPE_F32 && (f32_only || dtype != MUON_DTYPE_BF16))
+    return fail(MUON_ERR_UNSUPPORTED, "stack %d: %s dtype %d is not %s", i, what, dtype, f32_only ? "F32" : "F32 or BF16");
+  if (ld < d.cols || ld > MAX_STRIDE)
+    return fail(MUON_ERR_INVALID_ARGUMENT, "stack %d: %s row stride %lld out of [cols = %lld, 2^40]", i, what,
+                (long long)ld, (long long)d.cols);
+  if (stride < 0 || stride > MAX_STRIDE)
+    return fail(MUON_ERR_INVALID_ARGUMENT, "stack %d: %s block stride %lld out of [0, 2^40]", i, what,
+                (long long)stride);
+  if (written && d.blocks > 1) {
+    const bool apart = stride >= (d.rows - 1) * ld + d.cols;
+    const bool beside = stride >= d.cols && (d.blocks - 1) * stride + d.cols <= ld;
+    if (!apart && !beside)
+      return fail(MUON_ERR_ALIAS, "stack %d: blocks of %s share elements (rows %lld, cols %lld, row stride %lld, block "
+                  "stride %lld)", i, what, (long long)d.rows, (long long)d.cols, (long long)ld, (long long)stride);
+  }
+  return MUON_OK;
+}
+
+muon_status check_ptr(int32_t i, const char* what, const void* p, int esz) {
+  if (!p) return fail(MUON_ERR_INVALID_ARGUMENT, "stack %d: %s pointer is NULL", i, what);
+  if (reinterpret_cast<uintptr_t>(p) % uintptr_t(esz) != 0)
+    return fail(MUON_ERR_UNSUPPORTED, "stack %d: %s pointer is not aligned to %d bytes", i, what, esz);
+  return MUON_OK;
+}
+
+bool finite3(const muon_ns_coeffs& c) { return std::isfinite(c.a) && std::isfinite(c.b) && std::isfinite(c.c); }
+
+muon_status check_steps(const Call& c) {
+  if (c.ns_steps < 0 || c.ns_steps > MAX_NS_STEPS)
+    return fail(MUON_ERR_INVALID_ARGUMENT, "ns_steps %d out of range [0, %d]", c.ns_steps, MAX_NS_STEPS);
+  if (!finite3(c.co)) return fail(MUON_ERR_INVALID_ARGUMENT, "ns_coeffs must be finite");
+  if (c.schedule)
+    for (int32_t k = 0; k < c.ns_steps; ++k)
+      if (!finite3(c.schedule[k])) return fail(MUON_ERR_INVALID_ARGUMENT, "ns_schedule[%d] is not finite", k);
+  return MUON_OK;
+}
+
+// Sizes, dtypes and strides of every stack (no pointers).
+muon_status check_descs(const Call& c) {
+  int64_t total = 0;
+  for (int32_t i = 0; i < c.count; ++i) {
+    const muon_block_desc& d = c.stacks[i];
+    if (d.blocks < 0 || d.blocks > MAX_BLOCKS)
+      return fail(d.blocks < 0 ? MUON_ERR_INVALID_ARGUMENT : MUON_ERR_UNSUPPORTED,
+                  "stack %d: %lld blocks out of [0, 2^20]", i, (long long)d.blocks);
+    if (d.rows < 1 || d.cols < 1)
+      return fail(MUON_ERR_INVALID_ARGUMENT, "stack %d: rows and cols must be >= 1 (got %lld x %lld)", i,
+                  (long long)d.rows, (long long)d.cols);
+    if (d.rows > MAX_DIM || d.cols > MAX_DIM)
+      return fail(MUON_ERR_UNSUPPORTED, "stack %d: rows and cols must be <= %lld", i, (long long)MAX_DIM);
+    if (std::min(d.rows, d.cols) > BLOCK_MAX_M)
+      return fail(MUON_ERR_UNSUPPORTED, "stack %d: blocks of %lld x %lld; min(rows, cols) must be <= %d (larger "
+                  "matrices: muon_ns_batched, muon_step_batched)", i, (long long)d.rows, (long long)d.cols, BLOCK_MAX_M);
+    if (d.reserved != 0) return fail(MUON_ERR_INVALID_ARGUMENT, "stack %d: reserved must be 0", i);
+    muon_status st = check_view(i, c.op == MUON_BLOCKS_STEP ? "grad" : "x_in", d, d.ld_grad, d.stride_grad,
+                                d.grad_dtype, false, false);
+    if (st == MUON_OK)
+      st = check_view(i, c.op == MUON_BLOCKS_STEP ? "param" : c.op == MUON_BLOCKS_VJP ? "grad_in" : "x_out", d,
+                      d.ld_param, d.stride_param, d.param_dtype, false, true);
+    if (st == MUON_OK && c.op == MUON_BLOCKS_VJP)
+      st = check_view(i, "grad_out", d, d.ld_mom, d.stride_mom, d.mom_dtype, false, false);
+    if (st == MUON_OK && c.op == MUON_BLOCKS_STEP)
+      st = check_view(i, "momentum", d, d.ld_mom, d.stride_mom, d.mom_dtype, true, true);
+    if (st != MUON_OK) return st;
+    total += d.blocks;
+    // a block has at most 2^16 / 128 gram workgroups (and fewer apply workgroups)
+    if (total > (int64_t(1) << 21))
+      return fail(MUON_ERR_UNSUPPORTED, "more than 2^21 blocks in one call");
+  }
+  return MUON_OK;
+}
+
+muon_status check_hparams(const Call& c) {
+  if (!c.hp) return fail(MUON_ERR_INVALID_ARGUMENT, "hparams is NULL");
+  const muon_step_hparams& h = *c.hp;
+  if (!std::isfinite(h.lr)) return fail(MUON_ERR_INVALID_ARGUMENT, "lr is not finite");
+  if (!(h.beta >= 0.f && h.beta < 1.f)) return fail(MUON_ERR_INVALID_ARGUMENT, "beta must be in [0, 1)");
+  if (h.nesterov != 0 && h.nesterov != 1) return fail(MUON_ERR_INVALID_ARGUMENT, "nesterov must be 0 or 1");
+  if (h.scale_rule < MUON_SCALE_NONE || h.scale_rule > MUON_SCALE_RMS_MATCH)
+    return fail(MUON_ERR_INVALID_ARGUMENT, "unknown scale_rule %d", h.scale_rule);
+  if (!h.options) return MUON_OK;
+  const muon_step_options& o = *h.options;
+  if (!std::isfinite(o.weight_decay) || o.weight_decay < 0.f)
+    return fail(MUON_ERR_INVALID_ARGUMENT, "weight_decay must be finite and >= 0");
+  if (o.momentum_kind != MUON_MOMENTUM_HEAVY_BALL && o.momentum_kind != MUON_MOMENTUM_EMA)
+    return fail(MUON_ERR_INVALID_ARGUMENT, "unknown momentum_kind %d", o.momentum_kind);
+  if (o.launch_mode < MUON_LAUNCH_AUTO || o.launch_mode > MUON_LAUNCH_CHAIN)
+    return fail(MUON_ERR_INVALID_ARGUMENT, "unknown launch_mode %d", o.launch_mode);
+  if (o.tile_mode < MUON_TILES_AUTO || o.tile_mode > MUON_TILES_SMALL)
+    return fail(MUON_ERR_INVALID_ARGUMENT, "unknown tile_mode %d", o.tile_mode);
+  if (o.launch_mode != MUON_LAUNCH_AUTO || o.tile_mode != MUON_TILES_AUTO)
+    return fail(MUON_ERR_UNSUPPORTED, "launch_mode and tile_mode must be AUTO for blocks");
+  for (int32_t i = 0; i < c.count; ++i) {
+    if (o.lr_per_matrix && !std::isfinite(o.lr_per_matrix[i]))
+      return fail(MUON_ERR_INVALID_ARGUMENT, "lr_per_matrix[%d] is not finite", i);
+    if (o.scale_per_matrix && !std::isfinite(o.scale_per_matrix[i]))
+      return fail(MUON_ERR_INVALID_ARGUMENT, "scale_per_matrix[%d] is not finite", i);
+  }
+  return MUON_OK;
+}
+
+muon_status validate(const Call& c) {
+  if (c.count < 0 || c.count > MAX_COUNT)
+    return fail(MUON_ERR_INVALID_ARGUMENT, "count %d out of range [0, %d]", c.count, MAX_COUNT);
+  muon_status st;
+  if (c.op == MUON_BLOCKS_STEP && (st = check_hparams(c)) != MUON_OK) return st;
+  if ((st = check_steps(c)) != MUON_OK) return st;
+  if (c.count == 0) return MUON_OK;
+  if (!c.stacks) return fail(MUON_ERR_INVALID_ARGUMENT, "stacks is NULL");
+  const bool vjp = c.op == MUON_BLOCKS_VJP, step = c.op == MUON_BLOCKS_STEP;
+  if (!c.x || !c.out || ((vjp || step) && !c.y)) return fail(MUON_ERR_INVALID_ARGUMENT, "a pointer array is NULL");
+  if ((st = check_descs(c)) != MUON_OK) return st;
+  std::vector<Region> reg;
+  reg.reserve(size_t(c.count) * 3 + 1);
+  for (int32_t i = 0; i < c.count; ++i) {
+    const muon_block_desc& d = c.stacks[i];
+    if (d.blocks == 0) continue;
+    const char* xn = step ? "grad" : "x_in";
+    const char* yn = step ? "momentum" : "grad_out";
+    const char* on = step ? "param" : vjp ? "grad_in" : "x_out";
+    if ((st = check_ptr(i, xn, c.x[i], esize(d.grad_dtype))) != MUON_OK) return st;
+    if ((st = check_ptr(i, on, c.out[i], esize(d.param_dtype))) != MUON_OK) return st;
+    reg.push_back(region_of(c.x[i], d, d.ld_grad, d.stride_grad, esize(d.grad_dtype), false, i, xn));
+    reg.push_back(region_of(c.out[i], d, d.ld_param, d.stride_param, esize(d.param_dtype), true, i, on));
+    if (vjp || step) {
+      if ((st = check_ptr(i, yn, c.y[i], esize(d.mom_dtype))) != MUON_OK) return st;
+      reg.push_back(region_of(c.y[i], d, d.ld_mom, d.stride_mom, esize(d.mom_dtype), step, i, yn));
+    }
+    if (c.upd && c.upd[i]) {
+      if ((st = check_ptr(i, "update", c.upd[i], 4)) != MUON_OK) return st;
+      reg.push_back(region_of(c.upd[i], d, d.cols, d.rows * d.cols, 4, true, i, "update"));
+    }
+  }
+  if (c.ws) {
+    if (reinterpret_cast<uintptr_t>(c.ws) % 256 != 0)
+      return fail(MUON_ERR_UNSUPPORTED, "workspace is not aligned to 256 bytes");
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(c.ws);
+    reg.push_back({lo, lo + c.ws_bytes, 0, 0, true, -1, "workspace"});
+  }
+  return check_alias(reg);
+}
+
+// ------------------------------------------------------------------ stages
+
+// Largest |a + b l + c l^2| over the squared singular values an iterate has
+// (the usual quintic's stay below 1.45), at least 1.
+double step_gain(const muon_ns_coeffs& k) {
+  const double a = k.a, b = k.b, c = k.c, hi = 1.5;
+  double q = std::max({1.0, std::fabs(a), std::fabs(a + b * hi + c * hi * hi)});
+  if (c != 0) {
+    const double v = -b / (2 * c);
+    if (v > 0 && v < hi) q = std::max(q, std::fabs(a + b * v + c * v * v));
+  }
+  return q;
+}
+
+struct Stage {
+  int32_t first, steps;
+};
+
+std::vector<Stage> stages_of(const Call& c, double limit) {
+  std::vector<Stage> out;
+  int32_t j = 0;
+  while (j < c.ns_steps) {
+    int32_t r = 0;
+    double gain = 1.0;
+    while (j + r < c.ns_steps && r < BLOCK_STAGE_STEPS) {
+      gain *= step_gain(c.schedule ? c.schedule[j + r] : c.co);
+      if (r > 0 && !(gain <= limit)) break;
+      ++r;
+    }
+    out.push_back({j, r});
+    j += r;
+  }
+  if (out.empty()) out.push_back({0, 0});
+  return out;
+}
+
+// ------------------------------------------------------------------ groups
+
+struct Group {
+  int mt = 2;
+  bool f32 = false, xbf = false, ybf = false;  // result class, input types
+  double limit = LIMIT_BF16;
+  std::vector<int32_t> members;     // stacks of the call
+  int64_t blocks = 0;
+  std::vector<Stage> stages;
+  int32_t gram_wgs = 0, apply_wgs = 0;
+  std::vector<BlockStack> base;     // sizes and splits; views are filled per stage
+  std::vector<size_t> stage_off;    // per member: byte offset of its binary32 copy in a stage buffer
+  size_t stage_bytes = 0;           // one stage buffer
+  int32_t stage_bufs = 0, tables = 0;
+  // byte offsets in the workspace
+  size_t o_tab = 0, o_part = 0, o_p = 0, o_t = 0, o_scr = 0, o_stage = 0, end = 0;
+};
+
+bool vec16(const void* p, int64_t rows, int64_t blocks, int64_t ld, int64_t stride, int esz) {
+  const int64_t q = 16 / esz;
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows == 1 || ld % q == 0) && (blocks == 1 || stride % q == 0);
+}
+
+int64_t ld_of_stage(const muon_block_desc& d) { return round_up(d.cols, 4); }
+
+// Splits the call into groups and lays out the workspace (the groups run one
+// after another and share it).  Returns its size.
+size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
+  std::map<std::vector<int64_t>, size_t> where;
+  const bool vjp = c.op == MUON_BLOCKS_VJP;
+  for (int32_t i = 0; i < c.count; ++i) {
+    const muon_block_desc& d = c.stacks[i];
+    if (d.blocks == 0) continue;
+    const int64_t m = std::min(d.rows, d.cols), n = std::max(d.rows, d.cols);
+    Group g;
+    g.mt = block_mt(int(m));
+    g.f32 = d.param_dtype == MUON_DTYPE_F32;
+    g.xbf = d.grad_dtype == MUON_DTYPE_BF16;
+    g.ybf = vjp && d.mom_dtype == MUON_DTYPE_BF16;
+    g.limit = !g.f32 ? LIMIT_BF16 : vjp && n < 2 * m ? LIMIT_VJP_SQUARE : LIMIT_F32;
+    const std::vector<int64_t> key = {g.mt, g.f32, g.xbf, g.ybf, int64_t(g.limit)};
+    auto it = where.find(key);
+    if (it == where.end()) {
+      it = where.emplace(key, groups.size()).first;
+      groups.push_back(g);
+    }
+    Group& q = groups[it->second];
+    q.members.push_back(i);
+    q.blocks += d.blocks;
+  }
+  size_t need = 0;
+  for (Group& g : groups) {
+    const int kc = block_kc(g.mt), mp = 16 * g.mt;
+    const int kind = vjp ? BK_VJP : c.op == MUON_BLOCKS_STEP ? BK_STEP : BK_X;
+    g.stages = stages_of(c, g.limit);
+    // workgroups enough to fill the GPU four times over, each with two tiles
+    // of columns (Gram) or one strip (apply) at least
+    const int64_t want = std::max<int64_t>(1, (4 * int64_t(cus) + g.blocks - 1) / g.blocks);
+    int64_t goff = 0, aoff = 0, block0 = 0, part = 0;
+    for (int32_t i : g.members) {
+      const muon_block_desc& d = c.stacks[i];
+      BlockStack s;
+      memset(&s, 0, sizeof(s));
+      const bool tr = d.rows > d.cols;
+      s.m = int32_t(std::min(d.rows, d.cols));
+      s.n = int32_t(std::max(d.rows, d.cols));
+      s.cols = int32_t(d.cols);
+      s.blocks = int32_t(d.blocks);
+      s.block0 = int32_t(block0);
+      s.flags = tr ? BF_TR : 0;
+      s.gchunk = int32_t(std::max<int64_t>(round_up((s.n + want - 1) / want, kc), 2 * kc));
+      s.gsplit = (s.n + s.gchunk - 1) / s.gchunk;
+      const int64_t strips = (s.n + BLOCK_STRIP - 1) / BLOCK_STRIP;
+      s.achunk = int32_t(BLOCK_STRIP * ((strips + want - 1) / want));
+      s.asplit = (s.n + s.achunk - 1) / s.achunk;
+      s.goff = int32_t(goff);
+      s.aoff = int32_t(aoff);
+      s.part0 = part;
+      s.d = 1.f;
+      goff += d.blocks * s.gsplit;
+      aoff += d.blocks * s.asplit;
+      part += d.blocks * s.gsplit * block_kw(g.mt) * int64_t(block_part_floats(g.mt, kind));
+      block0 += d.blocks;
+      g.base.push_back(s);
+      g.stage_off.push_back(g.stage_bytes);
+      g.stage_bytes += align256(size_t(d.blocks) * size_t(d.rows) * size_t(ld_of_stage(d)) * 4);
+    }
+    g.gram_wgs = int32_t(goff);
+    g.apply_wgs = int32_t(aoff);
+    const int32_t nst = int32_t(g.stages.size());
+    g.tables = vjp ? 2 * nst - 1 : nst;
+    g.stage_bufs = nst == 1 ? 0 : vjp ? nst : 1;
+    const int pp = g.f32 ? 3 : 2;
+    size_t o = 0;
+    g.o_tab = o;
+    if (g.base.size() > size_t(BLOCK_INLINE)) o += align256(sizeof(BlockStack) * g.base.size() * size_t(g.tables));
+    g.o_part = o;
+    o += align256(size_t(part) * 4);
+    g.o_p = o;
+    o += align256(size_t(g.blocks) * pp * mp * mp * 2);
+    if (vjp) {
+      g.o_t = o;
+      o += align256(size_t(g.blocks) * pp * mp * mp * 2);
+      g.o_scr = o;
+      o += align256(size_t(g.blocks) * 2 * mp * mp * 4);
+    }
+    g.o_stage = o;
+    o += g.stage_bytes * size_t(g.stage_bufs);
+    g.end = o;
+    need = std::max(need, o);
+  }
+  return need;
+}
+
+double rule_scale(int rule, int64_t rows, int64_t cols) {
+  if (rule == MUON_SCALE_SQRT_ASPECT) return std::sqrt(std::max(1.0, double(rows) / double(cols)));
+  if (rule == MUON_SCALE_RMS_MATCH) return 0.2 * std::sqrt(double(std::max(rows, cols)));
+  return 1.0;
+}
+
+// Enqueues one group: every launch goes through `run(kernel class, launch)`.
+template <class Run>
+hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
+  const bool vjp = c.op == MUON_BLOCKS_VJP, step = c.op == MUON_BLOCKS_STEP;
+  const int pp = g.f32 ? 3 : 2;
+  float* parts = reinterpret_cast<float*>(ws + g.o_part);
+  uint16_t* P = reinterpret_cast<uint16_t*>(ws + g.o_p);
+  uint16_t* T = vjp ? reinterpret_cast<uint16_t*>(ws + g.o_t) : nullptr;
+  float* scr = vjp ? reinterpret_cast<float*>(ws + g.o_scr) : nullptr;
+  BlockMom mom = {0.f, 1.f, 0, 0};
+  if (step) {
+    mom.beta = c.hp->beta;
+    mom.nesterov = c.hp->nesterov;
+    mom.ema = c.hp->options && c.hp->options->momentum_kind == MUON_MOMENTUM_EMA;
+    mom.g1 = mom.ema ? 1.f - c.hp->beta : 1.f;
+  }
+  const int32_t nst = int32_t(g.stages.size());
+
+  // views of a member: the caller's tensors, or stage buffer `buf`
+  auto set_x = [&](BlockStack& s, size_t k, int buf) {
+    const int32_t i = g.members[k];
+    const muon_block_desc& d = c.stacks[i];
+    if (buf < 0) {
+      s.x = c.x[i];
+      s.x_ld = d.ld_grad;
+      s.x_bs = d.stride_grad;
+      if (g.xbf) s.flags |= BF_X_BF16;
+      if (vec16(c.x[i], d.rows, d.blocks, d.ld_grad, d.stride_grad, esize(d.grad_dtype))) s.flags |= BF_X_VEC;
+    } else {
+      s.x = ws + g.o_stage + size_t(buf) * g.stage_bytes + g.stage_off[k];
+      s.x_ld = ld_of_stage(d);
+      s.x_bs = d.rows * s.x_ld;
+      s.flags |= BF_X_VEC;
+    }
+  };
+  auto set_y = [&](BlockStack& s, size_t k, int buf) {
+    const int32_t i = g.members[k];
+    const muon_block_desc& d = c.stacks[i];
+    if (buf < 0) {
+      s.y = c.y[i];
+      s.y_ld = d.ld_mom;
+      s.y_bs = d.stride_mom;
+      if (d.mom_dtype == MUON_DTYPE_BF16) s.flags |= BF_Y_BF16;
+      if (vec16(c.y[i], d.rows, d.blocks, d.ld_mom, d.stride_mom, esize(d.mom_dtype))) s.flags |= BF_Y_VEC;
+    } else {
+      s.y = ws + g.o_stage + size_t(buf) * g.stage_bytes + g.stage_off[k];
+      s.y_ld = ld_of_stage(d);
+      s.y_bs = d.rows * s.y_ld;
+      s.flags |= BF_Y_VEC;
+    }
+  };
+  auto set_out = [&](BlockStack& s, size_t k, int buf) {
+    const int32_t i = g.members[k];
+    const muon_block_desc& d = c.stacks[i];
+    if (buf < 0) {
+      s.out = c.out[i];
+      s.out_ld = d.ld_param;
+      s.out_bs = d.stride_param;
+      if (!g.f32) s.flags |= BF_OUT_BF16;
+      if (vec16(c.out[i], d.rows, d.blocks, d.ld_param, d.stride_param, esize(d.param_dtype))) s.flags |= BF_OUT_VEC;
+      if (step) {
+        s.flags |= BF_WRITEBACK;
+        s.upd = c.upd ? c.upd[i] : nullptr;
+        const muon_step_options* o = c.hp->options;
+        const float lr = o && o->lr_per_matrix ? o->lr_per_matrix[i] : c.hp->lr;
+        const double sc = o && o->scale_per_matrix ? double(o->scale_per_matrix[i])
+                                                   : rule_scale(c.hp->scale_rule, d.rows, d.cols);
+        s.t = float(double(lr) * sc);
+        const float wd = o ? o->weight_decay : 0.f;
+        const float lw = lr * wd;
+        s.d = wd != 0.f ? 1.f - lw : 1.f;
+      }
+    } else {
+      s.out = ws + g.o_stage + size_t(buf) * g.stage_bytes + g.stage_off[k];
+      s.out_ld = ld_of_stage(d);
+      s.out_bs = d.rows * s.out_ld;
+      s.flags |= BF_OUT_VEC;
+    }
+  };
+
+  int32_t table = 0;
+  BlockTable tab;
+  memset(&tab, 0, sizeof(tab));
+  auto set_table = [&](const std::vector<BlockStack>& v) -> hipError_t {
+    tab.count = int32_t(v.size());
+    tab.ext = nullptr;
+    if (v.size() <= size_t(BLOCK_INLINE)) {
+      memcpy(tab.inl, v.data(), sizeof(BlockStack) * v.size());
+      return hipSuccess;
+    }
+    BlockStack* dev = reinterpret_cast<BlockStack*>(ws + g.o_tab) + size_t(table++) * v.size();
+    tab.ext = dev;
+    return launch_block_table(v.data(), int32_t(v.size()), dev, c.stream);
+  };
+  auto steps_of = [&](const Stage& st, bool first) {
+    BlockSteps s;
+    memset(&s, 0, sizeof(s));
+    s.steps = st.steps;
+    s.first = first;
+    for (int32_t k = 0; k < st.steps; ++k) {
+      const muon_ns_coeffs& co = c.schedule ? c.schedule[st.first + k] : c.co;
+      s.a[k] = co.a;
+      s.b[k] = co.b;
+      s.c[k] = co.c;
+    }
+    return s;
+  };
+
+  // forward stages; for the gradient all but the last, into a buffer each
+  const int32_t fwd = vjp ? nst - 1 : nst;
+  hipError_t e = hipSuccess;
+  for (int32_t i = 0; i < fwd && e == hipSuccess; ++i) {
+    std::vector<BlockStack> v = g.base;
+    const bool user_u = step && i == 0;
+    const int src = i == 0 ? -1 : vjp ? i - 1 : 0;
+    const int dst = vjp ? i : i == nst - 1 ? -1 : 0;
+    for (size_t k = 0; k < v.size(); ++k) {
+      set_x(v[k], k, src);
+      if (user_u) set_y(v[k], k, -1);
+      set_out(v[k], k, dst);
+    }
+    if ((e = set_table(v)) != hipSuccess) break;
+    const int kind = user_u ? BK_STEP : BK_X;
+    const int pl = g.f32 ? 3 : (user_u || i > 0 || !g.xbf) ? 2 : 1;
+    e = run(user_u ? MUON_KC_MOMENTUM : MUON_KC_GRAM, [&] {
+      return launch_block_gram(g.mt, pl, kind, tab, g.gram_wgs, parts, mom, c.stream);
+    });
+    if (e != hipSuccess) break;
+    const BlockSteps s = steps_of(g.stages[size_t(i)], i == 0);
+    e = run(MUON_KC_POLY, [&] {
+      return launch_block_iterate(g.mt, pp, BK_X, tab, int32_t(g.blocks), parts, P, nullptr, nullptr, s, c.stream);
+    });
+    if (e != hipSuccess) break;
+    e = run(MUON_KC_COMBINE, [&] {
+      return launch_block_apply(g.mt, pl, pp, kind, tab, g.apply_wgs, P, nullptr, mom, c.stream);
+    });
+  }
+  if (!vjp) return e;
+  // backward stages: the cotangent of stage i's input, in place in the last buffer
+  for (int32_t i = nst - 1; i >= 0 && e == hipSuccess; --i) {
+    std::vector<BlockStack> v = g.base;
+    for (size_t k = 0; k < v.size(); ++k) {
+      set_x(v[k], k, i - 1);
+      set_y(v[k], k, i == nst - 1 ? -1 : nst - 1);
+      set_out(v[k], k, i == 0 ? -1 : nst - 1);
+    }
+    if ((e = set_table(v)) != hipSuccess) break;
+    const bool bf = (i == 0 && g.xbf) && (i == nst - 1 && g.ybf);
+    const int pl = g.f32 ? 3 : bf ? 1 : 2;
+    e = run(MUON_KC_GRAM, [&] {
+      return launch_block_gram(g.mt, pl, BK_VJP, tab, g.gram_wgs, parts, mom, c.stream);
+    });
+    if (e != hipSuccess) break;
+    const BlockSteps s = steps_of(g.stages[size_t(i)], i == 0);
+    e = run(MUON_KC_POLY, [&] {
+      return launch_block_iterate(g.mt, pp, BK_VJP, tab, int32_t(g.blocks), parts, P, T, scr, s, c.stream);
+    });
+    if (e != hipSuccess) break;
+    e = run(MUON_KC_COMBINE, [&] {
+      return launch_block_apply(g.mt, pl, pp, BK_VJP, tab, g.apply_wgs, P, T, mom, c.stream);
+    });
+  }
+  return e;
+}
+
+// -------------------------------------------------------------- workspaces
+
+struct BlockDevice {
+  int cus = 0;
+  void* ws = nullptr;
+  size_t ws_bytes = 0;
+  hipEvent_t last = nullptr;   // after the last call that used ws
+  bool recorded = false;
+};
+std::map<int, BlockDevice> g_blocks;  // under api_mutex()
+
+void release_blocks() {
+  for (auto& kv : g_blocks) {
+    if (hipSetDevice(kv.first) != hipSuccess) continue;
+    (void)hipDeviceSynchronize();
+    if (kv.second.ws) (void)hipFree(kv.second.ws);
+    if (kv.second.last) (void)hipEventDestroy(kv.second.last);
+  }
+  g_blocks.clear();
+}
+struct HookRelease {
+  HookRelease() { api_release_hook = release_blocks; }
+} g_hook_release;
+
+muon_status current_device(BlockDevice** out) {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) {
+    (void)hipGetLastError();
+    return fail(MUON_ERR_HIP, "hipGetDevice failed (no HIP device?)");
+  }
+  BlockDevice& bd = g_blocks[dev];
+  if (bd.cus == 0) {
+    int cus = 0;
+    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) {
+      (void)hipGetLastError();
+      return fail(MUON_ERR_HIP, "cannot query the compute-unit count of device %d", dev);
+    }
+    bd.cus = cus;
+  }
+  *out = &bd;
+  return MUON_OK;
+}
+
+muon_status run_call(const Call& c) {
+  muon_status st = validate(c);
+  if (st != MUON_OK) return st;
+  bool any = false;
+  for (int32_t i = 0; i < c.count && !any; ++i) any = c.stacks[i].blocks > 0;
+  if (!any) return MUON_OK;
+  std::lock_guard<std::mutex> lock(api_mutex());
+  BlockDevice* bd = nullptr;
+  if ((st = current_device(&bd)) != MUON_OK) return st;
+  std::vector<Group> groups;
+  const size_t need = plan_groups(c, bd->cus, groups);
+
+  hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(c.stream, &cap) != hipSuccess) {
+    // the null stream while another stream captures
+    (void)hipGetLastError();
+    return fail(MUON_ERR_HIP, "the stream cannot be used during another stream's capture");
+  }
+  const bool capturing = cap != hipStreamCaptureStatusNone;
+  char* ws = reinterpret_cast<char*>(c.ws);
+  if (c.ws) {
+    if (c.ws_bytes < need)
+      return fail(MUON_ERR_INVALID_ARGUMENT, "the workspace holds %llu bytes; this call needs %zu",
+                  (unsigned long long)c.ws_bytes, need);
+  } else {
+    if (capturing)
+      return fail(MUON_ERR_UNSUPPORTED, "a captured call needs a workspace of the caller's "
+                  "(muon_blocks_workspace_bytes: %zu bytes)", need);
+    if (need > bd->ws_bytes) {
+      if (hipDeviceSynchronize() != hipSuccess)
+        return fail(MUON_ERR_HIP, "hipDeviceSynchronize failed: %s", hipGetErrorString(hipGetLastError()));
+      if (bd->ws) (void)hipFree(bd->ws);
+      bd->ws = nullptr;
+      bd->ws_bytes = 0;
+      void* p = nullptr;
+      if (api_device_alloc(&p, need) != hipSuccess) {
+        (void)hipGetLastError();
+        return fail(MUON_ERR_OUT_OF_MEMORY, "workspace allocation of %zu bytes failed", need);
+      }
+      bd->ws = p;
+      bd->ws_bytes = need;
+    }
+    if (!bd->last && hipEventCreateWithFlags(&bd->last, hipEventDisableTiming) != hipSuccess) {
+      bd->last = nullptr;
+      return fail(MUON_ERR_HIP, "hipEventCreate failed: %s", hipGetErrorString(hipGetLastError()));
+    }
+    if (bd->recorded && hipStreamWaitEvent(c.stream, bd->last, 0) != hipSuccess)
+      return fail(MUON_ERR_HIP, "ordering after the device's previous call failed: %s",
+                  hipGetErrorString(hipGetLastError()));
+    ws = reinterpret_cast<char*>(bd->ws);
+  }
+
+  hipError_t e = hipSuccess;
+  for (const Group& g : groups) {
+    e = enqueue_group(c, g, ws, [&](int kc, auto&& launch) -> hipError_t {
+      return capturing ? launch() : api_timed(kc, c.stream, launch);
+    });
+    if (e != hipSuccess) break;
+  }
+  if (!c.ws && hipEventRecord(bd->last, c.stream) == hipSuccess) bd->recorded = true;
+  if (e != hipSuccess) return fail(MUON_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+  return MUON_OK;
+}
+
+// Nothing crosses the ABI as an exception.
+muon_status guarded(const Call& c) {
+  api_clear_error();
+  try {
+    return run_call(c);
+  } catch (const std::bad_alloc&) {
+    return api_fail(MUON_ERR_OUT_OF_MEMORY, "host memory allocation failed");
+  } catch (...) {
+    return api_fail(MUON_ERR_HIP, "unexpected failure on the host");
+  }
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+muon_status muon_ns_blocks(const void* const* x_in, void* const* x_out, const muon_block_desc* stacks,
+                           int32_t count, muon_ns_coeffs ns_coeffs, int32_t ns_steps,
+                           const muon_ns_coeffs* ns_schedule, void* workspace, uint64_t workspace_bytes,
+                           void* stream) {
+  Call c;
+  c.op = MUON_BLOCKS_NS;
+  c.x = x_in;
+  c.out = x_out;
+  c.stacks = stacks;
+  c.count = count;
+  c.co = ns_coeffs;
+  c.ns_steps = ns_steps;
+  c.schedule = ns_schedule;
+  c.ws = workspace;
+  c.ws_bytes = workspace_bytes;
+  c.stream = reinterpret_cast<hipStream_t>(stream);
+  return guarded(c);
+}
+
+muon_status muon_ns_blocks_vjp(const void* const* x_in, const void* const* grad_out, void* const* grad_in,
+                               const muon_block_desc* stacks, int32_t count, muon_ns_coeffs ns_coeffs,
+                               int32_t ns_steps, const muon_ns_coeffs* ns_schedule, void* workspace,
+                               uint64_t workspace_bytes, void* stream) {
+  Call c;
+  c.op = MUON_BLOCKS_VJP;
+  c.x = x_in;
+  c.y = grad_out;
+  c.out = grad_in;
+  c.stacks = stacks;
+  c.count = count;
+  c.co = ns_coeffs;
+  c.ns_steps = ns_steps;
+  c.schedule = ns_schedule;
+  c.ws = workspace;
+  c.ws_bytes = workspace_bytes;
+  c.stream = reinterpret_cast<hipStream_t>(stream);
+  return guarded(c);
+}
+
+muon_status muon_step_blocks(void* const* params, const void* const* grads, void* const* momenta,
+                             const muon_block_desc* stacks, int32_t count, const muon_step_hparams* hparams,
+                             float* const* updates_out, void* workspace, uint64_t workspace_bytes, void* stream) {
+  Call c;
+  c.op = MUON_BLOCKS_STEP;
+  c.x = grads;
+  c.y = momenta;
+  c.out = params;
+  c.upd = updates_out;
+  c.stacks = stacks;
+  c.count = count;
+  c.hp = hparams;
+  if (hparams) {
+    c.co = hparams->ns_coeffs;
+    c.ns_steps = hparams->ns_steps;
+    c.schedule = hparams->options ? hparams->options->ns_schedule : nullptr;
+  }
+  c.ws = workspace;
+  c.ws_bytes = workspace_bytes;
+  c.stream = reinterpret_cast<hipStream_t>(stream);
+  return guarded(c);
+}
+
+uint64_t muon_blocks_workspace_bytes(int32_t op, const muon_block_desc* stacks, int32_t count,
+                                     muon_ns_coeffs ns_coeffs, int32_t ns_steps,
+                                     const muon_ns_coeffs* ns_schedule) {
+  api_clear_error();
+  if (op < MUON_BLOCKS_NS || op > MUON_BLOCKS_STEP) {
+    (void)fail(MUON_ERR_INVALID_ARGUMENT, "unknown op %d", op);
+    return 0;
+  }
+  try {
+    Call c;
+    c.op = op;
+    c.stacks = stacks;
+    c.count = count;
+    c.co = ns_coeffs;
+    c.ns_steps = ns_steps;
+    c.schedule = ns_schedule;
+    if (count < 0 || count > MAX_COUNT || (count > 0 && !stacks)) {
+      (void)fail(MUON_ERR_INVALID_ARGUMENT, "bad count or NULL stacks");
+      return 0;
+    }
+    if (check_steps(c) != MUON_OK || check_descs(c) != MUON_OK) return 0;
+    std::lock_guard<std::mutex> lock(api_mutex());
+    BlockDevice* bd = nullptr;
+    if (current_device(&bd) != MUON_OK) return 0;
+    std::vector<Group> groups;
+    return plan_groups(c, bd->cus, groups);
+  } catch (...) {
+    (void)api_fail(MUON_ERR_OUT_OF_MEMORY, "host memory allocation failed");
+    return 0;
+  }
+}
+
+}  // extern "C"

@@ -7,3 +7,4 @@ from .muon_oracle import (EPS, StepResult, frobenius_norm, momentum, muon_step, 
                           rel_frobenius, scale_factor, split_bf16x2, to_bf16,
                           write_back)
 from .adamw_oracle import adamw, adamw_constants  # noqa: F401
+from .blocks_oracle import orthogonalise_vjp  # noqa: F401

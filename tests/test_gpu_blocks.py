@@ -1,0 +1,583 @@
+"""The block operators on the GPU against the float64 oracle: orthogonalisation
+of stacks of small blocks, its gradient, and the Muon step on stacks.
+
+Tolerances (relative Frobenius error of one block).  With G the product over
+the steps of max(1, |a|, ...), the growth of a small singular value:
+
+* binary32 results: the values a step stores carry 2^-24 of the iterate's
+  norm, which the later steps multiply by at most G; a result of m rows has
+  norm about sqrt(m).  Some tens of such roundings (Gram sums, P, the apply
+  product) give T32 = 2^-24 (64 + 16 G / sqrt(m)).  A gradient passes the
+  same steps twice, and its Gram product with the cotangent: 4 T32.
+* bfloat16 results: half a step, 2^-8 of the value, plus what one stage of
+  growth up to 512 leaves of the Gram matrix's 2^-24: the Gram error is
+  carried on with the square of the growth at the singular values 1/512 and
+  less, 512^2 2^-24 = 2^-6 in the worst direction, and on a spectrum without
+  a preferred direction 1/sqrt(m) of that in norm, at most 2^-6 / sqrt(m);
+  blocks of a few rows have no singular value that small.  TB = 2^-8 + 2^-9.
+"""
+import ctypes
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as orc
+from muon_newton_schulz_02_amd import binding as mb
+
+from gpu_helpers import CUBIC, MUON, bits, f32, to_np
+
+pytestmark = pytest.mark.gpu
+
+BF, F = torch.bfloat16, torch.float32
+TB = 2.0 ** -8 + 2.0 ** -9
+
+
+def _announce(msg):
+    print(f"[case] {msg}", flush=True)
+    sys.stdout.flush()
+
+
+def _co(coeffs):
+    return np.float32(np.asarray(coeffs, dtype=np.float64)).astype(np.float64)
+
+
+def _gain(coeffs, steps):
+    g = 1.0
+    for a, b, c in orc.schedule(_co(coeffs), steps):
+        g *= max(1.0, max(abs(a + b * x + c * x * x) for x in np.linspace(0, 1.5, 31)))
+    return g
+
+
+def _tol(dtype, m, coeffs, steps, grad=False):
+    if dtype == BF:
+        return TB
+    return 2.0 ** -24 * (64 + 16 * _gain(coeffs, steps) / np.sqrt(m)) * (4 if grad else 1)
+
+
+def _make(blocks, rows, cols, dtype, gen, kind="dense", pad=0, scale=1.0):
+    """A stack view and the tensor it lies in: "dense" blocks in rows, "cols"
+    blocks side by side in the columns, "odd" with an odd element offset."""
+    val = torch.randn(blocks, rows, cols, generator=gen) * scale
+    if kind == "cols":
+        base = torch.full((rows, blocks * cols + pad), 7.0).to(dtype).cuda()
+        view = base[:, :blocks * cols].unflatten(1, (blocks, cols)).transpose(0, 1)
+    elif kind == "odd":
+        flat = torch.full((1 + blocks * rows * (cols + pad) + 5,), 7.0).to(dtype).cuda()
+        base = flat
+        view = flat[1:1 + blocks * rows * (cols + pad)].view(blocks, rows, cols + pad)[:, :, :cols]
+    else:
+        base = torch.full((blocks, rows, cols + pad), 7.0).to(dtype).cuda()
+        view = base[:, :, :cols]
+    view.copy_(val.to(dtype))
+    return view, base
+
+
+def _untouched(view, base):
+    """Every element of `base` outside `view` still holds 7."""
+    rest = base.clone()
+    rest.as_strided(view.shape, view.stride(), view.storage_offset()).fill_(7.0)
+    assert bool((rest == 7.0).all()), "elements outside the blocks were written"
+
+
+def _check_blocks(got, ref, tol, what):
+    got = to_np(got)
+    for b in range(len(ref)):
+        e, n = np.linalg.norm(got[b] - ref[b]), np.linalg.norm(ref[b])
+        assert np.isfinite(got[b]).all() and e <= tol * n, f"{what} block {b}: {e / max(n, 1e-300):.3e} > {tol:.3e}"
+
+
+SHAPES = [
+    # blocks, rows, cols, kind, pad
+    (1, 1, 1, "dense", 0),
+    (3, 1, 64, "dense", 0),
+    (3, 64, 1, "dense", 0),
+    (5, 2, 7, "odd", 1),
+    (2, 15, 300, "dense", 0),
+    (2, 16, 257, "odd", 0),
+    (2, 300, 17, "dense", 3),
+    (3, 31, 129, "cols", 0),
+    (3, 129, 32, "cols", 0),
+    (3, 200, 33, "cols", 5),
+    (2, 33, 40, "dense", 0),
+    (2, 48, 48, "odd", 3),
+    (2, 63, 1000, "dense", 8),
+    (2, 64, 64, "dense", 0),
+    (12, 64, 768, "dense", 0),
+    (2, 65, 96, "dense", 0),
+    (2, 90, 1111, "dense", 5),
+    (2, 1111, 90, "cols", 2),
+    (3, 127, 255, "odd", 0),
+    (2, 128, 1536, "dense", 0),
+    (2, 1536, 128, "cols", 0),
+    (1, 128, 128, "dense", 0),
+    (2, 4097, 5, "dense", 0),
+]
+
+
+def _run_ns(x, out, coeffs, steps, **kw):
+    mb.muon_ns_blocks([x], [out], ns_coeffs=coeffs if np.ndim(coeffs) == 1 else coeffs[0], ns_steps=steps,
+                      ns_schedule=None if np.ndim(coeffs) == 1 else coeffs, **kw)
+
+
+def _run_vjp(x, y, dx, coeffs, steps, **kw):
+    mb.muon_ns_blocks_vjp([x], [y], [dx], ns_coeffs=coeffs if np.ndim(coeffs) == 1 else coeffs[0], ns_steps=steps,
+                          ns_schedule=None if np.ndim(coeffs) == 1 else coeffs, **kw)
+
+
+@pytest.mark.parametrize("xdt,odt", [(BF, BF), (F, F), (F, BF), (BF, F)])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"{s[0]}x{s[1]}x{s[2]}-{s[3]}{s[4]}")
+def test_ns_shapes(shape, xdt, odt):
+    blocks, rows, cols, kind, pad = shape
+    _announce(f"ns {shape} {xdt} {odt}")
+    gen = torch.Generator().manual_seed(rows * 7 + cols)
+    x, _ = _make(blocks, rows, cols, xdt, gen, kind, pad)
+    out, base = _make(blocks, rows, cols, odt, gen, kind, pad)
+    _run_ns(x, out, MUON, 5)
+    torch.cuda.synchronize()
+    ref = [orc.orthogonalise(v, _co(MUON), 5) for v in to_np(x)]
+    _check_blocks(out, ref, _tol(odt, min(rows, cols), MUON, 5), "NS")
+    _untouched(out, base)
+
+
+@pytest.mark.parametrize("xdt,odt", [(BF, BF), (F, F), (F, BF), (BF, F)])
+@pytest.mark.parametrize("shape", SHAPES[1:], ids=lambda s: f"{s[0]}x{s[1]}x{s[2]}-{s[3]}{s[4]}")
+def test_vjp_shapes(shape, xdt, odt):
+    blocks, rows, cols, kind, pad = shape
+    _announce(f"vjp {shape} {xdt} {odt}")
+    gen = torch.Generator().manual_seed(rows * 7 + cols + 1)
+    x, _ = _make(blocks, rows, cols, xdt, gen, kind, pad)
+    y, _ = _make(blocks, rows, cols, xdt, gen, kind, pad)
+    dx, base = _make(blocks, rows, cols, odt, gen, kind, pad)
+    _run_vjp(x, y, dx, MUON, 5)
+    torch.cuda.synchronize()
+    ref = [orc.orthogonalise_vjp(v, w, _co(MUON), 5) for v, w in zip(to_np(x), to_np(y))]
+    _check_blocks(dx, ref, _tol(odt, min(rows, cols), MUON, 5, grad=True), "gradient")
+    _untouched(dx, base)
+
+
+SCHEDULE = [(2.0, -1.5, 0.5), (1.5, -0.5, 0.0), MUON, (15 / 8, -5 / 4, 3 / 8)]
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("coeffs,steps", [(MUON, 0), (MUON, 1), (MUON, 2), (MUON, 10), (CUBIC, 1), (CUBIC, 12),
+                                          (SCHEDULE, 4), ([CUBIC] * 40, 40)],
+                         ids=lambda v: str(v) if isinstance(v, int) else "s" if np.ndim(v) > 1 else f"{v[0]}")
+def test_steps_and_schedules(coeffs, steps, dt):
+    _announce(f"steps {steps} {coeffs[:1]} {dt}")
+    gen = torch.Generator().manual_seed(steps)
+    for rows, cols in ((20, 100), (100, 700), (300, 50)):
+        x, _ = _make(3, rows, cols, dt, gen, scale=1e-3)
+        y, _ = _make(3, rows, cols, dt, gen)
+        out, dx = torch.empty_like(x), torch.empty_like(x)
+        _run_ns(x, out, coeffs, steps)
+        _run_vjp(x, y, dx, coeffs, steps)
+        torch.cuda.synchronize()
+        xs, ys = to_np(x), to_np(y)
+        m = min(rows, cols)
+        _check_blocks(out, [orc.orthogonalise(v, _co(coeffs), steps) for v in xs], _tol(dt, m, coeffs, steps), "NS")
+        _check_blocks(dx, [orc.orthogonalise_vjp(v, w, _co(coeffs), steps) for v, w in zip(xs, ys)],
+                      _tol(dt, m, coeffs, steps, grad=True), "gradient")
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("power", [1.0, 2.0])
+def test_decaying_spectra(dt, power):
+    """Singular values i^-power: the smallest grow by the whole gain."""
+    _announce(f"spectra {power} {dt}")
+    gen = torch.Generator().manual_seed(5)
+    m, n = 96, 400
+    u = torch.linalg.qr(torch.randn(2, m, m, generator=gen, dtype=torch.float64))[0]
+    v = torch.linalg.qr(torch.randn(2, n, m, generator=gen, dtype=torch.float64))[0]
+    s = torch.arange(1, m + 1, dtype=torch.float64) ** -power
+    x = ((u * s) @ v.transpose(1, 2)).to(dt).cuda()
+    y = torch.randn(2, m, n, generator=gen).to(dt).cuda()
+    out, dx = torch.empty_like(x), torch.empty_like(x)
+    _run_ns(x, out, MUON, 5)
+    _run_vjp(x, y, dx, MUON, 5)
+    torch.cuda.synchronize()
+    _check_blocks(out, [orc.orthogonalise(v, _co(MUON), 5) for v in to_np(x)], _tol(dt, m, MUON, 5), "NS")
+    _check_blocks(dx, [orc.orthogonalise_vjp(v, w, _co(MUON), 5) for v, w in zip(to_np(x), to_np(y))],
+                  _tol(dt, m, MUON, 5, grad=True), "gradient")
+
+
+def test_gradient_against_differences():
+    """<dx, d> against central differences of the library's own forward pass (binary32)."""
+    _announce("differences")
+    gen = torch.Generator().manual_seed(9)
+    x = torch.randn(2, 24, 200, generator=gen).cuda()
+    y = torch.randn(2, 24, 200, generator=gen).cuda()
+    dx, o1, o2 = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    _run_vjp(x, y, dx, MUON, 5)
+    for k in range(4):
+        d = torch.randn(2, 24, 200, generator=gen).cuda()
+        h = 2.0 ** -7
+        _run_ns(x + h * d, o1, MUON, 5)
+        _run_ns(x - h * d, o2, MUON, 5)
+        torch.cuda.synchronize()
+        fd = ((o1 - o2).double() * y.double()).sum((1, 2)) / (2 * h)
+        an = (dx.double() * d.double()).sum((1, 2))
+        # the outputs are off by T32 of their norm sqrt(24), against y of norm
+        # sqrt(24 * 200) in a random direction: about T32 sqrt(24); truncation
+        # h^2 times the third derivative along d (relative size 1/14 of x)
+        lim = _tol(F, 24, MUON, 5) * 24 ** 0.5 * 4 / h + h * h * dx.double().norm().item() * d.double().norm().item()
+        assert (fd - an).abs().max().item() <= lim
+
+
+def test_zero_nan_and_infinite_blocks_stay_apart():
+    _announce("non-finite blocks")
+    gen = torch.Generator().manual_seed(2)
+    for dt in (BF, F):
+        for rows, cols in ((64, 200), (200, 20)):
+            x, _ = _make(5, rows, cols, dt, gen)
+            y, _ = _make(5, rows, cols, dt, gen)
+            x[1] = 0
+            x[2, 3, 4] = float("nan")
+            x[3, rows - 1, cols - 1] = float("inf")
+            out, dx = torch.empty_like(x), torch.empty_like(x)
+            _run_ns(x, out, MUON, 5)
+            _run_vjp(x, y, dx, MUON, 5)
+            torch.cuda.synchronize()
+            xs, ys, m = to_np(x), to_np(y), min(rows, cols)
+            for b in (0, 4):
+                _check_blocks(out[b:b + 1], [orc.orthogonalise(xs[b], _co(MUON), 5)], _tol(dt, m, MUON, 5), "NS")
+                _check_blocks(dx[b:b + 1], [orc.orthogonalise_vjp(xs[b], ys[b], _co(MUON), 5)],
+                              _tol(dt, m, MUON, 5, grad=True), "gradient")
+            assert bool((out[1] == 0).all())
+            _check_blocks(dx[1:2], [orc.orthogonalise_vjp(xs[1], ys[1], _co(MUON), 5)], _tol(dt, m, MUON, 5, True), "0")
+            for b in (2, 3):
+                assert bool(out[b].isnan().all()) and bool(dx[b].isnan().all())
+
+
+def test_tiny_and_large_scales():
+    """NS(s x) for s from 2^-40 to 2^40: eps matters below, nothing above."""
+    _announce("scales")
+    gen = torch.Generator().manual_seed(3)
+    x0 = torch.randn(2, 40, 90, generator=gen)
+    for e in (-40, -20, 20, 40):
+        for dt in (BF, F):
+            x = (x0 * 2.0 ** e).to(dt).cuda()
+            out = torch.empty(2, 40, 90, dtype=F, device="cuda")
+            _run_ns(x, out, MUON, 5)
+            torch.cuda.synchronize()
+            _check_blocks(out, [orc.orthogonalise(v, _co(MUON), 5) for v in to_np(x)], _tol(F, 40, MUON, 5), "NS")
+
+
+def _many(seed, dt, count=37):
+    gen = torch.Generator().manual_seed(seed)
+    xs, ys = [], []
+    for i in range(count):
+        blocks, rows, cols = 1 + i % 4, (8, 40, 128, 300)[i % 4], (100, 40, 200, 64)[(i // 2) % 4]
+        if min(rows, cols) > 128:
+            cols = 100
+        xs.append(torch.randn(blocks, rows, cols, generator=gen).to(dt).cuda())
+        ys.append(torch.randn(blocks, rows, cols, generator=gen).to(dt).cuda())
+    return xs, ys
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+def test_many_stacks_of_mixed_sizes(dt):
+    """More stacks than a launch carries in its arguments, in several groups; an empty stack among them."""
+    _announce(f"many stacks {dt}")
+    xs, ys = _many(4, dt)
+    xs.insert(5, torch.empty(0, 8, 100, dtype=dt, device="cuda"))
+    ys.insert(5, torch.empty(0, 8, 100, dtype=dt, device="cuda"))
+    outs, dxs = [torch.empty_like(x) for x in xs], [torch.empty_like(x) for x in xs]
+    mb.muon_ns_blocks(xs, outs, ns_coeffs=MUON, ns_steps=5)
+    mb.muon_ns_blocks_vjp(xs, ys, dxs, ns_coeffs=MUON, ns_steps=5)
+    torch.cuda.synchronize()
+    for x, y, o, d in zip(xs, ys, outs, dxs):
+        m = min(x.shape[1:])
+        _check_blocks(o, [orc.orthogonalise(v, _co(MUON), 5) for v in to_np(x)], _tol(dt, m, MUON, 5), "NS")
+        _check_blocks(d, [orc.orthogonalise_vjp(v, w, _co(MUON), 5) for v, w in zip(to_np(x), to_np(y))],
+                      _tol(dt, m, MUON, 5, grad=True), "gradient")
+
+
+def test_shared_and_broadcast_inputs():
+    """One block read by every block of a stack (stride 0), one cotangent for all."""
+    _announce("broadcast")
+    gen = torch.Generator().manual_seed(6)
+    x1, y1 = torch.randn(1, 30, 70, generator=gen).cuda(), torch.randn(1, 30, 70, generator=gen).cuda()
+    x, y = x1.expand(4, 30, 70), y1.expand(4, 30, 70)
+    out, dx = torch.empty(4, 30, 70, device="cuda"), torch.empty(4, 30, 70, device="cuda")
+    _run_ns(x, out, MUON, 5)
+    _run_vjp(x, y, dx, MUON, 5)
+    torch.cuda.synchronize()
+    _check_blocks(out, [orc.orthogonalise(to_np(x1)[0], _co(MUON), 5)] * 4, _tol(F, 30, MUON, 5), "NS")
+    _check_blocks(dx, [orc.orthogonalise_vjp(to_np(x1)[0], to_np(y1)[0], _co(MUON), 5)] * 4,
+                  _tol(F, 30, MUON, 5, grad=True), "gradient")
+
+
+# ------------------------------------------------------------------ the step
+
+def _step_case(shape, wdt, gdt, seed, count=1):
+    blocks, rows, cols, kind, pad = shape
+    gen = torch.Generator().manual_seed(seed)
+    st = []
+    for _ in range(count):
+        w, wb = _make(blocks, rows, cols, wdt, gen, kind, pad, 0.02)
+        g, _ = _make(blocks, rows, cols, gdt, gen, kind, pad)
+        m, mbase = _make(blocks, rows, cols, F, gen, kind, pad)
+        st.append((w, g, m, wb, mbase))
+    return st
+
+
+def _check_step_stack(w0, g0, m0, w, m, o, *, lr, beta, nesterov, coeffs, steps, scale, wd, kind, wdt):
+    for b in range(w0.shape[0]):
+        m_ref, u = orc.momentum(m0[b], g0[b], beta, bool(nesterov), kind)
+        assert np.array_equal(bits(m[b]), bits(m_ref)), "momentum not bit-exact"
+        ref = orc.orthogonalise(u, _co(coeffs), steps)
+        tol = TB if wdt == BF else _tol(F, min(ref.shape), coeffs, steps)
+        e = orc.rel_frobenius(o[b], ref)
+        assert e <= tol, f"update of block {b}: {e:.3e} > {tol:.3e}"
+        w_ref = orc.write_back(w0[b], o[b], lr, scale, wdt == BF, wd)
+        assert np.array_equal(bits(w[b]), bits(w_ref)), "write-back not bit-exact given O"
+
+
+@pytest.mark.parametrize("wdt,gdt", [(BF, BF), (F, F), (BF, F), (F, BF)])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"{s[0]}x{s[1]}x{s[2]}-{s[3]}{s[4]}")
+def test_step_shapes(shape, wdt, gdt):
+    _announce(f"step {shape} {wdt} {gdt}")
+    lr = f32(0.02)
+    (w, g, m, wb, mbase), = _step_case(shape, wdt, gdt, shape[1] * 3 + shape[2])
+    w0, g0, m0 = to_np(w), to_np(g), to_np(m)
+    o = torch.full(tuple(w.shape), float("nan"), device="cuda")
+    mb.muon_step_blocks([w], [g], [m], lr=lr, beta=0.95, nesterov=True, ns_coeffs=MUON, ns_steps=5, updates_out=[o])
+    torch.cuda.synchronize()
+    _check_step_stack(w0, g0, m0, to_np(w), to_np(m), to_np(o), lr=lr, beta=f32(0.95), nesterov=1, coeffs=MUON,
+                      steps=5, scale=1.0, wd=0.0, kind=0, wdt=wdt)
+    _untouched(w, wb)
+    _untouched(m, mbase)
+
+
+@pytest.mark.parametrize("wdt", [BF, F])
+@pytest.mark.parametrize("nesterov", [0, 1])
+@pytest.mark.parametrize("kind", [0, 1])
+def test_step_variants(wdt, nesterov, kind):
+    """EMA, plain momentum, weight decay, scale rules, per-stack rates and scales, schedules, no steps."""
+    _announce(f"step variants {wdt} {nesterov} {kind}")
+    cases = [
+        dict(scale_rule=mb.SCALE_RMS_MATCH, weight_decay=f32(0.1)),
+        dict(scale_rule=mb.SCALE_SQRT_ASPECT, lr_per_stack=[f32(0.01), f32(0.03)]),
+        dict(scale_per_stack=[f32(0.5), f32(2.0)], weight_decay=f32(0.01), ns_schedule=SCHEDULE),
+        dict(steps=0),
+        dict(steps=10),
+    ]
+    for i, kw in enumerate(cases):
+        st = _step_case((3, 200, 48, "cols", 0), wdt, BF, 50 + i) + _step_case((2, 60, 129, "dense", 3), wdt, BF, 60 + i)
+        before = [tuple(to_np(t) for t in s[:3]) for s in st]
+        outs = [torch.full(tuple(s[0].shape), float("nan"), device="cuda") for s in st]
+        kw = dict(kw)
+        steps = kw.pop("steps", len(kw["ns_schedule"]) if "ns_schedule" in kw else 5)
+        mb.muon_step_blocks([s[0] for s in st], [s[1] for s in st], [s[2] for s in st], lr=f32(0.02), beta=f32(0.9),
+                            nesterov=nesterov, ns_coeffs=MUON, ns_steps=steps, momentum_kind=kind,
+                            updates_out=outs, **kw)
+        torch.cuda.synchronize()
+        for k, (s, (w0, g0, m0)) in enumerate(zip(st, before)):
+            lr = kw["lr_per_stack"][k] if "lr_per_stack" in kw else f32(0.02)
+            sc = kw["scale_per_stack"][k] if "scale_per_stack" in kw else \
+                orc.scale_factor(kw.get("scale_rule", 0), *w0.shape[1:])
+            _check_step_stack(w0, g0, m0, to_np(s[0]), to_np(s[2]), to_np(outs[k]), lr=lr, beta=f32(0.9),
+                              nesterov=nesterov, coeffs=kw.get("ns_schedule", MUON), steps=steps, scale=sc,
+                              wd=kw.get("weight_decay", 0.0), kind=kind, wdt=wdt)
+
+
+def test_step_is_ns_of_the_momentum():
+    """The step's exported update equals muon_ns_blocks of U with binary32 results, and
+    muon_step_batched on the same blocks gives the same momentum and nearly the same weights."""
+    _announce("step against ns and against the whole-matrix step")
+    lr = f32(0.02)
+    (w, g, m, _, _), = _step_case((4, 128, 512, "dense", 0), F, F, 77)
+    w2, m2 = w.clone(), m.clone()
+    o = torch.empty(4, 128, 512, device="cuda")
+    mb.muon_step_blocks([w], [g], [m], lr=lr, beta=0.95, nesterov=False, ns_coeffs=MUON, ns_steps=5, updates_out=[o])
+    ns = torch.empty_like(o)
+    _run_ns(m, ns, MUON, 5)  # without Nesterov U is the updated momentum
+    mb.muon_step_batched(list(w2), list(g), list(m2), lr=lr, beta=0.95, nesterov=False, ns_coeffs=MUON, ns_steps=5,
+                         precision=mb.NS_F32)
+    torch.cuda.synchronize()
+    assert torch.equal(o, ns)
+    assert torch.equal(m, m2)
+    t = _tol(F, 128, MUON, 5)
+    assert ((w - w2).norm() / (lr * o.norm())).item() <= t + 1e-4  # muon_step_batched's own binary32 gate
+
+
+# ------------------------------------------- streams, graphs and workspaces
+
+def _bits(t):
+    return t.contiguous().view(torch.int16 if t.dtype == BF else torch.int32).cpu().numpy()
+
+
+def test_same_call_same_bits():
+    _announce("determinism")
+    xs, ys = _many(8, BF, 20)
+    outs = []
+    for _ in range(3):
+        o, d = [torch.empty_like(x) for x in xs], [torch.empty_like(x) for x in xs]
+        mb.muon_ns_blocks(xs, o, ns_coeffs=MUON, ns_steps=5)
+        mb.muon_ns_blocks_vjp(xs, ys, d, ns_coeffs=MUON, ns_steps=5)
+        torch.cuda.synchronize()
+        outs.append([_bits(t) for t in o + d])
+    for other in outs[1:]:
+        assert all(np.array_equal(a, b) for a, b in zip(outs[0], other))
+
+
+def test_calls_on_two_streams_run_in_call_order():
+    """The library's workspace is one per device: calls on two streams follow each other."""
+    _announce("two streams")
+    xs, ys = _many(11, BF, 24)
+    ref = [torch.empty_like(x) for x in xs]
+    refd = [torch.empty_like(x) for x in xs]
+    mb.muon_ns_blocks(xs, ref, ns_coeffs=MUON, ns_steps=5)
+    torch.cuda.synchronize()
+    mb.muon_ns_blocks_vjp(xs, ys, refd, ns_coeffs=MUON, ns_steps=5)
+    torch.cuda.synchronize()
+    sink = torch.zeros(1, device="cuda")
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    out, dx = [torch.zeros_like(x) for x in xs], [torch.zeros_like(x) for x in xs]
+    torch.cuda.synchronize()
+    mb.muon_mfma_probe(200_000, sink, stream=s1)
+    mb.muon_ns_blocks(xs, out, ns_coeffs=MUON, ns_steps=5, stream=s1)
+    mb.muon_ns_blocks_vjp(xs, ys, dx, ns_coeffs=MUON, ns_steps=5, stream=s2)
+    torch.cuda.synchronize()
+    assert all(np.array_equal(_bits(a), _bits(b)) for a, b in zip(out + dx, ref + refd))
+
+
+def _workspace(args, steps=5, extra=0, **kw):
+    return torch.empty(args.workspace_bytes(ns_coeffs=MUON, ns_steps=steps, **kw) + extra, dtype=torch.uint8,
+                       device="cuda")
+
+
+def test_own_workspace_and_its_size():
+    _announce("own workspace")
+    xs, ys = _many(12, F, 20)
+    ref, out = [torch.empty_like(x) for x in xs], [torch.empty_like(x) for x in xs]
+    mb.muon_ns_blocks_vjp(xs, ys, ref, ns_coeffs=MUON, ns_steps=5)
+    args = mb.VjpBlocksArgs(xs, ys, out)
+    ws = _workspace(args, extra=4096)
+    n = ws.numel() - 4096
+    ws.fill_(0xA5)
+    mb.muon_ns_blocks_vjp(args, ns_coeffs=MUON, ns_steps=5, workspace=ws[:n])
+    torch.cuda.synchronize()
+    assert all(np.array_equal(_bits(a), _bits(b)) for a, b in zip(out, ref))
+    assert bool((ws[n:] == 0xA5).all()), "written past the workspace"
+    with pytest.raises(mb.MuonError, match="INVALID_ARGUMENT"):
+        mb.muon_ns_blocks_vjp(args, ns_coeffs=MUON, ns_steps=5, workspace=ws[:n - 256])
+    with pytest.raises(mb.MuonError, match="UNSUPPORTED"):
+        mb.muon_ns_blocks_vjp(args, ns_coeffs=MUON, ns_steps=5, workspace=ws[64:])
+
+
+def test_captured_calls():
+    """Two graphs with workspaces of their own, replayed several times between eager calls."""
+    _announce("graphs")
+    xs, ys = _many(13, BF, 20)
+    outs = [torch.empty_like(x) for x in xs]
+    dxs = [torch.empty_like(x) for x in xs]
+    st = _step_case((12, 64, 768, "dense", 0), BF, BF, 14, count=3)
+    w, g, m = ([s[k] for s in st] for k in range(3))
+    hp = dict(lr=f32(0.02), beta=0.95, nesterov=True, ns_coeffs=MUON, ns_steps=5)
+    a1, a2, a3 = mb.NsBlocksArgs(xs, outs), mb.VjpBlocksArgs(xs, ys, dxs), mb.StepBlocksArgs(w, g, m)
+    ws1, ws2 = _workspace(a1), torch.empty(max(_workspace(a).numel() for a in (a2, a3)), dtype=torch.uint8,
+                                           device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with pytest.raises(mb.MuonError, match="UNSUPPORTED"):
+        bad = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(bad, stream=s):
+            mb.muon_ns_blocks(a1, ns_coeffs=MUON, ns_steps=5)
+    torch.cuda.synchronize()
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1, stream=s):
+        mb.muon_ns_blocks(a1, ns_coeffs=MUON, ns_steps=5, workspace=ws1)
+    with torch.cuda.graph(g2, stream=s):
+        mb.muon_ns_blocks_vjp(a2, ns_coeffs=MUON, ns_steps=5, workspace=ws2)
+        mb.muon_step_blocks(a3, workspace=ws2, **hp)
+    # the same calls eagerly on copies, with the library's workspace
+    we, me = [t.clone() for t in w], [t.clone() for t in m]
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for k in range(4):
+        for x in xs + ys:
+            x.mul_(1.25 if k % 2 else -0.5)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side[0]):
+            g1.replay()
+        with torch.cuda.stream(side[1]):
+            g2.replay()
+        ref, refd = [torch.empty_like(x) for x in xs], [torch.empty_like(x) for x in xs]
+        mb.muon_ns_blocks(xs, ref, ns_coeffs=MUON, ns_steps=5)
+        mb.muon_ns_blocks_vjp(xs, ys, refd, ns_coeffs=MUON, ns_steps=5)
+        mb.muon_step_blocks(we, g, me, **hp)
+        torch.cuda.synchronize()
+        for a, b in zip(outs + dxs + w + m, ref + refd + we + me):
+            assert np.array_equal(_bits(a), _bits(b)), f"replay {k}"
+
+
+def test_fault_hook_changes_nothing(monkeypatch):
+    _announce("allocation failure")
+    x = torch.randn(3, 50, 80).cuda()
+    out = torch.full((3, 50, 80), 3.0, device="cuda")
+    torch.cuda.synchronize()
+    mb.muon_release_workspace()
+    monkeypatch.setenv("MUON_FAULT_ALLOC", "1")
+    with pytest.raises(mb.MuonError, match="OUT_OF_MEMORY"):
+        _run_ns(x, out, MUON, 5)
+    torch.cuda.synchronize()
+    assert bool((out == 3.0).all())
+    monkeypatch.delenv("MUON_FAULT_ALLOC")
+    _run_ns(x, out, MUON, 5)
+    torch.cuda.synchronize()
+    _check_blocks(out, [orc.orthogonalise(v, _co(MUON), 5) for v in to_np(x)], _tol(F, 50, MUON, 5), "NS")
+
+
+def test_training_with_heads_and_the_rest():
+    """A run of them together: the attention heads of a layer by muon_step_blocks, its MLP by
+    muon_step_batched, the embedding by muon_adamw_batched, three steps; and the gradient of the
+    heads' orthogonalisation as a weight parametrisation."""
+    _announce("together")
+    gen = torch.Generator().manual_seed(21)
+    heads, dim, width = 4, 32, 96
+    q = (torch.randn(heads * dim, width, generator=gen) * 0.1).cuda()
+    o = (torch.randn(width, heads * dim, generator=gen) * 0.1).cuda()
+    up = (torch.randn(2 * width, width, generator=gen) * 0.1).cuda()
+    emb = (torch.randn(50, width, generator=gen) * 0.1).cuda()
+    mom = [torch.zeros_like(t) for t in (q, o, up)]
+    av, sq = torch.zeros_like(emb), torch.zeros_like(emb)
+
+    def rows(t):
+        return t.view(heads, dim, width)
+
+    def cols(t):
+        return t.unflatten(1, (heads, dim)).transpose(0, 1)
+
+    ref = {"q": to_np(q), "o": to_np(o), "mq": to_np(mom[0]), "mo": to_np(mom[1])}
+    hp = dict(lr=f32(0.02), beta=f32(0.95), nesterov=True, ns_coeffs=MUON, ns_steps=5)
+    for step in range(1, 4):
+        gs = [torch.randn(t.shape, generator=gen).cuda() for t in (q, o, up, emb)]
+        mb.muon_step_blocks([rows(q), cols(o)], [rows(gs[0]), cols(gs[1])], [rows(mom[0]), cols(mom[1])],
+                            weight_decay=f32(0.1), **hp)
+        mb.muon_step_batched([up], [gs[2]], [mom[2]], precision=mb.NS_F32, **hp)
+        mb.muon_adamw_batched([emb], [gs[3]], [av], [sq], lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, step=step)
+        torch.cuda.synchronize()
+        gq, go = to_np(gs[0]), to_np(gs[1])
+        for h in range(heads):
+            for name, mname, g, sl in (("q", "mq", gq, np.s_[h * dim:(h + 1) * dim, :]),
+                                       ("o", "mo", go, np.s_[:, h * dim:(h + 1) * dim])):
+                r = orc.muon_step(ref[name][sl], g[sl], ref[mname][sl], lr=hp["lr"], beta=hp["beta"], nesterov=True,
+                                  coeffs=_co(MUON), steps=5, weight_decay=f32(0.1), param_bf16=False)
+                ref[name][sl], ref[mname][sl] = r.w, r.m
+        for name, t in (("q", q), ("o", o)):
+            # three updates of norm lr |O|, each off by T32
+            lim = 3 * hp["lr"] * _tol(F, dim, MUON, 5) * np.sqrt(heads * dim) * 2 + 1e-6 * np.linalg.norm(ref[name])
+            assert np.linalg.norm(to_np(t) - ref[name]) <= lim
+    # q as NS(v), loss <NS(v) t, t'>: the gradient with respect to v
+    t, t2 = torch.randn(width, 7, generator=gen).cuda(), torch.randn(heads * dim, 7, generator=gen).cuda()
+    out, dv = torch.empty_like(q), torch.empty_like(q)
+    mb.muon_ns_blocks([rows(q)], [rows(out)], ns_coeffs=MUON, ns_steps=5)
+    mb.muon_ns_blocks_vjp([rows(q)], [rows(t2 @ t.T)], [rows(dv)], ns_coeffs=MUON, ns_steps=5)
+    torch.cuda.synchronize()
+    qn, yn = to_np(q), to_np(t2 @ t.T)
+    for h in range(heads):
+        sl = np.s_[h * dim:(h + 1) * dim]
+        _check_blocks(dv[None, sl], [orc.orthogonalise_vjp(qn[sl], yn[sl], _co(MUON), 5)],
+                      _tol(F, dim, MUON, 5, grad=True), "gradient")
