@@ -7,12 +7,22 @@
 // every matrix is a function of A_0, so the order of factors is free and the
 // derivative is its own adjoint.
 //
-// Wave w of MT holds column panel w (16 columns) of every matrix in its
-// registers, as the MT accumulator tiles of v_mfma_f32_16x16x4f32: such a
-// tile is at the same time the B operand of the next product with k taken in
-// the order 16 kt + 4 (lane / 16) + v, so a product L R only needs L in LDS,
-// read along its rows 16 bytes a lane.  Within a step the left factors are A
-// (and D), then Q (and dQ).
+// Products run on v_mfma_f32_16x16x32_f16 with every operand split into two
+// binary16 parts (22 bits) and three products, hi*hi + hi*lo + lo*hi, summed
+// in binary32.  A panel of 16 columns is scaled by a power of two first, so
+// that its largest element lies in [2^14, 2^15): parts of smaller elements
+// then stay exact down to 2^-39 of it, and no matrix overflows the format.
+// Against binary32 products (v_mfma_f32_16x16x4f32) the results' errors are
+// the same to a factor of 1.3 (they come from the Gram matrix), at 3/16 of
+// the matrix-core time: 48 blocks of 128 x 1536, 161 us before.
+//
+// Wave w of MT holds column panel w of every matrix in its registers, as the
+// accumulator tiles of the products.  Two such tiles, one above the other,
+// are at the same time the B operand of a later product's k-step of 32, with
+// k taken in the order 32 kk + {4 g + v, 16 + 4 g + v} (g = lane / 16).  A
+// product L R therefore needs only L in LDS, and as every matrix is symmetric
+// but for rounding, row i of L is column i: the operand registers are stored
+// as they are, 16 bytes a lane, and read back the same way by every wave.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -25,16 +35,117 @@ namespace {
 
 constexpr float NORM_EPS = 1e-7f;
 
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+
+// A column panel as product operand: hi and lo parts per k-step of 32, and
+// the power of two the values were multiplied with (the same in all lanes).
+template <int MT>
+struct Operand {
+  f16x8_t f[MT / 2][2];
+  int ex;
+};
+
+// The largest bits of a non-negative float over the wave, in a scalar register.
+__device__ __forceinline__ uint32_t wave_max_bits(float v) {
+  // rows of 16 lanes by rotation, then the four rows
+#define MUON_ROW_MAX(ctl) \
+  v = fmaxf(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, int(__float_as_uint(v)), ctl, 0xF, 0xF, false)))
+  MUON_ROW_MAX(0x128);  // row_ror:8
+  MUON_ROW_MAX(0x124);
+  MUON_ROW_MAX(0x122);
+  MUON_ROW_MAX(0x121);
+#undef MUON_ROW_MAX
+  const uint32_t b = __float_as_uint(v);
+  uint32_t m = __builtin_amdgcn_readlane(b, 0);
+  m = max(m, uint32_t(__builtin_amdgcn_readlane(b, 16)));
+  m = max(m, uint32_t(__builtin_amdgcn_readlane(b, 32)));
+  return max(m, uint32_t(__builtin_amdgcn_readlane(b, 48)));
+}
+
+template <int MT>
+__device__ __forceinline__ void split_panel(const f32x4_t (&X)[MT], Operand<MT>& o) {
+  float mx = 0.f;
+#pragma unroll
+  for (int kt = 0; kt < MT; ++kt)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) mx = fmaxf(mx, __builtin_fabsf(X[kt][v]));
+  // mx in [2^e, 2^(e + 1)) goes to [2^14, 2^15) (subnormals and zero below it)
+  o.ex = 14 + 127 - int(wave_max_bits(mx) >> 23);
+#pragma unroll
+  for (int kk = 0; kk < MT / 2; ++kk) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int v = 0; v < 4; v += 2) {
+        const f32x2_t x = {__builtin_amdgcn_ldexpf(X[2 * kk + h][v], o.ex),
+                           __builtin_amdgcn_ldexpf(X[2 * kk + h][v + 1], o.ex)};
+        const f16x2_t hi = __builtin_convertvector(x, f16x2_t);
+        const f32x2_t rest = {x[0] - float(hi[0]), x[1] - float(hi[1])};
+        const f16x2_t lo = __builtin_convertvector(rest, f16x2_t);
+        o.f[kk][0][4 * h + v] = hi[0];
+        o.f[kk][0][4 * h + v + 1] = hi[1];
+        o.f[kk][1][4 * h + v] = lo[0];
+        o.f[kk][1][4 * h + v + 1] = lo[1];
+      }
+  }
+}
+
+// A matrix in LDS: row i holds column i of the matrix, two parts.
+template <int MT>
+struct Left {
+  uint16_t v[2][16 * MT][16 * MT + 8];
+  int32_t ex[MT];
+};
+
+template <int MT>
+__device__ __forceinline__ void put_panel(Left<MT>& L, const Operand<MT>& o, int panel, int r, int g, int lane) {
+#pragma unroll
+  for (int kk = 0; kk < MT / 2; ++kk)
+#pragma unroll
+    for (int l = 0; l < 2; ++l)
+      *reinterpret_cast<f16x8_t*>(&L.v[l][16 * panel + r][32 * kk + 8 * g]) = o.f[kk][l];
+  if (lane == 0) L.ex[panel] = o.ex;
+}
+
+// acc = L X for the wave's panel X: MT independent sums.
+template <int MT>
+__device__ __forceinline__ void multiply(f32x4_t (&acc)[MT], const Left<MT>& L, const Operand<MT>& X, int r, int g) {
+#pragma unroll
+  for (int jt = 0; jt < MT; ++jt) acc[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int kk = 0; kk < MT / 2; ++kk) {
+#pragma unroll
+    for (int jt = 0; jt < MT; ++jt) {
+      const f16x8_t hi = *reinterpret_cast<const f16x8_t*>(&L.v[0][16 * jt + r][32 * kk + 8 * g]);
+      const f16x8_t lo = *reinterpret_cast<const f16x8_t*>(&L.v[1][16 * jt + r][32 * kk + 8 * g]);
+      acc[jt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, X.f[kk][0], acc[jt], 0, 0, 0);
+      acc[jt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, X.f[kk][1], acc[jt], 0, 0, 0);
+      acc[jt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, X.f[kk][0], acc[jt], 0, 0, 0);
+    }
+    if (MT >= 4) __builtin_amdgcn_sched_barrier(0);  // bounds how far the reads of L are hoisted
+  }
+#pragma unroll
+  for (int jt = 0; jt < MT; ++jt) {
+    const int e = -(L.ex[jt] + X.ex);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[jt][v] = __builtin_amdgcn_ldexpf(acc[jt][v], e);
+  }
+}
+
 template <int MT, int KIND>
-__global__ __launch_bounds__(64 * MT) void block_iterate_kernel(BlockTable tab, const float* __restrict__ partials,
-                                                                uint16_t* __restrict__ p_out,
-                                                                uint16_t* __restrict__ t_out,
-                                                                float* __restrict__ scratch, BlockSteps steps,
-                                                                int32_t pp) {
-  constexpr int MP = 16 * MT, LDM = MP + 4, NT = 64 * MT, KW = block_kw(MT);
+__global__ __launch_bounds__(64 * MT, 2) void block_iterate_kernel(
+    BlockTable tab, const float* __restrict__ partials, uint16_t* __restrict__ p_out, uint16_t* __restrict__ t_out,
+    float* __restrict__ scratch, BlockSteps steps, int32_t pp) {
+  constexpr int MP = 16 * MT, NT = 64 * MT, KW = block_kw(MT);
   constexpr bool VJP = KIND == BK_VJP;
-  __shared__ __attribute__((aligned(16))) float L0[MP][LDM];
-  __shared__ __attribute__((aligned(16))) float L1[VJP ? MP : 1][LDM];
+  constexpr int LDM = MP + 4;
+  // the Gram matrix (and Z) in binary32 first, then the left factors
+  union Lds {
+    float gram[VJP ? 2 : 1][MP][LDM];
+    Left<MT> left[VJP ? 2 : 1];
+  };
+  __shared__ __attribute__((aligned(16))) Lds lds;
   __shared__ float red[8];
 
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
@@ -47,8 +158,11 @@ __global__ __launch_bounds__(64 * MT) void block_iterate_kernel(BlockTable tab, 
   constexpr int PF = block_part_floats(MT, KIND);
   const int parts = st.gsplit * KW;
   const float* src = partials + st.part0 + int64_t(b) * parts * PF;
+  auto& L0 = lds.gram[0];
+  auto& L1 = lds.gram[VJP ? 1 : 0];
   for (int e = tid; e < PF / 4; e += NT) {
     f32x4_t s = *gmem(reinterpret_cast<const f32x4_t*>(src + 4 * e));
+#pragma unroll 4
     for (int q = 1; q < parts; ++q) s += *gmem(reinterpret_cast<const f32x4_t*>(src + int64_t(q) * PF + 4 * e));
     const int tile = e >> 6, rr = e & 15, gg = (e >> 4) & 3;
     constexpr int TRI = (MT / 2) * (MT + 1);
@@ -80,143 +194,131 @@ __global__ __launch_bounds__(64 * MT) void block_iterate_kernel(BlockTable tab, 
   const float norm = __builtin_sqrtf(tr);
   const float inv = steps.first ? 1.f / (norm + NORM_EPS) : 1.f;
 
-  f32x4_t A[MT], P[MT], D[VJP ? MT : 1], dP[VJP ? MT : 1];
+  // A_j (and its tangent) in binary32; P lives as an operand only, and its
+  // new value passes through A while A_j is one
+  f32x4_t A[MT], D[VJP ? MT : 1];
 #pragma unroll
   for (int kt = 0; kt < MT; ++kt)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int i = 16 * kt + 4 * g + v, j = 16 * w + r;
       A[kt][v] = (L0[i][j] * inv) * inv;
-      P[kt][v] = i == j ? 1.f : 0.f;
-      if (VJP) {
-        D[kt][v] = (0.5f * inv) * (L1[i][j] + L1[j][i]);
-        dP[kt][v] = 0.f;
-      }
+      if constexpr (VJP) D[kt][v] = (0.5f * inv) * (L1[i][j] + L1[j][i]);
     }
   float* sc = nullptr;
-  if (VJP) {
+  if constexpr (VJP) {
     // A_0 and D_0 are needed again for <dX_0, X_0>
-    sc = scratch + int64_t(blk) * (2 * MP * MP);
+    sc = scratch + int64_t(blk) * (2 * MP * MP) + 4 * tid;
 #pragma unroll
     for (int kt = 0; kt < MT; ++kt) {
-      *gmem(reinterpret_cast<f32x4_t*>(sc + (kt * NT + tid) * 4)) = A[kt];
-      *gmem(reinterpret_cast<f32x4_t*>(sc + ((MT + kt) * NT + tid) * 4)) = D[kt];
+      *gmem(reinterpret_cast<f32x4_t*>(sc + kt * NT * 4)) = A[kt];
+      *gmem(reinterpret_cast<f32x4_t*>(sc + (MT + kt) * NT * 4)) = D[kt];
     }
   }
 
-  auto put = [&](float (*L)[LDM], const f32x4_t* X) {
+  Left<MT>& LA = lds.left[0];
+  Left<MT>& LD = lds.left[VJP ? 1 : 0];
+  Operand<MT> oA, oP, oD, odP;  // oD, odP: the gradient's
+
+  // A -> Q = a I + b A + c A A in its place (D -> dQ), A_t left in oA (oD)
+  auto form_q = [&](int t) {
+    const float ca = steps.a[t], cb = steps.b[t], cc = steps.c[t];
+    split_panel<MT>(A, oA);
+    if constexpr (VJP) split_panel<MT>(D, oD);
+#pragma unroll
+    for (int kt = 0; kt < MT; ++kt) {
+      A[kt] *= cb;
+      if constexpr (VJP) D[kt] *= cb;
+    }
+    if (cc != 0.f) {
+      __syncthreads();  // the reads of LDS before are done
+      put_panel<MT>(LA, oA, w, r, g, lane);
+      if constexpr (VJP) put_panel<MT>(LD, oD, w, r, g, lane);
+      __syncthreads();
+      f32x4_t x[MT];
+      multiply<MT>(x, LA, oA, r, g);
+#pragma unroll
+      for (int kt = 0; kt < MT; ++kt) A[kt] += cc * x[kt];
+      if constexpr (VJP) {
+        multiply<MT>(x, LA, oD, r, g);
+#pragma unroll
+        for (int kt = 0; kt < MT; ++kt) D[kt] += cc * x[kt];
+        multiply<MT>(x, LD, oA, r, g);
+#pragma unroll
+        for (int kt = 0; kt < MT; ++kt) D[kt] += cc * x[kt];
+      }
+    }
 #pragma unroll
     for (int kt = 0; kt < MT; ++kt)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) L[16 * kt + 4 * g + v][16 * w + r] = X[kt][v];
+      for (int v = 0; v < 4; ++v)
+        if (16 * kt + 4 * g + v == 16 * w + r) A[kt][v] += ca;
   };
-  // C += L X
-  auto mul = [&](f32x4_t* C, const float (*L)[LDM], const f32x4_t* X) {
+  // (A, D) <- L (o, od) and its tangent
+  auto left_times = [&](const Operand<MT>& o, const Operand<MT>& od) {
+    multiply<MT>(A, LA, o, r, g);
+    if constexpr (VJP) {
+      f32x4_t x[MT];
+      multiply<MT>(D, LA, od, r, g);
+      multiply<MT>(x, LD, o, r, g);
 #pragma unroll
-    for (int jt = 0; jt < MT; ++jt)
-#pragma unroll
-      for (int kt = 0; kt < MT; ++kt) {
-        const f32x4_t l = *reinterpret_cast<const f32x4_t*>(&L[16 * jt + r][16 * kt + 4 * g]);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) C[jt] = __builtin_amdgcn_mfma_f32_16x16x4f32(l[v], X[kt][v], C[jt], 0, 0, 0);
-        // without a bound on how far the reads of L are hoisted they spill
-        if (MT == 8 && kt % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-      }
-  };
-  auto zero = [&](f32x4_t* C) {
-#pragma unroll
-    for (int kt = 0; kt < MT; ++kt) C[kt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  };
-
-  for (int t = 0; t < steps.steps; ++t) {
-    const float ca = steps.a[t], cb = steps.b[t], cc = steps.c[t];
-    const bool last = t + 1 == steps.steps;
-    f32x4_t Q[MT], dQ[VJP ? MT : 1];
-    zero(Q);
-    if (VJP) zero(dQ);
-    if (cc != 0.f) {
-      __syncthreads();  // the reads of the step before are done
-      put(L0, A);
-      if (VJP) put(L1, D);
-      __syncthreads();
-      mul(Q, L0, A);
-      if (VJP) {
-        mul(dQ, L0, D);
-        mul(dQ, L1, A);
-      }
+      for (int kt = 0; kt < MT; ++kt) D[kt] += x[kt];
     }
+  };
+  auto split_into = [&](Operand<MT>& o, Operand<MT>& od) {
+    split_panel<MT>(A, o);
+    if constexpr (VJP) split_panel<MT>(D, od);
+  };
+  if (steps.steps > 0) form_q(0);  // P = Q
+  if (steps.steps > 1) {
+    split_into(oP, odP);
+    __syncthreads();
+    put_panel<MT>(LA, oP, w, r, g, lane);
+    if constexpr (VJP) put_panel<MT>(LD, odP, w, r, g, lane);
+    __syncthreads();
+#pragma unroll 1
+    for (int t = 1; t < steps.steps; ++t) {
+      left_times(oA, oD);  // R = Q A
+      split_into(oA, oD);
+      left_times(oA, oD);  // A <- Q R
+      form_q(t);
+      __syncthreads();
+      {
+        Operand<MT> o;
+        split_panel<MT>(A, o);
+        put_panel<MT>(LA, o, w, r, g, lane);
+        if constexpr (VJP) {
+          split_panel<MT>(D, o);
+          put_panel<MT>(LD, o, w, r, g, lane);
+        }
+      }
+      __syncthreads();
+      left_times(oP, odP);  // P <- Q P
+      split_into(oP, odP);
+    }
+  }
+  // P is in A, dP in D
+  if (steps.steps == 0) {
 #pragma unroll
     for (int kt = 0; kt < MT; ++kt)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const float q = cb * A[kt][v] + cc * Q[kt][v];
-        Q[kt][v] = 16 * kt + 4 * g + v == 16 * w + r ? ca + q : q;
-        if (VJP) dQ[kt][v] = cb * D[kt][v] + cc * dQ[kt][v];
+        A[kt][v] = 16 * kt + 4 * g + v == 16 * w + r ? 1.f : 0.f;
+        if constexpr (VJP) D[kt][v] = 0.f;
       }
-    __syncthreads();
-    put(L0, Q);
-    if (VJP) put(L1, dQ);
-    __syncthreads();
-    {
-      f32x4_t N[MT], dN[VJP ? MT : 1];
-      zero(N);
-      mul(N, L0, P);
-      if (VJP) {
-        zero(dN);
-        mul(dN, L0, dP);
-        mul(dN, L1, P);
-#pragma unroll
-        for (int kt = 0; kt < MT; ++kt) dP[kt] = dN[kt];
-      }
-#pragma unroll
-      for (int kt = 0; kt < MT; ++kt) P[kt] = N[kt];
-    }
-    if (!last) {
-      f32x4_t R[MT], dR[VJP ? MT : 1];
-      zero(R);
-      mul(R, L0, A);
-      if (VJP) {
-        zero(dR);
-        mul(dR, L0, D);
-        mul(dR, L1, A);
-      }
-      zero(A);
-      mul(A, L0, R);
-      if (VJP) {
-        zero(D);
-        mul(D, L0, dR);
-        mul(D, L1, R);
-      }
-    }
   }
 
-  // P in bfloat16 parts (the panel's transpose: four consecutive columns of
-  // row 16 w + r; P is symmetric)
-  auto emit = [&](uint16_t* out, const f32x4_t* X) {
-    out += int64_t(blk) * pp * (MP * MP);
-#pragma unroll
-    for (int kt = 0; kt < MT; ++kt) {
-      uint32_t p01[3], p23[3];
-      split2<3>(X[kt][0], X[kt][1], p01);
-      split2<3>(X[kt][2], X[kt][3], p23);
-#pragma unroll
-      for (int l = 0; l < 3; ++l)
-        if (l < pp)
-          *gmem(reinterpret_cast<u32x2_t*>(out + (l * MP + 16 * w + r) * MP + 16 * kt + 4 * g)) =
-              u32x2_t{p01[l], p23[l]};
-    }
-  };
-  if (VJP) {
+  if constexpr (VJP) {
     float shift = 0.f;
     if (steps.first) {
       // <dX_0, X_0> = <P, D_0> + <2 dP, A_0>
       float k = 0.f;
 #pragma unroll
       for (int kt = 0; kt < MT; ++kt) {
-        const f32x4_t a0 = *gmem(reinterpret_cast<const f32x4_t*>(sc + (kt * NT + tid) * 4));
-        const f32x4_t d0 = *gmem(reinterpret_cast<const f32x4_t*>(sc + ((MT + kt) * NT + tid) * 4));
+        const f32x4_t a0 = *gmem(reinterpret_cast<const f32x4_t*>(sc + kt * NT * 4));
+        const f32x4_t d0 = *gmem(reinterpret_cast<const f32x4_t*>(sc + (MT + kt) * NT * 4));
 #pragma unroll
-        for (int v = 0; v < 4; ++v) k += P[kt][v] * d0[v] + 2.f * dP[kt][v] * a0[v];
+        for (int v = 0; v < 4; ++v) k += A[kt][v] * d0[v] + 2.f * D[kt][v] * a0[v];
       }
 #pragma unroll
       for (int d = 32; d > 0; d >>= 1) k += __shfl_xor(k, d);
@@ -232,16 +334,41 @@ __global__ __launch_bounds__(64 * MT) void block_iterate_kernel(BlockTable tab, 
     for (int kt = 0; kt < MT; ++kt)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const float tt = (2.f * dP[kt][v]) * inv * inv;
-        dP[kt][v] = 16 * kt + 4 * g + v == 16 * w + r ? tt - shift : tt;
+        const float tt = (2.f * D[kt][v]) * inv * inv;
+        D[kt][v] = 16 * kt + 4 * g + v == 16 * w + r ? tt - shift : tt;
       }
-    emit(t_out, dP);
   }
+#pragma unroll
+  for (int kt = 0; kt < MT; ++kt) A[kt] *= inv;
+
+  // out in bfloat16 parts, by rows, through LDS.  P X is not P^T X here: P is
+  // the product Q_k ... Q_0, whose last factors carry the largest errors, and
+  // they act on what the first ones have left of X's large singular values
+  __syncthreads();
 #pragma unroll
   for (int kt = 0; kt < MT; ++kt)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) P[kt][v] = P[kt][v] * inv;
-  emit(p_out, P);
+    for (int v = 0; v < 4; ++v) {
+      L0[16 * kt + 4 * g + v][16 * w + r] = A[kt][v];
+      if constexpr (VJP) L1[16 * kt + 4 * g + v][16 * w + r] = D[kt][v];
+    }
+  __syncthreads();
+#pragma unroll
+  for (int mat = 0; mat < (VJP ? 2 : 1); ++mat) {
+    uint16_t* out = (mat ? t_out : p_out) + int64_t(blk) * pp * (MP * MP);
+#pragma unroll 2
+    for (int u = tid; u < MP * (MP / 8); u += NT) {
+      const int row = u / (MP / 8), col = (u % (MP / 8)) * 8;
+      const f32x4_t x0 = *reinterpret_cast<const f32x4_t*>(&lds.gram[mat][row][col]);
+      const f32x4_t x1 = *reinterpret_cast<const f32x4_t*>(&lds.gram[mat][row][col + 4]);
+      const float v[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+      bf16x8_t o[3];
+      split8<3>(v, o);
+#pragma unroll
+      for (int l = 0; l < 3; ++l)
+        if (l < pp) *gmem(reinterpret_cast<bf16x8_t*>(out + l * (MP * MP) + row * MP + col)) = o[l];
+    }
+  }
 }
 
 }  // namespace

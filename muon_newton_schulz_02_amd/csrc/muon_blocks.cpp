@@ -38,9 +38,12 @@ constexpr int64_t MAX_STRIDE = int64_t(1) << 40;
 // 2e-5, as binary32 arithmetic on the iterates themselves.
 constexpr double LIMIT_BF16 = 512.0;
 constexpr double LIMIT_F32 = 48.0;
-// Binary32 gradients of nearly square blocks (n < 2 m), whose singular values
-// reach down to zero: one step a stage (a 100 x 100 block, six steps: 6e-6
-// against 2e-5 with LIMIT_F32; binary32 iterates 6e-6).
+// Binary32 results of nearly square blocks (n < 2 m), whose singular values
+// reach down to zero: two quintic steps a stage for the orthogonalisation,
+// one for its gradient (sixty random blocks, six steps, largest error: 2e-5
+// against 3e-5 with LIMIT_F32, and for the gradient the ninetieth percentile
+// 6e-6 against 2e-5; binary32 iterates 2e-5 and 6e-6).
+constexpr double LIMIT_F32_SQUARE = 12.0;
 constexpr double LIMIT_VJP_SQUARE = 1.0;
 
 muon_status fail(muon_status s, const char* fmt, ...) {
@@ -341,7 +344,7 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
     g.f32 = d.param_dtype == MUON_DTYPE_F32;
     g.xbf = d.grad_dtype == MUON_DTYPE_BF16;
     g.ybf = vjp && d.mom_dtype == MUON_DTYPE_BF16;
-    g.limit = !g.f32 ? LIMIT_BF16 : vjp && n < 2 * m ? LIMIT_VJP_SQUARE : LIMIT_F32;
+    g.limit = !g.f32 ? LIMIT_BF16 : n >= 2 * m ? LIMIT_F32 : vjp ? LIMIT_VJP_SQUARE : LIMIT_F32_SQUARE;
     const std::vector<int64_t> key = {g.mt, g.f32, g.xbf, g.ybf, int64_t(g.limit)};
     auto it = where.find(key);
     if (it == where.end()) {
