@@ -74,7 +74,7 @@ extern "C" {
 #endif
 
 /* One stack.  blocks in [0, 2^20] (0: skipped), rows and cols in [1, 65536]
- * with min(rows, cols) <= 128.  Which tensors the three groups of fields
+ * with min(rows, cols) <= 128, row strides up to 2^21.  Which tensors the three groups of fields
  * describe is said at each call; a group that a call does not name is
  * ignored.  reserved: 0.                                                    */
 typedef struct muon_block_desc {

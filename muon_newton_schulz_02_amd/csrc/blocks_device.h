@@ -27,91 +27,85 @@ __device__ __forceinline__ BlockStack find_stack(const BlockTable& tab, int b, K
   return t[lo];
 }
 
-__device__ __forceinline__ float load1f(const void* p, bool bf, int64_t e) {
-  return bf ? bf16_bits_to_float(gmem(reinterpret_cast<const uint16_t*>(p))[e])
-            : gmem(reinterpret_cast<const float*>(p))[e];
-}
+// Eight consecutive elements as loaded: bfloat16 in a, binary32 in a and b.
+struct Raw8 {
+  u32x4_t a, b;
+};
+// 16 bytes at any element's address (global accesses need no alignment on
+// this GPU; the compiler knows).
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
-__device__ __forceinline__ void load8f(const void* p, bool bf, int64_t e, float v[8]) {
-  if (bf) {
-    const u32x4_t r = *gmem(reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint16_t*>(p) + e));
+// The eight elements at byte `off` of `base` (the same in all lanes), of
+// which the first `valid` exist (the others are not read and come out as
+// zero).
+__device__ __forceinline__ void load_raw(Raw8& o, const char* base, uint32_t off, bool bf, int valid) {
+  const auto s = gmem(base) + off;
+  o.a = u32x4_t{0, 0, 0, 0};
+  o.b = u32x4_t{0, 0, 0, 0};
+  typedef __attribute__((address_space(1))) const u32x4_any GV;
+  if (valid >= 8) {
+    o.a = *(GV*)s;
+    if (!bf) o.b = *(GV*)(s + 16);
+  } else if (valid > 0) {
+    typedef __attribute__((address_space(1))) const uint16_t GH;
+    typedef __attribute__((address_space(1))) const uint32_t GW;
+    if (bf) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      v[2 * q] = __uint_as_float(r[q] << 16);
-      v[2 * q + 1] = __uint_as_float(r[q] & 0xFFFF0000u);
-    }
-  } else {
-    const f32x4_t a = *gmem(reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(p) + e));
-    const f32x4_t b = *gmem(reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(p) + e + 4));
-#pragma unroll
-    for (int q = 0; q < 4; ++q) { v[q] = a[q]; v[4 + q] = b[q]; }
-  }
-}
-
-__device__ __forceinline__ void load4f(const void* p, bool bf, int64_t e, float v[4]) {
-  if (bf) {
-    const u32x2_t r = *gmem(reinterpret_cast<const u32x2_t*>(reinterpret_cast<const uint16_t*>(p) + e));
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      v[2 * q] = __uint_as_float(r[q] << 16);
-      v[2 * q + 1] = __uint_as_float(r[q] & 0xFFFF0000u);
-    }
-  } else {
-    const f32x4_t a = *gmem(reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(p) + e));
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = a[q];
-  }
-}
-
-// N (4 or 8) consecutive elements from e, `vec`: as 16- or 8-byte loads.
-// Otherwise one by one, without branches: elements at or past `valid` are not
-// read (the load goes to element `safe`, which exists) and come out as zero.
-template <int N>
-__device__ __forceinline__ void load_vec(const void* p, bool bf, int64_t e, float v[N]) {
-  if constexpr (N == 8) load8f(p, bf, e, v); else load4f(p, bf, e, v);
-}
-template <int N>
-__device__ __forceinline__ void load_masked(const void* p, bool bf, int64_t e, int valid, int64_t safe, float v[N]) {
-  if (bf) {
-#pragma unroll
-    for (int q = 0; q < N; ++q) {
-      const float f = load1f(p, true, q < valid ? e + q : safe);
-      v[q] = q < valid ? f : 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < N; ++q) {
-      const float f = load1f(p, false, q < valid ? e + q : safe);
-      v[q] = q < valid ? f : 0.f;
-    }
-  }
-}
-
-// N (2, 4 or 8) consecutive elements to e.
-template <int N>
-__device__ __forceinline__ void store_vec(void* p, bool bf, int64_t e, const float v[N]) {
-  if (bf) {
-    uint32_t h[N / 2];
-#pragma unroll
-    for (int q = 0; q < N / 2; ++q) h[q] = float2_to_bf16x2_bits(v[2 * q], v[2 * q + 1]);
-    uint16_t* o = reinterpret_cast<uint16_t*>(p) + e;
-    if constexpr (N == 8) *gmem(reinterpret_cast<u32x4_t*>(o)) = u32x4_t{h[0], h[1], h[2], h[3]};
-    else if constexpr (N == 4) *gmem(reinterpret_cast<u32x2_t*>(o)) = u32x2_t{h[0], h[1]};
-    else *gmem(reinterpret_cast<uint32_t*>(o)) = h[0];
-  } else {
-    float* o = reinterpret_cast<float*>(p) + e;
-    if constexpr (N == 2) {
-      *gmem(reinterpret_cast<f32x2_t*>(o)) = f32x2_t{v[0], v[1]};
+      for (int q = 0; q < 7; ++q)
+        if (q < valid) o.a[q / 2] |= uint32_t(((GH*)s)[q]) << (16 * (q & 1));
     } else {
 #pragma unroll
-      for (int q = 0; q < N; q += 4)
-        *gmem(reinterpret_cast<f32x4_t*>(o + q)) = f32x4_t{v[q], v[q + 1], v[q + 2], v[q + 3]};
+      for (int q = 0; q < 7; ++q)
+        if (q < valid) {
+          if (q < 4) o.a[q] = ((GW*)s)[q]; else o.b[q - 4] = ((GW*)s)[q];
+        }
     }
   }
 }
-__device__ __forceinline__ void store1f(void* p, bool bf, int64_t e, float v) {
-  if (bf) gmem(reinterpret_cast<uint16_t*>(p))[e] = float_to_bf16_bits(v);
-  else gmem(reinterpret_cast<float*>(p))[e] = v;
+
+__device__ __forceinline__ void unpack(const Raw8& o, bool bf, float v[8]) {
+  if (bf) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[2 * q] = __uint_as_float(o.a[q] << 16);
+      v[2 * q + 1] = __uint_as_float(o.a[q] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] = __uint_as_float(o.a[q]);
+      v[4 + q] = __uint_as_float(o.b[q]);
+    }
+  }
+}
+
+__device__ __forceinline__ void store8(char* base, uint32_t off, bool bf, int valid, const float v[8]) {
+  const auto d = gmem(base) + off;
+  typedef __attribute__((address_space(1))) u32x4_any GV;
+  if (bf) {
+    typedef __attribute__((address_space(1))) uint16_t GH;
+    if (valid >= 8) {
+      *(GV*)d = u32x4_t{float2_to_bf16x2_bits(v[0], v[1]), float2_to_bf16x2_bits(v[2], v[3]),
+                        float2_to_bf16x2_bits(v[4], v[5]), float2_to_bf16x2_bits(v[6], v[7])};
+    } else {
+#pragma unroll
+      for (int q = 0; q < 7; ++q)
+        if (q < valid) ((GH*)d)[q] = float_to_bf16_bits(v[q]);
+    }
+  } else {
+    typedef __attribute__((address_space(1))) float GF;
+    if (valid >= 8) {
+      u32x4_t x, y;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) { x[q] = __float_as_uint(v[q]); y[q] = __float_as_uint(v[4 + q]); }
+      *(GV*)d = x;
+      *(GV*)(d + 16) = y;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 7; ++q)
+        if (q < valid) ((GF*)d)[q] = v[q];
+    }
+  }
 }
 
 // Two values as PL bfloat16 parts each (part p of v0 | part p of v1 << 16):

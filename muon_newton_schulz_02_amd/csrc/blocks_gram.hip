@@ -2,15 +2,15 @@
 // n columns (x unnormalised, wide orientation m x n), for the gradient also
 // Z = y x^T, for the step after the momentum update of the elements it reads.
 //
-// One workgroup takes `gchunk` columns of one block, KC at a time: its four
-// waves load a tile of x (each element once), split the elements into PL
-// bfloat16 parts and put them into LDS with k (the column) contiguous, then
-// each wave multiplies its 16 x 16 tiles with 16x16x32 MFMAs.  G is
-// symmetric: only tiles on or above the diagonal are formed, dealt out as
-// tile rows {p, MT-1-p}, MT + 1 tiles for each of the MT/2 pairs.  With fewer
-// than 8 tile rows the waves also share out the columns of a tile (KW = 8/MT
-// ways), each way a partial of its own.  Partials are summed in a fixed order
-// by the recursion kernel.
+// One workgroup of eight waves takes `gchunk` columns of one block, a tile of
+// KC at a time: every thread holds 16 elements of the next tile in flight
+// while the current one, split into PL bfloat16 parts, lies in LDS with k
+// (the column) contiguous, and the waves multiply its 16 x 16 tiles with
+// 16x16x32 MFMAs.  G is symmetric: only tiles on or above the diagonal are
+// formed, dealt out as tile rows {p, MT-1-p}, MT + 1 tiles for each of the
+// MT/2 pairs; the waves of a pair share out the tile's k-steps of 32, one
+// each, and add their sums up at the end, in order.  The partials of the
+// workgroups of a block are summed in order by the recursion kernel.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -21,48 +21,29 @@
 namespace muon {
 namespace {
 
-constexpr int GT = 256;  // threads
+constexpr int GT = BLOCK_THREADS;
 
-// Eight consecutive elements of x (mat 0) or y (mat 1), `valid` of which
-// exist; for the step U, after the momentum is updated in place.
-template <int KIND>
-__device__ __forceinline__ void load_tile(const BlockStack& st, int mat, int64_t xe, int64_t ye, int valid,
-                                          int64_t xs, int64_t ys, const BlockMom& mom, float v[8]) {
-  const bool xbf = st.flags & BF_X_BF16, ybf = st.flags & BF_Y_BF16;
-  const bool vec = valid >= 8 && (st.flags & (mat ? BF_Y_VEC : BF_X_VEC));
-  if (mat == 0) {
-    if (vec) load_vec<8>(st.x, xbf, xe, v);
-    else load_masked<8>(st.x, xbf, xe, valid, xs, v);
-    if (KIND == BK_STEP) {
-      float* mo = reinterpret_cast<float*>(const_cast<void*>(st.y));
-      float m[8];
-      if (valid >= 8 && (st.flags & BF_Y_VEC)) {
-        load_vec<8>(mo, false, ye, m);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = momentum_elem(v[q], m[q], mom);
-        store_vec<8>(mo, false, ye, m);
-      } else {
-        load_masked<8>(mo, false, ye, valid, ys, m);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          v[q] = momentum_elem(v[q], m[q], mom);
-          if (q < valid) gmem(mo)[ye + q] = m[q];
-        }
-      }
-    }
-  } else {
-    if (vec) load_vec<8>(st.y, ybf, ye, v);
-    else load_masked<8>(st.y, ybf, ye, valid, ys, v);
-  }
+// LDS bytes of the gram kernel's tiles with NBUF buffers.
+template <int MT, int PL, int KIND>
+constexpr int gram_tile_bytes() {
+  return (KIND == BK_VJP ? 2 : 1) * PL * 16 * MT * (block_kc(MT) + 8) * 2;
 }
 
-template <int MT, int PL, int KIND>
-__global__ __launch_bounds__(GT, 2) void block_gram_kernel(BlockTable tab, float* __restrict__ partials,
-                                                           BlockMom mom) {
-  constexpr int MP = 16 * MT, KC = block_kc(MT), KW = block_kw(MT), LDK = KC + 8;
+template <int MT, int PL, int KIND, int XT>
+__global__ __launch_bounds__(GT, KIND == BK_VJP ? 2 : 4) void block_gram_kernel(BlockTable tab,
+                                                                               float* __restrict__ partials,
+                                                                               BlockMom mom) {
+  constexpr int MP = 16 * MT, KC = block_kc(MT), LDK = KC + 8;
   constexpr int NM = KIND == BK_VJP ? 2 : 1;       // matrices staged: x (and y)
-  constexpr int KS = KC / 32 / KW;                 // k-steps of 32 per wave and tile
-  __shared__ __attribute__((aligned(16))) uint16_t lds[NM][PL][MP][LDK];
+  constexpr int KW = 16 / MT;                      // waves of a pair of tile rows = k-steps of a tile
+  // two buffers where two workgroups still fit a compute unit
+  constexpr int TB = gram_tile_bytes<MT, PL, KIND>(), NBUF = 2 * TB <= 80 * 1024 ? 2 : 1;
+  constexpr int NG = MT + 1, NZ = KIND == BK_VJP ? 2 * MT : 0;  // tiles of a wave
+  constexpr int RED = (MT / 2) * (NZ > NG ? NZ : NG) * 1024;    // the final sum's LDS
+  constexpr int LB = NBUF * TB > RED ? NBUF * TB : RED;
+  __shared__ __attribute__((aligned(16))) unsigned char lds_raw[LB];
+  typedef uint16_t Tile[NM][PL][MP][LDK];
+  Tile* const lds = reinterpret_cast<Tile*>(lds_raw);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, g = lane >> 4;
@@ -70,110 +51,153 @@ __global__ __launch_bounds__(GT, 2) void block_gram_kernel(BlockTable tab, float
   const int local = int(blockIdx.x) - st.goff;
   const int b = local / st.gsplit, sp = local - b * st.gsplit;
   const int k0 = sp * st.gchunk, k1 = min(st.n, k0 + st.gchunk);
-  const int64_t xo = int64_t(b) * st.x_bs, yo = int64_t(b) * st.y_bs;
+  const bool tr = st.flags & BF_TR;
+  const bool xbf = XT == BX_ANY ? (st.flags & BF_X_BF16) != 0 : XT == BX_BF16;
+  const bool ybf = KIND == BK_VJP && (PL == 1 || (st.flags & BF_Y_BF16));
+  const int xs = xbf ? 2 : 4, ys = ybf ? 2 : 4;
+
+  // the thread's two runs of 8 elements: rows contiguous along k, two runs of
+  // 8 columns (512 threads apart); transposed, 8 rows of two columns
+  const int row0 = tr ? (tid % (MP / 8)) * 8 : tid / (KC / 8);
+  const int col0 = tr ? (tid / (MP / 8)) * 2 : (tid % (KC / 8)) * 8;
+  constexpr int DR = GT / (KC / 8);
+  // first byte of the first tile, bytes from tile to tile, and the first
+  // run's byte offset in a tile
+  const char* xp = reinterpret_cast<const char*>(st.x) + (int64_t(b) * st.x_bs + (tr ? k0 * st.x_ld : k0)) * xs;
+  char* yp = reinterpret_cast<char*>(const_cast<void*>(st.y)) + (int64_t(b) * st.y_bs + (tr ? k0 * st.y_ld : k0)) * ys;
+  const int64_t xt = (tr ? KC * st.x_ld : KC) * xs, yt = (tr ? KC * st.y_ld : KC) * ys;
+  const uint32_t xl = uint32_t(st.x_ld) * xs, yl = uint32_t(st.y_ld) * ys;
+  const uint32_t xo = tr ? col0 * xl + row0 * xs : row0 * xl + col0 * xs;
+  const uint32_t yo = tr ? col0 * yl + row0 * ys : row0 * yl + col0 * ys;
+  const uint32_t xd = tr ? xl : DR * xl, yd = tr ? yl : DR * yl;
+  auto valid_of = [&](int q, int kn) {  // kn: columns from the tile's first one on
+    return tr ? (col0 + q < kn ? st.m - row0 : 0) : (row0 + q * DR < st.m ? kn - col0 : 0);
+  };
+
+  Raw8 rx[2], ry[2];
+  auto fetch = [&](int kn) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int valid = valid_of(q, kn);
+      load_raw(rx[q], xp, xo + q * xd, xbf, valid);
+      if (KIND == BK_STEP) load_raw(ry[q], yp, yo + q * yd, false, valid);
+      if (KIND == BK_VJP) load_raw(ry[q], yp, yo + q * yd, ybf, valid);
+    }
+  };
 
   const int p = wave % (MT / 2), kw = wave / (MT / 2);
-  f32x4_t acc[MT + 1];
+  f32x4_t acc[NG], zacc[NZ ? NZ : 1];
 #pragma unroll
-  for (int q = 0; q <= MT; ++q) acc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  f32x4_t zacc[KIND == BK_VJP ? 2 * MT : 1];
+  for (int q = 0; q < NG; ++q) acc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int q = 0; q < (KIND == BK_VJP ? 2 * MT : 1); ++q) zacc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int q = 0; q < NZ; ++q) zacc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
+  fetch(k1 - k0);
+  int buf = 0;
+#pragma unroll 1
   for (int kb = k0; kb < k1; kb += KC) {
-    const int kn = min(KC, k1 - kb);  // columns of this tile
-    if (kb > k0) __syncthreads();     // the last tile's reads are done
-    if (!(st.flags & BF_TR)) {
-      // rows contiguous along k: a thread takes 8 columns of one row
-      constexpr int UNITS = MP * (KC / 8);
+    if (NBUF == 1 && kb > k0) __syncthreads();  // the last tile's reads are done
+    Tile& tile = lds[buf];
 #pragma unroll
-      for (int u0 = 0; u0 < UNITS; u0 += GT) {
-        const int u = u0 + tid, row = u / (KC / 8), kk = (u % (KC / 8)) * 8;
-        const int valid = row < st.m ? kn - kk : 0;
-        bf16x8_t o[PL];
+    for (int mat = 0; mat < NM; ++mat) {
+      float v[2][8];
 #pragma unroll
-        for (int mat = 0; mat < NM; ++mat) {
-          float v[8];
-          load_tile<KIND>(st, mat, xo + int64_t(row) * st.x_ld + kb + kk, yo + int64_t(row) * st.y_ld + kb + kk, valid,
-                          xo, yo, mom, v);
-          split8<PL>(v, o);
+      for (int q = 0; q < 2; ++q) {
+        unpack(mat ? ry[q] : rx[q], mat ? ybf : xbf, v[q]);
+        if (KIND == BK_STEP) {
+          float m[8];
+          unpack(ry[q], false, m);
 #pragma unroll
-          for (int l = 0; l < PL; ++l) *reinterpret_cast<bf16x8_t*>(&lds[mat][l][row][kk]) = o[l];
+          for (int i = 0; i < 8; ++i) v[q][i] = momentum_elem(v[q][i], m[i], mom);
+          const int valid = valid_of(q, k1 - kb);
+          if (valid > 0) store8(yp, yo + q * yd, false, valid, m);
         }
       }
-    } else {
-      // contiguous along i: a thread takes 8 rows (i) of 4 columns (k)
-      constexpr int UNITS = (MP / 8) * (KC / 4);
-      if (UNITS >= GT || tid < UNITS) {
-        const int i0 = (tid % (MP / 8)) * 8, kk = (tid / (MP / 8)) * 4;
+      if (!tr) {
 #pragma unroll
-        for (int mat = 0; mat < NM; ++mat) {
-          float v[4][8];
+        for (int q = 0; q < 2; ++q) {
+          bf16x8_t o[PL];
+          split8<PL>(v[q], o);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            load_tile<KIND>(st, mat, xo + int64_t(kb + kk + k) * st.x_ld + i0, yo + int64_t(kb + kk + k) * st.y_ld + i0,
-                            kk + k < kn ? st.m - i0 : 0, xo, yo, mom, v[k]);
+          for (int l = 0; l < PL; ++l) *reinterpret_cast<bf16x8_t*>(&tile[mat][l][row0 + q * DR][col0]) = o[l];
+        }
+      } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t p01[PL], p23[PL];
-            split2<PL>(v[0][i], v[1][i], p01);
-            split2<PL>(v[2][i], v[3][i], p23);
+        for (int i = 0; i < 8; ++i) {
+          uint32_t o[PL];
+          split2<PL>(v[0][i], v[1][i], o);
 #pragma unroll
-            for (int l = 0; l < PL; ++l)
-              *reinterpret_cast<u32x2_t*>(&lds[mat][l][i0 + i][kk]) = u32x2_t{p01[l], p23[l]};
-          }
+          for (int l = 0; l < PL; ++l) *reinterpret_cast<uint32_t*>(&tile[mat][l][row0 + i][col0]) = o[l];
         }
       }
-      static_assert(UNITS <= GT, "one unit per thread");
+    }
+    if (kb + KC < k1) {
+      xp += xt;
+      yp += yt;
+      fetch(k1 - kb - KC);
     }
     __syncthreads();
+    const int ko = kw * 32 + 8 * g;
+    bf16x8_t a0[PL], a1[PL];
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int ko = (kw * KS + ks) * 32 + 8 * g;
-      bf16x8_t a0[PL], a1[PL];
+    for (int l = 0; l < PL; ++l) {
+      a0[l] = *reinterpret_cast<const bf16x8_t*>(&tile[0][l][16 * p + r][ko]);
+      a1[l] = *reinterpret_cast<const bf16x8_t*>(&tile[0][l][16 * (MT - 1 - p) + r][ko]);
+    }
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+      const bool first = q < MT - p;
+      const int tj = first ? p + q : MT - 1 - p + (q - (MT - p));
+      bf16x8_t bb[PL];
+#pragma unroll
+      for (int l = 0; l < PL; ++l) bb[l] = *reinterpret_cast<const bf16x8_t*>(&tile[0][l][16 * tj + r][ko]);
+      if (first) acc[q] = mfma_parts<PL, PL>(a0, bb, acc[q]);
+      else acc[q] = mfma_parts<PL, PL>(a1, bb, acc[q]);
+    }
+    if (KIND == BK_VJP) {
 #pragma unroll
       for (int l = 0; l < PL; ++l) {
-        a0[l] = *reinterpret_cast<const bf16x8_t*>(&lds[0][l][16 * p + r][ko]);
-        a1[l] = *reinterpret_cast<const bf16x8_t*>(&lds[0][l][16 * (MT - 1 - p) + r][ko]);
+        a0[l] = *reinterpret_cast<const bf16x8_t*>(&tile[NM - 1][l][16 * p + r][ko]);
+        a1[l] = *reinterpret_cast<const bf16x8_t*>(&tile[NM - 1][l][16 * (MT - 1 - p) + r][ko]);
       }
 #pragma unroll
-      for (int q = 0; q <= MT; ++q) {
-        const bool row0 = q < MT - p;
-        const int tj = row0 ? p + q : MT - 1 - p + (q - (MT - p));
+      for (int tj = 0; tj < MT; ++tj) {
         bf16x8_t bb[PL];
 #pragma unroll
-        for (int l = 0; l < PL; ++l) bb[l] = *reinterpret_cast<const bf16x8_t*>(&lds[0][l][16 * tj + r][ko]);
-        if (row0) acc[q] = mfma_parts<PL, PL>(a0, bb, acc[q]);
-        else acc[q] = mfma_parts<PL, PL>(a1, bb, acc[q]);
-      }
-      if (KIND == BK_VJP) {
-#pragma unroll
-        for (int l = 0; l < PL; ++l) {
-          a0[l] = *reinterpret_cast<const bf16x8_t*>(&lds[NM - 1][l][16 * p + r][ko]);
-          a1[l] = *reinterpret_cast<const bf16x8_t*>(&lds[NM - 1][l][16 * (MT - 1 - p) + r][ko]);
-        }
-#pragma unroll
-        for (int tj = 0; tj < MT; ++tj) {
-          bf16x8_t bb[PL];
-#pragma unroll
-          for (int l = 0; l < PL; ++l) bb[l] = *reinterpret_cast<const bf16x8_t*>(&lds[0][l][16 * tj + r][ko]);
-          zacc[tj] = mfma_parts<PL, PL>(a0, bb, zacc[tj]);
-          zacc[MT + tj] = mfma_parts<PL, PL>(a1, bb, zacc[MT + tj]);
-        }
+        for (int l = 0; l < PL; ++l) bb[l] = *reinterpret_cast<const bf16x8_t*>(&tile[0][l][16 * tj + r][ko]);
+        zacc[tj] = mfma_parts<PL, PL>(a0, bb, zacc[tj]);
+        zacc[MT + tj] = mfma_parts<PL, PL>(a1, bb, zacc[MT + tj]);
       }
     }
+    if (NBUF == 2) buf ^= 1;
   }
 
-  constexpr int PF = block_part_floats(MT, KIND);
-  float* out = partials + st.part0 + (int64_t(b) * (st.gsplit * KW) + sp * KW + kw) * PF;
+  // add up the KW sums of every tile, in order, and store them
+  f32x4_t* const red = reinterpret_cast<f32x4_t*>(lds_raw);
+  auto gather = [&](f32x4_t* t, int n) {
+    for (int s = 1; s < KW; ++s) {
+      __syncthreads();
+      if (kw == s)
 #pragma unroll
-  for (int q = 0; q <= MT; ++q)
-    *gmem(reinterpret_cast<f32x4_t*>(out + ((p * (MT + 1) + q) * 64 + lane) * 4)) = acc[q];
-  if (KIND == BK_VJP) {
-    out += (MT / 2) * (MT + 1) * 256;
+        for (int q = 0; q < n; ++q) red[(p * n + q) * 64 + lane] = t[q];
+      __syncthreads();
+      if (kw == 0)
 #pragma unroll
-    for (int q = 0; q < 2 * MT; ++q)
-      *gmem(reinterpret_cast<f32x4_t*>(out + ((p * 2 * MT + q) * 64 + lane) * 4)) = zacc[q];
+        for (int q = 0; q < n; ++q) t[q] += red[(p * n + q) * 64 + lane];
+    }
+  };
+  gather(acc, NG);
+  if (KIND == BK_VJP) gather(zacc, NZ);
+  if (kw == 0) {
+    constexpr int PF = block_part_floats(MT, KIND);
+    float* out = partials + st.part0 + (int64_t(b) * st.gsplit + sp) * PF;
+#pragma unroll
+    for (int q = 0; q < NG; ++q) *gmem(reinterpret_cast<f32x4_t*>(out + ((p * NG + q) * 64 + lane) * 4)) = acc[q];
+    if (KIND == BK_VJP) {
+      out += (MT / 2) * NG * 256;
+#pragma unroll
+      for (int q = 0; q < NZ; ++q) *gmem(reinterpret_cast<f32x4_t*>(out + ((p * NZ + q) * 64 + lane) * 4)) = zacc[q];
+    }
   }
 }
 
@@ -187,21 +211,23 @@ __global__ void block_table_kernel(BlockStackBatch in, int32_t n, BlockStack* __
 }
 
 template <int MT>
-hipError_t gram_mt(int pl, int kind, const BlockTable& tab, int32_t wgs, float* partials, const BlockMom& mom,
-                   hipStream_t stream) {
-#define MUON_GRAM(PL, KIND)                                                                                   \
-  if (pl == PL && kind == KIND) {                                                                             \
-    hipLaunchKernelGGL((block_gram_kernel<MT, PL, KIND>), dim3(wgs), dim3(GT), 0, stream, tab, partials, mom); \
-    return hipGetLastError();                                                                                 \
+hipError_t gram_mt(int pl, int kind, bool xbf, const BlockTable& tab, int32_t wgs, float* partials,
+                   const BlockMom& mom, hipStream_t stream) {
+#define MUON_GRAM(PL, KIND, XT)                                                                             \
+  if (pl == PL && kind == KIND && (XT == BX_ANY || xbf == (XT == BX_BF16))) {                               \
+    hipLaunchKernelGGL((block_gram_kernel<MT, PL, KIND, XT>), dim3(wgs), dim3(GT), 0, stream, tab, partials, \
+                       mom);                                                                                \
+    return hipGetLastError();                                                                               \
   }
-  MUON_GRAM(1, BK_X)
-  MUON_GRAM(2, BK_X)
-  MUON_GRAM(3, BK_X)
-  MUON_GRAM(2, BK_STEP)
-  MUON_GRAM(3, BK_STEP)
-  MUON_GRAM(1, BK_VJP)
-  MUON_GRAM(2, BK_VJP)
-  MUON_GRAM(3, BK_VJP)
+  MUON_GRAM(1, BK_X, BX_BF16)
+  MUON_GRAM(2, BK_X, BX_F32)
+  MUON_GRAM(3, BK_X, BX_ANY)
+  MUON_GRAM(2, BK_STEP, BX_BF16)
+  MUON_GRAM(2, BK_STEP, BX_F32)
+  MUON_GRAM(3, BK_STEP, BX_ANY)
+  MUON_GRAM(1, BK_VJP, BX_BF16)
+  MUON_GRAM(2, BK_VJP, BX_ANY)
+  MUON_GRAM(3, BK_VJP, BX_ANY)
 #undef MUON_GRAM
   return hipErrorInvalidValue;
 }
@@ -220,12 +246,12 @@ hipError_t launch_block_table(const BlockStack* host, int32_t count, BlockStack*
   return hipSuccess;
 }
 
-hipError_t launch_block_gram(int mt, int pl, int kind, const BlockTable& tab, int32_t wgs, float* partials,
-                             const BlockMom& mom, hipStream_t stream) {
+hipError_t launch_block_gram(int mt, int pl, int kind, bool xbf, const BlockTable& tab, int32_t wgs,
+                             float* partials, const BlockMom& mom, hipStream_t stream) {
   if (wgs <= 0) return hipSuccess;
-  return mt == 2   ? gram_mt<2>(pl, kind, tab, wgs, partials, mom, stream)
-         : mt == 4 ? gram_mt<4>(pl, kind, tab, wgs, partials, mom, stream)
-                   : gram_mt<8>(pl, kind, tab, wgs, partials, mom, stream);
+  return mt == 2   ? gram_mt<2>(pl, kind, xbf, tab, wgs, partials, mom, stream)
+         : mt == 4 ? gram_mt<4>(pl, kind, xbf, tab, wgs, partials, mom, stream)
+                   : gram_mt<8>(pl, kind, xbf, tab, wgs, partials, mom, stream);
 }
 
 }  // namespace muon

@@ -13,11 +13,8 @@ enum BlockFlags : uint32_t {
   BF_X_BF16 = 1,      // x is bfloat16 (else binary32)
   BF_Y_BF16 = 2,
   BF_OUT_BF16 = 4,
-  BF_X_VEC = 8,       // rows of x allow 16-byte access at multiples of 16 bytes
-  BF_Y_VEC = 16,
-  BF_OUT_VEC = 32,
-  BF_TR = 64,         // rows > cols: element (i, j) of the wide block is at j * ld + i
-  BF_WRITEBACK = 128  // apply: out is a weight, out <- rnd(out * d - t * O)
+  BF_TR = 8,          // rows > cols: element (i, j) of the wide block is at j * ld + i
+  BF_WRITEBACK = 16   // apply: out is a weight, out <- rnd(out * d - t * O)
 };
 
 // One stack as the kernels see it, at one stage of the computation.
@@ -72,21 +69,25 @@ enum BlockKind : int { BK_X = 0, BK_STEP = 1, BK_VJP = 2 };
 // Row tiles of 16 that a block of m rows is padded to: 2, 4 or 8 (the
 // kernels' template sizes; 32, 64 or 128 rows).
 constexpr int block_mt(int m) { return m <= 32 ? 2 : m <= 64 ? 4 : 8; }
-// Gram partials of one block and workgroup: 8 / MT waves sum separate columns.
-constexpr int block_kw(int mt) { return 8 / mt; }
-// Floats of one partial: the upper triangle of 16 x 16 tiles, and for the
+// Floats of a Gram partial: the upper triangle of 16 x 16 tiles, and for the
 // gradient all tiles of y x^T.
 constexpr int block_part_floats(int mt, int kind) {
   return ((mt / 2) * (mt + 1) + (kind == BK_VJP ? mt * mt : 0)) * 256;
 }
-// Columns a gram workgroup takes at a time, and columns of an apply workgroup's strip.
-constexpr int block_kc(int mt) { return mt == 2 ? 128 : 64; }
-constexpr int BLOCK_STRIP = 256;
+// The gram and apply passes work on tiles of all 16 MT rows by this many
+// columns, 8192 elements, 16 for each of the 512 threads.
+constexpr int BLOCK_THREADS = 512;
+constexpr int block_kc(int mt) { return 512 / mt; }
+// Element offsets within a tile are 32-bit byte offsets: at most 256 rows
+// apart by this row stride.
+constexpr int64_t BLOCK_MAX_LD = int64_t(1) << 21;
+// Type of x known when a kernel is compiled, or read from the flags.
+enum BlockXType : int { BX_F32 = 0, BX_BF16 = 1, BX_ANY = 2 };
 
 // The launchers.  pl: bfloat16 parts of an element of x (1, 2, 3); pp: parts
-// of an element of P (2, 3).
+// of an element of P (2, 3); xbf: x is bfloat16 in every stack.
 hipError_t launch_block_table(const BlockStack* host, int32_t count, BlockStack* dev, hipStream_t stream);
-hipError_t launch_block_gram(int mt, int pl, int kind, const BlockTable& tab, int32_t wgs, float* partials,
+hipError_t launch_block_gram(int mt, int pl, int kind, bool xbf, const BlockTable& tab, int32_t wgs, float* partials,
                              const BlockMom& mom, hipStream_t stream);
 // Sums the partials of every block, runs the recursion and writes P (and, for
 // the gradient, T) as pp planes of bfloat16 parts, mp x mp each.  scratch: 2
@@ -94,7 +95,7 @@ hipError_t launch_block_gram(int mt, int pl, int kind, const BlockTable& tab, in
 hipError_t launch_block_iterate(int mt, int pp, int kind, const BlockTable& tab, int32_t blocks,
                                 const float* partials, uint16_t* p_out, uint16_t* t_out, float* scratch,
                                 const BlockSteps& steps, hipStream_t stream);
-hipError_t launch_block_apply(int mt, int pl, int pp, int kind, const BlockTable& tab, int32_t wgs,
+hipError_t launch_block_apply(int mt, int pl, int pp, int kind, bool xbf, const BlockTable& tab, int32_t wgs,
                               const uint16_t* p, const uint16_t* t, const BlockMom& mom, hipStream_t stream);
 
 }  // namespace muon

@@ -137,7 +137,7 @@ template <int MT, int KIND>
 __global__ __launch_bounds__(64 * MT, 2) void block_iterate_kernel(
     BlockTable tab, const float* __restrict__ partials, uint16_t* __restrict__ p_out, uint16_t* __restrict__ t_out,
     float* __restrict__ scratch, BlockSteps steps, int32_t pp) {
-  constexpr int MP = 16 * MT, NT = 64 * MT, KW = block_kw(MT);
+  constexpr int MP = 16 * MT, NT = 64 * MT;
   constexpr bool VJP = KIND == BK_VJP;
   constexpr int LDM = MP + 4;
   // the Gram matrix (and Z) in binary32 first, then the left factors
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(64 * MT, 2) void block_iterate_kernel(
 
   // sum the partials, in order, into LDS (both triangles)
   constexpr int PF = block_part_floats(MT, KIND);
-  const int parts = st.gsplit * KW;
+  const int parts = st.gsplit;
   const float* src = partials + st.part0 + int64_t(b) * parts * PF;
   auto& L0 = lds.gram[0];
   auto& L1 = lds.gram[VJP ? 1 : 0];

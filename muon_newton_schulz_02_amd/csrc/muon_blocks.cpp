@@ -129,9 +129,9 @@ muon_status check_view(int32_t i, const char* what, const muon_block_desc& d, in
                        int32_t dtype, bool f32_only, bool written) {
   if (dtype != MUON_DTYPE_F32 && (f32_only || dtype != MUON_DTYPE_BF16))
     return fail(MUON_ERR_UNSUPPORTED, "stack %d: %s dtype %d is not %s", i, what, dtype, f32_only ? "F32" : "F32 or BF16");
-  if (ld < d.cols || ld > MAX_STRIDE)
-    return fail(MUON_ERR_INVALID_ARGUMENT, "stack %d: %s row stride %lld out of [cols = %lld, 2^40]", i, what,
-                (long long)ld, (long long)d.cols);
+  if (ld < d.cols || ld > BLOCK_MAX_LD)
+    return fail(ld < d.cols ? MUON_ERR_INVALID_ARGUMENT : MUON_ERR_UNSUPPORTED,
+                "stack %d: %s row stride %lld out of [cols = %lld, 2^21]", i, what, (long long)ld, (long long)d.cols);
   if (stride < 0 || stride > MAX_STRIDE)
     return fail(MUON_ERR_INVALID_ARGUMENT, "stack %d: %s block stride %lld out of [0, 2^40]", i, what,
                 (long long)stride);
@@ -323,11 +323,6 @@ struct Group {
   size_t o_tab = 0, o_part = 0, o_p = 0, o_t = 0, o_scr = 0, o_stage = 0, end = 0;
 };
 
-bool vec16(const void* p, int64_t rows, int64_t blocks, int64_t ld, int64_t stride, int esz) {
-  const int64_t q = 16 / esz;
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows == 1 || ld % q == 0) && (blocks == 1 || stride % q == 0);
-}
-
 int64_t ld_of_stage(const muon_block_desc& d) { return round_up(d.cols, 4); }
 
 // Splits the call into groups and lays out the workspace (the groups run one
@@ -360,9 +355,9 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
     const int kc = block_kc(g.mt), mp = 16 * g.mt;
     const int kind = vjp ? BK_VJP : c.op == MUON_BLOCKS_STEP ? BK_STEP : BK_X;
     g.stages = stages_of(c, g.limit);
-    // workgroups enough to fill the GPU four times over, each with two tiles
-    // of columns (Gram) or one strip (apply) at least
-    const int64_t want = std::max<int64_t>(1, (4 * int64_t(cus) + g.blocks - 1) / g.blocks);
+    // workgroups enough to fill the GPU four times over, two to a compute
+    // unit, each with two tiles of columns at least
+    const int64_t want = std::max<int64_t>(1, (8 * int64_t(cus) + g.blocks - 1) / g.blocks);
     int64_t goff = 0, aoff = 0, block0 = 0, part = 0;
     for (int32_t i : g.members) {
       const muon_block_desc& d = c.stacks[i];
@@ -377,8 +372,7 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
       s.flags = tr ? BF_TR : 0;
       s.gchunk = int32_t(std::max<int64_t>(round_up((s.n + want - 1) / want, kc), 2 * kc));
       s.gsplit = (s.n + s.gchunk - 1) / s.gchunk;
-      const int64_t strips = (s.n + BLOCK_STRIP - 1) / BLOCK_STRIP;
-      s.achunk = int32_t(BLOCK_STRIP * ((strips + want - 1) / want));
+      s.achunk = s.gchunk;
       s.asplit = (s.n + s.achunk - 1) / s.achunk;
       s.goff = int32_t(goff);
       s.aoff = int32_t(aoff);
@@ -386,7 +380,7 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
       s.d = 1.f;
       goff += d.blocks * s.gsplit;
       aoff += d.blocks * s.asplit;
-      part += d.blocks * s.gsplit * block_kw(g.mt) * int64_t(block_part_floats(g.mt, kind));
+      part += d.blocks * s.gsplit * int64_t(block_part_floats(g.mt, kind));
       block0 += d.blocks;
       g.base.push_back(s);
       g.stage_off.push_back(g.stage_bytes);
@@ -452,12 +446,10 @@ hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
       s.x_ld = d.ld_grad;
       s.x_bs = d.stride_grad;
       if (g.xbf) s.flags |= BF_X_BF16;
-      if (vec16(c.x[i], d.rows, d.blocks, d.ld_grad, d.stride_grad, esize(d.grad_dtype))) s.flags |= BF_X_VEC;
     } else {
       s.x = ws + g.o_stage + size_t(buf) * g.stage_bytes + g.stage_off[k];
       s.x_ld = ld_of_stage(d);
       s.x_bs = d.rows * s.x_ld;
-      s.flags |= BF_X_VEC;
     }
   };
   auto set_y = [&](BlockStack& s, size_t k, int buf) {
@@ -468,12 +460,10 @@ hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
       s.y_ld = d.ld_mom;
       s.y_bs = d.stride_mom;
       if (d.mom_dtype == MUON_DTYPE_BF16) s.flags |= BF_Y_BF16;
-      if (vec16(c.y[i], d.rows, d.blocks, d.ld_mom, d.stride_mom, esize(d.mom_dtype))) s.flags |= BF_Y_VEC;
     } else {
       s.y = ws + g.o_stage + size_t(buf) * g.stage_bytes + g.stage_off[k];
       s.y_ld = ld_of_stage(d);
       s.y_bs = d.rows * s.y_ld;
-      s.flags |= BF_Y_VEC;
     }
   };
   auto set_out = [&](BlockStack& s, size_t k, int buf) {
@@ -484,7 +474,6 @@ hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
       s.out_ld = d.ld_param;
       s.out_bs = d.stride_param;
       if (!g.f32) s.flags |= BF_OUT_BF16;
-      if (vec16(c.out[i], d.rows, d.blocks, d.ld_param, d.stride_param, esize(d.param_dtype))) s.flags |= BF_OUT_VEC;
       if (step) {
         s.flags |= BF_WRITEBACK;
         s.upd = c.upd ? c.upd[i] : nullptr;
@@ -501,7 +490,6 @@ hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
       s.out = ws + g.o_stage + size_t(buf) * g.stage_bytes + g.stage_off[k];
       s.out_ld = ld_of_stage(d);
       s.out_bs = d.rows * s.out_ld;
-      s.flags |= BF_OUT_VEC;
     }
   };
 
@@ -550,7 +538,7 @@ hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
     const int kind = user_u ? BK_STEP : BK_X;
     const int pl = g.f32 ? 3 : (user_u || i > 0 || !g.xbf) ? 2 : 1;
     e = run(user_u ? MUON_KC_MOMENTUM : MUON_KC_GRAM, [&] {
-      return launch_block_gram(g.mt, pl, kind, tab, g.gram_wgs, parts, mom, c.stream);
+      return launch_block_gram(g.mt, pl, kind, i == 0 && g.xbf, tab, g.gram_wgs, parts, mom, c.stream);
     });
     if (e != hipSuccess) break;
     const BlockSteps s = steps_of(g.stages[size_t(i)], i == 0);
@@ -559,7 +547,7 @@ hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
     });
     if (e != hipSuccess) break;
     e = run(MUON_KC_COMBINE, [&] {
-      return launch_block_apply(g.mt, pl, pp, kind, tab, g.apply_wgs, P, nullptr, mom, c.stream);
+      return launch_block_apply(g.mt, pl, pp, kind, i == 0 && g.xbf, tab, g.apply_wgs, P, nullptr, mom, c.stream);
     });
   }
   if (!vjp) return e;
@@ -575,7 +563,7 @@ hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
     const bool bf = (i == 0 && g.xbf) && (i == nst - 1 && g.ybf);
     const int pl = g.f32 ? 3 : bf ? 1 : 2;
     e = run(MUON_KC_GRAM, [&] {
-      return launch_block_gram(g.mt, pl, BK_VJP, tab, g.gram_wgs, parts, mom, c.stream);
+      return launch_block_gram(g.mt, pl, BK_VJP, i == 0 && g.xbf, tab, g.gram_wgs, parts, mom, c.stream);
     });
     if (e != hipSuccess) break;
     const BlockSteps s = steps_of(g.stages[size_t(i)], i == 0);
@@ -584,7 +572,7 @@ hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
     });
     if (e != hipSuccess) break;
     e = run(MUON_KC_COMBINE, [&] {
-      return launch_block_apply(g.mt, pl, pp, BK_VJP, tab, g.apply_wgs, P, T, mom, c.stream);
+      return launch_block_apply(g.mt, pl, pp, BK_VJP, i == 0 && g.xbf, tab, g.apply_wgs, P, T, mom, c.stream);
     });
   }
   return e;

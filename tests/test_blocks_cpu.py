@@ -79,7 +79,7 @@ PASSES = (mb.MUON_OK, mb.MUON_ERR_HIP)  # validation passed (no GPU here)
     (dict(rows=129, cols=129), mb.MUON_ERR_UNSUPPORTED),
     (dict(ld_grad=95), mb.MUON_ERR_INVALID_ARGUMENT),
     (dict(ld_param=95), mb.MUON_ERR_INVALID_ARGUMENT),
-    (dict(ld_param=(1 << 40) + 1), mb.MUON_ERR_INVALID_ARGUMENT),
+    (dict(ld_param=(1 << 21) + 1), mb.MUON_ERR_UNSUPPORTED),
     (dict(stride_grad=-1), mb.MUON_ERR_INVALID_ARGUMENT),
     (dict(stride_param=16 * 96 - 1), mb.MUON_ERR_ALIAS),
     (dict(stride_param=0), mb.MUON_ERR_ALIAS),
