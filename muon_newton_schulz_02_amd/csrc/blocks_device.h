@@ -15,16 +15,23 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
-// The stack whose range of workgroups (by `key`) holds workgroup b.
-template <class Key>
-__device__ __forceinline__ BlockStack find_stack(const BlockTable& tab, int b, Key key) {
-  const BlockStack* t = tab.ext ? tab.ext : tab.inl;
-  int lo = 0, hi = tab.count;
+// The stack whose range of workgroups (by member `key`) holds workgroup b
+// (the same in all lanes).  The table is the kernel's first argument: read
+// through the constant address space it takes scalar loads, and what it holds
+// stays in scalar registers.
+typedef __attribute__((address_space(4))) const BlockStack ConstStack;
+__device__ __forceinline__ BlockStack find_stack(int32_t BlockStack::*key, int b) {
+  typedef __attribute__((address_space(4))) const BlockTable ConstTable;
+  ConstTable* tab = (ConstTable*)__builtin_amdgcn_kernarg_segment_ptr();
+  ConstStack* t = tab->ext ? (ConstStack*)tab->ext : &tab->inl[0];
+  int lo = 0, hi = tab->count;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (key(t[mid]) <= b) lo = mid; else hi = mid;
+    if (t[mid].*key <= b) lo = mid; else hi = mid;
   }
-  return t[lo];
+  BlockStack s;
+  __builtin_memcpy(&s, (const BlockStack*)(t + lo), sizeof(s));
+  return s;
 }
 
 // Eight consecutive elements as loaded: bfloat16 in a, binary32 in a and b.

@@ -47,7 +47,7 @@ __global__ __launch_bounds__(GT, KIND == BK_VJP ? 2 : 4) void block_gram_kernel(
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, g = lane >> 4;
-  const BlockStack st = find_stack(tab, blockIdx.x, [](const BlockStack& s) { return s.goff; });
+  const BlockStack st = find_stack(&BlockStack::goff, blockIdx.x);
   const int local = int(blockIdx.x) - st.goff;
   const int b = local / st.gsplit, sp = local - b * st.gsplit;
   const int k0 = sp * st.gchunk, k1 = min(st.n, k0 + st.gchunk);

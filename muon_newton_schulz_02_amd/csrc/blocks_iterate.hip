@@ -151,7 +151,7 @@ __global__ __launch_bounds__(64 * MT, 2) void block_iterate_kernel(
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int r = lane & 15, g = lane >> 4;
   const int blk = blockIdx.x;
-  const BlockStack st = find_stack(tab, blk, [](const BlockStack& s) { return s.block0; });
+  const BlockStack st = find_stack(&BlockStack::block0, blk);
   const int b = blk - st.block0;
 
   // sum the partials, in order, into LDS (both triangles)
