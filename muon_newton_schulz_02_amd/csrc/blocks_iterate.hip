@@ -7,28 +7,32 @@
 // every matrix is a function of A_0, so the order of factors is free and the
 // derivative is its own adjoint.
 //
-// Products run on v_mfma_f32_16x16x32_f16 with every operand split into two
+// Products run on v_mfma_f32_32x32x16_f16 with every operand split into two
 // binary16 parts (22 bits) and three products, hi*hi + hi*lo + lo*hi, summed
-// in binary32.  A panel of 16 columns is scaled by a power of two first, so
-// that its largest element lies in [2^14, 2^15): parts of smaller elements
-// then stay exact down to 2^-39 of it, and no matrix overflows the format.
-// Against binary32 products (v_mfma_f32_16x16x4f32) the results' errors are
-// the same to a factor of 1.3 (they come from the Gram matrix), at 3/16 of
-// the matrix-core time: 48 blocks of 128 x 1536, 161 us before.
+// in binary32.  A matrix is scaled by a power of two first, so that its
+// largest element lies in [2^14, 2^15): parts of smaller elements then stay
+// exact down to 2^-39 of it, and no matrix overflows the format.  Against
+// binary32 products (v_mfma_f32_16x16x4f32) the results' errors are the same
+// to a factor of 1.3 (they come from the Gram matrix), at 3/16 of the
+// matrix-core time.
 //
-// Wave w of MT holds column panel w of every matrix in its registers, as the
-// accumulator tiles of the products.  Two such tiles, one above the other,
-// are at the same time the B operand of a later product's k-step of 32, with
-// k taken in the order 32 kk + {4 g + v, 16 + 4 g + v} (g = lane / 16).  A
+// Wave w holds columns 32 w to 32 w + 31 of every matrix in its registers, as
+// the accumulator tiles of the products.  Half of such a tile (8 of a lane's
+// 16 values) is at the same time the B operand of a later product's k-step of
+// 16, with k taken in the order {4 h + v, 8 + 4 h + v} (h = lane / 32).  A
 // product L R therefore needs only L in LDS, and as every matrix is symmetric
 // but for rounding, row i of L is column i: the operand registers are stored
 // as they are, 16 bytes a lane, and read back the same way by every wave.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "blocks_device.h"
 
 #pragma clang fp contract(off)
+
+#define MUON_INLINE __attribute__((always_inline))
 
 namespace muon {
 namespace {
@@ -38,16 +42,28 @@ constexpr float NORM_EPS = 1e-7f;
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
-// A column panel as product operand: hi and lo parts per k-step of 32, and
-// the power of two the values were multiplied with (the same in all lanes).
-template <int MT>
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// Row of value v of a lane in half h in an accumulator tile.
+__device__ __forceinline__ int tile_row32(int v, int h) { return 8 * (v >> 2) + 4 * h + (v & 3); }
+
+// A wave's columns as product operand: 2^ex times the values, as hi and lo
+// parts per k-step of 16.  ex is the same for all waves where the matrix goes
+// to LDS too.
+template <int NR>
 struct Operand {
-  f16x8_t f[MT / 2][2];
+  f16x8_t f[NR][2][2];  // row tile, half, part
   int ex;
 };
 
-// The largest bits of a non-negative float over the wave, in a scalar register.
-__device__ __forceinline__ uint32_t wave_max_bits(float v) {
+// The bits of the largest |X| over the wave, in a scalar register.
+template <int NR>
+__device__ __forceinline__ uint32_t max_bits(const f32x16_t (&X)[NR]) {
+  float v = 0.f;
+#pragma unroll
+  for (int kt = 0; kt < NR; ++kt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v = fmaxf(v, __builtin_fabsf(X[kt][i]));
   // rows of 16 lanes by rotation, then the four rows
 #define MUON_ROW_MAX(ctl) \
   v = fmaxf(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, int(__float_as_uint(v)), ctl, 0xF, 0xF, false)))
@@ -63,93 +79,100 @@ __device__ __forceinline__ uint32_t wave_max_bits(float v) {
   return max(m, uint32_t(__builtin_amdgcn_readlane(b, 48)));
 }
 
-template <int MT>
-__device__ __forceinline__ void split_panel(const f32x4_t (&X)[MT], Operand<MT>& o) {
-  float mx = 0.f;
+// 2^x takes a largest element in [2^e, 2^(e + 1)) to [2^14, 2^15); bounded so
+// that 2^x is a binary32 number (elements below 2^-106 come out smaller).
+__device__ __forceinline__ int scale_for(uint32_t bits) { return min(14 + 127 - int(bits >> 23), 120); }
+
+// The parts of 2^x X, one row tile.
+__device__ __forceinline__ void split_tile(const f32x16_t& X, float s, f16x8_t (&f)[2][2]) {
 #pragma unroll
-  for (int kt = 0; kt < MT; ++kt)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) mx = fmaxf(mx, __builtin_fabsf(X[kt][v]));
-  // mx in [2^e, 2^(e + 1)) goes to [2^14, 2^15) (subnormals and zero below it)
-  o.ex = 14 + 127 - int(wave_max_bits(mx) >> 23);
-#pragma unroll
-  for (int kk = 0; kk < MT / 2; ++kk) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int v = 0; v < 4; v += 2) {
-        const f32x2_t x = {__builtin_amdgcn_ldexpf(X[2 * kk + h][v], o.ex),
-                           __builtin_amdgcn_ldexpf(X[2 * kk + h][v + 1], o.ex)};
-        const f16x2_t hi = __builtin_convertvector(x, f16x2_t);
-        const f32x2_t rest = {x[0] - float(hi[0]), x[1] - float(hi[1])};
-        const f16x2_t lo = __builtin_convertvector(rest, f16x2_t);
-        o.f[kk][0][4 * h + v] = hi[0];
-        o.f[kk][0][4 * h + v + 1] = hi[1];
-        o.f[kk][1][4 * h + v] = lo[0];
-        o.f[kk][1][4 * h + v + 1] = lo[1];
-      }
+  for (int v = 0; v < 16; ++v) {
+    // mixed-precision multiply-adds: both parts rounded once
+    const _Float16 hi = _Float16(__builtin_fmaf(X[v], s, 0.f));
+    f[v / 8][0][v % 8] = hi;
+    f[v / 8][1][v % 8] = _Float16(__builtin_fmaf(X[v], s, -float(hi)));
   }
+  // opaque from here on: binary32 copies of the parts, kept for combine(),
+  // would spill
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int l = 0; l < 2; ++l) asm volatile("" : "+v"(f[i][l]));
 }
 
 // A matrix in LDS: row i holds column i of the matrix, two parts.
-template <int MT>
+template <int NR>
 struct Left {
-  uint16_t v[2][16 * MT][16 * MT + 8];
-  int32_t ex[MT];
+  uint16_t v[2][32 * NR][32 * NR + 8];
 };
 
-template <int MT>
-__device__ __forceinline__ void put_panel(Left<MT>& L, const Operand<MT>& o, int panel, int r, int g, int lane) {
+template <int NR>
+__device__ __forceinline__ void zero_sums(f32x16_t (&acc)[NR]) {
 #pragma unroll
-  for (int kk = 0; kk < MT / 2; ++kk)
+  for (int jt = 0; jt < NR; ++jt)
 #pragma unroll
-    for (int l = 0; l < 2; ++l)
-      *reinterpret_cast<f16x8_t*>(&L.v[l][16 * panel + r][32 * kk + 8 * g]) = o.f[kk][l];
-  if (lane == 0) L.ex[panel] = o.ex;
+    for (int v = 0; v < 16; ++v) acc[jt][v] = 0.f;
 }
 
-// acc = L X for the wave's panel X: MT independent sums.
-template <int MT>
-__device__ __forceinline__ void multiply(f32x4_t (&acc)[MT], const Left<MT>& L, const Operand<MT>& X, int r, int g) {
+// acc += L X for the wave's columns X, both as scaled.
+template <int NR>
+__device__ __forceinline__ void multiply(f32x16_t (&acc)[NR], const Left<NR>& L, const Operand<NR>& X, int c, int h) {
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int jt = 0; jt < MT; ++jt) acc[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int ks = 0; ks < 2 * NR; ++ks)
 #pragma unroll
-  for (int kk = 0; kk < MT / 2; ++kk) {
-#pragma unroll
-    for (int jt = 0; jt < MT; ++jt) {
-      const f16x8_t hi = *reinterpret_cast<const f16x8_t*>(&L.v[0][16 * jt + r][32 * kk + 8 * g]);
-      const f16x8_t lo = *reinterpret_cast<const f16x8_t*>(&L.v[1][16 * jt + r][32 * kk + 8 * g]);
-      acc[jt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, X.f[kk][0], acc[jt], 0, 0, 0);
-      acc[jt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, X.f[kk][1], acc[jt], 0, 0, 0);
-      acc[jt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, X.f[kk][0], acc[jt], 0, 0, 0);
+    for (int jt = 0; jt < NR; ++jt) {
+      const f16x8_t hi = *reinterpret_cast<const f16x8_t*>(&L.v[0][32 * jt + c][16 * ks + 8 * h]);
+      const f16x8_t lo = *reinterpret_cast<const f16x8_t*>(&L.v[1][32 * jt + c][16 * ks + 8 * h]);
+      acc[jt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo, X.f[ks / 2][ks & 1][0], acc[jt], 0, 0, 0);
+      acc[jt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi, X.f[ks / 2][ks & 1][1], acc[jt], 0, 0, 0);
+      acc[jt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi, X.f[ks / 2][ks & 1][0], acc[jt], 0, 0, 0);
     }
-    if (MT >= 4) __builtin_amdgcn_sched_barrier(0);  // bounds how far the reads of L are hoisted
-  }
+  // the reads of L run AHEAD pairs ahead of the products that take them (all
+  // of them at once would spill, one at a time waits for LDS)
+  constexpr int ITEMS = 2 * NR * NR, AHEAD = ITEMS < 4 ? ITEMS : 4;
+  __builtin_amdgcn_sched_group_barrier(0x100, 2 * AHEAD, 0);
 #pragma unroll
-  for (int jt = 0; jt < MT; ++jt) {
-    const int e = -(L.ex[jt] + X.ex);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) acc[jt][v] = __builtin_amdgcn_ldexpf(acc[jt][v], e);
+  for (int i = 0; i < ITEMS - AHEAD; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 3, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
   }
+  __builtin_amdgcn_sched_group_barrier(0x008, 3 * AHEAD, 0);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// acc = c 2^-e acc + b X
+template <int NR>
+__device__ __forceinline__ void combine(f32x16_t (&acc)[NR], float c, int e, float b, const Operand<NR>& X) {
+  const float ce = __builtin_amdgcn_ldexpf(c, -e), be = __builtin_amdgcn_ldexpf(b, -X.ex);
+#pragma unroll
+  for (int kt = 0; kt < NR; ++kt)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      float t = ce * acc[kt][v];
+      t = __builtin_fmaf(float(X.f[kt][v / 8][0][v % 8]), be, t);
+      acc[kt][v] = __builtin_fmaf(float(X.f[kt][v / 8][1][v % 8]), be, t);
+    }
 }
 
 template <int MT, int KIND>
-__global__ __launch_bounds__(64 * MT, 2) void block_iterate_kernel(
+__global__ __launch_bounds__(32 * MT, KIND == BK_VJP ? 1 : 2) void block_iterate_kernel(
     BlockTable tab, const float* __restrict__ partials, uint16_t* __restrict__ p_out, uint16_t* __restrict__ t_out,
     float* __restrict__ scratch, BlockSteps steps, int32_t pp) {
-  constexpr int MP = 16 * MT, NT = 64 * MT;
+  constexpr int MP = 16 * MT, NR = MT / 2, NW = MT / 2, NT = 64 * NW;
   constexpr bool VJP = KIND == BK_VJP;
   constexpr int LDM = MP + 4;
   // the Gram matrix (and Z) in binary32 first, then the left factors
   union Lds {
     float gram[VJP ? 2 : 1][MP][LDM];
-    Left<MT> left[VJP ? 2 : 1];
+    Left<NR> left[VJP ? 2 : 1];
   };
   __shared__ __attribute__((aligned(16))) Lds lds;
   __shared__ float red[8];
+  __shared__ int32_t mx[2][8];
 
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int r = lane & 15, g = lane >> 4;
+  const int c = lane & 31, h = lane >> 5;
   const int blk = blockIdx.x;
   const BlockStack st = find_stack(&BlockStack::block0, blk);
   const int b = blk - st.block0;
@@ -194,163 +217,214 @@ __global__ __launch_bounds__(64 * MT, 2) void block_iterate_kernel(
   const float norm = __builtin_sqrtf(tr);
   const float inv = steps.first ? 1.f / (norm + NORM_EPS) : 1.f;
 
-  // A_j (and its tangent) in binary32; P lives as an operand only, and its
-  // new value passes through A while A_j is one
-  f32x4_t A[MT], D[VJP ? MT : 1];
+  // A_j and P (and their tangents D and dP) live as operands; C (E) holds what
+  // the last product gave, 2^ec (2^ee) times the matrix.  A lane's values are
+  // rows 32 kt + tile_row32(v, h) of column 32 w + c.
+  f32x16_t C[NR], E[VJP ? NR : 1];
+  int ec = 0, ee = 0;
+  Operand<NR> oA, oP, oD, odP;
 #pragma unroll
-  for (int kt = 0; kt < MT; ++kt)
+  for (int kt = 0; kt < NR; ++kt)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int i = 16 * kt + 4 * g + v, j = 16 * w + r;
-      A[kt][v] = (L0[i][j] * inv) * inv;
-      if constexpr (VJP) D[kt][v] = (0.5f * inv) * (L1[i][j] + L1[j][i]);
+    for (int v = 0; v < 16; ++v) {
+      const int i = 32 * kt + tile_row32(v, h), j = 32 * w + c;
+      C[kt][v] = (L0[i][j] * inv) * inv;
+      if constexpr (VJP) E[kt][v] = (0.5f * inv) * (L1[i][j] + L1[j][i]);
     }
   float* sc = nullptr;
   if constexpr (VJP) {
     // A_0 and D_0 are needed again for <dX_0, X_0>
     sc = scratch + int64_t(blk) * (2 * MP * MP) + 4 * tid;
 #pragma unroll
-    for (int kt = 0; kt < MT; ++kt) {
-      *gmem(reinterpret_cast<f32x4_t*>(sc + kt * NT * 4)) = A[kt];
-      *gmem(reinterpret_cast<f32x4_t*>(sc + (MT + kt) * NT * 4)) = D[kt];
-    }
+    for (int kt = 0; kt < NR; ++kt)
+#pragma unroll
+      for (int v = 0; v < 16; v += 4) {
+        *gmem(reinterpret_cast<f32x4_t*>(sc + (4 * kt + v / 4) * NT * 4)) =
+            f32x4_t{C[kt][v], C[kt][v + 1], C[kt][v + 2], C[kt][v + 3]};
+        *gmem(reinterpret_cast<f32x4_t*>(sc + (4 * (NR + kt) + v / 4) * NT * 4)) =
+            f32x4_t{E[kt][v], E[kt][v + 1], E[kt][v + 2], E[kt][v + 3]};
+      }
   }
 
-  Left<MT>& LA = lds.left[0];
-  Left<MT>& LD = lds.left[VJP ? 1 : 0];
-  Operand<MT> oA, oP, oD, odP;  // oD, odP: the gradient's
-
-  // A -> Q = a I + b A + c A A in its place (D -> dQ), A_t left in oA (oD)
-  auto form_q = [&](int t) {
-    const float ca = steps.a[t], cb = steps.b[t], cc = steps.c[t];
-    split_panel<MT>(A, oA);
-    if constexpr (VJP) split_panel<MT>(D, oD);
+  Left<NR>& LA = lds.left[0];
+  Left<NR>& LD = lds.left[VJP ? 1 : 0];
+  int la = 0, ld = 0;  // powers of two of LA and LD
+  auto split_one = [&](const f32x16_t (&X)[NR], int e, Operand<NR>& o) MUON_INLINE {
+    const int x = scale_for(max_bits<NR>(X));
+    o.ex = e + x;
+    const float s = __builtin_amdgcn_ldexpf(1.f, x);
 #pragma unroll
-    for (int kt = 0; kt < MT; ++kt) {
-      A[kt] *= cb;
-      if constexpr (VJP) D[kt] *= cb;
+    for (int kt = 0; kt < NR; ++kt) {
+      split_tile(X[kt], s, o.f[kt]);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (cc != 0.f) {
-      __syncthreads();  // the reads of LDS before are done
-      put_panel<MT>(LA, oA, w, r, g, lane);
-      if constexpr (VJP) put_panel<MT>(LD, oD, w, r, g, lane);
-      __syncthreads();
-      f32x4_t x[MT];
-      multiply<MT>(x, LA, oA, r, g);
-#pragma unroll
-      for (int kt = 0; kt < MT; ++kt) A[kt] += cc * x[kt];
-      if constexpr (VJP) {
-        multiply<MT>(x, LA, oD, r, g);
-#pragma unroll
-        for (int kt = 0; kt < MT; ++kt) D[kt] += cc * x[kt];
-        multiply<MT>(x, LD, oA, r, g);
-#pragma unroll
-        for (int kt = 0; kt < MT; ++kt) D[kt] += cc * x[kt];
-      }
-    }
-#pragma unroll
-    for (int kt = 0; kt < MT; ++kt)
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (16 * kt + 4 * g + v == 16 * w + r) A[kt][v] += ca;
   };
-  // (A, D) <- L (o, od) and its tangent
-  auto left_times = [&](const Operand<MT>& o, const Operand<MT>& od) {
-    multiply<MT>(A, LA, o, r, g);
+  // C (E) as the wave's operand o (od)
+  auto split_into = [&](Operand<NR>& o, Operand<NR>& od) MUON_INLINE {
+    split_one(C, ec, o);
+    if constexpr (VJP) split_one(E, ee, od);
+  };
+  // X to LDS, and as operand o
+  auto put_one = [&](auto keep, const f32x16_t (&X)[NR], Left<NR>& L, int x, Operand<NR>& o) MUON_INLINE {
+    const float s = __builtin_amdgcn_ldexpf(1.f, x);
+#pragma unroll
+    for (int kt = 0; kt < NR; ++kt) {
+      f16x8_t f[2][2];
+      split_tile(X[kt], s, f);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int l = 0; l < 2; ++l) {
+          *reinterpret_cast<f16x8_t*>(&L.v[l][32 * w + c][32 * kt + 16 * i + 8 * h]) = f[i][l];
+          if constexpr (decltype(keep)::value) o.f[kt][i][l] = f[i][l];
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // C (E) to LDS, with one power of two for all waves; and as operand o (od)
+  auto put = [&](auto keep, Operand<NR>& o, Operand<NR>& od) MUON_INLINE {
+    // the power of two that each wave would take, and the least of them
+    const int xc = ec + scale_for(max_bits<NR>(C));
+    const int xe = VJP ? ee + scale_for(max_bits<VJP ? NR : 1>(E)) : 0;
+    if (lane == 0) {
+      mx[0][w] = xc;
+      if constexpr (VJP) mx[1][w] = xe;
+    }
+    __syncthreads();  // also: the reads of LDS before are done
+    la = mx[0][0];
+    if constexpr (VJP) ld = mx[1][0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) {
+      la = min(la, mx[0][i]);
+      if constexpr (VJP) ld = min(ld, mx[1][i]);
+    }
+    la = __builtin_amdgcn_readfirstlane(la);
+    put_one(keep, C, LA, la - ec, o);
     if constexpr (VJP) {
-      f32x4_t x[MT];
-      multiply<MT>(D, LA, od, r, g);
-      multiply<MT>(x, LD, o, r, g);
+      ld = __builtin_amdgcn_readfirstlane(ld);
+      put_one(keep, E, LD, ld - ee, od);
+    }
+    if constexpr (decltype(keep)::value) {
+      o.ex = la;
+      od.ex = ld;
+    }
+    __syncthreads();
+  };
+  // (C, E) <- L (o, od) and its tangent LA od + LD o
+  auto left_times = [&](const Operand<NR>& o, const Operand<NR>& od) MUON_INLINE {
+    zero_sums<NR>(C);
+    multiply<NR>(C, LA, o, c, h);
+    ec = la + o.ex;
+    if constexpr (VJP) {
+      zero_sums<NR>(E);
+      multiply<NR>(E, LA, od, c, h);
+      ee = ld + o.ex;
+      const int d = ee - (la + od.ex);
+      if (d != 0) {
 #pragma unroll
-      for (int kt = 0; kt < MT; ++kt) D[kt] += x[kt];
+        for (int jt = 0; jt < NR; ++jt)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) E[jt][v] = __builtin_amdgcn_ldexpf(E[jt][v], d);
+      }
+      multiply<NR>(E, LD, o, c, h);
     }
   };
-  auto split_into = [&](Operand<MT>& o, Operand<MT>& od) {
-    split_panel<MT>(A, o);
-    if constexpr (VJP) split_panel<MT>(D, od);
+  // C <- Q = a I + b A + c A A (E <- dQ) from A in C (D in E), left in oA (oD)
+  auto form_q = [&](int t) MUON_INLINE {
+    const float ca = steps.a[t], cb = steps.b[t], cc = steps.c[t];
+    put(std::true_type{}, oA, oD);
+    if (cc != 0.f) {
+      left_times(oA, oD);
+    } else {
+      zero_sums<NR>(C);
+      if constexpr (VJP) zero_sums<NR>(E);
+    }
+    combine<NR>(C, cc, ec, cb, oA);
+    if constexpr (VJP) combine<NR>(E, cc, ee, cb, oD);
+    ec = ee = 0;
+#pragma unroll
+    for (int kt = 0; kt < NR; ++kt)
+      if (kt == w) {
+#pragma unroll
+        for (int v = 0; v < 16; ++v) C[kt][v] += tile_row32(v, h) == c ? ca : 0.f;
+      }
   };
   if (steps.steps > 0) form_q(0);  // P = Q
   if (steps.steps > 1) {
-    split_into(oP, odP);
-    __syncthreads();
-    put_panel<MT>(LA, oP, w, r, g, lane);
-    if constexpr (VJP) put_panel<MT>(LD, odP, w, r, g, lane);
-    __syncthreads();
+    put(std::true_type{}, oP, odP);
 #pragma unroll 1
     for (int t = 1; t < steps.steps; ++t) {
       left_times(oA, oD);  // R = Q A
       split_into(oA, oD);
       left_times(oA, oD);  // A <- Q R
       form_q(t);
-      __syncthreads();
-      {
-        Operand<MT> o;
-        split_panel<MT>(A, o);
-        put_panel<MT>(LA, o, w, r, g, lane);
-        if constexpr (VJP) {
-          split_panel<MT>(D, o);
-          put_panel<MT>(LD, o, w, r, g, lane);
-        }
-      }
-      __syncthreads();
+      put(std::false_type{}, oA, oD);
       left_times(oP, odP);  // P <- Q P
-      split_into(oP, odP);
+      if (t + 1 < steps.steps) split_into(oP, odP);
     }
   }
-  // P is in A, dP in D
+  // P is in C, dP in E
   if (steps.steps == 0) {
+    ec = ee = 0;
 #pragma unroll
-    for (int kt = 0; kt < MT; ++kt)
+    for (int kt = 0; kt < NR; ++kt)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        A[kt][v] = 16 * kt + 4 * g + v == 16 * w + r ? 1.f : 0.f;
-        if constexpr (VJP) D[kt][v] = 0.f;
+      for (int v = 0; v < 16; ++v) {
+        C[kt][v] = kt == w && tile_row32(v, h) == c ? 1.f : 0.f;
+        if constexpr (VJP) E[kt][v] = 0.f;
       }
   }
 
+#pragma unroll
+  for (int kt = 0; kt < NR; ++kt)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      C[kt][v] = __builtin_amdgcn_ldexpf(C[kt][v], -ec);
+      if constexpr (VJP) E[kt][v] = __builtin_amdgcn_ldexpf(E[kt][v], -ee);
+    }
   if constexpr (VJP) {
     float shift = 0.f;
     if (steps.first) {
       // <dX_0, X_0> = <P, D_0> + <2 dP, A_0>
       float k = 0.f;
 #pragma unroll
-      for (int kt = 0; kt < MT; ++kt) {
-        const f32x4_t a0 = *gmem(reinterpret_cast<const f32x4_t*>(sc + kt * NT * 4));
-        const f32x4_t d0 = *gmem(reinterpret_cast<const f32x4_t*>(sc + (MT + kt) * NT * 4));
+      for (int kt = 0; kt < NR; ++kt)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) k += A[kt][v] * d0[v] + 2.f * D[kt][v] * a0[v];
-      }
+        for (int v = 0; v < 16; v += 4) {
+          const f32x4_t a0 = *gmem(reinterpret_cast<const f32x4_t*>(sc + (4 * kt + v / 4) * NT * 4));
+          const f32x4_t d0 = *gmem(reinterpret_cast<const f32x4_t*>(sc + (4 * (NR + kt) + v / 4) * NT * 4));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) k += C[kt][v + i] * d0[i] + 2.f * E[kt][v + i] * a0[i];
+        }
 #pragma unroll
       for (int d = 32; d > 0; d >>= 1) k += __shfl_xor(k, d);
       if (lane == 0) red[w] = k;
       __syncthreads();
       k = 0.f;
 #pragma unroll
-      for (int q = 0; q < MT; ++q) k += red[q];
+      for (int q = 0; q < NW; ++q) k += red[q];
       // a zero block has no direction: the norm's gradient is taken as zero
       shift = norm > 0.f ? inv * (k / norm) : 0.f;
     }
 #pragma unroll
-    for (int kt = 0; kt < MT; ++kt)
+    for (int kt = 0; kt < NR; ++kt)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float tt = (2.f * D[kt][v]) * inv * inv;
-        D[kt][v] = 16 * kt + 4 * g + v == 16 * w + r ? tt - shift : tt;
+      for (int v = 0; v < 16; ++v) {
+        const float tt = (2.f * E[kt][v]) * inv * inv;
+        E[kt][v] = kt == w && tile_row32(v, h) == c ? tt - shift : tt;
       }
   }
-#pragma unroll
-  for (int kt = 0; kt < MT; ++kt) A[kt] *= inv;
 
   // out in bfloat16 parts, by rows, through LDS.  P X is not P^T X here: P is
   // the product Q_k ... Q_0, whose last factors carry the largest errors, and
   // they act on what the first ones have left of X's large singular values
   __syncthreads();
 #pragma unroll
-  for (int kt = 0; kt < MT; ++kt)
+  for (int kt = 0; kt < NR; ++kt)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      L0[16 * kt + 4 * g + v][16 * w + r] = A[kt][v];
-      if constexpr (VJP) L1[16 * kt + 4 * g + v][16 * w + r] = D[kt][v];
+    for (int v = 0; v < 16; ++v) {
+      L0[32 * kt + tile_row32(v, h)][32 * w + c] = C[kt][v] * inv;
+      if constexpr (VJP) L1[32 * kt + tile_row32(v, h)][32 * w + c] = E[kt][v];
     }
   __syncthreads();
 #pragma unroll
@@ -379,7 +453,7 @@ hipError_t launch_block_iterate(int mt, int pp, int kind, const BlockTable& tab,
   if (blocks <= 0) return hipSuccess;
 #define MUON_ITER(MT, KIND)                                                                                      \
   if (mt == MT && kind == KIND) {                                                                                \
-    hipLaunchKernelGGL((block_iterate_kernel<MT, KIND>), dim3(blocks), dim3(64 * MT), 0, stream, tab, partials,  \
+    hipLaunchKernelGGL((block_iterate_kernel<MT, KIND>), dim3(blocks), dim3(32 * MT), 0, stream, tab, partials,  \
                        p_out, t_out, scratch, steps, pp);                                                        \
     return hipGetLastError();                                                                                    \
   }
