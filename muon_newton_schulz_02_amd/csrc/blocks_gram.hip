@@ -14,6 +14,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cstring>
+
 #include "blocks_device.h"
 
 #pragma clang fp contract(off)
@@ -201,13 +203,24 @@ __global__ __launch_bounds__(GT, KIND == BK_VJP ? 2 : 4) void block_gram_kernel(
   }
 }
 
-struct BlockStackBatch {
-  BlockStack s[BLOCK_INLINE];
-};
-
-__global__ void block_table_kernel(BlockStackBatch in, int32_t n, BlockStack* __restrict__ out) {
+__global__ void block_table_kernel(BlockTableBatch in, BlockStack* __restrict__ out) {
   const int i = threadIdx.x;
-  if (i < n) out[i] = in.s[i];
+  if (i >= in.n) return;
+  int c = 0;
+#pragma unroll
+  for (int q = 1; q < BLOCK_CLASSES; ++q)
+    if (i >= in.first[q]) c = q;
+  BlockStack s = in.cls[c];
+  const int k = i - in.first[c];
+  s.x = in.x[i];
+  s.y = in.y[i];
+  s.out = in.out[i];
+  s.upd = in.upd[i];
+  s.block0 += k * s.blocks;
+  s.goff += k * s.blocks * s.gsplit;
+  s.aoff += k * s.blocks * s.asplit;
+  s.part0 += int64_t(k) * s.blocks * s.gsplit * in.part;
+  out[i] = s;
 }
 
 template <int MT>
@@ -234,14 +247,43 @@ hipError_t gram_mt(int pl, int kind, bool xbf, const BlockTable& tab, int32_t wg
 
 }  // namespace
 
-hipError_t launch_block_table(const BlockStack* host, int32_t count, BlockStack* dev, hipStream_t stream) {
-  for (int32_t i = 0; i < count; i += BLOCK_INLINE) {
-    BlockStackBatch batch = {};
-    const int32_t n = count - i < BLOCK_INLINE ? count - i : BLOCK_INLINE;
-    for (int32_t k = 0; k < n; ++k) batch.s[k] = host[i + k];
-    hipLaunchKernelGGL(block_table_kernel, dim3(1), dim3(64), 0, stream, batch, n, dev + i);
+hipError_t launch_block_table(const BlockStack* host, int32_t count, int32_t part, BlockStack* dev,
+                              hipStream_t stream) {
+  // what two stacks of a run share
+  auto key = [](BlockStack s) {
+    s.x = s.y = nullptr;
+    s.out = nullptr;
+    s.upd = nullptr;
+    s.part0 = 0;
+    s.block0 = s.goff = s.aoff = 0;
+    return s;
+  };
+  for (int32_t i = 0; i < count;) {
+    BlockTableBatch b;
+    memset(&b, 0, sizeof(b));
+    b.part = part;
+    int32_t classes = 0;
+    BlockStack last;
+    while (i + b.n < count && b.n < BLOCK_BATCH) {
+      const BlockStack& s = host[i + b.n];
+      const BlockStack k = key(s);
+      if (classes == 0 || memcmp(&k, &last, sizeof(k)) != 0) {
+        if (classes == BLOCK_CLASSES) break;
+        b.first[classes] = b.n;
+        b.cls[classes++] = s;
+        last = k;
+      }
+      b.x[b.n] = s.x;
+      b.y[b.n] = s.y;
+      b.out[b.n] = s.out;
+      b.upd[b.n] = s.upd;
+      ++b.n;
+    }
+    for (int32_t c = classes; c < BLOCK_CLASSES; ++c) b.first[c] = b.n;
+    hipLaunchKernelGGL(block_table_kernel, dim3(1), dim3(128), 0, stream, b, dev + i);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    i += b.n;
   }
   return hipSuccess;
 }

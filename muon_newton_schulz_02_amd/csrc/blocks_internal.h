@@ -84,9 +84,27 @@ constexpr int64_t BLOCK_MAX_LD = int64_t(1) << 21;
 // Type of x known when a kernel is compiled, or read from the flags.
 enum BlockXType : int { BX_F32 = 0, BX_BF16 = 1, BX_ANY = 2 };
 
+// One launch of block_table_kernel: runs of stacks that differ in their
+// pointers only, each given by its first member.
+constexpr int BLOCK_BATCH = 96, BLOCK_CLASSES = 4;
+struct BlockTableBatch {
+  int32_t n;
+  int32_t first[BLOCK_CLASSES];   // first entry of each run (runs not used: n)
+  int32_t part;                   // floats of one workgroup's Gram partial
+  BlockStack cls[BLOCK_CLASSES];
+  const void* x[BLOCK_BATCH];
+  const void* y[BLOCK_BATCH];
+  void* out[BLOCK_BATCH];
+  float* upd[BLOCK_BATCH];
+};
+static_assert(sizeof(BlockTableBatch) <= 4096, "kernel arguments stay below 4 KiB");
+
 // The launchers.  pl: bfloat16 parts of an element of x (1, 2, 3); pp: parts
 // of an element of P (2, 3); xbf: x is bfloat16 in every stack.
-hipError_t launch_block_table(const BlockStack* host, int32_t count, BlockStack* dev, hipStream_t stream);
+// Writes a table of `count` stacks to device memory.  part: floats of one
+// workgroup's Gram partial.
+hipError_t launch_block_table(const BlockStack* host, int32_t count, int32_t part, BlockStack* dev,
+                              hipStream_t stream);
 hipError_t launch_block_gram(int mt, int pl, int kind, bool xbf, const BlockTable& tab, int32_t wgs, float* partials,
                              const BlockMom& mom, hipStream_t stream);
 // Sums the partials of every block, runs the recursion and writes P (and, for

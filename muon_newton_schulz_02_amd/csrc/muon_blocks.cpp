@@ -16,6 +16,7 @@
 #include <cstring>
 #include <map>
 #include <new>
+#include <tuple>
 #include <vector>
 
 #include "api_internal.h"
@@ -355,6 +356,14 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
     const int kc = block_kc(g.mt), mp = 16 * g.mt;
     const int kind = vjp ? BK_VJP : c.op == MUON_BLOCKS_STEP ? BK_STEP : BK_X;
     g.stages = stages_of(c, g.limit);
+    // members of equal shapes and strides next to each other: runs that differ
+    // in their pointers only take one entry of a table launch
+    auto key = [&](int32_t i) {
+      const muon_block_desc& d = c.stacks[i];
+      return std::make_tuple(d.rows, d.cols, d.blocks, d.ld_grad, d.ld_param, d.ld_mom, d.stride_grad, d.stride_param,
+                             d.stride_mom);
+    };
+    std::stable_sort(g.members.begin(), g.members.end(), [&](int32_t a, int32_t b) { return key(a) < key(b); });
     // workgroups enough to fill the GPU four times over, two to a compute
     // unit, each with two tiles of columns at least
     const int64_t want = std::max<int64_t>(1, (8 * int64_t(cus) + g.blocks - 1) / g.blocks);
@@ -494,6 +503,7 @@ hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
   };
 
   int32_t table = 0;
+  const int32_t part = block_part_floats(g.mt, vjp ? BK_VJP : BK_X);
   BlockTable tab;
   memset(&tab, 0, sizeof(tab));
   auto set_table = [&](const std::vector<BlockStack>& v) -> hipError_t {
@@ -505,7 +515,7 @@ hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
     }
     BlockStack* dev = reinterpret_cast<BlockStack*>(ws + g.o_tab) + size_t(table++) * v.size();
     tab.ext = dev;
-    return launch_block_table(v.data(), int32_t(v.size()), dev, c.stream);
+    return launch_block_table(v.data(), int32_t(v.size()), part, dev, c.stream);
   };
   auto steps_of = [&](const Stage& st, bool first) {
     BlockSteps s;
