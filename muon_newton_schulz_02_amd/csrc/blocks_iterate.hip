@@ -7,22 +7,22 @@
 // every matrix is a function of A_0, so the order of factors is free and the
 // derivative is its own adjoint.
 //
-// Products run on v_mfma_f32_32x32x16_f16 with every operand split into two
-// binary16 parts (22 bits) and three products, hi*hi + hi*lo + lo*hi, summed
-// in binary32.  A matrix is scaled by a power of two first, so that its
-// largest element lies in [2^14, 2^15): parts of smaller elements then stay
-// exact down to 2^-39 of it, and no matrix overflows the format.  Against
-// binary32 products (v_mfma_f32_16x16x4f32) the results' errors are the same
-// to a factor of 1.3 (they come from the Gram matrix), at 3/16 of the
-// matrix-core time.
+// Products run on binary16 MFMAs with every operand split into two parts (22
+// bits) and three products, hi*hi + hi*lo + lo*hi, summed in binary32.  A
+// matrix is scaled by a power of two first, so that its largest element lies
+// in [2^14, 2^15): parts of smaller elements then stay exact down to 2^-39 of
+// it, and no matrix overflows the format.  Against binary32 products
+// (v_mfma_f32_16x16x4f32) the results' errors are the same to a factor of 1.3
+// (they come from the Gram matrix), at 3/16 of the matrix-core time.
 //
-// Wave w holds columns 32 w to 32 w + 31 of every matrix in its registers, as
-// the accumulator tiles of the products.  Half of such a tile (8 of a lane's
-// 16 values) is at the same time the B operand of a later product's k-step of
-// 16, with k taken in the order {4 h + v, 8 + 4 h + v} (h = lane / 32).  A
-// product L R therefore needs only L in LDS, and as every matrix is symmetric
-// but for rounding, row i of L is column i: the operand registers are stored
-// as they are, 16 bytes a lane, and read back the same way by every wave.
+// A wave holds TS columns of every matrix in its registers (TS = 16 or 32), as
+// the accumulator tiles of v_mfma_f32_16x16x32_f16 or _32x32x16_f16.  A lane's
+// values 8 q, ..., 8 q + 7, counted through the tiles, are at the same time
+// the B operand of a later product's k-step q, with k taken in the order of
+// their rows.  A product L R therefore needs only L in LDS, and as every
+// matrix is symmetric but for rounding, row i of L is column i: the operand
+// registers are stored as they are, 16 bytes a lane, and read back the same
+// way by every wave.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -44,26 +44,52 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
-// Row of value v of a lane in half h in an accumulator tile.
-__device__ __forceinline__ int tile_row32(int v, int h) { return 8 * (v >> 2) + 4 * h + (v & 3); }
+// Accumulator tiles of TS x TS: V values a lane, of column lane % TS.
+template <int TS>
+struct Tile;
+template <>
+struct Tile<16> {
+  static constexpr int V = 4;
+  typedef f32x4_t Acc;
+  static __device__ __forceinline__ Acc mfma(f16x8_t a, f16x8_t b, Acc c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ int row(int v, int h) { return 4 * h + v; }
+};
+template <>
+struct Tile<32> {
+  static constexpr int V = 16;
+  typedef f32x16_t Acc;
+  static __device__ __forceinline__ Acc mfma(f16x8_t a, f16x8_t b, Acc c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ int row(int v, int h) { return 8 * (v >> 2) + 4 * h + (v & 3); }
+};
+
+// Shapes of an MP x MP matrix on waves of TS columns each.
+template <int MP, int TS>
+struct Shape {
+  static constexpr int NR = MP / TS, V = Tile<TS>::V, NV = NR * V, NQ = NV / 8;  // row tiles, values, k-steps
+  static constexpr int KS = MP / NQ;                                             // columns of a k-step
+  typedef typename Tile<TS>::Acc Acc;
+};
 
 // A wave's columns as product operand: 2^ex times the values, as hi and lo
-// parts per k-step of 16.  ex is the same for all waves where the matrix goes
-// to LDS too.
-template <int NR>
+// parts.  ex is the same for all waves where the matrix goes to LDS too.
+template <int NQ>
 struct Operand {
-  f16x8_t f[NR][2][2];  // row tile, half, part
+  f16x8_t f[NQ][2];
   int ex;
 };
 
 // The bits of the largest |X| over the wave, in a scalar register.
-template <int NR>
-__device__ __forceinline__ uint32_t max_bits(const f32x16_t (&X)[NR]) {
+template <class Acc, int NR, int V>
+__device__ __forceinline__ uint32_t max_bits(const Acc (&X)[NR]) {
   float v = 0.f;
 #pragma unroll
   for (int kt = 0; kt < NR; ++kt)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v = fmaxf(v, __builtin_fabsf(X[kt][i]));
+    for (int i = 0; i < V; ++i) v = fmaxf(v, __builtin_fabsf(X[kt][i]));
   // rows of 16 lanes by rotation, then the four rows
 #define MUON_ROW_MAX(ctl) \
   v = fmaxf(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, int(__float_as_uint(v)), ctl, 0xF, 0xF, false)))
@@ -83,54 +109,61 @@ __device__ __forceinline__ uint32_t max_bits(const f32x16_t (&X)[NR]) {
 // that 2^x is a binary32 number (elements below 2^-106 come out smaller).
 __device__ __forceinline__ int scale_for(uint32_t bits) { return min(14 + 127 - int(bits >> 23), 120); }
 
-// The parts of 2^x X, one row tile.
-__device__ __forceinline__ void split_tile(const f32x16_t& X, float s, f16x8_t (&f)[2][2]) {
+// The parts of s X for k-step q.  hi is cut off after 11 bits (its conversion
+// is then exact), lo is what is left of the binary32 product, rounded.
+template <class Acc, int NR, int V>
+__device__ __forceinline__ void split_step(const Acc (&X)[NR], int q, float s, f16x8_t& hi, f16x8_t& lo) {
 #pragma unroll
-  for (int v = 0; v < 16; ++v) {
-    // mixed-precision multiply-adds: both parts rounded once
-    const _Float16 hi = _Float16(__builtin_fmaf(X[v], s, 0.f));
-    f[v / 8][0][v % 8] = hi;
-    f[v / 8][1][v % 8] = _Float16(__builtin_fmaf(X[v], s, -float(hi)));
+  for (int e = 0; e < 8; e += 2) {
+    const int i = 8 * q + e;
+    const f32x2_t x = {X[i / V][i % V] * s, X[(i + 1) / V][(i + 1) % V] * s};
+    const f32x2_t top = {__uint_as_float(__float_as_uint(x[0]) & 0xFFFFE000u),
+                         __uint_as_float(__float_as_uint(x[1]) & 0xFFFFE000u)};
+    const f32x2_t rest = {x[0] - top[0], x[1] - top[1]};
+    const f16x2_t a = __builtin_convertvector(top, f16x2_t), b = __builtin_convertvector(rest, f16x2_t);
+    hi[e] = a[0];
+    hi[e + 1] = a[1];
+    lo[e] = b[0];
+    lo[e + 1] = b[1];
   }
   // opaque from here on: binary32 copies of the parts, kept for combine(),
   // would spill
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int l = 0; l < 2; ++l) asm volatile("" : "+v"(f[i][l]));
+  asm volatile("" : "+v"(hi), "+v"(lo));
 }
 
 // A matrix in LDS: row i holds column i of the matrix, two parts.
-template <int NR>
+template <int MP>
 struct Left {
-  uint16_t v[2][32 * NR][32 * NR + 8];
+  uint16_t v[2][MP][MP + 8];
 };
 
-template <int NR>
-__device__ __forceinline__ void zero_sums(f32x16_t (&acc)[NR]) {
+template <class Acc, int NR, int V>
+__device__ __forceinline__ void zero_sums(Acc (&acc)[NR]) {
 #pragma unroll
   for (int jt = 0; jt < NR; ++jt)
 #pragma unroll
-    for (int v = 0; v < 16; ++v) acc[jt][v] = 0.f;
+    for (int v = 0; v < V; ++v) acc[jt][v] = 0.f;
 }
 
 // acc += L X for the wave's columns X, both as scaled.
-template <int NR>
-__device__ __forceinline__ void multiply(f32x16_t (&acc)[NR], const Left<NR>& L, const Operand<NR>& X, int c, int h) {
+template <int MP, int TS>
+__device__ __forceinline__ void multiply(typename Tile<TS>::Acc (&acc)[MP / TS], const Left<MP>& L,
+                                         const Operand<Shape<MP, TS>::NQ>& X, int c, int h) {
+  using S = Shape<MP, TS>;
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int ks = 0; ks < 2 * NR; ++ks)
+  for (int q = 0; q < S::NQ; ++q)
 #pragma unroll
-    for (int jt = 0; jt < NR; ++jt) {
-      const f16x8_t hi = *reinterpret_cast<const f16x8_t*>(&L.v[0][32 * jt + c][16 * ks + 8 * h]);
-      const f16x8_t lo = *reinterpret_cast<const f16x8_t*>(&L.v[1][32 * jt + c][16 * ks + 8 * h]);
-      acc[jt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo, X.f[ks / 2][ks & 1][0], acc[jt], 0, 0, 0);
-      acc[jt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi, X.f[ks / 2][ks & 1][1], acc[jt], 0, 0, 0);
-      acc[jt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi, X.f[ks / 2][ks & 1][0], acc[jt], 0, 0, 0);
+    for (int jt = 0; jt < S::NR; ++jt) {
+      const f16x8_t hi = *reinterpret_cast<const f16x8_t*>(&L.v[0][TS * jt + c][S::KS * q + 8 * h]);
+      const f16x8_t lo = *reinterpret_cast<const f16x8_t*>(&L.v[1][TS * jt + c][S::KS * q + 8 * h]);
+      acc[jt] = Tile<TS>::mfma(lo, X.f[q][0], acc[jt]);
+      acc[jt] = Tile<TS>::mfma(hi, X.f[q][1], acc[jt]);
+      acc[jt] = Tile<TS>::mfma(hi, X.f[q][0], acc[jt]);
     }
   // the reads of L run AHEAD pairs ahead of the products that take them (all
   // of them at once would spill, one at a time waits for LDS)
-  constexpr int ITEMS = 2 * NR * NR, AHEAD = ITEMS < 4 ? ITEMS : 4;
+  constexpr int ITEMS = S::NQ * S::NR, AHEAD = ITEMS < 4 ? ITEMS : 4;
   __builtin_amdgcn_sched_group_barrier(0x100, 2 * AHEAD, 0);
 #pragma unroll
   for (int i = 0; i < ITEMS - AHEAD; ++i) {
@@ -142,37 +175,47 @@ __device__ __forceinline__ void multiply(f32x16_t (&acc)[NR], const Left<NR>& L,
 }
 
 // acc = c 2^-e acc + b X
-template <int NR>
-__device__ __forceinline__ void combine(f32x16_t (&acc)[NR], float c, int e, float b, const Operand<NR>& X) {
+template <int MP, int TS>
+__device__ __forceinline__ void combine(typename Tile<TS>::Acc (&acc)[MP / TS], float c, int e, float b,
+                                        const Operand<Shape<MP, TS>::NQ>& X) {
+  using S = Shape<MP, TS>;
   const float ce = __builtin_amdgcn_ldexpf(c, -e), be = __builtin_amdgcn_ldexpf(b, -X.ex);
 #pragma unroll
-  for (int kt = 0; kt < NR; ++kt)
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      float t = ce * acc[kt][v];
-      t = __builtin_fmaf(float(X.f[kt][v / 8][0][v % 8]), be, t);
-      acc[kt][v] = __builtin_fmaf(float(X.f[kt][v / 8][1][v % 8]), be, t);
-    }
+  for (int i = 0; i < S::NV; ++i) {
+    float t = ce * acc[i / S::V][i % S::V];
+    t = __builtin_fmaf(float(X.f[i / 8][0][i % 8]), be, t);
+    acc[i / S::V][i % S::V] = __builtin_fmaf(float(X.f[i / 8][1][i % 8]), be, t);
+  }
 }
 
+// Columns of a wave.  32 x 32 tiles run the matrix cores at their full rate
+// (16 x 16 ones at 0.6 of it) and read half as much of L; they need the
+// registers of four waves for an MP = 128 recursion, twice what the gradient's
+// has left, and leave too few waves for the smaller ones.
+constexpr int tile_size(int mt, int kind) { return mt == 8 && kind != BK_VJP ? 32 : 16; }
+constexpr int iterate_threads(int mt, int kind) { return 64 * 16 * mt / tile_size(mt, kind); }
+
 template <int MT, int KIND>
-__global__ __launch_bounds__(32 * MT, KIND == BK_VJP ? 1 : 2) void block_iterate_kernel(
+__global__ __launch_bounds__(iterate_threads(MT, KIND), 2) void block_iterate_kernel(
     BlockTable tab, const float* __restrict__ partials, uint16_t* __restrict__ p_out, uint16_t* __restrict__ t_out,
     float* __restrict__ scratch, BlockSteps steps, int32_t pp) {
-  constexpr int MP = 16 * MT, NR = MT / 2, NW = MT / 2, NT = 64 * NW;
+  constexpr int MP = 16 * MT, TS = tile_size(MT, KIND), NW = MP / TS, NT = 64 * NW;
+  using S = Shape<MP, TS>;
+  using Acc = typename S::Acc;
+  constexpr int NR = S::NR, V = S::V, NV = S::NV, NQ = S::NQ;
   constexpr bool VJP = KIND == BK_VJP;
   constexpr int LDM = MP + 4;
   // the Gram matrix (and Z) in binary32 first, then the left factors
   union Lds {
     float gram[VJP ? 2 : 1][MP][LDM];
-    Left<NR> left[VJP ? 2 : 1];
+    Left<MP> left[VJP ? 2 : 1];
   };
   __shared__ __attribute__((aligned(16))) Lds lds;
   __shared__ float red[8];
   __shared__ int32_t mx[2][8];
 
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int c = lane & 31, h = lane >> 5;
+  const int c = lane % TS, h = lane / TS;
   const int blk = blockIdx.x;
   const BlockStack st = find_stack(&BlockStack::block0, blk);
   const int b = blk - st.block0;
@@ -183,10 +226,25 @@ __global__ __launch_bounds__(32 * MT, KIND == BK_VJP ? 1 : 2) void block_iterate
   const float* src = partials + st.part0 + int64_t(b) * parts * PF;
   auto& L0 = lds.gram[0];
   auto& L1 = lds.gram[VJP ? 1 : 0];
-  for (int e = tid; e < PF / 4; e += NT) {
-    f32x4_t s = *gmem(reinterpret_cast<const f32x4_t*>(src + 4 * e));
-#pragma unroll 4
-    for (int q = 1; q < parts; ++q) s += *gmem(reinterpret_cast<const f32x4_t*>(src + int64_t(q) * PF + 4 * e));
+  constexpr int IT = (PF / 4 + NT - 1) / NT;
+  f32x4_t sum[IT];
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int e = min(it * NT + tid, PF / 4 - 1);
+    sum[it] = *gmem(reinterpret_cast<const f32x4_t*>(src + 4 * e));
+  }
+  for (int q = 1; q < parts; ++q) {
+    src += PF;
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int e = min(it * NT + tid, PF / 4 - 1);
+      sum[it] += *gmem(reinterpret_cast<const f32x4_t*>(src + 4 * e));
+    }
+  }
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int e = it * NT + tid;
+    if (e >= PF / 4) break;
     const int tile = e >> 6, rr = e & 15, gg = (e >> 4) & 3;
     constexpr int TRI = (MT / 2) * (MT + 1);
     if (!VJP || tile < TRI) {
@@ -196,15 +254,15 @@ __global__ __launch_bounds__(32 * MT, KIND == BK_VJP ? 1 : 2) void block_iterate
       for (int v = 0; v < 4; ++v) {
         const int i = 16 * ti + 4 * gg + v, j = 16 * tj + rr;
         if (ti != tj || i <= j) {
-          L0[i][j] = s[v];
-          L0[j][i] = s[v];
+          L0[i][j] = sum[it][v];
+          L0[j][i] = sum[it][v];
         }
       }
     } else {
       const int z = tile - TRI, p = z / (2 * MT), q = z % (2 * MT);
       const int ti = q < MT ? p : MT - 1 - p, tj = q % MT;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) L1[16 * ti + 4 * gg + v][16 * tj + rr] = s[v];
+      for (int v = 0; v < 4; ++v) L1[16 * ti + 4 * gg + v][16 * tj + rr] = sum[it][v];
     }
   }
   __syncthreads();
@@ -218,74 +276,70 @@ __global__ __launch_bounds__(32 * MT, KIND == BK_VJP ? 1 : 2) void block_iterate
   const float inv = steps.first ? 1.f / (norm + NORM_EPS) : 1.f;
 
   // A_j and P (and their tangents D and dP) live as operands; C (E) holds what
-  // the last product gave, 2^ec (2^ee) times the matrix.  A lane's values are
-  // rows 32 kt + tile_row32(v, h) of column 32 w + c.
-  f32x16_t C[NR], E[VJP ? NR : 1];
+  // the last product gave, 2^ec (2^ee) times the matrix.  Value i of a lane is
+  // row row_of(i) of column col.
+  Acc C[NR], E[VJP ? NR : 1];
   int ec = 0, ee = 0;
-  Operand<NR> oA, oP, oD, odP;
+  Operand<NQ> oA, oP, oD, odP;
+  const int col = TS * w + c;
+  auto row_of = [&](int i) { return TS * (i / V) + Tile<TS>::row(i % V, h); };
 #pragma unroll
-  for (int kt = 0; kt < NR; ++kt)
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int i = 32 * kt + tile_row32(v, h), j = 32 * w + c;
-      C[kt][v] = (L0[i][j] * inv) * inv;
-      if constexpr (VJP) E[kt][v] = (0.5f * inv) * (L1[i][j] + L1[j][i]);
-    }
+  for (int i = 0; i < NV; ++i) {
+    C[i / V][i % V] = (L0[row_of(i)][col] * inv) * inv;
+    if constexpr (VJP) E[i / V][i % V] = (0.5f * inv) * (L1[row_of(i)][col] + L1[col][row_of(i)]);
+  }
   float* sc = nullptr;
   if constexpr (VJP) {
     // A_0 and D_0 are needed again for <dX_0, X_0>
     sc = scratch + int64_t(blk) * (2 * MP * MP) + 4 * tid;
 #pragma unroll
-    for (int kt = 0; kt < NR; ++kt)
-#pragma unroll
-      for (int v = 0; v < 16; v += 4) {
-        *gmem(reinterpret_cast<f32x4_t*>(sc + (4 * kt + v / 4) * NT * 4)) =
-            f32x4_t{C[kt][v], C[kt][v + 1], C[kt][v + 2], C[kt][v + 3]};
-        *gmem(reinterpret_cast<f32x4_t*>(sc + (4 * (NR + kt) + v / 4) * NT * 4)) =
-            f32x4_t{E[kt][v], E[kt][v + 1], E[kt][v + 2], E[kt][v + 3]};
-      }
+    for (int i = 0; i < NV; i += 4) {
+      *gmem(reinterpret_cast<f32x4_t*>(sc + i * NT)) = f32x4_t{C[i / V][i % V], C[i / V][i % V + 1], C[i / V][i % V + 2],
+                                                               C[i / V][i % V + 3]};
+      *gmem(reinterpret_cast<f32x4_t*>(sc + (NV + i) * NT)) = f32x4_t{E[i / V][i % V], E[i / V][i % V + 1],
+                                                                      E[i / V][i % V + 2], E[i / V][i % V + 3]};
+    }
   }
 
-  Left<NR>& LA = lds.left[0];
-  Left<NR>& LD = lds.left[VJP ? 1 : 0];
+  Left<MP>& LA = lds.left[0];
+  Left<MP>& LD = lds.left[VJP ? 1 : 0];
   int la = 0, ld = 0;  // powers of two of LA and LD
-  auto split_one = [&](const f32x16_t (&X)[NR], int e, Operand<NR>& o) MUON_INLINE {
-    const int x = scale_for(max_bits<NR>(X));
+  auto split_one = [&](const Acc (&X)[NR], int e, Operand<NQ>& o) MUON_INLINE {
+    const int x = scale_for(max_bits<Acc, NR, V>(X));
     o.ex = e + x;
     const float s = __builtin_amdgcn_ldexpf(1.f, x);
 #pragma unroll
-    for (int kt = 0; kt < NR; ++kt) {
-      split_tile(X[kt], s, o.f[kt]);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int q = 0; q < NQ; ++q) {
+      split_step<Acc, NR, V>(X, q, s, o.f[q][0], o.f[q][1]);
+      if (NV >= 32) __builtin_amdgcn_sched_barrier(0);
     }
   };
   // C (E) as the wave's operand o (od)
-  auto split_into = [&](Operand<NR>& o, Operand<NR>& od) MUON_INLINE {
+  auto split_into = [&](Operand<NQ>& o, Operand<NQ>& od) MUON_INLINE {
     split_one(C, ec, o);
     if constexpr (VJP) split_one(E, ee, od);
   };
   // X to LDS, and as operand o
-  auto put_one = [&](auto keep, const f32x16_t (&X)[NR], Left<NR>& L, int x, Operand<NR>& o) MUON_INLINE {
+  auto put_one = [&](auto keep, const Acc (&X)[NR], Left<MP>& L, int x, Operand<NQ>& o) MUON_INLINE {
     const float s = __builtin_amdgcn_ldexpf(1.f, x);
 #pragma unroll
-    for (int kt = 0; kt < NR; ++kt) {
-      f16x8_t f[2][2];
-      split_tile(X[kt], s, f);
+    for (int q = 0; q < NQ; ++q) {
+      f16x8_t f[2];
+      split_step<Acc, NR, V>(X, q, s, f[0], f[1]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int l = 0; l < 2; ++l) {
-          *reinterpret_cast<f16x8_t*>(&L.v[l][32 * w + c][32 * kt + 16 * i + 8 * h]) = f[i][l];
-          if constexpr (decltype(keep)::value) o.f[kt][i][l] = f[i][l];
-        }
-      __builtin_amdgcn_sched_barrier(0);
+      for (int l = 0; l < 2; ++l) {
+        *reinterpret_cast<f16x8_t*>(&L.v[l][col][S::KS * q + 8 * h]) = f[l];
+        if constexpr (decltype(keep)::value) o.f[q][l] = f[l];
+      }
+      if (NV >= 32) __builtin_amdgcn_sched_barrier(0);
     }
   };
   // C (E) to LDS, with one power of two for all waves; and as operand o (od)
-  auto put = [&](auto keep, Operand<NR>& o, Operand<NR>& od) MUON_INLINE {
+  auto put = [&](auto keep, Operand<NQ>& o, Operand<NQ>& od) MUON_INLINE {
     // the power of two that each wave would take, and the least of them
-    const int xc = ec + scale_for(max_bits<NR>(C));
-    const int xe = VJP ? ee + scale_for(max_bits<VJP ? NR : 1>(E)) : 0;
+    const int xc = ec + scale_for(max_bits<Acc, NR, V>(C));
+    int xe = 0;
+    if constexpr (VJP) xe = ee + scale_for(max_bits<Acc, NR, V>(E));
     if (lane == 0) {
       mx[0][w] = xc;
       if constexpr (VJP) mx[1][w] = xe;
@@ -311,22 +365,20 @@ __global__ __launch_bounds__(32 * MT, KIND == BK_VJP ? 1 : 2) void block_iterate
     __syncthreads();
   };
   // (C, E) <- L (o, od) and its tangent LA od + LD o
-  auto left_times = [&](const Operand<NR>& o, const Operand<NR>& od) MUON_INLINE {
-    zero_sums<NR>(C);
-    multiply<NR>(C, LA, o, c, h);
+  auto left_times = [&](const Operand<NQ>& o, const Operand<NQ>& od) MUON_INLINE {
+    zero_sums<Acc, NR, V>(C);
+    multiply<MP, TS>(C, LA, o, c, h);
     ec = la + o.ex;
     if constexpr (VJP) {
-      zero_sums<NR>(E);
-      multiply<NR>(E, LA, od, c, h);
+      zero_sums<Acc, NR, V>(E);
+      multiply<MP, TS>(E, LA, od, c, h);
       ee = ld + o.ex;
       const int d = ee - (la + od.ex);
       if (d != 0) {
 #pragma unroll
-        for (int jt = 0; jt < NR; ++jt)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) E[jt][v] = __builtin_amdgcn_ldexpf(E[jt][v], d);
+        for (int i = 0; i < NV; ++i) E[i / V][i % V] = __builtin_amdgcn_ldexpf(E[i / V][i % V], d);
       }
-      multiply<NR>(E, LD, o, c, h);
+      multiply<MP, TS>(E, LD, o, c, h);
     }
   };
   // C <- Q = a I + b A + c A A (E <- dQ) from A in C (D in E), left in oA (oD)
@@ -336,17 +388,17 @@ __global__ __launch_bounds__(32 * MT, KIND == BK_VJP ? 1 : 2) void block_iterate
     if (cc != 0.f) {
       left_times(oA, oD);
     } else {
-      zero_sums<NR>(C);
-      if constexpr (VJP) zero_sums<NR>(E);
+      zero_sums<Acc, NR, V>(C);
+      if constexpr (VJP) zero_sums<Acc, NR, V>(E);
     }
-    combine<NR>(C, cc, ec, cb, oA);
-    if constexpr (VJP) combine<NR>(E, cc, ee, cb, oD);
+    combine<MP, TS>(C, cc, ec, cb, oA);
+    if constexpr (VJP) combine<MP, TS>(E, cc, ee, cb, oD);
     ec = ee = 0;
 #pragma unroll
     for (int kt = 0; kt < NR; ++kt)
       if (kt == w) {
 #pragma unroll
-        for (int v = 0; v < 16; ++v) C[kt][v] += tile_row32(v, h) == c ? ca : 0.f;
+        for (int v = 0; v < V; ++v) C[kt][v] += Tile<TS>::row(v, h) == c ? ca : 0.f;
       }
   };
   if (steps.steps > 0) form_q(0);  // P = Q
@@ -367,35 +419,29 @@ __global__ __launch_bounds__(32 * MT, KIND == BK_VJP ? 1 : 2) void block_iterate
   if (steps.steps == 0) {
     ec = ee = 0;
 #pragma unroll
-    for (int kt = 0; kt < NR; ++kt)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        C[kt][v] = kt == w && tile_row32(v, h) == c ? 1.f : 0.f;
-        if constexpr (VJP) E[kt][v] = 0.f;
-      }
+    for (int i = 0; i < NV; ++i) {
+      C[i / V][i % V] = row_of(i) == col ? 1.f : 0.f;
+      if constexpr (VJP) E[i / V][i % V] = 0.f;
+    }
   }
 
 #pragma unroll
-  for (int kt = 0; kt < NR; ++kt)
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      C[kt][v] = __builtin_amdgcn_ldexpf(C[kt][v], -ec);
-      if constexpr (VJP) E[kt][v] = __builtin_amdgcn_ldexpf(E[kt][v], -ee);
-    }
+  for (int i = 0; i < NV; ++i) {
+    C[i / V][i % V] = __builtin_amdgcn_ldexpf(C[i / V][i % V], -ec);
+    if constexpr (VJP) E[i / V][i % V] = __builtin_amdgcn_ldexpf(E[i / V][i % V], -ee);
+  }
   if constexpr (VJP) {
     float shift = 0.f;
     if (steps.first) {
       // <dX_0, X_0> = <P, D_0> + <2 dP, A_0>
       float k = 0.f;
 #pragma unroll
-      for (int kt = 0; kt < NR; ++kt)
+      for (int i = 0; i < NV; i += 4) {
+        const f32x4_t a0 = *gmem(reinterpret_cast<const f32x4_t*>(sc + i * NT));
+        const f32x4_t d0 = *gmem(reinterpret_cast<const f32x4_t*>(sc + (NV + i) * NT));
 #pragma unroll
-        for (int v = 0; v < 16; v += 4) {
-          const f32x4_t a0 = *gmem(reinterpret_cast<const f32x4_t*>(sc + (4 * kt + v / 4) * NT * 4));
-          const f32x4_t d0 = *gmem(reinterpret_cast<const f32x4_t*>(sc + (4 * (NR + kt) + v / 4) * NT * 4));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) k += C[kt][v + i] * d0[i] + 2.f * E[kt][v + i] * a0[i];
-        }
+        for (int j = 0; j < 4; ++j) k += C[i / V][i % V + j] * d0[j] + 2.f * E[i / V][i % V + j] * a0[j];
+      }
 #pragma unroll
       for (int d = 32; d > 0; d >>= 1) k += __shfl_xor(k, d);
       if (lane == 0) red[w] = k;
@@ -407,12 +453,10 @@ __global__ __launch_bounds__(32 * MT, KIND == BK_VJP ? 1 : 2) void block_iterate
       shift = norm > 0.f ? inv * (k / norm) : 0.f;
     }
 #pragma unroll
-    for (int kt = 0; kt < NR; ++kt)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const float tt = (2.f * E[kt][v]) * inv * inv;
-        E[kt][v] = kt == w && tile_row32(v, h) == c ? tt - shift : tt;
-      }
+    for (int i = 0; i < NV; ++i) {
+      const float tt = (2.f * E[i / V][i % V]) * inv * inv;
+      E[i / V][i % V] = row_of(i) == col ? tt - shift : tt;
+    }
   }
 
   // out in bfloat16 parts, by rows, through LDS.  P X is not P^T X here: P is
@@ -420,12 +464,10 @@ __global__ __launch_bounds__(32 * MT, KIND == BK_VJP ? 1 : 2) void block_iterate
   // they act on what the first ones have left of X's large singular values
   __syncthreads();
 #pragma unroll
-  for (int kt = 0; kt < NR; ++kt)
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      L0[32 * kt + tile_row32(v, h)][32 * w + c] = C[kt][v] * inv;
-      if constexpr (VJP) L1[32 * kt + tile_row32(v, h)][32 * w + c] = E[kt][v];
-    }
+  for (int i = 0; i < NV; ++i) {
+    L0[row_of(i)][col] = C[i / V][i % V] * inv;
+    if constexpr (VJP) L1[row_of(i)][col] = E[i / V][i % V];
+  }
   __syncthreads();
 #pragma unroll
   for (int mat = 0; mat < (VJP ? 2 : 1); ++mat) {
@@ -453,7 +495,7 @@ hipError_t launch_block_iterate(int mt, int pp, int kind, const BlockTable& tab,
   if (blocks <= 0) return hipSuccess;
 #define MUON_ITER(MT, KIND)                                                                                      \
   if (mt == MT && kind == KIND) {                                                                                \
-    hipLaunchKernelGGL((block_iterate_kernel<MT, KIND>), dim3(blocks), dim3(32 * MT), 0, stream, tab, partials,  \
+    hipLaunchKernelGGL((block_iterate_kernel<MT, KIND>), dim3(blocks), dim3(iterate_threads(MT, KIND)), 0, stream, tab, partials,  \
                        p_out, t_out, scratch, steps, pp);                                                        \
     return hipGetLastError();                                                                                    \
   }
