@@ -145,10 +145,11 @@ __device__ __forceinline__ void zero_sums(Acc (&acc)[NR]) {
     for (int v = 0; v < V; ++v) acc[jt][v] = 0.f;
 }
 
-// acc += L X for the wave's columns X, both as scaled.
-template <int MP, int TS>
-__device__ __forceinline__ void multiply(typename Tile<TS>::Acc (&acc)[MP / TS], const Left<MP>& L,
-                                         const Operand<Shape<MP, TS>::NQ>& X, int c, int h) {
+// acc[k] += L X[k], k < N, for the wave's columns X, all as scaled: every read
+// of L serves N products.
+template <int MP, int TS, int N>
+__device__ __forceinline__ void multiply(typename Tile<TS>::Acc (*const (&acc)[N])[MP / TS], const Left<MP>& L,
+                                         const Operand<Shape<MP, TS>::NQ>* const (&X)[N], int c, int h) {
   using S = Shape<MP, TS>;
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -157,9 +158,12 @@ __device__ __forceinline__ void multiply(typename Tile<TS>::Acc (&acc)[MP / TS],
     for (int jt = 0; jt < S::NR; ++jt) {
       const f16x8_t hi = *reinterpret_cast<const f16x8_t*>(&L.v[0][TS * jt + c][S::KS * q + 8 * h]);
       const f16x8_t lo = *reinterpret_cast<const f16x8_t*>(&L.v[1][TS * jt + c][S::KS * q + 8 * h]);
-      acc[jt] = Tile<TS>::mfma(lo, X.f[q][0], acc[jt]);
-      acc[jt] = Tile<TS>::mfma(hi, X.f[q][1], acc[jt]);
-      acc[jt] = Tile<TS>::mfma(hi, X.f[q][0], acc[jt]);
+#pragma unroll
+      for (int k = 0; k < N; ++k) (*acc[k])[jt] = Tile<TS>::mfma(lo, X[k]->f[q][0], (*acc[k])[jt]);
+#pragma unroll
+      for (int k = 0; k < N; ++k) (*acc[k])[jt] = Tile<TS>::mfma(hi, X[k]->f[q][1], (*acc[k])[jt]);
+#pragma unroll
+      for (int k = 0; k < N; ++k) (*acc[k])[jt] = Tile<TS>::mfma(hi, X[k]->f[q][0], (*acc[k])[jt]);
     }
   // the reads of L run AHEAD pairs ahead of the products that take them (all
   // of them at once would spill, one at a time waits for LDS)
@@ -167,10 +171,10 @@ __device__ __forceinline__ void multiply(typename Tile<TS>::Acc (&acc)[MP / TS],
   __builtin_amdgcn_sched_group_barrier(0x100, 2 * AHEAD, 0);
 #pragma unroll
   for (int i = 0; i < ITEMS - AHEAD; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 3, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 3 * N, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
   }
-  __builtin_amdgcn_sched_group_barrier(0x008, 3 * AHEAD, 0);
+  __builtin_amdgcn_sched_group_barrier(0x008, 3 * N * AHEAD, 0);
   __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -188,10 +192,11 @@ __device__ __forceinline__ void combine(typename Tile<TS>::Acc (&acc)[MP / TS], 
   }
 }
 
-// Columns of a wave.  32 x 32 tiles run the matrix cores at their full rate
-// (16 x 16 ones at 0.6 of it) and read half as much of L; they need the
-// registers of four waves for an MP = 128 recursion, twice what the gradient's
-// has left, and leave too few waves for the smaller ones.
+// Columns of a wave.  With 32 a 128 x 128 product reads half as much of L,
+// whose reads otherwise take longer than the MFMAs (1152 blocks: 302 us with
+// 16, 238 with 32); the gradient's matrices would not fit the registers (993
+// us against 762), and smaller blocks would have too few waves (64 rows, 12
+// blocks: 27 us against 17).
 constexpr int tile_size(int mt, int kind) { return mt == 8 && kind != BK_VJP ? 32 : 16; }
 constexpr int iterate_threads(int mt, int kind) { return 64 * 16 * mt / tile_size(mt, kind); }
 
@@ -367,18 +372,19 @@ __global__ __launch_bounds__(iterate_threads(MT, KIND), 2) void block_iterate_ke
   // (C, E) <- L (o, od) and its tangent LA od + LD o
   auto left_times = [&](const Operand<NQ>& o, const Operand<NQ>& od) MUON_INLINE {
     zero_sums<Acc, NR, V>(C);
-    multiply<MP, TS>(C, LA, o, c, h);
     ec = la + o.ex;
     if constexpr (VJP) {
       zero_sums<Acc, NR, V>(E);
-      multiply<MP, TS>(E, LA, od, c, h);
+      multiply<MP, TS, 2>({&C, &E}, LA, {&o, &od}, c, h);
       ee = ld + o.ex;
       const int d = ee - (la + od.ex);
       if (d != 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) E[i / V][i % V] = __builtin_amdgcn_ldexpf(E[i / V][i % V], d);
       }
-      multiply<MP, TS>(E, LD, o, c, h);
+      multiply<MP, TS, 1>({&E}, LD, {&o}, c, h);
+    } else {
+      multiply<MP, TS, 1>({&C}, LA, {&o}, c, h);
     }
   };
   // C <- Q = a I + b A + c A A (E <- dQ) from A in C (D in E), left in oA (oD)
