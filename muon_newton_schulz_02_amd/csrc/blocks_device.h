@@ -15,22 +15,27 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
-// The stack whose range of workgroups (by member `key`) holds workgroup b
-// (the same in all lanes).  The table is the kernel's first argument: read
-// through the constant address space it takes scalar loads, and what it holds
-// stays in scalar registers.
-typedef __attribute__((address_space(4))) const BlockStack ConstStack;
-__device__ __forceinline__ BlockStack find_stack(int32_t BlockStack::*key, int b) {
+// The stack whose range of workgroups (or blocks) holds number b, the same in
+// all lanes.  The table is the kernel's first argument.  The lanes compare 64
+// keys at a time, so that a workgroup waits for two loads, not for a search;
+// the descriptor is read through the constant address space and stays in
+// scalar registers.
+template <int KEY>
+__device__ __forceinline__ BlockStack find_stack(int b) {
+  typedef __attribute__((address_space(4))) const BlockStack ConstStack;
   typedef __attribute__((address_space(4))) const BlockTable ConstTable;
+  typedef __attribute__((address_space(4))) const int32_t ConstInt;
   ConstTable* tab = (ConstTable*)__builtin_amdgcn_kernarg_segment_ptr();
+  const int count = tab->count;
+  ConstInt* keys = tab->ext ? (ConstInt*)tab->ext_keys + KEY * count : &tab->keys[KEY][0];
   ConstStack* t = tab->ext ? (ConstStack*)tab->ext : &tab->inl[0];
-  int lo = 0, hi = tab->count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (t[mid].*key <= b) lo = mid; else hi = mid;
-  }
+  const int lane = threadIdx.x & 63;
+  int below = 0;  // keys not above b: they ascend, and the first is 0
+  for (int i = 0; i < count; i += 64)
+    below += __popcll(__ballot(i + lane < count && keys[min(i + lane, count - 1)] <= b));
+  const int at = __builtin_amdgcn_readfirstlane(below) - 1;
   BlockStack s;
-  __builtin_memcpy(&s, (const BlockStack*)(t + lo), sizeof(s));
+  __builtin_memcpy(&s, (const BlockStack*)(t + at), sizeof(s));
   return s;
 }
 

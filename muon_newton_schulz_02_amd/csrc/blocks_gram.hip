@@ -49,7 +49,7 @@ __global__ __launch_bounds__(GT, KIND == BK_VJP ? 2 : 4) void block_gram_kernel(
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, g = lane >> 4;
-  const BlockStack st = find_stack(&BlockStack::goff, blockIdx.x);
+  const BlockStack st = find_stack<KEY_GRAM>(blockIdx.x);
   const int local = int(blockIdx.x) - st.goff;
   const int b = local / st.gsplit, sp = local - b * st.gsplit;
   const int k0 = sp * st.gchunk, k1 = min(st.n, k0 + st.gchunk);
@@ -203,7 +203,8 @@ __global__ __launch_bounds__(GT, KIND == BK_VJP ? 2 : 4) void block_gram_kernel(
   }
 }
 
-__global__ void block_table_kernel(BlockTableBatch in, BlockStack* __restrict__ out) {
+__global__ void block_table_kernel(BlockTableBatch in, BlockStack* __restrict__ out, int32_t* __restrict__ keys,
+                                   int32_t stride) {
   const int i = threadIdx.x;
   if (i >= in.n) return;
   int c = 0;
@@ -221,6 +222,9 @@ __global__ void block_table_kernel(BlockTableBatch in, BlockStack* __restrict__ 
   s.aoff += k * s.blocks * s.asplit;
   s.part0 += int64_t(k) * s.blocks * s.gsplit * in.part;
   out[i] = s;
+  keys[KEY_GRAM * stride + i] = s.goff;
+  keys[KEY_BLOCK * stride + i] = s.block0;
+  keys[KEY_APPLY * stride + i] = s.aoff;
 }
 
 template <int MT>
@@ -247,7 +251,7 @@ hipError_t gram_mt(int pl, int kind, bool xbf, const BlockTable& tab, int32_t wg
 
 }  // namespace
 
-hipError_t launch_block_table(const BlockStack* host, int32_t count, int32_t part, BlockStack* dev,
+hipError_t launch_block_table(const BlockStack* host, int32_t count, int32_t part, BlockStack* dev, int32_t* keys,
                               hipStream_t stream) {
   // what two stacks of a run share
   auto key = [](BlockStack s) {
@@ -280,7 +284,7 @@ hipError_t launch_block_table(const BlockStack* host, int32_t count, int32_t par
       ++b.n;
     }
     for (int32_t c = classes; c < BLOCK_CLASSES; ++c) b.first[c] = b.n;
-    hipLaunchKernelGGL(block_table_kernel, dim3(1), dim3(128), 0, stream, b, dev + i);
+    hipLaunchKernelGGL(block_table_kernel, dim3(1), dim3(128), 0, stream, b, dev + i, keys + i, count);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     i += b.n;

@@ -37,14 +37,20 @@ struct BlockStack {
   int32_t blocks;
 };
 
+// First workgroups (and blocks) of the stacks, by kernel: what a workgroup
+// searches for its stack.
+enum BlockKey : int { KEY_GRAM = 0, KEY_BLOCK = 1, KEY_APPLY = 2, KEY_COUNT = 3 };
+
 // The stacks of a launch: up to BLOCK_INLINE in the kernel's arguments, else
 // in a device table (written by block_table_kernel, so that a call needs no
-// host-to-device copy).
+// host-to-device copy): ext_keys holds KEY_COUNT lists of `count` keys.
 constexpr int BLOCK_INLINE = 16;
 struct BlockTable {
   const BlockStack* ext;
+  const int32_t* ext_keys;
   int32_t count;
   int32_t pad;
+  int32_t keys[KEY_COUNT][BLOCK_INLINE];
   BlockStack inl[BLOCK_INLINE];
 };
 static_assert(sizeof(BlockTable) <= 3072, "kernel arguments stay small");
@@ -101,9 +107,9 @@ static_assert(sizeof(BlockTableBatch) <= 4096, "kernel arguments stay below 4 Ki
 
 // The launchers.  pl: bfloat16 parts of an element of x (1, 2, 3); pp: parts
 // of an element of P (2, 3); xbf: x is bfloat16 in every stack.
-// Writes a table of `count` stacks to device memory.  part: floats of one
-// workgroup's Gram partial.
-hipError_t launch_block_table(const BlockStack* host, int32_t count, int32_t part, BlockStack* dev,
+// Writes a table of `count` stacks and its keys to device memory.  part:
+// floats of one workgroup's Gram partial.
+hipError_t launch_block_table(const BlockStack* host, int32_t count, int32_t part, BlockStack* dev, int32_t* keys,
                               hipStream_t stream);
 hipError_t launch_block_gram(int mt, int pl, int kind, bool xbf, const BlockTable& tab, int32_t wgs, float* partials,
                              const BlockMom& mom, hipStream_t stream);

@@ -326,6 +326,9 @@ struct Group {
 
 int64_t ld_of_stage(const muon_block_desc& d) { return round_up(d.cols, 4); }
 
+// A device table and its keys.
+size_t table_bytes(size_t n) { return align256(sizeof(BlockStack) * n) + align256(sizeof(int32_t) * KEY_COUNT * n); }
+
 // Splits the call into groups and lays out the workspace (the groups run one
 // after another and share it).  Returns its size.
 size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
@@ -403,7 +406,7 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
     const int pp = g.f32 ? 3 : 2;
     size_t o = 0;
     g.o_tab = o;
-    if (g.base.size() > size_t(BLOCK_INLINE)) o += align256(sizeof(BlockStack) * g.base.size() * size_t(g.tables));
+    if (g.base.size() > size_t(BLOCK_INLINE)) o += table_bytes(g.base.size()) * size_t(g.tables);
     g.o_part = o;
     o += align256(size_t(part) * 4);
     g.o_p = o;
@@ -511,11 +514,19 @@ hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
     tab.ext = nullptr;
     if (v.size() <= size_t(BLOCK_INLINE)) {
       memcpy(tab.inl, v.data(), sizeof(BlockStack) * v.size());
+      for (size_t k = 0; k < v.size(); ++k) {
+        tab.keys[KEY_GRAM][k] = v[k].goff;
+        tab.keys[KEY_BLOCK][k] = v[k].block0;
+        tab.keys[KEY_APPLY][k] = v[k].aoff;
+      }
       return hipSuccess;
     }
-    BlockStack* dev = reinterpret_cast<BlockStack*>(ws + g.o_tab) + size_t(table++) * v.size();
+    char* at = ws + g.o_tab + size_t(table++) * table_bytes(v.size());
+    BlockStack* dev = reinterpret_cast<BlockStack*>(at);
+    int32_t* keys = reinterpret_cast<int32_t*>(at + align256(sizeof(BlockStack) * v.size()));
     tab.ext = dev;
-    return launch_block_table(v.data(), int32_t(v.size()), part, dev, c.stream);
+    tab.ext_keys = keys;
+    return launch_block_table(v.data(), int32_t(v.size()), part, dev, keys, c.stream);
   };
   auto steps_of = [&](const Stage& st, bool first) {
     BlockSteps s;
