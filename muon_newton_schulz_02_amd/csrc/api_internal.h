@@ -20,6 +20,8 @@ std::mutex& api_mutex();
 hipError_t api_device_alloc(void** p, size_t bytes);
 // Runs `launch` as kernel class `kc` of muon_timing_read (lock held).
 hipError_t api_timed(int kc, hipStream_t stream, const std::function<hipError_t()>& launch);
+// Whether launches are being timed (lock held).
+bool api_timing();
 // Called by muon_release_workspace with the lock held; null if unused.
 extern void (*api_release_hook)();
 

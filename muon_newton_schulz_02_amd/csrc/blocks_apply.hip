@@ -41,8 +41,9 @@ __global__ __launch_bounds__(AT, KIND == BK_VJP || PP == 3 ? 2 : 4) void block_a
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, g = lane >> 4;
   const int wr = wave % MT, wc = wave / MT;  // the wave's row tile and group of 64 columns
-  const BlockStack st = find_stack<KEY_APPLY>(blockIdx.x);
-  const int local = int(blockIdx.x) - st.aoff;
+  const int wg = block_number();
+  const BlockStack st = find_stack<KEY_APPLY>(wg);
+  const int local = wg - st.aoff;
   const int b = local / st.asplit, sp = local - b * st.asplit;
   const int c0 = sp * st.achunk, c1 = min(st.n, c0 + st.achunk);
   const bool tr = st.flags & BF_TR;

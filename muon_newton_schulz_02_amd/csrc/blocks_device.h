@@ -15,6 +15,12 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
+// The workgroup's number among those of all launches over the table.
+__device__ __forceinline__ int block_number() {
+  typedef __attribute__((address_space(4))) const BlockTable ConstTable;
+  return int(blockIdx.x) + ((ConstTable*)__builtin_amdgcn_kernarg_segment_ptr())->first;
+}
+
 // The stack whose range of workgroups (or blocks) holds number b, the same in
 // all lanes.  The table is the kernel's first argument.  The lanes compare 64
 // keys at a time, so that a workgroup waits for two loads, not for a search;

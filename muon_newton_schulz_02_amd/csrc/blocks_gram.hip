@@ -49,8 +49,9 @@ __global__ __launch_bounds__(GT, KIND == BK_VJP ? 2 : 4) void block_gram_kernel(
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, g = lane >> 4;
-  const BlockStack st = find_stack<KEY_GRAM>(blockIdx.x);
-  const int local = int(blockIdx.x) - st.goff;
+  const int wg = block_number();
+  const BlockStack st = find_stack<KEY_GRAM>(wg);
+  const int local = wg - st.goff;
   const int b = local / st.gsplit, sp = local - b * st.gsplit;
   const int k0 = sp * st.gchunk, k1 = min(st.n, k0 + st.gchunk);
   const bool tr = st.flags & BF_TR;

@@ -49,7 +49,7 @@ struct BlockTable {
   const BlockStack* ext;
   const int32_t* ext_keys;
   int32_t count;
-  int32_t pad;
+  int32_t first;      // number of the launch's first workgroup (or block): a launch may take a part of them
   int32_t keys[KEY_COUNT][BLOCK_INLINE];
   BlockStack inl[BLOCK_INLINE];
 };

@@ -221,7 +221,7 @@ __global__ __launch_bounds__(iterate_threads(MT, KIND), 2) void block_iterate_ke
 
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int c = lane % TS, h = lane / TS;
-  const int blk = blockIdx.x;
+  const int blk = block_number();
   const BlockStack st = find_stack<KEY_BLOCK>(blk);
   const int b = blk - st.block0;
 

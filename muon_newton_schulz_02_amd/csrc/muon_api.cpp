@@ -1781,6 +1781,7 @@ hipError_t api_device_alloc(void** p, size_t bytes) { return device_alloc(p, byt
 hipError_t api_timed(int kc, hipStream_t stream, const std::function<hipError_t()>& launch) {
   return timed(kc, stream, launch);
 }
+bool api_timing() { return g_timing; }
 void (*api_release_hook)() = nullptr;
 
 }  // namespace muon

@@ -431,22 +431,18 @@ double rule_scale(int rule, int64_t rows, int64_t cols) {
   return 1.0;
 }
 
-// Enqueues one group: every launch goes through `run(kernel class, launch)`.
-template <class Run>
-hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
+// One stage's three launches.
+struct Phase {
+  BlockTable tab;
+  int kind = BK_X, pl = 1;
+  bool xbf = false;
+  BlockSteps steps;
+};
+
+// The stages of a group in order, with their tables (written on the call's
+// stream where they are in device memory).
+hipError_t group_phases(const Call& c, const Group& g, char* ws, std::vector<Phase>& out) {
   const bool vjp = c.op == MUON_BLOCKS_VJP, step = c.op == MUON_BLOCKS_STEP;
-  const int pp = g.f32 ? 3 : 2;
-  float* parts = reinterpret_cast<float*>(ws + g.o_part);
-  uint16_t* P = reinterpret_cast<uint16_t*>(ws + g.o_p);
-  uint16_t* T = vjp ? reinterpret_cast<uint16_t*>(ws + g.o_t) : nullptr;
-  float* scr = vjp ? reinterpret_cast<float*>(ws + g.o_scr) : nullptr;
-  BlockMom mom = {0.f, 1.f, 0, 0};
-  if (step) {
-    mom.beta = c.hp->beta;
-    mom.nesterov = c.hp->nesterov;
-    mom.ema = c.hp->options && c.hp->options->momentum_kind == MUON_MOMENTUM_EMA;
-    mom.g1 = mom.ema ? 1.f - c.hp->beta : 1.f;
-  }
   const int32_t nst = int32_t(g.stages.size());
 
   // views of a member: the caller's tensors, or stage buffer `buf`
@@ -507,11 +503,9 @@ hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
 
   int32_t table = 0;
   const int32_t part = block_part_floats(g.mt, vjp ? BK_VJP : BK_X);
-  BlockTable tab;
-  memset(&tab, 0, sizeof(tab));
-  auto set_table = [&](const std::vector<BlockStack>& v) -> hipError_t {
+  auto set_table = [&](BlockTable& tab, const std::vector<BlockStack>& v) -> hipError_t {
+    memset(&tab, 0, sizeof(tab));
     tab.count = int32_t(v.size());
-    tab.ext = nullptr;
     if (v.size() <= size_t(BLOCK_INLINE)) {
       memcpy(tab.inl, v.data(), sizeof(BlockStack) * v.size());
       for (size_t k = 0; k < v.size(); ++k) {
@@ -544,8 +538,10 @@ hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
 
   // forward stages; for the gradient all but the last, into a buffer each
   const int32_t fwd = vjp ? nst - 1 : nst;
-  hipError_t e = hipSuccess;
-  for (int32_t i = 0; i < fwd && e == hipSuccess; ++i) {
+  out.resize(size_t(fwd + (vjp ? nst : 0)));
+  size_t at = 0;
+  for (int32_t i = 0; i < fwd; ++i) {
+    Phase& p = out[at++];
     std::vector<BlockStack> v = g.base;
     const bool user_u = step && i == 0;
     const int src = i == 0 ? -1 : vjp ? i - 1 : 0;
@@ -555,48 +551,83 @@ hipError_t enqueue_group(const Call& c, const Group& g, char* ws, Run&& run) {
       if (user_u) set_y(v[k], k, -1);
       set_out(v[k], k, dst);
     }
-    if ((e = set_table(v)) != hipSuccess) break;
-    const int kind = user_u ? BK_STEP : BK_X;
-    const int pl = g.f32 ? 3 : (user_u || i > 0 || !g.xbf) ? 2 : 1;
-    e = run(user_u ? MUON_KC_MOMENTUM : MUON_KC_GRAM, [&] {
-      return launch_block_gram(g.mt, pl, kind, i == 0 && g.xbf, tab, g.gram_wgs, parts, mom, c.stream);
-    });
-    if (e != hipSuccess) break;
-    const BlockSteps s = steps_of(g.stages[size_t(i)], i == 0);
-    e = run(MUON_KC_POLY, [&] {
-      return launch_block_iterate(g.mt, pp, BK_X, tab, int32_t(g.blocks), parts, P, nullptr, nullptr, s, c.stream);
-    });
-    if (e != hipSuccess) break;
-    e = run(MUON_KC_COMBINE, [&] {
-      return launch_block_apply(g.mt, pl, pp, kind, i == 0 && g.xbf, tab, g.apply_wgs, P, nullptr, mom, c.stream);
-    });
+    p.kind = user_u ? BK_STEP : BK_X;
+    p.pl = g.f32 ? 3 : (user_u || i > 0 || !g.xbf) ? 2 : 1;
+    p.xbf = i == 0 && g.xbf;
+    p.steps = steps_of(g.stages[size_t(i)], i == 0);
+    const hipError_t e = set_table(p.tab, v);
+    if (e != hipSuccess) return e;
   }
-  if (!vjp) return e;
+  if (!vjp) return hipSuccess;
   // backward stages: the cotangent of stage i's input, in place in the last buffer
-  for (int32_t i = nst - 1; i >= 0 && e == hipSuccess; --i) {
+  for (int32_t i = nst - 1; i >= 0; --i) {
+    Phase& p = out[at++];
     std::vector<BlockStack> v = g.base;
     for (size_t k = 0; k < v.size(); ++k) {
       set_x(v[k], k, i - 1);
       set_y(v[k], k, i == nst - 1 ? -1 : nst - 1);
       set_out(v[k], k, i == 0 ? -1 : nst - 1);
     }
-    if ((e = set_table(v)) != hipSuccess) break;
-    const bool bf = (i == 0 && g.xbf) && (i == nst - 1 && g.ybf);
-    const int pl = g.f32 ? 3 : bf ? 1 : 2;
-    e = run(MUON_KC_GRAM, [&] {
-      return launch_block_gram(g.mt, pl, BK_VJP, i == 0 && g.xbf, tab, g.gram_wgs, parts, mom, c.stream);
-    });
-    if (e != hipSuccess) break;
-    const BlockSteps s = steps_of(g.stages[size_t(i)], i == 0);
-    e = run(MUON_KC_POLY, [&] {
-      return launch_block_iterate(g.mt, pp, BK_VJP, tab, int32_t(g.blocks), parts, P, T, scr, s, c.stream);
-    });
-    if (e != hipSuccess) break;
-    e = run(MUON_KC_COMBINE, [&] {
-      return launch_block_apply(g.mt, pl, pp, BK_VJP, i == 0 && g.xbf, tab, g.apply_wgs, P, T, mom, c.stream);
-    });
+    p.kind = BK_VJP;
+    p.xbf = i == 0 && g.xbf;
+    p.pl = g.f32 ? 3 : (p.xbf && i == nst - 1 && g.ybf) ? 1 : 2;
+    p.steps = steps_of(g.stages[size_t(i)], i == 0);
+    const hipError_t e = set_table(p.tab, v);
+    if (e != hipSuccess) return e;
   }
-  return e;
+  return hipSuccess;
+}
+
+// First gram and apply workgroup of block b (the group's count for b = all).
+void workgroups_at(const Group& g, int64_t b, int32_t& gram, int32_t& apply) {
+  gram = g.gram_wgs;
+  apply = g.apply_wgs;
+  for (size_t k = g.base.size(); k-- > 0;) {
+    const BlockStack& s = g.base[k];
+    if (b < s.block0 || b >= s.block0 + s.blocks) continue;
+    gram = s.goff + int32_t(b - s.block0) * s.gsplit;
+    apply = s.aoff + int32_t(b - s.block0) * s.asplit;
+  }
+}
+
+// Enqueues phase `p` for blocks [b0, b1) on `stream`; every launch goes
+// through run(kernel class, launch).  `after`, where not null, is recorded
+// behind the gram pass.
+template <class Run>
+hipError_t enqueue_phase(const Call& c, const Group& g, Phase& p, char* ws, int64_t b0, int64_t b1, hipStream_t stream,
+                         hipEvent_t after, Run&& run) {
+  const bool vjp = c.op == MUON_BLOCKS_VJP;
+  const int pp = g.f32 ? 3 : 2;
+  float* parts = reinterpret_cast<float*>(ws + g.o_part);
+  uint16_t* P = reinterpret_cast<uint16_t*>(ws + g.o_p);
+  uint16_t* T = vjp ? reinterpret_cast<uint16_t*>(ws + g.o_t) : nullptr;
+  float* scr = vjp ? reinterpret_cast<float*>(ws + g.o_scr) : nullptr;
+  BlockMom mom = {0.f, 1.f, 0, 0};
+  if (p.kind == BK_STEP) {
+    mom.beta = c.hp->beta;
+    mom.nesterov = c.hp->nesterov;
+    mom.ema = c.hp->options && c.hp->options->momentum_kind == MUON_MOMENTUM_EMA;
+    mom.g1 = mom.ema ? 1.f - c.hp->beta : 1.f;
+  }
+  int32_t g0, g1, a0, a1;
+  workgroups_at(g, b0, g0, a0);
+  workgroups_at(g, b1, g1, a1);
+  p.tab.first = g0;
+  hipError_t e = run(p.kind == BK_STEP ? MUON_KC_MOMENTUM : MUON_KC_GRAM, [&] {
+    return launch_block_gram(g.mt, p.pl, p.kind, p.xbf, p.tab, g1 - g0, parts, mom, stream);
+  });
+  if (e == hipSuccess && after) e = hipEventRecord(after, stream);
+  if (e != hipSuccess) return e;
+  p.tab.first = int32_t(b0);
+  e = run(MUON_KC_POLY, [&] {
+    return launch_block_iterate(g.mt, pp, p.kind == BK_VJP ? BK_VJP : BK_X, p.tab, int32_t(b1 - b0), parts, P, T, scr,
+                                p.steps, stream);
+  });
+  if (e != hipSuccess) return e;
+  p.tab.first = a0;
+  return run(MUON_KC_COMBINE, [&] {
+    return launch_block_apply(g.mt, p.pl, pp, p.kind, p.xbf, p.tab, a1 - a0, P, T, mom, stream);
+  });
 }
 
 // -------------------------------------------------------------- workspaces
@@ -607,6 +638,9 @@ struct BlockDevice {
   size_t ws_bytes = 0;
   hipEvent_t last = nullptr;   // after the last call that used ws
   bool recorded = false;
+  // the second stream of a large call and its events (fork, join)
+  hipStream_t side = nullptr;
+  hipEvent_t fork = nullptr, join = nullptr;
 };
 std::map<int, BlockDevice> g_blocks;  // under api_mutex()
 
@@ -616,6 +650,9 @@ void release_blocks() {
     (void)hipDeviceSynchronize();
     if (kv.second.ws) (void)hipFree(kv.second.ws);
     if (kv.second.last) (void)hipEventDestroy(kv.second.last);
+    if (kv.second.side) (void)hipStreamDestroy(kv.second.side);
+    if (kv.second.fork) (void)hipEventDestroy(kv.second.fork);
+    if (kv.second.join) (void)hipEventDestroy(kv.second.join);
   }
   g_blocks.clear();
 }
@@ -640,6 +677,48 @@ muon_status current_device(BlockDevice** out) {
   }
   *out = &bd;
   return MUON_OK;
+}
+
+// The side stream and its events; without them a call runs on its own stream.
+bool side_stream(BlockDevice& bd) {
+  if (!bd.side && hipStreamCreateWithFlags(&bd.side, hipStreamNonBlocking) != hipSuccess) bd.side = nullptr;
+  if (!bd.fork && hipEventCreateWithFlags(&bd.fork, hipEventDisableTiming) != hipSuccess) bd.fork = nullptr;
+  if (!bd.join && hipEventCreateWithFlags(&bd.join, hipEventDisableTiming) != hipSuccess) bd.join = nullptr;
+  if (bd.side && bd.fork && bd.join) return true;
+  (void)hipGetLastError();
+  return false;
+}
+
+// Blocks of the recursion that fill the GPU: below twice as many a call's
+// parts would run one after another anyway.
+int64_t fill_blocks(const Group& g, int op, int cus) { return int64_t(cus) * (g.mt == 8 ? 1 : 4); }
+
+// Enqueues one group.  The recursion keeps the matrix cores busy and the other
+// two passes the memory, so a large group is cut in two: the second part's
+// passes run on a side stream, behind the first part's gram pass, and each
+// part's recursion runs beside a pass over memory of the other part.
+hipError_t enqueue_group(const Call& c, const Group& g, char* ws, BlockDevice& bd, bool capturing) {
+  std::vector<Phase> phases;
+  hipError_t e = group_phases(c, g, ws, phases);
+  const int64_t fill = fill_blocks(g, c.op, bd.cus);
+  const bool split = !capturing && !api_timing() && g.blocks > fill && side_stream(bd);
+  const int64_t cut = !split ? g.blocks : (g.blocks + 1) / 2;
+  auto run = [&](int kc, auto&& launch) -> hipError_t {
+    return capturing ? launch() : api_timed(kc, c.stream, launch);
+  };
+  for (size_t i = 0; i < phases.size() && e == hipSuccess; ++i) {
+    e = enqueue_phase(c, g, phases[i], ws, 0, cut, c.stream, split && i == 0 ? bd.fork : nullptr, run);
+    if (!split || e != hipSuccess) continue;
+    if (i == 0) e = hipStreamWaitEvent(bd.side, bd.fork, 0);
+    if (e == hipSuccess) e = enqueue_phase(c, g, phases[i], ws, cut, g.blocks, bd.side, nullptr, run);
+  }
+  if (split) {
+    // also after a failed launch: what was enqueued belongs to this call
+    const hipError_t j = hipEventRecord(bd.join, bd.side);
+    const hipError_t w = j == hipSuccess ? hipStreamWaitEvent(c.stream, bd.join, 0) : j;
+    if (e == hipSuccess) e = w;
+  }
+  return e;
 }
 
 muon_status run_call(const Call& c) {
@@ -696,9 +775,7 @@ muon_status run_call(const Call& c) {
 
   hipError_t e = hipSuccess;
   for (const Group& g : groups) {
-    e = enqueue_group(c, g, ws, [&](int kc, auto&& launch) -> hipError_t {
-      return capturing ? launch() : api_timed(kc, c.stream, launch);
-    });
+    e = enqueue_group(c, g, ws, *bd, capturing);
     if (e != hipSuccess) break;
   }
   if (!c.ws && hipEventRecord(bd->last, c.stream) == hipSuccess) bd->recorded = true;
