@@ -29,14 +29,21 @@ constexpr int AT = BLOCK_THREADS;
 __device__ __forceinline__ int tile_row(int j) { return (j & ~63) + (j & 3) * 16 + ((j & 63) >> 2); }
 
 template <int MT, int PL, int PP, int KIND, int XT>
-__global__ __launch_bounds__(AT, KIND == BK_VJP || PP == 3 ? 2 : 4) void block_apply_kernel(BlockTable tab, const uint16_t* __restrict__ pf,
+__global__ __launch_bounds__(AT, KIND == BK_VJP && PL > 1 ? 2 : 4) void block_apply_kernel(BlockTable tab, const uint16_t* __restrict__ pf,
                                                             const uint16_t* __restrict__ tf, BlockMom mom) {
   constexpr int MP = 16 * MT, KC = block_kc(MT), LDX = MP + 8;
   constexpr int NM = KIND == BK_VJP ? 2 : 1;
   constexpr int LDO = KC + 4, LDT = MP + 4;  // results by rows of x, or by columns
   constexpr int OB = (MP * LDO > KC * LDT ? MP * LDO : KC * LDT);
-  __shared__ __attribute__((aligned(16))) uint16_t xs[NM][PL][KC][LDX];
-  __shared__ __attribute__((aligned(16))) float os[OB];
+  // the results' tile takes the place of x's (two more barriers a tile) where
+  // both would leave no room for a second workgroup: 12 layers of binary32
+  // heads of 64 x 768, 70 us apart, APPLY_SHARED us together
+  constexpr int XB = NM * PL * KC * LDX * 2;
+  constexpr bool SHARE = XB + OB * 4 > 80 * 1024 && XB >= OB * 4;
+  __shared__ __attribute__((aligned(16))) unsigned char lds_raw[SHARE ? XB : XB + OB * 4];
+  typedef uint16_t XTile[PL][KC][LDX];
+  XTile* const xs = reinterpret_cast<XTile*>(lds_raw);
+  float* const os = reinterpret_cast<float*>(SHARE ? lds_raw : lds_raw + XB);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, g = lane >> 4;
@@ -166,6 +173,7 @@ __global__ __launch_bounds__(AT, KIND == BK_VJP || PP == 3 ? 2 : 4) void block_a
           acc[t] = mfma_parts<PP, PL>(a, x, acc[t]);
         }
       }
+    if (SHARE) __syncthreads();
     // row 16 wr + 4 g + v, columns 64 wc + 4 r + {0 .. 3}
     if (!tr) {
 #pragma unroll
@@ -203,6 +211,7 @@ __global__ __launch_bounds__(AT, KIND == BK_VJP || PP == 3 ? 2 : 4) void block_a
       store8(op, oo + q * od, obf, valid, o);
     }
     op += ot;
+    if (SHARE && kb + KC < c1) __syncthreads();
   }
 }
 

@@ -689,19 +689,28 @@ bool side_stream(BlockDevice& bd) {
   return false;
 }
 
-// Blocks of the recursion that fill the GPU: below twice as many a call's
-// parts would run one after another anyway.
-int64_t fill_blocks(const Group& g, int op, int cus) { return int64_t(cus) * (g.mt == 8 ? 1 : 4); }
+// Whether a group is worth two streams.  Measured, two streams against one:
+// several stages (binary32 results; 64 x 768 and 128 x 1536 blocks): 128 blocks
+// 1.02, 300 1.07 to 1.11, 576 1.06 to 1.17; the gradient of 128-row blocks, of
+// which a compute unit holds one: 200 blocks 1.05, 260 1.25, 600 1.12, 1000
+// 0.99 (64 rows: 0.95 to 0.98, not split); one forward stage of them, two to a
+// compute unit, gains where a second round of the recursion would be nearly
+// empty: 576 blocks 1.08, 600 1.09, but 512 0.89, 700 0.90 to 1.02, 1152 0.97.
+bool two_streams(const Group& g, int op, int64_t cus) {
+  if (g.stages.size() > 1) return g.blocks >= cus / 2;
+  if (g.mt != 8) return false;
+  if (op == MUON_BLOCKS_VJP) return g.blocks >= cus * 3 / 4;
+  return g.blocks > 2 * cus && g.blocks <= cus * 5 / 2;
+}
 
 // Enqueues one group.  The recursion keeps the matrix cores busy and the other
-// two passes the memory, so a large group is cut in two: the second part's
+// two passes the memory, so a group may be cut in two: the second part's
 // passes run on a side stream, behind the first part's gram pass, and each
 // part's recursion runs beside a pass over memory of the other part.
 hipError_t enqueue_group(const Call& c, const Group& g, char* ws, BlockDevice& bd, bool capturing) {
   std::vector<Phase> phases;
   hipError_t e = group_phases(c, g, ws, phases);
-  const int64_t fill = fill_blocks(g, c.op, bd.cus);
-  const bool split = !capturing && !api_timing() && g.blocks > fill && side_stream(bd);
+  const bool split = !capturing && !api_timing() && two_streams(g, c.op, bd.cus) && side_stream(bd);
   const int64_t cut = !split ? g.blocks : (g.blocks + 1) / 2;
   auto run = [&](int kc, auto&& launch) -> hipError_t {
     return capturing ? launch() : api_timed(kc, c.stream, launch);
