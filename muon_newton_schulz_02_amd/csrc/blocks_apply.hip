@@ -28,18 +28,28 @@ constexpr int AT = BLOCK_THREADS;
 // are four consecutive columns.
 __device__ __forceinline__ int tile_row(int j) { return (j & ~63) + (j & 3) * 16 + ((j & 63) >> 2); }
 
+// Whether a compute unit holds two workgroups (four waves a SIMD, 128
+// registers each): not where those do not reach, which are the gradient on
+// more parts or rows (146 to 256 registers) and the binary32 step at 128 rows
+// (198; it moves 4.9 TB/s with one workgroup or two).
+constexpr bool two_resident(int mt, int pl, int kind) {
+  return kind == BK_VJP ? pl == 1 || (pl == 2 && mt < 8) : kind == BK_X || pl < 3 || mt < 8;
+}
+
 template <int MT, int PL, int PP, int KIND, int XT>
-__global__ __launch_bounds__(AT, KIND == BK_VJP && PL > 1 ? 2 : 4) void block_apply_kernel(BlockTable tab, const uint16_t* __restrict__ pf,
-                                                            const uint16_t* __restrict__ tf, BlockMom mom) {
+__global__ __launch_bounds__(AT, two_resident(MT, PL, KIND) ? 4 : 2) void block_apply_kernel(
+    BlockTable tab, const uint16_t* __restrict__ pf, const uint16_t* __restrict__ tf, BlockMom mom) {
   constexpr int MP = 16 * MT, KC = block_kc(MT), LDX = MP + 8;
   constexpr int NM = KIND == BK_VJP ? 2 : 1;
   constexpr int LDO = KC + 4, LDT = MP + 4;  // results by rows of x, or by columns
   constexpr int OB = (MP * LDO > KC * LDT ? MP * LDO : KC * LDT);
   // the results' tile takes the place of x's (two more barriers a tile) where
-  // both would leave no room for a second workgroup: 12 layers of binary32
-  // heads of 64 x 768, 70 us apart, APPLY_SHARED us together
+  // both would leave no room for the second workgroup.  Binary32, 576 blocks
+  // of 64 x 768: 63 us apart, 53 us together, with the write-back 92 and 79;
+  // 600 of 128 x 1536: 309 and 251; bfloat16 gradients of binary32 blocks,
+  // 576 of 64 x 768: 86 and 63, 1000 of 32 x 1536: 126 and 101
   constexpr int XB = NM * PL * KC * LDX * 2;
-  constexpr bool SHARE = XB + OB * 4 > 80 * 1024 && XB >= OB * 4;
+  constexpr bool SHARE = two_resident(MT, PL, KIND) && XB + OB * 4 > 80 * 1024 && XB >= OB * 4;
   __shared__ __attribute__((aligned(16))) unsigned char lds_raw[SHARE ? XB : XB + OB * 4];
   typedef uint16_t XTile[PL][KC][LDX];
   XTile* const xs = reinterpret_cast<XTile*>(lds_raw);

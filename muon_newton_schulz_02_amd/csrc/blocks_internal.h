@@ -53,7 +53,7 @@ struct BlockTable {
   int32_t keys[KEY_COUNT][BLOCK_INLINE];
   BlockStack inl[BLOCK_INLINE];
 };
-static_assert(sizeof(BlockTable) <= 3072, "kernel arguments stay small");
+static_assert(sizeof(BlockTable) + 512 <= 4096, "kernel arguments stay below 4 KiB");
 
 // Momentum of the step: M <- beta M + g1 G, U = nesterov ? g1 G + beta M : M
 // with g1 = 1 (heavy ball) or fl32(1 - beta) (EMA).
