@@ -159,9 +159,8 @@ __device__ __forceinline__ void split8(const float v[8], bf16x8_t out[PL]) {
 // acc += sum of the products of a's and b's parts that are not below the
 // last part's place (hi*hi, hi*lo, lo*hi; with three parts also mid*mid,
 // hi*lo2, lo2*hi), smallest first.
-template <int PA, int PB>
+template <int PA, int PB, int S = (PA > PB ? PA : PB) - 1>
 __device__ __forceinline__ f32x4_t mfma_parts(const bf16x8_t a[PA], const bf16x8_t b[PB], f32x4_t acc) {
-  constexpr int S = (PA > PB ? PA : PB) - 1;
 #pragma unroll
   for (int s = S; s >= 0; --s)
 #pragma unroll

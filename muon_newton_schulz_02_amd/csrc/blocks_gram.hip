@@ -37,6 +37,11 @@ __global__ __launch_bounds__(GT, KIND == BK_VJP ? 2 : 4) void block_gram_kernel(
                                                                                BlockMom mom) {
   constexpr int MP = 16 * MT, KC = block_kc(MT), LDK = KC + 8;
   constexpr int NM = KIND == BK_VJP ? 2 : 1;       // matrices staged: x (and y)
+  // two parts: lo*lo too, so that G is the Gram matrix of the values as split.
+  // Its sum of squares, 2^-19 of the trace, would else be missing on the
+  // diagonal, where small singular values show it (one and three at 1/200 of
+  // it: error 1.8e-2 without, 2.1e-3 with; no change in time)
+  constexpr int GS = PL == 2 ? 2 : PL - 1;
   constexpr int KW = 16 / MT;                      // waves of a pair of tile rows = k-steps of a tile
   // two buffers where two workgroups still fit a compute unit
   constexpr int TB = gram_tile_bytes<MT, PL, KIND>(), NBUF = 2 * TB <= 80 * 1024 ? 2 : 1;
@@ -154,8 +159,8 @@ __global__ __launch_bounds__(GT, KIND == BK_VJP ? 2 : 4) void block_gram_kernel(
       bf16x8_t bb[PL];
 #pragma unroll
       for (int l = 0; l < PL; ++l) bb[l] = *reinterpret_cast<const bf16x8_t*>(&tile[0][l][16 * tj + r][ko]);
-      if (first) acc[q] = mfma_parts<PL, PL>(a0, bb, acc[q]);
-      else acc[q] = mfma_parts<PL, PL>(a1, bb, acc[q]);
+      if (first) acc[q] = mfma_parts<PL, PL, GS>(a0, bb, acc[q]);
+      else acc[q] = mfma_parts<PL, PL, GS>(a1, bb, acc[q]);
     }
     if (KIND == BK_VJP) {
 #pragma unroll
@@ -168,8 +173,8 @@ __global__ __launch_bounds__(GT, KIND == BK_VJP ? 2 : 4) void block_gram_kernel(
         bf16x8_t bb[PL];
 #pragma unroll
         for (int l = 0; l < PL; ++l) bb[l] = *reinterpret_cast<const bf16x8_t*>(&tile[0][l][16 * tj + r][ko]);
-        zacc[tj] = mfma_parts<PL, PL>(a0, bb, zacc[tj]);
-        zacc[MT + tj] = mfma_parts<PL, PL>(a1, bb, zacc[MT + tj]);
+        zacc[tj] = mfma_parts<PL, PL, GS>(a0, bb, zacc[tj]);
+        zacc[MT + tj] = mfma_parts<PL, PL, GS>(a1, bb, zacc[MT + tj]);
       }
     }
     if (NBUF == 2) buf ^= 1;

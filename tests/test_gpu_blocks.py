@@ -202,6 +202,42 @@ def test_decaying_spectra(dt, power):
                   _tol(dt, m, MUON, 5, grad=True), "gradient")
 
 
+@pytest.mark.parametrize("xdt,odt", [(BF, BF), (F, BF), (F, F)])
+@pytest.mark.parametrize("m,n", [(4, 64), (16, 1024), (64, 768), (128, 300)])
+@pytest.mark.parametrize("ratio", [50, 200, 1000])
+def test_one_large_singular_value(m, n, ratio, xdt, odt):
+    """One singular value and m - 1 at 1/ratio of it: the Gram matrix holds the others' squares least exactly.
+
+    With O = p(A_0) X_0, an error E of A_0 gives p'(l) s E in the m - 1 small directions (s the small singular value
+    of X_0, l = s^2).  E is a few roundings of the trace, 1: four of 2^-24 a direction.  O has norm f(s) sqrt(m - 1)
+    at least.  Binary32 results start again before the growth passes 48, where E counts (48 / G)^2 as much."""
+    _announce(f"one large {m} {n} {ratio} {xdt} {odt}")
+    gen = torch.Generator().manual_seed(m + ratio)
+    u = torch.linalg.qr(torch.randn(8, m, m, generator=gen, dtype=torch.float64))[0]
+    v = torch.linalg.qr(torch.randn(8, n, m, generator=gen, dtype=torch.float64))[0]
+    sv = torch.full((m,), 1.0 / ratio, dtype=torch.float64)
+    sv[0] = 1
+    x = ((u * sv) @ v.transpose(1, 2)).to(xdt).cuda()
+    out = torch.empty_like(x, dtype=odt)
+    _run_ns(x, out, MUON, 5)
+    torch.cuda.synchronize()
+
+    def f(s):
+        for a, b, c in orc.schedule(_co(MUON), 5):
+            s = s * (a + b * s * s + c * s ** 4)
+        return s
+
+    s = 1 / ratio / np.sqrt(1 + (m - 1) / ratio ** 2)
+    # p(l) = f(s) / s; p'(l) = (f'(s) - f(s) / s) / (2 l), over the values that rounding x spreads s to
+    worst = 0.0
+    for t in np.linspace(0.8, 1.25, 91) * s:
+        h = t * 1e-6
+        worst = max(worst, abs((f(t + h) - f(t - h)) / (2 * h) - f(t) / t) / (2 * t) / abs(f(t)))
+    e = 4 * 2.0 ** -24 * worst
+    tol = TB + e if odt == BF else _tol(F, m, MUON, 5) + e * (48 / 485) ** 2
+    _check_blocks(out, [orc.orthogonalise(w, _co(MUON), 5) for w in to_np(x)], tol, "NS")
+
+
 def test_gradient_against_differences():
     """<dx, d> against central differences of the library's own forward pass (binary32)."""
     _announce("differences")
@@ -511,6 +547,166 @@ def test_captured_calls():
         torch.cuda.synchronize()
         for a, b in zip(outs + dxs + w + m, ref + refd + we + me):
             assert np.array_equal(_bits(a), _bits(b)), f"replay {k}"
+
+
+# Groups of stacks that the library runs in two parts, the second on a stream
+# of its own: op, result type, stacks (blocks, rows, cols).  Their middle lies
+# inside a stack, or between two of a table in device memory.
+PARTED = [
+    ("ns", F, [(77, 40, 64), (61, 64, 40)]),
+    ("ns", F, [(9, 20, 100)] * 20),
+    ("ns", BF, [(530, 70, 80)]),
+    ("vjp", F, [(150, 16, 20)]),
+    ("vjp", F, [(67, 100, 20), (68, 18, 70)]),
+    ("vjp", BF, [(201, 66, 90)]),
+    ("step", F, [(131, 33, 70)]),
+    ("step", F, [(140, 128, 64)]),
+    ("step", BF, [(17, 130, 65)] * 32),
+]
+
+
+def _parted(op, dt, stacks, seed):
+    """Arguments, the call and its written tensors."""
+    gen = torch.Generator().manual_seed(seed)
+    xs = [torch.randn(s, generator=gen).to(dt).cuda() for s in stacks]
+    if op == "step":
+        ws = [(torch.randn(s, generator=gen) * 0.02).to(dt).cuda() for s in stacks]
+        ms = [torch.randn(s, generator=gen).cuda() for s in stacks]
+        args = mb.StepBlocksArgs(ws, xs, ms)
+        return args, lambda **k: mb.muon_step_blocks(args, lr=f32(0.02), beta=0.95, nesterov=True, ns_coeffs=MUON,
+                                                     ns_steps=5, **k), ws + ms, xs
+    outs = [torch.empty_like(x) for x in xs]
+    if op == "ns":
+        args = mb.NsBlocksArgs(xs, outs)
+        return args, lambda **k: mb.muon_ns_blocks(args, ns_coeffs=MUON, ns_steps=5, **k), outs, xs
+    ys = [torch.randn(s, generator=gen).to(dt).cuda() for s in stacks]
+    args = mb.VjpBlocksArgs(xs, ys, outs)
+    return args, lambda **k: mb.muon_ns_blocks_vjp(args, ns_coeffs=MUON, ns_steps=5, **k), outs, (xs, ys)
+
+
+@pytest.mark.parametrize("op,dt,stacks", PARTED, ids=lambda v: v if isinstance(v, str) else f"{len(v)}-{v[0]}"
+                         if isinstance(v, list) else str(v)[6:])
+def test_parts_on_two_streams_keep_the_bits(op, dt, stacks):
+    """A captured call runs on one stream, an eager one in two parts: the same bits, whatever else runs."""
+    _announce(f"parted {op} {dt} {stacks[0]} x {len(stacks)}")
+    args, call, written, inputs = _parted(op, dt, stacks, 31)
+    start = [t.clone() for t in written]
+    ws = _workspace(args)
+
+    def reset():
+        for t, t0 in zip(written, start):
+            t.copy_(t0)
+
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        call(workspace=ws)
+    reset()
+    graph.replay()
+    torch.cuda.synchronize()
+    ref = [t.clone() for t in written]
+    if op != "step":
+        for k, i in ((0, 0), (0, stacks[0][0] // 2), (len(stacks) - 1, stacks[-1][0] - 1)):
+            tol = _tol(dt, min(stacks[k][1:]), MUON, 5, grad=op == "vjp")
+            if op == "ns":
+                r = orc.orthogonalise(to_np(inputs[k][i]), _co(MUON), 5)
+            else:
+                r = orc.orthogonalise_vjp(to_np(inputs[0][k][i]), to_np(inputs[1][k][i]), _co(MUON), 5)
+            _check_blocks(ref[k][i:i + 1], [r], tol, op)
+    # with the library's workspace, its own, and timed; another call of the same kind beside it
+    other, call2, written2, _ = _parted(op, dt, stacks, 31)
+    ws2 = _workspace(other)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for kw in (dict(), dict(workspace=ws)):
+        reset()
+        for t, t0 in zip(written2, start):
+            t.copy_(t0)
+        torch.cuda.synchronize()
+        call(stream=s1, **kw)
+        call2(stream=s2, workspace=ws2)
+        torch.cuda.synchronize()
+        for a, b, r in zip(written, written2, ref):
+            assert np.array_equal(_bits(a), _bits(r)) and np.array_equal(_bits(b), _bits(r))
+    # the parts are joined: work that follows on the stream finds the whole result
+    reset()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s1):
+        call(stream=s1)
+        after = [t.clone() for t in written]
+        for t in written:
+            t.zero_()
+    torch.cuda.synchronize()
+    assert all(np.array_equal(_bits(a), _bits(r)) for a, r in zip(after, ref))
+    assert all(bool((t == 0).all()) for t in written)
+
+
+def _plain64(x, coeffs, steps):
+    """NS of a batch in float64 (wide or tall)."""
+    x = x.double()
+    if x.shape[1] > x.shape[2]:
+        return _plain64(x.transpose(1, 2), coeffs, steps).transpose(1, 2)
+    x = x / (x.flatten(1).norm(dim=1)[:, None, None] + 1e-7)
+    for a, b, c in orc.schedule(_co(coeffs), steps):
+        g = x @ x.transpose(1, 2)
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return x
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("blocks,rows,cols", [(300_001, 2, 3), (1 << 20, 1, 1), (2, 64, 65536), (1, 65536, 3),
+                                              (1, 128, 65536)])
+def test_largest_sizes(blocks, rows, cols, dt):
+    _announce(f"large {blocks} {rows} {cols} {dt}")
+    gen = torch.Generator().manual_seed(15)
+    x = torch.randn(blocks, rows, cols, generator=gen).to(dt).cuda()
+    out = torch.empty_like(x)
+    _run_ns(x, out, MUON, 5)
+    ref = _plain64(x, MUON, 5)
+    err = (out.double() - ref).flatten(1).norm(dim=1) / ref.flatten(1).norm(dim=1)
+    assert err.max().item() <= _tol(dt, min(rows, cols), MUON, 5)
+    mb.muon_release_workspace()
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+def test_offsets_past_32_bits(dt):
+    """Blocks more than 2^32 elements apart, and the longest row stride in both orientations."""
+    _announce(f"offsets {dt}")
+    gen = torch.Generator().manual_seed(16)
+    far = 2 ** 32 + 24
+    for rows, cols in ((40, 200), (200, 40)):
+        bufs = [torch.empty(far + rows * cols, dtype=dt, device="cuda") for _ in range(2)]
+        x, out = (b.as_strided((2, rows, cols), (far, cols, 1)) for b in bufs)
+        x.copy_(torch.randn(2, rows, cols, generator=gen).to(dt))
+        _run_ns(x, out, MUON, 5)
+        torch.cuda.synchronize()
+        _check_blocks(out, [orc.orthogonalise(v, _co(MUON), 5) for v in to_np(x)], _tol(dt, 40, MUON, 5), "far")
+        del x, out, bufs
+    ld = 2 ** 21
+    for rows, cols in ((300, 20), (120, 300)):
+        bufs = [torch.empty((rows - 1) * ld + cols, dtype=dt, device="cuda") for _ in range(3)]
+        x, y, out = (b.as_strided((1, rows, cols), (0, ld, 1)) for b in bufs)
+        x.copy_(torch.randn(1, rows, cols, generator=gen).to(dt))
+        y.copy_(torch.randn(1, rows, cols, generator=gen).to(dt))
+        _run_vjp(x, y, out, MUON, 5)
+        torch.cuda.synchronize()
+        ref = [orc.orthogonalise_vjp(to_np(x)[0], to_np(y)[0], _co(MUON), 5)]
+        _check_blocks(out, ref, _tol(dt, min(rows, cols), MUON, 5, grad=True), "stride")
+        del x, y, out, bufs
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("count", [16, 17, 96, 97, 230])
+def test_table_launches(count):
+    """Up to 16 stacks in a launch's arguments, 96 pointers and four shapes a table launch above."""
+    _announce(f"tables {count}")
+    gen = torch.Generator().manual_seed(count)
+    xs = [torch.randn(1 + i % 2, 9 + i % 7, 17 + i % 5, generator=gen).cuda() for i in range(count)]
+    outs = [torch.empty_like(x) for x in xs]
+    mb.muon_ns_blocks(xs, outs, ns_coeffs=CUBIC, ns_steps=3)
+    torch.cuda.synchronize()
+    for x, o in zip(xs, outs):
+        _check_blocks(o, [orc.orthogonalise(v, _co(CUBIC), 3) for v in to_np(x)],
+                      _tol(F, min(x.shape[1:]), CUBIC, 3), "NS")
 
 
 def test_fault_hook_changes_nothing(monkeypatch):
