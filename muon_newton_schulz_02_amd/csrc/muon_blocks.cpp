@@ -393,7 +393,10 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
       s.flags = tr ? BF_TR : 0;
       s.gchunk = int32_t(std::max<int64_t>(round_up((s.n + want - 1) / want, kc), 2 * kc));
       s.gsplit = (s.n + s.gchunk - 1) / s.gchunk;
-      s.achunk = s.gchunk;
+      // apply workgroups of six tiles at most: what runs at a time lies closer
+      // together in memory (1152 blocks of 128 x 1536, the step's: 2 tiles 500
+      // us, 4 488, 6 482, 12 494, 24 534)
+      s.achunk = std::min(s.gchunk, 6 * kc);
       s.asplit = (s.n + s.achunk - 1) / s.achunk;
       s.goff = int32_t(goff);
       s.aoff = int32_t(aoff);
