@@ -197,8 +197,7 @@ __global__ __launch_bounds__(GT, KIND == BK_VJP ? 2 : 4) void block_gram_kernel(
   gather(acc, NG);
   if (KIND == BK_VJP) gather(zacc, NZ);
   if (kw == 0) {
-    constexpr int PF = block_part_floats(MT, KIND);
-    float* out = partials + st.part0 + (int64_t(b) * st.gsplit + sp) * PF;
+    float* out = partials + st.part0 + (int64_t(b) * st.gsplit + sp) * st.part;
 #pragma unroll
     for (int q = 0; q < NG; ++q) *gmem(reinterpret_cast<f32x4_t*>(out + ((p * NG + q) * 64 + lane) * 4)) = acc[q];
     if (KIND == BK_VJP) {
@@ -226,7 +225,7 @@ __global__ void block_table_kernel(BlockTableBatch in, BlockStack* __restrict__ 
   s.block0 += k * s.blocks;
   s.goff += k * s.blocks * s.gsplit;
   s.aoff += k * s.blocks * s.asplit;
-  s.part0 += int64_t(k) * s.blocks * s.gsplit * in.part;
+  s.part0 += int64_t(k) * s.blocks * s.gsplit * s.part;
   out[i] = s;
   keys[KEY_GRAM * stride + i] = s.goff;
   keys[KEY_BLOCK * stride + i] = s.block0;
@@ -257,7 +256,7 @@ hipError_t gram_mt(int pl, int kind, bool xbf, const BlockTable& tab, int32_t wg
 
 }  // namespace
 
-hipError_t launch_block_table(const BlockStack* host, int32_t count, int32_t part, BlockStack* dev, int32_t* keys,
+hipError_t launch_block_table(const BlockStack* host, int32_t count, BlockStack* dev, int32_t* keys,
                               hipStream_t stream) {
   // what two stacks of a run share
   auto key = [](BlockStack s) {
@@ -271,7 +270,6 @@ hipError_t launch_block_table(const BlockStack* host, int32_t count, int32_t par
   for (int32_t i = 0; i < count;) {
     BlockTableBatch b;
     memset(&b, 0, sizeof(b));
-    b.part = part;
     int32_t classes = 0;
     BlockStack last;
     while (i + b.n < count && b.n < BLOCK_BATCH) {

@@ -27,6 +27,7 @@ struct BlockStack {
   int64_t out_ld, out_bs;
   float* upd;         // exported update, blocks x rows x cols contiguous, or null
   int64_t part0;      // first float of the stack's Gram partials
+  int64_t part;       // floats from one workgroup's partial to the next (the same at every stage)
   int32_t m, n;       // wide shape
   int32_t cols;       // row length of upd
   int32_t block0;     // index of the stack's first block in the launch
@@ -96,7 +97,6 @@ constexpr int BLOCK_BATCH = 96, BLOCK_CLASSES = 4;
 struct BlockTableBatch {
   int32_t n;
   int32_t first[BLOCK_CLASSES];   // first entry of each run (runs not used: n)
-  int32_t part;                   // floats of one workgroup's Gram partial
   BlockStack cls[BLOCK_CLASSES];
   const void* x[BLOCK_BATCH];
   const void* y[BLOCK_BATCH];
@@ -107,9 +107,8 @@ static_assert(sizeof(BlockTableBatch) <= 4096, "kernel arguments stay below 4 Ki
 
 // The launchers.  pl: bfloat16 parts of an element of x (1, 2, 3); pp: parts
 // of an element of P (2, 3); xbf: x is bfloat16 in every stack.
-// Writes a table of `count` stacks and its keys to device memory.  part:
-// floats of one workgroup's Gram partial.
-hipError_t launch_block_table(const BlockStack* host, int32_t count, int32_t part, BlockStack* dev, int32_t* keys,
+// Writes a table of `count` stacks and its keys to device memory.
+hipError_t launch_block_table(const BlockStack* host, int32_t count, BlockStack* dev, int32_t* keys,
                               hipStream_t stream);
 hipError_t launch_block_gram(int mt, int pl, int kind, bool xbf, const BlockTable& tab, int32_t wgs, float* partials,
                              const BlockMom& mom, hipStream_t stream);

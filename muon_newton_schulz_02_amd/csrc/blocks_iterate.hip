@@ -230,7 +230,7 @@ __global__ __launch_bounds__(iterate_threads(MT, KIND), 2) void block_iterate_ke
   // sum the partials, in order, into LDS (both triangles)
   constexpr int PF = block_part_floats(MT, KIND);
   const int parts = st.gsplit;
-  const float* src = partials + st.part0 + int64_t(b) * parts * PF;
+  const float* src = partials + st.part0 + int64_t(b) * parts * st.part;
   auto& L0 = lds.gram[0];
   auto& L1 = lds.gram[VJP ? 1 : 0];
   constexpr int IT = (PF / 4 + NT - 1) / NT;
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(iterate_threads(MT, KIND), 2) void block_iterate_ke
     sum[it] = *gmem(reinterpret_cast<const f32x4_t*>(src + 4 * e));
   }
   for (int q = 1; q < parts; ++q) {
-    src += PF;
+    src += st.part;
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
       const int e = min(it * NT + tid, PF / 4 - 1);

@@ -401,10 +401,11 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
       s.goff = int32_t(goff);
       s.aoff = int32_t(aoff);
       s.part0 = part;
+      s.part = block_part_floats(g.mt, kind);
       s.d = 1.f;
       goff += d.blocks * s.gsplit;
       aoff += d.blocks * s.asplit;
-      part += d.blocks * s.gsplit * int64_t(block_part_floats(g.mt, kind));
+      part += d.blocks * s.gsplit * s.part;
       block0 += d.blocks;
       g.base.push_back(s);
       g.stage_off.push_back(g.stage_bytes);
@@ -514,7 +515,6 @@ hipError_t group_phases(const Call& c, const Group& g, char* ws, std::vector<Pha
   };
 
   int32_t table = 0;
-  const int32_t part = block_part_floats(g.mt, vjp ? BK_VJP : BK_X);
   auto set_table = [&](BlockTable& tab, const std::vector<BlockStack>& v) -> hipError_t {
     memset(&tab, 0, sizeof(tab));
     tab.count = int32_t(v.size());
@@ -532,7 +532,7 @@ hipError_t group_phases(const Call& c, const Group& g, char* ws, std::vector<Pha
     int32_t* keys = reinterpret_cast<int32_t*>(at + align256(sizeof(BlockStack) * v.size()));
     tab.ext = dev;
     tab.ext_keys = keys;
-    return launch_block_table(v.data(), int32_t(v.size()), part, dev, keys, c.stream);
+    return launch_block_table(v.data(), int32_t(v.size()), dev, keys, c.stream);
   };
   auto steps_of = [&](const Stage& st, bool first) {
     BlockSteps s;

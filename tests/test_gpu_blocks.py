@@ -640,6 +640,27 @@ def test_parts_on_two_streams_keep_the_bits(op, dt, stacks):
     assert all(bool((t == 0).all()) for t in written)
 
 
+@pytest.mark.parametrize("blocks,m,n", [(300, 64, 768), (301, 40, 768), (200, 100, 300)])
+def test_parts_of_a_gradient_at_different_stages(blocks, m, n):
+    """One part of a gradient may be at a backward stage while the other is at a forward one, whose Gram partials are
+    shorter: neither touches the other's."""
+    _announce(f"stages apart {blocks} {m} {n}")
+    args, call, (dx,), _ = _parted("vjp", F, [(blocks, m, n)], 32)
+    ws = _workspace(args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        call(workspace=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    ref = _bits(dx)
+    for _ in range(8):
+        dx.fill_(float("nan"))
+        call()
+        torch.cuda.synchronize()
+        assert np.array_equal(_bits(dx), ref)
+
+
 def _plain64(x, coeffs, steps):
     """NS of a batch in float64 (wide or tall)."""
     x = x.double()
