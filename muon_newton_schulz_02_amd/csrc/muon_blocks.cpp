@@ -41,14 +41,16 @@ constexpr int64_t MAX_STRIDE = int64_t(1) << 40;
 // 4 x 64 up to 3e-3 beside the rounding of the result, 16 x 1024 1e-3.
 constexpr double LIMIT_BF16 = 512.0;
 constexpr double LIMIT_F32 = 48.0;
-// Blocks of so few rows that a single bad direction counts are nearly square
-// up to n < 4 m, and take LIMIT_F32 for bfloat16 results: the worst of 300000
-// random 2 x 3 blocks 2e-2 with LIMIT_BF16, 3.6e-3 so (2 x 4: 6e-3 and 3.7e-3;
-// half a step of the result is up to 3.9e-3).
-constexpr int64_t FEW_ROWS = 16;
-// Binary32 results of nearly square blocks (n < 2 m; m <= 16: n < 4 m), whose
-// singular values reach down to zero: two quintic steps a stage for the
-// orthogonalisation, one for its gradient (sixty random blocks, six steps, largest error: 2e-5
+// Blocks of so few rows that a single bad direction counts (m <= 4; m <= 16
+// up to n < 4 m) take LIMIT_F32 for bfloat16 results, and for binary32 ones
+// the limits of nearly square blocks: the worst of 300000 random 2 x 3 blocks
+// 2e-2 with LIMIT_BF16, 3.6e-3 so (2 x 4: 6e-3 and 3.7e-3; half a step of the
+// result is up to 3.9e-3); binary32, 3 x 212 with a singular value 100 times
+// the rest, 8e-6 with LIMIT_F32, 1.9e-6 so, binary32 iterates 2.0e-6.
+constexpr int64_t FEW_ROWS = 4, FEW_ROWS_SHORT = 16;
+// Binary32 results of nearly square blocks (n < 2 m), whose singular values
+// reach down to zero: two quintic steps a stage for the orthogonalisation, one
+// for its gradient (sixty random blocks, six steps, largest error: 2e-5
 // against 3e-5 with LIMIT_F32, and for the gradient the ninetieth percentile
 // 6e-6 against 2e-5; binary32 iterates 2e-5 and 6e-6).
 constexpr double LIMIT_F32_SQUARE = 12.0;
@@ -350,7 +352,7 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
     g.f32 = d.param_dtype == MUON_DTYPE_F32;
     g.xbf = d.grad_dtype == MUON_DTYPE_BF16;
     g.ybf = vjp && d.mom_dtype == MUON_DTYPE_BF16;
-    const bool few = m <= FEW_ROWS && n < 4 * m, square = few || n < 2 * m;
+    const bool few = m <= FEW_ROWS || (m <= FEW_ROWS_SHORT && n < 4 * m), square = few || n < 2 * m;
     g.limit = !g.f32 ? (few ? LIMIT_F32 : LIMIT_BF16)
               : !square ? LIMIT_F32 : vjp ? LIMIT_VJP_SQUARE : LIMIT_F32_SQUARE;
     const std::vector<int64_t> key = {g.mt, g.f32, g.xbf, g.ybf, int64_t(g.limit)};
