@@ -378,13 +378,19 @@ __global__ __launch_bounds__(iterate_threads(MT, KIND), 2) void block_iterate_ke
     if constexpr (VJP) {
       zero_sums<Acc, NR, V>(E);
       multiply<MP, TS, 2>({&C, &E}, LA, {&o, &od}, c, h);
-      ee = ld + o.ex;
-      const int d = ee - (la + od.ex);
-      if (d != 0) {
+      // with the larger power of two for the sum, unless it could overflow:
+      // where o is zero or below 2^-48 of what LD o adds to (rows of x that
+      // are zero, y's are not)
+      const int d = (ld + o.ex) - (la + od.ex);
+      ee = la + od.ex;
+      if (d <= 48) {
+        ee = ld + o.ex;
+        if (d != 0) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) E[i / V][i % V] = __builtin_amdgcn_ldexpf(E[i / V][i % V], d);
+          for (int i = 0; i < NV; ++i) E[i / V][i % V] = __builtin_amdgcn_ldexpf(E[i / V][i % V], d);
+        }
+        multiply<MP, TS, 1>({&E}, LD, {&o}, c, h);
       }
-      multiply<MP, TS, 1>({&E}, LD, {&o}, c, h);
     } else {
       multiply<MP, TS, 1>({&C}, LA, {&o}, c, h);
     }

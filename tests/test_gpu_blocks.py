@@ -286,6 +286,31 @@ def test_zero_nan_and_infinite_blocks_stay_apart():
                 assert bool(out[b].isnan().all()) and bool(dx[b].isnan().all())
 
 
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("rows,cols", [(40, 90), (64, 768), (128, 200), (300, 100)])
+@pytest.mark.parametrize("small", [0.0, 2.0 ** -60, 2.0 ** -110])
+def test_rows_of_zeros_and_tiny_rows(rows, cols, dt, small):
+    """Whole groups of rows of x (of columns where rows > cols) that are zero, or 2^-60 and 2^-110 of the others: y is
+    not, and the gradient there is P y."""
+    _announce(f"zero rows {rows} {cols} {dt} {small}")
+    gen = torch.Generator().manual_seed(rows)
+    x, _ = _make(3, rows, cols, dt, gen)
+    y, _ = _make(3, rows, cols, dt, gen)
+    part = x if rows <= cols else x.transpose(1, 2)
+    part[0, 16:32] *= small
+    part[1, :32] *= small
+    part[2, 5:6] *= small
+    part[2, 20:] *= small
+    out, dx = torch.empty_like(x), torch.empty_like(x)
+    _run_ns(x, out, MUON, 5)
+    _run_vjp(x, y, dx, MUON, 5)
+    torch.cuda.synchronize()
+    xs, ys, m = to_np(x), to_np(y), min(rows, cols)
+    _check_blocks(out, [orc.orthogonalise(v, _co(MUON), 5) for v in xs], _tol(dt, m, MUON, 5), "NS")
+    _check_blocks(dx, [orc.orthogonalise_vjp(v, w, _co(MUON), 5) for v, w in zip(xs, ys)],
+                  _tol(dt, m, MUON, 5, grad=True), "gradient")
+
+
 def test_tiny_and_large_scales():
     """NS(s x) for s from 2^-40 to 2^40: eps matters below, nothing above."""
     _announce("scales")
