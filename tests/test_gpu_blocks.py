@@ -311,6 +311,21 @@ def test_rows_of_zeros_and_tiny_rows(rows, cols, dt, small):
                   _tol(dt, m, MUON, 5, grad=True), "gradient")
 
 
+@pytest.mark.parametrize("e", [-100, -60, 60])
+@pytest.mark.parametrize("m,n", [(20, 100), (64, 768), (100, 130)])
+def test_scale_of_the_cotangent(m, n, e):
+    """The gradient is linear in y: 2^e y gives 2^e times it.  The parts of 2^-100 y that leave the range of bfloat16
+    are 2^-18 of it at most."""
+    _announce(f"cotangent 2^{e} {m} {n}")
+    gen = torch.Generator().manual_seed(m)
+    x, y = (torch.randn(3, m, n, generator=gen).cuda() for _ in range(2))
+    d0, d1 = torch.empty_like(x), torch.empty_like(x)
+    _run_vjp(x, y, d0, MUON, 5)
+    _run_vjp(x, y * 2.0 ** e, d1, MUON, 5)
+    torch.cuda.synchronize()
+    _check_blocks(d1, [to_np(d) * 2.0 ** e for d in d0], 2.0 ** -16, "gradient")
+
+
 def test_tiny_and_large_scales():
     """NS(s x) for s from 2^-40 to 2^40: eps matters below, nothing above."""
     _announce("scales")
