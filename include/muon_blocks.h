@@ -29,10 +29,13 @@
  * matrix of the current iterate (one more pass over the block) before the
  * steps since the last one multiply small singular values by more than a
  * limit: 512 where results are bfloat16 (five steps of the usual quintic,
- * 3.4445^5 = 485, are one pass; the error of a block whose singular values
- * span three decades stays below 1e-3), 48 where they are binary32 (errors
- * as those of the iteration carried out in binary32).  The gradient with
- * binary32 results takes a Gram matrix for every step where n < 2 m.
+ * 3.4445^5 = 485, are one pass), 48 where they are binary32.  Blocks of up to
+ * four rows, and of up to 16 with n < 4 m, take 48 for bfloat16 results; they
+ * and blocks with n < 2 m take 12 for binary32 ones, and their gradient a
+ * Gram matrix for every step.  Measured against float64: bfloat16 results are
+ * off by their rounding and up to 3e-3 more (4 x 64, one singular value 100
+ * times the others; 1e-3 from 16 rows on), binary32 results about as much as
+ * the same iteration carried out in binary32 (1e-6 to 1e-5).
  *
  * Conventions are those of muon.h (device memory of the current device,
  * strides in elements, validation before anything is enqueued, no
@@ -47,22 +50,28 @@
  *   - A block that holds a NaN or an infinity, or whose squared norm
  *     overflows binary32, gives NaN (its own block only).  A zero block gives
  *     zeros, and a zero gradient through the norm.
- *   - Products run on the bfloat16 matrix cores on operands split into
+ *   - Products over n run on the bfloat16 matrix cores on operands split into
  *     bfloat16 parts, with binary32 sums: bfloat16 inputs are one part
- *     (exact), binary32 values two parts (16 bits) where results are
- *     bfloat16 and three parts (24 bits) where they are binary32.  Results do
- *     not depend on the other stacks of a call or on their order, except that
- *     the Gram sums over n are split by the number of blocks in the call;
- *     the same call gives the same bits every time.
+ *     (exact), binary32 values two parts (17 bits) where results are bfloat16
+ *     and three parts (24 bits) where they are binary32.  The recursion runs
+ *     on two binary16 parts (24 bits).  Results do not depend on the other
+ *     stacks of a call or on their order, except that the Gram sums over n
+ *     are split by the number of blocks in the call; the same call gives the
+ *     same bits every time, captured or not.
  *   - Workspace: with workspace = NULL the library keeps one per device (grown
  *     on demand, freed by muon_release_workspace), and calls on a device that
  *     use it run one after another in the order they were made, whatever
  *     their streams.  With a workspace of the caller's (256-byte aligned
  *     device memory of muon_blocks_workspace_bytes bytes) the call only
- *     launches kernels on `stream`: it may be captured into a HIP graph, and
- *     calls or graphs with different workspaces may overlap; those that share
- *     one must not.  A call on a capturing stream with workspace = NULL is
- *     UNSUPPORTED.
+ *     launches kernels: calls or graphs with different workspaces may
+ *     overlap; those that share one must not.
+ *   - Capture: a call on a capturing stream needs a workspace of the caller's
+ *     (UNSUPPORTED without) and records kernels on `stream` only.  Pointers,
+ *     sizes, coefficients, rates and decay are those of the capture.
+ *   - Streams: a call that is not captured may run part of a large group of
+ *     blocks on a second stream of the library's, one per device, at the
+ *     default priority.  That part starts after what `stream` held before the
+ *     call, and `stream` goes on after it.
  */
 #ifndef MUON_MI355X_BLOCKS_H
 #define MUON_MI355X_BLOCKS_H
@@ -73,10 +82,10 @@
 extern "C" {
 #endif
 
-/* One stack.  blocks in [0, 2^20] (0: skipped), rows and cols in [1, 65536]
- * with min(rows, cols) <= 128, row strides up to 2^21.  Which tensors the three groups of fields
- * describe is said at each call; a group that a call does not name is
- * ignored.  reserved: 0.                                                    */
+/* One stack.  blocks in [0, 2^20] (0: skipped; at most 2^21 in a call), rows
+ * and cols in [1, 65536] with min(rows, cols) <= 128, row strides up to 2^21.
+ * Which tensors the three groups of fields describe is said at each call; a
+ * group that a call does not name is ignored.  reserved: 0.                 */
 typedef struct muon_block_desc {
   int64_t blocks, rows, cols;
   int64_t ld_param, ld_grad, ld_mom;             /* row strides, >= cols     */
