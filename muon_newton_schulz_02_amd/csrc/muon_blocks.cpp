@@ -399,6 +399,12 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
       // together in memory (1152 blocks of 128 x 1536, the step's: 2 tiles 500
       // us, 4 488, 6 482, 12 494, 24 534)
       s.achunk = std::min(s.gchunk, 6 * kc);
+      // one tile each where every compute unit has one at most (two tiles and
+      // one: 12 blocks of 64 x 768 5.3 and 4.3 us, 12 binary32 ones of 16 rows
+      // 7.9 and 5.4, their gradient 11.2 and 7.3; with two workgroups a
+      // compute unit no gain, the gradient 15.1 and 17.7).  A gram pass so cut
+      // gains 0.8 us and the recursion, which adds up its partials, loses 1
+      if (g.blocks * ((s.n + kc - 1) / kc) <= cus) s.achunk = kc;
       s.asplit = (s.n + s.achunk - 1) / s.achunk;
       s.goff = int32_t(goff);
       s.aoff = int32_t(aoff);
