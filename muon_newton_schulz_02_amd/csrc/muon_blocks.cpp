@@ -333,6 +333,20 @@ struct Group {
   size_t o_tab = 0, o_part = 0, o_p = 0, o_t = 0, o_scr = 0, o_stage = 0, end = 0;
 };
 
+// Whether a group is worth two streams.  Measured, two streams against one:
+// several stages (binary32 results; 64 x 768 and 128 x 1536 blocks): 128 blocks
+// 1.02, 300 1.07 to 1.11, 576 1.06 to 1.17; the gradient of 128-row blocks, of
+// which a compute unit holds one: 200 blocks 1.05, 260 1.25, 600 1.12, 1000
+// 0.99 (64 rows: 0.95 to 0.98, not split); one forward stage of them, two to a
+// compute unit, gains where a second round of the recursion would be nearly
+// empty: 576 blocks 1.08, 600 1.09, but 512 0.89, 700 0.90 to 1.02, 1152 0.97.
+bool two_streams(const Group& g, int op, int64_t cus) {
+  if (g.stages.size() > 1) return g.blocks >= cus / 2;
+  if (g.mt != 8) return false;
+  if (op == MUON_BLOCKS_VJP) return g.blocks >= cus * 3 / 4;
+  return g.blocks > 2 * cus && g.blocks <= cus * 5 / 2;
+}
+
 int64_t ld_of_stage(const muon_block_desc& d) { return round_up(d.cols, 4); }
 
 // A device table and its keys.
@@ -378,9 +392,19 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
                              d.stride_mom);
     };
     std::stable_sort(g.members.begin(), g.members.end(), [&](int32_t a, int32_t b) { return key(a) < key(b); });
-    // workgroups enough to fill the GPU four times over, two to a compute
-    // unit, each with two tiles of columns at least
-    const int64_t want = std::max<int64_t>(1, (8 * int64_t(cus) + g.blocks - 1) / g.blocks);
+    // gram workgroups enough to fill the GPU once, two to a compute unit, each
+    // with two tiles of columns at least: more even ones write more partials
+    // (128 rows: 36 KB each, the gradient's 100), which the recursion reads.
+    // Both passes with 8, 4, 2 and 1 workgroups a compute unit: the gradient of
+    // 288 bfloat16 blocks of 128 x 1536 420, 378, 361 and 356 us, 576 of them
+    // forward 227, 219, 218 and 218; the step of 48 79, 79, 76 and 79, of 1152
+    // 714, 728, 725 and 721.  The apply pass takes four times as many.
+    const int64_t launch = two_streams(g, c.op, cus) ? (g.blocks + 1) / 2 : g.blocks;
+    const int64_t per = (2 * int64_t(cus) + launch - 1) / launch;
+    const int64_t aper = (8 * int64_t(cus) + g.blocks - 1) / g.blocks;
+    auto chunk = [&](int64_t n, int64_t split) {
+      return int32_t(std::max<int64_t>(round_up((n + split - 1) / split, kc), 2 * kc));
+    };
     int64_t goff = 0, aoff = 0, block0 = 0, part = 0;
     for (int32_t i : g.members) {
       const muon_block_desc& d = c.stacks[i];
@@ -393,12 +417,12 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
       s.blocks = int32_t(d.blocks);
       s.block0 = int32_t(block0);
       s.flags = tr ? BF_TR : 0;
-      s.gchunk = int32_t(std::max<int64_t>(round_up((s.n + want - 1) / want, kc), 2 * kc));
+      s.gchunk = chunk(s.n, per);
       s.gsplit = (s.n + s.gchunk - 1) / s.gchunk;
       // apply workgroups of six tiles at most: what runs at a time lies closer
       // together in memory (1152 blocks of 128 x 1536, the step's: 2 tiles 500
       // us, 4 488, 6 482, 12 494, 24 534)
-      s.achunk = std::min(s.gchunk, 6 * kc);
+      s.achunk = std::min(chunk(s.n, aper), 6 * kc);
       // one tile each where every compute unit has one at most (two tiles and
       // one: 12 blocks of 64 x 768 5.3 and 4.3 us, 12 binary32 ones of 16 rows
       // 7.9 and 5.4, their gradient 11.2 and 7.3; with two workgroups a
@@ -707,20 +731,6 @@ bool side_stream(BlockDevice& bd) {
   if (bd.side && bd.fork && bd.join) return true;
   (void)hipGetLastError();
   return false;
-}
-
-// Whether a group is worth two streams.  Measured, two streams against one:
-// several stages (binary32 results; 64 x 768 and 128 x 1536 blocks): 128 blocks
-// 1.02, 300 1.07 to 1.11, 576 1.06 to 1.17; the gradient of 128-row blocks, of
-// which a compute unit holds one: 200 blocks 1.05, 260 1.25, 600 1.12, 1000
-// 0.99 (64 rows: 0.95 to 0.98, not split); one forward stage of them, two to a
-// compute unit, gains where a second round of the recursion would be nearly
-// empty: 576 blocks 1.08, 600 1.09, but 512 0.89, 700 0.90 to 1.02, 1152 0.97.
-bool two_streams(const Group& g, int op, int64_t cus) {
-  if (g.stages.size() > 1) return g.blocks >= cus / 2;
-  if (g.mt != 8) return false;
-  if (op == MUON_BLOCKS_VJP) return g.blocks >= cus * 3 / 4;
-  return g.blocks > 2 * cus && g.blocks <= cus * 5 / 2;
 }
 
 // Enqueues one group.  The recursion keeps the matrix cores busy and the other
