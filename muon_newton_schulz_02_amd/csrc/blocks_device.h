@@ -23,9 +23,9 @@ __device__ __forceinline__ int block_number() {
 
 // The stack whose range of workgroups (or blocks) holds number b, the same in
 // all lanes.  The table is the kernel's first argument.  The lanes compare 64
-// keys at a time, so that a workgroup waits for two loads, not for a search;
-// the descriptor is read through the constant address space and stays in
-// scalar registers.
+// keys at a time, every 64^k-th first, so that a workgroup waits for two loads
+// (up to 64 stacks; four for 2^18), not for a search; the descriptor is read
+// through the constant address space and stays in scalar registers.
 template <int KEY>
 __device__ __forceinline__ BlockStack find_stack(int b) {
   typedef __attribute__((address_space(4))) const BlockStack ConstStack;
@@ -36,10 +36,14 @@ __device__ __forceinline__ BlockStack find_stack(int b) {
   ConstInt* keys = tab->ext ? (ConstInt*)tab->ext_keys + KEY * count : &tab->keys[KEY][0];
   ConstStack* t = tab->ext ? (ConstStack*)tab->ext : &tab->inl[0];
   const int lane = threadIdx.x & 63;
-  int below = 0;  // keys not above b: they ascend, and the first is 0
-  for (int i = 0; i < count; i += 64)
-    below += __popcll(__ballot(i + lane < count && keys[min(i + lane, count - 1)] <= b));
-  const int at = __builtin_amdgcn_readfirstlane(below) - 1;
+  int step = 1, at = 0;  // keys ascend, and keys[at] <= b (the first is 0)
+  while (step * 64 < count) step *= 64;
+  for (;; step /= 64) {
+    const int i = at + lane * step;
+    const int below = __popcll(__ballot(i < count && keys[min(i, count - 1)] <= b));
+    at += (__builtin_amdgcn_readfirstlane(below) - 1) * step;
+    if (step == 1) break;
+  }
   BlockStack s;
   __builtin_memcpy(&s, (const BlockStack*)(t + at), sizeof(s));
   return s;

@@ -770,6 +770,76 @@ def test_table_launches(count):
                       _tol(F, min(x.shape[1:]), CUBIC, 3), "NS")
 
 
+def test_thousands_of_stacks():
+    _announce("20000 stacks")
+    gen = torch.Generator().manual_seed(40)
+    base = torch.randn(20000, 1, 6, 9, generator=gen).cuda()
+    out = torch.empty_like(base)
+    mb.muon_ns_blocks(list(base), list(out), ns_coeffs=MUON, ns_steps=5)
+    ref = _plain64(base[:, 0], MUON, 5)
+    err = (out[:, 0].double() - ref).flatten(1).norm(dim=1) / ref.flatten(1).norm(dim=1)
+    assert err.max().item() <= _tol(F, 6, MUON, 5)
+
+
+def test_calls_from_two_threads():
+    """Calls made at once share the library's workspace one after another."""
+    import threading
+
+    _announce("threads")
+    cases = [_parted("ns", F, [(77, 40, 64), (61, 64, 40)], 41), _parted("vjp", BF, [(30, 66, 90), (5, 20, 300)], 42)]
+    ref = []
+    for _, call, written, _ in cases:
+        call()
+        torch.cuda.synchronize()
+        ref.append([_bits(t) for t in written])
+        for t in written:
+            t.zero_()
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(k):
+        try:
+            torch.cuda.set_device(0)
+            stream = torch.cuda.Stream()
+            for _ in range(20):
+                cases[k][1](stream=stream)
+            stream.synchronize()
+        except Exception as e:  # handed to the test below
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for (_, _, written, _), r in zip(cases, ref):
+        assert all(np.array_equal(_bits(t), b) for t, b in zip(written, r))
+
+
+def test_timing_counts_the_passes():
+    """With per-kernel timing a call runs on one stream, in the classes of the whole-matrix step, to the same bits."""
+    _announce("timing")
+    args, call, written, _ = _parted("step", F, [(131, 33, 70)], 43)
+    start = [t.clone() for t in written]
+    call()
+    torch.cuda.synchronize()
+    ref = [_bits(t) for t in written]
+    for t, t0 in zip(written, start):
+        t.copy_(t0)
+    mb.muon_timing_enable(True)
+    try:
+        call()
+        torch.cuda.synchronize()
+        launches = {k: n for k, (_, n) in mb.muon_timing_read().items()}
+    finally:
+        mb.muon_timing_enable(False)
+    assert all(np.array_equal(_bits(t), r) for t, r in zip(written, ref))
+    assert launches["momentum"] == 1 and launches["gram"] == 1  # two stages: the first one's gram pass has the momentum
+    assert launches["poly"] == 2 and launches["combine"] == 2
+
+
 def test_fault_hook_changes_nothing(monkeypatch):
     _announce("allocation failure")
     x = torch.randn(3, 50, 80).cuda()
