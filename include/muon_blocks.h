@@ -68,10 +68,10 @@
  *   - Capture: a call on a capturing stream needs a workspace of the caller's
  *     (UNSUPPORTED without) and records kernels on `stream` only.  Pointers,
  *     sizes, coefficients, rates and decay are those of the capture.
- *   - Streams: a call that is not captured may run part of a large group of
- *     blocks on a second stream of the library's, one per device, at the
- *     default priority.  That part starts after what `stream` held before the
- *     call, and `stream` goes on after it.
+ *   - Streams: a call that is not captured may run parts of a large group of
+ *     blocks on further streams of the library's (up to two a device, at the
+ *     default priority).  They start after what `stream` held before the
+ *     call, and `stream` goes on after them.
  */
 #ifndef MUON_MI355X_BLOCKS_H
 #define MUON_MI355X_BLOCKS_H

@@ -325,6 +325,7 @@ struct Group {
   int64_t blocks = 0;
   std::vector<Stage> stages;
   int32_t gram_wgs = 0, apply_wgs = 0;
+  int parts = 1;                    // of an eager call
   std::vector<BlockStack> base;     // sizes and splits; views are filled per stage
   std::vector<size_t> stage_off;    // per member: byte offset of its binary32 copy in a stage buffer
   size_t stage_bytes = 0;           // one stage buffer
@@ -333,18 +334,26 @@ struct Group {
   size_t o_tab = 0, o_part = 0, o_p = 0, o_t = 0, o_scr = 0, o_stage = 0, end = 0;
 };
 
-// Whether a group is worth two streams.  Measured, two streams against one:
-// several stages (binary32 results; 64 x 768 and 128 x 1536 blocks): 128 blocks
-// 1.02, 300 1.07 to 1.11, 576 1.06 to 1.17; the gradient of 128-row blocks, of
-// which a compute unit holds one: 200 blocks 1.05, 260 1.25, 600 1.12, 1000
-// 0.99 (64 rows: 0.95 to 0.98, not split); one forward stage of them, two to a
-// compute unit, gains where a second round of the recursion would be nearly
-// empty: 576 blocks 1.08, 600 1.09, but 512 0.89, 700 0.90 to 1.02, 1152 0.97.
-bool two_streams(const Group& g, int op, int64_t cus) {
-  if (g.stages.size() > 1) return g.blocks >= cus / 2;
-  if (g.mt != 8) return false;
-  if (op == MUON_BLOCKS_VJP) return g.blocks >= cus * 3 / 4;
-  return g.blocks > 2 * cus && g.blocks <= cus * 5 / 2;
+// Parts of a group that an eager call runs on streams of their own.  Measured,
+// time on one stream over time in two, three and four parts:
+//  - several stages (binary32): the gradient 130 blocks 0.97 to 1.04, 216 to
+//    600 1.03 to 1.20 in two; forward at 128 rows 130 to 200 0.97 to 1.01, 300
+//    to 600 1.04 to 1.06 in two; at 64 rows 576 0.96 to 1.00, 1200 1.04;
+//  - the bfloat16 step at 128 rows 400 blocks 0.99, 0.96, 1.03; 520 to 1500
+//    1.00 to 1.04, 1.02 to 1.09, 0.99 to 1.05;
+//  - the other bfloat16 calls at 128 rows gain where a second round of the
+//    recursion (a compute unit holds two blocks, of the gradient one) would be
+//    nearly empty: the gradient 260 to 330 1.10 to 1.13 in two, 400 0.98, 200
+//    0.93, 640 1.00; forward 520 to 576 1.01 to 1.04, 640 0.91, 1152 0.97;
+//  - the same at 64 rows 0.95 to 0.98.
+constexpr int MAX_PARTS = 3;
+int parts_of(const Group& g, int op, int64_t cus) {
+  const bool vjp = op == MUON_BLOCKS_VJP;
+  if (g.stages.size() > 1) return g.blocks >= (vjp ? cus * 3 / 4 : g.mt == 8 ? cus : 4 * cus) ? 2 : 1;
+  if (g.mt != 8) return 1;
+  const int64_t round = vjp ? cus : 2 * cus;
+  if (op == MUON_BLOCKS_STEP) return g.blocks > round ? 3 : 1;
+  return g.blocks > round && g.blocks <= round + cus * 3 / 8 ? 2 : 1;
 }
 
 int64_t ld_of_stage(const muon_block_desc& d) { return round_up(d.cols, 4); }
@@ -399,7 +408,8 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
     // 288 bfloat16 blocks of 128 x 1536 420, 378, 361 and 356 us, 576 of them
     // forward 227, 219, 218 and 218; the step of 48 79, 79, 76 and 79, of 1152
     // 714, 728, 725 and 721.  The apply pass takes four times as many.
-    const int64_t launch = two_streams(g, c.op, cus) ? (g.blocks + 1) / 2 : g.blocks;
+    g.parts = parts_of(g, c.op, cus);
+    const int64_t launch = (g.blocks + g.parts - 1) / g.parts;
     const int64_t per = (2 * int64_t(cus) + launch - 1) / launch;
     const int64_t aper = (8 * int64_t(cus) + g.blocks - 1) / g.blocks;
     auto chunk = [&](int64_t n, int64_t split) {
@@ -682,9 +692,9 @@ struct BlockDevice {
   size_t ws_bytes = 0;
   hipEvent_t last = nullptr;   // after the last call that used ws
   bool recorded = false;
-  // the second stream of a large call and its events (fork, join)
-  hipStream_t side = nullptr;
-  hipEvent_t fork = nullptr, join = nullptr;
+  // the further streams of a large call and their events
+  hipStream_t side[MAX_PARTS - 1] = {};
+  hipEvent_t fork[MAX_PARTS - 1] = {}, join[MAX_PARTS - 1] = {};
 };
 std::map<int, BlockDevice> g_blocks;  // under api_mutex()
 
@@ -694,9 +704,11 @@ void release_blocks() {
     (void)hipDeviceSynchronize();
     if (kv.second.ws) (void)hipFree(kv.second.ws);
     if (kv.second.last) (void)hipEventDestroy(kv.second.last);
-    if (kv.second.side) (void)hipStreamDestroy(kv.second.side);
-    if (kv.second.fork) (void)hipEventDestroy(kv.second.fork);
-    if (kv.second.join) (void)hipEventDestroy(kv.second.join);
+    for (int k = 0; k < MAX_PARTS - 1; ++k) {
+      if (kv.second.side[k]) (void)hipStreamDestroy(kv.second.side[k]);
+      if (kv.second.fork[k]) (void)hipEventDestroy(kv.second.fork[k]);
+      if (kv.second.join[k]) (void)hipEventDestroy(kv.second.join[k]);
+    }
   }
   g_blocks.clear();
 }
@@ -723,38 +735,49 @@ muon_status current_device(BlockDevice** out) {
   return MUON_OK;
 }
 
-// The side stream and its events; without them a call runs on its own stream.
-bool side_stream(BlockDevice& bd) {
-  if (!bd.side && hipStreamCreateWithFlags(&bd.side, hipStreamNonBlocking) != hipSuccess) bd.side = nullptr;
-  if (!bd.fork && hipEventCreateWithFlags(&bd.fork, hipEventDisableTiming) != hipSuccess) bd.fork = nullptr;
-  if (!bd.join && hipEventCreateWithFlags(&bd.join, hipEventDisableTiming) != hipSuccess) bd.join = nullptr;
-  if (bd.side && bd.fork && bd.join) return true;
-  (void)hipGetLastError();
-  return false;
+// The streams of `parts` parts and their events; without them a call runs on
+// its own stream.
+bool side_streams(BlockDevice& bd, int parts) {
+  for (int k = 0; k < parts - 1; ++k) {
+    if (!bd.side[k] && hipStreamCreateWithFlags(&bd.side[k], hipStreamNonBlocking) != hipSuccess) bd.side[k] = nullptr;
+    if (!bd.fork[k] && hipEventCreateWithFlags(&bd.fork[k], hipEventDisableTiming) != hipSuccess) bd.fork[k] = nullptr;
+    if (!bd.join[k] && hipEventCreateWithFlags(&bd.join[k], hipEventDisableTiming) != hipSuccess) bd.join[k] = nullptr;
+    if (!bd.side[k] || !bd.fork[k] || !bd.join[k]) {
+      (void)hipGetLastError();
+      return false;
+    }
+  }
+  return true;
 }
 
 // Enqueues one group.  The recursion keeps the matrix cores busy and the other
-// two passes the memory, so a group may be cut in two: the second part's
-// passes run on a side stream, behind the first part's gram pass, and each
-// part's recursion runs beside a pass over memory of the other part.
+// two passes the memory, so a group may be cut into parts: each but the first
+// runs on a stream of its own, behind the gram pass of the part before, and
+// one part's recursion runs beside another's passes over memory.
 hipError_t enqueue_group(const Call& c, const Group& g, char* ws, BlockDevice& bd, bool capturing) {
   std::vector<Phase> phases;
   hipError_t e = group_phases(c, g, ws, phases);
-  const bool split = !capturing && !api_timing() && two_streams(g, c.op, bd.cus) && side_stream(bd);
-  const int64_t cut = !split ? g.blocks : (g.blocks + 1) / 2;
+  const bool split = g.parts > 1 && !capturing && !api_timing() && side_streams(bd, g.parts);
+  const int parts = split ? g.parts : 1;
   auto run = [&](int kc, auto&& launch) -> hipError_t {
     return capturing ? launch() : api_timed(kc, c.stream, launch);
   };
-  for (size_t i = 0; i < phases.size() && e == hipSuccess; ++i) {
-    e = enqueue_phase(c, g, phases[i], ws, 0, cut, c.stream, split && i == 0 ? bd.fork : nullptr, run);
-    if (!split || e != hipSuccess) continue;
-    if (i == 0) e = hipStreamWaitEvent(bd.side, bd.fork, 0);
-    if (e == hipSuccess) e = enqueue_phase(c, g, phases[i], ws, cut, g.blocks, bd.side, nullptr, run);
-  }
-  if (split) {
-    // also after a failed launch: what was enqueued belongs to this call
-    const hipError_t j = hipEventRecord(bd.join, bd.side);
-    const hipError_t w = j == hipSuccess ? hipStreamWaitEvent(c.stream, bd.join, 0) : j;
+  int used = 1;
+  for (size_t i = 0; i < phases.size() && e == hipSuccess; ++i)
+    for (int k = 0; k < parts && e == hipSuccess; ++k) {
+      hipStream_t s = k == 0 ? c.stream : bd.side[k - 1];
+      if (i == 0 && k > 0) {
+        e = hipStreamWaitEvent(s, bd.fork[k - 1], 0);
+        if (e != hipSuccess) break;
+        used = k + 1;
+      }
+      e = enqueue_phase(c, g, phases[i], ws, g.blocks * k / parts, g.blocks * (k + 1) / parts, s,
+                        i == 0 && k + 1 < parts ? bd.fork[k] : nullptr, run);
+    }
+  // also after a failed launch: what was enqueued belongs to this call
+  for (int k = 1; k < used; ++k) {
+    const hipError_t j = hipEventRecord(bd.join[k - 1], bd.side[k - 1]);
+    const hipError_t w = j == hipSuccess ? hipStreamWaitEvent(c.stream, bd.join[k - 1], 0) : j;
     if (e == hipSuccess) e = w;
   }
   return e;

@@ -589,9 +589,10 @@ def test_captured_calls():
             assert np.array_equal(_bits(a), _bits(b)), f"replay {k}"
 
 
-# Groups of stacks that the library runs in two parts, the second on a stream
-# of its own: op, result type, stacks (blocks, rows, cols).  Their middle lies
-# inside a stack, or between two of a table in device memory.
+# Groups of stacks about as large as those that the library runs in two or three
+# parts, all but the first on streams of their own: op, result type, stacks
+# (blocks, rows, cols).  The parts meet inside a stack, or between two of a
+# table in device memory.
 PARTED = [
     ("ns", F, [(77, 40, 64), (61, 64, 40)]),
     ("ns", F, [(9, 20, 100)] * 20),
@@ -602,6 +603,11 @@ PARTED = [
     ("step", F, [(131, 33, 70)]),
     ("step", F, [(140, 128, 64)]),
     ("step", BF, [(17, 130, 65)] * 32),
+    ("ns", F, [(9, 70, 150)] * 30),
+    ("ns", F, [(1030, 12, 30)]),
+    ("vjp", F, [(197, 16, 20)]),
+    ("vjp", BF, [(129, 66, 90), (130, 100, 70)]),
+    ("step", F, [(260, 128, 64)]),
 ]
 
 
