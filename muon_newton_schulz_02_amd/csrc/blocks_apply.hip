@@ -133,6 +133,19 @@ __global__ __launch_bounds__(AT, two_resident(MT, PL, KIND) ? 4 : 2) void block_
   for (int kb = c0; kb < c1; kb += KC) {
 #pragma unroll
     for (int mat = 0; mat < NM; ++mat) {
+      if constexpr (PL == 1) {  // bfloat16 as it is
+        const Raw8(&raw)[2] = mat ? ry : rx;
+        if (!tr) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint32_t*>(&xs[mat][0][tile_row(col0 + i)][row0]) = pair_bf16(raw[0], raw[1], i);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<u32x4_t*>(&xs[mat][0][tile_row(col0 + q * dcol)][row0]) = raw[q].a;
+        }
+        continue;
+      }
       float v[2][8];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {

@@ -170,6 +170,11 @@ __device__ __forceinline__ void split2(float v0, float v1, uint32_t part[PL]) {
   }
 }
 
+// The i-th elements of two runs of eight bfloat16, side by side.
+__device__ __forceinline__ uint32_t pair_bf16(const Raw8& r0, const Raw8& r1, int i) {
+  return __builtin_amdgcn_perm(r1.a[i / 2], r0.a[i / 2], i & 1 ? 0x07060302u : 0x05040100u);
+}
+
 // Four runs of two values as PL operands of eight bfloat16.
 template <int PL>
 __device__ __forceinline__ void split8(const float v[8], bf16x8_t out[PL]) {

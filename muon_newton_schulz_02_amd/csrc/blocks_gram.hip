@@ -115,6 +115,19 @@ __global__ __launch_bounds__(GT, KIND == BK_VJP ? 2 : 4) void block_gram_kernel(
     Tile& tile = lds[buf];
 #pragma unroll
     for (int mat = 0; mat < NM; ++mat) {
+      if constexpr (PL == 1) {  // bfloat16 as it is
+        const Raw8(&raw)[2] = mat ? ry : rx;
+        if (!tr) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<u32x4_t*>(&tile[mat][0][row0 + q * DR][col0]) = raw[q].a;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint32_t*>(&tile[mat][0][row0 + i][col0]) = pair_bf16(raw[0], raw[1], i);
+        }
+        continue;
+      }
       float v[2][8];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
