@@ -73,8 +73,11 @@ __global__ __launch_bounds__(GT, KIND == BK_VJP ? 2 : 4) void block_gram_kernel(
 
   // the thread's two runs of 8 elements: rows contiguous along k, two runs of
   // 8 columns (512 threads apart); transposed, 8 rows of two columns
-  const int row0 = tr ? (tid % (MP / 8)) * 8 : tid / (KC / 8);
-  const int col0 = tr ? (tid / (MP / 8)) * 2 : (tid % (KC / 8)) * 8;
+  // (transposed, a wave takes 32 rows of 32 columns: its stores to LDS, a row
+  // of x each, then meet two to a bank, eight with all rows of 8 columns)
+  constexpr int RB = MP / 32;
+  const int row0 = tr ? (tid & 3) * 8 + wave % RB * 32 : tid / (KC / 8);
+  const int col0 = tr ? (lane >> 2) * 2 + wave / RB * 32 : (tid % (KC / 8)) * 8;
   constexpr int DR = GT / (KC / 8);
   // first byte of the first tile, bytes from tile to tile, and the first
   // run's byte offset in a tile
