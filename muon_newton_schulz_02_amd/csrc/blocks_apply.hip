@@ -133,7 +133,8 @@ __global__ __launch_bounds__(AT, two_resident(MT, PL, KIND) ? 4 : 2) void block_
   for (int kb = c0; kb < c1; kb += KC) {
 #pragma unroll
     for (int mat = 0; mat < NM; ++mat) {
-      if constexpr (PL == 1) {  // bfloat16 as it is
+      // bfloat16 as it is (the gradient at 128 rows would spill: 98 us, 110 so)
+      if constexpr (PL == 1 && (KIND != BK_VJP || MT < 8)) {
         const Raw8(&raw)[2] = mat ? ry : rx;
         if (!tr) {
 #pragma unroll
