@@ -13,10 +13,10 @@
 // runs of 8 elements of its rows, whichever way the block is stored.
 //
 // Bound by memory: the step's pass over 1152 bfloat16 blocks of 128 x 1536
-// (gradient, momentum and weight read, weight written, 2.27 GB) 484 us, 4.7
-// TB/s; 576 blocks read and written (0.45 GB) 111 us, 4.1 TB/s; 576 binary32
-// blocks of 64 x 768 (0.23 GB) 52 us, 4.3 TB/s; the gradient of 288 blocks of
-// 128 x 1536 (0.34 GB) 98 us, 3.5 TB/s.  Loads and stores past the caches
+// (gradient, momentum and weight read, weight written, 2.27 GB) 487 us, 4.7
+// TB/s; 576 blocks read and written (0.45 GB) 114 us, 4.0 TB/s; 576 binary32
+// blocks of 64 x 768 (0.23 GB) 55 us, 4.1 TB/s; the gradient of 288 blocks of
+// 128 x 1536 (0.34 GB) 99 to 103 us, 3.4 TB/s.  Loads and stores past the caches
 // (nontemporal) gave the largest call 4% and took 5% to 10% from calls whose
 // tensors stay in the last-level cache.
 #include <hip/hip_runtime.h>

@@ -14,9 +14,9 @@
 //
 // Bound by memory from some hundred blocks on, by the latency of a few
 // dependent loads below: the step's pass over 1152 bfloat16 blocks of
-// 128 x 1536 (gradient and momentum read, momentum written, 2.27 GB) 468 us,
-// 4.8 TB/s, as fast as a copy; 576 blocks read only (0.23 GB) 69 us, 3.3 TB/s;
-// 576 binary32 blocks of 64 x 768 31 us, 3.6 TB/s; 12 bfloat16 ones 4.9 us.
+// 128 x 1536 (gradient and momentum read, momentum written, 2.27 GB) 451 us,
+// 5.0 TB/s, as fast as a copy; 576 blocks read only (0.23 GB) 70 us, 3.2 TB/s;
+// 576 binary32 blocks of 64 x 768 32 us, 3.5 TB/s; 12 bfloat16 ones 4.8 us.
 // Two tiles in flight instead of one took the same time.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

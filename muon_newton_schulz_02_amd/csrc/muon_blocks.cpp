@@ -403,14 +403,17 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
     std::stable_sort(g.members.begin(), g.members.end(), [&](int32_t a, int32_t b) { return key(a) < key(b); });
     // gram workgroups enough to fill the GPU once, two to a compute unit, each
     // with two tiles of columns at least: more even ones write more partials
-    // (128 rows: 36 KB each, the gradient's 100), which the recursion reads.
-    // Both passes with 8, 4, 2 and 1 workgroups a compute unit: the gradient of
-    // 288 bfloat16 blocks of 128 x 1536 420, 378, 361 and 356 us, 576 of them
-    // forward 227, 219, 218 and 218; the step of 48 79, 79, 76 and 79, of 1152
-    // 714, 728, 725 and 721.  The apply pass takes four times as many.
+    // (128 rows: 36 KB each, the gradient's 100), which the recursion reads;
+    // two a block, up to where even those are many rounds.  Both passes with 8,
+    // 4, 2 and 1 workgroups a compute unit: the gradient of 288 bfloat16 blocks
+    // of 128 x 1536 420, 378, 361 and 356 us, 576 of them forward 227, 219, 218
+    // and 218; the step of 48 79, 79, 76 and 79, of 1152 (two a block, one, one
+    // and one) 714, 728, 725 and 721; 576 binary32 blocks of 64 x 768 (four a
+    // block, two, one and one) 51, 49, 50 and 49, the step's Gram pass 78 with
+    // one and 72 us with two.  The apply pass takes four times as many.
     g.parts = parts_of(g, c.op, cus);
     const int64_t launch = (g.blocks + g.parts - 1) / g.parts;
-    const int64_t per = (2 * int64_t(cus) + launch - 1) / launch;
+    const int64_t per = std::max<int64_t>((2 * int64_t(cus) + launch - 1) / launch, launch < 8 * cus ? 2 : 1);
     const int64_t aper = (8 * int64_t(cus) + g.blocks - 1) / g.blocks;
     auto chunk = [&](int64_t n, int64_t split) {
       return int32_t(std::max<int64_t>(round_up((n + split - 1) / split, kc), 2 * kc));
