@@ -617,6 +617,15 @@ class _BlocksArgs:
         return got
 
 
+def _stacks(cls, first, *rest):
+    """The call's arguments: `first` if it is prebuilt (it holds all tensors), or built from the lists."""
+    if not isinstance(first, cls):
+        return cls(first, *rest)
+    if any(r is not None for r in rest):
+        raise ValueError(f"a {cls.__name__} holds every tensor of the call: build it with them")
+    return first
+
+
 def _on_device(device):
     return torch.cuda.device(device if device is not None else -1)
 
@@ -685,7 +694,7 @@ class StepBlocksArgs(_BlocksArgs):
 def muon_ns_blocks(x_in, x_out=None, *, ns_coeffs, ns_steps, ns_schedule=None, workspace=None, stream=None):
     """x_out[i][b] = Newton-Schulz orthogonalisation of block x_in[i][b], on
     lists of (blocks, rows, cols) stacks (or on a prebuilt NsBlocksArgs)."""
-    args = x_in if isinstance(x_in, NsBlocksArgs) else NsBlocksArgs(x_in, x_out)
+    args = _stacks(NsBlocksArgs, x_in, x_out)
     if args.count == 0:
         return
     sched, keep = _schedule(ns_schedule, ns_steps)
@@ -701,7 +710,7 @@ def muon_ns_blocks_vjp(x_in, grad_out=None, grad_in=None, *, ns_coeffs, ns_steps
                        stream=None):
     """grad_in[i] = gradient with respect to x_in[i] of <muon_ns_blocks(x_in[i]), grad_out[i]>
     (lists of stacks, or a prebuilt VjpBlocksArgs)."""
-    args = x_in if isinstance(x_in, VjpBlocksArgs) else VjpBlocksArgs(x_in, grad_out, grad_in)
+    args = _stacks(VjpBlocksArgs, x_in, grad_out, grad_in)
     if args.count == 0:
         return
     sched, keep = _schedule(ns_schedule, ns_steps)
@@ -719,7 +728,7 @@ def muon_step_blocks(params, grads=None, momenta=None, *, lr, beta, nesterov, ns
                      lr_per_stack=None, scale_per_stack=None, updates_out=None, workspace=None, stream=None):
     """One Muon step on lists of stacks (or on a prebuilt StepBlocksArgs), every
     block orthogonalised as a matrix of its own."""
-    args = params if isinstance(params, StepBlocksArgs) else StepBlocksArgs(params, grads, momenta, updates_out)
+    args = _stacks(StepBlocksArgs, params, grads, momenta, updates_out)
     if args.count == 0:
         return
     opt, keep = _step_options(args.count, ns_steps, ns_schedule, weight_decay, momentum_kind, lr_per_stack,

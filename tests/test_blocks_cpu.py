@@ -214,6 +214,9 @@ def test_binding_refusals():
     with pytest.raises(TypeError):
         mb.NsBlocksArgs([x.half()], [x])
     mb.muon_ns_blocks([], [], ns_coeffs=MUON, ns_steps=5)
+    with pytest.raises(ValueError, match="StepBlocksArgs holds every tensor"):
+        mb.muon_step_blocks(mb.StepBlocksArgs([], [], []), updates_out=[], lr=0.02, beta=0.95, nesterov=True,
+                            ns_coeffs=MUON, ns_steps=5)
 
 
 # ------------------------------------------------------------- oracle pins
