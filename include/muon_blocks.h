@@ -50,6 +50,8 @@
  *   - A block that holds a NaN or an infinity, or whose squared norm
  *     overflows binary32, gives NaN (its own block only).  A zero block gives
  *     zeros, and a zero gradient through the norm.
+ *     With respect to a block of norm above 2^60 the gradient, 2^-60 of the
+ *     cotangent and less, loses bits to the range of binary32.
  *   - Products over n run on the bfloat16 matrix cores on operands split into
  *     bfloat16 parts, with binary32 sums: bfloat16 inputs are one part
  *     (exact), binary32 values two parts (17 bits) where results are bfloat16
