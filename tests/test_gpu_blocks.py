@@ -14,7 +14,8 @@ the steps of max(1, |a|, ...), the growth of a small singular value:
   carried on with the square of the growth at the singular values 1/512 and
   less, 512^2 2^-24 = 2^-6 in the worst direction, and on a spectrum without
   a preferred direction 1/sqrt(m) of that in norm, at most 2^-6 / sqrt(m);
-  blocks of a few rows have no singular value that small.  TB = 2^-8 + 2^-9.
+  blocks of a few rows, where one direction counts, start again after a growth
+  of 48.  TB = 2^-8 + 2^-9.
 """
 import ctypes
 import sys
