@@ -288,7 +288,9 @@ __global__ __launch_bounds__(iterate_threads(MT, KIND), 2) void block_iterate_ke
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) tr += __shfl_xor(tr, d);
   const float norm = __builtin_sqrtf(tr);
-  const float inv = steps.first ? 1.f / (norm + NORM_EPS) : 1.f;
+  // an infinite ||x||^2 may be the sum of finite squares: A_0 = (G 0) 0 would
+  // be zero and P finite, so that the results came out as zeros
+  const float inv = !steps.first ? 1.f : tr < __builtin_inff() ? 1.f / (norm + NORM_EPS) : __builtin_nanf("");
 
   // A_j and P (and their tangents D and dP) live as operands; C (E) holds what
   // the last product gave, 2^ec (2^ee) times the matrix.  Value i of a lane is

@@ -915,3 +915,42 @@ def test_training_with_heads_and_the_rest():
         sl = np.s_[h * dim:(h + 1) * dim]
         _check_blocks(dv[None, sl], [orc.orthogonalise_vjp(qn[sl], yn[sl], _co(MUON), 5)],
                       _tol(F, dim, MUON, 5, grad=True), "gradient")
+
+
+# ------------------------------------------------- norms that leave the range
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("rows,cols", [(64, 768), (768, 128), (20, 30)])
+@pytest.mark.parametrize("coeffs,steps", [(MUON, 5), (MUON, 0), (CUBIC, 1)], ids=lambda v: str(v))
+def test_norm_that_overflows_gives_nan(rows, cols, dt, coeffs, steps):
+    """A block whose elements, and whose rows' squared norms, are finite while the sum of the squares is not; a block
+    with an infinite element.  Both are NaN throughout, after any number of steps; the blocks beside them are not."""
+    _announce(f"norm overflow {rows} {cols} {dt} {steps}")
+    gen = torch.Generator().manual_seed(rows + steps)
+    val = torch.randn(4, rows, cols, generator=gen)
+    # a row's (or column's) squared norm stays below 2^127 and that of the whole block is above 2^128
+    short, long = min(rows, cols), max(rows, cols)
+    e = int(np.floor((127 - np.log2(long)) / 2))
+    assert 2 * e + np.log2(long) < 127.5 and 2 * e + np.log2(rows * cols) > 128, "block too small for the case"
+    val[1] = torch.sign(val[1]) * 2.0 ** e
+    val[2, rows - 1, 0] = float("inf")
+    x, y = val.to(dt).cuda(), torch.randn(4, rows, cols, generator=gen).to(dt).cuda()
+    assert bool(x[1].isfinite().all())
+    out, dx = torch.empty_like(x), torch.empty_like(x)
+    _run_ns(x, out, coeffs, steps)
+    _run_vjp(x, y, dx, coeffs, steps)
+    # the step: U = g where the momentum starts at zero without Nesterov
+    w, m, o = torch.zeros_like(x), torch.zeros(4, rows, cols, device="cuda"), torch.zeros(4, rows, cols, device="cuda")
+    mb.muon_step_blocks([w], [x], [m], lr=f32(0.5), beta=0.5, nesterov=False, ns_coeffs=coeffs, ns_steps=steps,
+                        updates_out=[o])
+    torch.cuda.synchronize()
+    assert torch.equal(m, x.float())
+    for t in (out, dx, w, o):
+        assert bool(t[1].isnan().all()) and bool(t[2].isnan().all())
+    xs, ys = to_np(x), to_np(y)
+    for b in (0, 3):
+        ref = [orc.orthogonalise(xs[b], _co(coeffs), steps)]
+        _check_blocks(out[b:b + 1], ref, _tol(dt, short, coeffs, steps), "NS")
+        _check_blocks(o[b:b + 1], ref, _tol(dt, short, coeffs, steps), "step")
+        _check_blocks(dx[b:b + 1], [orc.orthogonalise_vjp(xs[b], ys[b], _co(coeffs), steps)],
+                      _tol(dt, short, coeffs, steps, grad=True), "gradient")
