@@ -202,7 +202,8 @@ muon_status check_descs(const Call& c) {
       st = check_view(i, "momentum", d, d.ld_mom, d.stride_mom, d.mom_dtype, true, true);
     if (st != MUON_OK) return st;
     total += d.blocks;
-    // a block has at most 2^16 / 128 gram workgroups (and fewer apply workgroups)
+    // the numbers of workgroups fit 31 bits: in a call of so many blocks one has
+    // one gram workgroup and at most 2^16 / (6 * 64) apply workgroups
     if (total > (int64_t(1) << 21))
       return fail(MUON_ERR_UNSUPPORTED, "more than 2^21 blocks in one call");
   }
@@ -647,6 +648,21 @@ void workgroups_at(const Group& g, int64_t b, int32_t& gram, int32_t& apply) {
   }
 }
 
+// Launches workgroups [first, end) of a pass over `tab` by launch(how many).
+// HIP takes fewer than 2^32 threads a launch (2^21 blocks of 1 x 5000 are 2^23
+// apply workgroups of 512): more run in slices, which the table's first
+// workgroup allows.
+template <class Launch>
+hipError_t in_slices(BlockTable& tab, int32_t first, int32_t end, Launch&& launch) {
+  constexpr int32_t SLICE = 1 << 22;
+  hipError_t e = hipSuccess;
+  for (int32_t at = first; at < end && e == hipSuccess; at += std::min(SLICE, end - at)) {
+    tab.first = at;
+    e = launch(std::min(SLICE, end - at));
+  }
+  return e;
+}
+
 // Enqueues phase `p` for blocks [b0, b1) on `stream`; every launch goes
 // through run(kernel class, launch).  `after`, where not null, is recorded
 // behind the gram pass.
@@ -669,9 +685,10 @@ hipError_t enqueue_phase(const Call& c, const Group& g, Phase& p, char* ws, int6
   int32_t g0, g1, a0, a1;
   workgroups_at(g, b0, g0, a0);
   workgroups_at(g, b1, g1, a1);
-  p.tab.first = g0;
   hipError_t e = run(p.kind == BK_STEP ? MUON_KC_MOMENTUM : MUON_KC_GRAM, [&] {
-    return launch_block_gram(g.mt, p.pl, p.kind, p.xbf, p.tab, g1 - g0, parts, mom, stream);
+    return in_slices(p.tab, g0, g1, [&](int32_t wgs) {
+      return launch_block_gram(g.mt, p.pl, p.kind, p.xbf, p.tab, wgs, parts, mom, stream);
+    });
   });
   if (e == hipSuccess && after) e = hipEventRecord(after, stream);
   if (e != hipSuccess) return e;
@@ -681,9 +698,10 @@ hipError_t enqueue_phase(const Call& c, const Group& g, Phase& p, char* ws, int6
                                 p.steps, stream);
   });
   if (e != hipSuccess) return e;
-  p.tab.first = a0;
   return run(MUON_KC_COMBINE, [&] {
-    return launch_block_apply(g.mt, p.pl, pp, p.kind, p.xbf, p.tab, a1 - a0, P, T, mom, stream);
+    return in_slices(p.tab, a0, a1, [&](int32_t wgs) {
+      return launch_block_apply(g.mt, p.pl, pp, p.kind, p.xbf, p.tab, wgs, P, T, mom, stream);
+    });
   });
 }
 

@@ -954,3 +954,28 @@ def test_norm_that_overflows_gives_nan(rows, cols, dt, coeffs, steps):
         _check_blocks(o[b:b + 1], ref, _tol(dt, short, coeffs, steps), "step")
         _check_blocks(dx[b:b + 1], [orc.orthogonalise_vjp(xs[b], ys[b], _co(coeffs), steps)],
                       _tol(dt, short, coeffs, steps, grad=True), "gradient")
+
+
+def test_more_threads_than_a_launch_takes():
+    """2^21 blocks of 1 x 5000 take 2^23 apply workgroups of 512 threads, 2^32 in all: they run in slices.  Block b reads
+    elements b .. b + 4999 of one buffer, and a row's result is a multiple of the row."""
+    n, blocks = 5000, 1 << 20
+    _announce(f"2 x {blocks} blocks of 1 x {n}")
+    gen = torch.Generator().manual_seed(61)
+    base = torch.randn(2 * blocks + n, generator=gen).to(BF).cuda()
+    xs = [base[k * blocks:].as_strided((blocks, 1, n), (1, n, 1)) for k in range(2)]
+    outs = [torch.empty(blocks, 1, n, dtype=BF, device="cuda") for _ in range(2)]
+    mb.muon_ns_blocks(xs, outs, ns_coeffs=CUBIC, ns_steps=3)
+    s = 1.0
+    for a, b, c in orc.schedule(_co(CUBIC), 3):
+        s = s * (a + b * s * s + c * s ** 4)
+    worst, chunk = 0.0, 1 << 14
+    for x, out in zip(xs, outs):
+        for b in range(0, blocks, chunk):
+            u, o = x[b:b + chunk, 0].double(), out[b:b + chunk, 0].double()
+            o -= u * (s / u.norm(dim=1, keepdim=True))
+            worst = max(worst, (o.norm(dim=1).max() / s).item())
+    del outs, out, o, u
+    mb.muon_release_workspace()
+    torch.cuda.empty_cache()
+    assert worst <= TB
