@@ -45,6 +45,10 @@
  *     share elements: stride >= (rows - 1) ld + cols, or side by side in the
  *     same rows: stride >= cols and (blocks - 1) stride + cols <= ld.
  *     Read-only tensors take any stride >= 0 (0: one block for all).
+ *   - Blocks of one tensor may lie between those of another (query, key and
+ *     value heads in turns in one weight).  Where one of the two is written,
+ *     such tensors need equal strides, or equal row strides and columns apart;
+ *     others whose address ranges meet are ALIAS.
  *   - Elements outside the blocks (row padding, other columns) are neither
  *     read nor written.
  *   - A block that holds a NaN or an infinity, or whose squared norm

@@ -88,11 +88,12 @@ struct Call {
 
 // ------------------------------------------------------------- validation
 
-// Bytes a tensor of blocks may touch, and the grid its rows lie on: rows
-// start `row` bytes apart from the first and are `win` bytes long (row = 0:
-// no such grid).
+// Bytes a tensor of blocks may touch: runs of `run` bytes, at lo + i bs + r rs
+// for i < blocks and r < rows; and the grid its rows lie on: rows start `row`
+// bytes apart from the first and are `win` bytes long (row = 0: no such grid).
 struct Region {
   uintptr_t lo, hi;
+  int64_t blocks, bs, rows, rs, run;
   uint64_t row, win;
   bool written;
   int32_t idx;
@@ -104,6 +105,11 @@ Region region_of(const void* p, const muon_block_desc& d, int64_t ld, int64_t st
   Region r;
   r.lo = reinterpret_cast<uintptr_t>(p);
   r.hi = r.lo + uint64_t((d.blocks - 1) * stride + (d.rows - 1) * ld + d.cols) * uint64_t(esz);
+  r.blocks = stride > 0 ? d.blocks : 1;
+  r.bs = stride * esz;
+  r.rows = d.rows;
+  r.rs = ld * esz;
+  r.run = d.cols * esz;
   r.row = r.win = 0;
   if (d.blocks == 1 || stride % ld == 0) {
     r.row = uint64_t(ld) * esz;
@@ -118,8 +124,39 @@ Region region_of(const void* p, const muon_block_desc& d, int64_t ld, int64_t st
   return r;
 }
 
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0 ? 1 : 0); }  // b > 0
+
+// Whether two tensors of equal strides share a byte, exactly: whether their
+// distance is x bs + y rs + z with x, y and z among the differences of two
+// block numbers, row numbers and places in a run.  A stride that one of them
+// does not use (one block, one row) is the other's.  Of the larger stride's
+// differences few can be met where blocks lie apart or side by side; true
+// where strides differ or many would have to be tried (read-only tensors).
+bool runs_meet(const Region& a, const Region& b) {
+  if ((a.blocks > 1 && b.blocks > 1 && a.bs != b.bs) || (a.rows > 1 && b.rows > 1 && a.rs != b.rs)) return true;
+  struct Axis {
+    int64_t step, lo, hi;  // differences lo .. hi, `step` bytes each
+  };
+  Axis o = {a.blocks > 1 ? a.bs : b.bs, 1 - b.blocks, a.blocks - 1};
+  Axis i = {a.rows > 1 ? a.rs : b.rs, 1 - b.rows, a.rows - 1};
+  for (Axis* x : {&o, &i})
+    if (x->lo == x->hi || x->step == 0) *x = {1, 0, 0};
+  if (o.step < i.step) std::swap(o, i);
+  const int64_t d = int64_t(b.lo - a.lo), zlo = 1 - b.run, zhi = a.run - 1;
+  const int64_t x0 = std::max(o.lo, -floor_div(i.hi * i.step + zhi - d, o.step));
+  const int64_t x1 = std::min(o.hi, floor_div(d - i.lo * i.step - zlo, o.step));
+  if (x1 - x0 > 64) return true;
+  for (int64_t x = x0; x <= x1; ++x) {
+    const int64_t e = d - x * o.step;  // y step + z
+    const int64_t y0 = std::max(i.lo, -floor_div(zhi - e, i.step)), y1 = std::min(i.hi, floor_div(e - zlo, i.step));
+    if (y0 <= y1) return true;
+  }
+  return false;
+}
+
 bool share_bytes(const Region& a, const Region& b) {  // a.lo <= b.lo
   if (b.lo >= a.hi) return false;
+  if (!runs_meet(a, b)) return false;
   if (a.row == 0 || a.row != b.row) return true;
   // rows on one grid: disjoint if the windows are
   const uint64_t d = (b.lo - a.lo) % a.row;
@@ -275,7 +312,7 @@ muon_status validate(const Call& c) {
     if (reinterpret_cast<uintptr_t>(c.ws) % 256 != 0)
       return fail(MUON_ERR_UNSUPPORTED, "workspace is not aligned to 256 bytes");
     const uintptr_t lo = reinterpret_cast<uintptr_t>(c.ws);
-    reg.push_back({lo, lo + c.ws_bytes, 0, 0, true, -1, "workspace"});
+    reg.push_back({lo, lo + c.ws_bytes, 1, 0, 1, 0, int64_t(c.ws_bytes), 0, 0, true, -1, "workspace"});
   }
   return check_alias(reg);
 }

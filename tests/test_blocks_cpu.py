@@ -219,6 +219,92 @@ def test_binding_refusals():
                             ns_coeffs=MUON, ns_steps=5)
 
 
+def _touched(d, base, esz):
+    """Bytes that the blocks of a written tensor cover."""
+    return {base + esz * (b * d.stride_param + r * d.ld_param + c) + k
+            for b in range(d.blocks) for r in range(d.rows) for c in range(d.cols) for k in range(esz)}
+
+
+def _two_written(L, d0, d1, off, esz=2):
+    """Status of an NS call whose two stacks' outputs start `off` elements apart."""
+    g0, g1 = BASE + (8 << 40), BASE + (9 << 40)
+    return _call(L, mb.BLOCKS_NS, [d0, d1], ptrs=[(BASE, g0, 0), (BASE + esz * off, g1, 0)])
+
+
+def test_interleaved_stacks(L):
+    """Stacks whose blocks lie between each other's: parts of one weight kept per head, (heads, 3, dim, width) or
+    (width, heads, 3, dim), and the even and odd heads of one."""
+    if torch.cuda.is_available():
+        pytest.skip("would launch on made-up addresses")
+    heads, dim, width = 12, 64, 768
+    cases = [
+        # blocks of rows: q, k and v of each head, one after another
+        (_desc(heads, dim, width, ld=width, stride=3 * dim * width), dim * width, 2 * dim * width),
+        # blocks of columns, (width, heads, 3, dim)
+        (_desc(heads, width, dim, ld=3 * heads * dim, stride=3 * dim), dim, 2 * dim),
+        # even and odd heads
+        (_desc(heads // 2, dim, width, ld=width, stride=2 * dim * width), dim * width, dim * width),
+        (_desc(heads // 2, width, dim, ld=heads * dim, stride=2 * dim), dim, dim),
+        # padded rows, of which one head's are between another's: columns 0-99 and 100-199 of 256
+        (_desc(heads, dim, 100, ld=256, stride=2 * dim * 256), 100, dim * 256),
+    ]
+    for d, lo, hi in cases:
+        for off in (lo, hi):
+            for first, second in ((0, off), (off, 0)):
+                assert _two_written(L, d, d, second - first) == mb.MUON_ERR_HIP, mb.muon_last_error()
+        # an element before the first place that is free, and one behind the last
+        assert _two_written(L, d, d, lo - 1) == mb.MUON_ERR_ALIAS
+        assert _two_written(L, d, d, 1 - lo) == mb.MUON_ERR_ALIAS
+        assert _two_written(L, d, d, 0) == mb.MUON_ERR_ALIAS
+    d, lo, hi = cases[0]
+    assert _two_written(L, d, d, hi + 1) == mb.MUON_ERR_ALIAS
+    # three parts in one call of every operator
+    st = [_desc(heads, dim, width, ld=width, stride=3 * dim * width) for _ in range(3)]
+    ptrs = [tuple(BASE + (k << 40) + e * i * dim * width for k, e in ((0, 2), (1, 2), (2, 4))) for i in range(3)]
+    for op in OPS:
+        assert _call(L, op, st, ptrs=ptrs) == mb.MUON_ERR_HIP, mb.muon_last_error()
+
+
+def test_overlap_rule_against_sets_of_bytes(L):
+    """Random pairs of small written stacks: a pair that shares a byte is refused, whatever its strides; one with equal
+    strides is refused for that alone."""
+    if torch.cuda.is_available():
+        pytest.skip("would launch on made-up addresses")
+    import random
+    rng = random.Random(5)
+    seen = {(beside, overlap): 0 for beside in (True, False) for overlap in (True, False)}
+    for _ in range(4000):
+        descs = []
+        rows, cols, ld = rng.randint(1, 4), rng.randint(1, 4), rng.randint(4, 16)
+        beside = rng.random() < 0.5
+        blocks = rng.randint(1, max(1, ld // cols)) if beside else rng.randint(1, 4)
+        stride = rng.randint(cols, max(cols, (ld - cols) // max(blocks - 1, 1))) if beside else \
+            rng.randint((rows - 1) * ld + cols, 3 * rows * ld)
+        for k in range(2):
+            # the second stack differs in its extents alone, or (every fourth) in its strides too
+            r, c, b = (rows, cols, blocks) if k == 0 else (rng.randint(1, rows), rng.randint(1, cols), rng.randint(1, blocks))
+            same = k == 0 or rng.random() < 0.75
+            descs.append(_desc(b, r, c, ld=ld if same else ld + 4, stride=stride if same else stride + 5 * (ld + 4),
+                               pdt=mb.DTYPE_F32, gdt=mb.DTYPE_F32))
+        if any(d.blocks > 1 and not (d.stride_param >= (d.rows - 1) * d.ld_param + d.cols or
+                                     (d.stride_param >= d.cols and (d.blocks - 1) * d.stride_param + d.cols <= d.ld_param))
+               for d in descs):
+            continue  # a stack that overlaps itself
+        off = rng.randint(-3 * ld, 3 * ld)
+        for d in descs:
+            d.stride_grad, d.ld_grad = 0, d.cols
+        overlap = bool(_touched(descs[0], 0, 4) & _touched(descs[1], 4 * off, 4))
+        got = _two_written(L, *descs, off, esz=4)
+        assert got in (mb.MUON_ERR_ALIAS, mb.MUON_ERR_HIP)
+        if overlap:
+            assert got == mb.MUON_ERR_ALIAS, ([(d.blocks, d.rows, d.cols, d.ld_param, d.stride_param) for d in descs], off)
+        a, b = descs
+        if (a.ld_param, a.stride_param) == (b.ld_param, b.stride_param):
+            seen[beside, overlap] += 1
+            assert got == (mb.MUON_ERR_ALIAS if overlap else mb.MUON_ERR_HIP), off
+    assert min(seen.values()) >= 100
+
+
 # ------------------------------------------------------------- oracle pins
 
 def _np_rng(seed):

@@ -979,3 +979,33 @@ def test_more_threads_than_a_launch_takes():
     mb.muon_release_workspace()
     torch.cuda.empty_cache()
     assert worst <= TB
+
+
+@pytest.mark.parametrize("kind", ["rows", "cols"])
+@pytest.mark.parametrize("dt", [BF, F])
+def test_parts_of_one_weight_kept_per_head(dt, kind):
+    """Query, key and value of each head one after another in one weight, as three stacks of a call: the bits of the same
+    blocks in tensors of their own."""
+    _announce(f"fused weight {kind} {dt}")
+    heads, dim, width = 5, 24, 70
+    gen = torch.Generator().manual_seed(71)
+    shape = (heads, 3, dim, width) if kind == "rows" else (width, heads, 3, dim)
+
+    def parts(t):
+        return list(t.unbind(1)) if kind == "rows" else [t[:, :, k].transpose(0, 1) for k in range(3)]
+
+    w, g = (torch.randn(shape, generator=gen).to(dt).cuda() for _ in range(2))
+    m = torch.randn(shape, generator=gen).cuda()
+    own = [[p.contiguous() for p in parts(t)] for t in (w, g, m)]
+    hp = dict(lr=f32(0.02), beta=f32(0.95), nesterov=True, ns_coeffs=MUON, ns_steps=5)
+    mb.muon_step_blocks(parts(w), parts(g), parts(m), **hp)
+    mb.muon_step_blocks(*own, **hp)
+    out, dx = torch.zeros_like(w), torch.zeros_like(w)
+    ref, refd = ([torch.zeros_like(p) for p in own[0]] for _ in range(2))
+    mb.muon_ns_blocks(parts(g), parts(out), ns_coeffs=MUON, ns_steps=5)
+    mb.muon_ns_blocks_vjp(parts(g), parts(w), parts(dx), ns_coeffs=MUON, ns_steps=5)
+    mb.muon_ns_blocks(own[1], ref, ns_coeffs=MUON, ns_steps=5)
+    mb.muon_ns_blocks_vjp(own[1], own[0], refd, ns_coeffs=MUON, ns_steps=5)
+    torch.cuda.synchronize()
+    for t, r in ((w, own[0]), (m, own[2]), (out, ref), (dx, refd)):
+        assert all(np.array_equal(_bits(a), _bits(b)) for a, b in zip(parts(t), r))
