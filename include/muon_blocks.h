@@ -94,7 +94,7 @@ extern "C" {
  * group that a call does not name is ignored.  reserved: 0.                 */
 typedef struct muon_block_desc {
   int64_t blocks, rows, cols;
-  int64_t ld_param, ld_grad, ld_mom;             /* row strides, >= cols     */
+  int64_t ld_param, ld_grad, ld_mom;             /* row strides, >= cols; any where rows = 1 */
   int64_t stride_param, stride_grad, stride_mom; /* from block to block      */
   int32_t param_dtype, grad_dtype, mom_dtype;
   int32_t reserved;

@@ -590,8 +590,7 @@ class _BlocksArgs:
                     raise ValueError(f"stack {i}: {name} has shape {tuple(t.shape)}, not {shape}")
                 if t.stride(2) != 1 and t.shape[2] > 1:
                     raise ValueError(f"{name}[{i}] must have unit column stride")
-                ld = max(int(t.stride(1)), int(t.shape[2])) if t.shape[1] == 1 else int(t.stride(1))
-                setattr(d, f"ld_{field}", ld)
+                setattr(d, f"ld_{field}", int(t.stride(1)))
                 setattr(d, f"stride_{field}", int(t.stride(0)) if t.shape[0] > 1 else 0)
                 setattr(d, f"{field}_dtype", dtype_code(t.dtype))
                 if not t.is_cuda:

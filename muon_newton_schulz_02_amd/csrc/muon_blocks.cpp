@@ -67,6 +67,9 @@ muon_status fail(muon_status s, const char* fmt, ...) {
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+// A row stride as the descriptor gives it, or of blocks of one row, where it
+// may be anything, their length.
+int64_t row_stride(const muon_block_desc& d, int64_t ld) { return d.rows == 1 ? d.cols : ld; }
 int esize(int32_t dt) { return dt == MUON_DTYPE_BF16 ? 2 : 4; }
 
 struct Call {
@@ -102,6 +105,7 @@ struct Region {
 
 Region region_of(const void* p, const muon_block_desc& d, int64_t ld, int64_t stride, int esz, bool written,
                  int32_t idx, const char* what) {
+  ld = row_stride(d, ld);
   Region r;
   r.lo = reinterpret_cast<uintptr_t>(p);
   r.hi = r.lo + uint64_t((d.blocks - 1) * stride + (d.rows - 1) * ld + d.cols) * uint64_t(esz);
@@ -176,6 +180,7 @@ muon_status check_view(int32_t i, const char* what, const muon_block_desc& d, in
                        int32_t dtype, bool f32_only, bool written) {
   if (dtype != MUON_DTYPE_F32 && (f32_only || dtype != MUON_DTYPE_BF16))
     return fail(MUON_ERR_UNSUPPORTED, "stack %d: %s dtype %d is not %s", i, what, dtype, f32_only ? "F32" : "F32 or BF16");
+  ld = row_stride(d, ld);
   if (ld < d.cols || ld > BLOCK_MAX_LD)
     return fail(ld < d.cols ? MUON_ERR_INVALID_ARGUMENT : MUON_ERR_UNSUPPORTED,
                 "stack %d: %s row stride %lld out of [cols = %lld, 2^21]", i, what, (long long)ld, (long long)d.cols);
@@ -547,7 +552,7 @@ hipError_t group_phases(const Call& c, const Group& g, char* ws, std::vector<Pha
     const muon_block_desc& d = c.stacks[i];
     if (buf < 0) {
       s.x = c.x[i];
-      s.x_ld = d.ld_grad;
+      s.x_ld = row_stride(d, d.ld_grad);
       s.x_bs = d.stride_grad;
       if (g.xbf) s.flags |= BF_X_BF16;
     } else {
@@ -561,7 +566,7 @@ hipError_t group_phases(const Call& c, const Group& g, char* ws, std::vector<Pha
     const muon_block_desc& d = c.stacks[i];
     if (buf < 0) {
       s.y = c.y[i];
-      s.y_ld = d.ld_mom;
+      s.y_ld = row_stride(d, d.ld_mom);
       s.y_bs = d.stride_mom;
       if (d.mom_dtype == MUON_DTYPE_BF16) s.flags |= BF_Y_BF16;
     } else {
@@ -575,7 +580,7 @@ hipError_t group_phases(const Call& c, const Group& g, char* ws, std::vector<Pha
     const muon_block_desc& d = c.stacks[i];
     if (buf < 0) {
       s.out = c.out[i];
-      s.out_ld = d.ld_param;
+      s.out_ld = row_stride(d, d.ld_param);
       s.out_bs = d.stride_param;
       if (!g.f32) s.flags |= BF_OUT_BF16;
       if (step) {

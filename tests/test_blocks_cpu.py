@@ -305,6 +305,23 @@ def test_overlap_rule_against_sets_of_bytes(L):
     assert min(seen.values()) >= 100
 
 
+@pytest.mark.parametrize("op", OPS)
+def test_row_stride_of_single_rows(L, op):
+    """Blocks of one row have no next row: their row stride is not looked at."""
+    if torch.cuda.is_available():
+        pytest.skip("would launch on made-up addresses")
+    for ld in (0, 1, 95, (1 << 21) + 1, 1 << 50):
+        d = _desc(blocks=3, rows=1, cols=96, ld=ld, stride=96)
+        assert _call(L, op, [d]) == mb.MUON_ERR_HIP, mb.muon_last_error()
+        # nor by the overlap rules: next to each other, and one element into each other
+        (p, g, m), (_, g1, m1) = _three(), _three(1)
+        for off, status in ((3 * 96, mb.MUON_ERR_HIP), (3 * 96 - 1, mb.MUON_ERR_ALIAS)):
+            assert _call(L, op, [d, d], ptrs=[(p, g, m), (p + 2 * off, g1, m1)]) == status
+        # blocks that share elements still do
+        assert _call(L, op, [_desc(blocks=3, rows=1, cols=96, ld=ld, stride=95)]) == mb.MUON_ERR_ALIAS
+    assert _call(L, op, [_desc(blocks=3, rows=2, cols=96, ld=95, stride=192)]) == mb.MUON_ERR_INVALID_ARGUMENT
+
+
 # ------------------------------------------------------------- oracle pins
 
 def _np_rng(seed):

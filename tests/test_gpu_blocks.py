@@ -1009,3 +1009,23 @@ def test_parts_of_one_weight_kept_per_head(dt, kind):
     torch.cuda.synchronize()
     for t, r in ((w, own[0]), (m, own[2]), (out, ref), (dx, refd)):
         assert all(np.array_equal(_bits(a), _bits(b)) for a, b in zip(parts(t), r))
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+def test_single_rows_of_any_row_stride(dt):
+    """(blocks, 1, cols) views whose row stride, never used, is 0 or the whole matrix."""
+    _announce(f"single rows {dt}")
+    gen = torch.Generator().manual_seed(72)
+    n, cols = 3000, 750  # 2.25 million elements, past the largest row stride
+    x, y, out, dx = (torch.randn(n, cols, generator=gen).to(dt).cuda() for _ in range(4))
+    views = [t.view(1, n, cols).transpose(0, 1) for t in (x, y, out, dx)]
+    assert views[0].stride(1) > 2 ** 21
+    _run_ns(views[0], views[2], CUBIC, 3)
+    _run_vjp(views[0], views[1], views[3], CUBIC, 3)
+    ref, refd = torch.empty_like(x), torch.empty_like(x)
+    _run_ns(x.as_strided((n, 1, cols), (cols, 0, 1)), ref.view(n, 1, cols), CUBIC, 3)
+    _run_vjp(x.view(n, 1, cols), y.view(n, 1, cols), refd.as_strided((n, 1, cols), (cols, 1, 1)), CUBIC, 3)
+    torch.cuda.synchronize()
+    assert np.array_equal(_bits(out), _bits(ref)) and np.array_equal(_bits(dx), _bits(refd))
+    _check_blocks(out[:5, None], [orc.orthogonalise(v[None], _co(CUBIC), 3) for v in to_np(x[:5])],
+                  _tol(dt, 1, CUBIC, 3), "NS")
