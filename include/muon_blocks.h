@@ -69,15 +69,15 @@
  *     use it run one after another in the order they were made, whatever
  *     their streams.  With a workspace of the caller's (256-byte aligned
  *     device memory of muon_blocks_workspace_bytes bytes) the call only
- *     launches kernels: calls or graphs with different workspaces may
- *     overlap; those that share one must not.
+ *     launches kernels, on `stream`: calls or graphs with different workspaces
+ *     may overlap; those that share one must not.
  *   - Capture: a call on a capturing stream needs a workspace of the caller's
  *     (UNSUPPORTED without) and records kernels on `stream` only.  Pointers,
  *     sizes, coefficients, rates and decay are those of the capture.
- *   - Streams: a call that is not captured may run parts of a large group of
- *     blocks on further streams of the library's (up to two a device, at the
- *     default priority).  They start after what `stream` held before the
- *     call, and `stream` goes on after them.
+ *   - Streams: a call with the library's workspace may run parts of a large
+ *     group of blocks on further streams of the library's (up to two a device,
+ *     at the default priority).  They start after what `stream` held before
+ *     the call, and `stream` goes on after them.
  */
 #ifndef MUON_MI355X_BLOCKS_H
 #define MUON_MI355X_BLOCKS_H

@@ -368,7 +368,7 @@ struct Group {
   int64_t blocks = 0;
   std::vector<Stage> stages;
   int32_t gram_wgs = 0, apply_wgs = 0;
-  int parts = 1;                    // of an eager call
+  int parts = 1;                    // of a call with the library's workspace
   std::vector<BlockStack> base;     // sizes and splits; views are filled per stage
   std::vector<size_t> stage_off;    // per member: byte offset of its binary32 copy in a stage buffer
   size_t stage_bytes = 0;           // one stage buffer
@@ -377,7 +377,8 @@ struct Group {
   size_t o_tab = 0, o_part = 0, o_p = 0, o_t = 0, o_scr = 0, o_stage = 0, end = 0;
 };
 
-// Parts of a group that an eager call runs on streams of their own.  Measured,
+// Parts of a group that a call with the library's workspace runs on streams of
+// their own.  Measured,
 // time on one stream over time in two, three and four parts:
 //  - several stages (binary32): the gradient 130 blocks 0.97 to 1.04, 216 to
 //    600 1.03 to 1.20 in two; forward at 128 rows 130 to 200 0.97 to 1.01, 300
@@ -816,11 +817,14 @@ bool side_streams(BlockDevice& bd, int parts) {
 // Enqueues one group.  The recursion keeps the matrix cores busy and the other
 // two passes the memory, so a group may be cut into parts: each but the first
 // runs on a stream of its own, behind the gram pass of the part before, and
-// one part's recursion runs beside another's passes over memory.
+// one part's recursion runs beside another's passes over memory.  The streams
+// are the device's: only calls with the library's workspace use them, which
+// run one after another anyway.  A call with a workspace of its own would wait
+// behind whatever an earlier call's parts still wait for.
 hipError_t enqueue_group(const Call& c, const Group& g, char* ws, BlockDevice& bd, bool capturing) {
   std::vector<Phase> phases;
   hipError_t e = group_phases(c, g, ws, phases);
-  const bool split = g.parts > 1 && !capturing && !api_timing() && side_streams(bd, g.parts);
+  const bool split = g.parts > 1 && !c.ws && !api_timing() && side_streams(bd, g.parts);
   const int parts = split ? g.parts : 1;
   auto run = [&](int kc, auto&& launch) -> hipError_t {
     return capturing ? launch() : api_timed(kc, c.stream, launch);

@@ -1029,3 +1029,40 @@ def test_single_rows_of_any_row_stride(dt):
     assert np.array_equal(_bits(out), _bits(ref)) and np.array_equal(_bits(dx), _bits(refd))
     _check_blocks(out[:5, None], [orc.orthogonalise(v[None], _co(CUBIC), 3) for v in to_np(x[:5])],
                   _tol(dt, 1, CUBIC, 3), "NS")
+
+
+def test_a_held_back_call_holds_no_other():
+    """A large call on a stream that waits for a long time (one spinning thread), and another on a stream of its own, each
+    with a workspace of its own: the second ends before the wait does.  Streams may share a hardware queue, whose order
+    they then keep, so one of four other streams has to show it."""
+    _announce("held back")
+    (a, call_a, _, _), (b, call_b, out_b, _) = (_parted("ns", F, [(600, 128, 256)], seed) for seed in (81, 82))
+    ws_a, ws_b = _workspace(a), _workspace(b)
+    streams = [torch.cuda.Stream() for _ in range(5)]
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    call_b(workspace=ws_b)
+    torch.cuda._sleep(1000)
+    torch.cuda.synchronize()
+    ref = [_bits(t) for t in out_b]
+    ev[0].record()
+    torch.cuda._sleep(1_000_000)
+    ev[1].record()
+    torch.cuda.synchronize()
+    cycles = int(1_000_000 * 100 / ev[0].elapsed_time(ev[1]))  # 100 ms
+    before = 0
+    for s in streams[1:]:
+        for t in out_b:
+            t.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(streams[0]):
+            torch.cuda._sleep(cycles)
+        waited, done_b = torch.cuda.Event(), torch.cuda.Event()
+        waited.record(streams[0])
+        call_a(workspace=ws_a, stream=streams[0])
+        call_b(workspace=ws_b, stream=s)
+        done_b.record(s)
+        done_b.synchronize()
+        before += not waited.query()
+        torch.cuda.synchronize()
+        assert all(np.array_equal(_bits(t), r) for t, r in zip(out_b, ref))
+    assert before > 0
