@@ -902,6 +902,9 @@ muon_status run_call(const Call& c) {
     ws = reinterpret_cast<char*>(bd->ws);
   }
 
+  // an error that an earlier call of the thread's left would be taken for one of
+  // the first launch, whose kernel runs all the same
+  (void)hipGetLastError();
   hipError_t e = hipSuccess;
   for (const Group& g : groups) {
     e = enqueue_group(c, g, ws, *bd, capturing);

@@ -1066,3 +1066,23 @@ def test_a_held_back_call_holds_no_other():
         torch.cuda.synchronize()
         assert all(np.array_equal(_bits(t), r) for t, r in zip(out_b, ref))
     assert before > 0
+
+
+def test_an_earlier_error_is_not_this_call_s():
+    """HIP keeps a thread's last error until it is asked for: a refused call before (a device that is not there) is not
+    taken for a failed launch."""
+    _announce("earlier error")
+    hip = ctypes.CDLL("libamdhip64.so")
+    lr = f32(0.02)
+    (w, g, m, _, _), = _step_case((4, 40, 96, "dense", 0), BF, BF, 91)
+    w2, m2 = w.clone(), m.clone()
+    outs = [torch.full((4, 40, 96), float("nan"), device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for t in ((w, m, outs[0]), (w2, m2, outs[1])):
+        if t[0] is w:
+            assert hip.hipSetDevice(999) != 0
+        mb.muon_step_blocks([t[0]], [g], [t[1]], lr=lr, beta=0.95, nesterov=True, ns_coeffs=MUON, ns_steps=5,
+                            updates_out=[t[2]])
+    torch.cuda.synchronize()
+    for a, b in ((w, w2), (m, m2), (outs[0], outs[1])):
+        assert np.array_equal(_bits(a), _bits(b))
