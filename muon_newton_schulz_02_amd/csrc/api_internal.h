@@ -12,8 +12,9 @@
 
 namespace muon {
 
-// Sets the calling thread's last error and returns `s`.
-muon_status api_fail(muon_status s, const char* text);
+// Sets the calling thread's last error (none if there is no memory for the
+// text) and returns `s`.
+muon_status api_fail(muon_status s, const char* text) noexcept;
 void api_clear_error();
 std::mutex& api_mutex();
 // hipMalloc behind MUON_FAULT_ALLOC.

@@ -1774,7 +1774,14 @@ muon_status run_adamw(const AdamwCall& c) {
 
 }  // namespace
 
-muon_status api_fail(muon_status s, const char* text) { return fail(s, "%s", text); }
+muon_status api_fail(muon_status s, const char* text) noexcept {
+  try {
+    return fail(s, "%s", text);
+  } catch (...) {  // no memory for the text
+    t_last_error.clear();
+    return s;
+  }
+}
 void api_clear_error() { t_last_error.clear(); }
 std::mutex& api_mutex() { return g_mu; }
 hipError_t api_device_alloc(void** p, size_t bytes) { return device_alloc(p, bytes); }

@@ -322,6 +322,21 @@ def test_row_stride_of_single_rows(L, op):
     assert _call(L, op, [_desc(blocks=3, rows=2, cols=96, ld=95, stride=192)]) == mb.MUON_ERR_INVALID_ARGUMENT
 
 
+def test_no_exception_leaves_a_c_entry(L, tmp_path):
+    """Without memory for the error's text a call still ends with its status (host_plan/blocks_nomem.cpp)."""
+    import shutil
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("needs g++")
+    here = os.path.dirname(os.path.abspath(__file__))
+    exe = str(tmp_path / "blocks_nomem")
+    r = subprocess.run([gxx, "-std=c++17", "-O1", "-Wall", "-rdynamic", "-I", os.path.dirname(HEADER), "-o", exe,
+                        os.path.join(here, "host_plan", "blocks_nomem.cpp"), "-ldl"], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
+    r = subprocess.run([exe, mb.LIB_PATH], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "54 calls, 0 threw" in r.stdout, r.stdout + r.stderr[-2000:]
+
+
 # ------------------------------------------------------------- oracle pins
 
 def _np_rng(seed):
