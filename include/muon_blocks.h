@@ -28,14 +28,24 @@
  * square the condition number, so the recursion starts again from the Gram
  * matrix of the current iterate (one more pass over the block) before the
  * steps since the last one multiply small singular values by more than a
- * limit: 512 where results are bfloat16 (five steps of the usual quintic,
- * 3.4445^5 = 485, are one pass), 48 where they are binary32.  Blocks of up to
- * four rows, and of up to 16 with n < 4 m, take 48 for bfloat16 results; they
- * and blocks with n < 2 m take 12 for binary32 ones, and their gradient a
- * Gram matrix for every step.  Measured against float64: bfloat16 results are
- * off by their rounding and up to 3e-3 more (4 x 64, one singular value 100
- * times the others; 1e-3 from 16 rows on), binary32 results about as much as
- * the same iteration carried out in binary32 (1e-6 to 1e-5).
+ * limit.  With g the growth by all steps (1.5 a cubic step, 3.4445 one of the
+ * usual quintic):
+ *   - bfloat16 results: 512, so that five quintic steps (g = 485) are one pass;
+ *     48 for blocks of up to four rows, and of up to 16 with n < 4 m;
+ *   - binary32 results: sqrt(3.5 g), at least 12 and at most 48 (five quintic
+ *     steps 3 + 2, eight cubic ones 4 + 4); 12 where g is more than 512, and for
+ *     blocks of few rows as above or with n < 2 m, whose gradient takes a Gram
+ *     matrix for every step.
+ * There are as few stages as that allows, as even as can be.  Measured against
+ * float64:
+ *   - bfloat16 results and gradients are off by their rounding and up to 3e-3
+ *     more (one singular value 100 to 3000 times the others); where x is
+ *     binary32 and of rank one alone, by 2^-18 g;
+ *   - binary32 ones by up to four times what the same iteration carried out in
+ *     binary32 is, or by 5e-6 where that is more (most 1e-6 to 1e-5; rank one
+ *     alone 2^-24 g, and so is that iteration).  Five quintic steps leave more
+ *     where one singular value is about 20 times the others, 2e-5 to 4e-5, and
+ *     gradients there and up to 50 times, as much; ones alone up to 6e-5.
  *
  * Conventions are those of muon.h (device memory of the current device,
  * strides in elements, validation before anything is enqueued, no

@@ -33,14 +33,26 @@ constexpr int64_t MAX_STRIDE = int64_t(1) << 40;
 
 // Largest growth of small singular values between two Gram matrices.  The
 // Gram matrix holds eigenvalues down to about 2^-24 of its trace, and the
-// recursion carries its error on with the square of that growth; measured
-// against float64 over spectra from flat to i^-3 and rank-16 spikes, five
-// quintic steps: 512 (one stage) 1e-4 to 6e-4, 48 (3 + 2 steps) 1e-6 to
-// 2e-5, as binary32 arithmetic on the iterates themselves.  One singular
-// value and m - 1 others at 1/50 to 1/1000 of it are one stage's worst case:
-// 4 x 64 up to 3e-3 beside the rounding of the result, 16 x 1024 1e-3.
+// recursion carries its error on with the square of that growth, and so do the
+// stages behind it in their turn.  Errors measured against float64; "one large"
+// is a block of one singular value and m - 1 others at 1/20 to 1/3000 of it.
+//
+// bfloat16 results: 512, one stage for five quintic steps (485; spectra from flat
+// to i^-3 and rank-16 spikes 1e-4 to 6e-4, one large 3e-3 beside the rounding of
+// the result and for the gradient too).
 constexpr double LIMIT_BF16 = 512.0;
-constexpr double LIMIT_F32 = 48.0;
+// Binary32 results: 12 where the growth by all steps is more than 512 (six
+// quintic steps, gradient of Gaussian blocks of 128 x 257: 3 + 3 steps 4e-5, 2 +
+// 2 + 2 6e-6, binary32 iterates 4e-6), else the square root of RATIO times it,
+// between 12 and 48: binary32 iterates lose with the whole growth, a stage with
+// its square.  Cubic steps on 64 x 200: eight as one stage 2e-6 (Gaussian), 8e-6
+// (plus 10) and 1.7e-5 (plus 100), as 4 + 4 7e-7, 1.4e-6 and 3e-6, binary32
+// iterates 2e-7, 7e-7 and 2e-6; nine 2e-6, 1e-5 and 2.4e-5, as 5 + 4 8e-7, 1.3e-6
+// and 3e-6.  Three quintic steps as one 1.5e-6, 4e-6 and 1.3e-5, as 2 + 1 1.3e-6,
+// 1.0e-6 and 5e-6.  Five quintic steps are 3 + 2: 2e-6 to 8e-6, but one large at
+// 1/20 2e-5 to 4e-5 and its gradient 4e-5, where binary32 iterates give 2e-6;
+// 2 + 2 + 1 would give that too, at 1.3 to 1.5 times the time.
+constexpr double LIMIT_F32 = 48.0, LIMIT_F32_LEAST = 12.0, RATIO_F32 = 3.5;
 // Blocks of so few rows that a single bad direction counts (m <= 4; m <= 16
 // up to n < 4 m) take LIMIT_F32 for bfloat16 results, and for binary32 ones
 // the limits of nearly square blocks: the worst of 300000 random 2 x 3 blocks
@@ -49,11 +61,10 @@ constexpr double LIMIT_F32 = 48.0;
 // the rest, 8e-6 with LIMIT_F32, 1.9e-6 so, binary32 iterates 2.0e-6.
 constexpr int64_t FEW_ROWS = 4, FEW_ROWS_SHORT = 16;
 // Binary32 results of nearly square blocks (n < 2 m), whose singular values
-// reach down to zero: two quintic steps a stage for the orthogonalisation, one
-// for its gradient (sixty random blocks, six steps, largest error: 2e-5
-// against 3e-5 with LIMIT_F32, and for the gradient the ninetieth percentile
-// 6e-6 against 2e-5; binary32 iterates 2e-5 and 6e-6).
-constexpr double LIMIT_F32_SQUARE = 12.0;
+// reach down to zero: LIMIT_F32_LEAST, two quintic steps a stage, for the
+// orthogonalisation, one step for its gradient (sixty random blocks, six steps,
+// largest error: 2e-5 against 3e-5 with LIMIT_F32, and for the gradient the
+// ninetieth percentile 6e-6 against 2e-5; binary32 iterates 2e-5 and 6e-6).
 constexpr double LIMIT_VJP_SQUARE = 1.0;
 
 muon_status fail(muon_status s, const char* fmt, ...) {
@@ -340,22 +351,52 @@ struct Stage {
   int32_t first, steps;
 };
 
-std::vector<Stage> stages_of(const Call& c, double limit) {
+double step_gain_of(const Call& c, int32_t j) { return step_gain(c.schedule ? c.schedule[j] : c.co); }
+
+// The limits of blocks that are neither of few rows nor nearly square.
+struct Limits {
+  double bf16, f32;
+};
+Limits limits_of(const Call& c) {
+  double total = 1.0;
+  for (int32_t j = 0; j < c.ns_steps && total <= LIMIT_BF16; ++j) total *= step_gain_of(c, j);
+  if (total > LIMIT_BF16) return {LIMIT_BF16, LIMIT_F32_LEAST};
+  return {LIMIT_BF16, std::min(LIMIT_F32, std::max(LIMIT_F32_LEAST, std::sqrt(RATIO_F32 * total)))};
+}
+
+// Stages as long as the limit allows.
+std::vector<Stage> cut_stages(const std::vector<double>& gains, double limit) {
   std::vector<Stage> out;
-  int32_t j = 0;
-  while (j < c.ns_steps) {
-    int32_t r = 0;
-    double gain = 1.0;
-    while (j + r < c.ns_steps && r < BLOCK_STAGE_STEPS) {
-      gain *= step_gain(c.schedule ? c.schedule[j + r] : c.co);
-      if (r > 0 && !(gain <= limit)) break;
-      ++r;
-    }
+  const int32_t n = int32_t(gains.size());
+  for (int32_t j = 0; j < n;) {
+    int32_t r = 1;
+    double gain = gains[size_t(j)];
+    while (j + r < n && r < BLOCK_STAGE_STEPS && gain * gains[size_t(j + r)] <= limit) gain *= gains[size_t(j + r++)];
     out.push_back({j, r});
     j += r;
   }
   if (out.empty()) out.push_back({0, 0});
   return out;
+}
+
+// As few stages as the limit allows, and these as even as can be: the least
+// limit that gives as many.
+std::vector<Stage> stages_of(const Call& c, double limit) {
+  std::vector<double> gains;
+  for (int32_t j = 0; j < c.ns_steps; ++j) gains.push_back(step_gain_of(c, j));
+  std::vector<Stage> best = cut_stages(gains, limit);
+  double lo = 0.0, hi = std::log2(limit);
+  for (int32_t k = 0; k < 24 && best.size() > 1; ++k) {
+    const double mid = 0.5 * (lo + hi);
+    std::vector<Stage> s = cut_stages(gains, std::exp2(mid));
+    if (s.size() > best.size()) {
+      lo = mid;
+    } else {
+      hi = mid;
+      best = std::move(s);
+    }
+  }
+  return best;
 }
 
 // ------------------------------------------------------------------ groups
@@ -410,6 +451,7 @@ size_t table_bytes(size_t n) { return align256(sizeof(BlockStack) * n) + align25
 size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
   std::map<std::vector<int64_t>, size_t> where;
   const bool vjp = c.op == MUON_BLOCKS_VJP;
+  const Limits limits = limits_of(c);
   for (int32_t i = 0; i < c.count; ++i) {
     const muon_block_desc& d = c.stacks[i];
     if (d.blocks == 0) continue;
@@ -420,9 +462,11 @@ size_t plan_groups(const Call& c, int cus, std::vector<Group>& groups) {
     g.xbf = d.grad_dtype == MUON_DTYPE_BF16;
     g.ybf = vjp && d.mom_dtype == MUON_DTYPE_BF16;
     const bool few = m <= FEW_ROWS || (m <= FEW_ROWS_SHORT && n < 4 * m), square = few || n < 2 * m;
-    g.limit = !g.f32 ? (few ? LIMIT_F32 : LIMIT_BF16)
-              : !square ? LIMIT_F32 : vjp ? LIMIT_VJP_SQUARE : LIMIT_F32_SQUARE;
-    const std::vector<int64_t> key = {g.mt, g.f32, g.xbf, g.ybf, int64_t(g.limit)};
+    g.limit = !g.f32 ? (few ? LIMIT_F32 : limits.bf16)
+              : !square ? limits.f32 : vjp ? LIMIT_VJP_SQUARE : LIMIT_F32_LEAST;
+    int64_t limit_bits;
+    memcpy(&limit_bits, &g.limit, sizeof(limit_bits));
+    const std::vector<int64_t> key = {g.mt, g.f32, g.xbf, g.ybf, limit_bits};
     auto it = where.find(key);
     if (it == where.end()) {
       it = where.emplace(key, groups.size()).first;

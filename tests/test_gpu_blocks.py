@@ -1086,3 +1086,89 @@ def test_an_earlier_error_is_not_this_call_s():
     torch.cuda.synchronize()
     for a, b in ((w, w2), (m, m2), (outs[0], outs[1])):
         assert np.array_equal(_bits(a), _bits(b))
+
+
+# -------------------------------------- the stages, against binary32 iterates
+
+def _iterates(x, y, coeffs, steps):
+    """NS of a batch and its gradient along y, by the iteration and its reverse, in the batch's type."""
+    if x.shape[1] > x.shape[2]:
+        return tuple(t.transpose(1, 2) for t in _iterates(x.transpose(1, 2), y.transpose(1, 2), coeffs, steps))
+    norm = x.flatten(1).norm(dim=1)[:, None, None]
+    xs = [x / (norm + 1e-7)]
+    sched = orc.schedule(_co(coeffs), steps)
+    for a, b, c in sched:
+        z = xs[-1]
+        g = z @ z.transpose(1, 2)
+        xs.append(a * z + (b * g + c * (g @ g)) @ z)
+    for (a, b, c), z in zip(reversed(sched), reversed(xs[:-1])):
+        g = z @ z.transpose(1, 2)
+        s = y @ z.transpose(1, 2)
+        s = s + s.transpose(1, 2)
+        y = a * y + (b * g + c * (g @ g)) @ y + (b * s + c * (s @ g + g @ s)) @ z
+    inv = 1 / (norm + 1e-7)
+    return xs[-1], inv * (y - xs[0] * (y * x).sum((1, 2), keepdim=True) / norm)
+
+
+def _structured(rows, cols, gen):
+    """Blocks with a few large directions: name, batch of four."""
+    m, n = sorted((rows, cols))
+    r = torch.randn(4, m, n, generator=gen)
+    one = torch.randn(4, m, 1, generator=gen) @ torch.randn(4, 1, n, generator=gen)
+    many = torch.randn(4, m, 16, generator=gen) @ torch.randn(4, 16, n, generator=gen)
+    u = torch.linalg.qr(torch.randn(4, m, m, generator=gen, dtype=torch.float64))[0]
+    v = torch.linalg.qr(torch.randn(4, n, m, generator=gen, dtype=torch.float64))[0]
+    out = {"noise": r, "plus 1": r + 1, "plus 10": r + 10, "plus 100": r + 100, "rank 1 and noise": one + 0.01 * r,
+           "rank 16 and noise": r + many * (100 * (m ** 0.5 + n ** 0.5) / (m * n) ** 0.5)}
+    for ratio in (20, 200, 1000):
+        sv = torch.full((m,), 1.0 / ratio, dtype=torch.float64)
+        sv[0] = 1
+        out[f"one {ratio} times the rest"] = ((u * sv) @ v.transpose(1, 2)).float()
+    return {k: t if rows <= cols else t.transpose(1, 2).contiguous() for k, t in out.items()}
+
+
+def _worst(got, ref):
+    return ((got.double().cpu() - ref).flatten(1).norm(dim=1) / ref.flatten(1).norm(dim=1)).max().item()
+
+
+STAGED = [(CUBIC, 8), (CUBIC, 9), (MUON, 3), (MUON, 6), (MUON, 8), (MUON, 10)]
+
+
+@pytest.mark.parametrize("coeffs,steps", STAGED, ids=lambda v: str(v) if isinstance(v, int) else f"{v[0]}")
+@pytest.mark.parametrize("rows,cols", [(64, 200), (300, 40), (100, 801), (16, 128)])
+def test_binary32_results_against_binary32_iterates(rows, cols, coeffs, steps):
+    """Both forms round to 2^-24 of an iterate a few times a step, and what follows multiplies these alike.  The staged one
+    rounds a Gram matrix, P and P x beside, once a stage; they are carried on with the stage's growth squared, which its
+    limit keeps to 3.5 times the growth of all steps, or to 12^2.  Four times the iterates' error, and 64 roundings."""
+    _announce(f"binary32 stages {rows} {cols} {coeffs} {steps}")
+    gen = torch.Generator().manual_seed(rows + steps)
+    for name, x in _structured(rows, cols, gen).items():
+        y = torch.randn(x.shape, generator=gen)
+        xg, yg = x.cuda(), y.cuda()
+        out, dx = torch.empty_like(xg), torch.empty_like(xg)
+        _run_ns(xg, out, coeffs, steps)
+        _run_vjp(xg, yg, dx, coeffs, steps)
+        torch.cuda.synchronize()
+        refs = _iterates(x.double(), y.double(), coeffs, steps)
+        for what, got, ref, it in zip(("NS", "gradient"), (out, dx), refs, _iterates(x, y, coeffs, steps)):
+            e, e32 = _worst(got, ref), _worst(it, ref)
+            assert e <= 4 * e32 + 64 * 2.0 ** -24, f"{what}, {name}: {e:.2e}, iterates {e32:.2e}"
+
+
+@pytest.mark.parametrize("coeffs,steps", [(CUBIC, 8), (CUBIC, 9), (MUON, 3), (MUON, 5)],
+                         ids=lambda v: str(v) if isinstance(v, int) else f"{v[0]}")
+@pytest.mark.parametrize("rows,cols", [(64, 200), (300, 40), (128, 128)])
+def test_blocks_of_rank_one(rows, cols, coeffs, steps):
+    """All ones, and rank one: beside one direction nothing but the rounding of X_0 and of the sums, which the steps
+    multiply by their whole growth, while the result has the norm of that one direction: T32 with |O| for sqrt(m)."""
+    _announce(f"rank one {rows} {cols} {coeffs} {steps}")
+    gen = torch.Generator().manual_seed(rows)
+    one = torch.randn(4, rows, 1, generator=gen) @ torch.randn(4, 1, cols, generator=gen)
+    for name, x in (("ones", torch.ones(4, rows, cols)), ("rank one", one)):
+        out = torch.empty_like(x.cuda())
+        _run_ns(x.cuda(), out, coeffs, steps)
+        torch.cuda.synchronize()
+        ref = _iterates(x.double(), x.double(), coeffs, steps)[0]
+        tol = 2.0 ** -24 * (64 + 16 * _gain(coeffs, steps) / ref.flatten(1).norm(dim=1).min().item())
+        e = _worst(out, ref)
+        assert e <= tol, f"{name}: {e:.2e} > {tol:.2e}"
