@@ -31,7 +31,8 @@
  * limit.  With g the growth by all steps (1.5 a cubic step, 3.4445 one of the
  * usual quintic):
  *   - bfloat16 results: 512, so that five quintic steps (g = 485) are one pass;
- *     48 for blocks of up to four rows, and of up to 16 with n < 4 m;
+ *     150 where g is more; 48 for blocks of up to four rows, and of up to 16
+ *     with n < 4 m;
  *   - binary32 results: sqrt(3.5 g), at least 12 and at most 48 (five quintic
  *     steps 3 + 2, eight cubic ones 4 + 4); 12 where g is more than 512, and for
  *     blocks of few rows as above or with n < 2 m, whose gradient takes a Gram

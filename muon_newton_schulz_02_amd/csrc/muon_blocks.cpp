@@ -37,10 +37,12 @@ constexpr int64_t MAX_STRIDE = int64_t(1) << 40;
 // stages behind it in their turn.  Errors measured against float64; "one large"
 // is a block of one singular value and m - 1 others at 1/20 to 1/3000 of it.
 //
-// bfloat16 results: 512, one stage for five quintic steps (485; spectra from flat
-// to i^-3 and rank-16 spikes 1e-4 to 6e-4, one large 3e-3 beside the rounding of
-// the result and for the gradient too).
-constexpr double LIMIT_BF16 = 512.0;
+// bfloat16 results: one stage up to a growth of 512 by all steps (five quintic
+// ones, 485, spectra from flat to i^-3 and rank-16 spikes 1e-4 to 6e-4, one
+// large 3e-3 beside the rounding of the result and for the gradient too),
+// stages of up to 150 where there is more (eight quintic steps, one large: 5 + 3
+// steps 4e-3 and the gradient 3e-2, 4 + 4 steps 2e-4 and 1e-3).
+constexpr double LIMIT_BF16 = 512.0, LIMIT_BF16_MORE = 150.0;
 // Binary32 results: 12 where the growth by all steps is more than 512 (six
 // quintic steps, gradient of Gaussian blocks of 128 x 257: 3 + 3 steps 4e-5, 2 +
 // 2 + 2 6e-6, binary32 iterates 4e-6), else the square root of RATIO times it,
@@ -360,7 +362,7 @@ struct Limits {
 Limits limits_of(const Call& c) {
   double total = 1.0;
   for (int32_t j = 0; j < c.ns_steps && total <= LIMIT_BF16; ++j) total *= step_gain_of(c, j);
-  if (total > LIMIT_BF16) return {LIMIT_BF16, LIMIT_F32_LEAST};
+  if (total > LIMIT_BF16) return {LIMIT_BF16_MORE, LIMIT_F32_LEAST};
   return {LIMIT_BF16, std::min(LIMIT_F32, std::max(LIMIT_F32_LEAST, std::sqrt(RATIO_F32 * total)))};
 }
 

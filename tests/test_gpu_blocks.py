@@ -1172,3 +1172,23 @@ def test_blocks_of_rank_one(rows, cols, coeffs, steps):
         tol = 2.0 ** -24 * (64 + 16 * _gain(coeffs, steps) / ref.flatten(1).norm(dim=1).min().item())
         e = _worst(out, ref)
         assert e <= tol, f"{name}: {e:.2e} > {tol:.2e}"
+
+
+@pytest.mark.parametrize("steps", [6, 7, 8, 9, 10])
+@pytest.mark.parametrize("m,n", [(16, 64), (16, 1024), (64, 768), (128, 300)])
+def test_bfloat16_results_of_many_steps(m, n, steps):
+    """More growth than one stage takes: results and gradients of blocks with large directions stay within TB, and with
+    what binary32 iterates lose where that counts beside it."""
+    _announce(f"bfloat16 stages {m} {n} {steps}")
+    gen = torch.Generator().manual_seed(m + steps)
+    for name, x in _structured(m, n, gen).items():
+        x, y = x.to(BF), torch.randn(x.shape, generator=gen).to(BF)
+        xg, yg = x.cuda(), y.cuda()
+        out, dx = torch.empty_like(xg), torch.empty_like(xg)
+        _run_ns(xg, out, MUON, steps)
+        _run_vjp(xg, yg, dx, MUON, steps)
+        torch.cuda.synchronize()
+        refs = _iterates(x.double(), y.double(), MUON, steps)
+        for what, got, ref, it in zip(("NS", "gradient"), (out, dx), refs, _iterates(x.float(), y.float(), MUON, steps)):
+            e, e32 = _worst(got, ref), _worst(it, ref)
+            assert e <= TB + 4 * e32, f"{what}, {name}: {e:.2e}, iterates {e32:.2e}"
