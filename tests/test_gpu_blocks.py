@@ -1192,3 +1192,66 @@ def test_bfloat16_results_of_many_steps(m, n, steps):
         for what, got, ref, it in zip(("NS", "gradient"), (out, dx), refs, _iterates(x.float(), y.float(), MUON, steps)):
             e, e32 = _worst(got, ref), _worst(it, ref)
             assert e <= TB + 4 * e32, f"{what}, {name}: {e:.2e}, iterates {e32:.2e}"
+
+
+# ------------------------- the binary32 update of a step on bfloat16 weights
+
+def _tol_update(m, coeffs, steps, norm=None):
+    """Of an update that is not rounded to bfloat16: U and P are 17 bits each, so off by 2^-18.  The steps multiply an error
+    of U, of norm 2^-18 beside X_0's 1, by G at most, and a result has norm sqrt(m) (`norm`, where that is known and
+    less).  P, of norm G at most in every direction, is off by 2^-18 of that and acts on singular values of up to 2 /
+    sqrt(m) of noise (1 of other blocks).  No more than 2^-9, what one stage leaves of its Gram matrix."""
+    size = norm if norm is not None else np.sqrt(m)
+    return min(2.0 ** -9, 3 * 2.0 ** -18 * _gain(coeffs, steps) / size)
+
+
+@pytest.mark.parametrize("gdt", [BF, F])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"{s[0]}x{s[1]}x{s[2]}-{s[3]}{s[4]}")
+def test_update_of_bfloat16_weights(shape, gdt):
+    """One bfloat16 part of U would leave 1.6e-3 to 3.6e-3."""
+    _announce(f"update {shape} {gdt}")
+    (w, g, m, _, _), = _step_case(shape, BF, gdt, shape[1] * 5 + shape[2])
+    g0, m0 = to_np(g), to_np(m)
+    o = torch.full(tuple(w.shape), float("nan"), device="cuda")
+    mb.muon_step_blocks([w], [g], [m], lr=f32(0.02), beta=0.95, nesterov=True, ns_coeffs=MUON, ns_steps=5,
+                        updates_out=[o])
+    torch.cuda.synchronize()
+    got, tol = to_np(o), _tol_update(min(shape[1:3]), MUON, 5)
+    for b in range(shape[0]):
+        ref = orc.orthogonalise(orc.momentum(m0[b], g0[b], f32(0.95), True, 0)[1], _co(MUON), 5)
+        e = orc.rel_frobenius(got[b], ref)
+        assert e <= tol, f"block {b}: {e:.2e} > {tol:.2e}"
+
+
+@pytest.mark.parametrize("wdt", [BF, F])
+@pytest.mark.parametrize("rows,cols", [(16, 128), (64, 200), (300, 100), (128, 300)])
+def test_step_on_structured_gradients(rows, cols, wdt):
+    """The step's own kernels on blocks with a few large directions (U is the gradient): the update of bfloat16 weights
+    within the roundings of _tol_update and four of 2^-24 of the Gram matrix, carried on by the stage; that of binary32
+    ones the same as muon_ns_blocks."""
+    _announce(f"structured step {rows} {cols} {wdt}")
+    gen = torch.Generator().manual_seed(rows)
+    for name, x in _structured(rows, cols, gen).items():
+        g = x.cuda()
+        w, m, o = torch.zeros_like(g, dtype=wdt), torch.zeros_like(g), torch.empty_like(g)
+        mb.muon_step_blocks([w], [g], [m], lr=f32(0.5), beta=0.0, nesterov=False, ns_coeffs=MUON, ns_steps=5,
+                            updates_out=[o])
+        torch.cuda.synchronize()
+        assert torch.equal(m, g)
+        if wdt == F:
+            out = torch.empty_like(g)
+            _run_ns(g, out, MUON, 5)
+            assert np.array_equal(_bits(o), _bits(out)), name
+            continue
+        ref = _iterates(x.double(), x.double(), MUON, 5)[0]
+        for b in range(4):
+            # s |p'(s^2)| over the singular values that an iterate may have: what a unit error of A_0 gives
+            t = np.logspace(-5, 0, 2001)
+            f = [t * (1 + d) for d in (-1e-6, 0.0, 1e-6)]
+            for a, bb, c in orc.schedule(_co(MUON), 5):
+                f = [v * (a + bb * v * v + c * v ** 4) for v in f]
+            dp = np.abs(((f[2] - f[0]) / (2e-6 * t) - f[1] / t) / (2 * t)).max()
+            size = ref[b].norm().item()
+            tol = 3 * 2.0 ** -18 * _gain(MUON, 5) / size + 4 * 2.0 ** -24 * dp / size
+            e = _worst(o[b:b + 1], ref[b:b + 1])
+            assert e <= tol, f"{name}, block {b}: {e:.2e} > {tol:.2e}"
