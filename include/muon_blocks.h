@@ -43,10 +43,10 @@
  *     more (one singular value 100 to 3000 times the others); where x is
  *     binary32 and of rank one alone, by 2^-18 g;
  *   - binary32 ones by up to four times what the same iteration carried out in
- *     binary32 is, or by 5e-6 where that is more (most 1e-6 to 1e-5; rank one
- *     alone 2^-24 g, and so is that iteration).  Five quintic steps leave more
- *     where one singular value is about 20 times the others, 2e-5 to 4e-5, and
- *     gradients there and up to 50 times, as much; ones alone up to 6e-5.
+ *     binary32 is, and 5e-6 beside (most 1e-6 to 1e-5; rank one alone some
+ *     2^-24 g, and so is that iteration).  Five quintic steps leave more where
+ *     one singular value is about 20 times the others, 2e-5 to 4e-5, and as
+ *     much for gradients there and up to 50 times; ones alone up to 6e-5.
  *
  * Conventions are those of muon.h (device memory of the current device,
  * strides in elements, validation before anything is enqueued, no
@@ -148,7 +148,8 @@ muon_status muon_ns_blocks_vjp(const void* const* x_in, const void* const* grad_
  * momentum_kind, and lr_per_matrix and scale_per_matrix with one entry per
  * stack; launch_mode and tile_mode must be AUTO (0).  updates_out: NULL, or
  * per stack NULL or the binary32 update O that the write-back used, blocks x
- * rows x cols contiguous.  Errors as muon_ns_blocks.                        */
+ * rows x cols contiguous, as exact as results of the parameters' type are
+ * before they are rounded.  Errors as muon_ns_blocks.                       */
 muon_status muon_step_blocks(void* const* params, const void* const* grads, void* const* momenta,
                              const muon_block_desc* stacks, int32_t count, const muon_step_hparams* hparams,
                              float* const* updates_out, void* workspace, uint64_t workspace_bytes, void* stream);
