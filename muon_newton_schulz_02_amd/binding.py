@@ -629,6 +629,13 @@ def _on_device(device):
     return torch.cuda.device(device if device is not None else -1)
 
 
+def _stream_on(stream, device):
+    """Handle of `stream` (the device's current one for None), which has to be a stream of `device`."""
+    if getattr(stream, "device", device) != device:
+        raise ValueError(f"stream is on {stream.device}, the stacks on {device}")
+    return _stream_handle(stream)
+
+
 def _coeffs(ns_coeffs) -> NsCoeffs:
     a, b, c = ns_coeffs
     return NsCoeffs(float(a), float(b), float(c))
@@ -700,7 +707,7 @@ def muon_ns_blocks(x_in, x_out=None, *, ns_coeffs, ns_steps, ns_schedule=None, w
     with _on_device(args.device):
         ws, nbytes = _workspace(workspace, args.device)
         status = lib().muon_ns_blocks(args.ptrs["grad"], args.ptrs["param"], args.descs, args.count,
-                                      _coeffs(ns_coeffs), int(ns_steps), sched, ws, nbytes, _stream_handle(stream))
+                                      _coeffs(ns_coeffs), int(ns_steps), sched, ws, nbytes, _stream_on(stream, args.device))
         del keep
         _check(status)
 
@@ -717,7 +724,7 @@ def muon_ns_blocks_vjp(x_in, grad_out=None, grad_in=None, *, ns_coeffs, ns_steps
         ws, nbytes = _workspace(workspace, args.device)
         status = lib().muon_ns_blocks_vjp(args.ptrs["grad"], args.ptrs["mom"], args.ptrs["param"], args.descs,
                                           args.count, _coeffs(ns_coeffs), int(ns_steps), sched, ws, nbytes,
-                                          _stream_handle(stream))
+                                          _stream_on(stream, args.device))
         del keep
         _check(status)
 
@@ -737,6 +744,6 @@ def muon_step_blocks(params, grads=None, momenta=None, *, lr, beta, nesterov, ns
     with _on_device(args.device):
         ws, nbytes = _workspace(workspace, args.device)
         status = lib().muon_step_blocks(args.ptrs["param"], args.ptrs["grad"], args.ptrs["mom"], args.descs, args.count,
-                                        ctypes.byref(hp), args.updates, ws, nbytes, _stream_handle(stream))
+                                        ctypes.byref(hp), args.updates, ws, nbytes, _stream_on(stream, args.device))
         del keep
         _check(status)

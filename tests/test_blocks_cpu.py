@@ -337,6 +337,15 @@ def test_no_exception_leaves_a_c_entry(L, tmp_path):
     assert r.returncode == 0 and "54 calls, 0 threw" in r.stdout, r.stdout + r.stderr[-2000:]
 
 
+def test_stream_of_another_device_is_refused():
+    """Kernels would run on the stream's device, on the other one's memory."""
+    from types import SimpleNamespace
+    one = SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=7)
+    assert mb._stream_on(one, torch.device("cuda", 1)) == 7 and mb._stream_on(9, torch.device("cuda", 1)) == 9
+    with pytest.raises(ValueError, match="stream is on cuda:1, the stacks on cuda:0"):
+        mb._stream_on(one, torch.device("cuda", 0))
+
+
 # ------------------------------------------------------------- oracle pins
 
 def _np_rng(seed):
