@@ -42,11 +42,11 @@
  *   - bfloat16 results and gradients are off by their rounding and up to 3e-3
  *     more (one singular value 100 to 3000 times the others); where x is
  *     binary32 and of rank one alone, by 2^-18 g;
- *   - binary32 ones by up to four times what the same iteration carried out in
- *     binary32 is, and 5e-6 beside (most 1e-6 to 1e-5; rank one alone some
- *     2^-24 g, and so is that iteration).  Five quintic steps leave more where
- *     one singular value is about 20 times the others, 2e-5 to 4e-5, and as
- *     much for gradients there and up to 50 times; ones alone up to 6e-5.
+ *   - binary32 ones by up to about five times what the same iteration carried
+ *     out in binary32 is, and 5e-6 beside (most 1e-6 to 1e-5; rank one alone
+ *     some 2^-24 g, and so is that iteration).  Five quintic steps leave more
+ *     where one singular value is about 20 times the others, 2e-5 to 4e-5, and
+ *     as much for gradients there and up to 50 times; ones alone up to 6e-5.
  *
  * Conventions are those of muon.h (device memory of the current device,
  * strides in elements, validation before anything is enqueued, no
