@@ -39,9 +39,9 @@ constexpr int64_t MAX_STRIDE = int64_t(1) << 40;
 //
 // bfloat16 results: one stage up to a growth of 512 by all steps (five quintic
 // ones, 485, spectra from flat to i^-3 and rank-16 spikes 1e-4 to 6e-4, one
-// large 3e-3 beside the rounding of the result and for the gradient too),
-// stages of up to 150 where there is more (eight quintic steps, one large: 5 + 3
-// steps 4e-3 and the gradient 3e-2, 4 + 4 steps 2e-4 and 1e-3).
+// large and its gradient 3e-3 beside the rounding of the result), stages of up
+// to 150 where there is more (eight quintic steps, one large at 1/200 in binary32
+// arithmetic: 5 + 3 steps 4e-3 and the gradient 3e-2, 4 + 4 2e-4 and 1e-3).
 constexpr double LIMIT_BF16 = 512.0, LIMIT_BF16_MORE = 150.0;
 // Binary32 results: 12 where the growth by all steps is more than 512 (six
 // quintic steps, gradient of Gaussian blocks of 128 x 257: 3 + 3 steps 4e-5, 2 +

@@ -1135,11 +1135,14 @@ STAGED = [(CUBIC, 8), (CUBIC, 9), (MUON, 3), (MUON, 6), (MUON, 8), (MUON, 10)]
 
 
 @pytest.mark.parametrize("coeffs,steps", STAGED, ids=lambda v: str(v) if isinstance(v, int) else f"{v[0]}")
-@pytest.mark.parametrize("rows,cols", [(64, 200), (300, 40), (100, 801), (16, 128)])
+@pytest.mark.parametrize("rows,cols", [(64, 200), (300, 40), (100, 801), (16, 128), (128, 257)])
 def test_binary32_results_against_binary32_iterates(rows, cols, coeffs, steps):
     """Both forms round to 2^-24 of an iterate a few times a step, and what follows multiplies these alike.  The staged one
     rounds a Gram matrix, P and P x beside, once a stage; they are carried on with the stage's growth squared, which its
-    limit keeps to 3.5 times the growth of all steps, or to 12^2.  Four times the iterates' error, and 64 roundings."""
+    limit keeps to 3.5 times the growth of all steps, or to 12^2.  Its products are of operands in two parts: 2^-24 for
+    each of two operands, for the product of the low parts, which is left out, and for the sum, where the iterates'
+    have the sum's alone.  So four times the iterates' error, and 64 roundings; the tangents of the gradient are sums of
+    two products each, so twice that for it."""
     _announce(f"binary32 stages {rows} {cols} {coeffs} {steps}")
     gen = torch.Generator().manual_seed(rows + steps)
     for name, x in _structured(rows, cols, gen).items():
@@ -1152,7 +1155,8 @@ def test_binary32_results_against_binary32_iterates(rows, cols, coeffs, steps):
         refs = _iterates(x.double(), y.double(), coeffs, steps)
         for what, got, ref, it in zip(("NS", "gradient"), (out, dx), refs, _iterates(x, y, coeffs, steps)):
             e, e32 = _worst(got, ref), _worst(it, ref)
-            assert e <= 4 * e32 + 64 * 2.0 ** -24, f"{what}, {name}: {e:.2e}, iterates {e32:.2e}"
+            factor = 4 if what == "NS" else 8
+            assert e <= factor * e32 + 64 * 2.0 ** -24, f"{what}, {name}: {e:.2e}, iterates {e32:.2e}"
 
 
 @pytest.mark.parametrize("coeffs,steps", [(CUBIC, 8), (CUBIC, 9), (MUON, 3), (MUON, 5)],
