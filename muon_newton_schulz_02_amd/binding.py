@@ -1,5 +1,5 @@
-"""ctypes binding of libmuon_mi355x.so (declared in include/muon.h and
-include/muon_blocks.h).
+"""ctypes binding of libmuon_mi355x.so (declared in include/muon.h,
+include/muon_blocks.h, include/muon_experts.h and include/muon_head.h).
 
 Argument marshalling only: tensors become device pointers, row strides and
 dtype codes; the torch stream becomes a hipStream_t.  Every step of the
@@ -124,6 +124,42 @@ BLOCKS_VJP = 1
 BLOCKS_STEP = 2
 
 
+class ExpertsDesc(ctypes.Structure):
+    """muon_experts_desc (include/muon_experts.h)."""
+    _fields_ = [
+        ("experts", ctypes.c_int64), ("rows", ctypes.c_int64), ("in_dim", ctypes.c_int64), ("out_dim", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64), ("ld_w", ctypes.c_int64), ("stride_w", ctypes.c_int64),
+        ("ld_grad_x", ctypes.c_int64), ("ld_grad_w", ctypes.c_int64), ("stride_grad_w", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("grad_w_dtype", ctypes.c_int32), ("w_order", ctypes.c_int32),
+        ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int64),
+    ]
+
+
+WEIGHT_OUT_IN = 0
+WEIGHT_IN_OUT = 1
+
+EXPERTS_PRODUCT = 0
+EXPERTS_GRAD_X = 1
+EXPERTS_GRAD_W = 2
+EXPERTS_GRAD_X_W = 3
+
+
+class HeadDesc(ctypes.Structure):
+    """muon_head_desc (include/muon_head.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("vocab", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64), ("ld_w", ctypes.c_int64), ("ld_grad_x", ctypes.c_int64), ("ld_grad_w", ctypes.c_int64),
+        ("ignore_index", ctypes.c_int64), ("softcap", ctypes.c_float), ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int64),
+    ]
+
+
+HEAD_LOSS = 0
+HEAD_GRAD_X = 1
+HEAD_GRAD_W = 2
+HEAD_GRAD_X_W = 3
+
+
 _VP = ctypes.c_void_p
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _lib = None
@@ -193,6 +229,19 @@ def lib() -> ctypes.CDLL:
     L.muon_step_blocks.restype = i32
     L.muon_blocks_workspace_bytes.argtypes = [i32, B, i32, NsCoeffs, i32, C]
     L.muon_blocks_workspace_bytes.restype = u64
+    E, H = ctypes.POINTER(ExpertsDesc), ctypes.POINTER(HeadDesc)
+    L.muon_experts_product.argtypes = [_VP, _VP, _VP, _VP, E, _VP, u64, _VP]
+    L.muon_experts_product.restype = i32
+    L.muon_experts_product_vjp.argtypes = [_VP, _VP, _VP, _VP, _VP, _VP, E, _VP, u64, _VP]
+    L.muon_experts_product_vjp.restype = i32
+    L.muon_experts_workspace_bytes.argtypes = [i32, E]
+    L.muon_experts_workspace_bytes.restype = u64
+    L.muon_head_loss.argtypes = [_VP, _VP, _VP, _VP, _VP, H, _VP, u64, _VP]
+    L.muon_head_loss.restype = i32
+    L.muon_head_loss_vjp.argtypes = [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, H, _VP, u64, _VP]
+    L.muon_head_loss_vjp.restype = i32
+    L.muon_head_workspace_bytes.argtypes = [i32, H]
+    L.muon_head_workspace_bytes.restype = u64
     _lib = L
     return L
 
@@ -747,3 +796,253 @@ def muon_step_blocks(params, grads=None, momenta=None, *, lr, beta, nesterov, ns
                                         ctypes.byref(hp), args.updates, ws, nbytes, _stream_on(stream, args.device))
         del keep
         _check(status)
+
+
+# ------------------------------------------- experts' products, the head's loss
+
+
+class _OperatorArgs:
+    """Checked tensors of a call, built once and reused by every call on them.
+    All live on one GPU; the calls run on it, whatever the current device."""
+
+    def __init__(self, **tensors):
+        """tensors: name -> tensor, or None where the call does without."""
+        self.device = None
+        self.t = tensors
+        for name, t in tensors.items():
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError(f"{name} is on {t.device}, not on a GPU")
+            if self.device is None:
+                self.device = t.device
+            elif t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, other tensors on {self.device}")
+
+    def ptr(self, name):
+        t = self.t[name]
+        return None if t is None else t.data_ptr()
+
+    def shaped(self, name, shape, dtype):
+        t = self.t[name]
+        if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+            raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} (got {t.dtype}, {tuple(t.shape)})")
+
+    def flat(self, name):
+        t = self.t[name]
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _ld(t, name):
+    """Row stride of a matrix whose rows are contiguous."""
+    if t is None:
+        return 0
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D (got shape {tuple(t.shape)})")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return int(t.stride(0))
+
+
+def _weight_layout(t, name):
+    """(order, row stride, expert stride) of an (experts, out, in) stack, whose rows or whose columns are contiguous."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D: experts, out, in (got shape {tuple(t.shape)})")
+    stride = int(t.stride(0)) if t.shape[0] > 1 else 0
+    if t.shape[2] == 1 or t.stride(2) == 1:
+        return WEIGHT_OUT_IN, int(t.stride(1)), stride
+    if t.shape[1] == 1 or t.stride(1) == 1:
+        return WEIGHT_IN_OUT, int(t.stride(2)), stride
+    raise ValueError(f"{name} must have contiguous rows or columns (strides {tuple(t.stride())})")
+
+
+class _ExpertsArgs(_OperatorArgs):
+    def _describe(self, rows, w, gw, in_dim, out_dim, x, y, gx):
+        d = self.desc = ExpertsDesc()
+        d.rows, d.in_dim, d.out_dim = rows, in_dim, out_dim
+        d.ld_x, d.ld_y, d.ld_grad_x = _ld(x, "x"), _ld(y, "y or grad_y"), _ld(gx, "grad_x")
+        offsets = self.t["offsets"]
+        if offsets.dim() != 1 or offsets.dtype != torch.int32 or offsets.shape[0] < 1:
+            raise ValueError("offsets must be 1-D int32, experts + 1 of them")
+        self.flat("offsets")
+        d.experts = offsets.shape[0] - 1
+        d.w_order = WEIGHT_OUT_IN
+        if w is not None:
+            self.shaped("w", (d.experts, out_dim, in_dim), self.dtype)
+            d.w_order, d.ld_w, d.stride_w = _weight_layout(w, "w")
+        if gw is not None:
+            if tuple(gw.shape) != (d.experts, out_dim, in_dim):
+                raise ValueError(f"grad_w must have shape {(d.experts, out_dim, in_dim)} (got {tuple(gw.shape)})")
+            order, d.ld_grad_w, d.stride_grad_w = _weight_layout(gw, "grad_w")
+            if w is not None and order != d.w_order:
+                raise ValueError("grad_w must lie in memory in w's order")
+            d.w_order = order
+            d.grad_w_dtype = dtype_code(gw.dtype)
+        d.dtype = dtype_code(self.dtype)
+
+    def workspace_bytes(self) -> int:
+        """Bytes a `workspace` of the call needs."""
+        with _on_device(self.device):
+            got = int(lib().muon_experts_workspace_bytes(self.op, self.desc))
+            detail = muon_last_error()
+        if not got and detail:
+            raise MuonError(MUON_ERR_INVALID_ARGUMENT, detail)
+        return got
+
+
+class ExpertsArgs(_ExpertsArgs):
+    """Tensors of muon_experts_product: x (rows, in), w (experts, out, in) with
+    contiguous rows or columns, offsets (experts + 1, int32), y (rows, out)."""
+
+    op = EXPERTS_PRODUCT
+
+    def __init__(self, x, w, offsets, y):
+        super().__init__(x=x, w=w, offsets=offsets, y=y)
+        self.dtype = x.dtype
+        if x.dim() != 2 or w.dim() != 3:
+            raise ValueError("x must be (rows, in) and w (experts, out, in)")
+        self.shaped("y", (x.shape[0], w.shape[1]), self.dtype)
+        self._describe(int(x.shape[0]), w, None, int(x.shape[1]), int(w.shape[1]), x, y, None)
+
+
+class ExpertsVjpArgs(_ExpertsArgs):
+    """Tensors of muon_experts_product_vjp.  grad_x (rows, in) needs w, grad_w
+    (experts, out, in) needs x; what is not needed may be None."""
+
+    def __init__(self, x, w, offsets, grad_y, grad_x=None, grad_w=None):
+        super().__init__(x=x, w=w, offsets=offsets, grad_y=grad_y, grad_x=grad_x, grad_w=grad_w)
+        self.dtype = grad_y.dtype
+        if grad_x is None and grad_w is None:
+            raise ValueError("grad_x and grad_w are both None")
+        if grad_x is not None and w is None:
+            raise ValueError("grad_x needs w")
+        if grad_w is not None and x is None:
+            raise ValueError("grad_w needs x")
+        if grad_y.dim() != 2:
+            raise ValueError("grad_y must be (rows, out)")
+        rows, out_dim = (int(s) for s in grad_y.shape)
+        in_dim = int((x if x is not None else grad_x).shape[-1])
+        self.shaped("x", (rows, in_dim), self.dtype)
+        self.shaped("grad_x", (rows, in_dim), self.dtype)
+        self.op = (EXPERTS_GRAD_X if grad_x is not None else 0) | (EXPERTS_GRAD_W if grad_w is not None else 0)
+        self._describe(rows, w, grad_w, in_dim, out_dim, x, grad_y, grad_x)
+
+
+def _prebuilt(cls, first, rest, kw):
+    """The call's arguments: `first` if it is prebuilt (it holds all tensors), or built from them."""
+    if not isinstance(first, cls):
+        return cls(first, *rest, **kw)
+    if any(r is not None for r in (*rest, *kw.values())):
+        raise ValueError(f"a {cls.__name__} holds every tensor of the call: build it with them")
+    return first
+
+
+def muon_experts_product(x, w=None, offsets=None, y=None, *, workspace=None, stream=None):
+    """y[r] = W_e x[r] for the rows offsets[e] <= r < offsets[e + 1] of every
+    expert e (or on a prebuilt ExpertsArgs)."""
+    a = _prebuilt(ExpertsArgs, x, (w, offsets, y), {})
+    with _on_device(a.device):
+        ws, nbytes = _workspace(workspace, a.device)
+        _check(lib().muon_experts_product(a.ptr("x"), a.ptr("w"), a.ptr("offsets"), a.ptr("y"), a.desc, ws, nbytes,
+                                          _stream_on(stream, a.device)))
+
+
+def muon_experts_product_vjp(x, w=None, offsets=None, grad_y=None, grad_x=None, grad_w=None, *, accumulate=False,
+                             workspace=None, stream=None):
+    """The gradients of <muon_experts_product(x, w), grad_y> with respect to x
+    and w, each if its tensor is given (or on a prebuilt ExpertsVjpArgs).
+    accumulate: grad_w is added to."""
+    a = _prebuilt(ExpertsVjpArgs, x, (w, offsets, grad_y), {"grad_x": grad_x, "grad_w": grad_w})
+    with _on_device(a.device):
+        ws, nbytes = _workspace(workspace, a.device)
+        desc = ExpertsDesc.from_buffer_copy(a.desc)
+        desc.accumulate = int(bool(accumulate))
+        _check(lib().muon_experts_product_vjp(a.ptr("x"), a.ptr("w"), a.ptr("offsets"), a.ptr("grad_y"), a.ptr("grad_x"),
+                                              a.ptr("grad_w"), desc, ws, nbytes, _stream_on(stream, a.device)))
+
+
+class _HeadArgs(_OperatorArgs):
+    def _describe(self, x, w, gx, gw):
+        if x.dim() != 2 or w.dim() != 2:
+            raise ValueError("x must be (rows, dim) and w (vocab, dim)")
+        d = self.desc = HeadDesc()
+        d.rows, d.dim, d.vocab = int(x.shape[0]), int(x.shape[1]), int(w.shape[0])
+        self.shaped("w", (d.vocab, d.dim), x.dtype)
+        self.shaped("targets", (d.rows,), torch.int64)
+        self.flat("targets")
+        for name in ("loss", "lse", "grad_loss", "grad_lse"):
+            if name in self.t:
+                self.shaped(name, (d.rows,), torch.float32)
+                self.flat(name)
+        self.dtype = x.dtype
+        d.dtype = dtype_code(x.dtype)
+        d.ld_x, d.ld_w = _ld(x, "x"), _ld(w, "w")
+        if gx is not None:
+            self.shaped("grad_x", (d.rows, d.dim), x.dtype)
+            d.ld_grad_x = _ld(gx, "grad_x")
+        if gw is not None:
+            self.shaped("grad_w", (d.vocab, d.dim), x.dtype)
+            d.ld_grad_w = _ld(gw, "grad_w")
+
+    def workspace_bytes(self) -> int:
+        """Bytes a `workspace` of the call needs."""
+        with _on_device(self.device):
+            got = int(lib().muon_head_workspace_bytes(self.op, self.desc))
+            detail = muon_last_error()
+        if not got and detail:
+            raise MuonError(MUON_ERR_INVALID_ARGUMENT, detail)
+        return got
+
+
+class HeadLossArgs(_HeadArgs):
+    """Tensors of muon_head_loss: x (rows, dim), w (vocab, dim), targets (rows,
+    int64), loss and lse (rows, float32)."""
+
+    op = HEAD_LOSS
+
+    def __init__(self, x, w, targets, loss, lse):
+        super().__init__(x=x, w=w, targets=targets, loss=loss, lse=lse)
+        self._describe(x, w, None, None)
+
+
+class HeadLossVjpArgs(_HeadArgs):
+    """Tensors of muon_head_loss_vjp: those of the loss, grad_loss and grad_lse
+    (rows, float32; grad_lse may be None), grad_x (rows, dim) and grad_w
+    (vocab, dim), either None if not wanted."""
+
+    def __init__(self, x, w, targets, lse, grad_loss, grad_x=None, grad_w=None, grad_lse=None):
+        super().__init__(x=x, w=w, targets=targets, lse=lse, grad_loss=grad_loss, grad_lse=grad_lse, grad_x=grad_x,
+                         grad_w=grad_w)
+        if grad_x is None and grad_w is None:
+            raise ValueError("grad_x and grad_w are both None")
+        self.op = (HEAD_GRAD_X if grad_x is not None else 0) | (HEAD_GRAD_W if grad_w is not None else 0)
+        self._describe(x, w, grad_x, grad_w)
+
+
+def muon_head_loss(x, w=None, targets=None, loss=None, lse=None, *, softcap=0.0, ignore_index=-100, workspace=None,
+                   stream=None):
+    """loss[r] and lse[r] of the head w's logits of row x[r] (or on a prebuilt
+    HeadLossArgs), both 0 where targets[r] is ignore_index."""
+    a = _prebuilt(HeadLossArgs, x, (w, targets, loss, lse), {})
+    with _on_device(a.device):
+        ws, nbytes = _workspace(workspace, a.device)
+        desc = HeadDesc.from_buffer_copy(a.desc)
+        desc.softcap, desc.ignore_index = float(softcap), int(ignore_index)
+        _check(lib().muon_head_loss(a.ptr("x"), a.ptr("w"), a.ptr("targets"), a.ptr("loss"), a.ptr("lse"), desc, ws,
+                                    nbytes, _stream_on(stream, a.device)))
+
+
+def muon_head_loss_vjp(x, w=None, targets=None, lse=None, grad_loss=None, grad_x=None, grad_w=None, *, grad_lse=None,
+                       softcap=0.0, ignore_index=-100, workspace=None, stream=None):
+    """The gradients of <loss, grad_loss> + <lse, grad_lse> with respect to x and
+    w, each if its tensor is given (or on a prebuilt HeadLossVjpArgs)."""
+    a = _prebuilt(HeadLossVjpArgs, x, (w, targets, lse, grad_loss),
+                  {"grad_x": grad_x, "grad_w": grad_w, "grad_lse": grad_lse})
+    with _on_device(a.device):
+        ws, nbytes = _workspace(workspace, a.device)
+        desc = HeadDesc.from_buffer_copy(a.desc)
+        desc.softcap, desc.ignore_index = float(softcap), int(ignore_index)
+        _check(lib().muon_head_loss_vjp(a.ptr("x"), a.ptr("w"), a.ptr("targets"), a.ptr("lse"), a.ptr("grad_loss"),
+                                        a.ptr("grad_lse"), a.ptr("grad_x"), a.ptr("grad_w"), desc, ws, nbytes,
+                                        _stream_on(stream, a.device)))

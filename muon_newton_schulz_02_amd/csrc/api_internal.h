@@ -23,7 +23,8 @@ hipError_t api_device_alloc(void** p, size_t bytes);
 hipError_t api_timed(int kc, hipStream_t stream, const std::function<hipError_t()>& launch);
 // Whether launches are being timed (lock held).
 bool api_timing();
-// Called by muon_release_workspace with the lock held; null if unused.
+// Called by muon_release_workspace with the lock held; null if unused.  A file
+// that sets it calls what it held before.
 extern void (*api_release_hook)();
 
 }  // namespace muon

@@ -1,0 +1,131 @@
+// Kernels of the head's loss beside its products: the packing of the rows that
+// have a target, and the loss from the tiles' maxima and sums.
+#include <algorithm>
+
+#include "products_device.h"
+
+namespace muon {
+namespace {
+
+constexpr int NT = 256;
+
+__device__ __forceinline__ bool has_target(const HeadRows& a, int64_t t) {
+  return t != a.ignore_index && t >= 0 && t < a.vocab;
+}
+
+// Each workgroup packs `chunk` rows: it counts the rows with a target before
+// them by itself (8 bytes a row, read from L2), which saves a launch and a wait;
+// the chunks are cut so that 512 workgroups at most do it.  The copy of x gives
+// the products rows at 16-byte boundaries, and takes ignored rows out of them:
+// their work, and whatever their x holds.
+template <class T>
+__global__ __launch_bounds__(NT) void head_rows_kernel(const HeadRows a) {
+  __shared__ int wave_sum[NT / 64];
+  __shared__ int place[NT];   // where a row of this step goes, or -1
+  __shared__ int start;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r0 = blockIdx.x * a.chunk, r1 = min(r0 + a.chunk, a.rows);
+  int before = 0;
+  for (int r = tid; r < r0; r += NT) before += has_target(a, a.targets[r]) ? 1 : 0;
+  for (int s = 1; s < 64; s *= 2) before += __shfl_xor(before, s);
+  if (lane == 0) wave_sum[wave] = before;
+  __syncthreads();
+  if (tid == 0) {
+    int s = 0;
+    for (int w = 0; w < NT / 64; ++w) s += wave_sum[w];
+    start = s;
+  }
+  __syncthreads();
+  int pos0 = start;
+  for (int b = r0; b < r1; b += NT) {
+    const int r = b + tid;
+    const int64_t t = r < r1 ? a.targets[r] : a.ignore_index;
+    const bool seen = r < r1 && has_target(a, t);
+    const uint64_t votes = __ballot(seen);
+    __syncthreads();
+    if (lane == 0) wave_sum[wave] = __popcll(votes);
+    __syncthreads();
+    int at = pos0 + __popcll(votes & ((uint64_t(1) << lane) - 1)), all = 0;
+    for (int w = 0; w < NT / 64; ++w) {
+      if (w < wave) at += wave_sum[w];
+      all += wave_sum[w];
+    }
+    pos0 += all;
+    if (seen) {
+      a.row[at] = r;
+      a.target[at] = int(t);
+      if (a.lse_in) {
+        const float g = a.grad_loss[r], h = a.grad_lse ? a.grad_lse[r] : 0.f;
+        a.lse_c[at] = a.lse_in[r];
+        a.ga[at] = g + h;
+        a.gb[at] = g;
+      }
+    } else if (r < r1 && a.loss) {
+      const float v = t == a.ignore_index ? 0.f : __builtin_nanf("");
+      a.loss[r] = v;
+      a.lse_out[r] = v;
+    }
+    place[tid] = seen ? at : -1;
+    __syncthreads();
+    // the rows of x, a wave each
+    const int rows = min(NT, r1 - b);
+    const T* x = reinterpret_cast<const T*>(a.x);
+    T* xc = reinterpret_cast<T*>(a.xc);
+    T* gx = reinterpret_cast<T*>(a.grad_x);
+    for (int w = wave; w < rows; w += NT / 64) {
+      const int p = place[w];
+      if (p >= 0) {
+        for (int c = lane; c < a.dim; c += 64) xc[int64_t(p) * a.ld_xc + c] = x[int64_t(b + w) * a.ld_x + c];
+      } else if (gx) {
+        for (int c = lane; c < a.dim; c += 64) gx[int64_t(b + w) * a.ld_grad_x + c] = T(0);
+      }
+    }
+  }
+  if (r1 == a.rows && tid == 0) {
+    a.offsets[0] = 0;
+    a.offsets[1] = pos0;
+  }
+}
+
+// A wave a row: the maximum over the tiles, the sums brought to it.
+__global__ __launch_bounds__(NT) void head_finish_kernel(const HeadFinish a) {
+  const int lane = threadIdx.x & 63;
+  const int i = blockIdx.x * (NT / 64) + (threadIdx.x >> 6);
+  if (i >= min(a.offsets[1], a.rows)) return;
+  const float2* s = a.stats + int64_t(i) * a.tiles;
+  float m = -INFINITY, sum = 0.f;
+  for (int t = lane; t < a.tiles; t += 64) {
+    const float2 v = s[t];
+    const float n = fmaxf(m, v.x), f = n == -INFINITY ? 0.f : n;
+    sum = sum * __expf(m - f) + v.y * __expf(v.x - f);
+    m = n;
+  }
+  for (int d = 1; d < 64; d *= 2) {
+    const float om = __shfl_xor(m, d), os = __shfl_xor(sum, d);
+    const float n = fmaxf(m, om), f = n == -INFINITY ? 0.f : n;
+    sum = sum * __expf(m - f) + os * __expf(om - f);
+    m = n;
+  }
+  if (lane == 0) {
+    const float lse = (m == -INFINITY ? 0.f : m) + logf(sum);
+    const int r = a.row[i];
+    a.lse[r] = lse;
+    a.loss[r] = lse - a.logit[i];
+  }
+}
+
+}  // namespace
+
+hipError_t launch_head_rows(const HeadRows& a, hipStream_t stream) {
+  const unsigned grid = unsigned((a.rows + a.chunk - 1) / a.chunk);
+  if (a.f32) hipLaunchKernelGGL((head_rows_kernel<float>), dim3(grid), dim3(NT), 0, stream, a);
+  else hipLaunchKernelGGL((head_rows_kernel<uint16_t>), dim3(grid), dim3(NT), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_finish(const HeadFinish& a, hipStream_t stream) {
+  hipLaunchKernelGGL(head_finish_kernel, dim3(unsigned((a.rows + NT / 64 - 1) / (NT / 64))), dim3(NT), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace muon

@@ -807,6 +807,7 @@ struct BlockDevice {
   hipEvent_t fork[MAX_PARTS - 1] = {}, join[MAX_PARTS - 1] = {};
 };
 std::map<int, BlockDevice> g_blocks;  // under api_mutex()
+void (*g_next_release)() = nullptr;   // of another file that keeps state
 
 void release_blocks() {
   for (auto& kv : g_blocks) {
@@ -821,9 +822,13 @@ void release_blocks() {
     }
   }
   g_blocks.clear();
+  if (g_next_release) g_next_release();
 }
 struct HookRelease {
-  HookRelease() { api_release_hook = release_blocks; }
+  HookRelease() {
+    g_next_release = api_release_hook;
+    api_release_hook = release_blocks;
+  }
 } g_hook_release;
 
 muon_status current_device(BlockDevice** out) {

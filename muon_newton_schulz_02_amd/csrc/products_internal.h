@@ -1,0 +1,97 @@
+// Types shared by the host side of the expert products and of the head's loss
+// (muon_experts.h, muon_head.h) and their kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace muon {
+
+// C[i][j] = sum_k P[i][k] Q[j][k] (i < m, j < n), the form of every product
+// here.  An operand lies in row form (k contiguous) or in k-row form (the rows of
+// C, or its columns, contiguous):
+//   NT  P and Q in row form      y = x W^T, logits
+//   NN  P row form, Q k-row      grad_x = grad_y W
+//   TN  both k-row form          grad_W = grad_y^T x
+enum ProductForm : int { FORM_NT = 0, FORM_NN = 1, FORM_TN = 2 };
+
+// What becomes of C.
+//   STORE  out = C + addend, rounded to out's type
+//   LSE    a maximum and a sum of exponentials for every row and tile of columns,
+//          and the target's logit
+//   DZ     the gradient of the loss with respect to the logits C
+enum ProductEpilogue : int { EPI_STORE = 0, EPI_LSE = 1, EPI_DZ = 2 };
+
+// One launch.  Groups (experts) split the rows of P and C for NT and NN, and k
+// for TN: group g has rows [offsets[g], offsets[g + 1]) of P (TN: of P and Q),
+// offsets clamped to [0, rows].  Strides are in elements.
+struct ProductArgs {
+  const void* p;
+  const void* q;
+  void* out;
+  const void* add;             // addend, in add's type and out's layout (no map), or null
+  const int32_t* offsets;      // groups + 1, or null: one group of all rows
+  const int32_t* map;          // row of `out` for a row of C, or null
+  int64_t ld_p, ld_q, ld_out, ld_add;
+  int64_t es_q, es_out;        // from one group's Q (NT, NN) or out (TN) to the next
+  int64_t p_elems;             // elements from p's first to the end of its last row
+  int64_t q_elems;             // the same for q (NT, NN: for one group's)
+  int32_t groups, rows;
+  int32_t m, n, k;             // m: TN; k: NT and NN
+  int32_t f32;                 // type of p and q: 1 binary32, 0 bfloat16
+  int32_t out_f32, add_f32;
+  // head
+  float cap, inv_cap;          // soft cap (0: none)
+  int32_t col0;                // vocabulary index of column 0
+  int32_t stat_tiles;          // tiles of columns of a row of `stats`
+  const int32_t* target;       // of every row of C
+  const float* lse;
+  const float* ga;             // grad_loss + grad_lse
+  const float* gb;             // grad_loss
+  float* logit;                // the target's logit (soft-capped)
+  float2* stats;               // [row][tile]: maximum, sum of exp(z - maximum)
+};
+
+// Columns of a tile of `stats` that launch_product writes.
+int32_t product_tile_n(int form, const ProductArgs& a);
+hipError_t launch_product(int form, int epi, const ProductArgs& a, int cus, hipStream_t stream);
+
+// The head's rows that have a target, packed: offsets = {0, their number}, and
+// for each its row, target, and (gradient) lse, ga and gb; the rows of x copied to
+// xc.  Writes what rows without a target get: loss and lse (forward), grad_x.
+struct HeadRows {
+  const void* x;
+  const int64_t* targets;
+  const float* lse_in;
+  const float* grad_loss;
+  const float* grad_lse;       // may be null
+  void* xc;
+  int32_t* offsets;
+  int32_t* row;
+  int32_t* target;
+  float* lse_c;
+  float* ga;
+  float* gb;
+  float* loss;                 // forward: written where there is no target
+  float* lse_out;
+  void* grad_x;                // gradient: zeroed where there is no target; may be null
+  int64_t ld_x, ld_xc, ld_grad_x;
+  int64_t ignore_index, vocab;
+  int32_t rows, dim, f32;
+  int32_t chunk;               // rows of a workgroup
+};
+hipError_t launch_head_rows(const HeadRows& a, hipStream_t stream);
+
+// loss and lse of the packed rows from the tiles' maxima and sums.
+struct HeadFinish {
+  const float2* stats;
+  const float* logit;
+  const int32_t* offsets;
+  const int32_t* row;
+  float* loss;
+  float* lse;
+  int32_t tiles, rows;
+};
+hipError_t launch_head_finish(const HeadFinish& a, hipStream_t stream);
+
+}  // namespace muon

@@ -8,3 +8,4 @@ from .muon_oracle import (EPS, StepResult, frobenius_norm, momentum, muon_step, 
                           write_back)
 from .adamw_oracle import adamw, adamw_constants  # noqa: F401
 from .blocks_oracle import orthogonalise_vjp  # noqa: F401
+from . import training_oracle as training  # noqa: F401

@@ -1,0 +1,285 @@
+"""Products grouped by expert and their gradients on the GPU, against float64.
+
+Tolerance of every element: half a step of the result's type, and u = 2^-24
+times (terms + 4) times the sum of |products| for binary32 sums, with four more
+for binary32 operands that are multiplied in parts."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as orc
+from muon_newton_schulz_02_amd import binding as mb
+
+pytestmark = pytest.mark.gpu
+U = orc.training.U
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def check(got, want, reach, terms, dtype, what=""):
+    step = torch.finfo(dtype).eps / 2
+    tol = step * np.abs(want) + (1 + step) * (terms + 8) * U * reach + 1e-45
+    off = np.abs(np64(got) - want)
+    assert not np.isnan(off).any(), f"{what}: NaN"
+    worst = (off / tol).max() if off.size else 0.0
+    assert worst <= 1, f"{what}: {worst:.3g} times the tolerance"
+
+
+def matrix(rows, cols, dtype, gen, pad=0, scale=1.0, lead=0):
+    """rows x cols in a wider buffer whose padding holds NaN, `lead` elements after its start."""
+    buf = torch.full((lead + rows * (cols + pad),), float("nan"), dtype=dtype)
+    t = buf[lead:].view(rows, cols + pad)[:, :cols]
+    t.copy_(torch.randn(rows, cols, generator=gen) * scale)
+    dev = buf.cuda()
+    return dev[lead:].view(rows, cols + pad)[:, :cols]
+
+
+def stack(experts, out, inn, dtype, gen, order=mb.WEIGHT_OUT_IN, pad=0, lead=0):
+    rows, cols = (out, inn) if order == mb.WEIGHT_OUT_IN else (inn, out)
+    t = matrix(experts * rows, cols, dtype, gen, pad, inn ** -0.5, lead).unflatten(0, (experts, rows))
+    return t if order == mb.WEIGHT_OUT_IN else t.transpose(1, 2)
+
+
+def offsets_of(counts, first=0):
+    return torch.tensor(np.concatenate([[first], first + np.cumsum(counts)]).astype(np.int32), device="cuda")
+
+
+def run_all(counts, inn, out, dtype, *, spare=0, first=0, order=mb.WEIGHT_OUT_IN, pad=0, lead=0, gw_dtype=None, seed=0):
+    """Forward and both gradients; every element checked, and what belongs to no expert left as it was."""
+    dt = DTYPES[dtype]
+    gen = torch.Generator().manual_seed(seed)
+    experts, rows = len(counts), first + int(sum(counts)) + spare
+    off = offsets_of(counts, first)
+    x, gy = matrix(rows, inn, dt, gen, pad, lead=lead), matrix(rows, out, dt, gen, pad, lead=lead)
+    free = torch.ones(rows, dtype=torch.bool)
+    free[first:first + int(sum(counts))] = False
+    x[free.cuda()] = float("nan")            # rows of no expert
+    gy[free.cuda()] = float("nan")
+    w = stack(experts, out, inn, dt, gen, order, pad, lead)
+    y, gx = matrix(rows, out, dt, gen, pad, lead=lead), matrix(rows, inn, dt, gen, pad, lead=lead)
+    gdt = dt if gw_dtype is None else DTYPES[gw_dtype]
+    gw = stack(experts, out, inn, gdt, gen, order, pad, lead)
+    y0, gx0, gw0 = y.clone(), gx.clone(), gw.clone()
+    mb.muon_experts_product(x, w, off, y)
+    mb.muon_experts_product_vjp(x, w, off, gy, gx, gw)
+    torch.cuda.synchronize()
+    o = off.cpu().numpy()
+    keep = ~free.numpy()
+    xs, gys, ws = np.nan_to_num(np64(x)), np.nan_to_num(np64(gy)), np64(w)
+    want, reach = orc.training.experts(xs, ws, o)
+    check(y[keep], want[keep], reach[keep], inn, dt, "y")
+    want, reach = orc.training.experts(gys, ws.transpose(0, 2, 1), o)
+    check(gx[keep], want[keep], reach[keep], out, dt, "grad_x")
+    want, reach = orc.training.experts_grad_w(xs, gys, o)
+    check(gw, want, reach, max(counts, default=0), gdt, "grad_w")
+    assert torch.equal(y[~keep], y0[~keep]) and torch.equal(gx[~keep], gx0[~keep])
+    # once more, added to
+    gw.copy_(gw0)
+    mb.muon_experts_product_vjp(x, None, off, gy, grad_w=gw, accumulate=True)
+    check(gw, np64(gw0) + want, reach + np.abs(np64(gw0)), max(counts, default=0) + 1, gdt, "grad_w, accumulated")
+    return x, w, off, gy, y, gx, gw
+
+
+SHAPES = [
+    # counts, in, out
+    ([1], 1, 1),
+    ([3], 2, 5),
+    ([1], 64, 32),
+    ([0], 40, 24),
+    ([2, 0, 1], 7, 9),
+    ([5, 3], 8, 8),
+    ([17, 0, 0, 33, 1], 63, 65),
+    ([64, 128], 64, 64),
+    ([100, 257, 31], 129, 255),
+    ([255, 256, 257], 200, 333),
+    ([1, 1, 1, 1, 1, 1, 1, 1], 512, 96),
+    ([300, 5, 0, 700], 520, 264),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,inn,out", SHAPES)
+def test_sizes(counts, inn, out, dtype):
+    run_all(counts, inn, out, dtype, spare=3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("order", [mb.WEIGHT_OUT_IN, mb.WEIGHT_IN_OUT])
+@pytest.mark.parametrize("pad,lead", [(0, 0), (1, 0), (8, 0), (3, 1), (0, 1), (0, 8)])
+def test_orders_strides_and_alignment(pad, lead, order, dtype):
+    run_all([70, 0, 131], 96, 72, dtype, spare=2, first=5, order=order, pad=pad, lead=lead)
+    run_all([40, 21], 77, 131, dtype, order=order, pad=pad, lead=lead)
+
+
+def test_large_tiles_and_long_sums():
+    run_all([700, 0, 2000, 1348], 1536, 520, "bf16", spare=1)
+    run_all([4100, 9], 264, 776, "bf16")
+    run_all([1100, 300], 400, 392, "f32")
+
+
+def test_many_experts():
+    counts = np.random.default_rng(3).integers(0, 4, 2048).tolist()
+    run_all(counts, 24, 40, "bf16")
+
+
+@pytest.mark.parametrize("gw_dtype", ["bf16", "f32"])
+def test_gradient_type(gw_dtype):
+    run_all([90, 3, 200], 136, 120, "bf16", gw_dtype=gw_dtype)
+
+
+def test_gradients_against_differences():
+    """<y, gy> is linear in x and in w: differences of it are exact but for rounding."""
+    gen = torch.Generator().manual_seed(1)
+    x, w = matrix(30, 20, torch.float32, gen), stack(3, 12, 20, torch.float32, gen)
+    gy, off = matrix(30, 12, torch.float32, gen), offsets_of([9, 0, 20])
+    gx, gw = torch.zeros_like(x), torch.zeros(3, 12, 20, device="cuda")
+    mb.muon_experts_product_vjp(x, w, off, gy, gx, gw)
+
+    def value(x, w):
+        y = torch.zeros(30, 12, device="cuda")
+        mb.muon_experts_product(x, w, off, y)
+        return (y.double() * gy.double())[:29].sum().item()
+
+    dx, dw = torch.randn(30, 20, generator=gen).cuda(), torch.randn(3, 12, 20, generator=gen).cuda()
+    # |y| and |gy| of order 1 to 4, 348 elements, binary32 results: 348 * 16 * 2^-23 = 7e-4, and as much from x + dx
+    assert abs(value(x + dx, w) - value(x, w) - (gx.double() * dx.double())[:29].sum().item()) < 1.5e-3
+    assert abs(value(x, w + dw) - value(x, w) - (gw.double() * dw.double()).sum().item()) < 1.5e-3
+
+
+@pytest.mark.parametrize("offsets", [
+    [0, 5, 3, 9], [-7, 4, 6, 9], [0, 4, 1000000, 8], [9, 9, 9, 9], [2, 30, 30, 30], [-2147483648, 2147483647, 0, 5],
+])
+def test_offsets_that_are_no_offsets_stay_in_range(offsets):
+    """Whatever the offsets hold: rows outside every expert's clamped range stay, a row inside one range has its value."""
+    gen = torch.Generator().manual_seed(2)
+    rows, inn, out = 12, 16, 24
+    x, w = matrix(rows, inn, torch.bfloat16, gen), stack(3, out, inn, torch.bfloat16, gen)
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    y = torch.full((rows, out), 77.0, dtype=torch.bfloat16, device="cuda")
+    mb.muon_experts_product(x, w, off, y)
+    torch.cuda.synchronize()
+    lo = [min(max(o, 0), rows) for o in offsets[:3]]
+    hi = [max(a, min(o, rows)) for a, o in zip(lo, offsets[1:])]
+    for r in range(rows):
+        mine = [e for e in range(3) if lo[e] <= r < hi[e]]
+        if not mine:
+            assert (y[r] == 77.0).all()
+        elif len(mine) == 1:
+            want, reach = orc.training.experts(np64(x[r:r + 1]), np64(w[mine[0]:mine[0] + 1]), [0, 1])
+            check(y[r:r + 1], want, reach, inn, torch.bfloat16, f"row {r}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nan_and_infinity_stay_in_their_rows(dtype):
+    gen = torch.Generator().manual_seed(4)
+    dt = DTYPES[dtype]
+    x, w, gy = matrix(300, 72, dt, gen), stack(3, 40, 72, dt, gen), matrix(300, 40, dt, gen)
+    off = offsets_of([100, 100, 100])
+    x[7, 71] = float("nan")
+    x[150, 0] = float("inf")
+    y, gw = torch.zeros(300, 40, dtype=dt, device="cuda"), torch.zeros(3, 40, 72, dtype=dt, device="cuda")
+    mb.muon_experts_product(x, w, off, y)
+    mb.muon_experts_product_vjp(x, None, off, gy, grad_w=gw)
+    bad = ~torch.isfinite(y).all(1)
+    assert bad.nonzero().flatten().tolist() == [7, 150] and torch.isnan(y[7]).all()
+    hit = ~torch.isfinite(gw)
+    want = torch.zeros_like(hit)
+    want[0, :, 71] = True
+    want[1, :, 0] = True
+    assert torch.equal(hit, want)
+
+
+def test_shared_and_interleaved_weights():
+    """One weight for all experts (stride 0), and experts beside each other in the same rows."""
+    gen = torch.Generator().manual_seed(5)
+    x, off = matrix(50, 40, torch.bfloat16, gen), offsets_of([20, 30])
+    one = stack(1, 24, 40, torch.bfloat16, gen)
+    y = torch.zeros(50, 24, dtype=torch.bfloat16, device="cuda")
+    mb.muon_experts_product(x, one.expand(2, 24, 40), off, y)
+    want, reach = orc.training.experts(np64(x), np.repeat(np64(one), 2, 0), [0, 20, 50])
+    check(y, want, reach, 40, torch.bfloat16)
+    wide = matrix(24, 80, torch.bfloat16, gen)
+    w = wide.unflatten(1, (2, 40)).transpose(0, 1)          # (2, 24, 40), rows 80 apart
+    mb.muon_experts_product(x, w, off, y)
+    want, reach = orc.training.experts(np64(x), np64(w), [0, 20, 50])
+    check(y, want, reach, 40, torch.bfloat16)
+    gy = matrix(50, 24, torch.bfloat16, gen)
+    gwide = torch.zeros(24, 80, device="cuda")
+    mb.muon_experts_product_vjp(x, None, off, gy, grad_w=gwide.unflatten(1, (2, 40)).transpose(0, 1))
+    want, reach = orc.training.experts_grad_w(np64(x), np64(gy), [0, 20, 50])
+    check(gwide.unflatten(1, (2, 40)).transpose(0, 1), want, reach, 30, torch.float32)
+
+
+def test_no_rows_at_all():
+    w, off = torch.ones(3, 8, 16, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    x, gy = torch.zeros(0, 16, device="cuda"), torch.zeros(0, 8, device="cuda")
+    gw = torch.full((3, 8, 16), 5.0, device="cuda")
+    mb.muon_experts_product(x, w, off, torch.zeros(0, 8, device="cuda"))
+    mb.muon_experts_product_vjp(x, w, off, gy, grad_w=gw, accumulate=True)
+    assert (gw == 5.0).all()
+    mb.muon_experts_product_vjp(x, w, off, gy, grad_w=gw)
+    assert (gw == 0.0).all()
+
+
+def test_same_bits_captured_and_on_other_streams():
+    gen = torch.Generator().manual_seed(6)
+    counts = [130, 0, 270, 41]
+    x, w, gy = matrix(441, 264, torch.bfloat16, gen), stack(4, 136, 264, torch.bfloat16, gen), matrix(441, 136, torch.bfloat16, gen)
+    off = offsets_of(counts)
+    outs = [[torch.zeros(441, 136, dtype=torch.bfloat16, device="cuda"), torch.zeros(441, 264, dtype=torch.bfloat16, device="cuda"),
+             torch.zeros(4, 136, 264, device="cuda")] for _ in range(3)]
+    fwd = [mb.ExpertsArgs(x, w, off, o[0]) for o in outs]
+    bwd = [mb.ExpertsVjpArgs(x, w, off, gy, o[1], o[2]) for o in outs]
+    ws = [torch.empty(max(1, fwd[0].workspace_bytes(), bwd[0].workspace_bytes()), dtype=torch.uint8, device="cuda") for _ in range(2)]
+
+    def both(i, ws=None, stream=None):
+        mb.muon_experts_product(fwd[i], workspace=ws, stream=stream)
+        mb.muon_experts_product_vjp(bwd[i], workspace=ws, stream=stream)
+
+    both(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    both(1, ws[0], side)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        both(2, ws[1])
+    for _ in range(3):
+        for t in outs[2]:
+            t.fill_(3.0)
+        graph.replay()
+        both(1, ws[0], side)
+        torch.cuda.synchronize()
+        for i in (1, 2):
+            assert all(torch.equal(a, b) for a, b in zip(outs[0], outs[i]))
+    # new routing without a new capture: the offsets are read when the kernels run
+    off.copy_(offsets_of([10, 200, 0, 231]))
+    graph.replay()
+    both(0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs[0], outs[2]))
+
+
+def test_binding_refusals():
+    x, off = torch.zeros(4, 8, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    w, y = torch.zeros(2, 6, 8, device="cuda"), torch.zeros(4, 6, device="cuda")
+    for bad in [dict(off=off.long()), dict(off=off[None]), dict(w=w.bfloat16()), dict(w=w[:1]), dict(y=y[:3]),
+                dict(x=x.t()), dict(y=torch.zeros(4, 12, device="cuda")[:, ::2]),
+                dict(w=torch.zeros(2, 12, 16, device="cuda")[:, ::2, ::2]), dict(w=w.cpu())]:
+        a = dict(dict(x=x, w=w, off=off, y=y), **bad)
+        with pytest.raises((ValueError, TypeError)):
+            mb.muon_experts_product(a["x"], a["w"], a["off"], a["y"])
+    gy, gx, gw = torch.zeros(4, 6, device="cuda"), torch.zeros(4, 8, device="cuda"), torch.zeros(2, 6, 8, device="cuda")
+    with pytest.raises(ValueError, match="both None"):
+        mb.muon_experts_product_vjp(x, w, off, gy)
+    with pytest.raises(ValueError, match="needs w"):
+        mb.muon_experts_product_vjp(x, None, off, gy, gx)
+    with pytest.raises(ValueError, match="needs x"):
+        mb.muon_experts_product_vjp(None, w, off, gy, None, gw)
+    with pytest.raises(ValueError, match="order"):
+        mb.muon_experts_product_vjp(x, w, off, gy, gx, torch.zeros(2, 8, 6, device="cuda").transpose(1, 2))
+    with pytest.raises(ValueError, match="holds every tensor"):
+        mb.muon_experts_product(mb.ExpertsArgs(x, w, off, y), w)

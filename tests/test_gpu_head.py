@@ -1,0 +1,278 @@
+"""The head's loss and its gradient on the GPU, against float64, with the bounds
+that oracle/training_oracle.py derives; and one training step of experts and head
+through to the optimizer's calls."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as orc
+from muon_newton_schulz_02_amd import binding as mb
+
+pytestmark = pytest.mark.gpu
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def matrix(rows, cols, dtype, gen, pad=0, scale=1.0, lead=0):
+    """rows x cols in a wider buffer whose padding holds NaN, `lead` elements after its start."""
+    buf = torch.full((lead + rows * (cols + pad),), float("nan"), dtype=dtype)
+    t = buf[lead:].view(rows, cols + pad)[:, :cols]
+    t.copy_(torch.randn(rows, cols, generator=gen) * scale)
+    return buf.cuda()[lead:].view(rows, cols + pad)[:, :cols]
+
+
+def check(got, want, tol, dtype, what):
+    step = torch.finfo(dtype).eps / 2
+    tol = tol + step * (np.abs(want) + tol) + 1e-45
+    g = np64(got)
+    assert np.array_equal(np.isnan(g), np.isnan(want)), f"{what}: NaN in other places"
+    with np.errstate(invalid="ignore"):
+        worst = np.nanmax(np.abs(g - want) / tol) if g.size else 0.0
+    assert worst <= 1, f"{what}: {worst:.3g} times the tolerance"
+
+
+def case(rows, dim, vocab, dtype, *, cap=0.0, ignored=0.0, pad=0, lead=0, scale=1.0, seed=0, lse_too=True, stray=False):
+    dt = DTYPES[dtype]
+    gen = torch.Generator().manual_seed(seed)
+    x, w = matrix(rows, dim, dt, gen, pad, scale, lead), matrix(vocab, dim, dt, gen, pad, dim ** -0.5 * 2, lead)
+    t = torch.randint(vocab, (rows,), generator=gen)
+    t[torch.rand(rows, generator=gen) < ignored] = -100
+    if stray and rows > 2:
+        t[0], t[rows // 2] = vocab, -5
+    off = (t < 0) | (t >= vocab)
+    x[off.cuda()] = float("nan")                   # what ignored rows hold does not matter
+    g, h = torch.randn(rows, generator=gen), torch.randn(rows, generator=gen)
+    g[off] = float("nan")
+    h[off] = float("inf")
+    t, g, h = t.cuda(), g.cuda(), (h.cuda() if lse_too else None)
+    loss, lse = (torch.full((rows,), 7.0, device="cuda") for _ in range(2))
+    gx, gw = matrix(rows, dim, dt, gen, pad, lead=lead), matrix(vocab, dim, dt, gen, pad, lead=lead)
+    mb.muon_head_loss(x, w, t, loss, lse, softcap=cap)
+    mb.muon_head_loss_vjp(x, w, t, lse, g, gx, gw, grad_lse=h, softcap=cap)
+    torch.cuda.synchronize()
+    want = orc.training.head(np.nan_to_num(np64(x)), np64(w), t.cpu().numpy(), cap, -100, np.nan_to_num(np64(g)),
+                             None if h is None else np.nan_to_num(np64(h), posinf=0.0),
+                             half_step=torch.finfo(dt).eps / 2)
+    for name, got, odt in (("loss", loss, torch.float32), ("lse", lse, torch.float32), ("grad_x", gx, dt), ("grad_w", gw, dt)):
+        check(got, want[name], want["tol_" + name], odt, name)
+    return x, w, t, lse, g, h, gx, gw
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cap", [0.0, 15.0])
+@pytest.mark.parametrize("rows,dim,vocab", [
+    (1, 1, 1), (1, 8, 2), (2, 3, 5), (1, 64, 1000), (5, 40, 257), (64, 64, 256), (65, 129, 1023), (300, 96, 2500),
+    (257, 200, 4097),
+])
+def test_sizes(rows, dim, vocab, cap, dtype):
+    case(rows, dim, vocab, dtype, cap=cap)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pad,lead", [(1, 0), (8, 0), (3, 1), (0, 1)])
+def test_strides_and_alignment(pad, lead, dtype):
+    case(70, 72, 600, dtype, cap=15.0, ignored=0.2, pad=pad, lead=lead)
+    case(33, 77, 515, dtype, ignored=0.2, pad=pad, lead=lead)
+
+
+@pytest.mark.parametrize("ignored", [0.1, 0.9, 1.1])
+@pytest.mark.parametrize("rows", [7, 700])
+def test_ignored_rows(rows, ignored):
+    case(rows, 48, 900, "bf16", ignored=ignored, stray=True)
+    case(rows, 48, 900, "f32", ignored=ignored, stray=True, lse_too=False)
+
+
+def test_a_vocabulary_in_pieces():
+    """More columns than one piece of the gradient holds."""
+    case(3, 16, 300_001, "bf16", cap=30.0)
+    x, w, t, lse, g, h, gx, gw = case(900, 264, 5000, "bf16", ignored=0.1)
+    args = mb.HeadLossVjpArgs(x, w, t, lse, g, gx, gw, grad_lse=h)
+    assert args.workspace_bytes() >= 2 * 900 * 5000
+
+
+def test_large_logits_and_sure_rows():
+    """Logits up to some hundreds: no overflow, p of 1 and 0."""
+    case(64, 64, 700, "f32", scale=60.0)
+    case(64, 64, 700, "bf16", scale=60.0, cap=15.0)
+
+
+def test_non_finite_logits():
+    gen = torch.Generator().manual_seed(3)
+    x, w = matrix(6, 32, torch.float32, gen), matrix(90, 32, torch.float32, gen)
+    x[1, 3] = float("nan")
+    x[2, 0] = float("inf")
+    t = torch.zeros(6, dtype=torch.int64, device="cuda")
+    loss, lse = torch.zeros(6, device="cuda"), torch.zeros(6, device="cuda")
+    mb.muon_head_loss(x, w, t, loss, lse)
+    assert torch.isfinite(loss[[0, 3, 4, 5]]).all() and torch.isnan(loss[1]) and not torch.isfinite(loss[2])
+    gx = torch.zeros_like(x)
+    mb.muon_head_loss_vjp(x, w, t, lse, torch.ones(6, device="cuda"), gx)
+    assert torch.isfinite(gx[[0, 3, 4, 5]]).all() and torch.isnan(gx[1]).all() and torch.isnan(gx[2]).all()
+
+
+def test_gradient_against_differences():
+    """binary32, a step of 2^-6 along a direction: the central difference is off by its third derivative, h^2 / 6 times
+    some units, 4e-5 times 10, and the rounding of the loss over the step, 40 rows of 2^-23 * 8 / 2^-6 = 2.4e-3."""
+    gen = torch.Generator().manual_seed(8)
+    x, w = matrix(40, 24, torch.float32, gen), matrix(300, 24, torch.float32, gen, scale=0.3)
+    t = torch.randint(300, (40,), generator=gen).cuda()
+    g = torch.rand(40, generator=gen).cuda()
+
+    def value(x, w):
+        loss, lse = torch.zeros(40, device="cuda"), torch.zeros(40, device="cuda")
+        mb.muon_head_loss(x, w, t, loss, lse, softcap=4.0)
+        return (loss.double() * g.double()).sum().item(), lse
+
+    gx, gw = torch.zeros_like(x), torch.zeros_like(w)
+    mb.muon_head_loss_vjp(x, w, t, value(x, w)[1], g, gx, gw, softcap=4.0)
+    h = 2.0 ** -6
+    for a, grad in ((0, gx), (1, gw)):
+        d = torch.randn(*grad.shape, generator=gen).cuda()
+        d /= d.norm()
+        up, down = ((x + s * h * d, w) if a == 0 else (x, w + s * h * d) for s in (1, -1))
+        assert abs((value(*up)[0] - value(*down)[0]) / (2 * h) - (grad.double() * d.double()).sum().item()) < 3e-3
+
+
+def test_one_gradient_at_a_time_is_the_same():
+    x, w, t, lse, g, h, gx, gw = case(130, 96, 1500, "bf16", ignored=0.2)
+    a, b = torch.zeros_like(gx), torch.zeros_like(gw)
+    mb.muon_head_loss_vjp(x, w, t, lse, g, a, None, grad_lse=h)
+    mb.muon_head_loss_vjp(x, w, t, lse, g, None, b, grad_lse=h)
+    assert torch.equal(a, gx) and torch.equal(b, gw)
+
+
+def test_no_rows():
+    w, gw = torch.ones(30, 16, device="cuda"), torch.full((30, 16), 3.0, device="cuda")
+    x, t, f = torch.zeros(0, 16, device="cuda"), torch.zeros(0, dtype=torch.int64, device="cuda"), torch.zeros(0, device="cuda")
+    mb.muon_head_loss(x, w, t, f, f.clone())
+    mb.muon_head_loss_vjp(x, w, t, f, f, None, gw)
+    assert (gw == 0).all()
+
+
+def test_captured_with_workspaces_and_streams():
+    gen = torch.Generator().manual_seed(6)
+    rows, dim, vocab = 150, 72, 1300
+    x, w = matrix(rows, dim, torch.bfloat16, gen), matrix(vocab, dim, torch.bfloat16, gen)
+    t = torch.randint(vocab, (rows,), generator=gen).cuda()
+    t[::7] = -100
+    g = torch.full((rows,), 1 / rows, device="cuda")
+    sets = []
+    for _ in range(3):
+        loss, lse = torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda")
+        gx, gw = torch.zeros(rows, dim, dtype=torch.bfloat16, device="cuda"), torch.zeros(vocab, dim, dtype=torch.bfloat16, device="cuda")
+        sets.append((mb.HeadLossArgs(x, w, t, loss, lse), mb.HeadLossVjpArgs(x, w, t, lse, g, gx, gw), (loss, lse, gx, gw)))
+    need = max(sets[0][0].workspace_bytes(), sets[0][1].workspace_bytes())
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
+
+    def both(i, ws=None, stream=None):
+        mb.muon_head_loss(sets[i][0], softcap=15.0, workspace=ws, stream=stream)
+        mb.muon_head_loss_vjp(sets[i][1], softcap=15.0, workspace=ws, stream=stream)
+
+    both(0)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(2, ws[1])
+    for _ in range(3):
+        for o in sets[2][2]:
+            o.fill_(9.0)
+        graph.replay()
+        both(1, ws[0], side)
+        both(0)
+        torch.cuda.synchronize()
+        for i in (1, 2):
+            assert all(torch.equal(a, b) for a, b in zip(sets[0][2], sets[i][2]))
+    with pytest.raises(mb.MuonError, match="holds"):
+        mb.muon_head_loss(sets[0][0], workspace=ws[0][:256])
+    with pytest.raises(mb.MuonError, match="captured"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            mb.muon_head_loss(sets[0][0])
+    torch.cuda.synchronize()
+
+
+def test_library_workspace_orders_streams_and_is_released():
+    gen = torch.Generator().manual_seed(7)
+    x, w = matrix(200, 64, torch.float32, gen), matrix(900, 64, torch.float32, gen)
+    t = torch.randint(900, (200,), generator=gen).cuda()
+    outs = [(torch.zeros(200, device="cuda"), torch.zeros(200, device="cuda")) for _ in range(6)]
+    torch.cuda.synchronize()
+    for i, (loss, lse) in enumerate(outs):
+        if i == 3:
+            torch.cuda.synchronize()
+            mb.muon_release_workspace()
+        mb.muon_head_loss(x, w, t, loss, lse, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert all(torch.equal(outs[0][k], o[k]) for o in outs for k in (0, 1))
+
+
+def test_allocation_failure_changes_nothing(monkeypatch):
+    gen = torch.Generator().manual_seed(9)
+    x, w = matrix(20, 16, torch.float32, gen), matrix(50, 16, torch.float32, gen)
+    t = torch.randint(50, (20,), generator=gen).cuda()
+    loss, lse = torch.full((20,), 4.0, device="cuda"), torch.full((20,), 4.0, device="cuda")
+    mb.muon_release_workspace()
+    monkeypatch.setenv("MUON_FAULT_ALLOC", "1")
+    with pytest.raises(mb.MuonError) as e:
+        mb.muon_head_loss(x, w, t, loss, lse)
+    assert e.value.status == mb.MUON_ERR_OUT_OF_MEMORY and (loss == 4.0).all()
+    monkeypatch.delenv("MUON_FAULT_ALLOC")
+    mb.muon_head_loss(x, w, t, loss, lse)
+    assert (loss != 4.0).all()
+
+
+def test_binding_refusals():
+    x, w = torch.zeros(4, 8, device="cuda"), torch.zeros(9, 8, device="cuda")
+    t, f = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.zeros(4, device="cuda")
+    for bad in [dict(t=t.int()), dict(t=t[:3]), dict(w=w.bfloat16()), dict(loss=f.double()), dict(lse=f[:2]), dict(x=x.t()),
+                dict(w=w.cpu()), dict(loss=torch.zeros(8, device="cuda")[::2])]:
+        a = dict(dict(x=x, w=w, t=t, loss=f, lse=f.clone()), **bad)
+        with pytest.raises((ValueError, TypeError)):
+            mb.muon_head_loss(a["x"], a["w"], a["t"], a["loss"], a["lse"])
+    with pytest.raises(ValueError, match="both None"):
+        mb.muon_head_loss_vjp(x, w, t, f, f)
+    with pytest.raises(mb.MuonError, match="softcap"):
+        mb.muon_head_loss(x, w, t, f, f.clone(), softcap=-1.0)
+
+
+def test_a_training_step_from_experts_to_the_optimizer():
+    """Experts, the head's loss, their gradients, then the Muon step on the experts and AdamW on the head, as a program
+    has them; the gradients against float64 through the whole chain."""
+    gen = torch.Generator().manual_seed(11)
+    experts, inner, outer, vocab, rows = 4, 96, 64, 700, 240
+    counts = [100, 0, 90, 50]
+    off = torch.tensor(np.cumsum([0] + counts).astype(np.int32), device="cuda")
+    w = matrix(experts * outer, inner, torch.float32, gen, scale=inner ** -0.5).view(experts, outer, inner)
+    head = matrix(vocab, outer, torch.float32, gen, scale=outer ** -0.5)
+    x = matrix(rows, inner, torch.float32, gen)
+    t = torch.randint(vocab, (rows,), generator=gen).cuda()
+    t[::5] = -100
+    g = torch.full((rows,), 1.0 / int((t >= 0).sum()), device="cuda")
+    y, gy = torch.zeros(rows, outer, device="cuda"), torch.zeros(rows, outer, device="cuda")
+    loss, lse = torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda")
+    gw, gh, gx = torch.zeros_like(w), torch.zeros_like(head), torch.zeros_like(x)
+    mb.muon_experts_product(x, w, off, y)
+    mb.muon_head_loss(y, head, t, loss, lse, softcap=15.0)
+    mb.muon_head_loss_vjp(y, head, t, lse, g, gy, gh, softcap=15.0)
+    mb.muon_experts_product_vjp(x, w, off, gy, gx, gw)
+    xd, wd, hd = (v.detach().double().cpu().requires_grad_(True) for v in (x, w, head))
+    yd = torch.cat([xd[a:b] @ wd[e].t() for e, (a, b) in enumerate(zip(off[:-1].tolist(), off[1:].tolist()))])
+    z = 15.0 * torch.tanh(yd @ hd.t() / 15.0)
+    ref = torch.nn.functional.cross_entropy(z, t.cpu(), ignore_index=-100)
+    ref.backward()
+    assert abs((loss.double() * g.double()).sum().item() - ref.item()) < 1e-5     # 192 losses of 7, 2^-22 relative each
+    for name, got, want in (("head", gh, hd.grad), ("experts", gw, wd.grad), ("x", gx, xd.grad)):
+        # binary32 through three products of 64 to 700 terms: (64 + 700 + 96) 2^-24 = 5e-5 at the very most
+        err = (got.double().cpu() - want).norm() / want.norm()
+        assert err < 5e-5, (name, err)
+    w0, h0 = w.clone(), head.clone()
+    mom, m1, m2 = torch.zeros_like(w), torch.zeros_like(head), torch.zeros_like(head)
+    mb.muon_step_blocks([w], [gw], [mom], lr=0.02, beta=0.95, nesterov=True, ns_coeffs=(3.4445, -4.7750, 2.0315), ns_steps=5)
+    mb.muon_adamw_batched([head.view(-1)], [gh.view(-1)], [m1.view(-1)], [m2.view(-1)], lr=1e-3, beta1=0.9, beta2=0.95,
+                          eps=1e-8, weight_decay=0.0, step=1)
+    torch.cuda.synchronize()
+    assert torch.equal(mom, gw) and not torch.equal(w[0], w0[0]) and torch.equal(w[1], w0[1])   # expert 1 had no rows
+    assert not torch.equal(head, h0) and torch.isfinite(w).all() and torch.isfinite(head).all()
