@@ -144,7 +144,7 @@ ProductArgs logits_args(const Call& c, const Plan& p, char* ws, int64_t c0, int6
   return a;
 }
 
-Plan plan_of(const Call& c) {
+Plan plan_of(const Call& c, int cus) {
   const muon_head_desc& d = *c.desc;
   Plan p = {};
   size_t at = 0;
@@ -161,7 +161,7 @@ Plan plan_of(const Call& c) {
   p.xc = take(t * p.ld_xc * esz);
   if (c.op == MUON_HEAD_LOSS) {
     const ProductArgs a = logits_args(c, p, nullptr, 0, d.vocab);
-    const int tn = product_tile_n(FORM_NT, a);
+    const int tn = product_tile_n(FORM_NT, a, cus);
     p.tiles = int32_t((d.vocab + tn - 1) / tn);
     p.logit = take(4 * t);
     p.stats = take(8 * t * p.tiles);
@@ -306,7 +306,7 @@ muon_status run(const Call& c) {
   if ((st = op_device(&cus)) != MUON_OK) return st;
   if (empty)
     return op_run(0, c.ws, c.ws_bytes, c.stream, [&](char*, bool) { return enqueue_empty(c, cus); });
-  const Plan p = plan_of(c);
+  const Plan p = plan_of(c, cus);
   return op_run(p.bytes, c.ws, c.ws_bytes, c.stream,
                 [&](char* ws, bool capturing) { return enqueue(c, p, ws, cus, capturing); });
 }
@@ -370,7 +370,7 @@ uint64_t muon_head_workspace_bytes(int32_t op, const muon_head_desc* desc) {
     muon_status st = check_desc(c);
     int cus = 0;
     if (st == MUON_OK) st = op_device(&cus);
-    if (st == MUON_OK && desc->rows > 0) need = plan_of(c).bytes;
+    if (st == MUON_OK && desc->rows > 0) need = plan_of(c, cus).bytes;
     return st;
   });
   return need;

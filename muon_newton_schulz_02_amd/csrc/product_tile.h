@@ -1,0 +1,874 @@
+// Tile code of the products of the experts and of the head (products_internal.h):
+// operand staging, the MFMA k-loop and the epilogues.  Each including file gets its
+// own copy (anonymous namespace).
+//
+// A persistent grid walks the tiles of C, BM x BN each.  Operands go from memory
+// through registers to LDS, one stage (128 bytes of k a row: 64 bfloat16 or 32
+// binary32) at a time, double-buffered; the k-loop overlaps, inside each wave, a
+// k-slab's MFMAs with the LDS reads of the next one, the LDS writes of the next
+// stage and the loads of the one after it.  A tile's first stage is loaded during
+// the tile before.
+//
+// Operands are the caller's tensors as they lie: any row stride, any alignment of
+// their element.  A load is 16 bytes at an element boundary (the memory unit takes
+// any), and which 16 bytes is clamped so that none lies outside the tensor: rows
+// past the tile's end read its last row, which only changes results that are not
+// stored; the last stage of a tile moves a chunk that would leave the tensor back to
+// its last 16 bytes, and shifts and masks it on the way to LDS, so that everything
+// past the end of k is zero whatever memory holds there.  (A chunk of an earlier
+// stage can pass the end of its row in k-row form only; the row after it is there, and
+// as long as rows are 16 bytes apart that is inside the tensor.  The launcher sends
+// anything narrower, and operands below 16 bytes, to the small kernel.)
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "products_device.h"
+
+#pragma clang fp contract(off)
+
+namespace muon {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));   // 16 bytes at any element
+typedef __attribute__((address_space(1))) const char gchar;
+typedef __attribute__((address_space(1))) const u32x4_any gload16;
+typedef __attribute__((address_space(1))) u32x4_any gstore16;
+
+constexpr int NUM_XCD = 8;
+constexpr int KB = 128;     // bytes of k per stage
+constexpr int PITCH = 144;  // LDS pitch of an operand row in row form
+
+// This wave's LDS accesses complete, then s_barrier: unlike __syncthreads it does
+// not wait for global loads and stores in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Tile shapes: BM x BN over WM x WN waves.
+template <int BM_, int BN_, int WM_, int WN_, bool F32_>
+struct Shape {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NT = WM_ * WN_ * 64;
+  static constexpr bool F32 = F32_;
+  static constexpr int ESZ = F32 ? 4 : 2, KE = KB / ESZ, KS = F32 ? 8 : 16;
+  static constexpr int WTP = BM / WM, WTQ = BN / WN, FP = WTP / 32, FQ = WTQ / 32;
+  static constexpr int CP = BM * 8 / NT, CQ = BN * 8 / NT;   // 16-byte chunks of a stage per thread
+  static_assert(CP >= 1 && CQ >= 1 && BM * 8 % NT == 0 && BN * 8 % NT == 0, "whole chunks per thread");
+};
+
+// LDS of an operand of R rows.  Row form: row r at r PITCH (a fragment read of 32
+// rows then meets every bank evenly).  k-row form: k-row k at k * pitch; bfloat16
+// fragments come from ds_read_b64_tr_b16, whose half-wave reads 4 k-rows x 64 bytes,
+// on distinct banks where the pitch is 64 or 192 modulo 256; binary32 ones from
+// 4-byte reads, whose halves are 4 k-rows apart, on distinct banks where four
+// pitches are 128 modulo 256.
+template <class S, int R, bool KROW>
+struct Lds {
+  static constexpr int pitch = !KROW ? PITCH : S::F32 ? R * 4 + 32 : (R * 2 % 256 == 0 || R * 2 % 256 == 128) ? R * 2 + 64 : R * 2;
+  static_assert(!KROW || S::F32 || pitch % 256 == 64 || pitch % 256 == 192, "banks");
+  static constexpr int bytes = KROW ? S::KE * pitch : R * PITCH;
+};
+
+template <class S, int FORM>
+struct Layout {
+  static constexpr bool PK = FORM == FORM_TN, QK = FORM != FORM_NT;   // k-row form
+  using LP = Lds<S, S::BM, PK>;
+  using LQ = Lds<S, S::BN, QK>;
+  static constexpr int P0 = 0, Q0 = 2 * LP::bytes, BYTES = 2 * LP::bytes + 2 * LQ::bytes;
+};
+
+// ------------------------------------------------------------------ tiles
+
+// One tile of C.
+struct Tile {
+  int g;            // group
+  int lo;           // the group's first row
+  int i0, j0;       // first row of C in the group, first column
+  int m, n;         // rows and columns from there on
+  int k;
+};
+
+// Where an operand of a tile comes from.
+struct Source {
+  const char* base;     // element (row 0 of the tile, k = 0)
+  const char* begin;    // first byte of the tensor
+  const char* end;      // one past its last
+  int64_t ld;           // row stride in bytes
+  int valid;            // rows (row form) or columns (k-row form) of the tile that exist
+};
+
+template <class S, int FORM, int OPD>
+__device__ __forceinline__ Source source_of(const ProductArgs& a, const Tile& t) {
+  constexpr int E = S::ESZ;
+  Source s;
+  if constexpr (OPD == 0) {
+    s.begin = reinterpret_cast<const char*>(a.p);
+    s.end = s.begin + a.p_elems * E;
+    s.ld = a.ld_p * E;
+    s.valid = t.m;
+    s.base = FORM == FORM_TN ? s.begin + t.lo * s.ld + t.i0 * E : s.begin + (int64_t(t.lo) + t.i0) * s.ld;
+  } else {
+    s.begin = reinterpret_cast<const char*>(a.q) + (FORM == FORM_TN ? 0 : t.g * a.es_q * E);
+    s.end = s.begin + a.q_elems * E;
+    s.ld = a.ld_q * E;
+    s.valid = t.n;
+    s.base = FORM == FORM_NT ? s.begin + t.j0 * s.ld
+             : FORM == FORM_NN ? s.begin + t.j0 * E : s.begin + t.lo * s.ld + t.j0 * E;
+  }
+  return s;
+}
+
+// This thread's loads of an operand: `at` advances from stage to stage, the
+// offsets stay, until the last stage has its own.
+template <int C>
+struct Loads {
+  const char* at;
+  uint32_t off[C];
+};
+
+// Chunk c of a stage: row form, row c / 8 and 16 bytes at 16 (c % 8); k-row form,
+// k-row c / (R ESZ / 16) and 16 bytes of it.
+template <class S, int R, bool KROW>
+__device__ __forceinline__ void chunk_at(int c, int& row, int& byte) {
+  constexpr int PER = KROW ? R * S::ESZ / 16 : 8;
+  row = c / PER;
+  byte = (c % PER) * 16;
+}
+
+// A copy of the thread's index that the compiler takes for a new value: what is
+// computed from it stays where it is used, instead of being kept in registers (or in
+// scratch memory) through the k-loop.
+__device__ __forceinline__ int fresh(int tid) {
+  int t;
+  asm volatile("v_mov_b32 %0, %1" : "=v"(t) : "v"(tid));
+  return t;
+}
+
+template <class S, int R, bool KROW, int C>
+__device__ __forceinline__ void first_loads(Loads<C>& l, const Source& s, int tid) {
+  l.at = s.base;
+  tid = fresh(tid);
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    int row, byte;
+    chunk_at<S, R, KROW>(tid + S::NT * i, row, byte);
+    if constexpr (KROW) l.off[i] = uint32_t(row * s.ld) + (byte < s.valid * S::ESZ ? byte : 0);
+    else l.off[i] = uint32_t(min(row, s.valid - 1) * s.ld) + byte;
+  }
+}
+
+// The byte address, relative to the tile's base, of chunk c in the last stage kt of
+// k values in all; wanted past the end of k: -1.
+template <class S, int R, bool KROW>
+__device__ __forceinline__ int64_t last_chunk(const Source& s, int c, int kt, int k, int& row, int& byte) {
+  chunk_at<S, R, KROW>(c, row, byte);
+  if constexpr (KROW) {
+    if (kt * S::KE + row >= k) return -1;
+    return (int64_t(kt) * S::KE + row) * s.ld + (byte < s.valid * S::ESZ ? byte : 0);
+  } else {
+    if (kt * KB + byte >= k * S::ESZ) return -1;
+    return min(row, s.valid - 1) * s.ld + kt * KB + byte;
+  }
+}
+
+// Offsets of the last stage: from 16 bytes before the tile's base, or from the
+// tensor's begin, so that the tensor's last 16 bytes are not before it.
+template <class S, int R, bool KROW, int C>
+__device__ __forceinline__ void last_loads(Loads<C>& l, const Source& s, int kt, int k, int tid) {
+  int64_t from = 0;
+  if constexpr (KROW) from = int64_t(kt) * S::KE * s.ld;       // whole k-rows, 64 bits
+  const int64_t back = min(int64_t(16), int64_t(s.base - s.begin) + from);
+  l.at = s.base + from - back;
+  const int64_t most = (s.end - 16) - l.at;
+  tid = fresh(tid);
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    int row, byte;
+    const int64_t a = last_chunk<S, R, KROW>(s, tid + S::NT * i, kt, k, row, byte);
+    l.off[i] = uint32_t(min(a < 0 ? int64_t(0) : a - from + back, most));
+  }
+}
+
+template <int C>
+__device__ __forceinline__ void load_chunks(u32x4 (&r)[C], const Loads<C>& l) {
+  gchar* at = (gchar*)l.at;
+#pragma unroll
+  for (int i = 0; i < C; ++i) r[i] = *reinterpret_cast<gload16*>(at + l.off[i]);
+}
+
+// bytes [s, 16) of v, zeros behind; s >= 0
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int s) {
+  uint64_t lo = v[0] | (uint64_t(v[1]) << 32), hi = v[2] | (uint64_t(v[3]) << 32);
+  if (s >= 16) return u32x4{0, 0, 0, 0};
+  if (s >= 8) {
+    lo = hi;
+    hi = 0;
+    s -= 8;
+  }
+  if (s > 0) {
+    lo = (lo >> (8 * s)) | (hi << (64 - 8 * s));
+    hi >>= 8 * s;
+  }
+  return u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+}
+
+// v's first `bytes` bytes, zeros behind (a multiple of 2; 16 and more: all)
+__device__ __forceinline__ u32x4 keep_first(u32x4 v, int bytes) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const int b = bytes - 4 * d;
+    v[d] = b >= 4 ? v[d] : b == 2 ? (v[d] & 0xFFFFu) : 0u;
+  }
+  return v;
+}
+
+// Chunks I0 .. I1 - 1 of a stage to LDS at `dst`.
+template <class S, int R, bool KROW, int C>
+__device__ __forceinline__ void store_chunks(const u32x4 (&r)[C], char* dst, int tid, int i0, int i1) {
+  using L = Lds<S, R, KROW>;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    if (i < i0 || i >= i1) continue;
+    int row, byte;
+    chunk_at<S, R, KROW>(tid + S::NT * i, row, byte);
+    *reinterpret_cast<u32x4*>(dst + row * L::pitch + byte) = r[i];
+  }
+}
+
+// The same for the last stage: what last_loads moved back is moved forward again,
+// and what lies past the end of k becomes zero.
+template <class S, int R, bool KROW, int C>
+__device__ __forceinline__ void store_last(const u32x4 (&r)[C], const Source& s, int kt, int k, char* dst, int tid,
+                                           int i0, int i1) {
+  using L = Lds<S, R, KROW>;
+  const int64_t most = (s.end - 16) - s.base;
+  tid = fresh(tid);
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    if (i < i0 || i >= i1) continue;
+    int row, byte;
+    const int64_t a = last_chunk<S, R, KROW>(s, tid + S::NT * i, kt, k, row, byte);
+    u32x4 v = a < 0 ? u32x4{0, 0, 0, 0} : r[i];
+    if (a > most) v = shift_down(v, int(a - most));
+    if constexpr (!KROW) v = keep_first(v, k * S::ESZ - (kt * KB + byte));
+    *reinterpret_cast<u32x4*>(dst + row * L::pitch + byte) = v;
+  }
+}
+
+// ------------------------------------------------------------------ fragments
+
+// F fragments of 32 rows (columns of C for Q), one k-slab ks; `w0` is the wave's
+// first row of the operand.
+template <class S, int R, bool KROW, int F>
+__device__ __forceinline__ void read_frags(u32x4* f, const char* lds, int w0, int ks, int lane) {
+  using L = Lds<S, R, KROW>;
+  const int half = lane >> 5;
+  if constexpr (!KROW) {
+    const char* p = lds + (w0 + (lane & 31)) * PITCH + half * 16 + ks * 32;
+#pragma unroll
+    for (int x = 0; x < F; ++x) f[x] = *reinterpret_cast<const u32x4*>(p + x * 32 * PITCH);
+  } else if constexpr (!S::F32) {
+    // lane 4 e + m of each 16-lane group points at k-row e, columns 4 m .. 4 m + 3
+    // of its 16; lane j of the group receives k-rows 0 .. 3 of column j
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 ls16x4;
+    typedef __attribute__((address_space(3))) char lchar;
+    lchar* p = (lchar*)(lds + (8 * half + ((lane & 15) >> 2) + ks * 16) * L::pitch +
+                        2 * (w0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3)));
+#pragma unroll
+    for (int x = 0; x < F; ++x) {
+      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4*)(p + x * 64)));
+      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4*)(p + x * 64 + 4 * L::pitch)));
+      f[x] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
+  } else {
+    const char* p = lds + (4 * half + ks * 8) * L::pitch + 4 * (w0 + (lane & 31));
+#pragma unroll
+    for (int x = 0; x < F; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[x][e] = *reinterpret_cast<const uint32_t*>(p + x * 128 + e * L::pitch);
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void mfma(f32x16& acc, const u32x4& q, const u32x4& p) {
+  if constexpr (!F32) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, q), __builtin_bit_cast(bf16x8, p), acc, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(q[e]), __uint_as_float(p[e]), acc, 0, 0, 0);
+  }
+}
+
+// ------------------------------------------------------------------ epilogues
+
+// Accumulators: acc[j][i][4 g + e] is row wp WTP + 32 i + (lane & 31) and column
+// wq WTQ + 32 j + 8 g + 4 (lane / 32) + e of the tile.
+
+// v[0 .. 7] (OF32: 4) to out, `cnt` of them; + addend.
+template <bool OF32>
+__device__ __forceinline__ void store_run(const ProductArgs& a, float* v, int64_t at, int64_t add_at, int cnt) {
+  constexpr int N = OF32 ? 4 : 8;
+  if (a.add) {
+    if (a.add_f32) {
+      const float* ad = reinterpret_cast<const float*>(a.add) + add_at;
+      if (cnt == N) {
+#pragma unroll
+        for (int h = 0; h < N / 4; ++h) {
+          const u32x4 w = *reinterpret_cast<gload16*>((gchar*)(ad + 4 * h));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * h + e] += __uint_as_float(w[e]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (e < cnt) v[e] += ad[e];
+      }
+    } else {
+      const uint16_t* ad = reinterpret_cast<const uint16_t*>(a.add) + add_at;
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (e < cnt) v[e] += bf16_bits_to_float(ad[e]);
+    }
+  }
+  if constexpr (OF32) {
+    float* o = reinterpret_cast<float*>(a.out) + at;
+    if (cnt == N) {
+      *reinterpret_cast<gstore16*>((__attribute__((address_space(1))) char*)o) =
+          u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (e < cnt) o[e] = v[e];
+    }
+  } else {
+    uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + at;
+    if (cnt == N) {
+      *reinterpret_cast<gstore16*>((__attribute__((address_space(1))) char*)o) =
+          u32x4{float2_to_bf16x2_bits(v[0], v[1]), float2_to_bf16x2_bits(v[2], v[3]),
+                float2_to_bf16x2_bits(v[4 % N], v[5 % N]), float2_to_bf16x2_bits(v[6 % N], v[7 % N])};
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (e < cnt) o[e] = float_to_bf16_bits(v[e]);
+    }
+  }
+}
+
+// C to `out`.  OF32: out is binary32.  WIDE: staged in LDS as binary32 (for binary32
+// outputs and addends), a part of the tile's rows at a time where all do not fit;
+// else as bfloat16.
+template <class S, int FORM, bool OF32, bool WIDE>
+__device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t,
+                                           char* smem, int tid) {
+  constexpr int ES = WIDE ? 4 : 2, EP = S::BN * ES + 16;
+  constexpr int LDS = Layout<S, FORM>::BYTES;
+  constexpr int PASSES = S::BM * EP <= LDS ? 1 : S::BM / 2 * EP <= LDS ? 2 : 4;
+  constexpr int ROWS = S::BM / PASSES;
+  static_assert(ROWS * EP <= LDS && S::WTP % 32 == 0, "staging fits");
+  const int tt = fresh(tid);
+  const int lane = tt & 63, half = lane >> 5, w = tt >> 6, wq = w % S::WN, wp = w / S::WN;
+#pragma unroll 1
+  for (int pass = 0; pass < PASSES; ++pass) {
+    if (pass > 0) lds_barrier();
+#pragma unroll
+    for (int i = 0; i < S::FP; ++i) {
+      const int r = wp * S::WTP + 32 * i + (lane & 31) - pass * ROWS;
+      if (PASSES == 1 || (r >= 0 && r < ROWS)) {
+#pragma unroll
+        for (int j = 0; j < S::FQ; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const f32x16& c = acc[j][i];
+            char* d = smem + r * EP + (wq * S::WTQ + 32 * j + 8 * g + 4 * half) * ES;
+            if constexpr (WIDE) *reinterpret_cast<f32x4*>(d) = f32x4{c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
+            else *reinterpret_cast<u32x2*>(d) = u32x2{float2_to_bf16x2_bits(c[4 * g], c[4 * g + 1]),
+                                                      float2_to_bf16x2_bits(c[4 * g + 2], c[4 * g + 3])};
+          }
+      }
+    }
+    lds_barrier();
+    constexpr int N = OF32 ? 4 : 8, CPR = S::BN / N;      // elements of a run, runs of a row
+    const int rows = min(ROWS, t.m - pass * ROWS);
+    constexpr int ITER = ROWS * CPR / S::NT > 0 ? ROWS * CPR / S::NT : 1;
+#pragma unroll 4
+    for (int k = 0; k < ITER; ++k) {
+      const int q = tt + k * S::NT;
+      const int r = q / CPR, c = q % CPR * N;
+      const int cnt = min(N, t.n - c);
+      if (r >= rows || cnt <= 0) continue;
+      const int64_t crow = t.i0 + pass * ROWS + r + (FORM == FORM_TN ? 0 : t.lo);
+      const int64_t g0 = FORM == FORM_TN ? t.g * a.es_out : 0;
+      const int64_t row = a.map ? a.map[crow] : crow;
+      const int64_t at = g0 + row * a.ld_out + t.j0 + c;
+      if constexpr (!WIDE) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(smem + r * EP + c * 2);
+        uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + at;
+        if (cnt == N) {
+          *reinterpret_cast<gstore16*>((__attribute__((address_space(1))) char*)o) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (e < cnt) o[e] = uint16_t(v[e / 2] >> (16 * (e & 1)));
+        }
+      } else {
+        float v[N];
+#pragma unroll
+        for (int h = 0; h < N / 4; ++h) {
+          const f32x4 x = *reinterpret_cast<const f32x4*>(smem + r * EP + (c + 4 * h) * 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * h + e] = x[e];
+        }
+        store_run<OF32>(a, v, at, g0 + crow * a.ld_add + t.j0 + c, cnt);
+      }
+    }
+  }
+}
+
+// Every row's maximum and sum of exponentials over the tile's columns, and the
+// target's logit.
+template <class S>
+__device__ __forceinline__ void lse_tile(f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t, char* smem,
+                                         int tid) {
+  const int tt = fresh(tid);
+  const int lane = tt & 63, half = lane >> 5, w = tt >> 6, wq = w % S::WN, wp = w / S::WN;
+  const int c0 = wq * S::WTQ + 4 * half;
+  const bool whole = t.n >= S::BN;
+  float2* part = reinterpret_cast<float2*>(smem);           // [row of the tile][wave column]
+#pragma unroll
+  for (int i = 0; i < S::FP; ++i) {
+    const int r = wp * S::WTP + 32 * i + (lane & 31);
+    const int target = r < t.m ? a.target[t.i0 + r] - a.col0 - t.j0 : -1;
+#pragma unroll
+    for (int j = 0; j < S::FQ; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int c = c0 + 32 * j + 8 * (v >> 2) + (v & 3);
+        const float z = soft_capped(acc[j][i][v], a.cap, a.inv_cap);
+        acc[j][i][v] = whole || c < t.n ? z : -INFINITY;
+      }
+    if (__any(target >= wq * S::WTQ && target < (wq + 1) * S::WTQ)) {
+#pragma unroll
+      for (int j = 0; j < S::FQ; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          if (target == c0 + 32 * j + 8 * (v >> 2) + (v & 3)) a.logit[t.i0 + r] = acc[j][i][v];
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < S::FQ; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) mx = fmaxf(mx, acc[j][i][v]);
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < S::FQ; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) sum += __expf(acc[j][i][v] - base);
+    sum += __shfl_xor(sum, 32);
+    if (half == 0) part[r * S::WN + wq] = make_float2(mx, sum);
+  }
+  lds_barrier();
+  for (int r = tt; r < min(S::BM, t.m); r += S::NT) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < S::WN; ++q) m = fmaxf(m, part[r * S::WN + q].x);
+    const float base = m == -INFINITY ? 0.f : m;
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < S::WN; ++q) sum += part[r * S::WN + q].y * __expf(part[r * S::WN + q].x - base);
+    a.stats[int64_t(t.i0 + r) * a.stat_tiles + t.j0 / S::BN] = make_float2(m, sum);
+  }
+}
+
+// The logits become the loss's gradient with respect to them.
+template <class S>
+__device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t, int tid) {
+  const int tt = fresh(tid);
+  const int lane = tt & 63, w = tt >> 6, wq = w % S::WN, wp = w / S::WN;
+  const int c0 = wq * S::WTQ + 4 * (lane >> 5);
+#pragma unroll
+  for (int i = 0; i < S::FP; ++i) {
+    const int r = min(wp * S::WTP + 32 * i + (lane & 31), t.m - 1) + t.i0;
+    const int target = a.target[r] - a.col0 - t.j0;
+    const float lse = a.lse[r], ga = a.ga[r], gb = a.gb[r];
+    const bool here = __any(target >= wq * S::WTQ && target < (wq + 1) * S::WTQ);
+#pragma unroll
+    for (int j = 0; j < S::FQ; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const float z = soft_capped(acc[j][i][v], a.cap, a.inv_cap);
+        const int c = c0 + 32 * j + 8 * (v >> 2) + (v & 3);
+        acc[j][i][v] = logit_gradient(a, z, here ? c : -1, here ? target : -2, lse, ga, gb);
+      }
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+
+// Inclusive sums over the groups of their tiles of rows: pre[g + 1] - pre[g] tiles
+// of BM rows, pre[0] = 0.  All threads take part.
+template <class S>
+__device__ __forceinline__ void count_tiles(const ProductArgs& a, int* pre, int tid) {
+  __shared__ int wave_sum[S::NT / 64];
+  const int lane = tid & 63, wave = tid >> 6;
+  int carry = 0;
+  if (tid == 0) pre[0] = 0;
+  for (int b = 0; b < a.groups; b += S::NT) {
+    const int g = b + tid;
+    int v = 0;
+    if (g < a.groups) {
+      int lo, hi;
+      group_range(a, g, lo, hi);
+      v = (hi - lo + S::BM - 1) / S::BM;
+    }
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) {
+      const int o = __shfl_up(v, s);
+      if (lane >= s) v += o;
+    }
+    if (lane == 63) wave_sum[wave] = v;
+    __syncthreads();
+    int before = carry, all = 0;
+#pragma unroll
+    for (int w = 0; w < S::NT / 64; ++w) {
+      if (w < wave) before += wave_sum[w];
+      all += wave_sum[w];
+    }
+    if (g < a.groups) pre[g + 1] = before + v;
+    carry += all;
+    __syncthreads();
+  }
+  __syncthreads();
+}
+
+// Tiles of C go through the columns in bands of BAND rows of tiles, so that the
+// tiles that run together on an XCD (32 or more) share panels of P and Q in its L2.
+constexpr int BAND = 8;
+
+template <class S, int FORM>
+__device__ __forceinline__ Tile tile_at(const ProductArgs& a, const int* pre, int t) {
+  Tile r;
+  const int nt = (a.n + S::BN - 1) / S::BN;
+  int mt, first;          // tiles of rows of the group, number of its first tile
+  if constexpr (FORM == FORM_TN) {
+    mt = (a.m + S::BM - 1) / S::BM;
+    r.g = t / (mt * nt);
+    first = r.g * mt * nt;
+  } else {
+    int lo = 0, hi = a.groups;          // pre[lo] nt <= t < pre[hi] nt
+    const int rt = t / nt;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (pre[mid] <= rt) lo = mid;
+      else hi = mid;
+    }
+    r.g = __builtin_amdgcn_readfirstlane(lo);
+    const int p0 = __builtin_amdgcn_readfirstlane(pre[r.g]);
+    mt = __builtin_amdgcn_readfirstlane(pre[r.g + 1]) - p0;
+    first = p0 * nt;
+  }
+  const int u = t - first, b = u / (BAND * nt), rows = min(BAND, mt - b * BAND), v = u - b * BAND * nt;
+  r.i0 = (b * BAND + v % rows) * S::BM;
+  r.j0 = v / rows * S::BN;
+  int lo, hi;
+  group_range(a, r.g, lo, hi);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+  r.lo = lo;
+  r.n = a.n - r.j0;
+  if constexpr (FORM == FORM_TN) {
+    r.m = a.m - r.i0;
+    r.k = hi - lo;
+  } else {
+    r.m = hi - lo - r.i0;
+    r.k = a.k;
+  }
+  return r;
+}
+
+template <class S, int FORM, int EPI>
+__global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
+  using LY = Layout<S, FORM>;
+  constexpr bool PK = LY::PK, QK = LY::QK;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  int* pre = reinterpret_cast<int*>(smem + LY::BYTES);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wq = w % S::WN, wp = w / S::WN;
+
+  // Which tiles are this workgroup's: workgroup b runs on XCD b % 8.  Tiles of equal
+  // work (NT, NN): a contiguous eighth of them for each XCD.  TN, where k differs from
+  // group to group: the grid takes as many consecutive tiles at a time as it has
+  // workgroups, so that a long group is spread over all of them.
+  const int xcd = blockIdx.x % NUM_XCD, slot = blockIdx.x / NUM_XCD, slots = gridDim.x / NUM_XCD;
+  int tile, step, end;
+  if constexpr (FORM == FORM_TN) {
+    end = a.groups * ((a.m + S::BM - 1) / S::BM) * ((a.n + S::BN - 1) / S::BN);
+    tile = xcd * slots + slot;
+    step = gridDim.x;
+  } else {
+    count_tiles<S>(a, pre, tid);
+    const int total = __builtin_amdgcn_readfirstlane(pre[a.groups]) * ((a.n + S::BN - 1) / S::BN);
+    const int per = (total + NUM_XCD - 1) / NUM_XCD;
+    tile = xcd * per + slot;
+    end = min((xcd + 1) * per, total);
+    step = slots;
+  }
+  if (tile >= end) return;
+
+  u32x4 rp[S::CP], rq[S::CQ];
+  Loads<S::CP> lp;
+  Loads<S::CQ> lq;
+  auto stages = [](const Tile& t) { return (t.k + S::KE - 1) / S::KE; };
+  // the addresses of the first stage of a tile
+  auto begin_tile = [&](const Tile& t, const Source& sp, const Source& sq) {
+    if (stages(t) > 1) {
+      first_loads<S, S::BM, PK>(lp, sp, tid);
+      first_loads<S, S::BN, QK>(lq, sq, tid);
+    } else {
+      last_loads<S, S::BM, PK>(lp, sp, 0, t.k, tid);
+      last_loads<S, S::BN, QK>(lq, sq, 0, t.k, tid);
+    }
+  };
+  Tile t = tile_at<S, FORM>(a, pre, tile);
+  Source sp = source_of<S, FORM, 0>(a, t), sq = source_of<S, FORM, 1>(a, t);
+  if (t.k > 0) {
+    begin_tile(t, sp, sq);
+    load_chunks(rp, lp);
+    load_chunks(rq, lq);
+  }
+
+#pragma unroll 1
+  while (true) {
+    const int nk = stages(t);
+    f32x16 acc[S::FQ][S::FP];
+#pragma unroll
+    for (int j = 0; j < S::FQ; ++j)
+#pragma unroll
+      for (int i = 0; i < S::FP; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[j][i][v] = 0.f;
+
+    const int ntile = tile + step;
+    const bool more = ntile < end;
+    Tile tn = t;
+    Source np = sp, nq = sq;
+    // the addresses that stage g of this tile is loaded from; g = nk: the next
+    // tile's first.  Nothing is loaded where there is none.
+    auto address = [&](int g) -> bool {
+      if (g < nk - 1) {
+        lp.at += PK ? S::KE * sp.ld : KB;
+        lq.at += QK ? S::KE * sq.ld : KB;
+        return true;
+      }
+      if (g == nk - 1) {
+        last_loads<S, S::BM, PK>(lp, sp, g, t.k, tid);
+        last_loads<S, S::BN, QK>(lq, sq, g, t.k, tid);
+        return true;
+      }
+      if (!more) return false;
+      tn = tile_at<S, FORM>(a, pre, ntile);
+      np = source_of<S, FORM, 0>(a, tn);
+      nq = source_of<S, FORM, 1>(a, tn);
+      if (tn.k <= 0) return false;
+      begin_tile(tn, np, nq);
+      return true;
+    };
+
+    if (nk == 0) {
+      if (address(0)) {
+        load_chunks(rp, lp);
+        load_chunks(rq, lq);
+      }
+    } else {
+      u32x4 F[2][S::FQ + S::FP];
+      constexpr int HP = (S::CP + 1) / 2, HQ = (S::CQ + 1) / 2, HF = (S::FP + 1) / 2;
+      auto frags = [&](u32x4* f, auto buf_c, int ks) {
+        constexpr int BUF = decltype(buf_c)::value;
+        read_frags<S, S::BN, QK, S::FQ>(f, smem + LY::Q0 + BUF * LY::LQ::bytes, wq * S::WTQ, ks, lane);
+        read_frags<S, S::BM, PK, S::FP>(f + S::FQ, smem + LY::P0 + BUF * LY::LP::bytes, wp * S::WTP, ks, lane);
+      };
+      auto multiply = [&](const u32x4* f, int h) {
+#pragma unroll
+        for (int j = 0; j < S::FQ; ++j)
+#pragma unroll
+          for (int i = 0; i < S::FP; ++i)
+            if (i / HF == h) mfma<S::F32>(acc[j][i], f[j], f[S::FQ + i]);
+      };
+      // half h of an operand's chunks of stage g to buffer BUF; LAST: g is the last stage
+      auto put_p = [&](auto buf_c, auto last_c, int g, int h) {
+        char* d = smem + LY::P0 + decltype(buf_c)::value * LY::LP::bytes;
+        if constexpr (decltype(last_c)::value) store_last<S, S::BM, PK>(rp, sp, g, t.k, d, tid, h ? HP : 0, h ? S::CP : HP);
+        else store_chunks<S, S::BM, PK>(rp, d, tid, h ? HP : 0, h ? S::CP : HP);
+      };
+      auto put_q = [&](auto buf_c, auto last_c, int g, int h) {
+        char* d = smem + LY::Q0 + decltype(buf_c)::value * LY::LQ::bytes;
+        if constexpr (decltype(last_c)::value) store_last<S, S::BN, QK>(rq, sq, g, t.k, d, tid, h ? HQ : 0, h ? S::CQ : HQ);
+        else store_chunks<S, S::BN, QK>(rq, d, tid, h ? HQ : 0, h ? S::CQ : HQ);
+      };
+      using I0 = std::integral_constant<int, 0>;
+      using I1 = std::integral_constant<int, 1>;
+      using Yes = std::true_type;
+      using No = std::false_type;
+      // stage kt is in buffer BUF.  MODE 0: store stage kt + 1, load stage kt + 2;
+      // 1: store the last stage, load the next tile's first; 2: the last stage.
+      auto stage = [&](const int kt, auto buf_c, auto mode_c) {
+        constexpr int BUF = decltype(buf_c)::value, MODE = decltype(mode_c)::value;
+        using CUR = std::integral_constant<int, BUF>;
+        using NXT = std::integral_constant<int, BUF ^ 1>;
+        using LAST = std::integral_constant<bool, MODE == 1>;
+        bool load = false;
+        frags(F[1], CUR{}, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(F[0], 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (MODE != 2) put_p(NXT{}, LAST{}, kt + 1, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(F[0], 1);
+        __builtin_amdgcn_sched_barrier(0);
+        frags(F[0], CUR{}, 2);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(F[1], 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (MODE != 2) {
+          put_p(NXT{}, LAST{}, kt + 1, 1);
+          put_q(NXT{}, LAST{}, kt + 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(F[1], 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (MODE == 0) {
+          address(kt + 2);
+          load_chunks(rp, lp);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        frags(F[1], CUR{}, 3);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(F[0], 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (MODE != 2) put_q(NXT{}, LAST{}, kt + 1, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(F[0], 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (MODE == 0) load_chunks(rq, lq);
+        if constexpr (MODE == 1) {
+          load = address(kt + 2);
+          if (load) {
+            load_chunks(rp, lp);
+            load_chunks(rq, lq);
+          }
+        }
+        lds_barrier();
+        if constexpr (MODE != 2) frags(F[0], NXT{}, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(F[1], 0);
+        multiply(F[1], 1);
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      // stage g is in buffer (g + nk) % 2, so that the last one is in buffer 1
+      if (nk == 1) {
+        put_p(I1{}, Yes{}, 0, 0);
+        put_p(I1{}, Yes{}, 0, 1);
+        put_q(I1{}, Yes{}, 0, 0);
+        put_q(I1{}, Yes{}, 0, 1);
+        if (address(1)) {
+          load_chunks(rp, lp);
+          load_chunks(rq, lq);
+        }
+        lds_barrier();
+        frags(F[0], I1{}, 0);
+        stage(0, I1{}, std::integral_constant<int, 2>{});
+      } else {
+        int kt = 0;
+        if (nk & 1) {
+          put_p(I1{}, No{}, 0, 0);
+          put_p(I1{}, No{}, 0, 1);
+          put_q(I1{}, No{}, 0, 0);
+          put_q(I1{}, No{}, 0, 1);
+          address(1);
+          load_chunks(rp, lp);
+          load_chunks(rq, lq);
+          lds_barrier();
+          frags(F[0], I1{}, 0);
+          stage(0, I1{}, I0{});
+          kt = 1;
+        } else {
+          put_p(I0{}, No{}, 0, 0);
+          put_p(I0{}, No{}, 0, 1);
+          put_q(I0{}, No{}, 0, 0);
+          put_q(I0{}, No{}, 0, 1);
+          address(1);
+          load_chunks(rp, lp);
+          load_chunks(rq, lq);
+          lds_barrier();
+          frags(F[0], I0{}, 0);
+        }
+#pragma unroll 1
+        for (; kt + 2 < nk; kt += 2) {
+          stage(kt, I0{}, I0{});
+          stage(kt + 1, I1{}, I0{});
+        }
+        stage(nk - 2, I0{}, I1{});
+        stage(nk - 1, I1{}, std::integral_constant<int, 2>{});
+      }
+    }
+
+    if constexpr (EPI == EPI_LSE) {
+      lse_tile<S>(acc, a, t, smem, tid);
+    } else {
+      if constexpr (EPI == EPI_DZ) gradient_tile<S>(acc, a, t, tid);
+      if constexpr (EPI == EPI_DZ) {
+        store_tile<S, FORM, S::F32, S::F32>(acc, a, t, smem, tid);
+      } else if constexpr (S::F32) {
+        store_tile<S, FORM, true, true>(acc, a, t, smem, tid);
+      } else {
+        if (a.out_f32) store_tile<S, FORM, true, true>(acc, a, t, smem, tid);
+        else if (a.add) store_tile<S, FORM, false, true>(acc, a, t, smem, tid);
+        else store_tile<S, FORM, false, false>(acc, a, t, smem, tid);
+      }
+    }
+    if (!more) break;
+    lds_barrier();
+    tile = ntile;
+    t = tn;
+    sp = np;
+    sq = nq;
+  }
+}
+
+template <class S, int FORM, int EPI>
+hipError_t launch_shape(const ProductArgs& a, int cus, hipStream_t stream) {
+  using LY = Layout<S, FORM>;
+  const size_t lds = LY::BYTES + (FORM == FORM_TN ? 0 : (size_t(a.groups) + 1) * 4);
+  const int64_t nt = (a.n + S::BN - 1) / S::BN;
+  const int64_t mt = FORM == FORM_TN ? int64_t(a.groups) * ((a.m + S::BM - 1) / S::BM)
+                                     : a.rows / S::BM + std::min(a.groups, a.rows);   // at most
+  // workgroups that a compute unit holds: by its LDS, and by waves (8 a unit at 256 registers)
+  const int fit = std::max(1, std::min(int((160 * 1024) / (lds + 64)), 2048 / S::NT / 4));
+  const int64_t grid = std::min<int64_t>((mt * nt + NUM_XCD - 1) / NUM_XCD * NUM_XCD,
+                                         int64_t(cus) / NUM_XCD * NUM_XCD * fit);
+  if (grid <= 0) return hipSuccess;
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&product_kernel<S, FORM, EPI>),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((product_kernel<S, FORM, EPI>), dim3(unsigned(grid)), dim3(S::NT), lds, stream, a);
+  return hipGetLastError();
+}
+
+using Large = Shape<256, 256, 2, 4, false>;
+using Medium = Shape<128, 128, 2, 2, false>;
+using Small = Shape<32, 128, 1, 4, false>;
+using MediumF32 = Shape<128, 128, 2, 2, true>;
+using SmallF32 = Shape<32, 128, 1, 4, true>;
+
+}  // namespace
+}  // namespace muon

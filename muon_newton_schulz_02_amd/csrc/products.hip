@@ -81,9 +81,36 @@ hipError_t launch_small(const ProductArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-int32_t product_tile_n(int, const ProductArgs&) { return TS; }
+namespace {
 
-hipError_t launch_product(int form, int epi, const ProductArgs& a, int, hipStream_t stream) {
+int product_shape(int form, const ProductArgs& a, int cus) {
+  const int64_t esz = a.f32 ? 4 : 2;
+  // 16-byte loads (product_tile.h)
+  if (a.p_elems * esz < 16 || a.q_elems * esz < 16 || (form == FORM_TN && a.ld_p * esz < 16) ||
+      (form != FORM_NT && a.ld_q * esz < 16))
+    return SHAPE_NAIVE;
+  const int64_t rows = form == FORM_TN ? a.m : a.rows / a.groups;       // of a group, on average
+  if (form != FORM_TN && rows <= 32) return SHAPE_SMALL;
+  const int64_t groups = form == FORM_TN ? a.groups : std::max<int64_t>(1, std::min<int64_t>(a.groups, a.rows / 256));
+  const int64_t large = groups * ((rows + 255) / 256) * ((a.n + 255) / 256);
+  return large >= cus ? SHAPE_LARGE : SHAPE_MEDIUM;
+}
+
+}  // namespace
+
+int32_t product_tile_n(int form, const ProductArgs& a, int cus) {
+  switch (product_shape(form, a, cus)) {
+    case SHAPE_NAIVE: return TS;
+    case SHAPE_LARGE: return a.f32 ? 128 : 256;
+    default: return 128;
+  }
+}
+
+hipError_t launch_product(int form, int epi, const ProductArgs& a, int cus, hipStream_t stream) {
+  const int shape = product_shape(form, a, cus);
+  if (shape != SHAPE_NAIVE)
+    return form == FORM_NT ? launch_nt(shape, epi, a, cus, stream)
+           : form == FORM_NN ? launch_nn(shape, a, cus, stream) : launch_tn(shape, a, cus, stream);
   if (epi == EPI_LSE) return launch_small<FORM_NT, EPI_LSE>(a, stream);
   if (epi == EPI_DZ) return launch_small<FORM_NT, EPI_DZ>(a, stream);
   switch (form) {

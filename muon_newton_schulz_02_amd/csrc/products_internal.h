@@ -52,8 +52,14 @@ struct ProductArgs {
   float2* stats;               // [row][tile]: maximum, sum of exp(z - maximum)
 };
 
+// Tile shapes (binary32 and TN have no large or small one of their own).
+enum ProductShape : int { SHAPE_NAIVE = 0, SHAPE_SMALL = 1, SHAPE_MEDIUM = 2, SHAPE_LARGE = 3 };
+hipError_t launch_nt(int shape, int epi, const ProductArgs& a, int cus, hipStream_t stream);
+hipError_t launch_nn(int shape, const ProductArgs& a, int cus, hipStream_t stream);
+hipError_t launch_tn(int shape, const ProductArgs& a, int cus, hipStream_t stream);
+
 // Columns of a tile of `stats` that launch_product writes.
-int32_t product_tile_n(int form, const ProductArgs& a);
+int32_t product_tile_n(int form, const ProductArgs& a, int cus);
 hipError_t launch_product(int form, int epi, const ProductArgs& a, int cus, hipStream_t stream);
 
 // The head's rows that have a target, packed: offsets = {0, their number}, and
