@@ -41,6 +41,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));   // 16 bytes at any element
 typedef __attribute__((address_space(1))) const char gchar;
+typedef __attribute__((address_space(3))) char lchar;
+typedef __attribute__((address_space(3))) u32x4 lu32x4;
 typedef __attribute__((address_space(1))) const u32x4_any gload16;
 typedef __attribute__((address_space(1))) u32x4_any gstore16;
 
@@ -100,7 +102,7 @@ struct Source {
   const char* base;     // element (row 0 of the tile, k = 0)
   const char* begin;    // first byte of the tensor
   const char* end;      // one past its last
-  int64_t ld;           // row stride in bytes
+  uint32_t ld;          // row stride in bytes (2^23 at most)
   int valid;            // rows (row form) or columns (k-row form) of the tile that exist
 };
 
@@ -108,19 +110,23 @@ template <class S, int FORM, int OPD>
 __device__ __forceinline__ Source source_of(const ProductArgs& a, const Tile& t) {
   constexpr int E = S::ESZ;
   Source s;
+  // formed where it is used, from values the compiler takes for new ones: kept
+  // through the k-loop the sources of two tiles would not fit the scalar registers
+  int lo = t.lo, i0 = t.i0, j0 = t.j0, grp = t.g;
+  asm volatile("" : "+s"(lo), "+s"(i0), "+s"(j0), "+s"(grp));
   if constexpr (OPD == 0) {
     s.begin = reinterpret_cast<const char*>(a.p);
     s.end = s.begin + a.p_elems * E;
-    s.ld = a.ld_p * E;
+    s.ld = uint32_t(a.ld_p * E);
     s.valid = t.m;
-    s.base = FORM == FORM_TN ? s.begin + t.lo * s.ld + t.i0 * E : s.begin + (int64_t(t.lo) + t.i0) * s.ld;
+    s.base = FORM == FORM_TN ? s.begin + int64_t(lo) * s.ld + i0 * E : s.begin + (int64_t(lo) + i0) * s.ld;
   } else {
-    s.begin = reinterpret_cast<const char*>(a.q) + (FORM == FORM_TN ? 0 : t.g * a.es_q * E);
+    s.begin = reinterpret_cast<const char*>(a.q) + (FORM == FORM_TN ? 0 : grp * a.es_q * E);
     s.end = s.begin + a.q_elems * E;
-    s.ld = a.ld_q * E;
+    s.ld = uint32_t(a.ld_q * E);
     s.valid = t.n;
-    s.base = FORM == FORM_NT ? s.begin + t.j0 * s.ld
-             : FORM == FORM_NN ? s.begin + t.j0 * E : s.begin + t.lo * s.ld + t.j0 * E;
+    s.base = FORM == FORM_NT ? s.begin + int64_t(j0) * s.ld
+             : FORM == FORM_NN ? s.begin + j0 * E : s.begin + int64_t(lo) * s.ld + j0 * E;
   }
   return s;
 }
@@ -159,40 +165,54 @@ __device__ __forceinline__ void first_loads(Loads<C>& l, const Source& s, int ti
   for (int i = 0; i < C; ++i) {
     int row, byte;
     chunk_at<S, R, KROW>(tid + S::NT * i, row, byte);
-    if constexpr (KROW) l.off[i] = uint32_t(row * s.ld) + (byte < s.valid * S::ESZ ? byte : 0);
-    else l.off[i] = uint32_t(min(row, s.valid - 1) * s.ld) + byte;
+    if constexpr (KROW) l.off[i] = row * s.ld + (byte < s.valid * S::ESZ ? byte : 0);
+    else l.off[i] = min(row, s.valid - 1) * s.ld + byte;
   }
 }
 
-// The byte address, relative to the tile's base, of chunk c in the last stage kt of
-// k values in all; wanted past the end of k: -1.
+// The last stage, kt, of k values in all.  Its loads count from `at`, 16 bytes
+// before its base, or the tensor's begin; `most` is the offset of the tensor's last
+// 16 bytes from there, which is then never negative.
+struct Last {
+  const char* at;
+  uint32_t back;        // base - at
+  uint32_t most;
+};
+template <class S, bool KROW>
+__device__ __forceinline__ Last last_of(const Source& s, int kt) {
+  const char* base = s.base + (KROW ? int64_t(kt) * S::KE * s.ld : int64_t(0));
+  Last l;
+  l.back = uint32_t(min(int64_t(16), int64_t(base - s.begin)));
+  l.at = base - l.back;
+  l.most = uint32_t(min(int64_t(0xFFFFFFFF), int64_t(s.end - 16 - l.at)));
+  return l;
+}
+
+// The offset wanted for chunk c of it; false: past the end of k.
 template <class S, int R, bool KROW>
-__device__ __forceinline__ int64_t last_chunk(const Source& s, int c, int kt, int k, int& row, int& byte) {
+__device__ __forceinline__ bool last_chunk(const Source& s, const Last& l, int c, int kt, int k, uint32_t& off, int& row,
+                                           int& byte) {
   chunk_at<S, R, KROW>(c, row, byte);
   if constexpr (KROW) {
-    if (kt * S::KE + row >= k) return -1;
-    return (int64_t(kt) * S::KE + row) * s.ld + (byte < s.valid * S::ESZ ? byte : 0);
+    off = row * s.ld + (byte < s.valid * S::ESZ ? byte : 0) + l.back;
+    return kt * S::KE + row < k;
   } else {
-    if (kt * KB + byte >= k * S::ESZ) return -1;
-    return min(row, s.valid - 1) * s.ld + kt * KB + byte;
+    off = min(row, s.valid - 1) * s.ld + uint32_t(kt * KB + byte) + l.back;
+    return kt * KB + byte < k * S::ESZ;
   }
 }
 
-// Offsets of the last stage: from 16 bytes before the tile's base, or from the
-// tensor's begin, so that the tensor's last 16 bytes are not before it.
 template <class S, int R, bool KROW, int C>
 __device__ __forceinline__ void last_loads(Loads<C>& l, const Source& s, int kt, int k, int tid) {
-  int64_t from = 0;
-  if constexpr (KROW) from = int64_t(kt) * S::KE * s.ld;       // whole k-rows, 64 bits
-  const int64_t back = min(int64_t(16), int64_t(s.base - s.begin) + from);
-  l.at = s.base + from - back;
-  const int64_t most = (s.end - 16) - l.at;
+  const Last z = last_of<S, KROW>(s, kt);
+  l.at = z.at;
   tid = fresh(tid);
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     int row, byte;
-    const int64_t a = last_chunk<S, R, KROW>(s, tid + S::NT * i, kt, k, row, byte);
-    l.off[i] = uint32_t(min(a < 0 ? int64_t(0) : a - from + back, most));
+    uint32_t off;
+    const bool in = last_chunk<S, R, KROW>(s, z, tid + S::NT * i, kt, k, off, row, byte);
+    l.off[i] = in ? min(off, z.most) : 0u;
   }
 }
 
@@ -203,20 +223,13 @@ __device__ __forceinline__ void load_chunks(u32x4 (&r)[C], const Loads<C>& l) {
   for (int i = 0; i < C; ++i) r[i] = *reinterpret_cast<gload16*>(at + l.off[i]);
 }
 
-// bytes [s, 16) of v, zeros behind; s >= 0
+// bytes [s, 16) of v, zeros behind; s in [0, 16]
 __device__ __forceinline__ u32x4 shift_down(u32x4 v, int s) {
-  uint64_t lo = v[0] | (uint64_t(v[1]) << 32), hi = v[2] | (uint64_t(v[3]) << 32);
-  if (s >= 16) return u32x4{0, 0, 0, 0};
-  if (s >= 8) {
-    lo = hi;
-    hi = 0;
-    s -= 8;
-  }
-  if (s > 0) {
-    lo = (lo >> (8 * s)) | (hi << (64 - 8 * s));
-    hi >>= 8 * s;
-  }
-  return u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+  const uint64_t lo = v[0] | (uint64_t(v[1]) << 32), hi = v[2] | (uint64_t(v[3]) << 32);
+  const int b = (8 * s) & 63;
+  const uint64_t high = hi >> b, mixed = (lo >> b) | ((hi << 1) << (63 - b));
+  const uint64_t l = s >= 16 ? 0 : s >= 8 ? high : mixed, h = s >= 8 ? 0 : high;
+  return u32x4{uint32_t(l), uint32_t(l >> 32), uint32_t(h), uint32_t(h >> 32)};
 }
 
 // v's first `bytes` bytes, zeros behind (a multiple of 2; 16 and more: all)
@@ -229,71 +242,88 @@ __device__ __forceinline__ u32x4 keep_first(u32x4 v, int bytes) {
   return v;
 }
 
-// Chunks I0 .. I1 - 1 of a stage to LDS at `dst`.
+// Where this thread's chunk 0 lies in an operand's LDS buffer; chunk i is
+// i chunk_step further.
+template <class S, int R, bool KROW>
+__device__ __forceinline__ int chunk_lds(int tid) {
+  int row, byte;
+  chunk_at<S, R, KROW>(tid, row, byte);
+  return row * Lds<S, R, KROW>::pitch + byte;
+}
+template <class S, int R, bool KROW>
+constexpr int chunk_step() {
+  constexpr int PER = KROW ? R * S::ESZ / 16 : 8;
+  static_assert(S::NT % PER == 0, "whole rows between a thread's chunks");
+  return S::NT / PER * Lds<S, R, KROW>::pitch;
+}
+
+// Chunks I0 .. I1 - 1 of a stage to LDS; `dst`: this thread's chunk 0.
 template <class S, int R, bool KROW, int C>
-__device__ __forceinline__ void store_chunks(const u32x4 (&r)[C], char* dst, int tid, int i0, int i1) {
-  using L = Lds<S, R, KROW>;
+__device__ __forceinline__ void store_chunks(const u32x4 (&r)[C], lchar* dst, int i0, int i1) {
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     if (i < i0 || i >= i1) continue;
-    int row, byte;
-    chunk_at<S, R, KROW>(tid + S::NT * i, row, byte);
-    *reinterpret_cast<u32x4*>(dst + row * L::pitch + byte) = r[i];
+    *reinterpret_cast<lu32x4*>(dst + i * chunk_step<S, R, KROW>()) = r[i];
   }
 }
 
 // The same for the last stage: what last_loads moved back is moved forward again,
 // and what lies past the end of k becomes zero.
 template <class S, int R, bool KROW, int C>
-__device__ __forceinline__ void store_last(const u32x4 (&r)[C], const Source& s, int kt, int k, char* dst, int tid,
+__device__ __forceinline__ void store_last(const u32x4 (&r)[C], const Source& s, int kt, int k, lchar* dst, int tid,
                                            int i0, int i1) {
-  using L = Lds<S, R, KROW>;
-  const int64_t most = (s.end - 16) - s.base;
+  const Last z = last_of<S, KROW>(s, kt);
   tid = fresh(tid);
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     if (i < i0 || i >= i1) continue;
     int row, byte;
-    const int64_t a = last_chunk<S, R, KROW>(s, tid + S::NT * i, kt, k, row, byte);
-    u32x4 v = a < 0 ? u32x4{0, 0, 0, 0} : r[i];
-    if (a > most) v = shift_down(v, int(a - most));
+    uint32_t off;
+    const bool in = last_chunk<S, R, KROW>(s, z, tid + S::NT * i, kt, k, off, row, byte);
+    u32x4 v = shift_down(r[i], in ? (off > z.most ? int(off - z.most) : 0) : 16);
     if constexpr (!KROW) v = keep_first(v, k * S::ESZ - (kt * KB + byte));
-    *reinterpret_cast<u32x4*>(dst + row * L::pitch + byte) = v;
+    *reinterpret_cast<lu32x4*>(dst + i * chunk_step<S, R, KROW>()) = v;
   }
 }
 
 // ------------------------------------------------------------------ fragments
 
-// F fragments of 32 rows (columns of C for Q), one k-slab ks; `w0` is the wave's
-// first row of the operand.
-template <class S, int R, bool KROW, int F>
-__device__ __forceinline__ void read_frags(u32x4* f, const char* lds, int w0, int ks, int lane) {
+// This lane's place in fragment 0, k-slab 0 of a wave whose first row of the operand
+// (column of C for Q) is w0.
+template <class S, int R, bool KROW>
+__device__ __forceinline__ int frag_lds(int w0, int lane) {
   using L = Lds<S, R, KROW>;
   const int half = lane >> 5;
+  if constexpr (!KROW) return (w0 + (lane & 31)) * PITCH + half * 16;
+  // lane 4 e + m of each 16-lane group points at k-row e, columns 4 m .. 4 m + 3 of
+  // its 16; lane j of the group receives k-rows 0 .. 3 of column j
+  else if constexpr (!S::F32) return (8 * half + ((lane & 15) >> 2)) * L::pitch + 2 * (w0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3));
+  else return 4 * half * L::pitch + 4 * (w0 + (lane & 31));
+}
+
+// F fragments of 32 rows, one k-slab ks; `p`: this lane's place.
+template <class S, int R, bool KROW, int F>
+__device__ __forceinline__ void read_frags(u32x4* f, lchar* p, int ks) {
+  using L = Lds<S, R, KROW>;
   if constexpr (!KROW) {
-    const char* p = lds + (w0 + (lane & 31)) * PITCH + half * 16 + ks * 32;
 #pragma unroll
-    for (int x = 0; x < F; ++x) f[x] = *reinterpret_cast<const u32x4*>(p + x * 32 * PITCH);
+    for (int x = 0; x < F; ++x) f[x] = *reinterpret_cast<const lu32x4*>(p + ks * 32 + x * 32 * PITCH);
   } else if constexpr (!S::F32) {
-    // lane 4 e + m of each 16-lane group points at k-row e, columns 4 m .. 4 m + 3
-    // of its 16; lane j of the group receives k-rows 0 .. 3 of column j
     typedef short s16x4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s16x4 ls16x4;
-    typedef __attribute__((address_space(3))) char lchar;
-    lchar* p = (lchar*)(lds + (8 * half + ((lane & 15) >> 2) + ks * 16) * L::pitch +
-                        2 * (w0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3)));
+    lchar* q = p + ks * 16 * L::pitch;
 #pragma unroll
     for (int x = 0; x < F; ++x) {
-      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4*)(p + x * 64)));
-      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4*)(p + x * 64 + 4 * L::pitch)));
+      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4*)(q + x * 64)));
+      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4*)(q + x * 64 + 4 * L::pitch)));
       f[x] = u32x4{lo[0], lo[1], hi[0], hi[1]};
     }
   } else {
-    const char* p = lds + (4 * half + ks * 8) * L::pitch + 4 * (w0 + (lane & 31));
+    typedef __attribute__((address_space(3))) const uint32_t lu32;
 #pragma unroll
     for (int x = 0; x < F; ++x)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f[x][e] = *reinterpret_cast<const uint32_t*>(p + x * 128 + e * L::pitch);
+      for (int e = 0; e < 4; ++e) f[x][e] = *reinterpret_cast<lu32*>(p + (ks * 8 + e) * L::pitch + x * 128);
   }
 }
 
@@ -625,12 +655,23 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
   }
   if (tile >= end) return;
 
+  // One register for each operand's stores and fragment reads; everything else is an
+  // immediate (opaque, or the compiler keeps one register for each sum)
+  lchar* put_at_p = (lchar*)smem + LY::P0 + chunk_lds<S, S::BM, PK>(tid);
+  lchar* put_at_q = (lchar*)smem + LY::Q0 + chunk_lds<S, S::BN, QK>(tid);
+  lchar* frag_p = (lchar*)smem + LY::P0 + frag_lds<S, S::BM, PK>(wp * S::WTP, lane);
+  lchar* frag_q = (lchar*)smem + LY::Q0 + frag_lds<S, S::BN, QK>(wq * S::WTQ, lane);
+  asm volatile("" : "+v"(put_at_p), "+v"(put_at_q), "+v"(frag_p), "+v"(frag_q));
   u32x4 rp[S::CP], rq[S::CQ];
   Loads<S::CP> lp;
   Loads<S::CQ> lq;
+  // bytes from one stage of an operand in k-row form to the next (64 k-rows of 2^22
+  // bytes, or 32 of 2^23: 2^28 at most)
+  const uint32_t step_p = uint32_t(S::KE * a.ld_p * S::ESZ), step_q = uint32_t(S::KE * a.ld_q * S::ESZ);
   auto stages = [](const Tile& t) { return (t.k + S::KE - 1) / S::KE; };
   // the addresses of the first stage of a tile
-  auto begin_tile = [&](const Tile& t, const Source& sp, const Source& sq) {
+  auto begin_tile = [&](const Tile& t) {
+    const Source sp = source_of<S, FORM, 0>(a, t), sq = source_of<S, FORM, 1>(a, t);
     if (stages(t) > 1) {
       first_loads<S, S::BM, PK>(lp, sp, tid);
       first_loads<S, S::BN, QK>(lq, sq, tid);
@@ -640,9 +681,8 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
     }
   };
   Tile t = tile_at<S, FORM>(a, pre, tile);
-  Source sp = source_of<S, FORM, 0>(a, t), sq = source_of<S, FORM, 1>(a, t);
   if (t.k > 0) {
-    begin_tile(t, sp, sq);
+    begin_tile(t);
     load_chunks(rp, lp);
     load_chunks(rq, lq);
   }
@@ -661,41 +701,35 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
     const int ntile = tile + step;
     const bool more = ntile < end;
     Tile tn = t;
-    Source np = sp, nq = sq;
-    // the addresses that stage g of this tile is loaded from; g = nk: the next
-    // tile's first.  Nothing is loaded where there is none.
-    auto address = [&](int g) -> bool {
+    // the addresses that stage g >= 1 of this tile is loaded from
+    auto address = [&](int g) {
       if (g < nk - 1) {
-        lp.at += PK ? S::KE * sp.ld : KB;
-        lq.at += QK ? S::KE * sq.ld : KB;
-        return true;
+        lp.at += PK ? step_p : KB;
+        lq.at += QK ? step_q : KB;
+      } else {
+        last_loads<S, S::BM, PK>(lp, source_of<S, FORM, 0>(a, t), g, t.k, tid);
+        last_loads<S, S::BN, QK>(lq, source_of<S, FORM, 1>(a, t), g, t.k, tid);
       }
-      if (g == nk - 1) {
-        last_loads<S, S::BM, PK>(lp, sp, g, t.k, tid);
-        last_loads<S, S::BN, QK>(lq, sq, g, t.k, tid);
-        return true;
-      }
-      if (!more) return false;
+    };
+    // the next tile's first stage, if there is one
+    auto load_next = [&] {
+      if (!more) return;
       tn = tile_at<S, FORM>(a, pre, ntile);
-      np = source_of<S, FORM, 0>(a, tn);
-      nq = source_of<S, FORM, 1>(a, tn);
-      if (tn.k <= 0) return false;
-      begin_tile(tn, np, nq);
-      return true;
+      if (tn.k <= 0) return;
+      begin_tile(tn);
+      load_chunks(rp, lp);
+      load_chunks(rq, lq);
     };
 
     if (nk == 0) {
-      if (address(0)) {
-        load_chunks(rp, lp);
-        load_chunks(rq, lq);
-      }
+      load_next();
     } else {
       u32x4 F[2][S::FQ + S::FP];
       constexpr int HP = (S::CP + 1) / 2, HQ = (S::CQ + 1) / 2, HF = (S::FP + 1) / 2;
       auto frags = [&](u32x4* f, auto buf_c, int ks) {
         constexpr int BUF = decltype(buf_c)::value;
-        read_frags<S, S::BN, QK, S::FQ>(f, smem + LY::Q0 + BUF * LY::LQ::bytes, wq * S::WTQ, ks, lane);
-        read_frags<S, S::BM, PK, S::FP>(f + S::FQ, smem + LY::P0 + BUF * LY::LP::bytes, wp * S::WTP, ks, lane);
+        read_frags<S, S::BN, QK, S::FQ>(f, frag_q + BUF * LY::LQ::bytes, ks);
+        read_frags<S, S::BM, PK, S::FP>(f + S::FQ, frag_p + BUF * LY::LP::bytes, ks);
       };
       auto multiply = [&](const u32x4* f, int h) {
 #pragma unroll
@@ -706,14 +740,14 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
       };
       // half h of an operand's chunks of stage g to buffer BUF; LAST: g is the last stage
       auto put_p = [&](auto buf_c, auto last_c, int g, int h) {
-        char* d = smem + LY::P0 + decltype(buf_c)::value * LY::LP::bytes;
-        if constexpr (decltype(last_c)::value) store_last<S, S::BM, PK>(rp, sp, g, t.k, d, tid, h ? HP : 0, h ? S::CP : HP);
-        else store_chunks<S, S::BM, PK>(rp, d, tid, h ? HP : 0, h ? S::CP : HP);
+        lchar* d = put_at_p + decltype(buf_c)::value * LY::LP::bytes;
+        if constexpr (decltype(last_c)::value) store_last<S, S::BM, PK>(rp, source_of<S, FORM, 0>(a, t), g, t.k, d, tid, h ? HP : 0, h ? S::CP : HP);
+        else store_chunks<S, S::BM, PK>(rp, d, h ? HP : 0, h ? S::CP : HP);
       };
       auto put_q = [&](auto buf_c, auto last_c, int g, int h) {
-        char* d = smem + LY::Q0 + decltype(buf_c)::value * LY::LQ::bytes;
-        if constexpr (decltype(last_c)::value) store_last<S, S::BN, QK>(rq, sq, g, t.k, d, tid, h ? HQ : 0, h ? S::CQ : HQ);
-        else store_chunks<S, S::BN, QK>(rq, d, tid, h ? HQ : 0, h ? S::CQ : HQ);
+        lchar* d = put_at_q + decltype(buf_c)::value * LY::LQ::bytes;
+        if constexpr (decltype(last_c)::value) store_last<S, S::BN, QK>(rq, source_of<S, FORM, 1>(a, t), g, t.k, d, tid, h ? HQ : 0, h ? S::CQ : HQ);
+        else store_chunks<S, S::BN, QK>(rq, d, h ? HQ : 0, h ? S::CQ : HQ);
       };
       using I0 = std::integral_constant<int, 0>;
       using I1 = std::integral_constant<int, 1>;
@@ -726,7 +760,6 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
         using CUR = std::integral_constant<int, BUF>;
         using NXT = std::integral_constant<int, BUF ^ 1>;
         using LAST = std::integral_constant<bool, MODE == 1>;
-        bool load = false;
         frags(F[1], CUR{}, 1);
         __builtin_amdgcn_sched_barrier(0);
         multiply(F[0], 0);
@@ -760,13 +793,7 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
         multiply(F[0], 1);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (MODE == 0) load_chunks(rq, lq);
-        if constexpr (MODE == 1) {
-          load = address(kt + 2);
-          if (load) {
-            load_chunks(rp, lp);
-            load_chunks(rq, lq);
-          }
-        }
+        if constexpr (MODE == 1) load_next();
         lds_barrier();
         if constexpr (MODE != 2) frags(F[0], NXT{}, 0);
         __builtin_amdgcn_sched_barrier(0);
@@ -780,10 +807,7 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
         put_p(I1{}, Yes{}, 0, 1);
         put_q(I1{}, Yes{}, 0, 0);
         put_q(I1{}, Yes{}, 0, 1);
-        if (address(1)) {
-          load_chunks(rp, lp);
-          load_chunks(rq, lq);
-        }
+        load_next();
         lds_barrier();
         frags(F[0], I1{}, 0);
         stage(0, I1{}, std::integral_constant<int, 2>{});
@@ -840,8 +864,6 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
     lds_barrier();
     tile = ntile;
     t = tn;
-    sp = np;
-    sq = nq;
   }
 }
 
