@@ -9,8 +9,23 @@ namespace {
 
 constexpr int NT = 256;
 
-__device__ __forceinline__ bool has_target(const HeadRows& a, int64_t t) {
+template <class A>
+__device__ __forceinline__ bool has_target(const A& a, int64_t t) {
   return t != a.ignore_index && t >= 0 && t < a.vocab;
+}
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));   // 16 bytes at any element
+
+// A row of n elements by a wave, 16 bytes a lane; src null: zeros.
+template <class T>
+__device__ __forceinline__ void copy_row(T* dst, const T* src, int n, int lane) {
+  constexpr int V = 16 / sizeof(T);
+  const int whole = n / V;
+  for (int c = lane; c < whole; c += 64)
+    *gmem(reinterpret_cast<u32x4_any*>(dst + c * V)) =
+        src ? *gmem(reinterpret_cast<const u32x4_any*>(src + c * V)) : u32x4_any{0, 0, 0, 0};
+  for (int c = whole * V + lane; c < n; c += 64) dst[c] = src ? src[c] : T(0);
 }
 
 // Each workgroup packs `chunk` rows: it counts the rows with a target before
@@ -75,9 +90,9 @@ __global__ __launch_bounds__(NT) void head_rows_kernel(const HeadRows a) {
     for (int w = wave; w < rows; w += NT / 64) {
       const int p = place[w];
       if (p >= 0) {
-        for (int c = lane; c < a.dim; c += 64) xc[int64_t(p) * a.ld_xc + c] = x[int64_t(b + w) * a.ld_x + c];
+        copy_row(xc + int64_t(p) * a.ld_xc, x + int64_t(b + w) * a.ld_x, a.dim, lane);
       } else if (gx) {
-        for (int c = lane; c < a.dim; c += 64) gx[int64_t(b + w) * a.ld_grad_x + c] = T(0);
+        copy_row(gx + int64_t(b + w) * a.ld_grad_x, static_cast<const T*>(nullptr), a.dim, lane);
       }
     }
   }
@@ -91,7 +106,11 @@ __global__ __launch_bounds__(NT) void head_rows_kernel(const HeadRows a) {
 __global__ __launch_bounds__(NT) void head_finish_kernel(const HeadFinish a) {
   const int lane = threadIdx.x & 63;
   const int i = blockIdx.x * (NT / 64) + (threadIdx.x >> 6);
-  if (i >= min(a.offsets[1], a.rows)) return;
+  if (i >= (a.targets ? a.rows : min(a.offsets[1], a.rows))) return;
+  if (a.targets && !has_target(a, a.targets[i])) {
+    if (lane == 0) a.loss[i] = a.lse[i] = a.targets[i] == a.ignore_index ? 0.f : __builtin_nanf("");
+    return;
+  }
   const float2* s = a.stats + int64_t(i) * a.tiles;
   float m = -INFINITY, sum = 0.f;
   for (int t = lane; t < a.tiles; t += 64) {
@@ -108,7 +127,7 @@ __global__ __launch_bounds__(NT) void head_finish_kernel(const HeadFinish a) {
   }
   if (lane == 0) {
     const float lse = (m == -INFINITY ? 0.f : m) + logf(sum);
-    const int r = a.row[i];
+    const int r = a.targets ? i : a.row[i];
     a.lse[r] = lse;
     a.loss[r] = lse - a.logit[i];
   }

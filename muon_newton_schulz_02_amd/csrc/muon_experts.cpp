@@ -180,7 +180,17 @@ int product_args(const Call& c, int op, ProductArgs& a) {
   return product == oi ? FORM_NT : FORM_NN;
 }
 
-size_t workspace_need(const Call&, int) { return 0; }
+// The calls of one op run in turn and share it.
+size_t workspace_need(const Call& c, int cus) {
+  size_t need = 0;
+  for (int op : {MUON_EXPERTS_GRAD_X, MUON_EXPERTS_GRAD_W, MUON_EXPERTS_PRODUCT}) {
+    if (op == MUON_EXPERTS_PRODUCT ? c.op != op : !(c.op & op)) continue;
+    ProductArgs a;
+    const int form = product_args(c, op, a);
+    need = std::max(need, op_align256(product_plan(form, EPI_STORE, a, cus).bytes));
+  }
+  return need;
+}
 
 muon_status run(const Call& c) {
   muon_status st = check_desc(c);
@@ -190,11 +200,11 @@ muon_status run(const Call& c) {
   if (c.desc->rows == 0 && !(c.op & MUON_EXPERTS_GRAD_W)) return MUON_OK;
   int cus = 0;
   if ((st = op_device(&cus)) != MUON_OK) return st;
-  return op_run(workspace_need(c, cus), c.ws, c.ws_bytes, c.stream, [&](char*, bool capturing) {
+  return op_run(workspace_need(c, cus), c.ws, c.ws_bytes, c.stream, [&](char* ws, bool capturing) {
     auto one = [&](int op) -> hipError_t {
       ProductArgs a;
       const int form = product_args(c, op, a);
-      auto launch = [&] { return launch_product(form, EPI_STORE, a, cus, c.stream); };
+      auto launch = [&] { return launch_product(form, EPI_STORE, a, cus, ws, c.stream); };
       return capturing ? launch() : api_timed(MUON_KC_COMBINE, c.stream, launch);
     };
     hipError_t e = hipSuccess;

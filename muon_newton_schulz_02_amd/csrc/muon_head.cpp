@@ -17,6 +17,11 @@ constexpr int64_t MAX_ROWS = 1 << 20, MAX_DIM = 65536, MAX_VOCAB = 1 << 24, MAX_
 // PIECE_LEAST columns, whatever the rows).
 constexpr int64_t PIECE_BYTES = int64_t(512) << 20, PIECE_LEAST = 2048;
 
+// Up to so many rows the forward pass takes x as it lies, the rows without a target
+// among them: packing would be a launch of its own (8 us of 42 for one row over 32768 x
+// 1536), for less work in products that read W at the rate of memory anyway.
+constexpr int64_t DIRECT_ROWS = 256;
+
 struct Call {
   int op = MUON_HEAD_LOSS;
   const void* x = nullptr;
@@ -107,11 +112,12 @@ muon_status check_buffers(const Call& c) {
 
 // Where everything lies in the workspace.
 struct Plan {
-  size_t offsets, row, target, xc, lse, ga, gb, logit, stats, dz, acc, bytes;
+  size_t offsets, row, target, xc, lse, ga, gb, logit, stats, dz, acc, part, bytes;
   int64_t ld_xc;       // elements of a packed row of x (and of acc)
   int64_t piece;       // columns of a piece of the vocabulary
   int64_t ld_dz;
   int32_t tiles;       // tiles of columns of the whole vocabulary (forward)
+  bool direct;         // the rows are not packed
 };
 
 // What the product of the logits of columns [c0, c0 + n) takes.
@@ -126,6 +132,15 @@ ProductArgs logits_args(const Call& c, const Plan& p, char* ws, int64_t c0, int6
   a.ld_q = ldw;
   a.q_elems = span(n, d.dim, ldw);
   a.offsets = reinterpret_cast<const int32_t*>(ws + p.offsets);
+  a.target = reinterpret_cast<const int32_t*>(ws + p.target);
+  if (p.direct) {
+    a.p = c.x;
+    a.ld_p = row_stride(d.rows, d.dim, d.ld_x);
+    a.p_elems = span(d.rows, d.dim, d.ld_x);
+    a.offsets = nullptr;
+    a.target = nullptr;
+    a.targets = c.targets;
+  }
   a.groups = 1;
   a.rows = int32_t(d.rows);
   a.n = int32_t(n);
@@ -134,7 +149,6 @@ ProductArgs logits_args(const Call& c, const Plan& p, char* ws, int64_t c0, int6
   a.cap = d.softcap;
   a.inv_cap = d.softcap != 0.f ? 1.f / d.softcap : 0.f;
   a.col0 = int32_t(c0);
-  a.target = reinterpret_cast<const int32_t*>(ws + p.target);
   a.logit = reinterpret_cast<float*>(ws + p.logit);
   a.stats = reinterpret_cast<float2*>(ws + p.stats);
   a.stat_tiles = p.tiles;
@@ -142,6 +156,63 @@ ProductArgs logits_args(const Call& c, const Plan& p, char* ws, int64_t c0, int6
   a.ga = reinterpret_cast<const float*>(ws + p.ga);
   a.gb = reinterpret_cast<const float*>(ws + p.gb);
   return a;
+}
+
+// The logits' gradients of a piece.
+ProductArgs dz_args(const Call& c, const Plan& p, char* ws, int64_t c0, int64_t n) {
+  ProductArgs a = logits_args(c, p, ws, c0, n);
+  a.out = ws + p.dz;
+  a.ld_out = p.ld_dz;
+  return a;
+}
+
+// grad_x from the piece that `a` makes: binary32 sums over the pieces, the last one's
+// rounded into grad_x.
+ProductArgs grad_x_args(const Call& c, const Plan& p, char* ws, const ProductArgs& a) {
+  const muon_head_desc& d = *c.desc;
+  const bool first = a.col0 == 0, last = a.col0 + int64_t(a.n) == d.vocab;
+  ProductArgs b = {};
+  b.p = a.out;
+  b.ld_p = p.ld_dz;
+  b.p_elems = span(d.rows, a.n, p.ld_dz);
+  b.q = a.q;
+  b.ld_q = a.ld_q;
+  b.q_elems = a.q_elems;
+  b.offsets = a.offsets;
+  b.groups = 1;
+  b.rows = a.rows;
+  b.n = int32_t(d.dim);
+  b.k = a.n;
+  b.f32 = a.f32;
+  b.out = last ? c.gx : ws + p.acc;
+  b.map = last ? reinterpret_cast<const int32_t*>(ws + p.row) : nullptr;
+  b.out_f32 = last ? a.f32 : 1;
+  b.ld_out = last ? row_stride(d.rows, d.dim, d.ld_grad_x) : p.ld_xc;
+  b.add = first ? nullptr : ws + p.acc;
+  b.add_f32 = 1;
+  b.ld_add = p.ld_xc;
+  return b;
+}
+
+// The rows of grad_w that the piece makes.
+ProductArgs grad_w_args(const Call& c, const Plan& p, const ProductArgs& a) {
+  const muon_head_desc& d = *c.desc;
+  ProductArgs b = {};
+  b.p = a.out;
+  b.ld_p = p.ld_dz;
+  b.p_elems = span(d.rows, a.n, p.ld_dz);
+  b.q = a.p;
+  b.ld_q = p.ld_xc;
+  b.q_elems = a.p_elems;
+  b.offsets = a.offsets;
+  b.groups = 1;
+  b.rows = a.rows;
+  b.m = a.n;
+  b.n = int32_t(d.dim);
+  b.f32 = b.out_f32 = a.f32;
+  b.ld_out = row_stride(d.vocab, d.dim, d.ld_grad_w);
+  b.out = reinterpret_cast<char*>(c.gw) + size_t(a.col0) * size_t(b.ld_out) * size_t(esize(d.dtype));
+  return b;
 }
 
 Plan plan_of(const Call& c, int cus) {
@@ -154,14 +225,17 @@ Plan plan_of(const Call& c, int cus) {
     return r;
   };
   const int64_t t = d.rows, esz = esize(d.dtype);
-  p.offsets = take(8);
-  p.row = take(4 * t);
-  p.target = take(4 * t);
+  p.direct = c.op == MUON_HEAD_LOSS && t <= DIRECT_ROWS;
   p.ld_xc = round_up(d.dim, 64);
-  p.xc = take(t * p.ld_xc * esz);
+  if (!p.direct) {
+    p.offsets = take(8);
+    p.row = take(4 * t);
+    p.target = take(4 * t);
+    p.xc = take(t * p.ld_xc * esz);
+  }
   if (c.op == MUON_HEAD_LOSS) {
     const ProductArgs a = logits_args(c, p, nullptr, 0, d.vocab);
-    const int tn = product_tile_n(FORM_NT, a, cus);
+    const int tn = product_tile_n(FORM_NT, EPI_LSE, a, cus);
     p.tiles = int32_t((d.vocab + tn - 1) / tn);
     p.logit = take(4 * t);
     p.stats = take(8 * t * p.tiles);
@@ -176,6 +250,13 @@ Plan plan_of(const Call& c, int cus) {
     p.ld_dz = p.piece;
     p.dz = take(t * p.ld_dz * esz);
     if ((c.op & MUON_HEAD_GRAD_X) && p.piece < d.vocab) p.acc = take(t * p.ld_xc * 4);
+    size_t part = 0;
+    for (int64_t c0 : {int64_t(0), (d.vocab - 1) / p.piece * p.piece}) {      // a whole piece, and the last one
+      const ProductArgs a = dz_args(c, p, nullptr, c0, std::min(p.piece, d.vocab - c0));
+      if (c.op & MUON_HEAD_GRAD_X) part = std::max(part, product_plan(FORM_NN, EPI_STORE, grad_x_args(c, p, nullptr, a), cus).bytes);
+      if (c.op & MUON_HEAD_GRAD_W) part = std::max(part, product_plan(FORM_TN, EPI_STORE, grad_w_args(c, p, a), cus).bytes);
+    }
+    p.part = take(int64_t(part));
   }
   p.bytes = at;
   return p;
@@ -183,7 +264,6 @@ Plan plan_of(const Call& c, int cus) {
 
 hipError_t enqueue(const Call& c, const Plan& p, char* ws, int cus, bool capturing) {
   const muon_head_desc& d = *c.desc;
-  const int64_t esz = esize(d.dtype);
   const bool fwd = c.op == MUON_HEAD_LOSS;
   auto timed = [&](int kc, const std::function<hipError_t()>& launch) -> hipError_t {
     return capturing ? launch() : api_timed(kc, c.stream, launch);
@@ -213,17 +293,20 @@ hipError_t enqueue(const Call& c, const Plan& p, char* ws, int cus, bool capturi
   h.dim = int32_t(d.dim);
   h.f32 = d.dtype == MUON_DTYPE_F32;
   h.chunk = int32_t(std::max<int64_t>(16, (d.rows + 511) / 512));
-  hipError_t e = timed(MUON_KC_MOMENTUM, [&] { return launch_head_rows(h, c.stream); });
+  hipError_t e = p.direct ? hipSuccess : timed(MUON_KC_MOMENTUM, [&] { return launch_head_rows(h, c.stream); });
   if (e != hipSuccess) return e;
   if (fwd) {
     const ProductArgs a = logits_args(c, p, ws, 0, d.vocab);
-    e = timed(MUON_KC_GRAM, [&] { return launch_product(FORM_NT, EPI_LSE, a, cus, c.stream); });
+    e = timed(MUON_KC_GRAM, [&] { return launch_product(FORM_NT, EPI_LSE, a, cus, ws + p.part, c.stream); });
     if (e != hipSuccess) return e;
     HeadFinish f = {};
     f.stats = a.stats;
     f.logit = a.logit;
     f.offsets = a.offsets;
     f.row = h.row;
+    f.targets = p.direct ? c.targets : nullptr;
+    f.ignore_index = d.ignore_index;
+    f.vocab = d.vocab;
     f.loss = c.loss;
     f.lse = c.lse;
     f.tiles = p.tiles;
@@ -232,52 +315,15 @@ hipError_t enqueue(const Call& c, const Plan& p, char* ws, int cus, bool capturi
   }
   for (int64_t c0 = 0; c0 < d.vocab && e == hipSuccess; c0 += p.piece) {
     const int64_t n = std::min(p.piece, d.vocab - c0);
-    const bool first = c0 == 0, last = c0 + n == d.vocab;
-    ProductArgs a = logits_args(c, p, ws, c0, n);
-    a.out = ws + p.dz;
-    a.ld_out = p.ld_dz;
-    e = timed(MUON_KC_GRAM, [&] { return launch_product(FORM_NT, EPI_DZ, a, cus, c.stream); });
+    const ProductArgs a = dz_args(c, p, ws, c0, n);
+    e = timed(MUON_KC_GRAM, [&] { return launch_product(FORM_NT, EPI_DZ, a, cus, ws + p.part, c.stream); });
     if (e == hipSuccess && c.gx) {
-      ProductArgs b = {};
-      b.p = a.out;
-      b.ld_p = p.ld_dz;
-      b.p_elems = span(d.rows, n, p.ld_dz);
-      b.q = a.q;
-      b.ld_q = a.ld_q;
-      b.q_elems = a.q_elems;
-      b.offsets = a.offsets;
-      b.groups = 1;
-      b.rows = a.rows;
-      b.n = int32_t(d.dim);
-      b.k = int32_t(n);
-      b.f32 = a.f32;
-      // binary32 sums over the pieces; the last one's are rounded into grad_x
-      b.out = last ? c.gx : ws + p.acc;
-      b.map = last ? h.row : nullptr;
-      b.out_f32 = last ? a.f32 : 1;
-      b.ld_out = last ? h.ld_grad_x : p.ld_xc;
-      b.add = first ? nullptr : ws + p.acc;
-      b.add_f32 = 1;
-      b.ld_add = p.ld_xc;
-      e = timed(MUON_KC_COMBINE, [&] { return launch_product(FORM_NN, EPI_STORE, b, cus, c.stream); });
+      const ProductArgs b = grad_x_args(c, p, ws, a);
+      e = timed(MUON_KC_COMBINE, [&] { return launch_product(FORM_NN, EPI_STORE, b, cus, ws + p.part, c.stream); });
     }
     if (e == hipSuccess && c.gw) {
-      ProductArgs b = {};
-      b.p = a.out;
-      b.ld_p = p.ld_dz;
-      b.p_elems = span(d.rows, n, p.ld_dz);
-      b.q = a.p;
-      b.ld_q = p.ld_xc;
-      b.q_elems = a.p_elems;
-      b.offsets = a.offsets;
-      b.groups = 1;
-      b.rows = a.rows;
-      b.m = int32_t(n);
-      b.n = int32_t(d.dim);
-      b.f32 = b.out_f32 = a.f32;
-      b.ld_out = row_stride(d.vocab, d.dim, d.ld_grad_w);
-      b.out = reinterpret_cast<char*>(c.gw) + size_t(c0) * size_t(b.ld_out) * size_t(esz);
-      e = timed(MUON_KC_COMBINE, [&] { return launch_product(FORM_TN, EPI_STORE, b, cus, c.stream); });
+      const ProductArgs b = grad_w_args(c, p, a);
+      e = timed(MUON_KC_COMBINE, [&] { return launch_product(FORM_TN, EPI_STORE, b, cus, ws + p.part, c.stream); });
     }
   }
   return e;
@@ -293,7 +339,7 @@ hipError_t enqueue_empty(const Call& c, int cus) {
   b.f32 = b.out_f32 = d.dtype == MUON_DTYPE_F32;
   b.ld_out = row_stride(d.vocab, d.dim, d.ld_grad_w);
   b.out = c.gw;
-  return launch_product(FORM_TN, EPI_STORE, b, cus, c.stream);
+  return launch_product(FORM_TN, EPI_STORE, b, cus, nullptr, c.stream);
 }
 
 muon_status run(const Call& c) {

@@ -94,7 +94,8 @@ struct Tile {
   int lo;           // the group's first row
   int i0, j0;       // first row of C in the group, first column
   int m, n;         // rows and columns from there on
-  int k;
+  int k0, k;        // first k, and how many
+  int part;         // partial matrix that it goes to, or -1: it is all of k
 };
 
 // Where an operand of a tile comes from.
@@ -112,21 +113,22 @@ __device__ __forceinline__ Source source_of(const ProductArgs& a, const Tile& t)
   Source s;
   // formed where it is used, from values the compiler takes for new ones: kept
   // through the k-loop the sources of two tiles would not fit the scalar registers
-  int lo = t.lo, i0 = t.i0, j0 = t.j0, grp = t.g;
-  asm volatile("" : "+s"(lo), "+s"(i0), "+s"(j0), "+s"(grp));
+  int lo = t.lo, i0 = t.i0, j0 = t.j0, grp = t.g, k0 = t.k0;
+  asm volatile("" : "+s"(lo), "+s"(i0), "+s"(j0), "+s"(grp), "+s"(k0));
   if constexpr (OPD == 0) {
     s.begin = reinterpret_cast<const char*>(a.p);
     s.end = s.begin + a.p_elems * E;
     s.ld = uint32_t(a.ld_p * E);
     s.valid = t.m;
-    s.base = FORM == FORM_TN ? s.begin + int64_t(lo) * s.ld + i0 * E : s.begin + (int64_t(lo) + i0) * s.ld;
+    s.base = FORM == FORM_TN ? s.begin + (int64_t(lo) + k0) * s.ld + i0 * E : s.begin + (int64_t(lo) + i0) * s.ld + k0 * E;
   } else {
     s.begin = reinterpret_cast<const char*>(a.q) + (FORM == FORM_TN ? 0 : grp * a.es_q * E);
     s.end = s.begin + a.q_elems * E;
     s.ld = uint32_t(a.ld_q * E);
     s.valid = t.n;
-    s.base = FORM == FORM_NT ? s.begin + int64_t(j0) * s.ld
-             : FORM == FORM_NN ? s.begin + j0 * E : s.begin + int64_t(lo) * s.ld + j0 * E;
+    s.base = FORM == FORM_NT   ? s.begin + int64_t(j0) * s.ld + k0 * E
+             : FORM == FORM_NN ? s.begin + int64_t(k0) * s.ld + j0 * E
+                               : s.begin + (int64_t(lo) + k0) * s.ld + j0 * E;
   }
   return s;
 }
@@ -343,13 +345,42 @@ __device__ __forceinline__ void mfma(f32x16& acc, const u32x4& q, const u32x4& p
 // Accumulators: acc[j][i][4 g + e] is row wp WTP + 32 i + (lane & 31) and column
 // wq WTQ + 32 j + 8 g + 4 (lane / 32) + e of the tile.
 
-// v[0 .. 7] (OF32: 4) to out, `cnt` of them; + addend.
+// Where a tile goes: its element (0, 0).
+struct Out {
+  char* at;
+  const char* add;          // addend's element (0, 0), or null
+  const int32_t* map;       // row of `at` for a row of the tile (from the tile's first), or null
+  int64_t ld, ld_add;
+};
+
+template <int FORM>
+__device__ __forceinline__ Out out_of(const ProductArgs& a, const Tile& t) {
+  Out o;
+  const int64_t row = t.i0 + (FORM == FORM_TN ? 0 : t.lo), g0 = FORM == FORM_TN ? t.g * a.es_out : 0;
+  if (t.part >= 0) {
+    o.ld = part_ld(a.n);
+    o.at = reinterpret_cast<char*>(a.part + (int64_t(t.part) * (FORM == FORM_TN ? a.m : a.rows) + row) * o.ld + t.j0);
+    o.add = nullptr;
+    o.map = nullptr;
+    o.ld_add = 0;
+    return o;
+  }
+  const int64_t first = g0 + (a.map ? 0 : row * a.ld_out) + t.j0, first_add = g0 + row * a.ld_add + t.j0;
+  o.at = reinterpret_cast<char*>(a.out) + first * (a.out_f32 ? 4 : 2);
+  o.add = a.add ? reinterpret_cast<const char*>(a.add) + first_add * (a.add_f32 ? 4 : 2) : nullptr;
+  o.map = a.map ? a.map + row : nullptr;
+  o.ld = a.ld_out;
+  o.ld_add = a.ld_add;
+  return o;
+}
+
+// v[0 .. 7] (OF32: 4), `cnt` of them, to element `at` of out, + addend's `add_at`.
 template <bool OF32>
-__device__ __forceinline__ void store_run(const ProductArgs& a, float* v, int64_t at, int64_t add_at, int cnt) {
+__device__ __forceinline__ void store_run(const Out& out, bool add_f32, float* v, int64_t at, int64_t add_at, int cnt) {
   constexpr int N = OF32 ? 4 : 8;
-  if (a.add) {
-    if (a.add_f32) {
-      const float* ad = reinterpret_cast<const float*>(a.add) + add_at;
+  if (out.add) {
+    if (add_f32) {
+      const float* ad = reinterpret_cast<const float*>(out.add) + add_at;
       if (cnt == N) {
 #pragma unroll
         for (int h = 0; h < N / 4; ++h) {
@@ -363,14 +394,14 @@ __device__ __forceinline__ void store_run(const ProductArgs& a, float* v, int64_
           if (e < cnt) v[e] += ad[e];
       }
     } else {
-      const uint16_t* ad = reinterpret_cast<const uint16_t*>(a.add) + add_at;
+      const uint16_t* ad = reinterpret_cast<const uint16_t*>(out.add) + add_at;
 #pragma unroll
       for (int e = 0; e < N; ++e)
         if (e < cnt) v[e] += bf16_bits_to_float(ad[e]);
     }
   }
   if constexpr (OF32) {
-    float* o = reinterpret_cast<float*>(a.out) + at;
+    float* o = reinterpret_cast<float*>(out.at) + at;
     if (cnt == N) {
       *reinterpret_cast<gstore16*>((__attribute__((address_space(1))) char*)o) =
           u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
@@ -380,7 +411,7 @@ __device__ __forceinline__ void store_run(const ProductArgs& a, float* v, int64_
         if (e < cnt) o[e] = v[e];
     }
   } else {
-    uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + at;
+    uint16_t* o = reinterpret_cast<uint16_t*>(out.at) + at;
     if (cnt == N) {
       *reinterpret_cast<gstore16*>((__attribute__((address_space(1))) char*)o) =
           u32x4{float2_to_bf16x2_bits(v[0], v[1]), float2_to_bf16x2_bits(v[2], v[3]),
@@ -397,8 +428,8 @@ __device__ __forceinline__ void store_run(const ProductArgs& a, float* v, int64_
 // outputs and addends), a part of the tile's rows at a time where all do not fit;
 // else as bfloat16.
 template <class S, int FORM, bool OF32, bool WIDE>
-__device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t,
-                                           char* smem, int tid) {
+__device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], const Out& out, bool add_f32,
+                                           const Tile& t, char* smem, int tid) {
   constexpr int ES = WIDE ? 4 : 2, EP = S::BN * ES + 16;
   constexpr int LDS = Layout<S, FORM>::BYTES;
   constexpr int PASSES = S::BM * EP <= LDS ? 1 : S::BM / 2 * EP <= LDS ? 2 : 4;
@@ -435,13 +466,11 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], co
       const int r = q / CPR, c = q % CPR * N;
       const int cnt = min(N, t.n - c);
       if (r >= rows || cnt <= 0) continue;
-      const int64_t crow = t.i0 + pass * ROWS + r + (FORM == FORM_TN ? 0 : t.lo);
-      const int64_t g0 = FORM == FORM_TN ? t.g * a.es_out : 0;
-      const int64_t row = a.map ? a.map[crow] : crow;
-      const int64_t at = g0 + row * a.ld_out + t.j0 + c;
+      const int row = pass * ROWS + r;
+      const int64_t at = (out.map ? out.map[row] : row) * out.ld + c;
       if constexpr (!WIDE) {
         const u32x4 v = *reinterpret_cast<const u32x4*>(smem + r * EP + c * 2);
-        uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + at;
+        uint16_t* o = reinterpret_cast<uint16_t*>(out.at) + at;
         if (cnt == N) {
           *reinterpret_cast<gstore16*>((__attribute__((address_space(1))) char*)o) = v;
         } else {
@@ -457,7 +486,7 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], co
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[4 * h + e] = x[e];
         }
-        store_run<OF32>(a, v, at, g0 + crow * a.ld_add + t.j0 + c, cnt);
+        store_run<OF32>(out, add_f32, v, at, row * out.ld_add + c, cnt);
       }
     }
   }
@@ -476,7 +505,7 @@ __device__ __forceinline__ void lse_tile(f32x16 (&acc)[S::FQ][S::FP], const Prod
 #pragma unroll
   for (int i = 0; i < S::FP; ++i) {
     const int r = wp * S::WTP + 32 * i + (lane & 31);
-    const int target = r < t.m ? a.target[t.i0 + r] - a.col0 - t.j0 : -1;
+    const int target = r < t.m ? target_of(a, t.i0 + r) - t.j0 : -1;
 #pragma unroll
     for (int j = 0; j < S::FQ; ++j)
 #pragma unroll
@@ -529,7 +558,7 @@ __device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const
 #pragma unroll
   for (int i = 0; i < S::FP; ++i) {
     const int r = min(wp * S::WTP + 32 * i + (lane & 31), t.m - 1) + t.i0;
-    const int target = a.target[r] - a.col0 - t.j0;
+    const int target = target_of(a, r) - t.j0;
     const float lse = a.lse[r], ga = a.ga[r], gb = a.gb[r];
     const bool here = __any(target >= wq * S::WTQ && target < (wq + 1) * S::WTQ);
 #pragma unroll
@@ -545,84 +574,54 @@ __device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const
 
 // ------------------------------------------------------------------ kernel
 
-// Inclusive sums over the groups of their tiles of rows: pre[g + 1] - pre[g] tiles
-// of BM rows, pre[0] = 0.  All threads take part.
-template <class S>
-__device__ __forceinline__ void count_tiles(const ProductArgs& a, int* pre, int tid) {
-  __shared__ int wave_sum[S::NT / 64];
-  const int lane = tid & 63, wave = tid >> 6;
-  int carry = 0;
-  if (tid == 0) pre[0] = 0;
-  for (int b = 0; b < a.groups; b += S::NT) {
-    const int g = b + tid;
-    int v = 0;
-    if (g < a.groups) {
-      int lo, hi;
-      group_range(a, g, lo, hi);
-      v = (hi - lo + S::BM - 1) / S::BM;
-    }
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) {
-      const int o = __shfl_up(v, s);
-      if (lane >= s) v += o;
-    }
-    if (lane == 63) wave_sum[wave] = v;
-    __syncthreads();
-    int before = carry, all = 0;
-#pragma unroll
-    for (int w = 0; w < S::NT / 64; ++w) {
-      if (w < wave) before += wave_sum[w];
-      all += wave_sum[w];
-    }
-    if (g < a.groups) pre[g + 1] = before + v;
-    carry += all;
-    __syncthreads();
-  }
-  __syncthreads();
-}
-
 // Tiles of C go through the columns in bands of BAND rows of tiles, so that the
 // tiles that run together on an XCD (32 or more) share panels of P and Q in its L2.
 constexpr int BAND = 8;
 
+// Tile number t.  NT, NN: pre counts the groups' tiles of rows; chunks of k follow each
+// other, all tiles of one before those of the next.  TN: pre counts their pieces of k.
 template <class S, int FORM>
-__device__ __forceinline__ Tile tile_at(const ProductArgs& a, const int* pre, int t) {
+__device__ __forceinline__ Tile tile_at(const ProductArgs& a, const int* pre, int chunk, int t) {
   Tile r;
   const int nt = (a.n + S::BN - 1) / S::BN;
-  int mt, first;          // tiles of rows of the group, number of its first tile
-  if constexpr (FORM == FORM_TN) {
-    mt = (a.m + S::BM - 1) / S::BM;
-    r.g = t / (mt * nt);
-    first = r.g * mt * nt;
-  } else {
-    int lo = 0, hi = a.groups;          // pre[lo] nt <= t < pre[hi] nt
-    const int rt = t / nt;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (pre[mid] <= rt) lo = mid;
-      else hi = mid;
-    }
-    r.g = __builtin_amdgcn_readfirstlane(lo);
-    const int p0 = __builtin_amdgcn_readfirstlane(pre[r.g]);
-    mt = __builtin_amdgcn_readfirstlane(pre[r.g + 1]) - p0;
-    first = p0 * nt;
+  int mt, piece = 0;        // tiles of rows of the group (TN: of C)
+  const int all = FORM == FORM_TN ? 0 : __builtin_amdgcn_readfirstlane(pre[a.groups]) * nt;
+  if constexpr (FORM != FORM_TN) {
+    piece = t / all;
+    t -= piece * all;
   }
-  const int u = t - first, b = u / (BAND * nt), rows = min(BAND, mt - b * BAND), v = u - b * BAND * nt;
+  mt = FORM == FORM_TN ? (a.m + S::BM - 1) / S::BM : 1;
+  const int u = t / (mt * nt);
+  int lo = 0, hi = a.groups;          // pre[lo] <= u < pre[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (pre[mid] <= u) lo = mid;
+    else hi = mid;
+  }
+  r.g = __builtin_amdgcn_readfirstlane(lo);
+  const int before = __builtin_amdgcn_readfirstlane(pre[r.g]), of = __builtin_amdgcn_readfirstlane(pre[r.g + 1]) - before;
+  if constexpr (FORM == FORM_TN) {
+    piece = u - before;
+    t -= u * mt * nt;
+  } else {
+    mt = of;
+    t -= before * nt;
+  }
+  const int b = t / (BAND * nt), rows = min(BAND, mt - b * BAND), v = t - b * BAND * nt;
   r.i0 = (b * BAND + v % rows) * S::BM;
   r.j0 = v / rows * S::BN;
-  int lo, hi;
-  group_range(a, r.g, lo, hi);
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  hi = __builtin_amdgcn_readfirstlane(hi);
-  r.lo = lo;
+  int first, end;
+  group_range(a, r.g, first, end);
+  first = __builtin_amdgcn_readfirstlane(first);
+  end = __builtin_amdgcn_readfirstlane(end);
+  r.lo = first;
   r.n = a.n - r.j0;
-  if constexpr (FORM == FORM_TN) {
-    r.m = a.m - r.i0;
-    r.k = hi - lo;
-  } else {
-    r.m = hi - lo - r.i0;
-    r.k = a.k;
-  }
+  const int k = FORM == FORM_TN ? end - first : a.k;
+  r.m = FORM == FORM_TN ? a.m - r.i0 : end - first - r.i0;
+  r.k0 = piece * chunk;                // below 2^31: a group's pieces end with its rows
+  r.k = min(chunk, k - r.k0);
+  if constexpr (FORM == FORM_TN) r.part = of > 1 ? 2 * (before - r.g) + piece : -1;
+  else r.part = k > chunk ? piece : -1;
   return r;
 }
 
@@ -640,14 +639,26 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
   // group to group: the grid takes as many consecutive tiles at a time as it has
   // workgroups, so that a long group is spread over all of them.
   const int xcd = blockIdx.x % NUM_XCD, slot = blockIdx.x / NUM_XCD, slots = gridDim.x / NUM_XCD;
-  int tile, step, end;
+  __shared__ int wave_sum[S::NT / 64];
+  int tile, step, end, chunk = a.chunk;
   if constexpr (FORM == FORM_TN) {
-    end = a.groups * ((a.m + S::BM - 1) / S::BM) * ((a.n + S::BN - 1) / S::BN);
+    chunk = safe_chunk<S::NT>(a, pre, wave_sum, tid);
+    group_sums<S::NT>(a.groups, pre, wave_sum, tid, [&](int g) {
+      int lo, hi;
+      group_range(a, g, lo, hi);
+      return pieces_of(hi - lo, chunk);
+    });
+    end = __builtin_amdgcn_readfirstlane(pre[a.groups]) * ((a.m + S::BM - 1) / S::BM) * ((a.n + S::BN - 1) / S::BN);
     tile = xcd * slots + slot;
     step = gridDim.x;
   } else {
-    count_tiles<S>(a, pre, tid);
-    const int total = __builtin_amdgcn_readfirstlane(pre[a.groups]) * ((a.n + S::BN - 1) / S::BN);
+    group_sums<S::NT>(a.groups, pre, wave_sum, tid, [&](int g) {
+      int lo, hi;
+      group_range(a, g, lo, hi);
+      return (hi - lo + S::BM - 1) / S::BM;
+    });
+    const int total = __builtin_amdgcn_readfirstlane(pre[a.groups]) * ((a.n + S::BN - 1) / S::BN) *
+                      (EPI == EPI_STORE ? (a.k + chunk - 1) / chunk : 1);
     const int per = (total + NUM_XCD - 1) / NUM_XCD;
     tile = xcd * per + slot;
     end = min((xcd + 1) * per, total);
@@ -680,7 +691,7 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
       last_loads<S, S::BN, QK>(lq, sq, 0, t.k, tid);
     }
   };
-  Tile t = tile_at<S, FORM>(a, pre, tile);
+  Tile t = tile_at<S, FORM>(a, pre, chunk, tile);
   if (t.k > 0) {
     begin_tile(t);
     load_chunks(rp, lp);
@@ -714,7 +725,7 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
     // the next tile's first stage, if there is one
     auto load_next = [&] {
       if (!more) return;
-      tn = tile_at<S, FORM>(a, pre, ntile);
+      tn = tile_at<S, FORM>(a, pre, chunk, ntile);
       if (tn.k <= 0) return;
       begin_tile(tn);
       load_chunks(rp, lp);
@@ -850,15 +861,12 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
       lse_tile<S>(acc, a, t, smem, tid);
     } else {
       if constexpr (EPI == EPI_DZ) gradient_tile<S>(acc, a, t, tid);
-      if constexpr (EPI == EPI_DZ) {
-        store_tile<S, FORM, S::F32, S::F32>(acc, a, t, smem, tid);
-      } else if constexpr (S::F32) {
-        store_tile<S, FORM, true, true>(acc, a, t, smem, tid);
-      } else {
-        if (a.out_f32) store_tile<S, FORM, true, true>(acc, a, t, smem, tid);
-        else if (a.add) store_tile<S, FORM, false, true>(acc, a, t, smem, tid);
-        else store_tile<S, FORM, false, false>(acc, a, t, smem, tid);
-      }
+      const Out out = out_of<FORM>(a, t);
+      if constexpr (S::F32) store_tile<S, FORM, true, true>(acc, out, a.add_f32, t, smem, tid);
+      else if constexpr (EPI == EPI_DZ) store_tile<S, FORM, false, false>(acc, out, false, t, smem, tid);
+      else if (a.out_f32 || t.part >= 0) store_tile<S, FORM, true, true>(acc, out, a.add_f32, t, smem, tid);
+      else if (a.add) store_tile<S, FORM, false, true>(acc, out, a.add_f32, t, smem, tid);
+      else store_tile<S, FORM, false, false>(acc, out, false, t, smem, tid);
     }
     if (!more) break;
     lds_barrier();
@@ -870,10 +878,12 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
 template <class S, int FORM, int EPI>
 hipError_t launch_shape(const ProductArgs& a, int cus, hipStream_t stream) {
   using LY = Layout<S, FORM>;
-  const size_t lds = LY::BYTES + (FORM == FORM_TN ? 0 : (size_t(a.groups) + 1) * 4);
+  const size_t lds = LY::BYTES + (size_t(a.groups) + 1) * 4;
   const int64_t nt = (a.n + S::BN - 1) / S::BN;
-  const int64_t mt = FORM == FORM_TN ? int64_t(a.groups) * ((a.m + S::BM - 1) / S::BM)
-                                     : a.rows / S::BM + std::min(a.groups, a.rows);   // at most
+  // tiles of rows and pieces of k, at most
+  const int64_t mt = FORM == FORM_TN ? (a.groups + int64_t(a.rows / a.chunk)) * ((a.m + S::BM - 1) / S::BM)
+                                     : (a.rows / S::BM + int64_t(std::min(a.groups, a.rows))) *
+                                           (EPI == EPI_STORE ? (a.k + a.chunk - 1) / a.chunk : 1);
   // workgroups that a compute unit holds: by its LDS, and by waves (8 a unit at 256 registers)
   const int fit = std::max(1, std::min(int((160 * 1024) / (lds + 64)), 2048 / S::NT / 4));
   const int64_t grid = std::min<int64_t>((mt * nt + NUM_XCD - 1) / NUM_XCD * NUM_XCD,
@@ -888,6 +898,7 @@ hipError_t launch_shape(const ProductArgs& a, int cus, hipStream_t stream) {
 
 using Large = Shape<256, 256, 2, 4, false>;
 using Medium = Shape<128, 128, 2, 2, false>;
+using MediumTn = Shape<128, 256, 2, 4, false>;
 using Small = Shape<32, 128, 1, 4, false>;
 using MediumF32 = Shape<128, 128, 2, 2, true>;
 using SmallF32 = Shape<32, 128, 1, 4, true>;

@@ -58,12 +58,12 @@ __global__ __launch_bounds__(TS * TS) void product_small_kernel(const ProductArg
       float sum = in ? __expf(z - (mx == -INFINITY ? 0.f : mx)) : 0.f;
       for (int s = 1; s < TS; s *= 2) sum += __shfl_xor(sum, s);
       if (in) {
-        if (j == a.target[i]) a.logit[i] = z;
+        if (j == target_of(a, i)) a.logit[i] = z;
         if (tx == 0) a.stats[int64_t(i) * a.stat_tiles + jt] = make_float2(mx, sum);
       }
     } else if (in) {
       const float z = soft_capped(c, a.cap, a.inv_cap);
-      const float d = logit_gradient(a, z, a.col0 + j, a.target[i], a.lse[i], a.ga[i], a.gb[i]);
+      const float d = logit_gradient(a, z, j, target_of(a, i), a.lse[i], a.ga[i], a.gb[i]);
       store1(a.out, int64_t(i) * a.ld_out + j, d, a.out_f32);
     }
   }
@@ -83,34 +83,175 @@ hipError_t launch_small(const ProductArgs& a, hipStream_t stream) {
 
 namespace {
 
-int product_shape(int form, const ProductArgs& a, int cus) {
-  const int64_t esz = a.f32 ? 4 : 2;
-  // 16-byte loads (product_tile.h)
-  if (a.p_elems * esz < 16 || a.q_elems * esz < 16 || (form == FORM_TN && a.ld_p * esz < 16) ||
-      (form != FORM_NT && a.ld_q * esz < 16))
-    return SHAPE_NAIVE;
-  const int64_t rows = form == FORM_TN ? a.m : a.rows / a.groups;       // of a group, on average
-  if (form != FORM_TN && rows <= 32) return SHAPE_SMALL;
-  const int64_t groups = form == FORM_TN ? a.groups : std::max<int64_t>(1, std::min<int64_t>(a.groups, a.rows / 256));
-  const int64_t large = groups * ((rows + 255) / 256) * ((a.n + 255) / 256);
-  return large >= cus ? SHAPE_LARGE : SHAPE_MEDIUM;
+constexpr int RT = 256;
+
+// Adds the partial sums of what was cut along k (ProductPlan), in order, to the
+// addend, and rounds.  A workgroup row (blockIdx.y) a group; four columns a thread.
+template <int FORM>
+__global__ __launch_bounds__(RT) void product_sum_kernel(const ProductArgs a) {
+  extern __shared__ int pre[];
+  __shared__ int wave_sum[RT / 64];
+  const int g = blockIdx.y, tid = threadIdx.x;
+  int lo, hi;
+  group_range(a, g, lo, hi);
+  int64_t slot = 0, rows_of, row0;
+  int pieces, rows;
+  if constexpr (FORM == FORM_TN) {
+    if (hi - lo <= a.chunk) return;
+    const int chunk = safe_chunk<RT>(a, pre, wave_sum, tid);
+    pieces = pieces_of(hi - lo, chunk);
+    if (pieces == 1) return;
+    group_sums<RT>(a.groups, pre, wave_sum, tid, [&](int x) {
+      int l, h;
+      group_range(a, x, l, h);
+      return pieces_of(h - l, chunk);
+    });
+    slot = 2 * int64_t(pre[g] - g);
+    rows = a.m;
+    rows_of = a.m;
+    row0 = 0;
+  } else {
+    pieces = (a.k + a.chunk - 1) / a.chunk;
+    rows = hi - lo;
+    rows_of = a.rows;
+    row0 = lo;
+  }
+  const int64_t ld = part_ld(a.n);
+  const int quads = int(ld / 4);
+  const int64_t base = FORM == FORM_TN ? g * a.es_out : 0;
+  for (int64_t q = int64_t(blockIdx.x) * RT + tid; q < int64_t(rows) * quads; q += int64_t(gridDim.x) * RT) {
+    const int64_t r = row0 + q / quads;
+    const int c = int(q % quads) * 4, cnt = min(4, a.n - c);
+    const float4* p = reinterpret_cast<const float4*>(a.part + (slot * rows_of + r) * ld + c);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < pieces; ++i) {
+      const float4 v = p[int64_t(i) * rows_of * (ld / 4)];
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    float v[4] = {s.x, s.y, s.z, s.w};
+    if (a.add) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < cnt) v[e] += load1(a.add, base + r * a.ld_add + c + e, a.add_f32);
+    }
+    const int64_t at = base + (a.map ? a.map[r] : r) * a.ld_out + c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < cnt) store1(a.out, at + e, v[e], a.out_f32);
+  }
 }
+
+template <int FORM>
+hipError_t launch_sum(const ProductArgs& a, int cus, hipStream_t stream) {
+  const int64_t rows = FORM == FORM_TN ? a.m : std::max(1, a.rows / a.groups);
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((rows * part_ld(a.n) / 4 + RT - 1) / RT, cus * 8 / a.groups + 1));
+  hipLaunchKernelGGL((product_sum_kernel<FORM>), dim3(unsigned(blocks), unsigned(a.groups)), dim3(RT),
+                     (size_t(a.groups) + 1) * 4, stream, a);
+  return hipGetLastError();
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-int32_t product_tile_n(int form, const ProductArgs& a, int cus) {
-  switch (product_shape(form, a, cus)) {
+// The fastest plan by a model of the time, in us: rounds of tiles over the GPU, a
+// stage of k (64 of bfloat16, 32 of binary32) and a tile's start and end measured for
+// each shape, and the partial sums' way to memory and back at 5 TB/s.
+ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus) {
+  const int64_t esz = a.f32 ? 4 : 2, ke = 128 / esz;
+  // 16-byte loads (product_tile.h)
+  if (a.p_elems * esz < 16 || a.q_elems * esz < 16 || (form == FORM_TN && a.ld_p * esz < 16) ||
+      (form != FORM_NT && a.ld_q * esz < 16))
+    return {SHAPE_NAIVE, 0, 0};
+  struct Kind {
+    int shape, bm, bn, per_cu;
+    double stage, ends;
+  };
+  static const Kind KINDS[] = {{SHAPE_LARGE, 256, 256, 1, 2.2, 8.0},
+                               {SHAPE_MEDIUM, 128, 128, 2, 1.5, 5.0},
+                               {SHAPE_SMALL, 32, 128, 3, 1.1, 3.0}};
+  static const Kind KINDS_TN[] = {{SHAPE_LARGE, 256, 256, 1, 2.3, 8.0}, {SHAPE_MEDIUM, 128, 256, 1, 1.4, 6.0}};
+  static const Kind KINDS_F32[] = {{SHAPE_MEDIUM, 128, 128, 2, 4.0, 5.0}, {SHAPE_SMALL, 32, 128, 3, 1.5, 3.0}};
+  static const Kind KINDS_F32_TN[] = {{SHAPE_MEDIUM, 128, 128, 2, 4.0, 5.0}};
+  const bool tn = form == FORM_TN;
+  const Kind* kinds = a.f32 ? (tn ? KINDS_F32_TN : KINDS_F32) : (tn ? KINDS_TN : KINDS);
+  const int nkinds = a.f32 ? (tn ? 1 : 2) : (tn ? 2 : 3);
+  const int64_t groups = std::max(1, a.groups);
+  ProductPlan best = {kinds[0].shape, 1 << 30, 0};
+  double least = 1e30;
+  for (int i = 0; i < nkinds; ++i) {
+    const Kind& s = kinds[i];
+    // tiles of rows: half a tile more a group than its rows fill
+    const int64_t mt = tn ? groups * ceil_div(a.m, s.bm)
+                          : groups == 1 ? ceil_div(a.rows, s.bm)
+                                        : std::max<int64_t>(std::min<int64_t>(groups, a.rows), a.rows / s.bm + groups / 2);
+    const int64_t tiles = mt * ceil_div(a.n, s.bn), slots = int64_t(cus) * s.per_cu;
+    const int64_t stages = std::max<int64_t>(1, ceil_div(tn ? a.rows / groups : a.k, ke));   // of a tile, on average
+    for (int cut = 1; cut <= 16; ++cut) {
+      if (cut > 1 && epi != EPI_STORE) break;
+      ProductPlan p = {s.shape, 1 << 30, 0};
+      double us;
+      if (!tn) {
+        const int64_t each = ceil_div(stages, cut);
+        if (cut > 1 && each < 4) break;
+        const int64_t chunks = ceil_div(stages, each);
+        if (chunks != cut) continue;
+        us = ceil_div(tiles * cut, slots) * (each * s.stage + s.ends);
+        if (cut > 1) {
+          p.chunk = int32_t(ceil_div(each * ke, 64) * 64);
+          p.bytes = size_t(chunks) * size_t(a.rows) * size_t(part_ld(a.n)) * 4;
+          us += 3.0 + 2e-6 / 5.0 * double(p.bytes);
+        }
+      } else {
+        // groups of very different lengths: a piece of 2^(cut - 1) x 512 rows at most, so that
+        // the longest tile is not much longer than a workgroup's share
+        if (cut == 16) break;
+        const int64_t chunk = cut == 1 ? int64_t(1) << 30 : int64_t(512) << (cut - 2);
+        if (cut > 1 && chunk >= a.rows) break;
+        // one group may have all rows
+        const int64_t longest = std::min<int64_t>(ceil_div(a.rows, ke), chunk / ke);
+        const double share = double(tiles) * stages * s.stage / slots + double(tiles) * s.ends / slots;
+        us = std::max(double(ceil_div(tiles, slots)) * s.ends + share, groups > 1 ? 0.5 * longest * s.stage : double(longest) * s.stage) ;
+        if (cut > 1) {
+          p.chunk = int32_t(chunk);
+          const int64_t pieces = 2 * (a.rows / chunk);
+          p.bytes = size_t(pieces) * size_t(a.m) * size_t(part_ld(a.n)) * 4;
+          us += 5.0 + 1e-6 / 5.0 * double(p.bytes) + double(pieces / 2) * (tiles / groups) * s.ends / slots;
+        }
+      }
+      if (p.bytes > (size_t(2) << 30)) continue;
+      if (us < least) {
+        least = us;
+        best = p;
+      }
+    }
+  }
+  return best;
+}
+
+int32_t product_tile_n(int form, int epi, const ProductArgs& a, int cus) {
+  switch (product_plan(form, epi, a, cus).shape) {
     case SHAPE_NAIVE: return TS;
-    case SHAPE_LARGE: return a.f32 ? 128 : 256;
+    case SHAPE_LARGE: return 256;
     default: return 128;
   }
 }
 
-hipError_t launch_product(int form, int epi, const ProductArgs& a, int cus, hipStream_t stream) {
-  const int shape = product_shape(form, a, cus);
-  if (shape != SHAPE_NAIVE)
-    return form == FORM_NT ? launch_nt(shape, epi, a, cus, stream)
-           : form == FORM_NN ? launch_nn(shape, a, cus, stream) : launch_tn(shape, a, cus, stream);
+hipError_t launch_product(int form, int epi, const ProductArgs& args, int cus, char* ws, hipStream_t stream) {
+  const ProductPlan plan = product_plan(form, epi, args, cus);
+  ProductArgs a = args;
+  if (plan.shape != SHAPE_NAIVE) {
+    a.chunk = plan.chunk;
+    a.part = reinterpret_cast<float*>(ws);
+    hipError_t e = form == FORM_NT   ? launch_nt(plan.shape, epi, a, cus, stream)
+                   : form == FORM_NN ? launch_nn(plan.shape, a, cus, stream) : launch_tn(plan.shape, a, cus, stream);
+    if (e == hipSuccess && plan.bytes)
+      e = form == FORM_TN ? launch_sum<FORM_TN>(a, cus, stream) : launch_sum<FORM_NT>(a, cus, stream);
+    return e;
+  }
   if (epi == EPI_LSE) return launch_small<FORM_NT, EPI_LSE>(a, stream);
   if (epi == EPI_DZ) return launch_small<FORM_NT, EPI_DZ>(a, stream);
   switch (form) {

@@ -38,13 +38,16 @@ struct ProductArgs {
   int64_t q_elems;             // the same for q (NT, NN: for one group's)
   int32_t groups, rows;
   int32_t m, n, k;             // m: TN; k: NT and NN
+  int32_t chunk;               // k values of a tile at most (STORE only; see ProductPlan)
+  float* part;                 // partial tiles of what is cut along k
   int32_t f32;                 // type of p and q: 1 binary32, 0 bfloat16
   int32_t out_f32, add_f32;
   // head
   float cap, inv_cap;          // soft cap (0: none)
   int32_t col0;                // vocabulary index of column 0
   int32_t stat_tiles;          // tiles of columns of a row of `stats`
-  const int32_t* target;       // of every row of C
+  const int32_t* target;       // of every row of C; null: targets
+  const int64_t* targets;      // the caller's
   const float* lse;
   const float* ga;             // grad_loss + grad_lse
   const float* gb;             // grad_loss
@@ -52,15 +55,33 @@ struct ProductArgs {
   float2* stats;               // [row][tile]: maximum, sum of exp(z - maximum)
 };
 
-// Tile shapes (binary32 and TN have no large or small one of their own).
+// Tile shapes.
 enum ProductShape : int { SHAPE_NAIVE = 0, SHAPE_SMALL = 1, SHAPE_MEDIUM = 2, SHAPE_LARGE = 3 };
 hipError_t launch_nt(int shape, int epi, const ProductArgs& a, int cus, hipStream_t stream);
 hipError_t launch_nn(int shape, const ProductArgs& a, int cus, hipStream_t stream);
 hipError_t launch_tn(int shape, const ProductArgs& a, int cus, hipStream_t stream);
 
+// How a product runs.  k may be cut into chunks, so that few tiles fill the GPU and
+// one long group does not hold up the rest: a tile then takes `chunk` of k, writes
+// binary32 partial sums, and a second kernel adds them, in order.
+//   NT, NN  every tile is cut alike: partial sums are (chunk of k) x rows x n
+//   TN      a group of more than `chunk` rows is cut into n_g pieces; with s_g the sum of
+//           n - 1 over the groups before it, its partial matrices (m x n) are 2 s_g,
+//           2 s_g + 1, .. (n <= 2 (n - 1), so groups do not meet), and there are 2 rows /
+//           chunk of them at most.  Offsets whose groups overlap, and have more rows in
+//           all than there are, are not cut.
+struct ProductPlan {
+  int shape;
+  int32_t chunk;               // k of a chunk, a multiple of 64
+  size_t bytes;                // of partial sums: workspace that launch_product needs
+};
+ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus);
+constexpr int64_t part_ld(int64_t n) { return (n + 3) / 4 * 4; }
+
 // Columns of a tile of `stats` that launch_product writes.
-int32_t product_tile_n(int form, const ProductArgs& a, int cus);
-hipError_t launch_product(int form, int epi, const ProductArgs& a, int cus, hipStream_t stream);
+int32_t product_tile_n(int form, int epi, const ProductArgs& a, int cus);
+// `ws`: 256-byte aligned, product_plan's bytes.
+hipError_t launch_product(int form, int epi, const ProductArgs& a, int cus, char* ws, hipStream_t stream);
 
 // The head's rows that have a target, packed: offsets = {0, their number}, and
 // for each its row, target, and (gradient) lse, ga and gb; the rows of x copied to
@@ -88,12 +109,15 @@ struct HeadRows {
 };
 hipError_t launch_head_rows(const HeadRows& a, hipStream_t stream);
 
-// loss and lse of the packed rows from the tiles' maxima and sums.
+// loss and lse from the tiles' maxima and sums: of the packed rows (`targets` null), or
+// of all rows, with what those without a target get.
 struct HeadFinish {
   const float2* stats;
   const float* logit;
   const int32_t* offsets;
   const int32_t* row;
+  const int64_t* targets;
+  int64_t ignore_index, vocab;
   float* loss;
   float* lse;
   int32_t tiles, rows;
