@@ -116,17 +116,17 @@ __global__ __launch_bounds__(NT) void head_finish_kernel(const HeadFinish a) {
   for (int t = lane; t < a.tiles; t += 64) {
     const float2 v = s[t];
     const float n = fmaxf(m, v.x), f = n == -INFINITY ? 0.f : n;
-    sum = sum * __expf(m - f) + v.y * __expf(v.x - f);
+    sum = sum * __builtin_amdgcn_exp2f(m - f) + v.y * __builtin_amdgcn_exp2f(v.x - f);
     m = n;
   }
   for (int d = 1; d < 64; d *= 2) {
     const float om = __shfl_xor(m, d), os = __shfl_xor(sum, d);
     const float n = fmaxf(m, om), f = n == -INFINITY ? 0.f : n;
-    sum = sum * __expf(m - f) + os * __expf(om - f);
+    sum = sum * __builtin_amdgcn_exp2f(m - f) + os * __builtin_amdgcn_exp2f(om - f);
     m = n;
   }
   if (lane == 0) {
-    const float lse = (m == -INFINITY ? 0.f : m) + logf(sum);
+    const float lse = __builtin_fmaf(m == -INFINITY ? 0.f : m, LN2, logf(sum));
     const int r = a.targets ? i : a.row[i];
     a.lse[r] = lse;
     a.loss[r] = lse - a.logit[i];

@@ -8,7 +8,9 @@ hipError_t launch_nt(int shape, int epi, const ProductArgs& a, int cus, hipStrea
     using S = decltype(s);
     switch (epi) {
       case EPI_LSE: return launch_shape<S, FORM_NT, EPI_LSE>(a, cus, stream);
+      case EPI_LSE_CAP: return launch_shape<S, FORM_NT, EPI_LSE_CAP>(a, cus, stream);
       case EPI_DZ: return launch_shape<S, FORM_NT, EPI_DZ>(a, cus, stream);
+      case EPI_DZ_CAP: return launch_shape<S, FORM_NT, EPI_DZ_CAP>(a, cus, stream);
       default: return launch_shape<S, FORM_NT, EPI_STORE>(a, cus, stream);
     }
   };

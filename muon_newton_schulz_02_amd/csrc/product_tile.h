@@ -424,12 +424,21 @@ __device__ __forceinline__ void store_run(const Out& out, bool add_f32, float* v
   }
 }
 
+// What a lane writes over its row's element in the target's column, for its FP rows:
+// the accumulators have the softmax's part alone (a change of theirs under a branch
+// costs as many copies as there are).
+template <class S>
+struct Patch {
+  int col[S::FP];           // column of the tile; -1: not this lane
+  float value[S::FP];
+};
+
 // C to `out`.  OF32: out is binary32.  WIDE: staged in LDS as binary32 (for binary32
 // outputs and addends), a part of the tile's rows at a time where all do not fit;
 // else as bfloat16.
 template <class S, int FORM, bool OF32, bool WIDE>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], const Out& out, bool add_f32,
-                                           const Tile& t, char* smem, int tid) {
+                                           const Tile& t, char* smem, int tid, const Patch<S>* patch = nullptr) {
   constexpr int ES = WIDE ? 4 : 2, EP = S::BN * ES + 16;
   constexpr int LDS = Layout<S, FORM>::BYTES;
   constexpr int PASSES = S::BM * EP <= LDS ? 1 : S::BM / 2 * EP <= LDS ? 2 : 4;
@@ -454,6 +463,12 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], co
             else *reinterpret_cast<u32x2*>(d) = u32x2{float2_to_bf16x2_bits(c[4 * g], c[4 * g + 1]),
                                                       float2_to_bf16x2_bits(c[4 * g + 2], c[4 * g + 3])};
           }
+        // after this lane's own write of the column, in order
+        if (patch && patch->col[i] >= 0) {
+          char* d = smem + r * EP + patch->col[i] * ES;
+          if constexpr (WIDE) *reinterpret_cast<float*>(d) = patch->value[i];
+          else *reinterpret_cast<uint16_t*>(d) = float_to_bf16_bits(patch->value[i]);
+        }
       }
     }
     lds_barrier();
@@ -494,7 +509,7 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], co
 
 // Every row's maximum and sum of exponentials over the tile's columns, and the
 // target's logit.
-template <class S>
+template <class S, bool CAP>
 __device__ __forceinline__ void lse_tile(f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t, char* smem,
                                          int tid) {
   const int tt = fresh(tid);
@@ -502,37 +517,51 @@ __device__ __forceinline__ void lse_tile(f32x16 (&acc)[S::FQ][S::FP], const Prod
   const int c0 = wq * S::WTQ + 4 * half;
   const bool whole = t.n >= S::BN;
   float2* part = reinterpret_cast<float2*>(smem);           // [row of the tile][wave column]
+  const SoftCap cap = soft_cap(a);
+  constexpr float scale = CAP ? 1.f : LOG2E;                // y = acc scale from here on
 #pragma unroll
   for (int i = 0; i < S::FP; ++i) {
     const int r = wp * S::WTP + 32 * i + (lane & 31);
     const int target = r < t.m ? target_of(a, t.i0 + r) - t.j0 : -1;
+    if constexpr (CAP) {
 #pragma unroll
-    for (int j = 0; j < S::FQ; ++j)
+      for (int j = 0; j < S::FQ; ++j)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int c = c0 + 32 * j + 8 * (v >> 2) + (v & 3);
-        const float z = soft_capped(acc[j][i][v], a.cap, a.inv_cap);
-        acc[j][i][v] = whole || c < t.n ? z : -INFINITY;
-      }
+        for (int v = 0; v < 16; ++v) {
+          const float l = acc[j][i][v];
+          acc[j][i][v] = capped_y<S::F32>(l, cap_r(l, cap), cap);
+          if (v % 8 == 7) __builtin_amdgcn_sched_barrier(0);     // few values at a time, or the chains spill
+        }
+    }
+    if (!whole) {
+#pragma unroll
+      for (int j = 0; j < S::FQ; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          if (c0 + 32 * j + 8 * (v >> 2) + (v & 3) >= t.n) acc[j][i][v] = -INFINITY;
+    }
     if (__any(target >= wq * S::WTQ && target < (wq + 1) * S::WTQ)) {
 #pragma unroll
       for (int j = 0; j < S::FQ; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v)
-          if (target == c0 + 32 * j + 8 * (v >> 2) + (v & 3)) a.logit[t.i0 + r] = acc[j][i][v];
+          if (target == c0 + 32 * j + 8 * (v >> 2) + (v & 3)) a.logit[t.i0 + r] = acc[j][i][v] * (CAP ? LN2 : 1.f);
     }
     float mx = -INFINITY;
 #pragma unroll
     for (int j = 0; j < S::FQ; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) mx = fmaxf(mx, acc[j][i][v]);
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    mx = fmaxf(mx, __shfl_xor(mx, 32)) * scale;
     const float base = mx == -INFINITY ? 0.f : mx;
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < S::FQ; ++j)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) sum += __expf(acc[j][i][v] - base);
+      for (int v = 0; v < 16; ++v) {
+        sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[j][i][v], scale, -base));
+        if (v % 8 == 7) __builtin_amdgcn_sched_barrier(0);
+      }
     sum += __shfl_xor(sum, 32);
     if (half == 0) part[r * S::WN + wq] = make_float2(mx, sum);
   }
@@ -544,30 +573,54 @@ __device__ __forceinline__ void lse_tile(f32x16 (&acc)[S::FQ][S::FP], const Prod
     const float base = m == -INFINITY ? 0.f : m;
     float sum = 0.f;
 #pragma unroll
-    for (int q = 0; q < S::WN; ++q) sum += part[r * S::WN + q].y * __expf(part[r * S::WN + q].x - base);
+    for (int q = 0; q < S::WN; ++q) sum += part[r * S::WN + q].y * __builtin_amdgcn_exp2f(part[r * S::WN + q].x - base);
     a.stats[int64_t(t.i0 + r) * a.stat_tiles + t.j0 / S::BN] = make_float2(m, sum);
   }
 }
 
-// The logits become the loss's gradient with respect to them.
-template <class S>
-__device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t, int tid) {
+// The logits become the loss's gradient with respect to them, but for the target's
+// column, which goes to `patch`.
+template <class S, bool CAP>
+__device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t, int tid,
+                                              Patch<S>& patch) {
   const int tt = fresh(tid);
   const int lane = tt & 63, w = tt >> 6, wq = w % S::WN, wp = w / S::WN;
   const int c0 = wq * S::WTQ + 4 * (lane >> 5);
+  const SoftCap cap = soft_cap(a);
 #pragma unroll
   for (int i = 0; i < S::FP; ++i) {
     const int r = min(wp * S::WTP + 32 * i + (lane & 31), t.m - 1) + t.i0;
     const int target = target_of(a, r) - t.j0;
-    const float lse = a.lse[r], ga = a.ga[r], gb = a.gb[r];
-    const bool here = __any(target >= wq * S::WTQ && target < (wq + 1) * S::WTQ);
+    const float lse = a.lse[r] * LOG2E, ga = a.ga[r];
+    const bool mine = target >= wq * S::WTQ && target < (wq + 1) * S::WTQ && ((target >> 2) & 1) == (lane >> 5);
+    patch.col[i] = mine ? target : -1;
+    patch.value[i] = 0.f;
+    if (__any(mine)) {
+      float l = 0.f;
+#pragma unroll
+      for (int j = 0; j < S::FQ; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) l = target == c0 + 32 * j + 8 * (v >> 2) + (v & 3) ? acc[j][i][v] : l;
+      if constexpr (CAP) {
+        const float q = cap_r(l, cap);
+        patch.value[i] = (ga * __builtin_amdgcn_exp2f(capped_y<S::F32>(l, q, cap) - lse) - a.gb[r]) * cap_slope(q);
+      } else {
+        patch.value[i] = ga * __builtin_amdgcn_exp2f(__builtin_fmaf(l, LOG2E, -lse)) - a.gb[r];
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < S::FQ; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const float z = soft_capped(acc[j][i][v], a.cap, a.inv_cap);
-        const int c = c0 + 32 * j + 8 * (v >> 2) + (v & 3);
-        acc[j][i][v] = logit_gradient(a, z, here ? c : -1, here ? target : -2, lse, ga, gb);
+        const float l = acc[j][i][v];
+        if constexpr (CAP) {
+          const float q = cap_r(l, cap);
+          acc[j][i][v] = ga * (cap_slope(q) * __builtin_amdgcn_exp2f(capped_y<S::F32>(l, q, cap) - lse));
+        } else {
+          acc[j][i][v] = ga * __builtin_amdgcn_exp2f(__builtin_fmaf(l, LOG2E, -lse));
+        }
+        if (v % 8 == 7) __builtin_amdgcn_sched_barrier(0);
       }
   }
 }
@@ -857,13 +910,15 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
       }
     }
 
-    if constexpr (EPI == EPI_LSE) {
-      lse_tile<S>(acc, a, t, smem, tid);
+    if constexpr (EPI == EPI_LSE || EPI == EPI_LSE_CAP) {
+      lse_tile<S, EPI == EPI_LSE_CAP>(acc, a, t, smem, tid);
+    } else if constexpr (EPI == EPI_DZ || EPI == EPI_DZ_CAP) {
+      Patch<S> patch;
+      gradient_tile<S, EPI == EPI_DZ_CAP>(acc, a, t, tid, patch);
+      store_tile<S, FORM, S::F32, S::F32>(acc, out_of<FORM>(a, t), false, t, smem, tid, &patch);
     } else {
-      if constexpr (EPI == EPI_DZ) gradient_tile<S>(acc, a, t, tid);
       const Out out = out_of<FORM>(a, t);
       if constexpr (S::F32) store_tile<S, FORM, true, true>(acc, out, a.add_f32, t, smem, tid);
-      else if constexpr (EPI == EPI_DZ) store_tile<S, FORM, false, false>(acc, out, false, t, smem, tid);
       else if (a.out_f32 || t.part >= 0) store_tile<S, FORM, true, true>(acc, out, a.add_f32, t, smem, tid);
       else if (a.add) store_tile<S, FORM, false, true>(acc, out, a.add_f32, t, smem, tid);
       else store_tile<S, FORM, false, false>(acc, out, false, t, smem, tid);

@@ -52,18 +52,22 @@ __global__ __launch_bounds__(TS * TS) void product_small_kernel(const ProductArg
         store1(a.out, base + row * a.ld_out + j, c, a.out_f32);
       }
     } else if constexpr (EPI == EPI_LSE) {
-      const float z = in ? soft_capped(c, a.cap, a.inv_cap) : -INFINITY;
-      float mx = z;
+      const SoftCap cap = soft_cap(a);
+      const float y = !in ? -INFINITY : a.cap != 0.f ? capped_y<true>(c, cap_r(c, cap), cap) : c * LOG2E;
+      float mx = y;
       for (int s = 1; s < TS; s *= 2) mx = fmaxf(mx, __shfl_xor(mx, s));
-      float sum = in ? __expf(z - (mx == -INFINITY ? 0.f : mx)) : 0.f;
+      float sum = in ? __builtin_amdgcn_exp2f(y - (mx == -INFINITY ? 0.f : mx)) : 0.f;
       for (int s = 1; s < TS; s *= 2) sum += __shfl_xor(sum, s);
       if (in) {
-        if (j == target_of(a, i)) a.logit[i] = z;
+        if (j == target_of(a, i)) a.logit[i] = a.cap != 0.f ? y * LN2 : c;
         if (tx == 0) a.stats[int64_t(i) * a.stat_tiles + jt] = make_float2(mx, sum);
       }
     } else if (in) {
-      const float z = soft_capped(c, a.cap, a.inv_cap);
-      const float d = logit_gradient(a, z, j, target_of(a, i), a.lse[i], a.ga[i], a.gb[i]);
+      const SoftCap cap = soft_cap(a);
+      const float r = cap_r(c, cap), y = a.cap != 0.f ? capped_y<true>(c, r, cap) : c * LOG2E;
+      float d = a.ga[i] * __builtin_amdgcn_exp2f(y - a.lse[i] * LOG2E);
+      if (j == target_of(a, i)) d -= a.gb[i];
+      if (a.cap != 0.f) d *= cap_slope(r);
       store1(a.out, int64_t(i) * a.ld_out + j, d, a.out_f32);
     }
   }
@@ -246,7 +250,8 @@ hipError_t launch_product(int form, int epi, const ProductArgs& args, int cus, c
   if (plan.shape != SHAPE_NAIVE) {
     a.chunk = plan.chunk;
     a.part = reinterpret_cast<float*>(ws);
-    hipError_t e = form == FORM_NT   ? launch_nt(plan.shape, epi, a, cus, stream)
+    const int kind = a.cap == 0.f ? epi : epi == EPI_LSE ? EPI_LSE_CAP : epi == EPI_DZ ? EPI_DZ_CAP : epi;
+    hipError_t e = form == FORM_NT   ? launch_nt(plan.shape, kind, a, cus, stream)
                    : form == FORM_NN ? launch_nn(plan.shape, a, cus, stream) : launch_tn(plan.shape, a, cus, stream);
     if (e == hipSuccess && plan.bytes)
       e = form == FORM_TN ? launch_sum<FORM_TN>(a, cus, stream) : launch_sum<FORM_NT>(a, cus, stream);

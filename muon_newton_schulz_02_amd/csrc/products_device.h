@@ -76,24 +76,29 @@ __device__ __forceinline__ int target_of(const ProductArgs& a, int i) {
   return t >= 0 && t < a.n ? int(t) : -1;
 }
 
-// z of a logit: cap tanh(l / cap), or l.  tanh u = 1 - 2 / (1 + e^2u) is off by
-// 2^-24 or two, absolute, and e^2u = inf gives 1.
-__device__ __forceinline__ float soft_capped(float l, float cap, float inv_cap) {
-  if (cap == 0.f) return l;
-  return cap * (1.f - 2.f / (1.f + __expf(2.f * (l * inv_cap))));
-}
+// Softmax in base 2: exponents are y = z log2 e, so that an exponential is one fma and
+// one v_exp_f32.  With a soft cap z = cap tanh(l / cap) = cap (1 - 2 r), r = 1 / (1 +
+// e^(2 l / cap)), whose slope in l is 4 r (1 - r).
+constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
+struct SoftCap {
+  float k;          // 2 log2 e / cap
+  float c2;         // cap log2 e
+};
+__device__ __forceinline__ SoftCap soft_cap(const ProductArgs& a) { return {2.f * LOG2E * a.inv_cap, a.cap * LOG2E}; }
 
-// Gradient with respect to the logit of column `col`: g_a p - g_b [col = target],
-// times the soft cap's slope 1 - (z / cap)^2.
-__device__ __forceinline__ float logit_gradient(const ProductArgs& a, float z, int col, int target, float lse,
-                                                float ga, float gb) {
-  float d = ga * __expf(z - lse);
-  if (col == target) d -= gb;
-  if (a.cap != 0.f) {
-    const float t = z * a.inv_cap;
-    d *= 1.f - t * t;
-  }
-  return d;
+__device__ __forceinline__ float cap_r(float l, const SoftCap& c) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l * c.k));     // e^.. = inf: 0
+}
+__device__ __forceinline__ float cap_slope(float r) { return 4.f * __builtin_fmaf(-r, r, r); }
+// cap (1 - 2 r) log2 e.  r is off by 2^-24, which EXACT (binary32 operands) avoids below
+// |u| = 0.3 with tanh's own series (its next term is 5e-8 there).
+template <bool EXACT>
+__device__ __forceinline__ float capped_y(float l, float r, const SoftCap& c) {
+  const float y = __builtin_fmaf(-2.f * c.c2, r, c.c2);
+  if constexpr (!EXACT) return y;
+  const float u = l * (c.k * (LN2 / 2.f)), s = u * u;
+  const float p = 1.f + s * (-0.333333343f + s * (0.133333340f + s * (-0.0539682545f + s * 0.0218694881f)));
+  return fabsf(u) < 0.3f ? c.c2 * (u * p) : y;
 }
 
 }  // namespace muon

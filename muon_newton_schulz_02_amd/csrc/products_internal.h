@@ -20,7 +20,8 @@ enum ProductForm : int { FORM_NT = 0, FORM_NN = 1, FORM_TN = 2 };
 //   LSE    a maximum and a sum of exponentials for every row and tile of columns,
 //          and the target's logit
 //   DZ     the gradient of the loss with respect to the logits C
-enum ProductEpilogue : int { EPI_STORE = 0, EPI_LSE = 1, EPI_DZ = 2 };
+// (_CAP: with a soft cap; launch_product chooses.)
+enum ProductEpilogue : int { EPI_STORE = 0, EPI_LSE = 1, EPI_DZ = 2, EPI_LSE_CAP = 3, EPI_DZ_CAP = 4 };
 
 // One launch.  Groups (experts) split the rows of P and C for NT and NN, and k
 // for TN: group g has rows [offsets[g], offsets[g + 1]) of P (TN: of P and Q),
@@ -52,7 +53,7 @@ struct ProductArgs {
   const float* ga;             // grad_loss + grad_lse
   const float* gb;             // grad_loss
   float* logit;                // the target's logit (soft-capped)
-  float2* stats;               // [row][tile]: maximum, sum of exp(z - maximum)
+  float2* stats;               // [row][tile], with y = z log2 e: maximum of y, sum of 2^(y - maximum)
 };
 
 // Tile shapes.
