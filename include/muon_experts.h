@@ -30,8 +30,9 @@
  *   - bfloat16 tensors are multiplied on the bfloat16 matrix cores (products
  *     exact), binary32 ones to binary32 accuracy; sums are binary32, and
  *     results are rounded once.
- *   - NaN and infinities stay in the rows (grad_W: in the expert) that hold them,
- *     as the formulas have it.
+ *   - A NaN or an infinity reaches the results whose sums it takes part in (the
+ *     row, or the expert's grad_W) and no others.  They are NaN or infinite, as the
+ *     formulas have it; with binary32 tensors also NaN where the formula is infinite.
  *   - The same call gives the same bits every time, captured or not.
  *   - Workspace: with workspace = NULL the library keeps one per device (grown
  *     on demand, freed by muon_release_workspace), and calls of this header and

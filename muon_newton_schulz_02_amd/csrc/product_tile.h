@@ -43,39 +43,43 @@ typedef u32x4 u32x4_any __attribute__((aligned(2)));   // 16 bytes at any elemen
 typedef __attribute__((address_space(1))) const char gchar;
 typedef __attribute__((address_space(3))) char lchar;
 typedef __attribute__((address_space(3))) u32x4 lu32x4;
+typedef __attribute__((address_space(3))) u32x2 lu32x2;
 typedef __attribute__((address_space(1))) const u32x4_any gload16;
 typedef __attribute__((address_space(1))) u32x4_any gstore16;
 
 constexpr int NUM_XCD = 8;
 constexpr int KB = 128;     // bytes of k per stage
-constexpr int PITCH = 144;  // LDS pitch of an operand row in row form
 
 // This wave's LDS accesses complete, then s_barrier: unlike __syncthreads it does
 // not wait for global loads and stores in flight.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// Tile shapes: BM x BN over WM x WN waves.
+// Tile shapes: BM x BN over WM x WN waves.  Binary32 operands become three bfloat16
+// parts on their way to LDS, x = hi + mid + lo with 8 bits each (exact), and a product
+// is six on the bfloat16 matrix cores: hi hi, hi mid, mid hi, mid mid, hi lo, lo hi; the
+// three left out are 2^-24 of it and less.  The binary32 matrix instructions do 1 / 16
+// of the bfloat16 ones' work a cycle, so six of these are 2.7 times as fast.
 template <int BM_, int BN_, int WM_, int WN_, bool F32_>
 struct Shape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NT = WM_ * WN_ * 64;
   static constexpr bool F32 = F32_;
-  static constexpr int ESZ = F32 ? 4 : 2, KE = KB / ESZ, KS = F32 ? 8 : 16;
+  static constexpr int ESZ = F32 ? 4 : 2, KE = KB / ESZ, PARTS = F32 ? 3 : 1, SLABS = KE / 16;
   static constexpr int WTP = BM / WM, WTQ = BN / WN, FP = WTP / 32, FQ = WTQ / 32;
   static constexpr int CP = BM * 8 / NT, CQ = BN * 8 / NT;   // 16-byte chunks of a stage per thread
   static_assert(CP >= 1 && CQ >= 1 && BM * 8 % NT == 0 && BN * 8 % NT == 0, "whole chunks per thread");
 };
 
-// LDS of an operand of R rows.  Row form: row r at r PITCH (a fragment read of 32
-// rows then meets every bank evenly).  k-row form: k-row k at k * pitch; bfloat16
-// fragments come from ds_read_b64_tr_b16, whose half-wave reads 4 k-rows x 64 bytes,
-// on distinct banks where the pitch is 64 or 192 modulo 256; binary32 ones from
-// 4-byte reads, whose halves are 4 k-rows apart, on distinct banks where four
-// pitches are 128 modulo 256.
+// LDS of an operand of R rows, bfloat16, part after part.  Row form: row r at r pitch,
+// 16 bytes more than its k, so that a fragment read of 32 rows meets every bank evenly
+// (144 and 80 bytes).  k-row form: k-row k at k * pitch; fragments come from
+// ds_read_b64_tr_b16, whose half-wave reads 4 k-rows x 64 bytes, on distinct banks
+// where the pitch is 64 or 192 modulo 256.
 template <class S, int R, bool KROW>
 struct Lds {
-  static constexpr int pitch = !KROW ? PITCH : S::F32 ? R * 4 + 32 : (R * 2 % 256 == 0 || R * 2 % 256 == 128) ? R * 2 + 64 : R * 2;
-  static_assert(!KROW || S::F32 || pitch % 256 == 64 || pitch % 256 == 192, "banks");
-  static constexpr int bytes = KROW ? S::KE * pitch : R * PITCH;
+  static constexpr int pitch = !KROW ? S::KE * 2 + 16 : (R * 2 % 256 == 0 || R * 2 % 256 == 128) ? R * 2 + 64 : R * 2;
+  static_assert(!KROW || pitch % 256 == 64 || pitch % 256 == 192, "banks");
+  static constexpr int part = KROW ? S::KE * pitch : R * pitch;
+  static constexpr int bytes = S::PARTS * part;
 };
 
 template <class S, int FORM>
@@ -250,7 +254,7 @@ template <class S, int R, bool KROW>
 __device__ __forceinline__ int chunk_lds(int tid) {
   int row, byte;
   chunk_at<S, R, KROW>(tid, row, byte);
-  return row * Lds<S, R, KROW>::pitch + byte;
+  return row * Lds<S, R, KROW>::pitch + byte * 2 / S::ESZ;
 }
 template <class S, int R, bool KROW>
 constexpr int chunk_step() {
@@ -259,14 +263,40 @@ constexpr int chunk_step() {
   return S::NT / PER * Lds<S, R, KROW>::pitch;
 }
 
+// Four binary32 values as three times four bfloat16: the upper half of the bits, of what
+// is left, and of what is left then.  Infinities and NaN have NaN parts.
+__device__ __forceinline__ void split4(const u32x4& x, u32x2 (&out)[3]) {
+  float v[4], mid[4], lo[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(x[e]);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) mid[e] = v[e] - __uint_as_float(x[e] & 0xFFFF0000u);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) lo[e] = mid[e] - __uint_as_float(__float_as_uint(mid[e]) & 0xFFFF0000u);
+  auto pack = [](uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); };
+  out[0] = u32x2{pack(x[0], x[1]), pack(x[2], x[3])};
+  out[1] = u32x2{pack(__float_as_uint(mid[0]), __float_as_uint(mid[1])), pack(__float_as_uint(mid[2]), __float_as_uint(mid[3]))};
+  out[2] = u32x2{pack(__float_as_uint(lo[0]), __float_as_uint(lo[1])), pack(__float_as_uint(lo[2]), __float_as_uint(lo[3]))};
+}
+
+template <class S, int R, bool KROW>
+__device__ __forceinline__ void store_chunk(const u32x4& v, lchar* dst) {
+  if constexpr (!S::F32) {
+    *reinterpret_cast<lu32x4*>(dst) = v;
+  } else {
+    u32x2 p[3];
+    split4(v, p);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) *reinterpret_cast<lu32x2*>(dst + i * Lds<S, R, KROW>::part) = p[i];
+  }
+}
+
 // Chunks I0 .. I1 - 1 of a stage to LDS; `dst`: this thread's chunk 0.
 template <class S, int R, bool KROW, int C>
 __device__ __forceinline__ void store_chunks(const u32x4 (&r)[C], lchar* dst, int i0, int i1) {
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    if (i < i0 || i >= i1) continue;
-    *reinterpret_cast<lu32x4*>(dst + i * chunk_step<S, R, KROW>()) = r[i];
-  }
+  for (int i = 0; i < C; ++i)
+    if (i >= i0 && i < i1) store_chunk<S, R, KROW>(r[i], dst + i * chunk_step<S, R, KROW>());
 }
 
 // The same for the last stage: what last_loads moved back is moved forward again,
@@ -284,7 +314,7 @@ __device__ __forceinline__ void store_last(const u32x4 (&r)[C], const Source& s,
     const bool in = last_chunk<S, R, KROW>(s, z, tid + S::NT * i, kt, k, off, row, byte);
     u32x4 v = shift_down(r[i], in ? (off > z.most ? int(off - z.most) : 0) : 16);
     if constexpr (!KROW) v = keep_first(v, k * S::ESZ - (kt * KB + byte));
-    *reinterpret_cast<lu32x4*>(dst + i * chunk_step<S, R, KROW>()) = v;
+    store_chunk<S, R, KROW>(v, dst + i * chunk_step<S, R, KROW>());
   }
 }
 
@@ -296,48 +326,36 @@ template <class S, int R, bool KROW>
 __device__ __forceinline__ int frag_lds(int w0, int lane) {
   using L = Lds<S, R, KROW>;
   const int half = lane >> 5;
-  if constexpr (!KROW) return (w0 + (lane & 31)) * PITCH + half * 16;
+  if constexpr (!KROW) return (w0 + (lane & 31)) * L::pitch + half * 16;
   // lane 4 e + m of each 16-lane group points at k-row e, columns 4 m .. 4 m + 3 of
   // its 16; lane j of the group receives k-rows 0 .. 3 of column j
-  else if constexpr (!S::F32) return (8 * half + ((lane & 15) >> 2)) * L::pitch + 2 * (w0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3));
-  else return 4 * half * L::pitch + 4 * (w0 + (lane & 31));
+  else return (8 * half + ((lane & 15) >> 2)) * L::pitch + 2 * (w0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3));
 }
 
-// F fragments of 32 rows, one k-slab ks; `p`: this lane's place.
+// F fragments of 32 rows of every part, one k-slab ks; `p`: this lane's place.
 template <class S, int R, bool KROW, int F>
 __device__ __forceinline__ void read_frags(u32x4* f, lchar* p, int ks) {
   using L = Lds<S, R, KROW>;
-  if constexpr (!KROW) {
 #pragma unroll
-    for (int x = 0; x < F; ++x) f[x] = *reinterpret_cast<const lu32x4*>(p + ks * 32 + x * 32 * PITCH);
-  } else if constexpr (!S::F32) {
-    typedef short s16x4 __attribute__((ext_vector_type(4)));
-    typedef __attribute__((address_space(3))) s16x4 ls16x4;
-    lchar* q = p + ks * 16 * L::pitch;
+  for (int part = 0; part < S::PARTS; ++part) {
+    lchar* q = p + part * L::part + ks * (KROW ? 16 * L::pitch : 32);
 #pragma unroll
     for (int x = 0; x < F; ++x) {
-      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4*)(q + x * 64)));
-      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4*)(q + x * 64 + 4 * L::pitch)));
-      f[x] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+      if constexpr (!KROW) {
+        f[part * F + x] = *reinterpret_cast<const lu32x4*>(q + x * 32 * L::pitch);
+      } else {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4 ls16x4;
+        const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4*)(q + x * 64)));
+        const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4*)(q + x * 64 + 4 * L::pitch)));
+        f[part * F + x] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+      }
     }
-  } else {
-    typedef __attribute__((address_space(3))) const uint32_t lu32;
-#pragma unroll
-    for (int x = 0; x < F; ++x)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f[x][e] = *reinterpret_cast<lu32*>(p + (ks * 8 + e) * L::pitch + x * 128);
   }
 }
 
-template <bool F32>
 __device__ __forceinline__ void mfma(f32x16& acc, const u32x4& q, const u32x4& p) {
-  if constexpr (!F32) {
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, q), __builtin_bit_cast(bf16x8, p), acc, 0, 0, 0);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(q[e]), __uint_as_float(p[e]), acc, 0, 0, 0);
-  }
+  acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, q), __builtin_bit_cast(bf16x8, p), acc, 0, 0, 0);
 }
 
 // ------------------------------------------------------------------ epilogues
@@ -788,19 +806,23 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
     if (nk == 0) {
       load_next();
     } else {
-      u32x4 F[2][S::FQ + S::FP];
+      u32x4 F[2][S::PARTS * (S::FQ + S::FP)];
       constexpr int HP = (S::CP + 1) / 2, HQ = (S::CQ + 1) / 2, HF = (S::FP + 1) / 2;
       auto frags = [&](u32x4* f, auto buf_c, int ks) {
         constexpr int BUF = decltype(buf_c)::value;
         read_frags<S, S::BN, QK, S::FQ>(f, frag_q + BUF * LY::LQ::bytes, ks);
-        read_frags<S, S::BM, PK, S::FP>(f + S::FQ, frag_p + BUF * LY::LP::bytes, ks);
+        read_frags<S, S::BM, PK, S::FP>(f + S::PARTS * S::FQ, frag_p + BUF * LY::LP::bytes, ks);
       };
       auto multiply = [&](const u32x4* f, int h) {
+        // parts of Q and P, the small products first
+        constexpr int QPART[6] = {0, 2, 1, 0, 1, 0}, PPART[6] = {2, 0, 1, 1, 0, 0};
 #pragma unroll
-        for (int j = 0; j < S::FQ; ++j)
+        for (int x = S::F32 ? 0 : 5; x < 6; ++x)
 #pragma unroll
-          for (int i = 0; i < S::FP; ++i)
-            if (i / HF == h) mfma<S::F32>(acc[j][i], f[j], f[S::FQ + i]);
+          for (int j = 0; j < S::FQ; ++j)
+#pragma unroll
+            for (int i = 0; i < S::FP; ++i)
+              if (i / HF == h) mfma(acc[j][i], f[QPART[x] * S::FQ + j], f[S::PARTS * S::FQ + PPART[x] * S::FP + i]);
       };
       // half h of an operand's chunks of stage g to buffer BUF; LAST: g is the last stage
       auto put_p = [&](auto buf_c, auto last_c, int g, int h) {
@@ -824,6 +846,38 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
         using CUR = std::integral_constant<int, BUF>;
         using NXT = std::integral_constant<int, BUF ^ 1>;
         using LAST = std::integral_constant<bool, MODE == 1>;
+        if constexpr (S::SLABS == 2) {
+          frags(F[1], CUR{}, 1);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(F[0], 0);
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (MODE != 2) {
+            put_p(NXT{}, LAST{}, kt + 1, 0);
+            put_p(NXT{}, LAST{}, kt + 1, 1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(F[0], 1);
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (MODE == 0) {
+            address(kt + 2);
+            load_chunks(rp, lp);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (MODE != 2) {
+            put_q(NXT{}, LAST{}, kt + 1, 0);
+            put_q(NXT{}, LAST{}, kt + 1, 1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (MODE == 0) load_chunks(rq, lq);
+          if constexpr (MODE == 1) load_next();
+          lds_barrier();
+          if constexpr (MODE != 2) frags(F[0], NXT{}, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(F[1], 0);
+          multiply(F[1], 1);
+          __builtin_amdgcn_sched_barrier(0);
+          return;
+        }
         frags(F[1], CUR{}, 1);
         __builtin_amdgcn_sched_barrier(0);
         multiply(F[0], 0);
@@ -955,7 +1009,7 @@ using Large = Shape<256, 256, 2, 4, false>;
 using Medium = Shape<128, 128, 2, 2, false>;
 using MediumTn = Shape<128, 256, 2, 4, false>;
 using Small = Shape<32, 128, 1, 4, false>;
-using MediumF32 = Shape<128, 128, 2, 2, true>;
+using MediumF32 = Shape<128, 128, 2, 4, true>;
 using SmallF32 = Shape<32, 128, 1, 4, true>;
 
 }  // namespace
