@@ -87,7 +87,8 @@ struct Layout {
   static constexpr bool PK = FORM == FORM_TN, QK = FORM != FORM_NT;   // k-row form
   using LP = Lds<S, S::BM, PK>;
   using LQ = Lds<S, S::BN, QK>;
-  static constexpr int P0 = 0, Q0 = 2 * LP::bytes, BYTES = 2 * LP::bytes + 2 * LQ::bytes;
+  // buffer b: P at b BUF, Q behind it
+  static constexpr int BUF = LP::bytes + LQ::bytes, BYTES = 2 * BUF;
 };
 
 // ------------------------------------------------------------------ tiles
@@ -117,7 +118,9 @@ __device__ __forceinline__ Source source_of(const ProductArgs& a, const Tile& t)
   Source s;
   // formed where it is used, from values the compiler takes for new ones: kept
   // through the k-loop the sources of two tiles would not fit the scalar registers
-  int lo = t.lo, i0 = t.i0, j0 = t.j0, grp = t.g, k0 = t.k0;
+  int lo = __builtin_amdgcn_readfirstlane(t.lo), i0 = __builtin_amdgcn_readfirstlane(t.i0),
+      j0 = __builtin_amdgcn_readfirstlane(t.j0), grp = __builtin_amdgcn_readfirstlane(t.g),
+      k0 = __builtin_amdgcn_readfirstlane(t.k0);
   asm volatile("" : "+s"(lo), "+s"(i0), "+s"(j0), "+s"(grp), "+s"(k0));
   if constexpr (OPD == 0) {
     s.begin = reinterpret_cast<const char*>(a.p);
@@ -135,6 +138,13 @@ __device__ __forceinline__ Source source_of(const ProductArgs& a, const Tile& t)
                                : s.begin + (int64_t(lo) + k0) * s.ld + j0 * E;
   }
   return s;
+}
+
+// The address in scalar registers.
+__device__ __forceinline__ const char* uniform(const char* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(v)), hi = __builtin_amdgcn_readfirstlane(uint32_t(v >> 32));
+  return reinterpret_cast<const char*>(lo | (uint64_t(hi) << 32));
 }
 
 // This thread's loads of an operand: `at` advances from stage to stage, the
@@ -165,7 +175,7 @@ __device__ __forceinline__ int fresh(int tid) {
 
 template <class S, int R, bool KROW, int C>
 __device__ __forceinline__ void first_loads(Loads<C>& l, const Source& s, int tid) {
-  l.at = s.base;
+  l.at = uniform(s.base);
   tid = fresh(tid);
 #pragma unroll
   for (int i = 0; i < C; ++i) {
@@ -208,11 +218,24 @@ __device__ __forceinline__ bool last_chunk(const Source& s, const Last& l, int c
   }
 }
 
-template <class S, int R, bool KROW, int C>
+// The last stage's loads.  WHOLE: every chunk of the product's operands lies inside its
+// row or behind the end of k; one behind it reads the first of its row (k-row) instead.
+template <class S, int R, bool KROW, bool WHOLE, int C>
 __device__ __forceinline__ void last_loads(Loads<C>& l, const Source& s, int kt, int k, int tid) {
-  const Last z = last_of<S, KROW>(s, kt);
-  l.at = z.at;
   tid = fresh(tid);
+  if constexpr (WHOLE) {
+    l.at = uniform(s.base + int64_t(kt) * (KROW ? int64_t(S::KE) * s.ld : int64_t(KB)));
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      int row, byte;
+      chunk_at<S, R, KROW>(tid + S::NT * i, row, byte);
+      if constexpr (KROW) l.off[i] = (kt * S::KE + row < k ? row * s.ld : 0u) + (byte < s.valid * S::ESZ ? byte : 0);
+      else l.off[i] = min(row, s.valid - 1) * s.ld + (kt * KB + byte < k * S::ESZ ? byte : 0);
+    }
+    return;
+  }
+  const Last z = last_of<S, KROW>(s, kt);
+  l.at = uniform(z.at);
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     int row, byte;
@@ -226,7 +249,11 @@ template <int C>
 __device__ __forceinline__ void load_chunks(u32x4 (&r)[C], const Loads<C>& l) {
   gchar* at = (gchar*)l.at;
 #pragma unroll
-  for (int i = 0; i < C; ++i) r[i] = *reinterpret_cast<gload16*>(at + l.off[i]);
+  for (int i = 0; i < C; ++i) {
+    uint32_t off = l.off[i];
+    asm volatile("" : "+v"(off));      // 32 bits up to here: the instruction adds them to a scalar base
+    r[i] = *reinterpret_cast<gload16*>(at + off);
+  }
 }
 
 // bytes [s, 16) of v, zeros behind; s in [0, 16]
@@ -301,11 +328,25 @@ __device__ __forceinline__ void store_chunks(const u32x4 (&r)[C], lchar* dst, in
 
 // The same for the last stage: what last_loads moved back is moved forward again,
 // and what lies past the end of k becomes zero.
-template <class S, int R, bool KROW, int C>
+template <class S, int R, bool KROW, bool WHOLE, int C>
 __device__ __forceinline__ void store_last(const u32x4 (&r)[C], const Source& s, int kt, int k, lchar* dst, int tid,
                                            int i0, int i1) {
-  const Last z = last_of<S, KROW>(s, kt);
   tid = fresh(tid);
+  if constexpr (WHOLE) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      if (i < i0 || i >= i1) continue;
+      int row, byte;
+      chunk_at<S, R, KROW>(tid + S::NT * i, row, byte);
+      const bool in = KROW ? kt * S::KE + row < k : kt * KB + byte < k * S::ESZ;
+      u32x4 v = r[i];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) v[d] = in ? v[d] : 0u;
+      store_chunk<S, R, KROW>(v, dst + i * chunk_step<S, R, KROW>());
+    }
+    return;
+  }
+  const Last z = last_of<S, KROW>(s, kt);
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     if (i < i0 || i >= i1) continue;
@@ -451,58 +492,77 @@ struct Patch {
   float value[S::FP];
 };
 
-// C to `out`.  OF32: out is binary32.  WIDE: staged in LDS as binary32 (for binary32
-// outputs and addends), a part of the tile's rows at a time where all do not fit;
-// else as bfloat16.
-template <class S, int FORM, bool OF32, bool WIDE>
-__device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], const Out& out, bool add_f32,
-                                           const Tile& t, char* smem, int tid, const Patch<S>* patch = nullptr) {
+// C to `out` through LDS, a part of the tile's rows at a time where all do not fit ROOM
+// bytes.  OF32: out is binary32.  WIDE: staged as binary32 (for binary32 outputs and
+// addends), else as bfloat16.
+template <class S, bool OF32, bool WIDE, int ROOM>
+__device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], const Out& out, bool add_f32, const Tile& t, char* stg, int tid,
+                                           const Patch<S>* patch = nullptr) {
   constexpr int ES = WIDE ? 4 : 2, EP = S::BN * ES + 16;
-  constexpr int LDS = Layout<S, FORM>::BYTES;
-  constexpr int PASSES = S::BM * EP <= LDS ? 1 : S::BM / 2 * EP <= LDS ? 2 : 4;
+  constexpr int PASSES = S::BM * EP <= ROOM ? 1 : S::BM / 2 * EP <= ROOM ? 2 : S::BM / 4 * EP <= ROOM ? 4 : 8;
   constexpr int ROWS = S::BM / PASSES;
-  static_assert(ROWS * EP <= LDS && S::WTP % 32 == 0, "staging fits");
+  static_assert(ROWS * EP <= ROOM && ROWS % 32 == 0, "staging fits");
   const int tt = fresh(tid);
-  const int lane = tt & 63, half = lane >> 5, w = tt >> 6, wq = w % S::WN, wp = w / S::WN;
+  const int lane = tt & 63, half = lane >> 5, w = __builtin_amdgcn_readfirstlane(tt >> 6), wq = w % S::WN, wp = w / S::WN;
+  constexpr int N = OF32 ? 4 : 8, CPR = S::BN / N;        // elements of a run, runs of a row
+  constexpr int ITER = ROWS * CPR / S::NT, STEP = S::NT / CPR;
+  static_assert(ITER * STEP == ROWS, "whole rows a step");
+  const int row0 = tt / CPR, col = tt % CPR * N;
+  // whole rows of the tile that lie evenly spaced: 32-bit offsets, no questions
+  const bool plain = t.n >= S::BN && !out.map && !(WIDE && (out.add || !OF32));
+  const uint32_t ld = uint32_t(out.ld * (OF32 ? 4 : 2));
 #pragma unroll 1
   for (int pass = 0; pass < PASSES; ++pass) {
     if (pass > 0) lds_barrier();
+    char* const lane_at = stg + (lane & 31) * EP + (wq * S::WTQ + 4 * half) * ES;
 #pragma unroll
     for (int i = 0; i < S::FP; ++i) {
-      const int r = wp * S::WTP + 32 * i + (lane & 31) - pass * ROWS;
-      if (PASSES == 1 || (r >= 0 && r < ROWS)) {
+      const int r0 = wp * S::WTP + 32 * i - pass * ROWS;
+      if (PASSES == 1 || (r0 >= 0 && r0 < ROWS)) {
+        char* const at = lane_at + r0 * EP;
 #pragma unroll
         for (int j = 0; j < S::FQ; ++j)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
+            char* d = at + (32 * j + 8 * g) * ES;
             const f32x16& c = acc[j][i];
-            char* d = smem + r * EP + (wq * S::WTQ + 32 * j + 8 * g + 4 * half) * ES;
             if constexpr (WIDE) *reinterpret_cast<f32x4*>(d) = f32x4{c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
             else *reinterpret_cast<u32x2*>(d) = u32x2{float2_to_bf16x2_bits(c[4 * g], c[4 * g + 1]),
                                                       float2_to_bf16x2_bits(c[4 * g + 2], c[4 * g + 3])};
+            if (g == 3) __builtin_amdgcn_sched_barrier(0);   // else all are rounded before any is stored
           }
         // after this lane's own write of the column, in order
         if (patch && patch->col[i] >= 0) {
-          char* d = smem + r * EP + patch->col[i] * ES;
+          char* d = stg + (r0 + (lane & 31)) * EP + patch->col[i] * ES;
           if constexpr (WIDE) *reinterpret_cast<float*>(d) = patch->value[i];
           else *reinterpret_cast<uint16_t*>(d) = float_to_bf16_bits(patch->value[i]);
         }
       }
     }
     lds_barrier();
-    constexpr int N = OF32 ? 4 : 8, CPR = S::BN / N;      // elements of a run, runs of a row
     const int rows = min(ROWS, t.m - pass * ROWS);
-    constexpr int ITER = ROWS * CPR / S::NT > 0 ? ROWS * CPR / S::NT : 1;
+    const char* src = stg + row0 * EP + col * ES;
+    if (plain) {
+      auto to = (__attribute__((address_space(1))) char*)(out.at + int64_t(pass) * ROWS * ld);
+      uint32_t off = row0 * ld + col * (OF32 ? 4 : 2);
 #pragma unroll 4
-    for (int k = 0; k < ITER; ++k) {
-      const int q = tt + k * S::NT;
-      const int r = q / CPR, c = q % CPR * N;
-      const int cnt = min(N, t.n - c);
-      if (r >= rows || cnt <= 0) continue;
+      for (int k = 0; k < ITER; ++k) {
+        if (row0 + k * STEP < rows) {
+          const u32x4 v = *reinterpret_cast<const u32x4*>(src + k * STEP * EP);
+          *reinterpret_cast<gstore16*>(to + off) = v;
+        }
+        off += STEP * ld;
+      }
+      continue;
+    }
+    const int cnt = min(N, t.n - col);
+    if (cnt <= 0) continue;
+#pragma unroll 1
+    for (int r = row0; r < rows; r += STEP, src += STEP * EP) {
       const int row = pass * ROWS + r;
-      const int64_t at = (out.map ? out.map[row] : row) * out.ld + c;
+      const int64_t at = int64_t(out.map ? out.map[row] : row) * out.ld + col;
       if constexpr (!WIDE) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(smem + r * EP + c * 2);
+        const u32x4 v = *reinterpret_cast<const u32x4*>(src);
         uint16_t* o = reinterpret_cast<uint16_t*>(out.at) + at;
         if (cnt == N) {
           *reinterpret_cast<gstore16*>((__attribute__((address_space(1))) char*)o) = v;
@@ -515,11 +575,11 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], co
         float v[N];
 #pragma unroll
         for (int h = 0; h < N / 4; ++h) {
-          const f32x4 x = *reinterpret_cast<const f32x4*>(smem + r * EP + (c + 4 * h) * 4);
+          const f32x4 x = *reinterpret_cast<const f32x4*>(src + 16 * h);
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[4 * h + e] = x[e];
         }
-        store_run<OF32>(out, add_f32, v, at, row * out.ld_add + c, cnt);
+        store_run<OF32>(out, add_f32, v, at, row * out.ld_add + col, cnt);
       }
     }
   }
@@ -685,7 +745,7 @@ __device__ __forceinline__ Tile tile_at(const ProductArgs& a, const int* pre, in
   group_range(a, r.g, first, end);
   first = __builtin_amdgcn_readfirstlane(first);
   end = __builtin_amdgcn_readfirstlane(end);
-  r.lo = first;
+  r.lo = first < end ? first : 0;      // nothing is read of a group without rows but zeros' addresses
   r.n = a.n - r.j0;
   const int k = FORM == FORM_TN ? end - first : a.k;
   r.m = FORM == FORM_TN ? a.m - r.i0 : end - first - r.i0;
@@ -696,7 +756,7 @@ __device__ __forceinline__ Tile tile_at(const ProductArgs& a, const int* pre, in
   return r;
 }
 
-template <class S, int FORM, int EPI>
+template <class S, int FORM, int EPI, bool WHOLE>
 __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
   using LY = Layout<S, FORM>;
   constexpr bool PK = LY::PK, QK = LY::QK;
@@ -713,7 +773,7 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
   __shared__ int wave_sum[S::NT / 64];
   int tile, step, end, chunk = a.chunk;
   if constexpr (FORM == FORM_TN) {
-    chunk = safe_chunk<S::NT>(a, pre, wave_sum, tid);
+    chunk = __builtin_amdgcn_readfirstlane(safe_chunk<S::NT>(a, pre, wave_sum, tid));
     group_sums<S::NT>(a.groups, pre, wave_sum, tid, [&](int g) {
       int lo, hi;
       group_range(a, g, lo, hi);
@@ -739,35 +799,76 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
 
   // One register for each operand's stores and fragment reads; everything else is an
   // immediate (opaque, or the compiler keeps one register for each sum)
-  lchar* put_at_p = (lchar*)smem + LY::P0 + chunk_lds<S, S::BM, PK>(tid);
-  lchar* put_at_q = (lchar*)smem + LY::Q0 + chunk_lds<S, S::BN, QK>(tid);
-  lchar* frag_p = (lchar*)smem + LY::P0 + frag_lds<S, S::BM, PK>(wp * S::WTP, lane);
-  lchar* frag_q = (lchar*)smem + LY::Q0 + frag_lds<S, S::BN, QK>(wq * S::WTQ, lane);
+  lchar* put_at_p = (lchar*)smem + chunk_lds<S, S::BM, PK>(tid);
+  lchar* put_at_q = (lchar*)smem + LY::LP::bytes + chunk_lds<S, S::BN, QK>(tid);
+  lchar* frag_p = (lchar*)smem + frag_lds<S, S::BM, PK>(wp * S::WTP, lane);
+  lchar* frag_q = (lchar*)smem + LY::LP::bytes + frag_lds<S, S::BN, QK>(wq * S::WTQ, lane);
   asm volatile("" : "+v"(put_at_p), "+v"(put_at_q), "+v"(frag_p), "+v"(frag_q));
+  int turn = LY::BUF;       // to the other buffer
   u32x4 rp[S::CP], rq[S::CQ];
   Loads<S::CP> lp;
   Loads<S::CQ> lq;
   // bytes from one stage of an operand in k-row form to the next (64 k-rows of 2^22
   // bytes, or 32 of 2^23: 2^28 at most)
   const uint32_t step_p = uint32_t(S::KE * a.ld_p * S::ESZ), step_q = uint32_t(S::KE * a.ld_q * S::ESZ);
-  auto stages = [](const Tile& t) { return (t.k + S::KE - 1) / S::KE; };
-  // the addresses of the first stage of a tile
-  auto begin_tile = [&](const Tile& t) {
-    const Source sp = source_of<S, FORM, 0>(a, t), sq = source_of<S, FORM, 1>(a, t);
-    if (stages(t) > 1) {
+  // (a group without rows has one of zeros)
+  auto stages = [](const Tile& t) { return max(1, (t.k + S::KE - 1) / S::KE); };
+  // the first stage of a tile, into registers
+  auto load_first = [&](const Tile& u) {
+    const Source sp = source_of<S, FORM, 0>(a, u), sq = source_of<S, FORM, 1>(a, u);
+    if (stages(u) > 1) {
       first_loads<S, S::BM, PK>(lp, sp, tid);
       first_loads<S, S::BN, QK>(lq, sq, tid);
     } else {
-      last_loads<S, S::BM, PK>(lp, sp, 0, t.k, tid);
-      last_loads<S, S::BN, QK>(lq, sq, 0, t.k, tid);
+      last_loads<S, S::BM, PK, WHOLE>(lp, sp, 0, u.k, tid);
+      last_loads<S, S::BN, QK, WHOLE>(lq, sq, 0, u.k, tid);
+    }
+    load_chunks(rp, lp);
+    load_chunks(rq, lq);
+  };
+  // the addresses that stage g >= 1 of tile u is loaded from
+  auto address = [&](const Tile& u, int g) {
+    if (g < stages(u) - 1) {
+      lp.at += PK ? step_p : KB;
+      lq.at += QK ? step_q : KB;
+    } else {
+      last_loads<S, S::BM, PK, WHOLE>(lp, source_of<S, FORM, 0>(a, u), g, u.k, tid);
+      last_loads<S, S::BN, QK, WHOLE>(lq, source_of<S, FORM, 1>(a, u), g, u.k, tid);
+    }
+  };
+  constexpr int HP = (S::CP + 1) / 2, HQ = (S::CQ + 1) / 2, HF = (S::FP + 1) / 2;
+  // chunks i0 .. i1 - 1 of an operand's stage g of tile u to LDS; last: g may be the last
+  // stage
+  auto put_p = [&](bool last, const Tile& u, int g, int i0, int i1) {
+    if (last) store_last<S, S::BM, PK, WHOLE>(rp, source_of<S, FORM, 0>(a, u), g, u.k, put_at_p, tid, i0, i1);
+    else store_chunks<S, S::BM, PK>(rp, put_at_p, i0, i1);
+  };
+  auto put_q = [&](bool last, const Tile& u, int g, int i0, int i1) {
+    if (last) store_last<S, S::BN, QK, WHOLE>(rq, source_of<S, FORM, 1>(a, u), g, u.k, put_at_q, tid, i0, i1);
+    else store_chunks<S, S::BN, QK>(rq, put_at_q, i0, i1);
+  };
+  // from one stage to the next the buffers that are stored to and read from change places
+  auto swap_put = [&] {
+    put_at_p += turn;
+    put_at_q += turn;
+    turn = -turn;
+  };
+  // The first stage of a tile, loaded before, to LDS; the second one into registers.
+  // Before it, stores and reads point at one buffer; after it, at one each.
+  auto prime = [&](const Tile& u) {
+    const int n = stages(u);
+    put_p(n == 1, u, 0, 0, S::CP);
+    put_q(n == 1, u, 0, 0, S::CQ);
+    swap_put();
+    if (n > 1) {
+      address(u, 1);
+      load_chunks(rp, lp);
+      load_chunks(rq, lq);
     }
   };
   Tile t = tile_at<S, FORM>(a, pre, chunk, tile);
-  if (t.k > 0) {
-    begin_tile(t);
-    load_chunks(rp, lp);
-    load_chunks(rq, lq);
-  }
+  load_first(t);
+  prime(t);
 
 #pragma unroll 1
   while (true) {
@@ -783,35 +884,19 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
     const int ntile = tile + step;
     const bool more = ntile < end;
     Tile tn = t;
-    // the addresses that stage g >= 1 of this tile is loaded from
-    auto address = [&](int g) {
-      if (g < nk - 1) {
-        lp.at += PK ? step_p : KB;
-        lq.at += QK ? step_q : KB;
-      } else {
-        last_loads<S, S::BM, PK>(lp, source_of<S, FORM, 0>(a, t), g, t.k, tid);
-        last_loads<S, S::BN, QK>(lq, source_of<S, FORM, 1>(a, t), g, t.k, tid);
-      }
-    };
     // the next tile's first stage, if there is one
     auto load_next = [&] {
       if (!more) return;
       tn = tile_at<S, FORM>(a, pre, chunk, ntile);
-      if (tn.k <= 0) return;
-      begin_tile(tn);
-      load_chunks(rp, lp);
-      load_chunks(rq, lq);
+      load_first(tn);
     };
 
-    if (nk == 0) {
-      load_next();
-    } else {
+    lds_barrier();       // the first stage is in LDS, the tile before has left it
+    {
       u32x4 F[2][S::PARTS * (S::FQ + S::FP)];
-      constexpr int HP = (S::CP + 1) / 2, HQ = (S::CQ + 1) / 2, HF = (S::FP + 1) / 2;
-      auto frags = [&](u32x4* f, auto buf_c, int ks) {
-        constexpr int BUF = decltype(buf_c)::value;
-        read_frags<S, S::BN, QK, S::FQ>(f, frag_q + BUF * LY::LQ::bytes, ks);
-        read_frags<S, S::BM, PK, S::FP>(f + S::PARTS * S::FQ, frag_p + BUF * LY::LP::bytes, ks);
+      auto frags = [&](u32x4* f, int ks) {
+        read_frags<S, S::BN, QK, S::FQ>(f, frag_q, ks);
+        read_frags<S, S::BM, PK, S::FP>(f + S::PARTS * S::FQ, frag_p, ks);
       };
       auto multiply = [&](const u32x4* f, int h) {
         // parts of Q and P, the small products first
@@ -824,144 +909,93 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
             for (int i = 0; i < S::FP; ++i)
               if (i / HF == h) mfma(acc[j][i], f[QPART[x] * S::FQ + j], f[S::PARTS * S::FQ + PPART[x] * S::FP + i]);
       };
-      // half h of an operand's chunks of stage g to buffer BUF; LAST: g is the last stage
-      auto put_p = [&](auto buf_c, auto last_c, int g, int h) {
-        lchar* d = put_at_p + decltype(buf_c)::value * LY::LP::bytes;
-        if constexpr (decltype(last_c)::value) store_last<S, S::BM, PK>(rp, source_of<S, FORM, 0>(a, t), g, t.k, d, tid, h ? HP : 0, h ? S::CP : HP);
-        else store_chunks<S, S::BM, PK>(rp, d, h ? HP : 0, h ? S::CP : HP);
-      };
-      auto put_q = [&](auto buf_c, auto last_c, int g, int h) {
-        lchar* d = put_at_q + decltype(buf_c)::value * LY::LQ::bytes;
-        if constexpr (decltype(last_c)::value) store_last<S, S::BN, QK>(rq, source_of<S, FORM, 1>(a, t), g, t.k, d, tid, h ? HQ : 0, h ? S::CQ : HQ);
-        else store_chunks<S, S::BN, QK>(rq, d, h ? HQ : 0, h ? S::CQ : HQ);
-      };
-      using I0 = std::integral_constant<int, 0>;
-      using I1 = std::integral_constant<int, 1>;
-      using Yes = std::true_type;
-      using No = std::false_type;
-      // stage kt is in buffer BUF.  MODE 0: store stage kt + 1, load stage kt + 2;
-      // 1: store the last stage, load the next tile's first; 2: the last stage.
-      auto stage = [&](const int kt, auto buf_c, auto mode_c) {
-        constexpr int BUF = decltype(buf_c)::value, MODE = decltype(mode_c)::value;
-        using CUR = std::integral_constant<int, BUF>;
-        using NXT = std::integral_constant<int, BUF ^ 1>;
-        using LAST = std::integral_constant<bool, MODE == 1>;
+      // One stage, kt: its MFMAs, the LDS writes of stage kt + 1 and the loads of stage kt + 2.
+      // MODE 0: both in this tile; 1: stage kt + 1 is the last one, the loads are the
+      // next tile's first stage; 2: kt is the last one.
+      auto stage = [&](const int kt, auto mode_c) {
+        constexpr int MODE = decltype(mode_c)::value;
+        constexpr bool LAST = MODE == 1;
+        // the other buffer is published, and this one's readers are done
+        auto turn_over = [&] {
+          lds_barrier();
+          frag_p -= turn;
+          frag_q -= turn;
+          if constexpr (MODE != 2) swap_put();
+          if constexpr (MODE == 0) frags(F[0], 0);
+          __builtin_amdgcn_sched_barrier(0);
+        };
+        frags(F[1], 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(F[0], 0);
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (S::SLABS == 2) {
-          frags(F[1], CUR{}, 1);
-          __builtin_amdgcn_sched_barrier(0);
-          multiply(F[0], 0);
-          __builtin_amdgcn_sched_barrier(0);
-          if constexpr (MODE != 2) {
-            put_p(NXT{}, LAST{}, kt + 1, 0);
-            put_p(NXT{}, LAST{}, kt + 1, 1);
-          }
+          if constexpr (MODE != 2) put_p(LAST, t, kt + 1, 0, S::CP);
           __builtin_amdgcn_sched_barrier(0);
           multiply(F[0], 1);
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (MODE == 0) {
-            address(kt + 2);
+            address(t, kt + 2);
             load_chunks(rp, lp);
           }
           __builtin_amdgcn_sched_barrier(0);
-          if constexpr (MODE != 2) {
-            put_q(NXT{}, LAST{}, kt + 1, 0);
-            put_q(NXT{}, LAST{}, kt + 1, 1);
-          }
+          if constexpr (MODE != 2) put_q(LAST, t, kt + 1, 0, S::CQ);
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (MODE == 0) load_chunks(rq, lq);
           if constexpr (MODE == 1) load_next();
-          lds_barrier();
-          if constexpr (MODE != 2) frags(F[0], NXT{}, 0);
-          __builtin_amdgcn_sched_barrier(0);
+          turn_over();
           multiply(F[1], 0);
           multiply(F[1], 1);
           __builtin_amdgcn_sched_barrier(0);
           return;
         }
-        frags(F[1], CUR{}, 1);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(F[0], 0);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (MODE != 2) put_p(NXT{}, LAST{}, kt + 1, 0);
+        if constexpr (MODE != 2) put_p(LAST, t, kt + 1, 0, HP);
         __builtin_amdgcn_sched_barrier(0);
         multiply(F[0], 1);
         __builtin_amdgcn_sched_barrier(0);
-        frags(F[0], CUR{}, 2);
+        frags(F[0], 2);
         __builtin_amdgcn_sched_barrier(0);
         multiply(F[1], 0);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (MODE != 2) {
-          put_p(NXT{}, LAST{}, kt + 1, 1);
-          put_q(NXT{}, LAST{}, kt + 1, 0);
+          put_p(LAST, t, kt + 1, HP, S::CP);
+          put_q(LAST, t, kt + 1, 0, HQ);
         }
         __builtin_amdgcn_sched_barrier(0);
         multiply(F[1], 1);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (MODE == 0) {
-          address(kt + 2);
+          address(t, kt + 2);
           load_chunks(rp, lp);
         }
         __builtin_amdgcn_sched_barrier(0);
-        frags(F[1], CUR{}, 3);
+        frags(F[1], 3);
         __builtin_amdgcn_sched_barrier(0);
         multiply(F[0], 0);
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (MODE != 2) put_q(NXT{}, LAST{}, kt + 1, 1);
+        if constexpr (MODE != 2) put_q(LAST, t, kt + 1, HQ, S::CQ);
         __builtin_amdgcn_sched_barrier(0);
         multiply(F[0], 1);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (MODE == 0) load_chunks(rq, lq);
         if constexpr (MODE == 1) load_next();
-        lds_barrier();
-        if constexpr (MODE != 2) frags(F[0], NXT{}, 0);
-        __builtin_amdgcn_sched_barrier(0);
+        turn_over();
         multiply(F[1], 0);
         multiply(F[1], 1);
         __builtin_amdgcn_sched_barrier(0);
       };
-      // stage g is in buffer (g + nk) % 2, so that the last one is in buffer 1
-      if (nk == 1) {
-        put_p(I1{}, Yes{}, 0, 0);
-        put_p(I1{}, Yes{}, 0, 1);
-        put_q(I1{}, Yes{}, 0, 0);
-        put_q(I1{}, Yes{}, 0, 1);
-        load_next();
-        lds_barrier();
-        frags(F[0], I1{}, 0);
-        stage(0, I1{}, std::integral_constant<int, 2>{});
-      } else {
+      if (nk > 1) {
         int kt = 0;
-        if (nk & 1) {
-          put_p(I1{}, No{}, 0, 0);
-          put_p(I1{}, No{}, 0, 1);
-          put_q(I1{}, No{}, 0, 0);
-          put_q(I1{}, No{}, 0, 1);
-          address(1);
-          load_chunks(rp, lp);
-          load_chunks(rq, lq);
-          lds_barrier();
-          frags(F[0], I1{}, 0);
-          stage(0, I1{}, I0{});
-          kt = 1;
-        } else {
-          put_p(I0{}, No{}, 0, 0);
-          put_p(I0{}, No{}, 0, 1);
-          put_q(I0{}, No{}, 0, 0);
-          put_q(I0{}, No{}, 0, 1);
-          address(1);
-          load_chunks(rp, lp);
-          load_chunks(rq, lq);
-          lds_barrier();
-          frags(F[0], I0{}, 0);
-        }
+        frags(F[0], 0);
 #pragma unroll 1
-        for (; kt + 2 < nk; kt += 2) {
-          stage(kt, I0{}, I0{});
-          stage(kt + 1, I1{}, I0{});
-        }
-        stage(nk - 2, I0{}, I1{});
-        stage(nk - 1, I1{}, std::integral_constant<int, 2>{});
+        for (; kt + 2 < nk; ++kt) stage(kt, std::integral_constant<int, 0>{});
+        stage(kt, std::integral_constant<int, 1>{});
+      } else {
+        load_next();
       }
+      // (its first fragments are read here, not across the branches: they would go
+      // through scratch memory)
+      frags(F[0], 0);
+      stage(nk - 1, std::integral_constant<int, 2>{});
     }
 
     if constexpr (EPI == EPI_LSE || EPI == EPI_LSE_CAP) {
@@ -969,23 +1003,24 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
     } else if constexpr (EPI == EPI_DZ || EPI == EPI_DZ_CAP) {
       Patch<S> patch;
       gradient_tile<S, EPI == EPI_DZ_CAP>(acc, a, t, tid, patch);
-      store_tile<S, FORM, S::F32, S::F32>(acc, out_of<FORM>(a, t), false, t, smem, tid, &patch);
+      store_tile<S, S::F32, S::F32, LY::BYTES>(acc, out_of<FORM>(a, t), false, t, smem, tid, &patch);
     } else {
       const Out out = out_of<FORM>(a, t);
-      if constexpr (S::F32) store_tile<S, FORM, true, true>(acc, out, a.add_f32, t, smem, tid);
-      else if (a.out_f32 || t.part >= 0) store_tile<S, FORM, true, true>(acc, out, a.add_f32, t, smem, tid);
-      else if (a.add) store_tile<S, FORM, false, true>(acc, out, a.add_f32, t, smem, tid);
-      else store_tile<S, FORM, false, false>(acc, out, false, t, smem, tid);
+      if constexpr (S::F32) store_tile<S, true, true, LY::BYTES>(acc, out, a.add_f32, t, smem, tid);
+      else if (a.out_f32 || t.part >= 0) store_tile<S, true, true, LY::BYTES>(acc, out, a.add_f32, t, smem, tid);
+      else if (a.add) store_tile<S, false, true, LY::BYTES>(acc, out, a.add_f32, t, smem, tid);
+      else store_tile<S, false, false, LY::BYTES>(acc, out, false, t, smem, tid);
     }
     if (!more) break;
     lds_barrier();
+    prime(tn);
     tile = ntile;
     t = tn;
   }
 }
 
-template <class S, int FORM, int EPI>
-hipError_t launch_shape(const ProductArgs& a, int cus, hipStream_t stream) {
+template <class S, int FORM, int EPI, bool WHOLE>
+hipError_t launch_whole(const ProductArgs& a, int cus, hipStream_t stream) {
   using LY = Layout<S, FORM>;
   const size_t lds = LY::BYTES + (size_t(a.groups) + 1) * 4;
   const int64_t nt = (a.n + S::BN - 1) / S::BN;
@@ -998,11 +1033,21 @@ hipError_t launch_shape(const ProductArgs& a, int cus, hipStream_t stream) {
   const int64_t grid = std::min<int64_t>((mt * nt + NUM_XCD - 1) / NUM_XCD * NUM_XCD,
                                          int64_t(cus) / NUM_XCD * NUM_XCD * fit);
   if (grid <= 0) return hipSuccess;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&product_kernel<S, FORM, EPI>),
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&product_kernel<S, FORM, EPI, WHOLE>),
                                      hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((product_kernel<S, FORM, EPI>), dim3(unsigned(grid)), dim3(S::NT), lds, stream, a);
+  hipLaunchKernelGGL((product_kernel<S, FORM, EPI, WHOLE>), dim3(unsigned(grid)), dim3(S::NT), lds, stream, a);
   return hipGetLastError();
+}
+
+// Two kernels: for operands whose 16-byte chunks end where their rows (k-row form), or
+// k (row form), end, and for any others, whose last stage is shifted and masked (one and
+// a half times the registers, some of them spilled, and a few us more a tile).
+template <class S, int FORM, int EPI>
+hipError_t launch_shape(const ProductArgs& a, int cus, hipStream_t stream) {
+  constexpr int V = 16 / S::ESZ;
+  const bool whole = FORM == FORM_TN ? a.m % V == 0 && a.n % V == 0 : a.k % V == 0 && (FORM == FORM_NT || a.n % V == 0);
+  return whole ? launch_whole<S, FORM, EPI, true>(a, cus, stream) : launch_whole<S, FORM, EPI, false>(a, cus, stream);
 }
 
 using Large = Shape<256, 256, 2, 4, false>;
