@@ -1,6 +1,7 @@
 // Products of the experts and of the head: the launcher, and the kernel for
 // operands too small for 16-byte loads.
 #include <algorithm>
+#include <cmath>
 
 #include "products_device.h"
 
@@ -161,75 +162,79 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// The fastest plan by a model of the time, in us: rounds of tiles over the GPU, a
-// stage of k (64 of bfloat16, 32 of binary32) and a tile's start and end measured for
-// each shape, and the partial sums' way to memory and back at 5 TB/s.
+// The fastest plan by a model of the time, in us: full rounds of tiles over the GPU and a
+// last one that fills a part of it, a stage of k (64 of bfloat16, 32 of binary32) measured
+// for each shape with every workgroup busy (`stage`) and with a quarter of them
+// (`alone`), a tile's start and end, and the partial sums' way to memory and back at 5 TB/s.
+struct Kind {
+  int shape, bm, bn, per_cu;
+  double stage, alone, ends;
+};
+constexpr Kind KINDS[] = {{SHAPE_LARGE, 256, 256, 1, 1.80, 1.10, 9.0},
+                          {SHAPE_MEDIUM, 128, 128, 2, 1.10, 0.54, 7.0},
+                          {SHAPE_SMALL, 32, 128, 3, 0.88, 0.43, 5.0}};
+constexpr Kind KINDS_TN[] = {{SHAPE_LARGE, 256, 256, 1, 1.72, 1.15, 11.0}, {SHAPE_MEDIUM, 128, 256, 1, 0.98, 0.72, 8.0}};
+constexpr Kind KINDS_F32[] = {{SHAPE_MEDIUM, 128, 128, 1, 1.55, 1.15, 6.0}, {SHAPE_SMALL, 32, 128, 2, 1.14, 0.71, 5.0}};
+constexpr Kind KINDS_F32_TN[] = {{SHAPE_MEDIUM, 128, 128, 1, 1.58, 1.19, 7.0}};
+
+// `tiles` tiles of `stages` stages each.
+double tiles_us(const Kind& s, double tiles, double stages, int cus) {
+  const double slots = double(cus) * s.per_cu, rounds = std::floor(tiles / slots), rest = tiles / slots - rounds;
+  double us = rounds * (stages * s.stage + s.ends);
+  if (rest > 0) us += stages * (s.alone + (s.stage - s.alone) * std::max(0.0, (rest - 0.25) / 0.75)) + s.ends;
+  return us;
+}
+
 ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus) {
   const int64_t esz = a.f32 ? 4 : 2, ke = 128 / esz;
   // 16-byte loads (product_tile.h)
   if (a.p_elems * esz < 16 || a.q_elems * esz < 16 || (form == FORM_TN && a.ld_p * esz < 16) ||
       (form != FORM_NT && a.ld_q * esz < 16))
     return {SHAPE_NAIVE, 0, 0};
-  struct Kind {
-    int shape, bm, bn, per_cu;
-    double stage, ends;
-  };
-  static const Kind KINDS[] = {{SHAPE_LARGE, 256, 256, 1, 2.2, 8.0},
-                               {SHAPE_MEDIUM, 128, 128, 2, 1.5, 5.0},
-                               {SHAPE_SMALL, 32, 128, 3, 1.1, 3.0}};
-  static const Kind KINDS_TN[] = {{SHAPE_LARGE, 256, 256, 1, 2.3, 8.0}, {SHAPE_MEDIUM, 128, 256, 1, 1.4, 6.0}};
-  static const Kind KINDS_F32[] = {{SHAPE_MEDIUM, 128, 128, 2, 4.0, 5.0}, {SHAPE_SMALL, 32, 128, 3, 1.5, 3.0}};
-  static const Kind KINDS_F32_TN[] = {{SHAPE_MEDIUM, 128, 128, 2, 4.0, 5.0}};
   const bool tn = form == FORM_TN;
   const Kind* kinds = a.f32 ? (tn ? KINDS_F32_TN : KINDS_F32) : (tn ? KINDS_TN : KINDS);
   const int nkinds = a.f32 ? (tn ? 1 : 2) : (tn ? 2 : 3);
   const int64_t groups = std::max(1, a.groups);
   ProductPlan best = {kinds[0].shape, 1 << 30, 0};
   double least = 1e30;
+  auto offer = [&](int shape, int64_t chunk, size_t bytes, double us) {
+    if (bytes > (size_t(2) << 30) || us >= least) return;
+    least = us;
+    best = {shape, int32_t(chunk), bytes};
+  };
   for (int i = 0; i < nkinds; ++i) {
     const Kind& s = kinds[i];
-    // tiles of rows: half a tile more a group than its rows fill
-    const int64_t mt = tn ? groups * ceil_div(a.m, s.bm)
-                          : groups == 1 ? ceil_div(a.rows, s.bm)
-                                        : std::max<int64_t>(std::min<int64_t>(groups, a.rows), a.rows / s.bm + groups / 2);
-    const int64_t tiles = mt * ceil_div(a.n, s.bn), slots = int64_t(cus) * s.per_cu;
-    const int64_t stages = std::max<int64_t>(1, ceil_div(tn ? a.rows / groups : a.k, ke));   // of a tile, on average
-    for (int cut = 1; cut <= 16; ++cut) {
-      if (cut > 1 && epi != EPI_STORE) break;
-      ProductPlan p = {s.shape, 1 << 30, 0};
-      double us;
-      if (!tn) {
+    const int64_t nt = ceil_div(a.n, s.bn);
+    if (!tn) {
+      // tiles of rows: a group's rows fill all but half of its last one
+      const int64_t mt = groups == 1 ? ceil_div(a.rows, s.bm)
+                                     : std::max<int64_t>(std::min<int64_t>(groups, a.rows), a.rows / s.bm + groups / 2);
+      const int64_t stages = ceil_div(a.k, ke);
+      if (mt * nt > (int64_t(1) << 30)) continue;        // tiles are counted in 31 bits
+      offer(s.shape, 1 << 30, 0, tiles_us(s, double(mt * nt), double(stages), cus));
+      for (int cut = 2; cut <= 32 && epi == EPI_STORE && mt * nt < 2 * cus * s.per_cu; ++cut) {
         const int64_t each = ceil_div(stages, cut);
-        if (cut > 1 && each < 4) break;
-        const int64_t chunks = ceil_div(stages, each);
-        if (chunks != cut) continue;
-        us = ceil_div(tiles * cut, slots) * (each * s.stage + s.ends);
-        if (cut > 1) {
-          p.chunk = int32_t(ceil_div(each * ke, 64) * 64);
-          p.bytes = size_t(chunks) * size_t(a.rows) * size_t(part_ld(a.n)) * 4;
-          us += 3.0 + 2e-6 / 5.0 * double(p.bytes);
-        }
-      } else {
-        // groups of very different lengths: a piece of 2^(cut - 1) x 512 rows at most, so that
-        // the longest tile is not much longer than a workgroup's share
-        if (cut == 16) break;
-        const int64_t chunk = cut == 1 ? int64_t(1) << 30 : int64_t(512) << (cut - 2);
-        if (cut > 1 && chunk >= a.rows) break;
-        // one group may have all rows
-        const int64_t longest = std::min<int64_t>(ceil_div(a.rows, ke), chunk / ke);
-        const double share = double(tiles) * stages * s.stage / slots + double(tiles) * s.ends / slots;
-        us = std::max(double(ceil_div(tiles, slots)) * s.ends + share, groups > 1 ? 0.5 * longest * s.stage : double(longest) * s.stage) ;
-        if (cut > 1) {
-          p.chunk = int32_t(chunk);
-          const int64_t pieces = 2 * (a.rows / chunk);
-          p.bytes = size_t(pieces) * size_t(a.m) * size_t(part_ld(a.n)) * 4;
-          us += 5.0 + 1e-6 / 5.0 * double(p.bytes) + double(pieces / 2) * (tiles / groups) * s.ends / slots;
-        }
+        if (each < 4) break;
+        if (ceil_div(stages, each) != cut) continue;
+        const size_t bytes = size_t(cut) * size_t(a.rows) * size_t(part_ld(a.n)) * 4;
+        offer(s.shape, each * ke, bytes, tiles_us(s, double(mt * nt * cut), double(each), cus) + 3.0 + 2e-6 / 5.0 * double(bytes));
       }
-      if (p.bytes > (size_t(2) << 30)) continue;
-      if (us < least) {
-        least = us;
-        best = p;
+    } else {
+      // Groups of very different lengths: on average a tile has `stages` stages, but one
+      // group may have half of all.
+      const int64_t mt = ceil_div(a.m, s.bm), all = ceil_div(a.rows, ke);
+      const double tiles = double(groups * mt * nt), stages = double(std::max<int64_t>(1, all / groups));
+      for (int step = 0; step < 8; ++step) {
+        const int64_t chunk = step == 0 ? int64_t(1) << 30 : int64_t(32768) >> (step - 1);
+        if (step > 0 && chunk >= a.rows) continue;
+        const bool cut = chunk < a.rows;
+        const int64_t longest = std::min(groups > 1 ? all / 2 + 1 : std::max<int64_t>(all, 1), ceil_div(chunk, ke));
+        const int64_t pieces = cut ? a.rows / chunk : 0;
+        const double count = tiles + double(pieces * mt * nt), each = cut || groups > 1 ? (tiles * stages) / count : stages;
+        double us = std::max(tiles_us(s, count, each, cus), double(longest) * s.alone + s.ends);
+        const size_t bytes = 2 * size_t(pieces) * size_t(a.m) * size_t(part_ld(a.n)) * 4;
+        if (cut) us += 5.0 + 1e-6 / 5.0 * double(bytes);
+        offer(s.shape, chunk, bytes, us);
       }
     }
   }
