@@ -926,21 +926,31 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
         };
         frags(F[1], 1);
         __builtin_amdgcn_sched_barrier(0);
-        multiply(F[0], 0);
-        __builtin_amdgcn_sched_barrier(0);
         if constexpr (S::SLABS == 2) {
-          if constexpr (MODE != 2) put_p(LAST, t, kt + 1, 0, S::CP);
-          __builtin_amdgcn_sched_barrier(0);
+          // The splitting of the next stage (some 7 instructions a value) goes between the
+          // MFMAs, a few at a time: behind them it would wait for the last one, and they
+          // for it.
+          multiply(F[0], 0);
           multiply(F[0], 1);
+          if constexpr (MODE != 2) {
+            put_p(LAST, t, kt + 1, 0, S::CP);
+            put_q(LAST, t, kt + 1, 0, S::CQ);
+          }
+          if constexpr (MODE == 0) {
+            constexpr int MFMAS = 6 * S::FQ * S::FP, VALU = (S::CP + S::CQ) * 26 / MFMAS + 1;
+#pragma unroll
+            for (int i = 0; i < MFMAS; ++i) {
+              __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+              __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+            }
+          }
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (MODE == 0) {
             address(t, kt + 2);
             load_chunks(rp, lp);
+            load_chunks(rq, lq);
           }
-          __builtin_amdgcn_sched_barrier(0);
-          if constexpr (MODE != 2) put_q(LAST, t, kt + 1, 0, S::CQ);
-          __builtin_amdgcn_sched_barrier(0);
-          if constexpr (MODE == 0) load_chunks(rq, lq);
           if constexpr (MODE == 1) load_next();
           turn_over();
           multiply(F[1], 0);
@@ -948,6 +958,8 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
           __builtin_amdgcn_sched_barrier(0);
           return;
         }
+        multiply(F[0], 0);
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (MODE != 2) put_p(LAST, t, kt + 1, 0, HP);
         __builtin_amdgcn_sched_barrier(0);
         multiply(F[0], 1);
