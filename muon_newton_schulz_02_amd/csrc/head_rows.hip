@@ -102,35 +102,42 @@ __global__ __launch_bounds__(NT) void head_rows_kernel(const HeadRows a) {
   }
 }
 
-// A wave a row: the maximum over the tiles, the sums brought to it.
+// W waves a row: the maximum over the tiles, the sums brought to it.  Four where there
+// are few rows, whose thousand tiles would be a chain of 16 loads for one.
+template <int W>
 __global__ __launch_bounds__(NT) void head_finish_kernel(const HeadFinish a) {
-  const int lane = threadIdx.x & 63;
-  const int i = blockIdx.x * (NT / 64) + (threadIdx.x >> 6);
-  if (i >= (a.targets ? a.rows : min(a.offsets[1], a.rows))) return;
-  if (a.targets && !has_target(a, a.targets[i])) {
-    if (lane == 0) a.loss[i] = a.lse[i] = a.targets[i] == a.ignore_index ? 0.f : __builtin_nanf("");
-    return;
-  }
-  const float2* s = a.stats + int64_t(i) * a.tiles;
+  __shared__ float2 part[NT / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i = blockIdx.x * (NT / 64 / W) + wave / W;
+  const bool row = i < (a.targets ? a.rows : min(a.offsets[1], a.rows));
+  const bool ignored = row && a.targets && !has_target(a, a.targets[i]);
   float m = -INFINITY, sum = 0.f;
-  for (int t = lane; t < a.tiles; t += 64) {
-    const float2 v = s[t];
-    const float n = fmaxf(m, v.x), f = n == -INFINITY ? 0.f : n;
-    sum = sum * __builtin_amdgcn_exp2f(m - f) + v.y * __builtin_amdgcn_exp2f(v.x - f);
-    m = n;
-  }
-  for (int d = 1; d < 64; d *= 2) {
-    const float om = __shfl_xor(m, d), os = __shfl_xor(sum, d);
+  auto join = [&](float om, float os) {
     const float n = fmaxf(m, om), f = n == -INFINITY ? 0.f : n;
     sum = sum * __builtin_amdgcn_exp2f(m - f) + os * __builtin_amdgcn_exp2f(om - f);
     m = n;
+  };
+  if (row && !ignored) {
+    const float2* s = a.stats + int64_t(i) * a.tiles;
+    for (int t = lane + 64 * (wave % W); t < a.tiles; t += 64 * W) join(s[t].x, s[t].y);
   }
-  if (lane == 0) {
-    const float lse = __builtin_fmaf(m == -INFINITY ? 0.f : m, LN2, logf(sum));
-    const int r = a.targets ? i : a.row[i];
-    a.lse[r] = lse;
-    a.loss[r] = lse - a.logit[i];
+  for (int d = 1; d < 64; d *= 2) join(__shfl_xor(m, d), __shfl_xor(sum, d));
+  if constexpr (W > 1) {
+    if (lane == 0) part[wave] = make_float2(m, sum);
+    __syncthreads();
+    m = -INFINITY;
+    sum = 0.f;
+    for (int w = 0; w < W; ++w) join(part[wave / W * W + w].x, part[wave / W * W + w].y);
   }
+  if (!row || lane != 0 || wave % W != 0) return;
+  const int r = a.targets ? i : a.row[i];
+  if (ignored) {
+    a.loss[r] = a.lse[r] = a.targets[i] == a.ignore_index ? 0.f : __builtin_nanf("");
+    return;
+  }
+  const float lse = __builtin_fmaf(m == -INFINITY ? 0.f : m, LN2, logf(sum));
+  a.lse[r] = lse;
+  a.loss[r] = lse - a.logit[i];
 }
 
 }  // namespace
@@ -143,7 +150,10 @@ hipError_t launch_head_rows(const HeadRows& a, hipStream_t stream) {
 }
 
 hipError_t launch_head_finish(const HeadFinish& a, hipStream_t stream) {
-  hipLaunchKernelGGL(head_finish_kernel, dim3(unsigned((a.rows + NT / 64 - 1) / (NT / 64))), dim3(NT), 0, stream, a);
+  const int waves = a.rows <= 1024 ? 4 : 1, per = NT / 64 / waves;
+  const dim3 grid(unsigned((a.rows + per - 1) / per));
+  if (waves == 4) hipLaunchKernelGGL(head_finish_kernel<4>, grid, dim3(NT), 0, stream, a);
+  else hipLaunchKernelGGL(head_finish_kernel<1>, grid, dim3(NT), 0, stream, a);
   return hipGetLastError();
 }
 

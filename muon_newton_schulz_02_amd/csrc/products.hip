@@ -162,6 +162,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
+// Rows of a group, on average, up to which a product is streamed.
+constexpr int64_t STREAM_ROWS = 16;
+
 // The fastest plan by a model of the time, in us: full rounds of tiles over the GPU and a
 // last one that fills a part of it, a stage of k (64 of bfloat16, 32 of binary32) measured
 // for each shape with every workgroup busy (`stage`) and with a quarter of them
@@ -191,6 +194,10 @@ ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus) {
   if (a.p_elems * esz < 16 || a.q_elems * esz < 16 || (form == FORM_TN && a.ld_p * esz < 16) ||
       (form != FORM_NT && a.ld_q * esz < 16))
     return {SHAPE_NAIVE, 0, 0};
+  // few rows: Q's way from memory is all (STREAM_ROWS)
+  if (form == FORM_NT && epi != EPI_DZ && a.k % (16 / esz) == 0 && a.rows <= STREAM_ROWS * std::max(1, a.groups) &&
+      (epi != EPI_STORE || (!a.add && !a.map && a.out_f32 == a.f32)) && a.rows < (1 << 20))
+    return {SHAPE_STREAM, 0, 0};
   const bool tn = form == FORM_TN;
   const Kind* kinds = a.f32 ? (tn ? KINDS_F32_TN : KINDS_F32) : (tn ? KINDS_TN : KINDS);
   const int nkinds = a.f32 ? (tn ? 1 : 2) : (tn ? 2 : 3);
@@ -244,6 +251,7 @@ ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus) {
 int32_t product_tile_n(int form, int epi, const ProductArgs& a, int cus) {
   switch (product_plan(form, epi, a, cus).shape) {
     case SHAPE_NAIVE: return TS;
+    case SHAPE_STREAM: return STREAM_TILE_N;
     case SHAPE_LARGE: return 256;
     default: return 128;
   }
@@ -256,6 +264,7 @@ hipError_t launch_product(int form, int epi, const ProductArgs& args, int cus, c
     a.chunk = plan.chunk;
     a.part = reinterpret_cast<float*>(ws);
     const int kind = a.cap == 0.f ? epi : epi == EPI_LSE ? EPI_LSE_CAP : epi == EPI_DZ ? EPI_DZ_CAP : epi;
+    if (plan.shape == SHAPE_STREAM) return launch_stream(kind, a, stream);
     hipError_t e = form == FORM_NT   ? launch_nt(plan.shape, kind, a, cus, stream)
                    : form == FORM_NN ? launch_nn(plan.shape, a, cus, stream) : launch_tn(plan.shape, a, cus, stream);
     if (e == hipSuccess && plan.bytes)

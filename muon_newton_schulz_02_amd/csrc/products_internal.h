@@ -57,10 +57,14 @@ struct ProductArgs {
 };
 
 // Tile shapes.
-enum ProductShape : int { SHAPE_NAIVE = 0, SHAPE_SMALL = 1, SHAPE_MEDIUM = 2, SHAPE_LARGE = 3 };
+enum ProductShape : int { SHAPE_NAIVE = 0, SHAPE_SMALL = 1, SHAPE_MEDIUM = 2, SHAPE_LARGE = 3, SHAPE_STREAM = 4 };
 hipError_t launch_nt(int shape, int epi, const ProductArgs& a, int cus, hipStream_t stream);
 hipError_t launch_nn(int shape, const ProductArgs& a, int cus, hipStream_t stream);
 hipError_t launch_tn(int shape, const ProductArgs& a, int cus, hipStream_t stream);
+// NT, STORE (without an addend or a map, out of the operands' type) and LSE, k a multiple
+// of 16 bytes.
+hipError_t launch_stream(int epi, const ProductArgs& a, hipStream_t stream);
+constexpr int STREAM_TILE_N = 32;
 
 // How a product runs.  k may be cut into chunks, so that few tiles fill the GPU and
 // one long group does not hold up the rest: a tile then takes `chunk` of k, writes
