@@ -19,8 +19,8 @@
  *     run, so a router on the GPU needs no synchronisation.  Offsets are taken
  *     as at most `rows` and at least 0, and an expert whose end is not above
  *     its start as one without rows: no value of theirs makes a call read or
- *     write out of range.  Ranges that overlap give the rows in them one of
- *     their experts' values.
+ *     write out of range.  Rows that lie in more than one range get any values in
+ *     y and grad_x.
  *   - Rows before offsets[0] and from offsets[experts] on belong to no expert:
  *     they are not read, and y and grad_x stay as they were there.
  *   - An expert without rows has grad_W_e = 0 (accumulate: unchanged).
@@ -42,6 +42,9 @@
  *     muon_experts_workspace_bytes bytes) calls with different workspaces may
  *     overlap; those that share one must not.  A call that needs none (0
  *     bytes) may overlap any other.
+ *   - While launches are timed (muon_timing_enable) products count as
+ *     MUON_KC_COMBINE, logits as MUON_KC_GRAM, the head's packing as
+ *     MUON_KC_MOMENTUM and its last pass as MUON_KC_NORM.
  *   - Capture: a call on a capturing stream that needs a workspace needs one of
  *     the caller's (UNSUPPORTED without).  It records kernels on `stream` only.
  */

@@ -30,7 +30,7 @@ __device__ __forceinline__ void copy_row(T* dst, const T* src, int n, int lane) 
 
 // Each workgroup packs `chunk` rows: it counts the rows with a target before
 // them by itself (8 bytes a row, read from L2), which saves a launch and a wait;
-// the chunks are cut so that 512 workgroups at most do it.  The copy of x gives
+// the chunks are cut so that about a thousand workgroups at most do it.  The copy of x gives
 // the products rows at 16-byte boundaries, and takes ignored rows out of them:
 // their work, and whatever their x holds.
 template <class T>
@@ -41,6 +41,7 @@ __global__ __launch_bounds__(NT) void head_rows_kernel(const HeadRows a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r0 = blockIdx.x * a.chunk, r1 = min(r0 + a.chunk, a.rows);
   int before = 0;
+#pragma unroll 8
   for (int r = tid; r < r0; r += NT) before += has_target(a, a.targets[r]) ? 1 : 0;
   for (int s = 1; s < 64; s *= 2) before += __shfl_xor(before, s);
   if (lane == 0) wave_sum[wave] = before;

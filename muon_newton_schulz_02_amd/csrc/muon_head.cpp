@@ -292,7 +292,7 @@ hipError_t enqueue(const Call& c, const Plan& p, char* ws, int cus, bool capturi
   h.rows = int32_t(d.rows);
   h.dim = int32_t(d.dim);
   h.f32 = d.dtype == MUON_DTYPE_F32;
-  h.chunk = int32_t(std::max<int64_t>(16, (d.rows + 511) / 512));
+  h.chunk = int32_t(std::max<int64_t>(4, (d.rows + 1023) / 1024));
   hipError_t e = p.direct ? hipSuccess : timed(MUON_KC_MOMENTUM, [&] { return launch_head_rows(h, c.stream); });
   if (e != hipSuccess) return e;
   if (fwd) {

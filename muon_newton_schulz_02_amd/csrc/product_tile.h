@@ -745,7 +745,7 @@ __device__ __forceinline__ Tile tile_at(const ProductArgs& a, const int* pre, in
   group_range(a, r.g, first, end);
   first = __builtin_amdgcn_readfirstlane(first);
   end = __builtin_amdgcn_readfirstlane(end);
-  r.lo = first < end ? first : 0;      // nothing is read of a group without rows but zeros' addresses
+  r.lo = first < end ? first : 0;      // TN: a group without rows reads the tensor's first row, as zeros
   r.n = a.n - r.j0;
   const int k = FORM == FORM_TN ? end - first : a.k;
   r.m = FORM == FORM_TN ? a.m - r.i0 : end - first - r.i0;
@@ -1053,8 +1053,8 @@ hipError_t launch_whole(const ProductArgs& a, int cus, hipStream_t stream) {
 }
 
 // Two kernels: for operands whose 16-byte chunks end where their rows (k-row form), or
-// k (row form), end, and for any others, whose last stage is shifted and masked (one and
-// a half times the registers, some of them spilled, and a few us more a tile).
+// k (row form), end, and for any others, whose last stage is shifted and masked (2 %
+// slower on 8192 x 1536 by 32768 x 1536: 780 us against 764).
 template <class S, int FORM, int EPI>
 hipError_t launch_shape(const ProductArgs& a, int cus, hipStream_t stream) {
   constexpr int V = 16 / S::ESZ;

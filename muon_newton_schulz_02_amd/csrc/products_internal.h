@@ -77,7 +77,7 @@ constexpr int STREAM_TILE_N = 32;
 //           all than there are, are not cut.
 struct ProductPlan {
   int shape;
-  int32_t chunk;               // k of a chunk, a multiple of 64
+  int32_t chunk;               // k of a chunk, whole stages
   size_t bytes;                // of partial sums: workspace that launch_product needs
 };
 ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus);

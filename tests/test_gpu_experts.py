@@ -120,6 +120,69 @@ def test_large_tiles_and_long_sums():
     run_all([1100, 300], 400, 392, "f32")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("counts", [[1], [16], [17], [32], [2, 0, 30, 1], [15, 16, 17]])
+@pytest.mark.parametrize("inn,out", [(8, 33), (136, 31), (1544, 65), (2048, 100)])
+def test_few_rows(inn, out, counts, dtype):
+    run_all(counts, inn, out, dtype, spare=1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_products_cut_along_k(dtype):
+    """Few tiles and a long sum: partial sums in a workspace, added in order."""
+    dt = DTYPES[dtype]
+    x, w, off, gy, y, gx, gw = run_all([130, 7], 4100, 96, dtype, spare=2)
+    assert mb.ExpertsArgs(x, w, off, y).workspace_bytes() > 0
+    x, w, off, gy, y, gx, gw = run_all([40, 0, 3000, 60], 72, 88, dtype, spare=2)
+    args = mb.ExpertsVjpArgs(x, None, off, gy, None, gw)
+    assert args.workspace_bytes() > 0
+    # the same with a workspace of the caller's, and one that is too small
+    other = torch.full_like(gw, float("nan"))
+    mine = mb.ExpertsVjpArgs(x, None, off, gy, None, other)
+    ws = torch.full((args.workspace_bytes(),), 255, dtype=torch.uint8, device="cuda")
+    mb.muon_experts_product_vjp(mine, workspace=ws)
+    mb.muon_experts_product_vjp(args)
+    assert torch.equal(other, gw)
+    with pytest.raises(mb.MuonError, match="holds"):
+        mb.muon_experts_product_vjp(mine, workspace=ws[:256])
+    # ranges that overlap: every expert's sum over its own
+    bad = torch.tensor([0, 3100, 1, 2500, 3102], dtype=torch.int32, device="cuda")
+    mb.muon_experts_product_vjp(x, None, bad, gy, None, gw, workspace=ws)
+    xs, gys = np.nan_to_num(np64(x)), np.nan_to_num(np64(gy))
+    xs[3100:] = gys[3100:] = 0
+    x[3100:] = gy[3100:] = 0
+    mb.muon_experts_product_vjp(x, None, bad, gy, None, gw, workspace=ws)
+    for e, (lo, hi) in enumerate([(0, 3100), (0, 0), (1, 2500), (2500, 3102)]):
+        want, reach = orc.training.experts_grad_w(xs, gys, [lo, hi])
+        check(gw[e:e + 1], want, reach, 3100, dt, f"expert {e}")
+
+
+def test_rows_and_experts_beyond_32_bits():
+    """Row strides that put the last row 4.4 GB from the first, an expert stride of 4.6 GB."""
+    gen = torch.Generator().manual_seed(12)
+    rows, inn, out, ld = 2100, 64, 40, 1 << 20
+    wide = [torch.empty(rows, ld, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    x, y = wide[0][:, 7:7 + inn], wide[1][:, 3:3 + out]
+    far = torch.empty(2, 2_300_000_000, dtype=torch.bfloat16, device="cuda")
+    w = far[:, 5:5 + out * inn].unflatten(1, (out, inn))
+    x.copy_(torch.randn(rows, inn, generator=gen))
+    w.copy_(torch.randn(2, out, inn, generator=gen))
+    off = offsets_of([1000, 1100])
+    near = torch.zeros(rows, out, dtype=torch.bfloat16, device="cuda")
+    mb.muon_experts_product(x, w, off, y)
+    mb.muon_experts_product(x.contiguous(), w.contiguous(), off, near)
+    assert torch.equal(y, near)
+    gx, gw = wide[0][:, 100:100 + inn], far[:, 9000:9000 + out * inn].unflatten(1, (out, inn))
+    gx0, gw0 = torch.zeros(rows, inn, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, out, inn, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(mb.MuonError, match="overlaps"):
+        mb.muon_experts_product_vjp(x, w, off, y, gx, gw)          # grad_x between x's rows: address ranges meet
+    gx = torch.empty(rows, ld, dtype=torch.bfloat16, device="cuda")[:, 1:1 + inn]
+    gw = torch.empty(2, 2_300_000_000, dtype=torch.bfloat16, device="cuda")[:, 1:1 + out * inn].unflatten(1, (out, inn))
+    mb.muon_experts_product_vjp(x, w, off, y, gx, gw)
+    mb.muon_experts_product_vjp(x.contiguous(), w.contiguous(), off, near, gx0, gw0)
+    assert torch.equal(gx, gx0) and torch.equal(gw, gw0)
+
+
 def test_many_experts():
     counts = np.random.default_rng(3).integers(0, 4, 2048).tolist()
     run_all(counts, 24, 40, "bf16")

@@ -2,6 +2,7 @@
 on the host before any HIP call, and the oracle against differences."""
 import os
 import re
+import shutil
 import subprocess
 
 import numpy as np
@@ -240,3 +241,17 @@ def test_oracle_against_differences():
     assert not y[4].any() and not gw[1].any()
     # both sides of <y, gy> as a bilinear form
     assert np.isclose((y * gy)[:4].sum(), (gx * x)[:4].sum()) and np.isclose((y * gy)[:4].sum(), (gw * we).sum())
+
+
+def test_no_exception_leaves_a_c_entry(L, tmp_path):
+    """Without memory for the error's text a call still ends with its status (host_plan/training_nomem.cpp)."""
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("needs g++")
+    here = os.path.dirname(os.path.abspath(__file__))
+    exe = str(tmp_path / "training_nomem")
+    r = subprocess.run([gxx, "-std=c++17", "-O1", "-I", INCLUDE, "-o", exe,
+                        os.path.join(here, "host_plan", "training_nomem.cpp"), "-ldl"], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    r = subprocess.run([exe, mb.LIB_PATH], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "72 calls, 0 threw" in r.stdout, r.stdout + r.stderr
