@@ -4,6 +4,7 @@
 namespace muon {
 
 hipError_t launch_nn(int shape, const ProductArgs& a, int cus, hipStream_t stream) {
+  if (a.f32 && shape == SHAPE_LARGE) return launch_shape<LargeF32, FORM_NN, EPI_STORE>(a, cus, stream);
   if (a.f32)
     return shape == SHAPE_SMALL ? launch_shape<SmallF32, FORM_NN, EPI_STORE>(a, cus, stream)
                                 : launch_shape<MediumF32, FORM_NN, EPI_STORE>(a, cus, stream);

@@ -66,6 +66,9 @@ struct Shape {
   static constexpr int ESZ = F32 ? 4 : 2, KE = KB / ESZ, PARTS = F32 ? 3 : 1, SLABS = KE / 16;
   static constexpr int WTP = BM / WM, WTQ = BN / WN, FP = WTP / 32, FQ = WTQ / 32;
   static constexpr int CP = BM * 8 / NT, CQ = BN * 8 / NT;   // 16-byte chunks of a stage per thread
+  // One LDS buffer where two would not fit: a stage's fragments are then all in registers
+  // before the next stage is stored.
+  static constexpr bool SINGLE = F32 && BM + BN > 256;
   static_assert(CP >= 1 && CQ >= 1 && BM * 8 % NT == 0 && BN * 8 % NT == 0, "whole chunks per thread");
 };
 
@@ -88,7 +91,7 @@ struct Layout {
   using LP = Lds<S, S::BM, PK>;
   using LQ = Lds<S, S::BN, QK>;
   // buffer b: P at b BUF, Q behind it
-  static constexpr int BUF = LP::bytes + LQ::bytes, BYTES = 2 * BUF;
+  static constexpr int BUF = LP::bytes + LQ::bytes, BYTES = (S::SINGLE ? 1 : 2) * BUF;
 };
 
 // ------------------------------------------------------------------ tiles
@@ -804,7 +807,7 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
   lchar* frag_p = (lchar*)smem + frag_lds<S, S::BM, PK>(wp * S::WTP, lane);
   lchar* frag_q = (lchar*)smem + LY::LP::bytes + frag_lds<S, S::BN, QK>(wq * S::WTQ, lane);
   asm volatile("" : "+v"(put_at_p), "+v"(put_at_q), "+v"(frag_p), "+v"(frag_q));
-  int turn = LY::BUF;       // to the other buffer
+  int turn = S::SINGLE ? 0 : LY::BUF;       // to the other buffer
   u32x4 rp[S::CP], rq[S::CQ];
   Loads<S::CP> lp;
   Loads<S::CQ> lq;
@@ -909,12 +912,54 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
             for (int i = 0; i < S::FP; ++i)
               if (i / HF == h) mfma(acc[j][i], f[QPART[x] * S::FQ + j], f[S::PARTS * S::FQ + PPART[x] * S::FP + i]);
       };
+      // binary32: the splitting of the next stage (some 7 instructions a value) goes between
+      // `mfmas` MFMAs, a few at a time: behind them it would wait for the last one, and
+      // they for it
+      auto interleave = [&](auto mfmas) {
+        constexpr int N = decltype(mfmas)::value, CHUNKS = S::CP + S::CQ, VALU = CHUNKS * 26 / N + 1;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+          __builtin_amdgcn_sched_group_barrier(0x200, (CHUNKS * 3 + N - 1) / N, 0);
+        }
+      };
       // One stage, kt: its MFMAs, the LDS writes of stage kt + 1 and the loads of stage kt + 2.
       // MODE 0: both in this tile; 1: stage kt + 1 is the last one, the loads are the
       // next tile's first stage; 2: kt is the last one.
       auto stage = [&](const int kt, auto mode_c) {
         constexpr int MODE = decltype(mode_c)::value;
         constexpr bool LAST = MODE == 1;
+        if constexpr (S::SINGLE) {
+          // On entry F holds the stage's two slabs (the second one's reads may be on their
+          // way).  The barriers: every wave has the stage, which may be overwritten; the
+          // next one is there.
+          multiply(F[0], 0);
+          __builtin_amdgcn_sched_barrier(0);
+          lds_barrier();
+          multiply(F[0], 1);
+          if constexpr (MODE != 2) {
+            put_p(LAST, t, kt + 1, 0, S::CP);
+            put_q(LAST, t, kt + 1, 0, S::CQ);
+          }
+          if constexpr (MODE == 0) interleave(std::integral_constant<int, 6 * S::FQ * (S::FP - HF)>{});
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (MODE == 0) {
+            address(t, kt + 2);
+            load_chunks(rp, lp);
+            load_chunks(rq, lq);
+          }
+          if constexpr (MODE == 1) load_next();
+          if constexpr (MODE != 2) lds_barrier();
+          if constexpr (MODE == 0) frags(F[0], 0);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(F[1], 0);
+          multiply(F[1], 1);
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (MODE == 0) frags(F[1], 1);
+          __builtin_amdgcn_sched_barrier(0);
+          return;
+        }
         // the other buffer is published, and this one's readers are done
         auto turn_over = [&] {
           lds_barrier();
@@ -927,24 +972,13 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
         frags(F[1], 1);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (S::SLABS == 2) {
-          // The splitting of the next stage (some 7 instructions a value) goes between the
-          // MFMAs, a few at a time: behind them it would wait for the last one, and they
-          // for it.
           multiply(F[0], 0);
           multiply(F[0], 1);
           if constexpr (MODE != 2) {
             put_p(LAST, t, kt + 1, 0, S::CP);
             put_q(LAST, t, kt + 1, 0, S::CQ);
           }
-          if constexpr (MODE == 0) {
-            constexpr int MFMAS = 6 * S::FQ * S::FP, VALU = (S::CP + S::CQ) * 26 / MFMAS + 1;
-#pragma unroll
-            for (int i = 0; i < MFMAS; ++i) {
-              __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-              __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
-              __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
-            }
-          }
+          if constexpr (MODE == 0) interleave(std::integral_constant<int, 6 * S::FQ * S::FP>{});
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (MODE == 0) {
             address(t, kt + 2);
@@ -998,6 +1032,7 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
       if (nk > 1) {
         int kt = 0;
         frags(F[0], 0);
+        if constexpr (S::SINGLE) frags(F[1], 1);
 #pragma unroll 1
         for (; kt + 2 < nk; ++kt) stage(kt, std::integral_constant<int, 0>{});
         stage(kt, std::integral_constant<int, 1>{});
@@ -1007,6 +1042,7 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
       // (its first fragments are read here, not across the branches: they would go
       // through scratch memory)
       frags(F[0], 0);
+      if constexpr (S::SINGLE) frags(F[1], 1);
       stage(nk - 1, std::integral_constant<int, 2>{});
     }
 
@@ -1066,6 +1102,7 @@ using Large = Shape<256, 256, 2, 4, false>;
 using Medium = Shape<128, 128, 2, 2, false>;
 using MediumTn = Shape<128, 256, 2, 4, false>;
 using Small = Shape<32, 128, 1, 4, false>;
+using LargeF32 = Shape<256, 128, 4, 2, true>;
 using MediumF32 = Shape<128, 128, 2, 4, true>;
 using SmallF32 = Shape<32, 128, 1, 4, true>;
 

@@ -186,8 +186,10 @@ constexpr Kind KINDS[] = {{SHAPE_LARGE, 256, 256, 1, 1.80, 1.10, 9.0},
                           {SHAPE_MEDIUM, 128, 128, 2, 1.10, 0.54, 7.0},
                           {SHAPE_SMALL, 32, 128, 3, 0.88, 0.43, 5.0}};
 constexpr Kind KINDS_TN[] = {{SHAPE_LARGE, 256, 256, 1, 1.72, 1.15, 11.0}, {SHAPE_MEDIUM, 128, 256, 1, 0.98, 0.72, 8.0}};
-constexpr Kind KINDS_F32[] = {{SHAPE_MEDIUM, 128, 128, 1, 1.55, 1.15, 6.0}, {SHAPE_SMALL, 32, 128, 2, 1.14, 0.71, 5.0}};
-constexpr Kind KINDS_F32_TN[] = {{SHAPE_MEDIUM, 128, 128, 1, 1.58, 1.19, 7.0}};
+constexpr Kind KINDS_F32[] = {{SHAPE_LARGE, 256, 128, 1, 2.58, 2.05, 7.0},
+                              {SHAPE_MEDIUM, 128, 128, 1, 1.42, 1.10, 5.0},
+                              {SHAPE_SMALL, 32, 128, 2, 1.10, 0.70, 5.0}};
+constexpr Kind KINDS_F32_TN[] = {{SHAPE_LARGE, 256, 128, 1, 2.62, 2.10, 8.0}, {SHAPE_MEDIUM, 128, 128, 1, 1.45, 1.15, 6.0}};
 
 // `tiles` tiles of `stages` stages each.
 double tiles_us(const Kind& s, double tiles, double stages, int cus) {
@@ -210,7 +212,7 @@ ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus) {
     return {SHAPE_STREAM, 0, 0};
   const bool tn = form == FORM_TN;
   const Kind* kinds = a.f32 ? (tn ? KINDS_F32_TN : KINDS_F32) : (tn ? KINDS_TN : KINDS);
-  const int nkinds = a.f32 ? (tn ? 1 : 2) : (tn ? 2 : 3);
+  const int nkinds = tn ? 2 : 3;
   const int64_t groups = std::max(1, a.groups);
   ProductPlan best = {kinds[0].shape, 1 << 30, 0};
   double least = 1e30;
@@ -262,7 +264,7 @@ int32_t product_tile_n(int form, int epi, const ProductArgs& a, int cus) {
   switch (product_plan(form, epi, a, cus).shape) {
     case SHAPE_NAIVE: return TS;
     case SHAPE_STREAM: return STREAM_TILE_N;
-    case SHAPE_LARGE: return 256;
+    case SHAPE_LARGE: return a.f32 ? 128 : 256;
     default: return 128;
   }
 }

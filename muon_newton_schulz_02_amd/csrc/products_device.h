@@ -32,6 +32,11 @@ __device__ __forceinline__ void group_sums(int groups, int* pre, int* wave_sum, 
   const int lane = tid & 63, wave = tid >> 6;
   int carry = 0;
   if (tid == 0) pre[0] = 0;
+  if (groups == 1) {
+    if (tid == 0) pre[1] = value(0);
+    __syncthreads();
+    return;
+  }
   for (int b = 0; b < groups; b += NT) {
     const int g = b + tid;
     int v = g < groups ? value(g) : 0;
