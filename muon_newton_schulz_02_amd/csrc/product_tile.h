@@ -734,6 +734,14 @@ __device__ __forceinline__ Tile tile_at(const ProductArgs& a, const int* pre, in
   }
   r.g = __builtin_amdgcn_readfirstlane(lo);
   const int before = __builtin_amdgcn_readfirstlane(pre[r.g]), of = __builtin_amdgcn_readfirstlane(pre[r.g + 1]) - before;
+  int slot = 2 * (before - r.g);
+  if constexpr (FORM == FORM_TN) {
+    if (a.queue) {
+      const int32_t* order = a.queue + QUEUE_PRE + a.groups + 1;
+      r.g = __builtin_amdgcn_readfirstlane(order[r.g]);
+      slot = __builtin_amdgcn_readfirstlane(order[a.groups + r.g]);
+    }
+  }
   if constexpr (FORM == FORM_TN) {
     piece = u - before;
     t -= u * mt * nt;
@@ -754,9 +762,27 @@ __device__ __forceinline__ Tile tile_at(const ProductArgs& a, const int* pre, in
   r.m = FORM == FORM_TN ? a.m - r.i0 : end - first - r.i0;
   r.k0 = piece * chunk;                // below 2^31: a group's pieces end with its rows
   r.k = min(chunk, k - r.k0);
-  if constexpr (FORM == FORM_TN) r.part = of > 1 ? 2 * (before - r.g) + piece : -1;
+  if constexpr (FORM == FORM_TN) r.part = of > 1 ? slot + piece : -1;
   else r.part = k > chunk ? piece : -1;
   return r;
+}
+
+// The queue of TN's tiles.  Strips of consecutive tiles, a column of a band each, belong
+// to the XCDs in turn, so that an XCD's tiles share panels in its L2; when all of its own
+// are taken a workgroup goes on with the other XCDs'.  Which workgroup has a tile changes
+// nothing in it.
+template <class S>
+__device__ __forceinline__ int strip_of(const ProductArgs& a) {
+  return min(BAND, (a.m + S::BM - 1) / S::BM);
+}
+__device__ __forceinline__ int queue_tile(const ProductArgs& a, int xcd, int strip, int end) {
+  for (int x = 0; x < QUEUE_XCD; ++x) {
+    const int got = __hip_atomic_fetch_add(a.queue + xcd * QUEUE_STEP, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int64_t t = (int64_t(got / strip) * QUEUE_XCD + xcd) * strip + got % strip;
+    if (t < end) return int(t);
+    xcd = (xcd + 1) % QUEUE_XCD;
+  }
+  return end;                        // none is left
 }
 
 template <class S, int FORM, int EPI, bool WHOLE>
@@ -771,20 +797,33 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
   // Which tiles are this workgroup's: workgroup b runs on XCD b % 8.  Tiles of equal
   // work (NT, NN): a contiguous eighth of them for each XCD.  TN, where k differs from
   // group to group: the grid takes as many consecutive tiles at a time as it has
-  // workgroups, so that a long group is spread over all of them.
+  // workgroups, so that a long group is spread over all of them; or, with a queue, each
+  // takes the next tile as it comes free, the longest ones first (queue_tile).
   const int xcd = blockIdx.x % NUM_XCD, slot = blockIdx.x / NUM_XCD, slots = gridDim.x / NUM_XCD;
   __shared__ int wave_sum[S::NT / 64];
   int tile, step, end, chunk = a.chunk;
+  __shared__ int taken;
   if constexpr (FORM == FORM_TN) {
-    chunk = __builtin_amdgcn_readfirstlane(safe_chunk<S::NT>(a, pre, wave_sum, tid));
-    group_sums<S::NT>(a.groups, pre, wave_sum, tid, [&](int g) {
-      int lo, hi;
-      group_range(a, g, lo, hi);
-      return pieces_of(hi - lo, chunk);
-    });
+    if (a.queue) {
+      chunk = a.queue[QUEUE_CHUNK];
+      for (int g = tid; g <= a.groups; g += S::NT) pre[g] = a.queue[QUEUE_PRE + g];
+      __syncthreads();
+    } else {
+      chunk = __builtin_amdgcn_readfirstlane(safe_chunk<S::NT>(a, pre, wave_sum, tid));
+      group_sums<S::NT>(a.groups, pre, wave_sum, tid, [&](int g) {
+        int lo, hi;
+        group_range(a, g, lo, hi);
+        return pieces_of(hi - lo, chunk);
+      });
+    }
     end = __builtin_amdgcn_readfirstlane(pre[a.groups]) * ((a.m + S::BM - 1) / S::BM) * ((a.n + S::BN - 1) / S::BN);
     tile = xcd * slots + slot;
     step = gridDim.x;
+    if (a.queue) {
+      if (tid == 0) taken = queue_tile(a, xcd, strip_of<S>(a), end);
+      __syncthreads();
+      tile = __builtin_amdgcn_readfirstlane(taken);
+    }
   } else {
     group_sums<S::NT>(a.groups, pre, wave_sum, tid, [&](int g) {
       int lo, hi;
@@ -884,11 +923,23 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[j][i][v] = 0.f;
 
-    const int ntile = tile + step;
-    const bool more = ntile < end;
+    int ntile = tile + step;
+    bool more = ntile < end;
     Tile tn = t;
-    // the next tile's first stage, if there is one
+    // the next tile's first stage, if there is one.  (TN: taken a stage before, and known to
+    // all after a barrier)
+    auto take = [&] {
+      if constexpr (FORM == FORM_TN) {
+        if (a.queue && fresh(tid) == 0) taken = queue_tile(a, blockIdx.x % NUM_XCD, strip_of<S>(a), end);
+      }
+    };
     auto load_next = [&] {
+      if constexpr (FORM == FORM_TN) {
+        if (a.queue) {
+          ntile = __builtin_amdgcn_readfirstlane(taken);
+          more = ntile < end;
+        }
+      }
       if (!more) return;
       tn = tile_at<S, FORM>(a, pre, chunk, ntile);
       load_first(tn);
@@ -926,10 +977,12 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
       };
       // One stage, kt: its MFMAs, the LDS writes of stage kt + 1 and the loads of stage kt + 2.
       // MODE 0: both in this tile; 1: stage kt + 1 is the last one, the loads are the
-      // next tile's first stage; 2: kt is the last one.
+      // next tile's first stage (TN: in the last stage); 2: kt is the last one.
       auto stage = [&](const int kt, auto mode_c) {
         constexpr int MODE = decltype(mode_c)::value;
         constexpr bool LAST = MODE == 1;
+        constexpr int NEXT = FORM == FORM_TN ? 2 : 1;
+        if constexpr (MODE == 1) take();
         if constexpr (S::SINGLE) {
           // On entry F holds the stage's two slabs (the second one's reads may be on their
           // way).  The barriers: every wave has the stage, which may be overwritten; the
@@ -949,7 +1002,7 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
             load_chunks(rp, lp);
             load_chunks(rq, lq);
           }
-          if constexpr (MODE == 1) load_next();
+          if constexpr (MODE == NEXT) load_next();
           if constexpr (MODE != 2) lds_barrier();
           if constexpr (MODE == 0) frags(F[0], 0);
           __builtin_amdgcn_sched_barrier(0);
@@ -985,7 +1038,7 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
             load_chunks(rp, lp);
             load_chunks(rq, lq);
           }
-          if constexpr (MODE == 1) load_next();
+          if constexpr (MODE == NEXT) load_next();
           turn_over();
           multiply(F[1], 0);
           multiply(F[1], 1);
@@ -1023,7 +1076,7 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
         multiply(F[0], 1);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (MODE == 0) load_chunks(rq, lq);
-        if constexpr (MODE == 1) load_next();
+        if constexpr (MODE == NEXT) load_next();
         turn_over();
         multiply(F[1], 0);
         multiply(F[1], 1);
@@ -1036,6 +1089,9 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
 #pragma unroll 1
         for (; kt + 2 < nk; ++kt) stage(kt, std::integral_constant<int, 0>{});
         stage(kt, std::integral_constant<int, 1>{});
+      } else if constexpr (FORM == FORM_TN) {
+        take();
+        lds_barrier();
       } else {
         load_next();
       }

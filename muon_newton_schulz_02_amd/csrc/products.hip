@@ -156,6 +156,57 @@ __global__ __launch_bounds__(RT) void product_sum_kernel(const ProductArgs a) {
   }
 }
 
+// The queue of TN's tiles (ProductPlan): groups by their number of rows, most first, by a
+// bitonic sort.  One workgroup; 5 us for eight groups, 7 for 64: its barriers' latency.
+constexpr int MAX_GROUPS = 2048;
+__global__ __launch_bounds__(RT) void product_order_kernel(const ProductArgs a) {
+  __shared__ uint64_t key[MAX_GROUPS];
+  __shared__ int pre[MAX_GROUPS + 1], rows[MAX_GROUPS];
+  __shared__ int wave_sum[RT / 64];
+  const int tid = threadIdx.x;
+  int32_t* pre_out = a.queue + QUEUE_PRE;
+  int32_t* order_out = pre_out + a.groups + 1;
+  int32_t* slot_out = order_out + a.groups;
+  for (int g = tid; g < a.groups; g += RT) {
+    int lo, hi;
+    group_range(a, g, lo, hi);
+    rows[g] = hi - lo;
+  }
+  // (a thread reads the rows that it wrote)
+  group_sums<RT>(a.groups, pre, wave_sum, tid, [&](int g) { return rows[g]; });
+  const int chunk = pre[a.groups] <= a.rows ? a.chunk : 1 << 30;      // as safe_chunk
+  __syncthreads();
+  if (tid < QUEUE_XCD) a.queue[tid * QUEUE_STEP] = 0;
+  if (tid == 0) a.queue[QUEUE_CHUNK] = chunk;
+  group_sums<RT>(a.groups, pre, wave_sum, tid, [&](int g) { return pieces_of(rows[g], chunk); });
+  int size = 1;
+  while (size < a.groups) size *= 2;
+  for (int g = tid; g < size; g += RT) {
+    if (g < a.groups) slot_out[g] = 2 * (pre[g] - g);
+    key[g] = g < a.groups ? uint64_t(uint32_t(~rows[g])) << 32 | uint32_t(g) : ~uint64_t(0);
+  }
+  __syncthreads();
+  for (int run = 2; run <= size; run *= 2) {
+    for (int apart = run / 2; apart > 0; apart /= 2) {
+      for (int i = tid; i < size / 2; i += RT) {
+        const int x = i / apart * 2 * apart + i % apart, y = x + apart;
+        const uint64_t kx = key[x], ky = key[y];
+        if ((kx > ky) == ((x & run) == 0)) {
+          key[x] = ky;
+          key[y] = kx;
+        }
+      }
+      __syncthreads();
+    }
+  }
+  group_sums<RT>(a.groups, pre, wave_sum, tid, [&](int i) { return pieces_of(int(~uint32_t(key[i] >> 32)), chunk); });
+  for (int i = tid; i < a.groups; i += RT) {
+    order_out[i] = int(uint32_t(key[i]));
+    pre_out[i] = pre[i];
+  }
+  if (tid == 0) pre_out[a.groups] = pre[a.groups];
+}
+
 template <int FORM>
 hipError_t launch_sum(const ProductArgs& a, int cus, hipStream_t stream) {
   const int64_t rows = FORM == FORM_TN ? a.m : std::max(1, a.rows / a.groups);
@@ -204,22 +255,23 @@ ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus) {
   // 16-byte loads (product_tile.h)
   if (a.p_elems * esz < 16 || a.q_elems * esz < 16 || (form == FORM_TN && a.ld_p * esz < 16) ||
       (form != FORM_NT && a.ld_q * esz < 16))
-    return {SHAPE_NAIVE, 0, 0};
+    return {SHAPE_NAIVE, 0, 0, 0};
   // few rows: Q's way from memory is all (a launch takes fewer than 2^32 threads)
   if (form == FORM_NT && epi != EPI_DZ && a.k % (16 / esz) == 0 && a.rows <= STREAM_ROWS * std::max(1, a.groups) &&
       (epi != EPI_STORE || (!a.add && !a.map && a.out_f32 == a.f32)) &&
       ceil_div(a.n, STREAM_TILE_N) * (a.rows / 16 + std::min(a.groups, a.rows)) <= (1 << 22))
-    return {SHAPE_STREAM, 0, 0};
+    return {SHAPE_STREAM, 0, 0, 0};
   const bool tn = form == FORM_TN;
   const Kind* kinds = a.f32 ? (tn ? KINDS_F32_TN : KINDS_F32) : (tn ? KINDS_TN : KINDS);
   const int nkinds = tn ? 2 : 3;
   const int64_t groups = std::max(1, a.groups);
-  ProductPlan best = {kinds[0].shape, 1 << 30, 0};
+  const size_t queue = (size_t(QUEUE_PRE) + 3 * size_t(groups) + 1 + 63) / 64 * 256;
+  ProductPlan best = {kinds[0].shape, 1 << 30, 0, 0};
   double least = 1e30;
-  auto offer = [&](int shape, int64_t chunk, size_t bytes, double us) {
+  auto offer = [&](int shape, int64_t chunk, size_t bytes, double us, bool queued) {
     if (bytes > (size_t(2) << 30) || us >= least) return;
     least = us;
-    best = {shape, int32_t(chunk), bytes};
+    best = {shape, int32_t(chunk), bytes + (queued ? queue : 0), queued ? queue : 0};
   };
   for (int i = 0; i < nkinds; ++i) {
     const Kind& s = kinds[i];
@@ -230,13 +282,13 @@ ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus) {
                                      : std::max<int64_t>(std::min<int64_t>(groups, a.rows), a.rows / s.bm + groups / 2);
       const int64_t stages = ceil_div(a.k, ke);
       if (mt * nt > (int64_t(1) << 30)) continue;        // tiles are counted in 31 bits
-      offer(s.shape, 1 << 30, 0, tiles_us(s, double(mt * nt), double(stages), cus));
+      offer(s.shape, 1 << 30, 0, tiles_us(s, double(mt * nt), double(stages), cus), false);
       for (int cut = 2; cut <= 32 && epi == EPI_STORE && mt * nt < 2 * cus * s.per_cu; ++cut) {
         const int64_t each = ceil_div(stages, cut);
         if (each < 4) break;
         if (ceil_div(stages, each) != cut) continue;
         const size_t bytes = size_t(cut) * size_t(a.rows) * size_t(part_ld(a.n)) * 4;
-        offer(s.shape, each * ke, bytes, tiles_us(s, double(mt * nt * cut), double(each), cus) + 3.0 + 2e-6 / 5.0 * double(bytes));
+        offer(s.shape, each * ke, bytes, tiles_us(s, double(mt * nt * cut), double(each), cus) + 3.0 + 2e-6 / 5.0 * double(bytes), false);
       }
     } else {
       // Groups of very different lengths: on average a tile has `stages` stages, but one
@@ -250,10 +302,20 @@ ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus) {
         const int64_t longest = std::min(groups > 1 ? all / 2 + 1 : std::max<int64_t>(all, 1), ceil_div(chunk, ke));
         const int64_t pieces = cut ? a.rows / chunk : 0;
         const double count = tiles + double(pieces * mt * nt), each = cut || groups > 1 ? (tiles * stages) / count : stages;
-        double us = std::max(tiles_us(s, count, each, cus), double(longest) * s.alone + s.ends);
         const size_t bytes = 2 * size_t(pieces) * size_t(a.m) * size_t(part_ld(a.n)) * 4;
-        if (cut) us += 5.0 + 1e-6 / 5.0 * double(bytes);
-        offer(s.shape, chunk, bytes, us);
+        const double sums = cut ? 5.0 + 1e-6 / 5.0 * double(bytes) : 0.0, alone = double(longest) * s.alone + s.ends;
+        // A queue keeps every workgroup busy until the last tiles, and costs a launch and
+        // what an idle GPU takes to start (12 us).  Without one, groups whose lengths differ
+        // leave some workgroups waiting: 15 % in the middle.  (16384 rows to 32 groups of 1536
+        // x 1536, shares e^N(0, 1): 147 us without, 113 with; to eight groups of 1536 x 6144:
+        // shares e^N(0, 1) 368 to 435 and 332 to 427, e^N(0, 2) 388 to 427 and 315 to 340,
+        // equal shares 315 and 330.)
+        const double slots = double(cus) * s.per_cu;
+        if (groups > 1 && count > slots)
+          offer(s.shape, chunk, bytes, 12.0 + sums + std::max(count / slots * (each * s.stage + s.ends) + 0.3 * each * s.stage, alone), true);
+        double us = sums + std::max(tiles_us(s, count, each, cus), alone);
+        if (groups > 1 && count > slots) us *= 1.15;
+        offer(s.shape, chunk, bytes, us, false);
       }
     }
   }
@@ -274,12 +336,18 @@ hipError_t launch_product(int form, int epi, const ProductArgs& args, int cus, c
   ProductArgs a = args;
   if (plan.shape != SHAPE_NAIVE) {
     a.chunk = plan.chunk;
-    a.part = reinterpret_cast<float*>(ws);
+    a.queue = plan.queue ? reinterpret_cast<int32_t*>(ws) : nullptr;
+    a.part = reinterpret_cast<float*>(ws + plan.queue);
     const int kind = a.cap == 0.f ? epi : epi == EPI_LSE ? EPI_LSE_CAP : epi == EPI_DZ ? EPI_DZ_CAP : epi;
     if (plan.shape == SHAPE_STREAM) return launch_stream(kind, a, stream);
+    if (plan.queue) {
+      hipLaunchKernelGGL(product_order_kernel, dim3(1), dim3(RT), 0, stream, a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
     hipError_t e = form == FORM_NT   ? launch_nt(plan.shape, kind, a, cus, stream)
                    : form == FORM_NN ? launch_nn(plan.shape, a, cus, stream) : launch_tn(plan.shape, a, cus, stream);
-    if (e == hipSuccess && plan.bytes)
+    if (e == hipSuccess && plan.bytes > plan.queue)
       e = form == FORM_TN ? launch_sum<FORM_TN>(a, cus, stream) : launch_sum<FORM_NT>(a, cus, stream);
     return e;
   }

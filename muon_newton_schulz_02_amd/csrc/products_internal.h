@@ -41,6 +41,8 @@ struct ProductArgs {
   int32_t m, n, k;             // m: TN; k: NT and NN
   int32_t chunk;               // k values of a tile at most (STORE only; see ProductPlan)
   float* part;                 // partial tiles of what is cut along k
+  int32_t* queue;              // TN: the tiles in the order of product_order_kernel, taken as
+                               // workgroups come free; null: every workgroup has its own
   int32_t f32;                 // type of p and q: 1 binary32, 0 bfloat16
   int32_t out_f32, add_f32;
   // head
@@ -78,9 +80,14 @@ constexpr int STREAM_TILE_N = 32;
 struct ProductPlan {
   int shape;
   int32_t chunk;               // k of a chunk, whole stages
-  size_t bytes;                // of partial sums: workspace that launch_product needs
+  size_t bytes;                // workspace that launch_product needs: partial sums,
+  size_t queue;                // and these bytes before them (ProductArgs::queue)
 };
 ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus);
+// The queue, in int32_t: NUM_XCD counters of tiles taken, QUEUE_STEP apart (a line of
+// memory each), the chunk, then pre[groups + 1] (sums of pieces, the groups with most rows
+// first), order[groups] and slot[groups] (2 s_g).
+constexpr int QUEUE_XCD = 8, QUEUE_STEP = 32, QUEUE_CHUNK = QUEUE_XCD * QUEUE_STEP, QUEUE_PRE = QUEUE_CHUNK + 1;
 constexpr int64_t part_ld(int64_t n) { return (n + 3) / 4 * 4; }
 
 // Columns of a tile of `stats` that launch_product writes.

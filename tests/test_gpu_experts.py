@@ -188,6 +188,82 @@ def test_many_experts():
     run_all(counts, 24, 40, "bf16")
 
 
+def many_lengths(experts, seed, long):
+    """Counts of which most are below 40, some nothing, and some long."""
+    rng = np.random.default_rng(seed)
+    counts = rng.integers(0, 40, experts)
+    counts[rng.integers(0, experts, experts // 10)] = 0
+    counts[rng.integers(0, experts, len(long))] = long
+    return counts.tolist()
+
+
+# (counts, in, out): more tiles than workgroups, in numbers of experts around powers of two,
+# equal and unequal lengths, and long ones among them
+QUEUED = [
+    (many_lengths(700, 0, [700, 300]), 300, 260),
+    (many_lengths(1025, 1, []), 136, 260),
+    ([9] * 1024, 257, 129),
+    (many_lengths(2047, 2, [1, 900]), 130, 70),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,inn,out", QUEUED)
+def test_weight_gradients_of_many_experts(counts, inn, out, dtype):
+    """Tiles taken as workgroups come free, the longest sums first."""
+    x, w, off, gy, y, gx, gw = run_all(counts, inn, out, dtype, spare=5, pad=1)
+    first = gw.clone()
+    args = mb.ExpertsVjpArgs(x, None, off, gy, None, first)
+    assert args.workspace_bytes() > 4 * 3 * len(counts)
+    ws = torch.full((args.workspace_bytes(),), 255, dtype=torch.uint8, device="cuda")
+    mb.muon_experts_product_vjp(args, workspace=ws)
+    # the same bits again, from a replayed graph too, and with other rows for the same experts
+    again = torch.zeros_like(gw)
+    mine = mb.ExpertsVjpArgs(x, None, off, gy, None, again)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        mb.muon_experts_product_vjp(mine, workspace=ws)
+    for turn in range(4):
+        again.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first, again)
+        if turn == 1:
+            off.copy_(offsets_of(counts[::-1]))
+            ws.fill_(171)
+            mb.muon_experts_product_vjp(args, workspace=ws)
+    # ranges that meet, go back and leave the rows
+    bad = torch.from_numpy(np.random.default_rng(5).integers(-9, x.shape[0] + 9, len(counts) + 1).astype(np.int32))
+    bad[1:-1:2] = bad[0:-2:2] + 3
+    xs, gys = np.nan_to_num(np64(x)), np.nan_to_num(np64(gy))
+    x.copy_(torch.nan_to_num(x))
+    gy.copy_(torch.nan_to_num(gy))
+    off.copy_(bad)
+    graph.replay()
+    torch.cuda.synchronize()
+    rows = x.shape[0]
+    for e in range(0, len(counts), 97):
+        lo = min(max(int(bad[e]), 0), rows)
+        hi = max(lo, min(int(bad[e + 1]), rows))
+        want, reach = orc.training.experts_grad_w(xs, gys, [lo, hi])
+        check(again[e:e + 1], want, reach, rows, DTYPES[dtype], f"expert {e}")
+
+
+@pytest.mark.parametrize("dtype,gw_dtype", [("bf16", "f32"), ("f32", "f32")])
+def test_weight_gradients_of_unequal_experts(dtype, gw_dtype):
+    """A few experts with many rows each, one of them with most, cut into pieces or not."""
+    args = None
+    for counts in ([6000, 150, 0, 900], [64, 200, 7, 130, 500, 1, 5000, 90]):
+        x, w, off, gy, y, gx, gw = run_all(counts, 1100, 1300, dtype, gw_dtype=gw_dtype)
+        same = torch.zeros_like(gw)
+        args = mb.ExpertsVjpArgs(x, None, off, gy, None, same)
+        first = gw.clone()
+        mb.muon_experts_product_vjp(mb.ExpertsVjpArgs(x, None, off, gy, None, first))
+        mb.muon_experts_product_vjp(args)
+        assert torch.equal(first, same)
+
+
 @pytest.mark.parametrize("gw_dtype", ["bf16", "f32"])
 def test_gradient_type(gw_dtype):
     run_all([90, 3, 200], 136, 120, "bf16", gw_dtype=gw_dtype)
