@@ -1,4 +1,4 @@
-// C = P Q^T for few rows (up to 32 of a group): bound by reading Q, so nothing is
+// C = P Q^T for few rows (16 of a group at a time): bound by reading Q, so nothing is
 // staged.  A workgroup has 32 columns of C and all of k, each of its eight waves every
 // eighth 128 bytes of it, so that the whole panel of Q (98 KB for 1536 of bfloat16) is
 // asked for at once; the waves' sums meet in LDS.  MFMA fragments come straight from
@@ -17,157 +17,135 @@ namespace {
 typedef float f32x4s __attribute__((ext_vector_type(4)));
 constexpr int SNT = 512, SW = SNT / 64, SBN = 32;
 
-template <bool F32, int RB, int EPI>
+template <bool F32, int EPI>
 __global__ __launch_bounds__(SNT) void product_stream_kernel(const ProductArgs a, const int nt) {
-  constexpr int ESZ = F32 ? 4 : 2, PARTS = F32 ? 3 : 1, U = F32 ? 2 : 3, ROWS = 16 * RB;
+  constexpr int ESZ = F32 ? 4 : 2, PARTS = F32 ? 3 : 1, U = F32 ? 2 : 3, ROWS = 16;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ int wave_sum[SW];
-  float* red = reinterpret_cast<float*>(smem);                 // [wave][row block][512]
-  int* pre = reinterpret_cast<int*>(smem + SW * RB * 512 * 4);
+  float* red = reinterpret_cast<float*>(smem);                 // [wave][512]
+  int* pre = reinterpret_cast<int*>(smem + SW * 512 * 4);
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int u = blockIdx.x / nt, j0 = (blockIdx.x - u * nt) * SBN;
-  int g = 0, i0 = u * ROWS, hi = a.rows;
+  const int u0 = blockIdx.x / nt, j0 = (blockIdx.x - u0 * nt) * SBN, n = a.n - j0;
+  int units = (a.rows + ROWS - 1) / ROWS;
   if (a.offsets) {
     group_sums<SNT>(a.groups, pre, wave_sum, tid, [&](int x) {
       int lo, end;
       group_range(a, x, lo, end);
       return (end - lo + ROWS - 1) / ROWS;
     });
-    if (u >= pre[a.groups]) return;
-    for (int end = a.groups; end - g > 1;) {
-      const int mid = (g + end) / 2;
-      if (pre[mid] <= u) g = mid;
-      else end = mid;
-    }
-    int lo;
-    group_range(a, g, lo, hi);
-    i0 = lo + (u - pre[g]) * ROWS;
+    units = pre[a.groups];
   }
-  const int m = hi - i0, n = a.n - j0;
-  if (m <= 0) return;
-
-  const int r16 = lane & 15, quarter = (lane >> 4) * 16;
-  const char* q[2];
-  const char* p[RB];
-#pragma unroll
-  for (int f = 0; f < 2; ++f)
-    q[f] = reinterpret_cast<const char*>(a.q) + (g * a.es_q + int64_t(min(j0 + 16 * f + r16, a.n - 1)) * a.ld_q) * ESZ;
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
-    p[b] = reinterpret_cast<const char*>(a.p) + int64_t(i0 + min(16 * b + r16, m - 1)) * a.ld_p * ESZ;
-  const int kb = a.k * ESZ, chunks = (kb + 127) / 128;
-  f32x4s acc[2][RB];
-#pragma unroll
-  for (int f = 0; f < 2; ++f)
-#pragma unroll
-    for (int b = 0; b < RB; ++b) acc[f][b] = f32x4s{0.f, 0.f, 0.f, 0.f};
-
-  // both halves of a 128-byte chunk; a piece past the end of k (a multiple of 16 bytes)
-  // is zeros, read from the row's start
-  auto load = [&](const char* row, int c, int h) {
-    const int at = c * 128 + h * 64 + quarter;
-    return *reinterpret_cast<gload16*>((gchar*)(row + (at < kb ? at : 0)));
-  };
-  auto clean = [&](u32x4 v, int c, int h) {
-    const bool in = c * 128 + h * 64 + quarter < kb;
-#pragma unroll
-    for (int d = 0; d < 4; ++d) v[d] = in ? v[d] : 0u;
-    return v;
-  };
-  for (int c0 = w; c0 < chunks; c0 += SW * U) {
-    u32x4 fq[U][2][2], fp[U][RB][2];
-#pragma unroll
-    for (int s = 0; s < U; ++s)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int f = 0; f < 2; ++f) fq[s][f][h] = load(q[f], c0 + s * SW, h);
-#pragma unroll
-        for (int b = 0; b < RB; ++b) fp[s][b][h] = load(p[b], c0 + s * SW, h);
+  // (once, but where groups overlap and have more rows than there are)
+  for (int u = u0; u < units; u += gridDim.x / nt) {
+    if (u != u0) __syncthreads();
+    int g = 0, i0 = u * ROWS, hi = a.rows;
+    if (a.offsets) {
+      for (int end = a.groups; end - g > 1;) {
+        const int mid = (g + end) / 2;
+        if (pre[mid] <= u) g = mid;
+        else end = mid;
       }
+      int lo;
+      group_range(a, g, lo, hi);
+      i0 = lo + (u - pre[g]) * ROWS;
+    }
+    const int m = hi - i0;
+
+    const int r16 = lane & 15, quarter = (lane >> 4) * 16;
+    const char* q[2];
 #pragma unroll
-    for (int s = 0; s < U; ++s) {
-      const int c = c0 + s * SW;
-      if (c >= chunks) continue;
-      if (c == chunks - 1) {
+    for (int f = 0; f < 2; ++f)
+      q[f] = reinterpret_cast<const char*>(a.q) + (g * a.es_q + int64_t(min(j0 + 16 * f + r16, a.n - 1)) * a.ld_q) * ESZ;
+    const char* p = reinterpret_cast<const char*>(a.p) + int64_t(i0 + min(r16, m - 1)) * a.ld_p * ESZ;
+    const int kb = a.k * ESZ, chunks = (kb + 127) / 128;
+    f32x4s acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+
+    // both halves of a 128-byte chunk; a piece past the end of k (a multiple of 16 bytes)
+    // is zeros, read from the row's start
+    auto load = [&](const char* row, int c, int h) {
+      const int at = c * 128 + h * 64 + quarter;
+      return *reinterpret_cast<gload16*>((gchar*)(row + (at < kb ? at : 0)));
+    };
+    auto clean = [&](u32x4 v, int c, int h) {
+      const bool in = c * 128 + h * 64 + quarter < kb;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) v[d] = in ? v[d] : 0u;
+      return v;
+    };
+    for (int c0 = w; c0 < chunks; c0 += SW * U) {
+      u32x4 fq[U][2][2], fp[U][2];
+#pragma unroll
+      for (int s = 0; s < U; ++s)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int f = 0; f < 2; ++f) fq[s][f][h] = clean(fq[s][f][h], c, h);
-#pragma unroll
-          for (int b = 0; b < RB; ++b) fp[s][b][h] = clean(fp[s][b][h], c, h);
+          for (int f = 0; f < 2; ++f) fq[s][f][h] = load(q[f], c0 + s * SW, h);
+          fp[s][h] = load(p, c0 + s * SW, h);
         }
-      }
-      auto mul = [&](f32x4s& d, const u32x4& x, const u32x4& y) {
-        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), d, 0, 0, 0);
-      };
-      if constexpr (!F32) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+      for (int s = 0; s < U; ++s) {
+        const int c = c0 + s * SW;
+        if (c >= chunks) continue;
+        if (c == chunks - 1) {
 #pragma unroll
-          for (int f = 0; f < 2; ++f)
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int b = 0; b < RB; ++b) mul(acc[f][b], fq[s][f][h], fp[s][b][h]);
-      } else {
-        auto split8 = [&](const u32x4 (&v)[2], u32x4 (&o)[PARTS]) {
-          u32x2 x[3], y[3];
-          split4(v[0], x);
-          split4(v[1], y);
-#pragma unroll
-          for (int i = 0; i < PARTS; ++i) o[i] = u32x4{x[i][0], x[i][1], y[i][0], y[i][1]};
+            for (int f = 0; f < 2; ++f) fq[s][f][h] = clean(fq[s][f][h], c, h);
+            fp[s][h] = clean(fp[s][h], c, h);
+          }
+        }
+        auto mul = [&](f32x4s& d, const u32x4& x, const u32x4& y) {
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), d, 0, 0, 0);
         };
-        u32x4 sp[RB][PARTS];
+        if constexpr (!F32) {
 #pragma unroll
-        for (int b = 0; b < RB; ++b) split8(fp[s][b], sp[b]);
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          u32x4 sq[PARTS];
-          split8(fq[s][f], sq);
-          constexpr int QPART[6] = {0, 2, 1, 0, 1, 0}, PPART[6] = {2, 0, 1, 1, 0, 0};
+            for (int f = 0; f < 2; ++f) mul(acc[f], fq[s][f][h], fp[s][h]);
+        } else {
+          auto split8 = [&](const u32x4 (&v)[2], u32x4 (&o)[PARTS]) {
+            u32x2 x[3], y[3];
+            split4(v[0], x);
+            split4(v[1], y);
 #pragma unroll
-          for (int x = 0; x < 6; ++x)
+            for (int i = 0; i < PARTS; ++i) o[i] = u32x4{x[i][0], x[i][1], y[i][0], y[i][1]};
+          };
+          u32x4 sp[PARTS];
+          split8(fp[s], sp);
 #pragma unroll
-            for (int b = 0; b < RB; ++b) mul(acc[f][b], sq[QPART[x] % PARTS], sp[b][PPART[x] % PARTS]);
+          for (int f = 0; f < 2; ++f) {
+            u32x4 sq[PARTS];
+            split8(fq[s][f], sq);
+            constexpr int QPART[6] = {0, 2, 1, 0, 1, 0}, PPART[6] = {2, 0, 1, 1, 0, 0};
+#pragma unroll
+            for (int x = 0; x < 6; ++x) mul(acc[f], sq[QPART[x] % PARTS], sp[PPART[x] % PARTS]);
+          }
         }
       }
     }
-  }
-  // lane's acc[f][b][e]: row 16 b + lane % 16, column 16 f + 4 (lane / 16) + e
+    // lane's acc[f][e]: row lane % 16, column 16 f + 4 (lane / 16) + e
 #pragma unroll
-  for (int b = 0; b < RB; ++b)
+    for (int f = 0; f < 2; ++f) *reinterpret_cast<f32x4s*>(red + w * 512 + f * 256 + lane * 4) = acc[f];
+    __syncthreads();
+    float v = 0.f;
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
-      *reinterpret_cast<f32x4s*>(red + (w * RB + b) * 512 + f * 256 + lane * 4) = acc[f][b];
-  __syncthreads();
-  float v[RB];
-#pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    v[b] = 0.f;
-#pragma unroll
-    for (int x = 0; x < SW; ++x) v[b] += red[(x * RB + b) * 512 + tid];
-  }
-  if constexpr (EPI == EPI_STORE) {
-    const int row = (tid % 256) / 4 % 16, col = tid / 256 * 16 + tid % 256 / 64 * 4 + tid % 4;
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-      if (16 * b + row < m && col < n) {
-        const int64_t at = int64_t(i0 + 16 * b + row) * a.ld_out + j0 + col;
-        if constexpr (F32) reinterpret_cast<float*>(a.out)[at] = v[b];
-        else reinterpret_cast<uint16_t*>(a.out)[at] = float_to_bf16_bits(v[b]);
+    for (int x = 0; x < SW; ++x) v += red[x * 512 + tid];
+    if constexpr (EPI == EPI_STORE) {
+      const int row = (tid % 256) / 4 % 16, col = tid / 256 * 16 + tid % 256 / 64 * 4 + tid % 4;
+      if (row < m && col < n) {
+        const int64_t at = int64_t(i0 + row) * a.ld_out + j0 + col;
+        if constexpr (F32) reinterpret_cast<float*>(a.out)[at] = v;
+        else reinterpret_cast<uint16_t*>(a.out)[at] = float_to_bf16_bits(v);
       }
-  } else {
-    // a row's 32 columns to half a wave
-    __syncthreads();
-#pragma unroll
-    for (int b = 0; b < RB; ++b) red[b * 512 + tid] = v[b];
-    __syncthreads();
-    const SoftCap cap = soft_cap(a);
-    const int row = tid / 32, col = tid % 32;
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      const float l = red[b * 512 + col / 16 * 256 + (col % 16 / 4 * 16 + row) * 4 + col % 4];
-      const int i = i0 + 16 * b + row;
-      const bool in = 16 * b + row < m && col < n;
+    } else {
+      // a row's 32 columns to half a wave
+      __syncthreads();
+      red[tid] = v;
+      __syncthreads();
+      const SoftCap cap = soft_cap(a);
+      const int row = tid / 32, col = tid % 32, i = i0 + row;
+      const float l = red[col / 16 * 256 + (col % 16 / 4 * 16 + row) * 4 + col % 4];
+      const bool in = row < m && col < n;
       const float y = !in ? -INFINITY : EPI == EPI_LSE_CAP ? capped_y<F32>(l, cap_r(l, cap), cap) : l * LOG2E;
       float mx = y;
 #pragma unroll
@@ -183,28 +161,26 @@ __global__ __launch_bounds__(SNT) void product_stream_kernel(const ProductArgs a
   }
 }
 
-template <bool F32, int RB>
+template <bool F32>
 hipError_t launch_rows(int epi, const ProductArgs& a, hipStream_t stream) {
   const int nt = (a.n + SBN - 1) / SBN;
-  const int64_t grid = int64_t(nt) * (a.rows / (16 * RB) + std::min(a.groups, a.rows));
-  const size_t lds = SW * RB * 512 * 4 + (size_t(a.groups) + 1) * 4;
+  const int64_t grid = int64_t(nt) * (a.rows / 16 + std::min(a.groups, a.rows));
+  const size_t lds = SW * 512 * 4 + (size_t(a.groups) + 1) * 4;
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(SNT), lds, stream, a, nt);
     return hipGetLastError();
   };
   switch (epi) {
-    case EPI_LSE: return go(product_stream_kernel<F32, RB, EPI_LSE>);
-    case EPI_LSE_CAP: return go(product_stream_kernel<F32, RB, EPI_LSE_CAP>);
-    default: return go(product_stream_kernel<F32, RB, EPI_STORE>);
+    case EPI_LSE: return go(product_stream_kernel<F32, EPI_LSE>);
+    case EPI_LSE_CAP: return go(product_stream_kernel<F32, EPI_LSE_CAP>);
+    default: return go(product_stream_kernel<F32, EPI_STORE>);
   }
 }
 
 }  // namespace
 
 hipError_t launch_stream(int epi, const ProductArgs& a, hipStream_t stream) {
-  const bool one = a.rows / std::max(1, a.groups) <= 16 && (a.groups > 1 || a.rows <= 16);
-  if (a.f32) return one ? launch_rows<true, 1>(epi, a, stream) : launch_rows<true, 2>(epi, a, stream);
-  return one ? launch_rows<false, 1>(epi, a, stream) : launch_rows<false, 2>(epi, a, stream);
+  return a.f32 ? launch_rows<true>(epi, a, stream) : launch_rows<false>(epi, a, stream);
 }
 
 }  // namespace muon

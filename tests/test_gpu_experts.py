@@ -128,6 +128,19 @@ def test_few_rows(inn, out, counts, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_few_rows_in_ranges_that_overlap(dtype):
+    """Ranges with many times the rows that there are, before the one range of a row's own: it is right there."""
+    dt = DTYPES[dtype]
+    gen = torch.Generator().manual_seed(17)
+    x, w = matrix(160, 72, dt, gen), stack(24, 40, 72, dt, gen)
+    off = torch.tensor([0, 150] * 12 + [160], dtype=torch.int32, device="cuda")
+    y = torch.full((160, 40), float("nan"), dtype=dt, device="cuda")
+    mb.muon_experts_product(x, w, off, y)
+    want, reach = orc.training.experts(np64(x)[150:], np64(w)[23:], [0, 10])
+    check(y[150:], want, reach, 72, dt, "the last expert's rows")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_products_cut_along_k(dtype):
     """Few tiles and a long sum: partial sums in a workspace, added in order."""
     dt = DTYPES[dtype]
