@@ -30,7 +30,7 @@
  *     [0, vocab) gives loss = lse = NaN, and a row that takes no part in the
  *     gradients either (its grad_x is 0).
  *   - bfloat16: logits, their softmax and all sums are binary32; dl is rounded
- *     to bfloat16 for the two products (relative 2^-9, independent from
+ *     to bfloat16 for the two products (relative 2^-8 at most, independent from
  *     element to element, as the rounding of the results).  binary32: to
  *     binary32 accuracy throughout.
  *   - A row with a NaN or an infinity among its logits has the values that the

@@ -497,10 +497,10 @@ struct Patch {
 
 // C to `out` through LDS, a part of the tile's rows at a time where all do not fit ROOM
 // bytes.  OF32: out is binary32.  WIDE: staged as binary32 (for binary32 outputs and
-// addends), else as bfloat16.
-template <class S, bool OF32, bool WIDE, int ROOM>
+// addends), else as bfloat16.  Multiplied by `unit`.
+template <class S, bool OF32, bool WIDE, int ROOM, bool UNIT = false>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], const Out& out, bool add_f32, const Tile& t, char* stg, int tid,
-                                           const Patch<S>* patch = nullptr) {
+                                           const Patch<S>* patch = nullptr, float unit = 1.f) {
   constexpr int ES = WIDE ? 4 : 2, EP = S::BN * ES + 16;
   constexpr int PASSES = S::BM * EP <= ROOM ? 1 : S::BM / 2 * EP <= ROOM ? 2 : S::BM / 4 * EP <= ROOM ? 4 : 8;
   constexpr int ROWS = S::BM / PASSES;
@@ -517,6 +517,8 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], co
 #pragma unroll 1
   for (int pass = 0; pass < PASSES; ++pass) {
     if (pass > 0) lds_barrier();
+    float factor = unit;
+    if (UNIT) asm volatile("" : "+v"(factor));      // a product of every accumulator would not fit the registers
     char* const lane_at = stg + (lane & 31) * EP + (wq * S::WTQ + 4 * half) * ES;
 #pragma unroll
     for (int i = 0; i < S::FP; ++i) {
@@ -528,10 +530,11 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], co
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             char* d = at + (32 * j + 8 * g) * ES;
-            const f32x16& c = acc[j][i];
-            if constexpr (WIDE) *reinterpret_cast<f32x4*>(d) = f32x4{c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
-            else *reinterpret_cast<u32x2*>(d) = u32x2{float2_to_bf16x2_bits(c[4 * g], c[4 * g + 1]),
-                                                      float2_to_bf16x2_bits(c[4 * g + 2], c[4 * g + 3])};
+            float c[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[e] = UNIT ? acc[j][i][4 * g + e] * factor : acc[j][i][4 * g + e];
+            if constexpr (WIDE) *reinterpret_cast<f32x4*>(d) = f32x4{c[0], c[1], c[2], c[3]};
+            else *reinterpret_cast<u32x2*>(d) = u32x2{float2_to_bf16x2_bits(c[0], c[1]), float2_to_bf16x2_bits(c[2], c[3])};
             if (g == 3) __builtin_amdgcn_sched_barrier(0);   // else all are rounded before any is stored
           }
         // after this lane's own write of the column, in order
@@ -589,7 +592,11 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], co
 }
 
 // Every row's maximum and sum of exponentials over the tile's columns, and the
-// target's logit.
+// target's logit: 8 bytes a row and tile go to memory instead of its logits.  A lane has
+// 64 of a row's 256 columns (FQ 16-column parts of its wave's, a half of each), so its
+// reductions are registers, one exchange between half-waves and four values in LDS.  Some
+// 12 instructions a logit with a soft cap (two exponentials, a reciprocal), 4 without:
+// 8192 x 1536 by 32768 786 us and 755.
 template <class S, bool CAP>
 __device__ __forceinline__ void lse_tile(f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t, char* smem,
                                          int tid) {
@@ -660,7 +667,8 @@ __device__ __forceinline__ void lse_tile(f32x16 (&acc)[S::FQ][S::FP], const Prod
 }
 
 // The logits become the loss's gradient with respect to them, but for the target's
-// column, which goes to `patch`.
+// column, which goes to `patch`.  From lse it is one exponential a logit; 8192 x 1536 by
+// 32768 with a soft cap 780 us, 512 MB of gradients written.
 template <class S, bool CAP>
 __device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t, int tid,
                                               Patch<S>& patch) {
@@ -668,11 +676,12 @@ __device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const
   const int lane = tt & 63, w = tt >> 6, wq = w % S::WN, wp = w / S::WN;
   const int c0 = wq * S::WTQ + 4 * (lane >> 5);
   const SoftCap cap = soft_cap(a);
+  const float per_unit = S::F32 ? 1.f : 1.f / *a.unit;
 #pragma unroll
   for (int i = 0; i < S::FP; ++i) {
     const int r = min(wp * S::WTP + 32 * i + (lane & 31), t.m - 1) + t.i0;
     const int target = target_of(a, r) - t.j0;
-    const float lse = a.lse[r] * LOG2E, ga = a.ga[r];
+    const float lse = a.lse[r] * LOG2E, ga = a.ga[r] * per_unit;
     const bool mine = target >= wq * S::WTQ && target < (wq + 1) * S::WTQ && ((target >> 2) & 1) == (lane >> 5);
     patch.col[i] = mine ? target : -1;
     patch.value[i] = 0.f;
@@ -684,9 +693,9 @@ __device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const
         for (int v = 0; v < 16; ++v) l = target == c0 + 32 * j + 8 * (v >> 2) + (v & 3) ? acc[j][i][v] : l;
       if constexpr (CAP) {
         const float q = cap_r(l, cap);
-        patch.value[i] = (ga * __builtin_amdgcn_exp2f(capped_y<S::F32>(l, q, cap) - lse) - a.gb[r]) * cap_slope(q);
+        patch.value[i] = (ga * __builtin_amdgcn_exp2f(capped_y<S::F32>(l, q, cap) - lse) - a.gb[r] * per_unit) * cap_slope(q);
       } else {
-        patch.value[i] = ga * __builtin_amdgcn_exp2f(__builtin_fmaf(l, LOG2E, -lse)) - a.gb[r];
+        patch.value[i] = ga * __builtin_amdgcn_exp2f(__builtin_fmaf(l, LOG2E, -lse)) - a.gb[r] * per_unit;
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -1111,9 +1120,14 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
     } else {
       const Out out = out_of<FORM>(a, t);
       if constexpr (S::F32) store_tile<S, true, true, LY::BYTES>(acc, out, a.add_f32, t, smem, tid);
-      else if (a.out_f32 || t.part >= 0) store_tile<S, true, true, LY::BYTES>(acc, out, a.add_f32, t, smem, tid);
-      else if (a.add) store_tile<S, false, true, LY::BYTES>(acc, out, a.add_f32, t, smem, tid);
-      else store_tile<S, false, false, LY::BYTES>(acc, out, false, t, smem, tid);
+      else {
+        float unit = 1.f;
+        constexpr bool UNIT = FORM != FORM_NT;
+        if (UNIT && a.unit && t.part < 0) unit = *a.unit;
+        if (a.out_f32 || t.part >= 0) store_tile<S, true, true, LY::BYTES, UNIT>(acc, out, a.add_f32, t, smem, tid, nullptr, unit);
+        else if (a.add) store_tile<S, false, true, LY::BYTES, UNIT>(acc, out, a.add_f32, t, smem, tid, nullptr, unit);
+        else store_tile<S, false, false, LY::BYTES, UNIT>(acc, out, false, t, smem, tid, nullptr, unit);
+      }
     }
     if (!more) break;
     lds_barrier();
@@ -1154,6 +1168,17 @@ hipError_t launch_shape(const ProductArgs& a, int cus, hipStream_t stream) {
   return whole ? launch_whole<S, FORM, EPI, true>(a, cus, stream) : launch_whole<S, FORM, EPI, false>(a, cus, stream);
 }
 
+// The shapes.  A stage of 256 x 256 needs half the loads and LDS reads a product of 128 x
+// 128, and one workgroup of it fills a compute unit's registers (128 accumulators a lane)
+// and LDS; the matrix cores are busy half the time at 1.7 to 2.0 GHz, to which their load
+// brings the clock.  The smaller ones are for what does not fill the GPU with these.
+//   bfloat16, 8192 rows, 1536 and 32768: logits (NT) 755 us, 1.09 PFLOP/s (tiles of 128
+//   x 128 896); dl W (NN, cut in four) 730 to 770 with the sums; dl^T x (TN) 690, 1.19
+//   16384 rows of eight groups, 1536 and 6144: NT 266 to 320 us by the groups' last tiles
+//   binary32, 1024 rows, 768 and 10007: TN 67 us, 128 x 128 tiles 75; 193 to 211 TFLOP/s of
+//   binary32 products, 1.16 to 1.27 PFLOP/s of the bfloat16 ones they are made of
+// Medium: 1337 x 333 to 20011 of 60 % ignored rows, NN 24 us; Small (32 rows): 634 rows of 42 by
+// 6457 20.6 us, Medium 20.1, Large 26.
 using Large = Shape<256, 256, 2, 4, false>;
 using Medium = Shape<128, 128, 2, 2, false>;
 using MediumTn = Shape<128, 256, 2, 4, false>;

@@ -54,6 +54,8 @@ struct ProductArgs {
   const float* lse;
   const float* ga;             // grad_loss + grad_lse
   const float* gb;             // grad_loss
+  // STORE of NN and TN: what C is multiplied by, DZ: divided by, or null (HeadRows::unit)
+  const float* unit;
   float* logit;                // the target's logit (soft-capped)
   float2* stats;               // [row][tile], with y = z log2 e: maximum of y, sum of 2^(y - maximum)
 };
@@ -111,6 +113,12 @@ struct HeadRows {
   float* lse_c;
   float* ga;
   float* gb;
+  // bfloat16 gradient: the significand of the first row's grad_loss, in [1, 2).  Gradients of
+  // the logits are kept in this unit: with one grad_loss for all rows (a mean's) the
+  // target's element, the largest by far, is then just below a power of two, where
+  // bfloat16's steps are finest relative to it, instead of wherever grad_loss puts it for
+  // all rows at once (1859 rows of 24 by 1815: grad_x 2.1e-3 from float64, not 2.6e-3).
+  float* unit;
   float* loss;                 // forward: written where there is no target
   float* lse_out;
   void* grad_x;                // gradient: zeroed where there is no target; may be null

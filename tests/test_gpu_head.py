@@ -165,6 +165,40 @@ def test_gradient_against_differences():
         assert abs((value(*up)[0] - value(*down)[0]) / (2 * h) - (grad.double() * d.double()).sum().item()) < 3e-3
 
 
+@pytest.mark.parametrize("g", [1.0 + 2.0 ** -8 + 2.0 ** -12, -(1.0 + 2.0 ** -8 + 2.0 ** -12) / 4096, 1.0 / 1859, 2.0 ** -120 * 1.99, 0.0])
+@pytest.mark.parametrize("first", [0, 3])
+def test_one_gradient_of_the_loss_for_all_rows_is_not_rounded(g, first):
+    """bfloat16.  With small logits p is below 2^-11 and the target's element is -g (1 - p).  Rounded as it is, it
+    could be 2^-8 off for all rows alike (the first g here: 2^-8 - 2^-12); in units of g's significand it is -1 or
+    next below, off by p or less.  The scale of the result, <got, want> / <want, want>, then is off by 2^-11, and by
+    the roundings of 300 x 64 results (and 64 x as many of grad_w's): 2^-8 each at most, independent, 2^-8 / sqrt(19200)
+    = 3e-5 together, of which ten times are allowed."""
+    gen = torch.Generator().manual_seed(21)
+    rows, dim, vocab = 300, 64, 5000
+    x, w = matrix(rows, dim, torch.bfloat16, gen, scale=0.05), matrix(vocab, dim, torch.bfloat16, gen, scale=dim ** -0.5)
+    t = torch.randint(vocab, (rows,), generator=gen).cuda()
+    t[:first] = -100                       # the first rows take no part
+    grad = torch.full((rows,), g, device="cuda")
+    grad[:first] = float("nan")
+    loss, lse = torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda")
+    gx, gw = torch.zeros_like(x), torch.zeros_like(w)
+    mb.muon_head_loss(x, w, t, loss, lse)
+    mb.muon_head_loss_vjp(x, w, t, lse, grad, gx, gw)
+    seen = (t >= 0).cpu().numpy()
+    at = t.cpu().numpy()[seen]
+    xd, wd = np64(x)[seen], np64(w)
+    d = np.exp(xd @ wd.T - np64(lse)[seen, None])
+    assert d.max() < 2.0 ** -11
+    d[np.arange(len(at)), at] -= 1
+    unit = np.float64(np.float32(g))
+    for got, want in ((np64(gx)[seen], unit * (d @ wd)), (np64(gw), unit * (d.T @ xd))):
+        if g == 0.0:
+            assert (got == 0).all()
+        else:
+            scale = (got / unit * (want / unit)).sum() / np.square(want / unit).sum()
+            assert abs(scale - 1) < 2.0 ** -11 + 3e-4
+
+
 def test_one_gradient_at_a_time_is_the_same():
     x, w, t, lse, g, h, gx, gw = case(130, 96, 1500, "bf16", ignored=0.2)
     a, b = torch.zeros_like(gx), torch.zeros_like(gw)
