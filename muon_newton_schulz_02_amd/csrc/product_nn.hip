@@ -9,6 +9,7 @@ hipError_t launch_nn(int shape, const ProductArgs& a, int cus, hipStream_t strea
     return shape == SHAPE_SMALL ? launch_shape<SmallF32, FORM_NN, EPI_STORE>(a, cus, stream)
                                 : launch_shape<MediumF32, FORM_NN, EPI_STORE>(a, cus, stream);
   if (shape == SHAPE_SMALL) return launch_shape<Small, FORM_NN, EPI_STORE>(a, cus, stream);
+  if (shape == SHAPE_NARROW) return launch_shape<Narrow, FORM_NN, EPI_STORE>(a, cus, stream);
   if (shape == SHAPE_MEDIUM) return launch_shape<Medium, FORM_NN, EPI_STORE>(a, cus, stream);
   return launch_shape<Large, FORM_NN, EPI_STORE>(a, cus, stream);
 }

@@ -14,6 +14,7 @@ hipError_t launch_nt(int shape, int epi, const ProductArgs& a, int cus, hipStrea
       default: return launch_shape<S, FORM_NT, EPI_STORE>(a, cus, stream);
     }
   };
+  if (shape == SHAPE_NARROW) return launch_shape<Narrow, FORM_NT, EPI_STORE>(a, cus, stream);
   if (a.f32) return shape == SHAPE_SMALL ? with(SmallF32{}) : shape == SHAPE_MEDIUM ? with(MediumF32{}) : with(LargeF32{});
   return shape == SHAPE_SMALL ? with(Small{}) : shape == SHAPE_MEDIUM ? with(Medium{}) : with(Large{});
 }

@@ -1177,12 +1177,14 @@ hipError_t launch_shape(const ProductArgs& a, int cus, hipStream_t stream) {
 //   16384 rows of eight groups, 1536 and 6144: NT 266 to 320 us by the groups' last tiles
 //   binary32, 1024 rows, 768 and 10007: TN 67 us, 128 x 128 tiles 75; 193 to 211 TFLOP/s of
 //   binary32 products, 1.16 to 1.27 PFLOP/s of the bfloat16 ones they are made of
+// Narrow (128 x 64, four waves, two workgroups a unit) is for few columns (Kind).
 // Medium: 1337 x 333 to 20011 of 60 % ignored rows, NN 24 us; Small (32 rows): 634 rows of 42 by
 // 6457 20.6 us, Medium 20.1, Large 26.
 using Large = Shape<256, 256, 2, 4, false>;
 using Medium = Shape<128, 128, 2, 2, false>;
 using MediumTn = Shape<128, 256, 2, 4, false>;
 using Small = Shape<32, 128, 1, 4, false>;
+using Narrow = Shape<128, 64, 2, 2, false>;
 using LargeF32 = Shape<256, 128, 4, 2, true>;
 using MediumF32 = Shape<128, 128, 2, 4, true>;
 using SmallF32 = Shape<32, 128, 1, 4, true>;

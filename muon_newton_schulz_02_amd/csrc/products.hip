@@ -237,10 +237,17 @@ struct Kind {
   int shape, bm, bn, per_cu;
   double stage, alone, ends;
 };
+// The narrow shape, for few columns: TN dl^T x of 2341 x 15034 and 25 33 us (52 without it), 2868
+// x 18624 and 97 43 (54), 8192 x 32768 and 64 107 (161); NN and NT, where it is taken up to its 64
+// columns (beyond them it lost up to a tenth): 16384 rows of eight groups, 4096 to 64 37 (44), 3394
+// rows of three, 4291 to 45 25 (32).
 constexpr Kind KINDS[] = {{SHAPE_LARGE, 256, 256, 1, 1.80, 1.10, 9.0},
                           {SHAPE_MEDIUM, 128, 128, 2, 1.10, 0.54, 7.0},
-                          {SHAPE_SMALL, 32, 128, 3, 0.88, 0.43, 5.0}};
-constexpr Kind KINDS_TN[] = {{SHAPE_LARGE, 256, 256, 1, 1.72, 1.15, 11.0}, {SHAPE_MEDIUM, 128, 256, 1, 0.98, 0.72, 8.0}};
+                          {SHAPE_SMALL, 32, 128, 3, 0.88, 0.43, 5.0},
+                          {SHAPE_NARROW, 128, 64, 2, 0.63, 0.40, 5.0}};
+constexpr Kind KINDS_TN[] = {{SHAPE_LARGE, 256, 256, 1, 1.72, 1.15, 11.0},
+                             {SHAPE_MEDIUM, 128, 256, 1, 0.98, 0.72, 8.0},
+                             {SHAPE_NARROW, 128, 64, 2, 0.63, 0.40, 5.0}};
 constexpr Kind KINDS_F32[] = {{SHAPE_LARGE, 256, 128, 1, 2.58, 2.05, 7.0},
                               {SHAPE_MEDIUM, 128, 128, 1, 1.42, 1.10, 5.0},
                               {SHAPE_SMALL, 32, 128, 2, 1.10, 0.70, 5.0}};
@@ -267,7 +274,7 @@ ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus) {
     return {SHAPE_STREAM, 0, 0, 0};
   const bool tn = form == FORM_TN;
   const Kind* kinds = a.f32 ? (tn ? KINDS_F32_TN : KINDS_F32) : (tn ? KINDS_TN : KINDS);
-  const int nkinds = tn ? 2 : 3;
+  const int nkinds = a.f32 ? (tn ? 2 : 3) : tn ? 3 : epi == EPI_STORE ? 4 : 3;
   const int64_t groups = std::max(1, a.groups);
   const size_t queue = (size_t(QUEUE_PRE) + 3 * size_t(groups) + 1 + 63) / 64 * 256;
   ProductPlan best = {kinds[0].shape, 1 << 30, 0, 0};
@@ -279,6 +286,7 @@ ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus) {
   };
   for (int i = 0; i < nkinds; ++i) {
     const Kind& s = kinds[i];
+    if (s.shape == SHAPE_NARROW && !tn && a.n > s.bn) continue;
     const int64_t nt = ceil_div(a.n, s.bn);
     if (!tn) {
       // tiles of rows: a group's rows fill all but half of its last one

@@ -61,7 +61,7 @@ struct ProductArgs {
 };
 
 // Tile shapes.
-enum ProductShape : int { SHAPE_NAIVE = 0, SHAPE_SMALL = 1, SHAPE_MEDIUM = 2, SHAPE_LARGE = 3, SHAPE_STREAM = 4 };
+enum ProductShape : int { SHAPE_NAIVE = 0, SHAPE_SMALL = 1, SHAPE_MEDIUM = 2, SHAPE_LARGE = 3, SHAPE_NARROW = 4, SHAPE_STREAM = 5 };
 hipError_t launch_nt(int shape, int epi, const ProductArgs& a, int cus, hipStream_t stream);
 hipError_t launch_nn(int shape, const ProductArgs& a, int cus, hipStream_t stream);
 hipError_t launch_tn(int shape, const ProductArgs& a, int cus, hipStream_t stream);

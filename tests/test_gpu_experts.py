@@ -141,6 +141,16 @@ def test_few_rows_in_ranges_that_overlap(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,inn,out", [
+    ([700, 0, 900, 5], 24, 700), ([1200, 1100], 63, 257), ([900, 900, 131], 700, 64), ([500, 1, 600], 129, 33),
+    ([2000], 64, 64), ([1500], 65, 31),
+])
+def test_few_columns(counts, inn, out, dtype):
+    run_all(counts, inn, out, dtype, spare=2, pad=1)
+    run_all(counts, inn, out, dtype, order=mb.WEIGHT_IN_OUT, gw_dtype="f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_products_cut_along_k(dtype):
     """Few tiles and a long sum: partial sums in a workspace, added in order."""
     dt = DTYPES[dtype]
