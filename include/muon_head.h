@@ -35,6 +35,9 @@
  *     binary32 accuracy throughout.
  *   - A row with a NaN or an infinity among its logits has the values that the
  *     formulas give, NaN or infinite, and so have gradients that it takes part in.
+ *     (Soft-capped) logits from 2^127 on in magnitude count as infinite.
+ *   - The soft cap itself is off by 2^-21 cap at most, and by 18 2^-24 of the logit
+ *     (bfloat16: with caps above 32), however large the cap.
  */
 #ifndef MUON_MI355X_HEAD_H
 #define MUON_MI355X_HEAD_H

@@ -11,6 +11,12 @@ hipError_t launch_nt(int shape, int epi, const ProductArgs& a, int cus, hipStrea
       case EPI_LSE_CAP: return launch_shape<S, FORM_NT, EPI_LSE_CAP>(a, cus, stream);
       case EPI_DZ: return launch_shape<S, FORM_NT, EPI_DZ>(a, cus, stream);
       case EPI_DZ_CAP: return launch_shape<S, FORM_NT, EPI_DZ_CAP>(a, cus, stream);
+      case EPI_LSE_LARGE_CAP:
+        if constexpr (!S::F32) return launch_shape<S, FORM_NT, EPI_LSE_LARGE_CAP>(a, cus, stream);
+        return hipErrorInvalidValue;
+      case EPI_DZ_LARGE_CAP:
+        if constexpr (!S::F32) return launch_shape<S, FORM_NT, EPI_DZ_LARGE_CAP>(a, cus, stream);
+        return hipErrorInvalidValue;
       default: return launch_shape<S, FORM_NT, EPI_STORE>(a, cus, stream);
     }
   };

@@ -597,7 +597,7 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], co
 // reductions are registers, one exchange between half-waves and four values in LDS.  Some
 // 12 instructions a logit with a soft cap (two exponentials, a reciprocal), 4 without:
 // 8192 x 1536 by 32768 786 us and 755.
-template <class S, bool CAP>
+template <class S, bool CAP, bool EXACT>
 __device__ __forceinline__ void lse_tile(f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t, char* smem,
                                          int tid) {
   const int tt = fresh(tid);
@@ -617,7 +617,7 @@ __device__ __forceinline__ void lse_tile(f32x16 (&acc)[S::FQ][S::FP], const Prod
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
           const float l = acc[j][i][v];
-          acc[j][i][v] = capped_y<S::F32>(l, cap_r(l, cap), cap);
+          acc[j][i][v] = capped_y<EXACT>(l, cap_r(l, cap), cap);
           if (v % 8 == 7) __builtin_amdgcn_sched_barrier(0);     // few values at a time, or the chains spill
         }
     }
@@ -669,7 +669,7 @@ __device__ __forceinline__ void lse_tile(f32x16 (&acc)[S::FQ][S::FP], const Prod
 // The logits become the loss's gradient with respect to them, but for the target's
 // column, which goes to `patch`.  From lse it is one exponential a logit; 8192 x 1536 by
 // 32768 with a soft cap 780 us, 512 MB of gradients written.
-template <class S, bool CAP>
+template <class S, bool CAP, bool EXACT>
 __device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t, int tid,
                                               Patch<S>& patch) {
   const int tt = fresh(tid);
@@ -693,7 +693,7 @@ __device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const
         for (int v = 0; v < 16; ++v) l = target == c0 + 32 * j + 8 * (v >> 2) + (v & 3) ? acc[j][i][v] : l;
       if constexpr (CAP) {
         const float q = cap_r(l, cap);
-        patch.value[i] = (ga * __builtin_amdgcn_exp2f(capped_y<S::F32>(l, q, cap) - lse) - a.gb[r] * per_unit) * cap_slope(q);
+        patch.value[i] = (ga * __builtin_amdgcn_exp2f(capped_y<EXACT>(l, q, cap) - lse) - a.gb[r] * per_unit) * cap_slope(q);
       } else {
         patch.value[i] = ga * __builtin_amdgcn_exp2f(__builtin_fmaf(l, LOG2E, -lse)) - a.gb[r] * per_unit;
       }
@@ -706,7 +706,7 @@ __device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const
         const float l = acc[j][i][v];
         if constexpr (CAP) {
           const float q = cap_r(l, cap);
-          acc[j][i][v] = ga * (cap_slope(q) * __builtin_amdgcn_exp2f(capped_y<S::F32>(l, q, cap) - lse));
+          acc[j][i][v] = ga * (cap_slope(q) * __builtin_amdgcn_exp2f(capped_y<EXACT>(l, q, cap) - lse));
         } else {
           acc[j][i][v] = ga * __builtin_amdgcn_exp2f(__builtin_fmaf(l, LOG2E, -lse));
         }
@@ -1111,11 +1111,12 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
       stage(nk - 1, std::integral_constant<int, 2>{});
     }
 
-    if constexpr (EPI == EPI_LSE || EPI == EPI_LSE_CAP) {
-      lse_tile<S, EPI == EPI_LSE_CAP>(acc, a, t, smem, tid);
-    } else if constexpr (EPI == EPI_DZ || EPI == EPI_DZ_CAP) {
+    constexpr bool EXACT = S::F32 || EPI == EPI_LSE_LARGE_CAP || EPI == EPI_DZ_LARGE_CAP;
+    if constexpr (epi_lse(EPI)) {
+      lse_tile<S, epi_cap(EPI), EXACT>(acc, a, t, smem, tid);
+    } else if constexpr (epi_dz(EPI)) {
       Patch<S> patch;
-      gradient_tile<S, EPI == EPI_DZ_CAP>(acc, a, t, tid, patch);
+      gradient_tile<S, epi_cap(EPI), EXACT>(acc, a, t, tid, patch);
       store_tile<S, S::F32, S::F32, LY::BYTES>(acc, out_of<FORM>(a, t), false, t, smem, tid, &patch);
     } else {
       const Out out = out_of<FORM>(a, t);

@@ -350,7 +350,9 @@ hipError_t launch_product(int form, int epi, const ProductArgs& args, int cus, c
     a.chunk = plan.chunk;
     a.queue = plan.queue ? reinterpret_cast<int32_t*>(ws) : nullptr;
     a.part = reinterpret_cast<float*>(ws + plan.queue);
-    const int kind = a.cap == 0.f ? epi : epi == EPI_LSE ? EPI_LSE_CAP : epi == EPI_DZ ? EPI_DZ_CAP : epi;
+    const bool large = !a.f32 && a.cap > FAST_CAP;
+    const int kind = a.cap == 0.f || epi == EPI_STORE ? epi : epi == EPI_LSE ? (large ? EPI_LSE_LARGE_CAP : EPI_LSE_CAP)
+                                                                             : (large ? EPI_DZ_LARGE_CAP : EPI_DZ_CAP);
     if (plan.shape == SHAPE_STREAM) return launch_stream(kind, a, stream);
     if (plan.queue) {
       hipLaunchKernelGGL(product_order_kernel, dim3(1), dim3(RT), 0, stream, a);

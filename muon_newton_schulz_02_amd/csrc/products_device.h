@@ -86,24 +86,29 @@ __device__ __forceinline__ int target_of(const ProductArgs& a, int i) {
 // e^(2 l / cap)), whose slope in l is 4 r (1 - r).
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 struct SoftCap {
+  float inv;        // 1 / cap
   float k;          // 2 log2 e / cap
   float c2;         // cap log2 e
 };
-__device__ __forceinline__ SoftCap soft_cap(const ProductArgs& a) { return {2.f * LOG2E * a.inv_cap, a.cap * LOG2E}; }
+__device__ __forceinline__ SoftCap soft_cap(const ProductArgs& a) { return {a.inv_cap, 2.f * LOG2E * a.inv_cap, a.cap * LOG2E}; }
 
 __device__ __forceinline__ float cap_r(float l, const SoftCap& c) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l * c.k));     // e^.. = inf: 0
 }
 __device__ __forceinline__ float cap_slope(float r) { return 4.f * __builtin_fmaf(-r, r, r); }
-// cap (1 - 2 r) log2 e.  r is off by 2^-24, which EXACT (binary32 operands) avoids below
-// |u| = 0.3 with tanh's own series (its next term is 5e-8 there).
+// cap (1 - 2 r) log2 e, off by some 5 2^-24 cap whatever l is.  EXACT: below |l / cap| = 0.3
+// l times tanh's own series (its next term is 5e-8 there), so that the error is 18 2^-24 of
+// the value at most, and a large cap leaves the logits as they are.
 template <bool EXACT>
 __device__ __forceinline__ float capped_y(float l, float r, const SoftCap& c) {
-  const float y = __builtin_fmaf(-2.f * c.c2, r, c.c2);
-  if constexpr (!EXACT) return y;
-  const float u = l * (c.k * (LN2 / 2.f)), s = u * u;
-  const float p = 1.f + s * (-0.333333343f + s * (0.133333340f + s * (-0.0539682545f + s * 0.0218694881f)));
-  return fabsf(u) < 0.3f ? c.c2 * (u * p) : y;
+  if constexpr (!EXACT) return __builtin_fmaf(-2.f * c.c2, r, c.c2);
+  const float y = c.c2 * __builtin_fmaf(-2.f, r, 1.f);
+  const float u = l * c.inv, s = u * u;
+  float p = __builtin_fmaf(s, 0.0218694881f, -0.0539682545f);
+  p = __builtin_fmaf(s, p, 0.133333340f);
+  p = __builtin_fmaf(s, p, -0.333333343f);
+  p = __builtin_fmaf(s, p, 1.f);
+  return fabsf(u) < 0.3f ? l * LOG2E * p : y;
 }
 
 }  // namespace muon

@@ -20,8 +20,17 @@ enum ProductForm : int { FORM_NT = 0, FORM_NN = 1, FORM_TN = 2 };
 //   LSE    a maximum and a sum of exponentials for every row and tile of columns,
 //          and the target's logit
 //   DZ     the gradient of the loss with respect to the logits C
-// (_CAP: with a soft cap; launch_product chooses.)
-enum ProductEpilogue : int { EPI_STORE = 0, EPI_LSE = 1, EPI_DZ = 2, EPI_LSE_CAP = 3, EPI_DZ_CAP = 4 };
+// (_CAP: with a soft cap, _LARGE_CAP: of bfloat16 operands above FAST_CAP; launch_product
+// chooses.)
+enum ProductEpilogue : int {
+  EPI_STORE = 0, EPI_LSE = 1, EPI_DZ = 2, EPI_LSE_CAP = 3, EPI_DZ_CAP = 4, EPI_LSE_LARGE_CAP = 5, EPI_DZ_LARGE_CAP = 6
+};
+constexpr bool epi_lse(int e) { return e == EPI_LSE || e == EPI_LSE_CAP || e == EPI_LSE_LARGE_CAP; }
+constexpr bool epi_dz(int e) { return e == EPI_DZ || e == EPI_DZ_CAP || e == EPI_DZ_LARGE_CAP; }
+constexpr bool epi_cap(int e) { return e >= EPI_LSE_CAP; }
+// Up to this cap logits of bfloat16 operands take the soft cap's short form, whose error of
+// 5 2^-24 cap is then no more than that of a binary32 logit of the cap's size.
+constexpr float FAST_CAP = 32.f;
 
 // One launch.  Groups (experts) split the rows of P and C for NT and NN, and k
 // for TN: group g has rows [offsets[g], offsets[g + 1]) of P (TN: of P and Q),

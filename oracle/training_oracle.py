@@ -40,9 +40,11 @@ def head(x, w, targets, softcap=0.0, ignore_index=-100, grad_loss=None, grad_lse
     the result itself is rounded.
 
     A logit is a sum of `dim` products in binary32: off by (dim + 4) u sum |x| |w| at most (four more for operands that
-    are multiplied in parts).  The soft cap has slope 1 at most and is itself evaluated to 6 u cap.  exp of an argument a
-    is off by (|a| + 4) u, relative; sums of at most 256 terms in turn and a tree above them by (256 + 64) u.  The
-    gradient with respect to a logit is rounded to the operands' type (half_step), and summed over by products again.
+    are multiplied in parts).  The soft cap has slope 1 at most and is itself evaluated to 6 u cap, and but for bfloat16
+    operands with caps up to 32 also to 18 u |z|: below |l / cap| = 0.3 by a series (0.9 u for what it leaves out, 6 u for
+    its roundings), above by 1 - 2 / (1 + e^(2 l / cap)), whose numerator's 4.2 u is most against 0.29 (14.4 u, and 3 u for
+    the constants).  exp of an argument a is off by (|a| + 4) u, relative; sums of at most 256 terms in turn and a tree
+    above them by (256 + 64) u.  The gradient with respect to a logit is rounded to the operands' type (half_step), and summed over by products again.
     """
     x, w = np.asarray(x, np.float64), np.asarray(w, np.float64)
     rows, dim = x.shape
@@ -58,7 +60,7 @@ def head(x, w, targets, softcap=0.0, ignore_index=-100, grad_loss=None, grad_lse
     z = l
     if softcap:
         z = softcap * np.tanh(l / softcap)
-        tol_z = tol_z + 6 * U * softcap
+        tol_z = tol_z + U * (6 * softcap if half_step > U and softcap <= 32 else np.minimum(6 * softcap, 18 * np.abs(z)))
     top = z.max(1, keepdims=True) if len(xs) else z
     lse = top + np.log(np.exp(z - top).sum(1, keepdims=True))
     p = np.exp(z - lse)

@@ -122,6 +122,15 @@ def test_a_long_vocabulary():
     case(3, 16, 300_001, "bf16", cap=30.0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cap", [33.0, 1e3, 1e6, 1e8, 1e20, 3.3e38])
+@pytest.mark.parametrize("rows,dim,vocab", [(3, 5, 40), (40, 64, 300), (300, 72, 1030), (1900, 200, 4099)])
+def test_large_soft_caps(rows, dim, vocab, cap, dtype):
+    """A cap far above the logits leaves them as they are: what its evaluation may be off by goes with the logit, not
+    with the cap (oracle/training_oracle.py)."""
+    case(rows, dim, vocab, dtype, cap=cap)
+
+
 def test_large_logits_and_sure_rows():
     """Logits up to some hundreds: no overflow, p of 1 and 0."""
     case(64, 64, 700, "f32", scale=60.0)
