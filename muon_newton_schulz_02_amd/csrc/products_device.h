@@ -82,8 +82,9 @@ __device__ __forceinline__ int target_of(const ProductArgs& a, int i) {
 }
 
 // Softmax in base 2: exponents are y = z log2 e, so that an exponential is one fma and
-// one v_exp_f32.  With a soft cap z = cap tanh(l / cap) = cap (1 - 2 r), r = 1 / (1 +
-// e^(2 l / cap)), whose slope in l is 4 r (1 - r).
+// one v_exp_f32.  With a soft cap z = cap tanh(l / cap), |z| = cap (1 - 2 r), r = 1 / (1 +
+// e^(2 |l| / cap)), whose slope in l is 4 r (1 - r).  (r of l itself would be next to 1 for
+// logits far below, and 1 - r the rounding of it.)
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 struct SoftCap {
   float inv;        // 1 / cap
@@ -93,16 +94,16 @@ struct SoftCap {
 __device__ __forceinline__ SoftCap soft_cap(const ProductArgs& a) { return {a.inv_cap, 2.f * LOG2E * a.inv_cap, a.cap * LOG2E}; }
 
 __device__ __forceinline__ float cap_r(float l, const SoftCap& c) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l * c.k));     // e^.. = inf: 0
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(fabsf(l) * c.k));     // e^.. = inf: 0
 }
 __device__ __forceinline__ float cap_slope(float r) { return 4.f * __builtin_fmaf(-r, r, r); }
-// cap (1 - 2 r) log2 e, off by some 5 2^-24 cap whatever l is.  EXACT: below |l / cap| = 0.3
+// z log2 e, off by some 5 2^-24 cap whatever l is.  EXACT: below |l / cap| = 0.3
 // l times tanh's own series (its next term is 5e-8 there), so that the error is 18 2^-24 of
 // the value at most, and a large cap leaves the logits as they are.
 template <bool EXACT>
 __device__ __forceinline__ float capped_y(float l, float r, const SoftCap& c) {
-  if constexpr (!EXACT) return __builtin_fmaf(-2.f * c.c2, r, c.c2);
-  const float y = c.c2 * __builtin_fmaf(-2.f, r, 1.f);
+  if constexpr (!EXACT) return copysignf(__builtin_fmaf(-2.f * c.c2, r, c.c2), l);
+  const float y = copysignf(c.c2 * __builtin_fmaf(-2.f, r, 1.f), l);
   const float u = l * c.inv, s = u * u;
   float p = __builtin_fmaf(s, 0.0218694881f, -0.0539682545f);
   p = __builtin_fmaf(s, p, 0.133333340f);

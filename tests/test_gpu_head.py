@@ -131,6 +131,29 @@ def test_large_soft_caps(rows, dim, vocab, cap, dtype):
     case(rows, dim, vocab, dtype, cap=cap)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,vocab", [(1, 64), (300, 64), (600, 2050)])
+@pytest.mark.parametrize("far", [2.0, -2.0, 4.0, -4.0, 6.0, -6.0, 8.0, -8.0])
+def test_slope_of_the_soft_cap_far_out(far, rows, vocab, dtype):
+    """The target's logit at `far` caps, all others 0: its gradient is (p - 1) times a slope of 4 e^(-2 |far|) or so.  The
+    slope's relative error is that of e^(2 |l| / cap), four roundings of the exponent and eight more of 2^-24; p's is some
+    20 of them; bfloat16: two roundings of half a step.  The gradients of `rows` equal rows are added: as many 2^-24."""
+    dt = DTYPES[dtype]
+    cap = 2.0
+    x, w = torch.ones(rows, 16, dtype=dt, device="cuda"), torch.zeros(vocab, 16, dtype=dt, device="cuda")
+    w[33, 5] = far * cap
+    t = torch.full((rows,), 33, device="cuda")
+    loss, lse = torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda")
+    gw = torch.zeros_like(w)
+    mb.muon_head_loss(x, w, t, loss, lse, softcap=cap)
+    mb.muon_head_loss_vjp(x, w, t, lse, torch.ones(rows, device="cuda"), None, gw, softcap=cap)
+    z = cap * np.tanh(far)
+    p = np.exp(z) / (vocab - 1 + np.exp(z))
+    want = rows * (p - 1) / np.cosh(far) ** 2
+    tol = (8 * abs(far) + 28 + rows) * 2.0 ** -24 + (2 * torch.finfo(dt).eps / 2 * 1.01 if dtype == "bf16" else 0.0)
+    assert np.abs(np64(gw)[33] / want - 1).max() <= tol
+
+
 def test_large_logits_and_sure_rows():
     """Logits up to some hundreds: no overflow, p of 1 and 0."""
     case(64, 64, 700, "f32", scale=60.0)
