@@ -146,7 +146,7 @@ __global__ __launch_bounds__(SNT) void product_stream_kernel(const ProductArgs a
       const int row = tid / 32, col = tid % 32, i = i0 + row;
       const float l = red[col / 16 * 256 + (col % 16 / 4 * 16 + row) * 4 + col % 4];
       const bool in = row < m && col < n;
-      const float y = !in ? -INFINITY : EPI == EPI_LSE_CAP ? capped_y<true>(l, cap_r(l, cap), cap) : l * LOG2E;
+      const float y = !in ? -INFINITY : EPI == EPI_LSE_CAP ? capped_y<true>(l, cap) : l * LOG2E;
       float mx = y;
 #pragma unroll
       for (int s = 1; s < 32; s *= 2) mx = fmaxf(mx, __shfl_xor(mx, s));

@@ -616,8 +616,7 @@ __device__ __forceinline__ void lse_tile(f32x16 (&acc)[S::FQ][S::FP], const Prod
       for (int j = 0; j < S::FQ; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-          const float l = acc[j][i][v];
-          acc[j][i][v] = capped_y<EXACT>(l, cap_r(l, cap), cap);
+          acc[j][i][v] = capped_y<EXACT>(acc[j][i][v], cap);
           if (v % 8 == 7) __builtin_amdgcn_sched_barrier(0);     // few values at a time, or the chains spill
         }
     }

@@ -111,5 +111,12 @@ __device__ __forceinline__ float capped_y(float l, float r, const SoftCap& c) {
   p = __builtin_fmaf(s, p, 1.f);
   return fabsf(u) < 0.3f ? l * LOG2E * p : y;
 }
+// The same where no slope is needed: the short form with r of l itself saves the sign (8192 x
+// 1536 by 32768 780 us, 788 with it).
+template <bool EXACT>
+__device__ __forceinline__ float capped_y(float l, const SoftCap& c) {
+  if constexpr (EXACT) return capped_y<true>(l, cap_r(l, c), c);
+  return __builtin_fmaf(-2.f * c.c2, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l * c.k)), c.c2);
+}
 
 }  // namespace muon
