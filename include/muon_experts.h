@@ -28,8 +28,9 @@
  *     not written, and do not change results.  They may be read within the
  *     tensor, from its first element to its last.
  *   - bfloat16 tensors are multiplied on the bfloat16 matrix cores (products
- *     exact), binary32 ones to binary32 accuracy; sums are binary32, and
- *     results are rounded once.
+ *     exact), binary32 ones to binary32 accuracy: a product is off by 2^-24 of
+ *     itself at most, and elements below 2^-110 in magnitude count with an error
+ *     of up to 2^-134.  Sums are binary32, and results are rounded once.
  *   - A NaN or an infinity reaches the results whose sums it takes part in (the
  *     row, or the expert's grad_W) and no others.  They are NaN or infinite, as the
  *     formulas have it; with binary32 tensors also NaN where the formula is infinite.

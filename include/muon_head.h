@@ -32,7 +32,7 @@
  *   - bfloat16: logits, their softmax and all sums are binary32; dl is rounded
  *     to bfloat16 for the two products (relative 2^-8 at most, independent from
  *     element to element, as the rounding of the results).  binary32: to
- *     binary32 accuracy throughout.
+ *     binary32 accuracy throughout (products as in muon_experts.h).
  *   - A row with a NaN or an infinity among its logits has the values that the
  *     formulas give, NaN or infinite, and so have gradients that it takes part in.
  *     (Soft-capped) logits from 2^127 on in magnitude count as infinite.

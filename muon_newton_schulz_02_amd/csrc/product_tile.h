@@ -55,10 +55,12 @@ constexpr int KB = 128;     // bytes of k per stage
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Tile shapes: BM x BN over WM x WN waves.  Binary32 operands become three bfloat16
-// parts on their way to LDS, x = hi + mid + lo with 8 bits each (exact), and a product
-// is six on the bfloat16 matrix cores: hi hi, hi mid, mid hi, mid mid, hi lo, lo hi; the
-// three left out are 2^-24 of it and less.  The binary32 matrix instructions do 1 / 16
-// of the bfloat16 ones' work a cycle, so six of these are 2.7 times as fast.
+// parts on their way to LDS, x = hi + mid + lo, each rounded to nearest: of an x in [1, 2)
+// mid is 2^-8 at most and lo 2^-17, and the sum is x (but for bits below 2^-133, bfloat16's
+// least number: elements under 2^-110 lose some).  A product is six on the bfloat16 matrix
+// cores: hi hi, hi mid, mid hi, mid mid, hi lo, lo hi; the three left out are 2^-24 of it
+// at most, and of either sign.  The binary32 matrix instructions do 1 / 16 of the bfloat16
+// ones' work a cycle, so six of these are 2.7 times as fast.
 template <int BM_, int BN_, int WM_, int WN_, bool F32_>
 struct Shape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NT = WM_ * WN_ * 64;
@@ -293,20 +295,25 @@ constexpr int chunk_step() {
   return S::NT / PER * Lds<S, R, KROW>::pitch;
 }
 
-// Four binary32 values as three times four bfloat16: the upper half of the bits, of what
-// is left, and of what is left then.  Infinities and NaN have NaN parts.
+// Four binary32 values as three times four bfloat16: the value, what is left, and what is
+// left then, each rounded to nearest.  Values that would round to infinity start from the
+// largest bfloat16 instead.  Infinities and NaN have NaN parts.
 __device__ __forceinline__ void split4(const u32x4& x, u32x2 (&out)[3]) {
-  float v[4], mid[4], lo[4];
+  constexpr float MOST = 3.38953139e38f;      // 0x7F7F0000
+  float v[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(x[e]);
+  out[0] = u32x2{float2_to_bf16x2_bits(__builtin_amdgcn_fmed3f(v[0], -MOST, MOST), __builtin_amdgcn_fmed3f(v[1], -MOST, MOST)),
+                 float2_to_bf16x2_bits(__builtin_amdgcn_fmed3f(v[2], -MOST, MOST), __builtin_amdgcn_fmed3f(v[3], -MOST, MOST))};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) mid[e] = v[e] - __uint_as_float(x[e] & 0xFFFF0000u);
+  for (int p = 1; p < 3; ++p) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) lo[e] = mid[e] - __uint_as_float(__float_as_uint(mid[e]) & 0xFFFF0000u);
-  auto pack = [](uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); };
-  out[0] = u32x2{pack(x[0], x[1]), pack(x[2], x[3])};
-  out[1] = u32x2{pack(__float_as_uint(mid[0]), __float_as_uint(mid[1])), pack(__float_as_uint(mid[2]), __float_as_uint(mid[3]))};
-  out[2] = u32x2{pack(__float_as_uint(lo[0]), __float_as_uint(lo[1])), pack(__float_as_uint(lo[2]), __float_as_uint(lo[3]))};
+    for (int h = 0; h < 2; ++h) {
+      v[2 * h] -= __uint_as_float(out[p - 1][h] << 16);
+      v[2 * h + 1] -= __uint_as_float(out[p - 1][h] & 0xFFFF0000u);
+      out[p][h] = float2_to_bf16x2_bits(v[2 * h], v[2 * h + 1]);
+    }
+  }
 }
 
 template <class S, int R, bool KROW>

@@ -354,6 +354,69 @@ def test_nan_and_infinity_stay_in_their_rows(dtype):
     assert torch.equal(hit, want)
 
 
+def one_term(rows, xs, ws):
+    """y of `rows` rows whose only element is one of xs, weights whose only elements are ws, and the exact products."""
+    xv, wv = np.resize(np.float32(xs), rows), np.float32(ws)
+    x, w = torch.zeros(rows, 64), torch.zeros(1, len(wv), 64)
+    x[:, 37], w[0, :, 37] = torch.from_numpy(xv), torch.from_numpy(wv)
+    y = torch.full((rows, len(wv)), float("nan"), device="cuda")
+    gx = torch.full((rows, 64), float("nan"), device="cuda")
+    w, off = w.cuda(), offsets_of([rows])
+    mb.muon_experts_product(x.cuda(), w, off, y)
+    # the same products by the form of grad_x: rows (x's one value, 0, ..) times w's one column of values
+    gy = torch.zeros(rows, len(wv))
+    gy[:, 0] = torch.from_numpy(xv)
+    mb.muon_experts_product_vjp(None, w, off, gy.cuda(), gx)
+    want = xv.astype(np.float64)[:, None] * wv.astype(np.float64)
+    return np64(y), np64(gx)[:, 37], want
+
+
+# (rows, columns): streamed, and tiles of each height
+ONE_TERM = [(5, 40), (60, 700), (700, 300), (9000, 2100)]
+
+
+@pytest.mark.parametrize("rows,cols", ONE_TERM)
+def test_binary32_products_of_the_longest_remainders(rows, cols):
+    """Operands whose bits past the eighth and the sixteenth are all ones, or a half step from it.  A product leaves out
+    2^-24 of itself at most; its parts are added to it by roundings of two more at most, and of 2^-6 of one."""
+    ends = [2.0 ** -7 - 2.0 ** -23, 2.0 ** -8 - 2.0 ** -16 - 2.0 ** -23, 2.0 ** -8 + 2.0 ** -17 - 2.0 ** -23, 2.0 ** -9 + 2.0 ** -17,
+            1.0 - 2.0 ** -23, 2.0 ** -8 - 2.0 ** -23]
+    vals = [s * (1 + e) for e in ends for s in (1.0, -1.0)]
+    y, gx, want = one_term(rows, vals, np.resize(vals, cols))
+    assert np.abs(y / want - 1).max() <= 3.1 * U
+    assert np.abs(gx / want[:, 0] - 1).max() <= 3.1 * U
+
+
+@pytest.mark.parametrize("rows,cols", ONE_TERM)
+def test_binary32_values_next_to_the_largest(rows, cols):
+    big = np.array([0x7F7F0000, 0x7F7F7FFF, 0x7F7F8000, 0x7F7F8001, 0x7F7FFFFF], np.uint32).view(np.float32)
+    y, gx, want = one_term(rows, np.concatenate([big, -big]), np.resize([0.5, -0.25, 0.0, 2.0 ** -100, -0.8], cols))
+    assert np.isfinite(y).all() and np.isfinite(gx).all()
+    assert (np.abs(y - want) <= 3.1 * U * np.abs(want)).all() and (np.abs(gx - want[:, 0]) <= 3.1 * U * np.abs(want[:, 0])).all()
+
+
+@pytest.mark.parametrize("rows,cols", ONE_TERM)
+def test_binary32_values_below_the_parts_range(rows, cols):
+    """Parts are bfloat16, whose least number is 2^-133: a value counts with an error of half that, whatever it is."""
+    rng = np.random.default_rng(0)
+    tiny = (1 + rng.random(56)) * 2.0 ** -np.repeat(np.arange(96, 152), 1).astype(np.float64)
+    y, gx, want = one_term(rows, tiny, np.resize(2.0 ** 100 * (1 + rng.random(31)), cols))
+    tol = 3.1 * U * np.abs(want) + 2.0 ** -134 * 2.0 ** 101
+    assert (np.abs(y - want) <= tol).all() and (np.abs(gx - want[:, 0]) <= tol[:, 0]).all()
+
+
+@pytest.mark.parametrize("rows", [10, 300])
+def test_binary32_sums_of_one_sign_have_no_bias(rows):
+    """What a product leaves out has either sign, as the sums' roundings have (some 5 of 2^-24 a sum of 4096 terms, at
+    random): the mean of 19200 sums' errors is a 138th of one's, 0.04."""
+    gen = torch.Generator().manual_seed(31)
+    x, w = torch.rand(rows, 4096, generator=gen) + 0.5, torch.rand(1, 19200 // rows, 4096, generator=gen) + 0.5
+    y = torch.zeros(rows, 19200 // rows, device="cuda")
+    mb.muon_experts_product(x.cuda(), w.cuda(), offsets_of([rows]), y)
+    want = x.double() @ w[0].double().t()
+    assert abs((y.double().cpu() / want - 1).mean().item()) < 0.25 * U
+
+
 def test_shared_and_interleaved_weights():
     """One weight for all experts (stride 0), and experts beside each other in the same rows."""
     gen = torch.Generator().manual_seed(5)
