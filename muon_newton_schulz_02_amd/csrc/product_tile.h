@@ -297,7 +297,9 @@ constexpr int chunk_step() {
 
 // Four binary32 values as three times four bfloat16: the value, what is left, and what is
 // left then, each rounded to nearest.  Values that would round to infinity start from the
-// largest bfloat16 instead.  Infinities and NaN have NaN parts.
+// largest bfloat16 instead.  Infinities and NaN have NaN parts.  (A first part that is cut
+// off, not rounded, saves two of 6.5 instructions a value and 1.5 % of the time, and leaves out
+// four times as much.)
 __device__ __forceinline__ void split4(const u32x4& x, u32x2 (&out)[3]) {
   constexpr float MOST = 3.38953139e38f;      // 0x7F7F0000
   float v[4];

@@ -1,5 +1,5 @@
 // Products of the experts and of the head: the launcher, and the kernel for
-// operands too small for 16-byte loads.
+// operands too narrow for 16-byte loads.
 #include <algorithm>
 #include <cmath>
 
@@ -8,10 +8,16 @@
 namespace muon {
 namespace {
 
-constexpr int TS = 16;  // a workgroup's tile: 16 x 16, one element a thread
+constexpr int TS = 16;        // rows and columns of a workgroup's tile at most
+constexpr int SMALL_NT = 1024;
 
+template <bool F32>
+__device__ __forceinline__ float load_as(const void* p, int64_t i) {
+  if constexpr (F32) return gmem(reinterpret_cast<const float*>(p))[i];
+  else return bf16_bits_to_float(gmem(reinterpret_cast<const uint16_t*>(p))[i]);
+}
 __device__ __forceinline__ float load1(const void* p, int64_t i, int f32) {
-  return f32 ? reinterpret_cast<const float*>(p)[i] : bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p)[i]);
+  return f32 ? load_as<true>(p, i) : load_as<false>(p, i);
 }
 
 __device__ __forceinline__ void store1(void* p, int64_t i, float v, int f32) {
@@ -19,30 +25,52 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float v, int f32) {
   else reinterpret_cast<uint16_t*>(p)[i] = float_to_bf16_bits(v);
 }
 
-// One element of C a thread, straight from the definition.
-template <int FORM, int EPI>
-__global__ __launch_bounds__(TS * TS) void product_small_kernel(const ProductArgs a) {
-  const int tx = threadIdx.x % TS, ty = threadIdx.x / TS;
-  const int nt = (a.n + TS - 1) / TS;
-  const bool tn = FORM == FORM_TN;
-  const int per_group = tn ? (a.m + TS - 1) / TS : (a.rows + TS - 1) / TS;
+// A workgroup of 2^(ti + tj + kl) threads: 2^ti x 2^tj elements of C, 2^kl threads for the
+// terms of each.
+struct SmallShape {
+  int ti, tj, kl;
+};
+
+// A few columns or rows of C, or a few terms: operands with rows of less than 16 bytes.  The
+// terms of an element go to as many threads as there are beside the elements, and are joined
+// in LDS: what such products have is a long k (16384 rows of 4 and 1536 bfloat16: grad_W
+// 147 us, and 5860 by a thread an element; grad_x of 4 from 1536 75 and 354).
+template <int FORM, int EPI, bool F32>
+__global__ __launch_bounds__(SMALL_NT) void product_small_kernel(const ProductArgs a, const SmallShape s) {
+  __shared__ float red[SMALL_NT];
+  constexpr bool tn = FORM == FORM_TN;
+  // along k where k lies along memory, or along the columns
+  const int tid = threadIdx.x, rest = tn ? tid : tid >> s.kl;
+  const int kk = tn ? tid >> (s.ti + s.tj) : tid & ((1 << s.kl) - 1);
+  const int tx = rest & ((1 << s.tj) - 1), ty = rest >> s.tj & ((1 << s.ti) - 1);
+  const int nt = (a.n + (1 << s.tj) - 1) >> s.tj;
+  const int per_group = ((tn ? a.m : a.rows) + (1 << s.ti) - 1) >> s.ti;
   const int64_t tiles = int64_t(a.groups) * per_group * nt;
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int jt = int(t % nt), it = int(t / nt % per_group), g = int(t / nt / per_group);
     int lo, hi;
     group_range(a, g, lo, hi);
     const int m = tn ? a.m : hi - lo, k = tn ? hi - lo : a.k;
-    const int i = it * TS + ty, j = jt * TS + tx;
-    const bool in = i < m && j < a.n;
+    const int i = (it << s.ti) + ty, j = (jt << s.tj) + tx;
+    bool in = i < m && j < a.n;
     float c = 0.f;
     if (in) {
       const int64_t q0 = tn ? int64_t(lo) * a.ld_q : int64_t(g) * a.es_q;
-      for (int x = 0; x < k; ++x) {
-        const float pv = tn ? load1(a.p, int64_t(lo + x) * a.ld_p + i, a.f32) : load1(a.p, int64_t(lo + i) * a.ld_p + x, a.f32);
-        const float qv = FORM == FORM_NT ? load1(a.q, q0 + int64_t(j) * a.ld_q + x, a.f32)
-                                         : load1(a.q, q0 + int64_t(x) * a.ld_q + j, a.f32);
-        c += pv * qv;
+#pragma unroll 8
+      for (int x = kk; x < k; x += 1 << s.kl) {
+        const float pv = load_as<F32>(a.p, tn ? int64_t(lo + x) * a.ld_p + i : int64_t(lo + i) * a.ld_p + x);
+        const float qv = load_as<F32>(a.q, FORM == FORM_NT ? q0 + int64_t(j) * a.ld_q + x : q0 + int64_t(x) * a.ld_q + j);
+        c = __builtin_fmaf(pv, qv, c);
       }
+    }
+    if (s.kl > 0) {
+      const int at = ty << s.tj | tx;
+      __syncthreads();
+      red[kk << (s.ti + s.tj) | at] = c;
+      __syncthreads();
+      if (kk == 0)
+        for (int x = 1; x < 1 << s.kl; ++x) c += red[x << (s.ti + s.tj) | at];
+      in = in && kk == 0;
     }
     if constexpr (EPI == EPI_STORE) {
       if (in) {
@@ -78,11 +106,21 @@ __global__ __launch_bounds__(TS * TS) void product_small_kernel(const ProductArg
 
 template <int FORM, int EPI>
 hipError_t launch_small(const ProductArgs& a, hipStream_t stream) {
-  const int64_t nt = (a.n + TS - 1) / TS, mt = ((FORM == FORM_TN ? a.m : a.rows) + TS - 1) / TS;
+  const int m = FORM == FORM_TN ? a.m : a.rows, k = FORM == FORM_TN ? a.rows : a.k;
+  SmallShape s = {4, 4, 0};
+  if (EPI == EPI_STORE) {
+    s = {};
+    while (s.ti < 4 && 1 << s.ti < m) ++s.ti;
+    while (s.tj < 4 && 1 << s.tj < a.n) ++s.tj;
+    // whole waves, and from there on 16 terms a thread at least
+    while (1 << (s.ti + s.tj + s.kl) < SMALL_NT && (s.ti + s.tj + s.kl < 6 || 16 << s.kl < k)) ++s.kl;
+  }
+  const int64_t nt = (a.n + (1 << s.tj) - 1) >> s.tj, mt = (m + (1 << s.ti) - 1) >> s.ti;
   const int64_t tiles = int64_t(a.groups) * mt * nt;
   if (tiles == 0) return hipSuccess;
-  hipLaunchKernelGGL((product_small_kernel<FORM, EPI>), dim3(unsigned(std::min<int64_t>(tiles, 1 << 16))),
-                     dim3(TS * TS), 0, stream, a);
+  const dim3 grid(unsigned(std::min<int64_t>(tiles, 1 << 16))), block(1u << (s.ti + s.tj + s.kl));
+  if (a.f32) hipLaunchKernelGGL((product_small_kernel<FORM, EPI, true>), grid, block, 0, stream, a, s);
+  else hipLaunchKernelGGL((product_small_kernel<FORM, EPI, false>), grid, block, 0, stream, a, s);
   return hipGetLastError();
 }
 

@@ -151,6 +151,41 @@ def test_few_columns(counts, inn, out, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("inn,out", [(1, 130), (3, 2100), (130, 1), (1500, 5), (7, 7), (2, 3)])
+def test_narrow_weights_and_long_sums(inn, out, dtype):
+    """Rows of less than 16 bytes, whose sums go to several threads."""
+    run_all([3000, 0, 1100, 17], inn, out, dtype, spare=3)
+    run_all([5, 0, 2000], inn, out, dtype, order=mb.WEIGHT_IN_OUT, lead=1, gw_dtype="f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_narrow_weights_take_no_multiple_of_wide_ones_time(dtype):
+    """16384 rows, 1536 by 3 columns against 1536 by 8: not 10 times the time (a sum by one thread took 150 times)."""
+    dt = DTYPES[dtype]
+    off = offsets_of([16384])
+
+    def ms(inn, out):
+        x, gy = torch.ones(16384, inn, dtype=dt, device="cuda"), torch.ones(16384, out, dtype=dt, device="cuda")
+        w, gx, gw = torch.ones(1, out, inn, dtype=dt, device="cuda"), torch.zeros_like(x), torch.zeros(1, out, inn, dtype=dt, device="cuda")
+        args = [mb.ExpertsVjpArgs(x, None, off, gy, None, gw), mb.ExpertsVjpArgs(None, w, off, gy, gx)]
+        took = []
+        for a in args:
+            times = []
+            for _ in range(5):
+                start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                start.record()
+                mb.muon_experts_product_vjp(a)
+                end.record()
+                torch.cuda.synchronize()
+                times.append(start.elapsed_time(end))
+            took.append(sorted(times)[2])
+        return took
+
+    for narrow in ((1536, 3), (3, 1536)):
+        assert all(a < 10 * b for a, b in zip(ms(*narrow), ms(*sorted((8, 1536), reverse=narrow[0] > narrow[1]))))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_products_cut_along_k(dtype):
     """Few tiles and a long sum: partial sums in a workspace, added in order."""
     dt = DTYPES[dtype]
