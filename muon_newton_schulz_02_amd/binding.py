@@ -985,7 +985,8 @@ def muon_experts_product_vjp(x, w=None, offsets=None, grad_y=None, grad_x=None, 
 
 
 class _HeadArgs(_OperatorArgs):
-    def _describe(self, x, w, gx, gw):
+    def _describe(self, x, w, gx, gw, softcap, ignore_index):
+        self.softcap, self.ignore_index = softcap, ignore_index
         if x.dim() != 2 or w.dim() != 2:
             raise ValueError("x must be (rows, dim) and w (vocab, dim)")
         d = self.desc = HeadDesc()
@@ -1007,6 +1008,22 @@ class _HeadArgs(_OperatorArgs):
             self.shaped("grad_w", (d.vocab, d.dim), x.dtype)
             d.ld_grad_w = _ld(gw, "grad_w")
 
+    def _agreed(self, name, given, default):
+        held = getattr(self, name)
+        if given is None:
+            return default if held is None else held
+        if held is not None and given != held:
+            raise ValueError(f"{name} is {given} in the call and {held} in its {type(self).__name__}")
+        return given
+
+    def described(self, softcap, ignore_index):
+        """The descriptor of a call.  What the arguments were built with holds where the call gives nothing; a call
+        that gives something else is refused: its gradient would be that of another loss."""
+        desc = HeadDesc.from_buffer_copy(self.desc)
+        desc.softcap = float(self._agreed("softcap", softcap, 0.0))
+        desc.ignore_index = int(self._agreed("ignore_index", ignore_index, -100))
+        return desc
+
     def workspace_bytes(self) -> int:
         """Bytes a `workspace` of the call needs."""
         with _on_device(self.device):
@@ -1019,52 +1036,56 @@ class _HeadArgs(_OperatorArgs):
 
 class HeadLossArgs(_HeadArgs):
     """Tensors of muon_head_loss: x (rows, dim), w (vocab, dim), targets (rows,
-    int64), loss and lse (rows, float32)."""
+    int64), loss and lse (rows, float32); and softcap and ignore_index for the
+    calls that do not give them (None: the calls' defaults)."""
 
     op = HEAD_LOSS
 
-    def __init__(self, x, w, targets, loss, lse):
+    def __init__(self, x, w, targets, loss, lse, *, softcap=None, ignore_index=None):
         super().__init__(x=x, w=w, targets=targets, loss=loss, lse=lse)
-        self._describe(x, w, None, None)
+        self._describe(x, w, None, None, softcap, ignore_index)
 
 
 class HeadLossVjpArgs(_HeadArgs):
     """Tensors of muon_head_loss_vjp: those of the loss, grad_loss and grad_lse
     (rows, float32; grad_lse may be None), grad_x (rows, dim) and grad_w
-    (vocab, dim), either None if not wanted."""
+    (vocab, dim), either None if not wanted; and softcap and ignore_index, which
+    are those of the loss, as in HeadLossArgs."""
 
-    def __init__(self, x, w, targets, lse, grad_loss, grad_x=None, grad_w=None, grad_lse=None):
+    def __init__(self, x, w, targets, lse, grad_loss, grad_x=None, grad_w=None, grad_lse=None, *, softcap=None,
+                 ignore_index=None):
         super().__init__(x=x, w=w, targets=targets, lse=lse, grad_loss=grad_loss, grad_lse=grad_lse, grad_x=grad_x,
                          grad_w=grad_w)
         if grad_x is None and grad_w is None:
             raise ValueError("grad_x and grad_w are both None")
         self.op = (HEAD_GRAD_X if grad_x is not None else 0) | (HEAD_GRAD_W if grad_w is not None else 0)
-        self._describe(x, w, grad_x, grad_w)
+        self._describe(x, w, grad_x, grad_w, softcap, ignore_index)
 
 
-def muon_head_loss(x, w=None, targets=None, loss=None, lse=None, *, softcap=0.0, ignore_index=-100, workspace=None,
+def muon_head_loss(x, w=None, targets=None, loss=None, lse=None, *, softcap=None, ignore_index=None, workspace=None,
                    stream=None):
     """loss[r] and lse[r] of the head w's logits of row x[r] (or on a prebuilt
-    HeadLossArgs), both 0 where targets[r] is ignore_index."""
+    HeadLossArgs), both 0 where targets[r] is ignore_index.  softcap and
+    ignore_index are 0 (no soft cap) and -100 where neither the call nor its
+    HeadLossArgs gives them."""
     a = _prebuilt(HeadLossArgs, x, (w, targets, loss, lse), {})
     with _Quick(a.device):
         ws, nbytes = _workspace(workspace, a.device)
-        desc = HeadDesc.from_buffer_copy(a.desc)
-        desc.softcap, desc.ignore_index = float(softcap), int(ignore_index)
+        desc = a.described(softcap, ignore_index)
         _check(lib().muon_head_loss(a.ptr("x"), a.ptr("w"), a.ptr("targets"), a.ptr("loss"), a.ptr("lse"), desc, ws,
                                     nbytes, _stream_of(stream, a.device)))
 
 
 def muon_head_loss_vjp(x, w=None, targets=None, lse=None, grad_loss=None, grad_x=None, grad_w=None, *, grad_lse=None,
-                       softcap=0.0, ignore_index=-100, workspace=None, stream=None):
+                       softcap=None, ignore_index=None, workspace=None, stream=None):
     """The gradients of <loss, grad_loss> + <lse, grad_lse> with respect to x and
-    w, each if its tensor is given (or on a prebuilt HeadLossVjpArgs)."""
+    w, each if its tensor is given (or on a prebuilt HeadLossVjpArgs).  softcap
+    and ignore_index are the loss's, with the same defaults: 0 and -100."""
     a = _prebuilt(HeadLossVjpArgs, x, (w, targets, lse, grad_loss),
                   {"grad_x": grad_x, "grad_w": grad_w, "grad_lse": grad_lse})
     with _Quick(a.device):
         ws, nbytes = _workspace(workspace, a.device)
-        desc = HeadDesc.from_buffer_copy(a.desc)
-        desc.softcap, desc.ignore_index = float(softcap), int(ignore_index)
+        desc = a.described(softcap, ignore_index)
         _check(lib().muon_head_loss_vjp(a.ptr("x"), a.ptr("w"), a.ptr("targets"), a.ptr("lse"), a.ptr("grad_loss"),
                                         a.ptr("grad_lse"), a.ptr("grad_x"), a.ptr("grad_w"), desc, ws, nbytes,
                                         _stream_of(stream, a.device)))

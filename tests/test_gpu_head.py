@@ -333,6 +333,36 @@ def test_binding_refusals():
         mb.muon_head_loss(x, w, t, f, f.clone(), softcap=-1.0)
 
 
+def test_prebuilt_arguments_hold_the_soft_cap():
+    """As a program uses them: softcap and ignore_index given once, with the tensors; gradients of that loss."""
+    gen = torch.Generator().manual_seed(41)
+    h, head = matrix(60, 48, torch.float32, gen, scale=4.0), matrix(500, 48, torch.float32, gen)
+    targets = torch.randint(500, (60,), generator=gen).cuda()
+    targets[::6] = 7
+    loss, lse, grad_loss = torch.zeros(60, device="cuda"), torch.zeros(60, device="cuda"), torch.ones(60, device="cuda")
+    grad_h, grad_head = torch.zeros(60, 48, device="cuda"), torch.zeros(500, 48, device="cuda")
+    mb.muon_head_loss(mb.HeadLossArgs(h, head, targets, loss, lse, softcap=5.0, ignore_index=7))
+    args = mb.HeadLossVjpArgs(h, head, targets, lse, grad_loss, grad_h, grad_head, softcap=5.0, ignore_index=7)
+    ws = torch.empty(args.workspace_bytes(), dtype=torch.uint8, device="cuda")
+    mb.muon_head_loss_vjp(args, workspace=ws)
+    want = orc.training.head(np64(h), np64(head), targets.cpu().numpy(), 5.0, 7, np64(grad_loss))
+    for name, got in (("loss", loss), ("lse", lse), ("grad_x", grad_h), ("grad_w", grad_head)):
+        check(got, want[name], want["tol_" + name], torch.float32, name)
+    # the same with the call's, and refused where the two differ
+    again = [torch.zeros_like(grad_h), torch.zeros_like(grad_head)]
+    mb.muon_head_loss_vjp(h, head, targets, lse, grad_loss, *again, softcap=5.0, ignore_index=7)
+    mb.muon_head_loss_vjp(args, softcap=5.0, ignore_index=7)
+    assert torch.equal(again[0], grad_h) and torch.equal(again[1], grad_head)
+    with pytest.raises(ValueError, match="softcap is 4.0 in the call and 5.0"):
+        mb.muon_head_loss_vjp(args, softcap=4.0)
+    with pytest.raises(ValueError, match="ignore_index"):
+        mb.muon_head_loss_vjp(args, ignore_index=-100)
+    # built without: the call's, or its defaults
+    bare = mb.HeadLossVjpArgs(h, head, targets, lse, grad_loss, *again)
+    mb.muon_head_loss_vjp(bare, softcap=5.0, ignore_index=7)
+    assert torch.equal(again[0], grad_h) and torch.equal(again[1], grad_head)
+
+
 def test_a_training_step_from_experts_to_the_optimizer():
     """Experts, the head's loss, their gradients, then the Muon step on the experts and AdamW on the head, as a program
     has them; the gradients against float64 through the whole chain."""
