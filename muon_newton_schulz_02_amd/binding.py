@@ -805,8 +805,13 @@ class _OperatorArgs:
     """Checked tensors of a call, built once and reused by every call on them.
     All live on one GPU; the calls run on it, whatever the current device."""
 
+    optional = ()
+
     def __init__(self, **tensors):
-        """tensors: name -> tensor, or None where the call does without."""
+        """tensors: name -> tensor, or None where the call does without (`optional`)."""
+        for name, t in tensors.items():
+            if t is None and name not in self.optional:
+                raise ValueError(f"{name} is missing")
         self.device = None
         self.t = tensors
         for name, t in tensors.items():
@@ -909,6 +914,8 @@ class ExpertsArgs(_ExpertsArgs):
 class ExpertsVjpArgs(_ExpertsArgs):
     """Tensors of muon_experts_product_vjp.  grad_x (rows, in) needs w, grad_w
     (experts, out, in) needs x; what is not needed may be None."""
+
+    optional = ("x", "w", "grad_x", "grad_w")
 
     def __init__(self, x, w, offsets, grad_y, grad_x=None, grad_w=None):
         super().__init__(x=x, w=w, offsets=offsets, grad_y=grad_y, grad_x=grad_x, grad_w=grad_w)
@@ -1051,6 +1058,8 @@ class HeadLossVjpArgs(_HeadArgs):
     (rows, float32; grad_lse may be None), grad_x (rows, dim) and grad_w
     (vocab, dim), either None if not wanted; and softcap and ignore_index, which
     are those of the loss, as in HeadLossArgs."""
+
+    optional = ("grad_lse", "grad_x", "grad_w")
 
     def __init__(self, x, w, targets, lse, grad_loss, grad_x=None, grad_w=None, grad_lse=None, *, softcap=None,
                  ignore_index=None):

@@ -212,6 +212,22 @@ def test_bindings_refuse_before_any_call():
         mb.muon_head_loss(x, w[0], torch.zeros(3, dtype=torch.int64), torch.zeros(3), torch.zeros(3))
 
 
+@pytest.mark.parametrize("call,missing", [
+    (lambda t: mb.muon_experts_product(t), "w"),
+    (lambda t: mb.muon_experts_product(t, t, None, t), "offsets"),
+    (lambda t: mb.muon_experts_product(None, t, t, t), "x"),
+    (lambda t: mb.muon_experts_product_vjp(t, t, t, None, t), "grad_y"),
+    (lambda t: mb.muon_experts_product_vjp(t, t, None, t, t), "offsets"),
+    (lambda t: mb.muon_head_loss(t), "w"),
+    (lambda t: mb.muon_head_loss(t, t, t, None, t), "loss"),
+    (lambda t: mb.muon_head_loss_vjp(t, t, t, t, None, t), "grad_loss"),
+    (lambda t: mb.muon_head_loss_vjp(None, t, t, t, t, t), "x"),
+])
+def test_bindings_name_what_is_missing(call, missing):
+    with pytest.raises(ValueError, match=f"^{missing} is missing"):
+        call(torch.zeros(2, 2))
+
+
 def test_oracle_against_differences():
     rng = np.random.default_rng(0)
     x, w = rng.normal(size=(5, 4)), rng.normal(size=(7, 4))
