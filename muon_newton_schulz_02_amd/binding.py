@@ -850,16 +850,20 @@ def _ld(t, name):
     return int(t.stride(0))
 
 
-def _weight_layout(t, name):
-    """(order, row stride, expert stride) of an (experts, out, in) stack, whose rows or whose columns are contiguous."""
+def _weight_layouts(t, name):
+    """{order: (row stride, expert stride)} of an (experts, out, in) stack whose rows or whose columns are contiguous: both
+    orders where it has one row or one column."""
     if t.dim() != 3:
         raise ValueError(f"{name} must be 3-D: experts, out, in (got shape {tuple(t.shape)})")
     stride = int(t.stride(0)) if t.shape[0] > 1 else 0
+    got = {}
     if t.shape[2] == 1 or t.stride(2) == 1:
-        return WEIGHT_OUT_IN, int(t.stride(1)), stride
+        got[WEIGHT_OUT_IN] = int(t.stride(1)), stride
     if t.shape[1] == 1 or t.stride(1) == 1:
-        return WEIGHT_IN_OUT, int(t.stride(2)), stride
-    raise ValueError(f"{name} must have contiguous rows or columns (strides {tuple(t.stride())})")
+        got[WEIGHT_IN_OUT] = int(t.stride(2)), stride
+    if not got:
+        raise ValueError(f"{name} must have contiguous rows or columns (strides {tuple(t.stride())})")
+    return got
 
 
 class _ExpertsArgs(_OperatorArgs):
@@ -872,17 +876,23 @@ class _ExpertsArgs(_OperatorArgs):
             raise ValueError("offsets must be 1-D int32, experts + 1 of them")
         self.flat("offsets")
         d.experts = offsets.shape[0] - 1
-        d.w_order = WEIGHT_OUT_IN
+        orders = (WEIGHT_OUT_IN, WEIGHT_IN_OUT)
         if w is not None:
             self.shaped("w", (d.experts, out_dim, in_dim), self.dtype)
-            d.w_order, d.ld_w, d.stride_w = _weight_layout(w, "w")
+            w_layouts = _weight_layouts(w, "w")
+            orders = [o for o in orders if o in w_layouts]
         if gw is not None:
             if tuple(gw.shape) != (d.experts, out_dim, in_dim):
                 raise ValueError(f"grad_w must have shape {(d.experts, out_dim, in_dim)} (got {tuple(gw.shape)})")
-            order, d.ld_grad_w, d.stride_grad_w = _weight_layout(gw, "grad_w")
-            if w is not None and order != d.w_order:
+            gw_layouts = _weight_layouts(gw, "grad_w")
+            orders = [o for o in orders if o in gw_layouts]
+            if not orders:
                 raise ValueError("grad_w must lie in memory in w's order")
-            d.w_order = order
+        d.w_order = orders[0]
+        if w is not None:
+            d.ld_w, d.stride_w = w_layouts[d.w_order]
+        if gw is not None:
+            d.ld_grad_w, d.stride_grad_w = gw_layouts[d.w_order]
             d.grad_w_dtype = dtype_code(gw.dtype)
         d.dtype = dtype_code(self.dtype)
 

@@ -473,6 +473,28 @@ def test_shared_and_interleaved_weights():
     check(gwide.unflatten(1, (2, 40)).transpose(0, 1), want, reach, 30, torch.float32)
 
 
+@pytest.mark.parametrize("inn,out", [(40, 1), (1, 40), (1, 1)])
+@pytest.mark.parametrize("padded", ["w", "grad_w"])
+def test_one_row_or_column_is_of_either_order(padded, inn, out):
+    """A weight of one row or column, its elements next to each other or not, beside a gradient that is the other."""
+    gen = torch.Generator().manual_seed(19)
+    x, gy, off = matrix(90, inn, torch.float32, gen), matrix(90, out, torch.float32, gen), offsets_of([50, 40])
+    w = torch.randn(2, inn, out, generator=gen).cuda().transpose(1, 2).contiguous()
+    gw, gx = torch.zeros_like(w), torch.zeros(90, inn, device="cuda")
+
+    def apart(t):                       # elements three apart, whichever way the one row or column goes
+        wide = torch.zeros(2, out * inn, 3, device="cuda")
+        wide[:, :, 0] = t.reshape(2, out * inn)
+        return wide[:, :, 0].view(2, out, inn)
+
+    w, gw = (apart(w), gw) if padded == "w" else (w, apart(gw))
+    mb.muon_experts_product_vjp(x, w, off, gy, gx, gw)
+    want, reach = orc.training.experts(np64(gy), np64(w).transpose(0, 2, 1), [0, 50, 90])
+    check(gx, want, reach, out, torch.float32, "grad_x")
+    want, reach = orc.training.experts_grad_w(np64(x), np64(gy), [0, 50, 90])
+    check(gw, want, reach, 50, torch.float32, "grad_w")
+
+
 def test_no_rows_at_all():
     w, off = torch.ones(3, 8, 16, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
     x, gy = torch.zeros(0, 16, device="cuda"), torch.zeros(0, 8, device="cuda")
