@@ -13,9 +13,14 @@ namespace muon {
 namespace {
 
 constexpr int64_t MAX_ROWS = 1 << 20, MAX_DIM = 65536, MAX_VOCAB = 1 << 24, MAX_LD = 1 << 21;
-// Bytes of a piece's gradients with respect to the logits (at least
-// PIECE_LEAST columns, whatever the rows).
+// Bytes of a piece's gradients with respect to the logits, or PIECE_LEAST columns of them
+// where that is more: with the most rows 4 GiB of bfloat16, 8 of binary32.
 constexpr int64_t PIECE_BYTES = int64_t(512) << 20, PIECE_LEAST = 2048;
+// The products reach the rows of a tile (256 at most, of those that there are) by 32-bit
+// offsets: those of the caller's tensors, and of a piece, which is wide where rows are few
+// (up to MAX_VOCAB columns, rounded up to whole tiles).
+static_assert(256 * MAX_LD * 4 < int64_t(1) << 32 && 256 * (PIECE_LEAST + 255) * 4 < int64_t(1) << 32 &&
+              PIECE_BYTES + 256 * 255 * 4 < int64_t(1) << 32, "offsets in a tile");
 
 // Up to so many rows the forward pass takes x as it lies, the rows without a target
 // among them: packing would be a launch of its own (8 us of 42 for one row over 32768 x

@@ -113,7 +113,9 @@ struct Source {
   const char* base;     // element (row 0 of the tile, k = 0)
   const char* begin;    // first byte of the tensor
   const char* end;      // one past its last
-  uint32_t ld;          // row stride in bytes (2^23 at most)
+  // row stride in bytes: 2^23 at most, the head's logits' gradients (few rows of a long
+  // vocabulary) 2^26; the rows of a tile that there are span less than 2^32
+  uint32_t ld;
   int valid;            // rows (row form) or columns (k-row form) of the tile that exist
 };
 
@@ -867,8 +869,8 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
   u32x4 rp[S::CP], rq[S::CQ];
   Loads<S::CP> lp;
   Loads<S::CQ> lq;
-  // bytes from one stage of an operand in k-row form to the next (64 k-rows of 2^22
-  // bytes, or 32 of 2^23: 2^28 at most)
+  // bytes from one stage of an operand in k-row form to the next: 64 k-rows of 2^25 bytes,
+  // or 32 of 2^26, 2^31 at most
   const uint32_t step_p = uint32_t(S::KE * a.ld_p * S::ESZ), step_q = uint32_t(S::KE * a.ld_q * S::ESZ);
   // (a group without rows has one of zeros)
   auto stages = [](const Tile& t) { return max(1, (t.k + S::KE - 1) / S::KE); };
