@@ -1003,10 +1003,12 @@ def muon_experts_product_vjp(x, w=None, offsets=None, grad_y=None, grad_x=None, 
 
 class _HeadArgs(_OperatorArgs):
     def _describe(self, x, w, gx, gw, softcap, ignore_index):
-        self.softcap, self.ignore_index = softcap, ignore_index
         if x.dim() != 2 or w.dim() != 2:
             raise ValueError("x must be (rows, dim) and w (vocab, dim)")
         d = self.desc = HeadDesc()
+        self.softcap, self.ignore_index = softcap, ignore_index
+        d.softcap = 0.0 if softcap is None else float(softcap)
+        d.ignore_index = -100 if ignore_index is None else int(ignore_index)
         d.rows, d.dim, d.vocab = int(x.shape[0]), int(x.shape[1]), int(w.shape[0])
         self.shaped("w", (d.vocab, d.dim), x.dtype)
         self.shaped("targets", (d.rows,), torch.int64)
@@ -1025,20 +1027,19 @@ class _HeadArgs(_OperatorArgs):
             self.shaped("grad_w", (d.vocab, d.dim), x.dtype)
             d.ld_grad_w = _ld(gw, "grad_w")
 
-    def _agreed(self, name, given, default):
-        held = getattr(self, name)
-        if given is None:
-            return default if held is None else held
-        if held is not None and given != held:
-            raise ValueError(f"{name} is {given} in the call and {held} in its {type(self).__name__}")
-        return given
-
     def described(self, softcap, ignore_index):
         """The descriptor of a call.  What the arguments were built with holds where the call gives nothing; a call
         that gives something else is refused: its gradient would be that of another loss."""
         desc = HeadDesc.from_buffer_copy(self.desc)
-        desc.softcap = float(self._agreed("softcap", softcap, 0.0))
-        desc.ignore_index = int(self._agreed("ignore_index", ignore_index, -100))
+        if softcap is not None:
+            if self.softcap is not None and softcap != self.softcap:
+                raise ValueError(f"softcap is {softcap} in the call and {self.softcap} in its {type(self).__name__}")
+            desc.softcap = float(softcap)
+        if ignore_index is not None:
+            if self.ignore_index is not None and ignore_index != self.ignore_index:
+                raise ValueError(f"ignore_index is {ignore_index} in the call and {self.ignore_index} in its "
+                                 f"{type(self).__name__}")
+            desc.ignore_index = int(ignore_index)
         return desc
 
     def workspace_bytes(self) -> int:

@@ -262,11 +262,6 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// Rows of a group, on average, up to which a product is streamed (two rows of 1536 by
-// 6144: 9.1 us, 15.5 on tiles of 32 x 128; 96 rows of 6144 over 32 experts by 1536: 91 and
-// 112).
-constexpr int64_t STREAM_ROWS = 16;
-
 // The fastest plan by a model of the time, in us: full rounds of tiles over the GPU and a
 // last one that fills a part of it, a stage of k (64 of bfloat16, 32 of binary32) measured
 // for each shape with every workgroup busy (`stage`) and with a quarter of them
@@ -299,17 +294,48 @@ double tiles_us(const Kind& s, double tiles, double stages, int cus) {
   return us;
 }
 
+// Few rows, where Q's way from memory is most of a product: the stream (product_stream.hip)
+// or tiles that are not cut.  Up to 16 rows a group on average, the stream where it is
+// faster by this: the turns of its workgroups (1024 at a time), Q from memory, and from the
+// caches x once for every 32 columns and Q again for every further 16 rows of a group; tiles
+// take 8 us and Q from memory at least.  Measured, stream and tiles, us, the rows spread
+// evenly / at random / all to one expert:
+//   bfloat16  64 experts, 1536 to 2048, a row each       86 /  43 /  17     73 /  42 /  12
+//                                       16 rows         110 / 133 /  89     77 /  86 /  19
+//             8 experts, 1536 to 6144,  a row each       29 /  21 /   9     32 /  24 /  21
+//                                       4 rows           30 /  30 /  13     25 /  25 /  12
+//             32 experts, 768 to 256,   8 rows            8 /  10 /   8     12 /  17 /  39
+//             32 experts, 6144 to 1536, 3 rows           90                112
+//             one, 1536 to 6144,        1 to 16 rows      7 to 8            13
+//   binary32  64 experts, 1536 to 2048, a row each      170 /  95 /  22    177 / 119 /  36
+//                                       16 rows         208 / 236 / 151    176 / 191 /  64
+//             8 experts, 1536 to 6144,  8 rows           64 /  60 /  32     69 /  64 /  40
+//             32 experts, 768 to 256,   16 rows          11 /  16 /  10     18 /  26 /  47
+// With more than 16 rows tiles are faster (64 experts, bfloat16, 24 rows 78 and 167).
+constexpr int64_t STREAM_ROWS = 16;
+struct StreamRates {
+  double turn, once, again, tiles;     // us, and bytes a us
+};
+constexpr StreamRates STREAM_BF16 = {6.5, 7.2e6, 7.2e6, 6.0e6}, STREAM_F32 = {8.5, 6.4e6, 11.0e6, 4.8e6};
+bool stream_rows(const ProductArgs& a, double tiles_us) {
+  const StreamRates& s = a.f32 ? STREAM_F32 : STREAM_BF16;
+  const double rows = a.rows, used = std::min(rows, double(std::max(1, a.groups)));
+  const double units = std::max(used, rows / 16 + used / 2), nt = double(ceil_div(a.n, STREAM_TILE_N));
+  const double row = double(a.k) * (a.f32 ? 4 : 2), once = used * a.n * row;
+  const double again = (units - used) * a.n * row + nt * rows * row;
+  return std::max(5.0, s.turn * units * nt / 1024) + once / s.once + again / s.again < std::max(tiles_us, 8.0 + once / s.tiles);
+}
+
 ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus) {
   const int64_t esz = a.f32 ? 4 : 2, ke = 128 / esz;
   // 16-byte loads (product_tile.h)
   if (a.p_elems * esz < 16 || a.q_elems * esz < 16 || (form == FORM_TN && a.ld_p * esz < 16) ||
       (form != FORM_NT && a.ld_q * esz < 16))
     return {SHAPE_NAIVE, 0, 0, 0};
-  // few rows: Q's way from memory is all (a launch takes fewer than 2^32 threads)
-  if (form == FORM_NT && epi != EPI_DZ && a.k % (16 / esz) == 0 && a.rows <= STREAM_ROWS * std::max(1, a.groups) &&
-      (epi != EPI_STORE || (!a.add && !a.map && a.out_f32 == a.f32)) &&
-      ceil_div(a.n, STREAM_TILE_N) * (a.rows / 16 + std::min(a.groups, a.rows)) <= (1 << 22))
-    return {SHAPE_STREAM, 0, 0, 0};
+  // (a launch takes fewer than 2^32 threads)
+  const bool few = form == FORM_NT && epi != EPI_DZ && a.k % (16 / esz) == 0 && a.rows <= STREAM_ROWS * std::max(1, a.groups) &&
+                   (epi != EPI_STORE || (!a.add && !a.map && a.out_f32 == a.f32)) &&
+                   ceil_div(a.n, STREAM_TILE_N) * (a.rows / 16 + std::min(a.groups, a.rows)) <= (1 << 22);
   const bool tn = form == FORM_TN;
   const Kind* kinds = a.f32 ? (tn ? KINDS_F32_TN : KINDS_F32) : (tn ? KINDS_TN : KINDS);
   const int nkinds = a.f32 ? (tn ? 2 : 3) : tn ? 3 : epi == EPI_STORE ? 4 : 3;
@@ -333,7 +359,7 @@ ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus) {
       const int64_t stages = ceil_div(a.k, ke);
       if (mt * nt > (int64_t(1) << 30)) continue;        // tiles are counted in 31 bits
       offer(s.shape, 1 << 30, 0, tiles_us(s, double(mt * nt), double(stages), cus), false);
-      for (int cut = 2; cut <= 32 && epi == EPI_STORE && mt * nt < 2 * cus * s.per_cu; ++cut) {
+      for (int cut = 2; cut <= 32 && epi == EPI_STORE && !few && mt * nt < 2 * cus * s.per_cu; ++cut) {
         const int64_t each = ceil_div(stages, cut);
         if (each < 4) break;
         if (ceil_div(stages, each) != cut) continue;
@@ -369,6 +395,7 @@ ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus) {
       }
     }
   }
+  if (few && stream_rows(a, least)) return {SHAPE_STREAM, 0, 0, 0};
   return best;
 }
 

@@ -127,6 +127,41 @@ def test_few_rows(inn, out, counts, dtype):
     run_all(counts, inn, out, dtype, spare=1)
 
 
+# at most 16 rows an expert on average, and many of them to one
+FEW_TO_ONE = [
+    ([0] * 9 + [200] + [3, 0] * 11, 768, 256),           # streamed, many blocks of rows an expert
+    ([0] * 20 + [900] + [1] * 43, 264, 520),
+    ([300] + [0] * 7 + [2] * 24, 1544, 2041),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,inn,out", FEW_TO_ONE)
+def test_few_rows_most_of_one_expert(counts, inn, out, dtype):
+    run_all(counts, inn, out, dtype, spare=2, first=1)
+
+
+def test_few_rows_that_all_go_to_one_expert_take_no_multiple_of_their_time():
+    """1024 rows of 64 experts, all of one, against 1024 rows of a single expert: not three times the time."""
+    x, y = torch.ones(1024, 1536, dtype=torch.bfloat16, device="cuda"), torch.zeros(1024, 2048, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, 2048, 1536, dtype=torch.bfloat16, device="cuda")
+
+    def ms(w, off):
+        args, times = mb.ExpertsArgs(x, w, off, y), []
+        for _ in range(7):
+            start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda.synchronize()
+            start.record()
+            for _ in range(10):
+                mb.muon_experts_product(args)
+            end.record()
+            torch.cuda.synchronize()
+            times.append(start.elapsed_time(end))
+        return sorted(times)[3]
+
+    assert ms(w, offsets_of([0] * 40 + [1024] + [0] * 23)) < 3 * ms(w[:1], offsets_of([1024]))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_few_rows_in_ranges_that_overlap(dtype):
     """Ranges with many times the rows that there are, before the one range of a row's own: it is right there."""
