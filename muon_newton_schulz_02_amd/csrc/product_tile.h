@@ -1189,8 +1189,9 @@ hipError_t launch_shape(const ProductArgs& a, int cus, hipStream_t stream) {
 //   binary32, 1024 rows, 768 and 10007: TN 67 us, 128 x 128 tiles 75; 193 to 211 TFLOP/s of
 //   binary32 products, 1.16 to 1.27 PFLOP/s of the bfloat16 ones they are made of
 // Narrow (128 x 64, four waves, two workgroups a unit) is for few columns (Kind).
-// Medium: 1337 x 333 to 20011 of 60 % ignored rows, NN 24 us; Small (32 rows): 634 rows of 42 by
-// 6457 20.6 us, Medium 20.1, Large 26.
+// Medium: 1337 x 333 to 20011 of 60 % ignored rows, NN 24 us.  Small (32 rows), for few:
+// 64 experts of 24 rows, 1536 to 2048, 78 us, 89 without it; 32 of 24, 768 to 256, 8.6 and 17.5;
+// the loss of 17 to 64 rows of 1536 by 32768 24.5 and 28, of 768 by 10007 14 and 19.5 (bfloat16).
 using Large = Shape<256, 256, 2, 4, false>;
 using Medium = Shape<128, 128, 2, 2, false>;
 using MediumTn = Shape<128, 256, 2, 4, false>;
