@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libmuon_mi355x.so")
 
 SOURCES = ["muon_api.cpp", "elementwise.hip", "ns_gemm.hip", "ns_chain.hip", "adamw.hip", "probe.hip",
            "noalloc.hip", "muon_blocks.cpp", "blocks_gram.hip", "blocks_iterate.hip", "blocks_apply.hip",
-           "op_workspace.cpp", "muon_experts.cpp", "muon_head.cpp", "products.hip", "head_rows.hip",
+           "op_workspace.cpp", "muon_experts.cpp", "muon_head.cpp", "products_plan.cpp", "products.hip", "head_rows.hip",
            "product_stream.hip", "product_nt.hip", "product_nn.hip", "product_tn.hip"]
 ARCH = os.environ.get("MUON_OFFLOAD_ARCH", "gfx950")
 

@@ -20,7 +20,7 @@ enum ProductForm : int { FORM_NT = 0, FORM_NN = 1, FORM_TN = 2 };
 //   LSE    a maximum and a sum of exponentials for every row and tile of columns,
 //          and the target's logit
 //   DZ     the gradient of the loss with respect to the logits C
-// (_CAP: with a soft cap, _LARGE_CAP: of bfloat16 operands above FAST_CAP; launch_product
+// (_CAP: with a soft cap, _LARGE_CAP: of bfloat16 operands above FAST_CAP; product_epilogue
 // chooses.)
 enum ProductEpilogue : int {
   EPI_STORE = 0, EPI_LSE = 1, EPI_DZ = 2, EPI_LSE_CAP = 3, EPI_DZ_CAP = 4, EPI_LSE_LARGE_CAP = 5, EPI_DZ_LARGE_CAP = 6
@@ -77,7 +77,7 @@ hipError_t launch_tn(int shape, const ProductArgs& a, int cus, hipStream_t strea
 // NT, STORE (without an addend or a map, out of the operands' type) and LSE, k a multiple
 // of 16 bytes.
 hipError_t launch_stream(int epi, const ProductArgs& a, hipStream_t stream);
-constexpr int STREAM_TILE_N = 32;
+constexpr int STREAM_TILE_N = 32, NAIVE_TILE_N = 16;
 
 // How a product runs.  k may be cut into chunks, so that few tiles fill the GPU and
 // one long group does not hold up the rest: a tile then takes `chunk` of k, writes
@@ -95,6 +95,8 @@ struct ProductPlan {
   size_t queue;                // and these bytes before them (ProductArgs::queue)
 };
 ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus);
+// STORE, LSE or DZ with the kind of soft cap that `a` has.
+int product_epilogue(int epi, const ProductArgs& a);
 // The queue, in int32_t: NUM_XCD counters of tiles taken, QUEUE_STEP apart (a line of
 // memory each), the chunk, then pre[groups + 1] (sums of pieces, the groups with most rows
 // first), order[groups] and slot[groups] (2 s_g).

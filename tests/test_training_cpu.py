@@ -12,6 +12,7 @@ import torch
 import oracle as orc
 from muon_newton_schulz_02_amd import binding as mb
 from muon_newton_schulz_02_amd import build as mbuild
+import training_cases
 
 INCLUDE = os.path.dirname(mb.HEADER)
 BASE = 0x7F0000000000
@@ -257,6 +258,93 @@ def test_oracle_against_differences():
     assert not y[4].any() and not gw[1].any()
     # both sides of <y, gy> as a bilinear form
     assert np.isclose((y * gy)[:4].sum(), (gx * x)[:4].sum()) and np.isclose((y * gy)[:4].sum(), (gw * we).sum())
+
+
+SHAPES = ("naive", "32", "128", "256", "narrow", "stream")
+FORMS = ("NT", "NN", "TN")
+EPILOGUES = ("store", "loss", "grad", "loss, cap", "grad, cap", "loss, large cap", "grad, large cap")
+HIP_INC = "/opt/rocm/include"
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    """The products of calls: lines of host_plan/training_plan.cpp to {name: [(form, epilogue, shape, f32, cut, queued)]}."""
+    gxx = shutil.which("g++")
+    if gxx is None or not os.path.exists(os.path.join(HIP_INC, "hip", "hip_runtime.h")):
+        pytest.skip("needs g++ and the HIP headers")
+    here = os.path.dirname(os.path.abspath(__file__))
+    csrc = os.path.join(os.path.dirname(mb.LIB_PATH), "csrc")
+    exe = str(tmp_path_factory.mktemp("plan") / "training_plan")
+    cmd = [gxx, "-std=c++17", "-O1", "-Wall", "-Wno-unused-result", "-D__HIP_PLATFORM_AMD__", "-I", HIP_INC, "-I", INCLUDE,
+           "-I", csrc, "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined", "-o", exe,
+           os.path.join(here, "host_plan", "training_plan.cpp"),
+           *(os.path.join(csrc, f) for f in ("muon_experts.cpp", "muon_head.cpp", "products_plan.cpp"))]
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-4000:]
+
+    def run(lines):
+        r = subprocess.run([exe], input="\n".join(lines), capture_output=True, text=True, timeout=120,
+                           env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0"))
+        assert r.returncode == 0 and "FAIL" not in r.stdout and "OUTSIDE" not in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+        got = {}
+        for line in r.stdout.splitlines():
+            name, *v = line.split()
+            form, epi, shape, f32, cut, queued = map(int, v)
+            got.setdefault(name, []).append((FORMS[form], EPILOGUES[epi], SHAPES[shape], "f32" if f32 else "bf16", cut, queued))
+        return got
+    return run
+
+
+def _head_lines(sizes, dtype, cap):
+    return [f"head {r}x{d}x{v} {r} {d} {v} {int(dtype == 'f32')} {cap}" for r, d, v in sizes]
+
+
+def test_every_kernel_of_the_head_has_a_test(plan):
+    """The sizes of tests/test_gpu_head.py reach each kernel of the logits: every shape, soft cap and type, k in whole 16
+    bytes and not; and the gradients' products on each shape, cut and not."""
+    logits, products = set(), set()
+    for dtype, caps in training_cases.HEAD_TILES_CAPS.items():
+        for cap in caps:
+            sizes = training_cases.HEAD_TILES + (training_cases.HEAD_LARGE if cap != 40.0 else [])
+            for name, got in plan(_head_lines(sizes, dtype, cap)).items():
+                whole = int(name.split("x")[1]) % 8 == 0
+                logits |= {(e, s, t, whole) for f, e, s, t, _, _ in got if f == "NT"}
+                products |= {(f, s, t, cut) for f, e, s, t, cut, _ in got if f != "NT"}
+    for dtype, kinds in (("bf16", ("", ", cap", ", large cap")), ("f32", ("", ", cap"))):
+        for kind in kinds:
+            for shape in ("128", "256"):
+                for whole in (False, True):
+                    assert {("loss" + kind, shape, dtype, whole), ("grad" + kind, shape, dtype, whole)} <= logits
+    assert {("NN", "256", "bf16", 0), ("NN", "256", "bf16", 1), ("TN", "256", "bf16", 0), ("NN", "128", "bf16", 1),
+            ("TN", "128", "bf16", 0), ("TN", "narrow", "bf16", 0), ("NN", "256", "f32", 0), ("NN", "256", "f32", 1),
+            ("TN", "256", "f32", 1), ("NN", "128", "f32", 1), ("TN", "128", "f32", 1)} <= products
+    small = set()
+    for dtype in ("bf16", "f32"):
+        for cap in (0.0, 15.0):
+            for got in plan(_head_lines(training_cases.HEAD_SIZES, dtype, cap)).values():
+                small |= {(e, s, t) for f, e, s, t, _, _ in got if f == "NT"}
+    for dtype in ("bf16", "f32"):
+        for kind in ("", ", cap"):
+            assert {("loss" + kind, s, dtype) for s in ("naive", "32", "stream")} <= small
+            assert {("grad" + kind, s, dtype) for s in ("naive", "32")} <= small
+
+
+def test_few_rows_are_streamed_only_where_that_is_faster(plan):
+    """The rule's measured sides: (experts, rows an expert, in, out, f32) and whether the product is streamed."""
+    sides = [
+        (64, 16, 1536, 2048, 0, False), (64, 1, 1536, 2048, 0, False), (8, 1, 1536, 6144, 0, True), (8, 4, 1536, 6144, 0, False),
+        (32, 8, 768, 256, 0, True), (32, 3, 6144, 1536, 0, True), (1, 1, 1536, 6144, 0, True), (1, 16, 1536, 6144, 0, True),
+        (64, 24, 1536, 2048, 0, False), (64, 1, 1536, 2048, 1, True), (64, 16, 1536, 2048, 1, False), (8, 8, 1536, 6144, 1, True),
+        (32, 16, 768, 256, 1, True),
+    ]
+    for i, (experts, per, inn, out, f32, streamed) in enumerate(sides):
+        got = plan([f"experts {i} {experts} {experts * per} {inn} {out} {f32} 0 {f32}"])[str(i)]
+        assert (got[0][2] == "stream") == streamed, sides[i]
+        assert got[0][4] == 0 or per > 16           # and needs no workspace
+    counts, inn, out = training_cases.FEW_TO_ONE[0]
+    for f32 in (0, 1):
+        got = plan([f"experts few {len(counts)} {sum(counts) + 3} {inn} {out} {f32} 0 {f32}"])["few"]
+        assert got[0][2] == "stream"
 
 
 def test_no_exception_leaves_a_c_entry(L, tmp_path):
