@@ -9,6 +9,7 @@ import torch
 
 import oracle as orc
 from muon_newton_schulz_02_amd import binding as mb
+from training_cases import FEW_TO_ONE
 
 pytestmark = pytest.mark.gpu
 U = orc.training.U
@@ -125,14 +126,6 @@ def test_large_tiles_and_long_sums():
 @pytest.mark.parametrize("inn,out", [(8, 33), (136, 31), (1544, 65), (2048, 100)])
 def test_few_rows(inn, out, counts, dtype):
     run_all(counts, inn, out, dtype, spare=1)
-
-
-# at most 16 rows an expert on average, and many of them to one
-FEW_TO_ONE = [
-    ([0] * 9 + [200] + [3, 0] * 11, 768, 256),           # streamed, many blocks of rows an expert
-    ([0] * 20 + [900] + [1] * 43, 264, 520),
-    ([300] + [0] * 7 + [2] * 24, 1544, 2041),
-]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

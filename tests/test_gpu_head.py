@@ -7,6 +7,7 @@ import torch
 
 import oracle as orc
 from muon_newton_schulz_02_amd import binding as mb
+from training_cases import HEAD_LARGE, HEAD_TILES, HEAD_TILES_CAPS
 
 pytestmark = pytest.mark.gpu
 DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
@@ -69,6 +70,59 @@ def case(rows, dim, vocab, dtype, *, cap=0.0, ignored=0.0, pad=0, lead=0, scale=
 ])
 def test_sizes(rows, dim, vocab, cap, dtype):
     case(rows, dim, vocab, dtype, cap=cap)
+
+
+@pytest.mark.parametrize("rows,dim,vocab", HEAD_TILES)
+@pytest.mark.parametrize("dtype,cap", [(d, c) for d, caps in HEAD_TILES_CAPS.items() for c in caps])
+def test_tiles_of_each_size(rows, dim, vocab, dtype, cap):
+    x, w, t, *_ = case(rows, dim, vocab, dtype, cap=cap, ignored=0.2, pad=1 if dim % 8 else 0, stray=True, seed=rows)
+    assert ((t >= vocab - 131) & (t < vocab)).any()         # targets in the last tile
+
+
+@pytest.mark.parametrize("rows,dim,vocab", HEAD_LARGE)
+@pytest.mark.parametrize("dtype,cap", [("bf16", 15.0), ("bf16", 0.0), ("f32", 15.0)])
+def test_gradients_on_the_largest_tiles(rows, dim, vocab, dtype, cap):
+    """Against float64 on the GPU; the bounds of oracle/training_oracle.py, element by element."""
+    dt, u = DTYPES[dtype], 2.0 ** -24
+    gen = torch.Generator().manual_seed(77)
+    x, w = matrix(rows, dim, dt, gen), matrix(vocab, dim, dt, gen, scale=dim ** -0.5 * 2)
+    t = torch.randint(vocab, (rows,), generator=gen)
+    t[torch.rand(rows, generator=gen) < 0.1] = -100
+    t, g = t.cuda(), torch.randn(rows, generator=gen).cuda()
+    loss, lse = torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda")
+    gx, gw = torch.full_like(x, float("nan")), torch.full_like(w, float("nan"))
+    mb.muon_head_loss(x, w, t, loss, lse, softcap=cap)
+    mb.muon_head_loss_vjp(x, w, t, lse, g, gx, gw, softcap=cap)
+    seen = t >= 0
+    assert (gx[~seen] == 0).all() and (loss[~seen] == 0).all()
+    xd, wd, at, gd = x.double()[seen], w.double(), t[seen], g.double()[seen, None]
+    row = torch.arange(len(at), device="cuda")
+    z = xd @ wd.t()
+    tol_z = (dim + 4) * u * (xd.abs() @ wd.abs().t())
+    if cap:
+        z = cap * torch.tanh(z / cap)
+        tol_z += 6 * u * cap
+    want = torch.logsumexp(z, 1, keepdim=True)
+    d = torch.exp(z - want)
+    tol_lse = (d * (tol_z + ((z - z.amax(1, keepdim=True)).abs() + 4) * u)).sum(1, keepdim=True) + 320 * u + 2 * u * want.abs()
+    assert ((lse[seen].double() - want[:, 0]).abs() <= 1.01 * tol_lse[:, 0]).all()
+    picked = z[row, at]
+    assert ((loss[seen].double() - (want[:, 0] - picked)).abs() <= 1.01 * (tol_lse[:, 0] + tol_z[row, at] + 2 * u * picked.abs())
+            + u * want[:, 0].abs()).all()
+    d *= gd
+    tol = d.abs() * (tol_z + tol_lse + ((z - want).abs() + 10) * u)
+    d[row, at] -= gd[:, 0]
+    tol[row, at] += 2 * u * gd[:, 0].abs()
+    if cap:
+        slope = 1 - (z / cap) ** 2
+        tol = tol * slope + d.abs() * (2 * z.abs() / cap ** 2 * tol_z + 6 * u)
+        d *= slope
+    step = torch.finfo(dt).eps / 2
+    tol += step * (d.abs() + tol) + 2.0 ** -126 * (gd.abs() + 2)
+    for got, ref, off in ((gx[seen], d @ wd, tol @ wd.abs() + (vocab + 68) * u * (d.abs() @ wd.abs())),
+                          (gw, d.t() @ xd, tol.t() @ xd.abs() + (len(at) + 4) * u * (d.abs().t() @ xd.abs()))):
+        off = off + step * (ref.abs() + off) + 1e-30
+        assert ((got.double() - ref).abs() <= off).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -172,6 +226,47 @@ def test_non_finite_logits():
     gx = torch.zeros_like(x)
     mb.muon_head_loss_vjp(x, w, t, lse, torch.ones(6, device="cuda"), gx)
     assert torch.isfinite(gx[[0, 3, 4, 5]]).all() and torch.isnan(gx[1]).all() and torch.isnan(gx[2]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cap", [0.0, 15.0, 50.0])
+@pytest.mark.parametrize("rows,dim,vocab", [(6, 32, 90), (6, 6, 90), (300, 72, 3000), (900, 200, 4227), (1030, 200, 7299)])
+def test_nan_and_infinity_stay_in_their_rows(rows, dim, vocab, cap, dtype):
+    """A row with a NaN is NaN.  One with an infinity has infinite logits: without a soft cap its results are not finite;
+    with one, for bfloat16, the logits are the cap or minus it, and their slope is 0.  Other rows keep their bits."""
+    dt = DTYPES[dtype]
+    gen = torch.Generator().manual_seed(51)
+    x, w = matrix(rows, dim, dt, gen), matrix(vocab, dim, dt, gen)
+    w[w == 0] = 1.0
+    t = torch.randint(vocab, (rows,), generator=gen).cuda()
+    ones = torch.ones(rows, device="cuda")
+
+    def run(x):
+        loss, lse, gx = torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda"), torch.zeros(rows, dim, dtype=dt, device="cuda")
+        mb.muon_head_loss(x, w, t, loss, lse, softcap=cap)
+        mb.muon_head_loss_vjp(x, w, t, lse, ones, gx, softcap=cap)
+        return loss, lse, gx
+
+    clean = run(x)
+    bad = x.clone()
+    a, b, c = 1, rows // 2, rows - 1
+    bad[a, dim - 1], bad[b, 0], bad[c, 3] = float("nan"), float("inf"), float("-inf")
+    got = run(bad)
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[[a, b, c]] = False
+    for u, v in zip(clean, got):
+        assert torch.equal(u[keep], v[keep]) and torch.isfinite(u).all()
+    assert torch.isnan(got[0][a]) and torch.isnan(got[1][a]) and torch.isnan(got[2][a]).all()
+    for r, column, sign in ((b, 0, 1.0), (c, 3, -1.0)):
+        if cap and dtype == "bf16":
+            z = cap * np.sign(sign * np64(w)[:, column])
+            lse = z.max() + np.log(np.exp(z - z.max()).sum())
+            # the cap to 6 u, the exponentials and their sum to 400
+            tol = 6 * cap * 2.0 ** -24 + 400 * 2.0 ** -24 + 4 * 2.0 ** -24 * abs(lse)
+            assert abs(got[1][r].item() - lse) <= tol and abs(got[0][r].item() - (lse - z[t[r].item()])) <= 2 * tol
+            assert (got[2][r] == 0).all()
+        elif not cap:
+            assert not torch.isfinite(got[1][r]) and not torch.isfinite(got[0][r]) and torch.isnan(got[2][r]).all()
 
 
 def test_gradient_against_differences():
