@@ -28,12 +28,6 @@ __device__ __forceinline__ void copy_row(T* dst, const T* src, int n, int lane) 
   for (int c = whole * V + lane; c < n; c += 64) dst[c] = src ? src[c] : T(0);
 }
 
-// In [1, 2); 1 for zeros, numbers below the normal ones, infinities and NaN.
-__device__ __forceinline__ float significand(float x) {
-  const uint32_t b = __float_as_uint(x), e = b >> 23 & 255;
-  return e == 0 || e == 255 ? 1.f : __uint_as_float((b & 0x7fffff) | 0x3f800000);
-}
-
 // Each workgroup packs `chunk` rows: it counts the rows with a target before
 // them by itself (8 bytes a row, read from L2), which saves a launch and a wait;
 // the chunks are cut so that about a thousand workgroups at most do it.  The copy of x gives
@@ -82,7 +76,6 @@ __global__ __launch_bounds__(NT) void head_rows_kernel(const HeadRows a) {
         a.lse_c[at] = a.lse_in[r];
         a.ga[at] = g + h;
         a.gb[at] = g;
-        if (at == 0 && a.unit) *a.unit = significand(g != 0.f ? g : g + h);
       }
     } else if (r < r1 && a.loss) {
       const float v = t == a.ignore_index ? 0.f : __builtin_nanf("");
@@ -108,7 +101,6 @@ __global__ __launch_bounds__(NT) void head_rows_kernel(const HeadRows a) {
   if (r1 == a.rows && tid == 0) {
     a.offsets[0] = 0;
     a.offsets[1] = pos0;
-    if (pos0 == 0 && a.unit) *a.unit = 1.f;
   }
 }
 

@@ -117,7 +117,7 @@ muon_status check_buffers(const Call& c) {
 
 // Where everything lies in the workspace.
 struct Plan {
-  size_t offsets, unit, row, target, xc, lse, ga, gb, logit, stats, dz, acc, part, bytes;
+  size_t offsets, row, target, xc, lse, ga, gb, rest, logit, stats, dz, acc, part, bytes;
   int64_t ld_xc;       // elements of a packed row of x (and of acc)
   int64_t piece;       // columns of a piece of the vocabulary
   int64_t ld_dz;
@@ -167,7 +167,7 @@ ProductArgs logits_args(const Call& c, const Plan& p, char* ws, int64_t c0, int6
 ProductArgs dz_args(const Call& c, const Plan& p, char* ws, int64_t c0, int64_t n) {
   ProductArgs a = logits_args(c, p, ws, c0, n);
   a.out = ws + p.dz;
-  if (!a.f32) a.unit = reinterpret_cast<const float*>(ws + p.unit);
+  if (!a.f32) a.rest = reinterpret_cast<float*>(ws + p.rest);
   a.ld_out = p.ld_dz;
   return a;
 }
@@ -190,7 +190,9 @@ ProductArgs grad_x_args(const Call& c, const Plan& p, char* ws, const ProductArg
   b.n = int32_t(d.dim);
   b.k = a.n;
   b.f32 = a.f32;
-  b.unit = a.unit;
+  b.target = a.target;
+  b.col0 = a.col0;
+  b.rest = a.rest;
   b.out = last ? c.gx : ws + p.acc;
   b.map = last ? reinterpret_cast<const int32_t*>(ws + p.row) : nullptr;
   b.out_f32 = last ? a.f32 : 1;
@@ -217,7 +219,9 @@ ProductArgs grad_w_args(const Call& c, const Plan& p, const ProductArgs& a) {
   b.m = a.n;
   b.n = int32_t(d.dim);
   b.f32 = b.out_f32 = a.f32;
-  b.unit = a.unit;
+  b.target = a.target;
+  b.col0 = a.col0;
+  b.rest = a.rest;
   b.ld_out = row_stride(d.vocab, d.dim, d.ld_grad_w);
   b.out = reinterpret_cast<char*>(c.gw) + size_t(a.col0) * size_t(b.ld_out) * size_t(esize(d.dtype));
   return b;
@@ -237,7 +241,6 @@ Plan plan_of(const Call& c, int cus) {
   p.ld_xc = round_up(d.dim, 64);
   if (!p.direct) {
     p.offsets = take(8);
-    if (c.op != MUON_HEAD_LOSS && d.dtype != MUON_DTYPE_F32) p.unit = take(4);
     p.row = take(4 * t);
     p.target = take(4 * t);
     p.xc = take(t * p.ld_xc * esz);
@@ -252,6 +255,7 @@ Plan plan_of(const Call& c, int cus) {
     p.lse = take(4 * t);
     p.ga = take(4 * t);
     p.gb = take(4 * t);
+    if (d.dtype != MUON_DTYPE_F32) p.rest = take(4 * t);
     const int64_t most = std::max(PIECE_LEAST, PIECE_BYTES / (std::max<int64_t>(t, 1) * esz));
     // pieces of one size, whole tiles of 256 columns
     const int64_t pieces = (d.vocab + most - 1) / most;
@@ -291,7 +295,6 @@ hipError_t enqueue(const Call& c, const Plan& p, char* ws, int cus, bool capturi
   h.lse_c = reinterpret_cast<float*>(ws + p.lse);
   h.ga = reinterpret_cast<float*>(ws + p.ga);
   h.gb = reinterpret_cast<float*>(ws + p.gb);
-  h.unit = fwd || h.f32 ? nullptr : reinterpret_cast<float*>(ws + p.unit);
   h.loss = fwd ? c.loss : nullptr;
   h.lse_out = fwd ? c.lse : nullptr;
   h.grad_x = c.gx;

@@ -3,15 +3,19 @@
 
 namespace muon {
 
-hipError_t launch_nn(int shape, const ProductArgs& a, int cus, hipStream_t stream) {
+hipError_t launch_nn(int shape, int epi, const ProductArgs& a, int cus, hipStream_t stream) {
   if (a.f32 && shape == SHAPE_LARGE) return launch_shape<LargeF32, FORM_NN, EPI_STORE>(a, cus, stream);
   if (a.f32)
     return shape == SHAPE_SMALL ? launch_shape<SmallF32, FORM_NN, EPI_STORE>(a, cus, stream)
                                 : launch_shape<MediumF32, FORM_NN, EPI_STORE>(a, cus, stream);
-  if (shape == SHAPE_SMALL) return launch_shape<Small, FORM_NN, EPI_STORE>(a, cus, stream);
-  if (shape == SHAPE_NARROW) return launch_shape<Narrow, FORM_NN, EPI_STORE>(a, cus, stream);
-  if (shape == SHAPE_MEDIUM) return launch_shape<Medium, FORM_NN, EPI_STORE>(a, cus, stream);
-  return launch_shape<Large, FORM_NN, EPI_STORE>(a, cus, stream);
+  auto with = [&](auto s) {
+    using S = decltype(s);
+    return epi == EPI_STORE_TARGET ? launch_shape<S, FORM_NN, EPI_STORE_TARGET>(a, cus, stream)
+                                   : launch_shape<S, FORM_NN, EPI_STORE>(a, cus, stream);
+  };
+  if (shape == SHAPE_SMALL) return with(Small{});
+  if (shape == SHAPE_NARROW) return with(Narrow{});
+  return shape == SHAPE_MEDIUM ? with(Medium{}) : with(Large{});
 }
 
 }  // namespace muon

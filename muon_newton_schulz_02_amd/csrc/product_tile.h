@@ -506,12 +506,38 @@ struct Patch {
   float value[S::FP];
 };
 
+// grad_x = dl W (NN): the rest of a row whose target is among the tile's k, and that target's
+// row of W, from which it is added to C.
+struct RowTarget {
+  const uint16_t* q;        // W's row of the target, at the tile's first column
+  int most;                 // four elements from there on end with W
+  bool in;
+  float rest;
+};
+__device__ __forceinline__ RowTarget row_target(const ProductArgs& a, const Tile& t, int r) {
+  const int row = t.lo + t.i0 + min(r, t.m - 1), k = a.target[row] - a.col0 - t.k0;
+  RowTarget z;
+  z.in = r < t.m && k >= 0 && k < t.k;
+  z.rest = z.in ? a.rest[row] : 0.f;
+  const int64_t at = int64_t(t.k0 + (z.in ? k : 0)) * a.ld_q + t.j0;
+  z.most = int(min(a.q_elems - 4 - at, int64_t(1) << 30));
+  z.q = reinterpret_cast<const uint16_t*>(a.q) + at;
+  return z;
+}
+// Four elements of it from column c; what would lie behind W's end is read before it, and shifted.
+__device__ __forceinline__ uint64_t target_run(const RowTarget& z, int c) {
+  typedef uint64_t u64_any __attribute__((aligned(2)));
+  const int o = min(c, z.most);
+  const uint64_t v = *gmem(reinterpret_cast<const u64_any*>(z.q + o)) >> (16 * (c - o) & 63);
+  return z.in ? v : 0;                // a row without a target has read one that may hold anything
+}
+
 // C to `out` through LDS, a part of the tile's rows at a time where all do not fit ROOM
 // bytes.  OF32: out is binary32.  WIDE: staged as binary32 (for binary32 outputs and
-// addends), else as bfloat16.  Multiplied by `unit`.
-template <class S, bool OF32, bool WIDE, int ROOM, bool UNIT = false>
+// addends), else as bfloat16.  TARGET: with what row_target adds.
+template <class S, bool OF32, bool WIDE, int ROOM, bool TARGET = false>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], const Out& out, bool add_f32, const Tile& t, char* stg, int tid,
-                                           const Patch<S>* patch = nullptr, float unit = 1.f) {
+                                           const Patch<S>* patch = nullptr, const ProductArgs* args = nullptr) {
   constexpr int ES = WIDE ? 4 : 2, EP = S::BN * ES + 16;
   constexpr int PASSES = S::BM * EP <= ROOM ? 1 : S::BM / 2 * EP <= ROOM ? 2 : S::BM / 4 * EP <= ROOM ? 4 : 8;
   constexpr int ROWS = S::BM / PASSES;
@@ -528,24 +554,29 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], co
 #pragma unroll 1
   for (int pass = 0; pass < PASSES; ++pass) {
     if (pass > 0) lds_barrier();
-    float factor = unit;
-    if (UNIT) asm volatile("" : "+v"(factor));      // a product of every accumulator would not fit the registers
     char* const lane_at = stg + (lane & 31) * EP + (wq * S::WTQ + 4 * half) * ES;
 #pragma unroll
     for (int i = 0; i < S::FP; ++i) {
       const int r0 = wp * S::WTP + 32 * i - pass * ROWS;
       if (PASSES == 1 || (r0 >= 0 && r0 < ROWS)) {
         char* const at = lane_at + r0 * EP;
+        RowTarget target;
+        if constexpr (TARGET) target = row_target(*args, t, wp * S::WTP + 32 * i + (lane & 31));
 #pragma unroll
         for (int j = 0; j < S::FQ; ++j)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             char* d = at + (32 * j + 8 * g) * ES;
-            float c[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c[e] = UNIT ? acc[j][i][4 * g + e] * factor : acc[j][i][4 * g + e];
-            if constexpr (WIDE) *reinterpret_cast<f32x4*>(d) = f32x4{c[0], c[1], c[2], c[3]};
-            else *reinterpret_cast<u32x2*>(d) = u32x2{float2_to_bf16x2_bits(c[0], c[1]), float2_to_bf16x2_bits(c[2], c[3])};
+            float c0 = acc[j][i][4 * g], c1 = acc[j][i][4 * g + 1], c2 = acc[j][i][4 * g + 2], c3 = acc[j][i][4 * g + 3];
+            if constexpr (TARGET) {
+              const uint64_t v = target_run(target, wq * S::WTQ + 4 * half + 32 * j + 8 * g);
+              c0 = __builtin_fmaf(target.rest, bf16_bits_to_float(uint32_t(v)), c0);
+              c1 = __builtin_fmaf(target.rest, bf16_bits_to_float(uint32_t(v >> 16)), c1);
+              c2 = __builtin_fmaf(target.rest, bf16_bits_to_float(uint32_t(v >> 32)), c2);
+              c3 = __builtin_fmaf(target.rest, bf16_bits_to_float(uint32_t(v >> 48)), c3);
+            }
+            if constexpr (WIDE) *reinterpret_cast<f32x4*>(d) = f32x4{c0, c1, c2, c3};
+            else *reinterpret_cast<u32x2*>(d) = u32x2{float2_to_bf16x2_bits(c0, c1), float2_to_bf16x2_bits(c2, c3)};
             if (g == 3) __builtin_amdgcn_sched_barrier(0);   // else all are rounded before any is stored
           }
         // after this lane's own write of the column, in order
@@ -686,12 +717,11 @@ __device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const
   const int lane = tt & 63, w = tt >> 6, wq = w % S::WN, wp = w / S::WN;
   const int c0 = wq * S::WTQ + 4 * (lane >> 5);
   const SoftCap cap = soft_cap(a);
-  const float per_unit = S::F32 ? 1.f : 1.f / *a.unit;
 #pragma unroll
   for (int i = 0; i < S::FP; ++i) {
     const int r = min(wp * S::WTP + 32 * i + (lane & 31), t.m - 1) + t.i0;
     const int target = target_of(a, r) - t.j0;
-    const float lse = a.lse[r] * LOG2E, ga = a.ga[r] * per_unit;
+    const float lse = a.lse[r] * LOG2E, ga = a.ga[r];
     const bool mine = target >= wq * S::WTQ && target < (wq + 1) * S::WTQ && ((target >> 2) & 1) == (lane >> 5);
     patch.col[i] = mine ? target : -1;
     patch.value[i] = 0.f;
@@ -703,10 +733,11 @@ __device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const
         for (int v = 0; v < 16; ++v) l = target == c0 + 32 * j + 8 * (v >> 2) + (v & 3) ? acc[j][i][v] : l;
       if constexpr (CAP) {
         const float q = cap_r(l, cap);
-        patch.value[i] = (ga * __builtin_amdgcn_exp2f(capped_y<EXACT>(l, q, cap) - lse) - a.gb[r] * per_unit) * cap_slope(q);
+        patch.value[i] = (ga * __builtin_amdgcn_exp2f(capped_y<EXACT>(l, q, cap) - lse) - a.gb[r]) * cap_slope(q);
       } else {
-        patch.value[i] = ga * __builtin_amdgcn_exp2f(__builtin_fmaf(l, LOG2E, -lse)) - a.gb[r] * per_unit;
+        patch.value[i] = ga * __builtin_amdgcn_exp2f(__builtin_fmaf(l, LOG2E, -lse)) - a.gb[r];
       }
+      if (!S::F32 && mine) a.rest[r] = rest_of(patch.value[i]);
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -723,6 +754,96 @@ __device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const
         if (v % 8 == 7) __builtin_amdgcn_sched_barrier(0);
       }
   }
+}
+
+// grad_W = dl^T x (TN): the rests of the tile's rows of k whose target is among its rows of
+// C, as a product of its own: 64 such rows of k at a time, in their order, one element each
+// (rounded to bfloat16: 2^-16 of the target's element), with their rows of x.  How many there
+// are differs by target, all rows may have one; 8192 rows over 32768 columns are a
+// stage or two a tile, and the look for them NNN us.
+template <class S>
+__device__ __forceinline__ void add_targets_tn(f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t, char* smem,
+                                               int* wave_sum, int tid) {
+  using LY = Layout<S, FORM_TN>;
+  constexpr int PER = 8, CHUNK = S::NT * PER, ROOM = 2 * CHUNK;
+  static_assert(!S::F32 && LY::BUF + ROOM * 4 <= LY::BYTES, "the list lies in the second buffer");
+  uint32_t* list = reinterpret_cast<uint32_t*>(smem + LY::BUF);       // row of k 256 + row of C
+  tid = fresh(tid);
+  const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wq = w % S::WN, wp = w / S::WN;
+  const int first = t.lo + t.k0, end = first + t.k, c0 = a.col0 + t.i0, m = min(t.m, S::BM);
+  auto products = [&](int count) {
+    for (int e0 = 0; e0 < count; e0 += S::KE) {
+      lds_barrier();                  // the list is there, the stage before has been read
+      for (int x = tid; x < LY::LP::bytes / 16; x += S::NT) *reinterpret_cast<u32x4*>(smem + 16 * x) = u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < S::CQ; ++i) {
+        int row, byte;
+        chunk_at<S, S::BN, true>(tid + S::NT * i, row, byte);
+        u32x4 v = {0, 0, 0, 0};
+        if (e0 + row < count) {
+          const char* x = reinterpret_cast<const char*>(a.q) + (int64_t(list[e0 + row] >> 8) * a.ld_q + t.j0) * 2;
+          v = *reinterpret_cast<gload16*>((gchar*)(x + (byte < t.n * 2 ? byte : 0)));
+        }
+        *reinterpret_cast<u32x4*>(smem + LY::LP::bytes + row * LY::LQ::pitch + byte) = v;
+      }
+      lds_barrier();
+      if (tid < S::KE && e0 + tid < count) {
+        const uint32_t e = list[e0 + tid];
+        reinterpret_cast<uint16_t*>(smem + tid * LY::LP::pitch)[e & 255] = float_to_bf16_bits(a.rest[e >> 8]);
+      }
+      lds_barrier();
+      lchar* fp = (lchar*)smem + frag_lds<S, S::BM, true>(wp * S::WTP, lane);
+      lchar* fq = (lchar*)smem + LY::LP::bytes + frag_lds<S, S::BN, true>(wq * S::WTQ, lane);
+#pragma unroll 1
+      for (int ks = 0; ks < S::SLABS; ++ks) {
+        u32x4 f[S::FQ + S::FP];
+        read_frags<S, S::BN, true, S::FQ>(f, fq, 0);
+        read_frags<S, S::BM, true, S::FP>(f + S::FQ, fp, 0);
+        fq += 16 * LY::LQ::pitch;
+        fp += 16 * LY::LP::pitch;
+#pragma unroll
+        for (int j = 0; j < S::FQ; ++j)
+#pragma unroll
+          for (int i = 0; i < S::FP; ++i) mfma(acc[j][i], f[j], f[S::FQ + i]);
+      }
+    }
+  };
+  int count = 0;
+#pragma unroll 1
+  for (int b = first; b < end; b += CHUNK) {
+    // this thread's PER rows, those of the threads before it come before them
+    int target[PER], mine = 0;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int r = b + tid * PER + e;
+      target[e] = r < end ? gmem(a.target)[r] - c0 : -1;
+      mine += target[e] >= 0 && target[e] < m ? 1 : 0;
+    }
+    int upto = mine;
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) {
+      const int o = __shfl_up(upto, s);
+      if (lane >= s) upto += o;
+    }
+    if (lane == 63) wave_sum[w] = upto;
+    lds_barrier();
+    int at = count + upto - mine, all = 0;
+#pragma unroll
+    for (int x = 0; x < S::NT / 64; ++x) {
+      if (x < w) at += wave_sum[x];
+      all += wave_sum[x];
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e)
+      if (target[e] >= 0 && target[e] < m) list[at++] = uint32_t(b + tid * PER + e) << 8 | uint32_t(target[e]);
+    count += __builtin_amdgcn_readfirstlane(all);
+    lds_barrier();                    // wave_sum has been read
+    if (count + CHUNK > ROOM || b + CHUNK >= end) {
+      products(count);
+      count = 0;
+    }
+  }
+  lds_barrier();
 }
 
 // ------------------------------------------------------------------ kernel
@@ -850,7 +971,7 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
       return (hi - lo + S::BM - 1) / S::BM;
     });
     const int total = __builtin_amdgcn_readfirstlane(pre[a.groups]) * ((a.n + S::BN - 1) / S::BN) *
-                      (EPI == EPI_STORE ? (a.k + chunk - 1) / chunk : 1);
+                      (epi_store(EPI) ? (a.k + chunk - 1) / chunk : 1);
     const int per = (total + NUM_XCD - 1) / NUM_XCD;
     tile = xcd * per + slot;
     end = min((xcd + 1) * per, total);
@@ -1129,15 +1250,14 @@ __global__ __launch_bounds__(S::NT) void product_kernel(const ProductArgs a) {
       gradient_tile<S, epi_cap(EPI), EXACT>(acc, a, t, tid, patch);
       store_tile<S, S::F32, S::F32, LY::BYTES>(acc, out_of<FORM>(a, t), false, t, smem, tid, &patch);
     } else {
+      if constexpr (EPI == EPI_STORE_TARGET && FORM == FORM_TN) add_targets_tn<S>(acc, a, t, smem, wave_sum, tid);
       const Out out = out_of<FORM>(a, t);
       if constexpr (S::F32) store_tile<S, true, true, LY::BYTES>(acc, out, a.add_f32, t, smem, tid);
       else {
-        float unit = 1.f;
-        constexpr bool UNIT = FORM != FORM_NT;
-        if (UNIT && a.unit && t.part < 0) unit = *a.unit;
-        if (a.out_f32 || t.part >= 0) store_tile<S, true, true, LY::BYTES, UNIT>(acc, out, a.add_f32, t, smem, tid, nullptr, unit);
-        else if (a.add) store_tile<S, false, true, LY::BYTES, UNIT>(acc, out, a.add_f32, t, smem, tid, nullptr, unit);
-        else store_tile<S, false, false, LY::BYTES, UNIT>(acc, out, false, t, smem, tid, nullptr, unit);
+        constexpr bool TARGET = EPI == EPI_STORE_TARGET && FORM == FORM_NN;
+        if (a.out_f32 || t.part >= 0) store_tile<S, true, true, LY::BYTES, TARGET>(acc, out, a.add_f32, t, smem, tid, nullptr, &a);
+        else if (a.add) store_tile<S, false, true, LY::BYTES, TARGET>(acc, out, a.add_f32, t, smem, tid, nullptr, &a);
+        else store_tile<S, false, false, LY::BYTES, TARGET>(acc, out, false, t, smem, tid, nullptr, &a);
       }
     }
     if (!more) break;
@@ -1156,7 +1276,7 @@ hipError_t launch_whole(const ProductArgs& a, int cus, hipStream_t stream) {
   // tiles of rows and pieces of k, at most
   const int64_t mt = FORM == FORM_TN ? (a.groups + int64_t(a.rows / a.chunk)) * ((a.m + S::BM - 1) / S::BM)
                                      : (a.rows / S::BM + int64_t(std::min(a.groups, a.rows))) *
-                                           (EPI == EPI_STORE ? (a.k + a.chunk - 1) / a.chunk : 1);
+                                           (epi_store(EPI) ? (a.k + a.chunk - 1) / a.chunk : 1);
   // workgroups that a compute unit holds: by its LDS, and by waves (8 a unit at 256 registers)
   const int fit = std::max(1, std::min(int((160 * 1024) / (lds + 64)), 2048 / S::NT / 4));
   const int64_t grid = std::min<int64_t>((mt * nt + NUM_XCD - 1) / NUM_XCD * NUM_XCD,

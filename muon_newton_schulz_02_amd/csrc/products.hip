@@ -57,7 +57,8 @@ __global__ __launch_bounds__(SMALL_NT) void product_small_kernel(const ProductAr
       const int64_t q0 = tn ? int64_t(lo) * a.ld_q : int64_t(g) * a.es_q;
 #pragma unroll 8
       for (int x = kk; x < k; x += 1 << s.kl) {
-        const float pv = load_as<F32>(a.p, tn ? int64_t(lo + x) * a.ld_p + i : int64_t(lo + i) * a.ld_p + x);
+        float pv = load_as<F32>(a.p, tn ? int64_t(lo + x) * a.ld_p + i : int64_t(lo + i) * a.ld_p + x);
+        if (!F32 && FORM != FORM_NT && a.rest && a.target[lo + (tn ? x : i)] - a.col0 == (tn ? i : x)) pv += a.rest[lo + (tn ? x : i)];
         const float qv = load_as<F32>(a.q, FORM == FORM_NT ? q0 + int64_t(j) * a.ld_q + x : q0 + int64_t(x) * a.ld_q + j);
         c = __builtin_fmaf(pv, qv, c);
       }
@@ -75,7 +76,6 @@ __global__ __launch_bounds__(SMALL_NT) void product_small_kernel(const ProductAr
       if (in) {
         int64_t row = tn ? i : lo + i;
         const int64_t base = tn ? int64_t(g) * a.es_out : 0;
-        if (a.unit) c *= *a.unit;
         if (a.add) c += load1(a.add, base + row * a.ld_add + j, a.add_f32);
         if (a.map) row = a.map[row];
         store1(a.out, base + row * a.ld_out + j, c, a.out_f32);
@@ -94,10 +94,11 @@ __global__ __launch_bounds__(SMALL_NT) void product_small_kernel(const ProductAr
     } else if (in) {
       const SoftCap cap = soft_cap(a);
       const float r = cap_r(c, cap), y = a.cap != 0.f ? capped_y<true>(c, r, cap) : c * LOG2E;
-      const float per_unit = a.unit ? 1.f / *a.unit : 1.f;
-      float d = a.ga[i] * per_unit * __builtin_amdgcn_exp2f(y - a.lse[i] * LOG2E);
-      if (j == target_of(a, i)) d -= a.gb[i] * per_unit;
+      float d = a.ga[i] * __builtin_amdgcn_exp2f(y - a.lse[i] * LOG2E);
+      const bool target = j == target_of(a, i);
+      if (target) d -= a.gb[i];
       if (a.cap != 0.f) d *= cap_slope(r);
+      if (target && !F32) a.rest[i] = rest_of(d);
       store1(a.out, int64_t(i) * a.ld_out + j, d, a.out_f32);
     }
   }
@@ -183,8 +184,7 @@ __global__ __launch_bounds__(RT) void product_sum_kernel(const ProductArgs a) {
         s.w += v[e].w;
       }
     }
-    const float unit = a.unit ? *a.unit : 1.f;
-    float v[4] = {s.x * unit, s.y * unit, s.z * unit, s.w * unit};
+    float v[4] = {s.x, s.y, s.z, s.w};
     if (a.add) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -274,7 +274,7 @@ hipError_t launch_product(int form, int epi, const ProductArgs& args, int cus, c
       if (e != hipSuccess) return e;
     }
     hipError_t e = form == FORM_NT   ? launch_nt(plan.shape, kind, a, cus, stream)
-                   : form == FORM_NN ? launch_nn(plan.shape, a, cus, stream) : launch_tn(plan.shape, a, cus, stream);
+                   : form == FORM_NN ? launch_nn(plan.shape, kind, a, cus, stream) : launch_tn(plan.shape, kind, a, cus, stream);
     if (e == hipSuccess && plan.bytes > plan.queue)
       e = form == FORM_TN ? launch_sum<FORM_TN>(a, cus, stream) : launch_sum<FORM_NT>(a, cus, stream);
     return e;

@@ -81,6 +81,12 @@ __device__ __forceinline__ int target_of(const ProductArgs& a, int i) {
   return t >= 0 && t < a.n ? int(t) : -1;
 }
 
+// What rounding to bfloat16 leaves of a number; 0 where that is infinite or NaN.
+__device__ __forceinline__ float rest_of(float v) {
+  const float r = v - bf16_bits_to_float(float_to_bf16_bits(v));
+  return fabsf(r) < INFINITY ? r : 0.f;
+}
+
 // Softmax in base 2: exponents are y = z log2 e, so that an exponential is one fma and
 // one v_exp_f32.  With a soft cap z = cap tanh(l / cap), |z| = cap (1 - 2 r), r = 1 / (1 +
 // e^(2 |l| / cap)), whose slope in l is 4 r (1 - r).  (r of l itself would be next to 1 for

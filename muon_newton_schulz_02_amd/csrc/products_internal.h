@@ -20,14 +20,18 @@ enum ProductForm : int { FORM_NT = 0, FORM_NN = 1, FORM_TN = 2 };
 //   LSE    a maximum and a sum of exponentials for every row and tile of columns,
 //          and the target's logit
 //   DZ     the gradient of the loss with respect to the logits C
+//   STORE_TARGET  (NN, TN of bfloat16 gradients of the logits) C with what these hold of
+//          their targets made whole by `rest`, stored
 // (_CAP: with a soft cap, _LARGE_CAP: of bfloat16 operands above FAST_CAP; product_epilogue
 // chooses.)
 enum ProductEpilogue : int {
-  EPI_STORE = 0, EPI_LSE = 1, EPI_DZ = 2, EPI_LSE_CAP = 3, EPI_DZ_CAP = 4, EPI_LSE_LARGE_CAP = 5, EPI_DZ_LARGE_CAP = 6
+  EPI_STORE = 0, EPI_LSE = 1, EPI_DZ = 2, EPI_LSE_CAP = 3, EPI_DZ_CAP = 4, EPI_LSE_LARGE_CAP = 5, EPI_DZ_LARGE_CAP = 6,
+  EPI_STORE_TARGET = 7
 };
+constexpr bool epi_store(int e) { return e == EPI_STORE || e == EPI_STORE_TARGET; }
 constexpr bool epi_lse(int e) { return e == EPI_LSE || e == EPI_LSE_CAP || e == EPI_LSE_LARGE_CAP; }
 constexpr bool epi_dz(int e) { return e == EPI_DZ || e == EPI_DZ_CAP || e == EPI_DZ_LARGE_CAP; }
-constexpr bool epi_cap(int e) { return e >= EPI_LSE_CAP; }
+constexpr bool epi_cap(int e) { return e >= EPI_LSE_CAP && e <= EPI_DZ_LARGE_CAP; }
 // Up to this cap logits of bfloat16 operands take the soft cap's short form, whose error of
 // 5 2^-24 cap is then no more than that of a binary32 logit of the cap's size.
 constexpr float FAST_CAP = 32.f;
@@ -63,8 +67,10 @@ struct ProductArgs {
   const float* lse;
   const float* ga;             // grad_loss + grad_lse
   const float* gb;             // grad_loss
-  // STORE of NN and TN: what C is multiplied by, DZ: divided by, or null (HeadRows::unit)
-  const float* unit;
+  // bfloat16 gradients of the logits: what the rounding leaves of every row's element in the
+  // target's column, by far the largest (0.9999 of the sum of squares in the d24 head's
+  // gradient).  DZ writes it, STORE of NN (P) and TN (P) adds it; null: binary32
+  float* rest;
   float* logit;                // the target's logit (soft-capped)
   float2* stats;               // [row][tile], with y = z log2 e: maximum of y, sum of 2^(y - maximum)
 };
@@ -72,8 +78,8 @@ struct ProductArgs {
 // Tile shapes.
 enum ProductShape : int { SHAPE_NAIVE = 0, SHAPE_SMALL = 1, SHAPE_MEDIUM = 2, SHAPE_LARGE = 3, SHAPE_NARROW = 4, SHAPE_STREAM = 5 };
 hipError_t launch_nt(int shape, int epi, const ProductArgs& a, int cus, hipStream_t stream);
-hipError_t launch_nn(int shape, const ProductArgs& a, int cus, hipStream_t stream);
-hipError_t launch_tn(int shape, const ProductArgs& a, int cus, hipStream_t stream);
+hipError_t launch_nn(int shape, int epi, const ProductArgs& a, int cus, hipStream_t stream);
+hipError_t launch_tn(int shape, int epi, const ProductArgs& a, int cus, hipStream_t stream);
 // NT, STORE (without an addend or a map, out of the operands' type) and LSE, k a multiple
 // of 16 bytes.
 hipError_t launch_stream(int epi, const ProductArgs& a, hipStream_t stream);
@@ -124,12 +130,6 @@ struct HeadRows {
   float* lse_c;
   float* ga;
   float* gb;
-  // bfloat16 gradient: the significand of the first row's grad_loss, in [1, 2).  Gradients of
-  // the logits are kept in this unit: with one grad_loss for all rows (a mean's) the
-  // target's element, the largest by far, is then just below a power of two, where
-  // bfloat16's steps are finest relative to it, instead of wherever grad_loss puts it for
-  // all rows at once (1859 rows of 24 by 1815: grad_x 2.1e-3 from float64, not 2.6e-3).
-  float* unit;
   float* loss;                 // forward: written where there is no target
   float* lse_out;
   void* grad_x;                // gradient: zeroed where there is no target; may be null

@@ -150,7 +150,8 @@ ProductPlan product_plan(int form, int epi, const ProductArgs& a, int cus) {
 }
 
 int product_epilogue(int epi, const ProductArgs& a) {
-  if (epi == EPI_STORE || a.cap == 0.f) return epi;
+  if (epi == EPI_STORE) return a.rest ? EPI_STORE_TARGET : EPI_STORE;
+  if (a.cap == 0.f) return epi;
   const bool large = !a.f32 && a.cap > FAST_CAP;
   return epi == EPI_LSE ? (large ? EPI_LSE_LARGE_CAP : EPI_LSE_CAP) : (large ? EPI_DZ_LARGE_CAP : EPI_DZ_CAP);
 }

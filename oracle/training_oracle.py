@@ -82,7 +82,10 @@ def head(x, w, targets, softcap=0.0, ignore_index=-100, grad_loss=None, grad_lse
         slope = 1 - (z / softcap) ** 2
         tol = tol * slope + np.abs(d) * (2 * np.abs(z) / softcap ** 2 * tol_z + 6 * U)
         d = d * slope
-    tol = tol + half_step * (np.abs(d) + tol) + TINY * (np.abs(g) + np.abs(h) + 2)
+    rounding = np.full(d.shape, half_step)
+    if half_step > U:
+        rounding[at, t] = half_step ** 2
+    tol = tol + rounding * (np.abs(d) + tol) + TINY * (np.abs(g) + np.abs(h) + 2)
     out["grad_x"], out["tol_grad_x"] = np.zeros((rows, dim)), np.zeros((rows, dim))
     out["grad_x"][seen] = d @ w
     # sums over the vocabulary, then over its pieces (64 of them at most)

@@ -188,7 +188,9 @@ def test_narrow_weights_and_long_sums(inn, out, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_narrow_weights_take_no_multiple_of_wide_ones_time(dtype):
-    """16384 rows, 1536 by 3 columns against 1536 by 8: not 10 times the time (a sum by one thread took 150 times)."""
+    """16384 rows, 1536 by 3 columns against 1536 by 8: not 40 times the time.  The wide one reads 50 MB, 10 us at 5 TB/s at
+    the least, the narrow one takes some 150, so that 15 is what the ratio may come to; a sum by one thread an element took
+    5900, 200 to 600 times."""
     dt = DTYPES[dtype]
     off = offsets_of([16384])
 
@@ -210,7 +212,7 @@ def test_narrow_weights_take_no_multiple_of_wide_ones_time(dtype):
         return took
 
     for narrow in ((1536, 3), (3, 1536)):
-        assert all(a < 10 * b for a, b in zip(ms(*narrow), ms(*sorted((8, 1536), reverse=narrow[0] > narrow[1]))))
+        assert all(a < 40 * b for a, b in zip(ms(*narrow), ms(*sorted((8, 1536), reverse=narrow[0] > narrow[1]))))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

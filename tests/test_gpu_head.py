@@ -326,6 +326,46 @@ def test_one_gradient_of_the_loss_for_all_rows_is_not_rounded(g, first):
             assert abs(scale - 1) < 2.0 ** -11 + 3e-4
 
 
+# rows, dim, vocabulary; the products' shapes as in tests/training_cases.py
+ROUNDED_ONCE = [(50, 24, 300), (700, 200, 3000), (1030, 333, 7299), (1300, 45, 230_000), *HEAD_LARGE]
+
+
+@pytest.mark.parametrize("cap", [0.0, 15.0])
+@pytest.mark.parametrize("targets", ["any", "few", "one"])
+@pytest.mark.parametrize("rows,dim,vocab", ROUNDED_ONCE)
+def test_bfloat16_gradients_are_off_by_their_own_rounding_alone(rows, dim, vocab, targets, cap):
+    """The gradient with respect to a logit is bfloat16 between the products, but the target's, by far the largest, is
+    kept in two parts.  With p of the others at most 0.1 and a sum of their squares of some hundredths, what their rounding
+    adds to the gradients is below 2^-8 / sqrt(3) 0.2 of them, against 2^-9.2 for the results' own rounding: 1.03 times
+    their error at most, in the mean square.  One target for all rows: the sum of all rows' rests in one row of grad_w."""
+    gen = torch.Generator().manual_seed(rows)
+    x = matrix(rows, dim, torch.bfloat16, gen, pad=dim % 2)
+    w = matrix(vocab, dim, torch.bfloat16, gen, scale=dim ** -0.5)
+    t = torch.randint(vocab, (rows,), generator=gen)
+    if targets != "any":
+        t = torch.tensor([vocab - 2, vocab // 3, 0])[t % 3] if targets == "few" else torch.full_like(t, vocab - 1)
+    t[3::10] = -100
+    t, g = t.cuda(), (torch.rand(rows, generator=gen) + 0.5).cuda() / rows
+    loss, lse = torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda")
+    gx, gw = torch.zeros_like(x), torch.zeros_like(w)
+    mb.muon_head_loss(x, w, t, loss, lse, softcap=cap)
+    mb.muon_head_loss_vjp(x, w, t, lse, g, gx, gw, softcap=cap)
+    seen = t >= 0
+    xd, wd, at = x.double()[seen], w.double(), t[seen]
+    z = xd @ wd.t()
+    if cap:
+        z = cap * torch.tanh(z / cap)
+    d = torch.softmax(z, 1)
+    assert d.amax() < 0.2 and d.square().sum(1).mean() < 0.04
+    d[torch.arange(len(at), device="cuda"), at] -= 1
+    d *= g.double()[seen, None]
+    if cap:
+        d *= 1 - (z / cap) ** 2
+    for got, want in ((gx[seen], d @ wd), (gw, d.t() @ xd)):
+        off, own = (got.double() - want).norm(), (want.bfloat16().double() - want).norm()
+        assert off <= 1.03 * own, (off / own).item()
+
+
 def test_one_gradient_at_a_time_is_the_same():
     x, w, t, lse, g, h, gx, gw = case(130, 96, 1500, "bf16", ignored=0.2)
     a, b = torch.zeros_like(gx), torch.zeros_like(gw)

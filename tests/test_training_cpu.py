@@ -262,7 +262,7 @@ def test_oracle_against_differences():
 
 SHAPES = ("naive", "32", "128", "256", "narrow", "stream")
 FORMS = ("NT", "NN", "TN")
-EPILOGUES = ("store", "loss", "grad", "loss, cap", "grad, cap", "loss, large cap", "grad, large cap")
+EPILOGUES = ("store", "loss", "grad", "loss, cap", "grad, cap", "loss, large cap", "grad, large cap", "store, targets")
 HIP_INC = "/opt/rocm/include"
 
 
@@ -302,7 +302,7 @@ def _head_lines(sizes, dtype, cap):
 def test_every_kernel_of_the_head_has_a_test(plan):
     """The sizes of tests/test_gpu_head.py reach each kernel of the logits: every shape, soft cap and type, k in whole 16
     bytes and not; and the gradients' products on each shape, cut and not."""
-    logits, products = set(), set()
+    logits, products, stores = set(), set(), set()
     for dtype, caps in training_cases.HEAD_TILES_CAPS.items():
         for cap in caps:
             sizes = training_cases.HEAD_TILES + (training_cases.HEAD_LARGE if cap != 40.0 else [])
@@ -310,11 +310,13 @@ def test_every_kernel_of_the_head_has_a_test(plan):
                 whole = int(name.split("x")[1]) % 8 == 0
                 logits |= {(e, s, t, whole) for f, e, s, t, _, _ in got if f == "NT"}
                 products |= {(f, s, t, cut) for f, e, s, t, cut, _ in got if f != "NT"}
+                stores |= {(e, t) for f, e, s, t, _, _ in got if f != "NT"}
     for dtype, kinds in (("bf16", ("", ", cap", ", large cap")), ("f32", ("", ", cap"))):
         for kind in kinds:
             for shape in ("128", "256"):
                 for whole in (False, True):
                     assert {("loss" + kind, shape, dtype, whole), ("grad" + kind, shape, dtype, whole)} <= logits
+    assert all(e == ("store, targets" if t == "bf16" else "store") for e, t in stores)
     assert {("NN", "256", "bf16", 0), ("NN", "256", "bf16", 1), ("TN", "256", "bf16", 0), ("NN", "128", "bf16", 1),
             ("TN", "128", "bf16", 0), ("TN", "narrow", "bf16", 0), ("NN", "256", "f32", 0), ("NN", "256", "f32", 1),
             ("TN", "256", "f32", 1), ("NN", "128", "f32", 1), ("TN", "128", "f32", 1)} <= products
