@@ -551,6 +551,14 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], co
   // whole rows of the tile that lie evenly spaced: 32-bit offsets, no questions
   const bool plain = t.n >= S::BN && !out.map && !(WIDE && (out.add || !OF32));
   const uint32_t ld = uint32_t(out.ld * (OF32 ? 4 : 2));
+  // the targets of all of a lane's rows at once, where the registers hold them
+  constexpr bool AHEAD = TARGET && S::FP * S::FQ <= 4;
+  RowTarget target[S::FP];
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int i = 0; i < S::FP; ++i) target[i] = row_target(*args, t, wp * S::WTP + 32 * i + (lane & 31));
+    __builtin_amdgcn_sched_barrier(0);
+  }
 #pragma unroll 1
   for (int pass = 0; pass < PASSES; ++pass) {
     if (pass > 0) lds_barrier();
@@ -560,8 +568,18 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], co
       const int r0 = wp * S::WTP + 32 * i - pass * ROWS;
       if (PASSES == 1 || (r0 >= 0 && r0 < ROWS)) {
         char* const at = lane_at + r0 * EP;
-        RowTarget target;
-        if constexpr (TARGET) target = row_target(*args, t, wp * S::WTP + 32 * i + (lane & 31));
+        // (all of a row's loads before the first is used)
+        float rest = 0.f;
+        uint64_t run[TARGET ? S::FQ : 1][4];
+        if constexpr (TARGET) {
+          if constexpr (!AHEAD) target[i] = row_target(*args, t, wp * S::WTP + 32 * i + (lane & 31));
+          rest = target[i].rest;
+#pragma unroll
+          for (int j = 0; j < S::FQ; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) run[j][g] = target_run(target[i], wq * S::WTQ + 4 * half + 32 * j + 8 * g);
+          __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int j = 0; j < S::FQ; ++j)
 #pragma unroll
@@ -569,11 +587,11 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::FQ][S::FP], co
             char* d = at + (32 * j + 8 * g) * ES;
             float c0 = acc[j][i][4 * g], c1 = acc[j][i][4 * g + 1], c2 = acc[j][i][4 * g + 2], c3 = acc[j][i][4 * g + 3];
             if constexpr (TARGET) {
-              const uint64_t v = target_run(target, wq * S::WTQ + 4 * half + 32 * j + 8 * g);
-              c0 = __builtin_fmaf(target.rest, bf16_bits_to_float(uint32_t(v)), c0);
-              c1 = __builtin_fmaf(target.rest, bf16_bits_to_float(uint32_t(v >> 16)), c1);
-              c2 = __builtin_fmaf(target.rest, bf16_bits_to_float(uint32_t(v >> 32)), c2);
-              c3 = __builtin_fmaf(target.rest, bf16_bits_to_float(uint32_t(v >> 48)), c3);
+              const uint64_t v = run[j][g];
+              c0 = __builtin_fmaf(rest, bf16_bits_to_float(uint32_t(v)), c0);
+              c1 = __builtin_fmaf(rest, bf16_bits_to_float(uint32_t(v >> 16)), c1);
+              c2 = __builtin_fmaf(rest, bf16_bits_to_float(uint32_t(v >> 32)), c2);
+              c3 = __builtin_fmaf(rest, bf16_bits_to_float(uint32_t(v >> 48)), c3);
             }
             if constexpr (WIDE) *reinterpret_cast<f32x4*>(d) = f32x4{c0, c1, c2, c3};
             else *reinterpret_cast<u32x2*>(d) = u32x2{float2_to_bf16x2_bits(c0, c1), float2_to_bf16x2_bits(c2, c3)};
@@ -757,45 +775,93 @@ __device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const
 }
 
 // grad_W = dl^T x (TN): the rests of the tile's rows of k whose target is among its rows of
-// C, as a product of its own: 64 such rows of k at a time, in their order, one element each
+// C, as a product of its own: 64 such rows of k at a time, in a fixed order, one element each
 // (rounded to bfloat16: 2^-16 of the target's element), with their rows of x.  How many there
-// are differs by target, all rows may have one; 8192 rows over 32768 columns are a
-// stage or two a tile, and the look for them NNN us.
+// are differs by target, all rows may have one; 8192 rows over 32768 columns are a stage or two
+// a tile.  8192 x 1536 by 32768 660 us, 652 without; 1337 x 333 by 20011, 60 % ignored, 31 and 26:
+// the waits for targets, rests and rows of x.
 template <class S>
 __device__ __forceinline__ void add_targets_tn(f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t, char* smem,
                                                int* wave_sum, int tid) {
   using LY = Layout<S, FORM_TN>;
-  constexpr int PER = 8, CHUNK = S::NT * PER, ROOM = 2 * CHUNK;
-  static_assert(!S::F32 && LY::BUF + ROOM * 4 <= LY::BYTES, "the list lies in the second buffer");
+  constexpr int PER = 16, CHUNK = S::NT * PER;
+  static_assert(!S::F32 && LY::BUF + CHUNK * 4 <= LY::BYTES, "the list lies in the second buffer");
   uint32_t* list = reinterpret_cast<uint32_t*>(smem + LY::BUF);       // row of k 256 + row of C
   tid = fresh(tid);
   const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wq = w % S::WN, wp = w / S::WN;
   const int first = t.lo + t.k0, end = first + t.k, c0 = a.col0 + t.i0, m = min(t.m, S::BM);
-  auto products = [&](int count) {
+  const char* q = reinterpret_cast<const char*>(a.q) + t.j0 * 2;
+#pragma unroll 1
+  for (int b = first; b < end; b += CHUNK) {
+    // a wave looks through 64 rows of every S::NT
+    const int r0 = b + tid;
+    int target[PER], mine = 0;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      target[e] = c0 - 1;
+      if (b + S::NT * e < end) target[e] = gmem(a.target)[min(r0 + S::NT * e, end - 1)];
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int v = target[e] - c0;
+      target[e] = r0 + S::NT * e < end && v < m ? v : -1;
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e) mine += __popcll(__ballot(target[e] >= 0));
+    if (lane == 0) wave_sum[w] = mine;
+    lds_barrier();
+    int at = 0, count = 0;
+#pragma unroll
+    for (int x = 0; x < S::NT / 64; ++x) {
+      if (x < w) at += wave_sum[x];
+      count += wave_sum[x];
+    }
+    count = __builtin_amdgcn_readfirstlane(count);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const uint64_t votes = __ballot(target[e] >= 0);
+      if (target[e] >= 0) list[at + __popcll(votes & ((uint64_t(1) << lane) - 1))] = uint32_t(r0 + S::NT * e) << 8 | uint32_t(target[e]);
+      at += __popcll(votes);
+    }
+#pragma unroll 1
     for (int e0 = 0; e0 < count; e0 += S::KE) {
       lds_barrier();                  // the list is there, the stage before has been read
-      for (int x = tid; x < LY::LP::bytes / 16; x += S::NT) *reinterpret_cast<u32x4*>(smem + 16 * x) = u32x4{0, 0, 0, 0};
+      // chunks as in a stage: x's rows, and rows of zeros but for a rest
+      u32x4 x[S::CQ];
 #pragma unroll
       for (int i = 0; i < S::CQ; ++i) {
         int row, byte;
         chunk_at<S, S::BN, true>(tid + S::NT * i, row, byte);
-        u32x4 v = {0, 0, 0, 0};
-        if (e0 + row < count) {
-          const char* x = reinterpret_cast<const char*>(a.q) + (int64_t(list[e0 + row] >> 8) * a.ld_q + t.j0) * 2;
-          v = *reinterpret_cast<gload16*>((gchar*)(x + (byte < t.n * 2 ? byte : 0)));
-        }
-        *reinterpret_cast<u32x4*>(smem + LY::LP::bytes + row * LY::LQ::pitch + byte) = v;
+        const uint32_t r = e0 + row < count ? list[e0 + row] >> 8 : first;
+        x[i] = *reinterpret_cast<gload16*>((gchar*)(q + int64_t(r) * a.ld_q * 2 + (byte < t.n * 2 ? byte : 0)));
       }
-      lds_barrier();
-      if (tid < S::KE && e0 + tid < count) {
-        const uint32_t e = list[e0 + tid];
-        reinterpret_cast<uint16_t*>(smem + tid * LY::LP::pitch)[e & 255] = float_to_bf16_bits(a.rest[e >> 8]);
+#pragma unroll
+      for (int i = 0; i < S::CP; ++i) {
+        int row, byte;
+        chunk_at<S, S::BM, true>(tid + S::NT * i, row, byte);
+        const uint32_t e = e0 + row < count ? list[e0 + row] : ~0u;
+        const int d = int(e & 255) * 2 - byte;
+        u32x4 v = {0, 0, 0, 0};
+        if (e != ~0u && d >= 0 && d < 16) {
+          const uint32_t bits = uint32_t(float_to_bf16_bits(a.rest[e >> 8])) << 8 * (d & 2);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) v[z] = d >> 2 == z ? bits : 0;
+        }
+        *reinterpret_cast<u32x4*>(smem + row * LY::LP::pitch + byte) = v;
+      }
+#pragma unroll
+      for (int i = 0; i < S::CQ; ++i) {
+        int row, byte;
+        chunk_at<S, S::BN, true>(tid + S::NT * i, row, byte);
+        if (e0 + row >= count) x[i] = u32x4{0, 0, 0, 0};
+        *reinterpret_cast<u32x4*>(smem + LY::LP::bytes + row * LY::LQ::pitch + byte) = x[i];
       }
       lds_barrier();
       lchar* fp = (lchar*)smem + frag_lds<S, S::BM, true>(wp * S::WTP, lane);
       lchar* fq = (lchar*)smem + LY::LP::bytes + frag_lds<S, S::BN, true>(wq * S::WTQ, lane);
 #pragma unroll 1
       for (int ks = 0; ks < S::SLABS; ++ks) {
+        if (e0 + 16 * ks >= count) break;
         u32x4 f[S::FQ + S::FP];
         read_frags<S, S::BN, true, S::FQ>(f, fq, 0);
         read_frags<S, S::BM, true, S::FP>(f + S::FQ, fp, 0);
@@ -807,43 +873,8 @@ __device__ __forceinline__ void add_targets_tn(f32x16 (&acc)[S::FQ][S::FP], cons
           for (int i = 0; i < S::FP; ++i) mfma(acc[j][i], f[j], f[S::FQ + i]);
       }
     }
-  };
-  int count = 0;
-#pragma unroll 1
-  for (int b = first; b < end; b += CHUNK) {
-    // this thread's PER rows, those of the threads before it come before them
-    int target[PER], mine = 0;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      const int r = b + tid * PER + e;
-      target[e] = r < end ? gmem(a.target)[r] - c0 : -1;
-      mine += target[e] >= 0 && target[e] < m ? 1 : 0;
-    }
-    int upto = mine;
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) {
-      const int o = __shfl_up(upto, s);
-      if (lane >= s) upto += o;
-    }
-    if (lane == 63) wave_sum[w] = upto;
-    lds_barrier();
-    int at = count + upto - mine, all = 0;
-#pragma unroll
-    for (int x = 0; x < S::NT / 64; ++x) {
-      if (x < w) at += wave_sum[x];
-      all += wave_sum[x];
-    }
-#pragma unroll
-    for (int e = 0; e < PER; ++e)
-      if (target[e] >= 0 && target[e] < m) list[at++] = uint32_t(b + tid * PER + e) << 8 | uint32_t(target[e]);
-    count += __builtin_amdgcn_readfirstlane(all);
-    lds_barrier();                    // wave_sum has been read
-    if (count + CHUNK > ROOM || b + CHUNK >= end) {
-      products(count);
-      count = 0;
-    }
+    lds_barrier();                    // list and wave_sum have been read
   }
-  lds_barrier();
 }
 
 // ------------------------------------------------------------------ kernel
