@@ -22,11 +22,14 @@
  *     write out of range.  Rows that lie in more than one range get any values in
  *     y and grad_x.
  *   - Rows before offsets[0] and from offsets[experts] on belong to no expert:
- *     they are not read, and y and grad_x stay as they were there.
+ *     what they hold does not matter, and y and grad_x stay as they were there.
  *   - An expert without rows has grad_W_e = 0 (accumulate: unchanged).
  *   - Elements outside the matrices (row padding, what lies between experts) are
- *     not written, and do not change results.  They may be read within the
- *     tensor, from its first element to its last.
+ *     not written, and do not change results.  They, and rows of no expert, may be
+ *     read within the tensor, from its first element to its last.
+ *   - Tensors overlap (ALIAS where one of them is written) where their address
+ *     ranges, first element to last, do: columns of one buffer beside each other
+ *     are refused, though their elements are apart.
  *   - bfloat16 tensors are multiplied on the bfloat16 matrix cores (products
  *     exact), binary32 ones to binary32 accuracy: a product is off by 2^-24 of
  *     itself at most, and elements below 2^-110 in magnitude count with an error

@@ -20,9 +20,10 @@
  * 15 tanh(x / 15) that "开发者千美元训3.8B模型 击败GPT-2" (aiproducthub.cn),
  * paragraph 影响, lists.
  *
- * The logits are never kept: the forward pass reduces every tile of them to a
- * maximum and a sum a row, the backward pass computes them again a piece of the
- * vocabulary at a time.  Conventions are those of muon_experts.h (workspace,
+ * The loss keeps no logits: it reduces every tile of them to a maximum and a sum
+ * a row, 8 bytes of workspace for 16 to 256 columns.  The gradient computes them again, a piece
+ * of the vocabulary at a time, and holds one piece's dl: 512 MiB of workspace at
+ * most, or 2048 columns where that is more.  Conventions are those of muon_experts.h (workspace,
  * capture and padding included; the two share the library's workspace), and:
  *   - targets is a device array of rows int64.  A row whose target is
  *     ignore_index has loss = lse = 0 and takes no part in the gradients, whatever x,
@@ -31,7 +32,8 @@
  *     gradients either (its grad_x is 0).
  *   - bfloat16: logits, their softmax and all sums are binary32; dl is rounded
  *     to bfloat16 for the two products (relative 2^-8 at most, independent from
- *     element to element, as the rounding of the results).  binary32: to
+ *     element to element), but for the target's element of every row, by far the
+ *     largest, which is kept to 2^-16.  binary32: to
  *     binary32 accuracy throughout (products as in muon_experts.h).
  *   - A row with a NaN or an infinity among its logits has the values that the
  *     formulas give, NaN or infinite, and so have gradients that it takes part in.
