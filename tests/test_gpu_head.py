@@ -7,7 +7,7 @@ import torch
 
 import oracle as orc
 from muon_newton_schulz_02_amd import binding as mb
-from training_cases import HEAD_LARGE, HEAD_TILES, HEAD_TILES_CAPS
+from training_cases import HEAD_LARGE, HEAD_LONG, HEAD_TILES, HEAD_TILES_CAPS
 
 pytestmark = pytest.mark.gpu
 DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
@@ -327,7 +327,7 @@ def test_one_gradient_of_the_loss_for_all_rows_is_not_rounded(g, first):
 
 
 # rows, dim, vocabulary; the products' shapes as in tests/training_cases.py
-ROUNDED_ONCE = [(50, 24, 300), (700, 200, 3000), (1030, 333, 7299), (1300, 45, 230_000), *HEAD_LARGE]
+ROUNDED_ONCE = [(50, 24, 300), (700, 200, 3000), (1030, 333, 7299), (1300, 45, 230_000), *HEAD_LARGE, *HEAD_LONG]
 
 
 @pytest.mark.parametrize("cap", [0.0, 15.0])

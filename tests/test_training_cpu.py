@@ -320,6 +320,8 @@ def test_every_kernel_of_the_head_has_a_test(plan):
     assert {("NN", "256", "bf16", 0), ("NN", "256", "bf16", 1), ("TN", "256", "bf16", 0), ("NN", "128", "bf16", 1),
             ("TN", "128", "bf16", 0), ("TN", "narrow", "bf16", 0), ("NN", "256", "f32", 0), ("NN", "256", "f32", 1),
             ("TN", "256", "f32", 1), ("NN", "128", "f32", 1), ("TN", "128", "f32", 1)} <= products
+    long = [got[3] for got in plan(_head_lines(training_cases.HEAD_LONG, "bf16", 0.0)).values()]
+    assert [(f, s, cut) for f, _, s, _, cut, _ in long] == [("TN", "256", 0), ("TN", "128", 0), ("TN", "narrow", 0), ("TN", "narrow", 1)]
     small = set()
     for dtype in ("bf16", "f32"):
         for cap in (0.0, 15.0):

@@ -9,6 +9,9 @@ HEAD_TILES_CAPS = {"bf16": [0.0, 15.0, 40.0], "f32": [0.0, 15.0]}
 # the gradients' products on the largest tiles too, cut along k and not
 HEAD_LARGE = [(6000, 1537, 6100), (5000, 1536, 12003)]
 
+# more rows than are looked through for a tile's targets at a time (8192, on narrow tiles 4096), on each shape of grad_w
+HEAD_LONG = [(9300, 1536, 8195), (9500, 400, 16000), (9500, 300, 9000), (9500, 45, 15000)]
+
 # head: one element a thread, streamed, tiles of 32 rows
 HEAD_SIZES = [
     (1, 1, 1), (1, 8, 2), (2, 3, 5), (1, 64, 1000), (5, 40, 257), (64, 64, 256), (65, 129, 1023), (300, 96, 2500),
