@@ -7,8 +7,9 @@
 // operands agree.)
 //
 // Two rows through 1536 x 6144 bfloat16 weights of one expert or two (19 or 38 MB) take
-// 9.1 us with the launch, staged 32 x 128 tiles 15.5; 604 MB of 32 experts 81 to 91
-// us, at 6.6 to 7.4 TB/s, and 112.  Those are for k that is not a multiple of 16 bytes.
+// 7.3 to 10.7 us with the launch, staged 32 x 128 tiles 13 to 16; 604 MB of 32 experts 81 to
+// 99 us, at 6.1 to 7.4 TB/s, and 112.  (Tiles are for k that is not a multiple of 16 bytes, and
+// for what the plan finds faster on them.)
 #include "product_tile.h"
 
 namespace muon {

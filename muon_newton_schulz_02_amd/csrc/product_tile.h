@@ -1335,10 +1335,10 @@ hipError_t launch_shape(const ProductArgs& a, int cus, hipStream_t stream) {
 // and LDS; the matrix cores are busy half the time at 1.7 to 2.0 GHz, to which their load
 // brings the clock.  The smaller ones are for what does not fill the GPU with these.
 //   bfloat16, 8192 rows, 1536 and 32768: logits (NT) 755 us, 1.09 PFLOP/s (tiles of 128
-//   x 128 896); dl W (NN, cut in four) 730 to 770 with the sums; dl^T x (TN) 690, 1.19
+//   x 128 896); dl W (NN, cut in four) 725 to 755 with the sums; dl^T x (TN) 660 to 690, 1.2
 //   16384 rows of eight groups, 1536 and 6144: NT 266 to 320 us by the groups' last tiles
-//   binary32, 1024 rows, 768 and 10007: TN 67 us, 128 x 128 tiles 75; 193 to 211 TFLOP/s of
-//   binary32 products, 1.16 to 1.27 PFLOP/s of the bfloat16 ones they are made of
+//   binary32, 717 rows (1024, 30 % ignored), 768 and 10007: TN 71 to 77 us, 128 x 128 tiles
+//   10 % more; 142 to 155 TFLOP/s of binary32 products, six times that of bfloat16 ones
 // Narrow (128 x 64, four waves, two workgroups a unit) is for few columns (Kind).
 // Medium: 1337 x 333 to 20011 of 60 % ignored rows, NN 24 us.  Small (32 rows), for few:
 // 64 experts of 24 rows, 1536 to 2048, 78 us, 89 without it; 32 of 24, 768 to 256, 8.6 and 17.5;
