@@ -507,7 +507,7 @@ struct Patch {
 };
 
 // grad_x = dl W (NN): the rest of a row whose target is among the tile's k, and that target's
-// row of W, from which it is added to C.
+// row of W, from which it is added to C (8192 x 1536 by 32768 707 us, 690 without; under a trace).
 struct RowTarget {
   const uint16_t* q;        // W's row of the target, at the tile's first column
   int most;                 // four elements from there on end with W
@@ -727,7 +727,7 @@ __device__ __forceinline__ void lse_tile(f32x16 (&acc)[S::FQ][S::FP], const Prod
 
 // The logits become the loss's gradient with respect to them, but for the target's
 // column, which goes to `patch`.  From lse it is one exponential a logit; 8192 x 1536 by
-// 32768 with a soft cap 780 us, 512 MB of gradients written.
+// 32768 with a soft cap 855 us under a trace, 512 MB of gradients written.
 template <class S, bool CAP, bool EXACT>
 __device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t, int tid,
                                               Patch<S>& patch) {
@@ -778,8 +778,8 @@ __device__ __forceinline__ void gradient_tile(f32x16 (&acc)[S::FQ][S::FP], const
 // C, as a product of its own: 64 such rows of k at a time, in a fixed order, one element each
 // (rounded to bfloat16: 2^-16 of the target's element), with their rows of x.  How many there
 // are differs by target, all rows may have one; 8192 rows over 32768 columns are a stage or two
-// a tile.  8192 x 1536 by 32768 660 us, 652 without; 1337 x 333 by 20011, 60 % ignored, 31 and 26:
-// the waits for targets, rests and rows of x.
+// a tile.  8192 x 1536 by 32768 677 us, 662 without (under a trace); 1337 x 333 by 20011, 60 %
+// ignored, 31 and 26: the waits for targets, rests and rows of x.
 template <class S>
 __device__ __forceinline__ void add_targets_tn(f32x16 (&acc)[S::FQ][S::FP], const ProductArgs& a, const Tile& t, char* smem,
                                                int* wave_sum, int tid) {
