@@ -791,37 +791,45 @@ __device__ __forceinline__ void add_targets_tn(f32x16 (&acc)[S::FQ][S::FP], cons
   const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wq = w % S::WN, wp = w / S::WN;
   const int first = t.lo + t.k0, end = first + t.k, c0 = a.col0 + t.i0, m = min(t.m, S::BM);
   const char* q = reinterpret_cast<const char*>(a.q) + t.j0 * 2;
+  // a wave looks through 64 rows of every `step`: its own, or, where there are few, all of them
+  const bool few = end - first <= 64 * PER;
+  const int step = few ? 64 : S::NT;
 #pragma unroll 1
   for (int b = first; b < end; b += CHUNK) {
-    // a wave looks through 64 rows of every S::NT
-    const int r0 = b + tid;
-    int target[PER], mine = 0;
+    const int r0 = b + (few ? lane : tid);
+    int target[PER], count = 0, at = 0;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
       target[e] = c0 - 1;
-      if (b + S::NT * e < end) target[e] = gmem(a.target)[min(r0 + S::NT * e, end - 1)];
+      if (b + step * e < end) target[e] = gmem(a.target)[min(r0 + step * e, end - 1)];
     }
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
       const int v = target[e] - c0;
-      target[e] = r0 + S::NT * e < end && v < m ? v : -1;
+      target[e] = r0 + step * e < end && v < m ? v : -1;
     }
 #pragma unroll
-    for (int e = 0; e < PER; ++e) mine += __popcll(__ballot(target[e] >= 0));
-    if (lane == 0) wave_sum[w] = mine;
-    lds_barrier();
-    int at = 0, count = 0;
+    for (int e = 0; e < PER; ++e) count += __popcll(__ballot(target[e] >= 0));
+    if (few) {
+      if (count == 0) return;         // all waves
+    } else {
+      if (lane == 0) wave_sum[w] = count;
+      lds_barrier();
+      count = 0;
 #pragma unroll
-    for (int x = 0; x < S::NT / 64; ++x) {
-      if (x < w) at += wave_sum[x];
-      count += wave_sum[x];
+      for (int x = 0; x < S::NT / 64; ++x) {
+        if (x < w) at += wave_sum[x];
+        count += wave_sum[x];
+      }
+      count = __builtin_amdgcn_readfirstlane(count);
     }
-    count = __builtin_amdgcn_readfirstlane(count);
+    if (!few || w == 0) {
 #pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      const uint64_t votes = __ballot(target[e] >= 0);
-      if (target[e] >= 0) list[at + __popcll(votes & ((uint64_t(1) << lane) - 1))] = uint32_t(r0 + S::NT * e) << 8 | uint32_t(target[e]);
-      at += __popcll(votes);
+      for (int e = 0; e < PER; ++e) {
+        const uint64_t votes = __ballot(target[e] >= 0);
+        if (target[e] >= 0) list[at + __popcll(votes & ((uint64_t(1) << lane) - 1))] = uint32_t(r0 + step * e) << 8 | uint32_t(target[e]);
+        at += __popcll(votes);
+      }
     }
 #pragma unroll 1
     for (int e0 = 0; e0 < count; e0 += S::KE) {

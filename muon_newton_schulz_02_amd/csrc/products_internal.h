@@ -33,7 +33,8 @@ constexpr bool epi_lse(int e) { return e == EPI_LSE || e == EPI_LSE_CAP || e == 
 constexpr bool epi_dz(int e) { return e == EPI_DZ || e == EPI_DZ_CAP || e == EPI_DZ_LARGE_CAP; }
 constexpr bool epi_cap(int e) { return e >= EPI_LSE_CAP && e <= EPI_DZ_LARGE_CAP; }
 // Up to this cap logits of bfloat16 operands take the soft cap's short form, whose error of
-// 5 2^-24 cap is then no more than that of a binary32 logit of the cap's size.
+// 5 2^-24 cap is then no more than that of a binary32 logit of the cap's size (8192 x 1536 by
+// 32768: loss 772 us, gradient 2415; the exact form 842 and 2495).
 constexpr float FAST_CAP = 32.f;
 
 // One launch.  Groups (experts) split the rows of P and C for NT and NN, and k
